@@ -292,6 +292,177 @@ int specverify_verify_noalloc(const specverify_batch *in, float temperature, uin
                               int32_t *n_accepted, int32_t *out_tokens, float *p_lse,
                               float *q_lse, void *cuda_stream);
 
+/* ==========================================================================
+ * Token trees over a paged key/value cache.
+ *
+ * Sequence b's drafts form a tree of nodes[b] nodes: node 0 is the pending
+ * token (the one the last step emitted, whose key and value are not in the
+ * cache yet), parent[b * max_nodes + j] < j the node that node j continues,
+ * parent of node 0 = -1. The cache holds lens[b] committed tokens of sequence
+ * b in slots 0 .. lens[b]-1; the program has stored the keys and values of
+ * the tree's nodes in the slots after them, node j in slot lens[b] + j. Node
+ * j's query, attention output and logits are row row_off[b] + j of their
+ * buffers (and nodes[b] = 0 says that the sequence sits this step out).
+ *
+ * A step: specverify_tree_attention in every layer of the target, then
+ * specverify_verify_tree on its logits, specverify_tree_commit, and for a
+ * bounded cache specverify_cache_accumulate and specverify_cache_evict.
+ *
+ * All calls are asynchronous on `cuda_stream`, allocate nothing, may be
+ * captured into a CUDA graph, and check on the device what they read there:
+ * a sequence with a bad size, row, parent, path or page id is left alone (see
+ * each call), the others are unaffected, and the sticky status word says so.
+ */
+
+typedef struct specverify_tree_ctx *specverify_tree_t;
+
+enum {
+    SPECVERIFY_FP16 = 2 /* IEEE binary16: caches and queries of the calls below only */
+};
+
+#define SPECVERIFY_MAX_NODES 128 /* nodes of one sequence's tree */
+
+/* More bits of the status word (specverify_tree_status). */
+enum {
+    SPECVERIFY_STATUS_BAD_TREE = 1 << 6, /* nodes[b] outside [0, max_nodes], a parent not before
+                                            its node, or an accepted path that does not rise */
+    SPECVERIFY_STATUS_BAD_CACHE = 1 << 7 /* a length that the page table does not hold, or a page
+                                            id outside [0, num_pages) */
+};
+
+/* A paged cache. Element (layer, page, head, token, i) of k and of v is at
+ * layer * layer_stride + page * page_stride + head * head_stride + token *
+ * token_stride + i, i < head_dim, from its base: a head-major pool, a
+ * token-major one, or a slice of a larger one. Bases and strides are multiples
+ * of 16 bytes. Slot s of sequence b is token s % page_size of page
+ * page_table[b * table_stride + s / page_size]. Slots past a sequence's tokens
+ * may hold anything. Pages that only attention reads may be shared by
+ * sequences; a page that a call writes (commit, evict) belongs to one. */
+typedef struct {
+    int32_t dtype;      /* SPECVERIFY_BF16 or SPECVERIFY_FP16 */
+    int32_t layers;     /* attention and accumulation take one layer */
+    int64_t num_pages;
+    int32_t page_size;  /* a multiple of 8 */
+    int32_t kv_heads;
+    int32_t head_dim;   /* 64 or 128 */
+    void *k, *v;
+    int64_t layer_stride, page_stride, head_stride, token_stride; /* elements, k and v alike */
+    float *mass;        /* attention weight gathered by each slot, per head; may be NULL */
+    int32_t *pos;       /* position in its sequence of the token in each slot; may be NULL */
+    int64_t mass_layer_stride, mass_page_stride, mass_head_stride, mass_token_stride;
+    const int32_t *page_table; /* [B, table_stride] */
+    int64_t table_stride;
+    int32_t max_pages;  /* pages of one sequence, <= table_stride */
+} specverify_cache;
+
+typedef struct {
+    int32_t B;
+    int32_t max_nodes;      /* row length of parent and tokens, 1 .. SPECVERIFY_MAX_NODES */
+    const int64_t *row_off; /* [B] */
+    const int32_t *nodes;   /* [B] */
+    const int32_t *parent;  /* [B, max_nodes] */
+    const int32_t *tokens;  /* [B, max_nodes]; read by specverify_verify_tree only */
+} specverify_tree;
+
+/* Create a handle on `device` for batches of at most max_batch sequences.
+ * Its workspace holds the pieces of attention rows whose keys were split over
+ * SMs, and the lists of an eviction of at most max_moves tokens (see
+ * specverify_cache_evict; 0 when it is not used). Calls of one handle share
+ * that workspace and follow one another on one stream: use a handle for each
+ * concurrently used stream, and for each captured graph that may run beside
+ * another. */
+int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch,
+                           int64_t max_moves);
+
+/* Release the handle; its queued work must have completed. NULL is accepted. */
+int specverify_tree_destroy(specverify_tree_t h);
+
+/* Synchronise `cuda_stream`, return and clear the handle's sticky status bits. */
+int specverify_tree_status(specverify_tree_t h, void *cuda_stream, int32_t *status_out);
+
+int specverify_tree_workspace_bytes(specverify_tree_t h, size_t *out);
+
+/* Attention of the tree's nodes over the cache. For node j, query head h and
+ * its key head h / (heads / kv_heads):
+ *   s_p = scale * <q[row_off[b] + j, h], k_p>  for the slots p that j sees:
+ *         every p < lens[b], and lens[b] + i for i = j and every ancestor i of j;
+ *   out = sum_p softmax(s)_p v_p,  lse = ln sum_p exp(s_p).
+ * q and out are [rows, heads, head_dim] of the cache's dtype, with their own
+ * row and head strides in elements (multiples of 16 bytes, as the bases);
+ * heads is a multiple of kv_heads, scale > 0; lse [rows, heads] may be NULL.
+ * The scores, the softmax statistics and the sums over values are fp32; a
+ * weight is rounded to the cache's dtype, relative to a running maximum,
+ * before it multiplies a value. A slot that a node does not see never reaches
+ * its result, whatever it holds. A bad sequence's rows are NaN; rows that
+ * belong to no sequence stay as they were. */
+int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache,
+                              const specverify_tree *tree, const int32_t *lens, const void *q,
+                              int64_t rows, int32_t heads, int64_t q_row_stride,
+                              int64_t q_head_stride, float scale, void *out,
+                              int64_t out_row_stride, int64_t out_head_stride, float *lse,
+                              void *cuda_stream);
+
+/* Greedy verify of a tree, the exact-match rule of specverify_verify_greedy
+ * on every branch: from node 0, while a child of the current node holds the
+ * argmax of the current node's target row (lowest index on ties; of equal
+ * children the lowest), go to that child. target [rows, row_stride] logits of
+ * dtype SPECVERIFY_FP32 or SPECVERIFY_BF16, rows 16-byte aligned. Outputs:
+ *   n_accepted [B]             nodes accepted after node 0; -1 for nodes[b] = 0 and for a
+ *                              bad sequence (size, row, parent, a token outside [0, V), or
+ *                              a NaN in a row on the path; other rows are not read);
+ *   out_tokens [B, max_nodes]  the accepted tokens, the argmax after the last, then -1;
+ *   path [B, max_nodes]        node 0 and the accepted nodes, then -1. */
+int specverify_verify_tree(specverify_tree_t h, const specverify_tree *tree, const void *target,
+                           int32_t dtype, int64_t V, int64_t row_stride, int64_t rows,
+                           int32_t *n_accepted, int32_t *out_tokens, int32_t *path,
+                           void *cuda_stream);
+
+/* Keep the accepted path: in every layer and head, slot lens[b] + i takes the
+ * key and value of slot lens[b] + path[b, i], i = 0 .. n_accepted[b]; where the
+ * cache has them, mass of these slots becomes 0 and pos seen[b] + i. new_lens
+ * [B] = lens + n_accepted + 1 and new_seen [B] = seen + n_accepted + 1 (seen:
+ * tokens of the sequence so far, evicted ones among them; seen and new_seen
+ * may be NULL where the cache has no pos). A sequence with n_accepted[b] = -1,
+ * or with a bad path, length or page, keeps its slots and both numbers. The
+ * outputs may not be the inputs. */
+int specverify_tree_commit(specverify_tree_t h, const specverify_cache *cache, int32_t B,
+                           int32_t max_nodes, const int32_t *lens, const int32_t *seen,
+                           const int32_t *n_accepted, const int32_t *path, int32_t *new_lens,
+                           int32_t *new_seen, void *cuda_stream);
+
+/* Add to mass the attention weight that the accepted nodes gave each slot,
+ * after the commit (node path[b, i] is in slot lens[b] + i; lens is the length
+ * before it):
+ *   mass[p, g] += sum_{i <= n_accepted[b]} sum_{h of key head g} [p <= lens[b] + i]
+ *                 exp(scale * <q[row_off[b] + path[b, i], h], k_p> - lse[that row, h]).
+ * q and lse are those of specverify_tree_attention. One layer a call. Sums
+ * are fp32 in a fixed order; a page that two sequences share gathers both. A
+ * sequence with n_accepted[b] = -1 or a bad path, row, length or page adds
+ * nothing. */
+int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cache,
+                                const specverify_tree *tree, const int32_t *lens,
+                                const int32_t *n_accepted, const int32_t *path, const void *q,
+                                int64_t rows, int32_t heads, int64_t q_row_stride,
+                                int64_t q_head_stride, const float *lse, float scale,
+                                void *cuda_stream);
+
+/* Cut every sequence of more than `budget` tokens down to `budget`, in each
+ * layer and key head by itself. Kept are the slots with pos < sink or pos >=
+ * seen[b] - recent (sink + recent <= budget), then those of the largest mass
+ * (ties: the lower slot; a NaN counts as the least). Kept slots at or past the
+ * budget move, in ascending order, into the freed slots below it, in
+ * ascending order, with key, value, mass and pos; the others stay where they
+ * are. mass_out and pos_out (strides of mass and pos) receive mass and pos of
+ * the first min(lens[b], budget) slots, and may be mass and pos themselves or
+ * buffers that do not overlap them. new_lens [B] = min(lens, budget), not lens
+ * itself; a sequence with a bad length or page keeps everything. Needs layers * B
+ * * kv_heads * min(budget, max_pages * page_size - budget) <= max_moves
+ * (SPECVERIFY_ERR_TOO_LARGE). */
+int specverify_cache_evict(specverify_tree_t h, const specverify_cache *cache, int32_t B,
+                           const int32_t *lens, const int32_t *seen, int32_t budget, int32_t sink,
+                           int32_t recent, float *mass_out, int32_t *pos_out, int32_t *new_lens,
+                           void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

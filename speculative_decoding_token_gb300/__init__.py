@@ -26,7 +26,8 @@ __all__ = ["SpecVerify", "SpecVerifyError", "build", "load", "specverify_create"
            "specverify_verify_noalloc",
            "specverify_device_status", "specverify_status_string", "specverify_workspace_bytes",
            "specverify_set_timing", "specverify_get_timing", "specverify_set_wait_limit",
-           "specverify_acceptance_stats", "specverify_row_features", "STATUS_BITS"]
+           "specverify_acceptance_stats", "specverify_row_features", "STATUS_BITS",
+           "SpecTree", "KVCache", "TokenTree"]
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -43,6 +44,8 @@ STATUS_BITS = {
     "bad_logit": 1 << 3,
     "timeout": 1 << 4,
     "bad_param": 1 << 5,
+    "bad_tree": 1 << 6,
+    "bad_cache": 1 << 7,
     "draw_slow": 1 << 8,
     "draw_zero_mass": 1 << 9,
 }
@@ -122,6 +125,8 @@ def load():
                   "specverify_get_timing", "specverify_set_wait_limit",
                   "specverify_acceptance_stats", "specverify_row_features"):
             getattr(lib, f).restype = ctypes.c_int
+        from . import tree
+        tree.bind(lib)
         _lib = lib
         return lib
 
@@ -434,3 +439,11 @@ class SpecVerify:
 
     def set_wait_limit(self, ns: int):
         specverify_set_wait_limit(self.h, ns)
+
+
+def __getattr__(name):
+    # the token-tree classes need torch, which this module imports only where it is used
+    if name in ("SpecTree", "KVCache", "TokenTree"):
+        from . import tree
+        return getattr(tree, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,121 @@
+// sv_tree.h -- types shared by the host library and the kernels of the
+// token-tree calls (not part of the public C ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "specverify.h"
+
+namespace sv {
+
+constexpr int kMaxNodes = SPECVERIFY_MAX_NODES;
+constexpr int kMaskWords = kMaxNodes / 32;
+
+// A paged cache, strides in bytes.
+struct CacheParams {
+    char *k, *v;
+    int64_t ls, ps, hs, ts;   // layer, page, head, token strides
+    float *mass;
+    int32_t *pos;
+    int64_t mls, mps, mhs, mts;  // of mass and pos, elements
+    const int32_t *table;
+    int64_t table_stride;
+    int64_t num_pages;
+    int32_t max_pages, page, kv_heads, d, layers;
+    int32_t fp16;             // 1: binary16, 0: bfloat16
+};
+
+struct TreeParams {
+    const int64_t *row_off;
+    const int32_t *nodes, *parent, *tokens;
+    int32_t B, max_nodes;
+};
+
+struct TreeAttnParams {
+    CacheParams c;
+    TreeParams t;
+    const int32_t *lens;
+    const char *q;
+    int64_t q_rs, q_hs;       // bytes
+    char *out;
+    int64_t o_rs, o_hs;       // bytes
+    float *lse;
+    int64_t rows;
+    int32_t heads, G;
+    float scale_log2;         // scale * log2(e)
+    int32_t *status;
+};
+
+struct TreeVerifyParams {
+    TreeParams t;
+    const char *target;
+    int64_t stride_bytes, V, rows;
+    int32_t *n_out, *tok_out, *path_out;
+    int32_t *status;
+};
+
+struct CommitParams {
+    CacheParams c;
+    int32_t B, max_nodes;
+    const int32_t *lens, *seen, *n, *path;
+    int32_t *new_lens, *new_seen;
+    int32_t *status;
+};
+
+struct AccumParams {
+    CacheParams c;
+    TreeParams t;
+    const int32_t *lens, *n, *path;
+    const char *q;
+    int64_t q_rs, q_hs;
+    const float *lse;
+    int64_t rows;
+    int32_t heads, G;
+    float scale_log2;
+    int32_t *status;
+};
+
+struct EvictParams {
+    CacheParams c;
+    int32_t B;
+    const int32_t *lens, *seen;
+    int32_t budget, sink, recent;
+    float *mass_out;
+    int32_t *pos_out, *new_lens;
+    int32_t moves;            // list entries of one item: min(budget, capacity - budget)
+    int32_t *move_src, *move_dst;  // [items, moves]
+    int32_t *move_cnt;        // [items]
+    int32_t *status;
+};
+
+cudaError_t prepare_tree();
+cudaError_t launch_tree_attention(const TreeAttnParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_tree_verify(const TreeVerifyParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s);
+cudaError_t launch_accumulate(const AccumParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// device helpers
+#ifdef __CUDACC__
+
+// Whether tokens [0, count) of sequence b fit its pages.
+__device__ __forceinline__ bool cache_holds(const CacheParams &c, int64_t count) {
+    return count >= 0 && count <= (int64_t)c.max_pages * c.page;
+}
+
+// Page i of sequence b, -1 for an id outside the pool.
+__device__ __forceinline__ int64_t page_at(const CacheParams &c, int b, int i) {
+    const int32_t id = __ldg(&c.table[(int64_t)b * c.table_stride + i]);
+    return id >= 0 && (int64_t)id < c.num_pages ? (int64_t)id : -1;
+}
+
+// The page that holds slot s of sequence b.
+__device__ __forceinline__ int64_t page_of(const CacheParams &c, int b, int s) {
+    return page_at(c, b, s / c.page);
+}
+
+#endif
+
+}  // namespace sv
