@@ -44,7 +44,20 @@ struct TreeAttnParams {
     int64_t rows;
     int32_t heads, G;
     float scale_log2;         // scale * log2(e)
+    int32_t box;              // tokens of one tiled copy: divides the page size and a tile
     int32_t *status;
+    // workspace: the pieces of rows whose slots were split over CTAs
+    float *piece_o;           // [CTAs, 2, 256, d]
+    float2 *piece_ml;         // [CTAs, 2, 256]: reference maximum (log2 scale), sum
+    struct AttnOwner *owner;  // [CTAs]
+};
+
+// The item that a CTA begins and another ends.
+struct AttnOwner {
+    int64_t row0;             // its tree's first row
+    int32_t pieces;           // 0: there is none
+    int32_t rows, first_row;  // of the item, and its first among the tree's rows of a key head
+    int32_t head;             // key head
 };
 
 struct TreeVerifyParams {
@@ -90,7 +103,9 @@ struct EvictParams {
 };
 
 cudaError_t prepare_tree();
-cudaError_t launch_tree_attention(const TreeAttnParams &p, int num_sms, cudaStream_t s);
+size_t attn_workspace(int ctas);
+void attn_place(TreeAttnParams &p, void *ws, int ctas);
+cudaError_t launch_tree_attention(TreeAttnParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_tree_verify(const TreeVerifyParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s);
 cudaError_t launch_accumulate(const AccumParams &p, int num_sms, cudaStream_t s);

@@ -15,6 +15,7 @@ struct specverify_tree_ctx {
     size_t ws_bytes = 0;
     int32_t *status = nullptr;
     int32_t *move_src = nullptr, *move_dst = nullptr, *move_cnt = nullptr;
+    void *attn = nullptr;
 };
 
 namespace {
@@ -145,7 +146,7 @@ int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch
     if (e == cudaSuccess) e = sv::prepare_tree();
     // an item moves at least one token, so max_moves bounds the items as well
     const size_t lists = sizeof(int32_t) * (size_t)max_moves;
-    h->ws_bytes = 256 + 3 * ((lists + 255) / 256 * 256);
+    h->ws_bytes = 256 + 3 * ((lists + 255) / 256 * 256) + sv::attn_workspace(h->num_sms);
     if (e == cudaSuccess) e = cudaMalloc(&h->ws, h->ws_bytes);
     if (e == cudaSuccess) e = cudaMemset(h->ws, 0, 256);
     if (e != cudaSuccess) {
@@ -160,6 +161,7 @@ int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch
         *p = reinterpret_cast<int32_t *>(w);
         w += (lists + 255) / 256 * 256;
     }
+    h->attn = w;
     *out = h;
     return SPECVERIFY_OK;
 }
@@ -224,6 +226,7 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
     p.G = heads / cache->kv_heads;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
+    sv::attn_place(p, h->attn, h->num_sms);
     return map_cuda(sv::launch_tree_attention(p, h->num_sms,
                                               static_cast<cudaStream_t>(cuda_stream)));
 }

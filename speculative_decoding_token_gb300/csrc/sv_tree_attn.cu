@@ -1,130 +1,874 @@
-// sv_tree_attn.cu -- attention of a tree of drafted tokens over a paged cache.
-//
-// Simplest form: a warp for each (node, query head), the head's elements over
-// its lanes, one slot after another with the running maximum and sum of the
+// sv_tree_attn.cu -- attention of a tree of drafted tokens over a paged cache,
+// one pass over the keys and values with the running maximum and sum of the
 // softmax (Milakov and Gimelshein, "Online normalizer calculation for
-// softmax"). Every row reads its keys for itself, so it is bound by
-// instructions, far from the cache's bytes.
+// softmax").
+//
+// The queries of a tree's nodes that share a key head are the rows of one
+// matrix, row r = node r / G, head r % G, so each key is read once for all of
+// them: S = Q K^T and O += P V run on the tensor core in tiles of 128 rows by
+// 128 slots. A persistent CTA per SM:
+//   warps 0-3, 4-7  two softmax groups, a row a thread: S from tensor memory,
+//                   P back to it;
+//   warp 8          issues the products (one thread);
+//   warp 9          copies K and V tiles into a ring of shared-memory slots
+//                   (warps 10 and 11 only complete its warpgroup).
+// The two groups take turns on the tensor core, one's softmax under the
+// other's products. Up to 128 rows share one Q tile and the groups alternate
+// over the slots' tiles (each with its own maximum, sum and O, joined at the
+// end); more rows make two Q tiles, a group each, over the same slots.
+//
+// All (sequence, key head, block of rows) items' tiles of 128 slots form one
+// line that is cut evenly over the CTAs. An item cut in pieces leaves each
+// piece's O (not yet divided), maximum and sum in the workspace, and a second
+// kernel joins the pieces; whole items are written directly.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "sv_common.cuh"
+#include "sv_tcgen05.cuh"
 #include "sv_tree.h"
 
 namespace sv {
 
 namespace {
 
-template <bool FP16>
-__device__ __forceinline__ float2 to_float2(uint32_t w) {
-    if (FP16) return __half22float2(*reinterpret_cast<__half2 *>(&w));
-    return make_float2(bf16_lo(w), bf16_hi(w));
+constexpr int kTile = 128;                 // rows of a Q tile, slots of a K or V tile
+constexpr int kSoftThreads = 256;
+constexpr int kAttnThreads = kSoftThreads + 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// A softmax thread holds a row of S. A launch of 384 threads gives each 168
+// registers; the groups draw 208 and the last warpgroup keeps 80 (the sum, 496
+// a thread triple, stays below the launch's 504).
+constexpr int kSoftRegs = 208, kOtherRegs = 80;
+constexpr int kTmemCols = 512;
+constexpr float kTiny = 1e-37f;            // least weight of a piece: keeps inf * weight infinite
+
+template <int D>
+struct Shape {
+    static constexpr int kPanel = kTile * 128;           // 64 elements of 128 rows
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kSlots = D == 128 ? 5 : 10;     // ring slots of a K or V tile
+    static constexpr int kRing = 2 * kTileBytes;         // after the two Q tiles
+    static constexpr int kMisc = kRing + kSlots * kTileBytes;
+    static constexpr int kSmem = kMisc + 2688;
+    // columns of tensor memory: S of both groups, then O of both; P lies over S
+    static constexpr uint32_t kS = 0, kO = 2 * kTile;
+};
+static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
+
+struct Misc {
+    uint32_t mask[kMaxNodes][kMaskWords];  // a node's ancestors and itself
+    int8_t parent[kMaxNodes];
+    uint64_t full[10], empty[10], q_full, s_full[2], p_full[2], o_full[2], drain;
+    uint32_t nonfinite[kMaskWords];        // nodes of this segment whose value has an inf or NaN
+    uint32_t tmem;
+    int32_t b0;                            // the CTA's first sequence,
+    long long rest0;                       // and its first tile in it
+    long long scan[kAttnThreads / 32];
+    int32_t abort;                         // a wait gave up
+};
+static_assert(sizeof(Misc) <= 2688, "Misc");
+
+// What sequence b contributes to the line of tiles; 0 tiles: idle or bad.
+struct Seq {
+    int L, T, tiles, blocks;
+    int64_t row0;
+};
+
+__device__ __forceinline__ int seq_error(const TreeAttnParams &P, int nodes, int64_t row0, int L) {
+    if (nodes < 0 || nodes > P.t.max_nodes) return SPECVERIFY_STATUS_BAD_TREE;
+    if (nodes == 0) return 0;
+    if (row0 < 0 || row0 > P.rows - nodes) return SPECVERIFY_STATUS_BAD_ROW;
+    if (L < 0 || !cache_holds(P.c, (int64_t)L + nodes)) return SPECVERIFY_STATUS_BAD_CACHE;
+    return 0;
 }
 
-template <bool FP16>
-__device__ __forceinline__ uint32_t from_float2(float a, float b) {
-    if (FP16) {
-        __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t *>(&h);
+__device__ __forceinline__ Seq seq_of(const TreeAttnParams &P, int b) {
+    Seq s;
+    s.T = P.t.nodes[b];
+    s.L = P.lens[b];
+    s.row0 = P.t.row_off[b];
+    s.tiles = s.blocks = 0;
+    if (s.T != 0 && seq_error(P, s.T, s.row0, s.L) == 0) {
+        s.tiles = (s.L + s.T + kTile - 1) / kTile;
+        s.blocks = (s.T * P.G + 2 * kTile - 1) / (2 * kTile);
     }
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
+    return s;
 }
 
-constexpr int kRowWarps = 4;
+// A run of tiles of one item, all of a CTA's work in line order. Every role
+// walks the same segments by itself.
+struct Segment {
+    Seq s;
+    int b, head, block, tile0, n;
+    int rows;      // of this item: up to 2 * kTile
+    bool pair;     // two Q tiles
+    bool first, last;  // holds the item's first, last tile
+};
+
+struct Walk {
+    int b;
+    long long rest;   // next tile within sequence b
+    long long left;   // tiles of this CTA still to do
+
+    __device__ bool next(const TreeAttnParams &P, Segment &g) {
+        if (left <= 0) return false;
+        for (;;) {
+            g.s = seq_of(P, b);
+            const long long all = (long long)g.s.tiles * g.s.blocks * P.c.kv_heads;
+            if (rest < all) break;
+            rest = 0;
+            ++b;
+        }
+        const int item = (int)(rest / g.s.tiles);
+        g.b = b;
+        g.tile0 = (int)(rest - (long long)item * g.s.tiles);
+        g.head = item / g.s.blocks;
+        g.block = item - g.head * g.s.blocks;
+        g.n = (int)min((long long)(g.s.tiles - g.tile0), left);
+        g.rows = min(g.s.T * P.G - g.block * 2 * kTile, 2 * kTile);
+        g.pair = g.rows > kTile;
+        g.first = g.tile0 == 0;
+        g.last = g.tile0 + g.n == g.s.tiles;
+        rest += g.n;
+        left -= g.n;
+        return true;
+    }
+};
+
+// Place of a segment's K and V tile j in the order of the ring's uses. Group w
+// needs K of its next tile before V of its current one.
+__device__ __forceinline__ uint32_t k_at(const Segment &g, int j) {
+    return g.pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1);
+}
+__device__ __forceinline__ uint32_t v_at(const Segment &g, int j) {
+    return g.pair ? 2 * j + 1 : min(2 * j + 2, 2 * g.n - 1);
+}
+
+// A wait that gives up after about two seconds, or once another has: the roles
+// then run through their work without waiting, and the status says so.
+__device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, int32_t *status) {
+    const uint32_t at = smem_u32(&bar);
+    if (mbar_try_wait(at, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait(at, parity)) return true;
+        if (*(volatile int32_t *)&M.abort) return false;
+        if (global_ns() - t0 > 2000000000ull) break;
+    }
+    *(volatile int32_t *)&M.abort = 1;
+    atomicOr(status, SPECVERIFY_STATUS_TIMEOUT);
+    return false;
+}
+
+// Barrier of the two softmax groups; returns whether any thread's v was true.
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    if (FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <bool FP16>
+__device__ __forceinline__ float half_at(uint32_t w, int i) {
+    const uint32_t x = (w >> (16 * i)) & 0xffffu;
+    return FP16 ? __half2float(__ushort_as_half((unsigned short)x)) : __uint_as_float(x << 16);
+}
+
+// The halves of w that are inf or NaN, as a mask of their bits.
+template <bool FP16>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+    constexpr uint32_t e = FP16 ? 0x7C00u : 0x7F80u;
+    return ((w & e) == e ? 0xffffu : 0u) | (((w >> 16) & e) == e ? 0xffff0000u : 0u);
+}
+
+// A weight is rounded to the cache's type relative to a reference maximum that
+// is raised only when the running one passes it by kSlack binades (until then
+// O and the sum need no rescaling). bfloat16 keeps fp32's range; binary16 has
+// weights from 2^-24 to 2^16, so the reference's weight is 2^kShift there.
+template <bool FP16>
+struct Range {
+    static constexpr float kSlack = FP16 ? 5.0f : 8.0f;
+    static constexpr float kShift = FP16 ? 10.0f : 0.0f;
+};
+
+// ---------------------------------------------------------------------------
+// softmax groups
 
 template <bool FP16, int D>
-__global__ void __launch_bounds__(kRowWarps * 32) tree_attn_kernel(const TreeAttnParams P) {
-    constexpr int W = D / 64;  // 32-bit words of a row in a lane
-    __shared__ uint32_t s_mask[kMaskWords];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.z, j = blockIdx.y, h = blockIdx.x * kRowWarps + warp;
-    const int mn = P.t.max_nodes;
-    const int nodes = P.t.nodes[b];
-    int bad = 0;
-    if (nodes < 0 || nodes > mn) bad = SPECVERIFY_STATUS_BAD_TREE;
-    const int64_t row0 = bad ? 0 : P.t.row_off[b];
-    if (!bad && nodes > 0 && (row0 < 0 || row0 > P.rows - nodes)) bad = SPECVERIFY_STATUS_BAD_ROW;
-    if (bad || j >= nodes) {
-        if (bad && threadIdx.x == 0) atomicOr(P.status, bad);
-        return;
+__device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk,
+                             uint32_t tmem) {
+    using Sh = Shape<D>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int w = warp >> 2;                   // group
+    const int row = (warp & 3) * 32 + lane;    // of the group's Q tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + Sh::kS + w * kTile;
+    const float c2 = P.scale_log2;
+    const float ninf = -INFINITY;
+    uint32_t s_phase = 0, o_phase[2] = {0, 0};
+    uint32_t base = 0;  // ring uses before this segment
+    Segment g;
+    while (walk.next(P, g)) {
+        soft_sync();  // the previous segment's reads of Q, O and the masks are over
+        const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
+        const bool tail = t_end > g.s.L;
+        const int64_t kv_off = (int64_t)g.head * P.c.hs;
+        // Q rows into their tiles, in 16-byte chunks swizzled within 8 rows
+        {
+            const int r_first = g.pair ? w * kTile : 0, r_count = min(kTile, g.rows - r_first);
+            const int t0 = g.pair ? tid & 127 : tid, tn = g.pair ? 128 : 256;
+            char *q = smem + (g.pair ? w * Sh::kTileBytes : 0);
+            constexpr int C = D / 8;
+#pragma unroll 8
+            for (int i = t0; i < r_count * C; i += tn) {
+                const int r = i / C, c = i % C;
+                const int gr = g.block * 2 * kTile + r_first + r;
+                const int node = gr / P.G, hh = gr - node * P.G;
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    P.q + (g.s.row0 + node) * P.q_rs + (int64_t)(g.head * P.G + hh) * P.q_hs + c * 16);
+                *reinterpret_cast<uint4 *>(q + (c >> 3) * Sh::kPanel + r * 128 +
+                                           (((c & 7) ^ (r & 7)) << 4)) = x;
+            }
+        }
+        fence_async_smem();
+        mbar_arrive(smem_u32(&M.q_full));
+        // pages, parents
+        bool bad_page = false, bad_tree = false;
+        for (int i = t_begin / P.c.page + tid; i <= (t_end - 1) / P.c.page; i += kSoftThreads)
+            bad_page |= page_at(P.c, g.b, i) < 0;
+        if (tail) {
+            if (tid < g.s.T) {
+                const int up = P.t.parent[(int64_t)g.b * P.t.max_nodes + tid];
+                bad_tree = tid == 0 ? up != -1 : (up < 0 || up >= tid);
+                M.parent[tid] = (int8_t)(bad_tree ? -1 : up);
+            }
+            if (tid < kMaskWords) M.nonfinite[tid] = 0;
+        }
+        if (bad_page) atomicOr(P.status, SPECVERIFY_STATUS_BAD_CACHE);
+        if (bad_tree) atomicOr(P.status, SPECVERIFY_STATUS_BAD_TREE);
+        const bool bad = soft_any(bad_page || bad_tree);
+        if (tail) {
+            if (tid < g.s.T) {
+                uint32_t m[kMaskWords] = {};
+                for (int i = tid; i >= 0; i = M.parent[i])
+#pragma unroll
+                    for (int q = 0; q < kMaskWords; ++q)
+                        if (i >> 5 == q) m[q] |= 1u << (i & 31);
+#pragma unroll
+                for (int q = 0; q < kMaskWords; ++q) M.mask[tid][q] = m[q];
+            }
+            if (!bad_page && !bad) {
+                constexpr int C = D / 8;
+                const int j0 = max(0, t_begin - g.s.L), j1 = t_end - g.s.L;
+                for (int i = tid; i < (j1 - j0) * C; i += kSoftThreads) {
+                    const int j = j0 + i / C, s = g.s.L + j;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(
+                        P.c.v + kv_off + page_of(P.c, g.b, s) * P.c.ps +
+                        (int64_t)(s % P.c.page) * P.c.ts + i % C * 16);
+                    if (nonfinite_bits<FP16>(x.x) | nonfinite_bits<FP16>(x.y) |
+                        nonfinite_bits<FP16>(x.z) | nonfinite_bits<FP16>(x.w))
+                        atomicOr(&M.nonfinite[j >> 5], 1u << (j & 31));
+                }
+            }
+            soft_sync();
+        }
+        // this thread's row
+        const int r_item = (g.pair ? w * kTile : 0) + row;
+        const int gr = g.block * 2 * kTile + min(r_item, g.rows - 1);
+        const int node = gr / P.G, qh = g.head * P.G + gr - node * P.G;
+        const bool warp_on = (g.pair ? w * kTile : 0) + (row & ~31) < g.rows;
+        float m_ref = ninf, l = 0.0f;
+        const int step = g.pair ? 1 : 2;
+        bool fresh = true;
+        for (int j = g.pair ? 0 : w; j < g.n; j += step) {
+            wait_on(M, M.s_full[w], s_phase, P.status);
+            s_phase ^= 1;
+            tc_fence_after();
+            const int t0 = t_begin + j * kTile;
+            const bool tail_tile = t0 + kTile > g.s.L;
+            if (warp_on) {
+                uint32_t s[kTile];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+                tmem_wait_ld();
+                if (tail_tile) {
+                    const int shift = t0 - g.s.L;  // column c is node c + shift, a token before 0
+                    const auto word = [&](int i) -> uint32_t {
+                        return i < 0 ? 0xffffffffu : (i >= kMaskWords ? 0u : M.mask[node][i]);
+                    };
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = 32 * q + shift;
+                        const uint32_t see =
+                            __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(see >> c & 1)) s[32 * q + c] = __float_as_uint(ninf);
+                    }
+                }
+                float mx = ninf;
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+                mx *= c2;
+                if (__any_sync(0xffffffffu, mx > m_ref + Range<FP16>::kSlack)) {
+                    const float up = fmaxf(m_ref, mx);
+                    const float f = m_ref == up ? 1.0f : ex2_approx(m_ref - up);
+                    m_ref = up;
+                    l *= f;
+                    if (!fresh) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            const uint32_t at = tmem + lanes + Sh::kO + w * D + c;
+                            tmem_ld32(at, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(at, o);
+                        }
+                    }
+                }
+                const float off = Range<FP16>::kShift - (m_ref == ninf ? 0.0f : m_ref);
+                const f32x2 c22 = pack2(c2, c2), off2 = pack2(off, off);
+                f32x2 sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int c = 64 * h + 2 * i;
+                        const float2 x = unpack2(
+                            fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c22, off2));
+                        const float a = ex2_approx(x.x), b = ex2_approx(x.y);
+                        if (i & 1)
+                            sum1 = add2(sum1, pack2(a, b));
+                        else
+                            sum0 = add2(sum0, pack2(a, b));
+                        p[i] = pack_half<FP16>(a, b);
+                    }
+                    tmem_st32(ts + 32 * h, p);
+                }
+                const float2 sum = unpack2(add2(sum0, sum1));
+                l += sum.x + sum.y;
+                tmem_wait_st();
+            }
+            fresh = false;
+            if (tail_tile && (!g.pair || w == 0)) {
+                // a slot past the tree, or a node's inf or NaN: 0 in the products
+                // (the latter are added where they are seen, below)
+                const uint32_t use = base + v_at(g, j);
+                wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status);
+                char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
+                const int r0 = max(0, g.s.L - t0), gone = g.s.L + g.s.T - t0;
+                for (int i = tid & 127; i < (kTile - r0) * (D / 8); i += 128) {
+                    const int r = r0 + i / (D / 8), c = i % (D / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::kPanel + r * 128 +
+                                                          ((c & 7) << 4));
+                    if (r >= gone) {
+                        *at = make_uint4(0, 0, 0, 0);
+                    } else {
+                        uint4 x = *at;
+                        const uint32_t a = nonfinite_bits<FP16>(x.x), b = nonfinite_bits<FP16>(x.y),
+                                       c4 = nonfinite_bits<FP16>(x.z),
+                                       d4 = nonfinite_bits<FP16>(x.w);
+                        if (a | b | c4 | d4)
+                            *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
+                    }
+                }
+                fence_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&M.p_full[w]));
+        }
+        // the item's sums
+        const bool used1 = g.pair || g.n > 1;
+        if (!g.pair || w == 0) {
+            wait_on(M, M.o_full[0], o_phase[0], P.status);
+        }
+        if (used1 && (!g.pair || w == 1)) {
+            wait_on(M, M.o_full[1], o_phase[1], P.status);
+        }
+        o_phase[0] ^= 1;
+        if (used1) o_phase[1] ^= 1;
+        tc_fence_after();
+        base += 2 * g.n;
+        float wgt[2] = {1.0f, 1.0f};
+        float mf = m_ref, lf = l;
+        if (!g.pair) {
+            // join the groups: each takes half of the columns
+            float2 *ml = reinterpret_cast<float2 *>(smem + Sh::kTileBytes);  // the unused Q tile
+            ml[w * kTile + row] = make_float2(m_ref, l);
+            soft_sync();
+            const float2 a = ml[row], b = ml[kTile + row];
+            mf = fmaxf(a.x, b.x);
+            wgt[0] = a.x == ninf ? 0.0f : fmaxf(ex2_approx(a.x - mf), kTiny);
+            wgt[1] = b.x == ninf ? 0.0f : fmaxf(ex2_approx(b.x - mf), kTiny);
+            lf = a.y * wgt[0] + (used1 ? b.y * wgt[1] : 0.0f);
+        }
+        if (bad) lf = NAN;
+        if (warp_on) {
+            const bool whole = g.first && g.last;
+            const bool mine = r_item < g.rows;
+            const float inv = whole ? (lf == 0.0f ? 0.0f : 1.0f / lf) : 1.0f;
+            const int64_t orow = g.s.row0 + node;
+            const int c_begin = g.pair ? 0 : w * (D / 2), c_end = g.pair ? D : c_begin + D / 2;
+            const int piece = g.first ? 1 : 0;  // a CTA's first and last segments may be pieces
+            const int64_t at = ((int64_t)blockIdx.x * 2 + piece) * (2 * kTile) + r_item;
+            bool any_odd = false;
+            if (tail)
+#pragma unroll
+                for (int q = 0; q < kMaskWords; ++q)
+                    any_odd |= (M.nonfinite[q] & M.mask[node][q]) != 0;
+#pragma unroll 1
+            for (int c = c_begin; c < c_end; c += 32) {
+                uint32_t o[32];
+                float f[32];
+                tmem_ld32(tmem + lanes + Sh::kO + (g.pair ? w * D : 0) + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * wgt[0];
+                if (!g.pair && used1) {
+                    tmem_ld32(tmem + lanes + Sh::kO + D + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(o[i]), wgt[1], f[i]);
+                }
+                if (any_odd && mine) {
+                    // a seen inf or NaN decides its element whatever its weight
+                    for (int j = 0; j < g.s.T; ++j) {
+                        if (!(M.nonfinite[j >> 5] & M.mask[node][j >> 5] & (1u << (j & 31)))) continue;
+                        const int s = g.s.L + j;
+                        const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                            P.c.v + kv_off + page_of(P.c, g.b, s) * P.c.ps +
+                            (int64_t)(s % P.c.page) * P.c.ts + c * 2);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t x = v[i], bits = nonfinite_bits<FP16>(x);
+                            if (bits & 0xffffu) f[2 * i] += half_at<FP16>(x, 0);
+                            if (bits >> 16) f[2 * i + 1] += half_at<FP16>(x, 1);
+                        }
+                    }
+                }
+                if (mine) {
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(P.out + orow * P.o_rs +
+                                                               (int64_t)qh * P.o_hs + c * 2);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(
+                                pack_half<FP16>(f[8 * i] * inv, f[8 * i + 1] * inv),
+                                pack_half<FP16>(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
+                                pack_half<FP16>(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
+                                pack_half<FP16>(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(P.piece_o + at * D + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    }
+                }
+            }
+            if (mine && (g.pair || w == 0)) {
+                if (!whole)
+                    P.piece_ml[at] = make_float2(mf, lf);
+                else if (P.lse)
+                    P.lse[orow * P.heads + qh] =
+                        (mf + log2f(lf) - Range<FP16>::kShift) * 0.6931471805599453f;
+            }
+        }
+        tc_fence_before();
     }
-    const int L = P.lens[b];
-    if (L < 0 || !cache_holds(P.c, (int64_t)L + nodes)) bad = SPECVERIFY_STATUS_BAD_CACHE;
-    for (int i = 0; i < nodes; ++i) {
-        const int up = P.t.parent[(int64_t)b * mn + i];
-        if (i == 0 ? up != -1 : (up < 0 || up >= i)) bad |= SPECVERIFY_STATUS_BAD_TREE;
+}
+
+// ---------------------------------------------------------------------------
+// products
+
+template <bool FP16, int D>
+__device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk, uint32_t tmem) {
+    using Sh = Shape<D>;
+    constexpr uint32_t dqk = mma_desc(FP16, false, kTile, kTile), dpv = mma_desc(FP16, true, kTile, D);
+    const uint32_t q0 = smem_u32(smem), ring = q0 + Sh::kRing;
+    uint32_t base = 0, q_phase = 0, p_phase[2] = {0, 0};
+    Segment g;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+        ok = wait_on(M, M.q_full, q_phase, P.status);
+        q_phase ^= 1;
+        const int steps = g.pair ? 2 * g.n : g.n;
+        // step t: group t % 2, tile t (or t / 2 when both groups take every tile)
+        const auto qk = [&](int t) {
+            const int j = g.pair ? t >> 1 : t, w = t & 1;
+            const uint32_t use = base + k_at(g, j), slot = use % Sh::kSlots;
+            if (!g.pair || w == 0)
+                ok = ok && wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t a = q0 + (g.pair ? w * Sh::kTileBytes : 0), b = ring + slot * Sh::kTileBytes;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * Sh::kPanel + (k & 3) * 32;
+                mma_ss(tmem + Sh::kS + w * kTile, smem_desc(a + off, 0), smem_desc(b + off, 0), dqk,
+                       k > 0);
+            }
+            mma_commit(smem_u32(&M.s_full[w]));
+            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]));
+        };
+        if (ok) qk(0);
+        if (ok && steps > 1) qk(1);
+        for (int t = 0; ok && t < steps; ++t) {
+            const int j = g.pair ? t >> 1 : t, w = t & 1;
+            const uint32_t use = base + v_at(g, j), slot = use % Sh::kSlots;
+            ok = wait_on(M, M.p_full[w], p_phase[w], P.status);
+            p_phase[w] ^= 1;
+            if (ok && (!g.pair || w == 0))
+                ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t b = ring + slot * Sh::kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + Sh::kO + w * D, tmem + Sh::kS + w * kTile + k * 8,
+                       smem_desc(b + k * 2048, Sh::kPanel), dpv, t >= 2 || k > 0);
+            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]));
+            if (t + 2 >= steps) mma_commit(smem_u32(&M.o_full[w]));
+            if (t + 2 < steps) qk(t + 2);
+        }
+        base += 2 * g.n;
     }
-    for (int i = threadIdx.x; i < kMaskWords; i += blockDim.x) s_mask[i] = 0;
+    if (!ok) {  // no product outlives the CTA
+        mma_commit(smem_u32(&M.drain));
+        mbar_wait_bounded(smem_u32(&M.drain), 0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// copies
+
+template <int D>
+__device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const CUtensorMap *mv,
+                          Misc &M, char *smem, Walk walk) {
+    using Sh = Shape<D>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(smem) + Sh::kRing;
+    const int box = P.box;
+    uint32_t use = 0;
+    Segment g;
+    bool ok = true;
+    while (ok && walk.next(P, g)) {
+        const int len = g.s.L + g.s.T;
+        const auto page_id = [&](int j) -> int {  // of the lane's box in tile j, -1: none
+            const int s = (g.tile0 + j) * kTile + lane * box;
+            return j < g.n && lane * box < kTile && s < len ? (int)page_of(P.c, g.b, s) : -1;
+        };
+        const auto copy = [&](const CUtensorMap *map, int j, int page) {
+            const uint32_t slot = use % Sh::kSlots, bar = smem_u32(&M.full[slot]);
+            ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                return;
+            }
+            ++use;
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box * D * 2);
+            __syncwarp();
+            if (page >= 0) {
+                const int s = (g.tile0 + j) * kTile + lane * box;
+                const uint32_t dst = ring + slot * Sh::kTileBytes + lane * box * 128;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tile_load(dst + c * Sh::kPanel, map, c * 64, s % P.c.page, g.head, page, bar);
+            }
+            __syncwarp();
+        };
+        // the order of k_at and v_at; page ids are fetched a tile ahead
+        int now = page_id(0), next = page_id(1);
+        copy(mk, 0, now);
+        for (int j = 0; ok && j < g.n; ++j) {
+            const int after = page_id(j + 2);
+            if (!g.pair && j + 1 < g.n) copy(mk, j + 1, next);
+            if (ok) copy(mv, j, now);
+            if (ok && g.pair && j + 1 < g.n) copy(mk, j + 1, next);
+            now = next;
+            next = after;
+        }
+    }
+    // no copy outlives the CTA
+    for (uint32_t u = use > Sh::kSlots ? use - Sh::kSlots : 0; u < use; ++u)
+        mbar_wait_bounded(smem_u32(&M.full[u % Sh::kSlots]), u / Sh::kSlots & 1);
+}
+
+// ---------------------------------------------------------------------------
+
+template <bool FP16, int D>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TreeAttnParams P,
+                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using Sh = Shape<D>;
+    extern __shared__ __align__(1024) char smem[];
+    Misc &M = *reinterpret_cast<Misc *>(smem + Sh::kMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (tid == 0) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(smem_u32(&M.full[i]), 1);
+            mbar_init(smem_u32(&M.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&M.q_full), kSoftThreads);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&M.s_full[w]), 1);
+            mbar_init(smem_u32(&M.p_full[w]), 128);
+            mbar_init(smem_u32(&M.o_full[w]), 1);
+        }
+        mbar_init(smem_u32(&M.drain), 1);
+        M.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&M.tmem), kTmemCols);
+
+    // the line of tiles: each thread a run of sequences, a scan over the threads
+    const int per = (P.t.B + kAttnThreads - 1) / kAttnThreads;
+    const int b0 = min(P.t.B, tid * per), b1 = min(P.t.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of(P, b);
+        mine += (long long)s.tiles * s.blocks * P.c.kv_heads;
+        if (s.tiles == 0 && s.T != 0 && b % (int)gridDim.x == (int)blockIdx.x) {
+            // a bad sequence: NaN in the rows that it names, if it names rows
+            const int bad = seq_error(P, s.T, s.row0, s.L);
+            atomicOr(P.status, bad);
+            if (bad == SPECVERIFY_STATUS_BAD_CACHE)
+                for (int64_t r = s.row0; r < s.row0 + s.T; ++r)
+                    for (int h = 0; h < P.heads; ++h) {
+                        for (int c = 0; c < D; ++c)
+                            reinterpret_cast<uint16_t *>(P.out + r * P.o_rs + h * P.o_hs)[c] = 0x7FFF;
+                        if (P.lse) P.lse[r * P.heads + h] = NAN;
+                    }
+        }
+    }
+    long long incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) M.scan[warp] = incl;
+    tc_fence_before();
     __syncthreads();
-    if (!bad && threadIdx.x == 0)
-        for (int i = j; i >= 0; i = P.t.parent[(int64_t)b * mn + i])
-            s_mask[i >> 5] |= 1u << (i & 31);
+    tc_fence_after();
+    long long before = incl - mine, total = 0;
+    for (int i = 0; i < kAttnThreads / 32; ++i) {
+        if (i < warp) before += M.scan[i];
+        total += M.scan[i];
+    }
+    const long long ctas = min((long long)gridDim.x, total);
+    const long long lo = (int)blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
+    const long long hi = (int)blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
+    if (lo < hi && before <= lo && lo < before + mine) {
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = seq_of(P, b);
+            const long long n = (long long)s.tiles * s.blocks * P.c.kv_heads;
+            if (lo < at + n) {
+                M.b0 = b;
+                M.rest0 = (int)(lo - at);
+                break;
+            }
+            at += n;
+        }
+    }
     __syncthreads();
-    if (h >= P.heads) return;
-    const int64_t row = row0 + j;
-    const uint32_t *qr = reinterpret_cast<const uint32_t *>(P.q + row * P.q_rs + h * P.q_hs);
-    float q[2 * W], o[2 * W];
-    for (int w = 0; w < W; ++w) {
-        const float2 f = to_float2<FP16>(qr[lane + 32 * w]);
-        q[2 * w] = f.x;
-        q[2 * w + 1] = f.y;
-        o[2 * w] = o[2 * w + 1] = 0.0f;
+    Walk walk{M.b0, M.rest0, hi - lo};
+    const uint32_t tmem = M.tmem;
+    if (warp < kSoftThreads / 32) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        softmax_role<FP16, D>(P, M, smem, walk, tmem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     }
-    float m = -INFINITY, l = 0.0f;
-    const int64_t head = (int64_t)(h / P.G) * P.c.hs;
-    for (int s = 0; s < L + nodes && !bad; ++s) {
-        if (s >= L && !(s_mask[(s - L) >> 5] >> ((s - L) & 31) & 1)) continue;
-        const int64_t pg = page_of(P.c, b, s);
-        if (pg < 0) {
-            bad = SPECVERIFY_STATUS_BAD_CACHE;
-            break;
-        }
-        const int64_t off = pg * P.c.ps + head + (int64_t)(s % P.c.page) * P.c.ts;
-        const uint32_t *kr = reinterpret_cast<const uint32_t *>(P.c.k + off);
-        const uint32_t *vr = reinterpret_cast<const uint32_t *>(P.c.v + off);
-        float x = 0.0f;
-        for (int w = 0; w < W; ++w) {
-            const float2 f = to_float2<FP16>(__ldg(kr + lane + 32 * w));
-            x = fmaf(q[2 * w], f.x, fmaf(q[2 * w + 1], f.y, x));
-        }
-        for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-        x *= P.scale_log2;
-        const float mn2 = fmaxf(m, x);
-        const float keep = exp2f(m - mn2), p = exp2f(x - mn2);
-        m = mn2;
-        l = l * keep + p;
-        for (int w = 0; w < W; ++w) {
-            const float2 f = to_float2<FP16>(__ldg(vr + lane + 32 * w));
-            o[2 * w] = fmaf(p, f.x, o[2 * w] * keep);
-            o[2 * w + 1] = fmaf(p, f.y, o[2 * w + 1] * keep);
+    if (warp == kMmaWarp) {
+        if (lane == 0) mma_role<FP16, D>(P, M, smem, walk, tmem);
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
+        load_role<D>(P, &mk, &mv, M, smem, walk);
+        // the item that this CTA begins and does not end, for the joining kernel
+        if (lane == 0) {
+            AttnOwner o{};
+            Walk v = walk;
+            Segment g;
+            long long at = lo;
+            while (v.next(P, g)) {
+                if (g.first && !g.last) {
+                    const long long end = at + g.s.tiles;  // line position after the item
+                    o.pieces = (int)((end * ctas - 1) / total) - (int)blockIdx.x + 1;
+                    o.rows = g.rows;
+                    o.first_row = g.block * 2 * kTile;
+                    o.head = g.head;
+                    o.row0 = g.s.row0;
+                }
+                at += g.n;
+            }
+            P.owner[blockIdx.x] = o;
         }
     }
-    if (bad && lane == 0) atomicOr(P.status, bad);
-    const float inv = bad ? NAN : 1.0f / l;
-    uint32_t *orow = reinterpret_cast<uint32_t *>(P.out + row * P.o_rs + h * P.o_hs);
-    for (int w = 0; w < W; ++w)
-        orow[lane + 32 * w] = from_float2<FP16>(o[2 * w] * inv, o[2 * w + 1] * inv);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
+}
+
+// Joins the pieces of the items that were cut: block (c, i) the rows 8 i .. of
+// the item that CTA c began, a warp a row. Piece 0 is c's last segment, the
+// next CTAs' first segments follow.
+constexpr int kJoinWarps = 8;
+
+template <bool FP16, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const AttnOwner o = P.owner[blockIdx.x];
+    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (o.pieces == 0 || r >= o.rows) return;
+    const auto at = [&](int i) -> int64_t {
+        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * (2 * kTile) + r;
+    };
+    float m = -INFINITY;
+    for (int i = lane; i < o.pieces; i += 32) m = fmaxf(m, P.piece_ml[at(i)].x);
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    constexpr int W = D / 32;
+    float l = 0.0f, f[W] = {};
+#pragma unroll 4
+    for (int i = 0; i < o.pieces; ++i) {
+        const float2 ml = P.piece_ml[at(i)];
+        const float wgt = ml.x == -INFINITY ? 0.0f : fmaxf(ex2_approx(ml.x - m), kTiny);
+        l = fmaf(ml.y, ml.x == -INFINITY ? 1.0f : wgt, l);  // a NaN sum stays one
+        const float *src = P.piece_o + at(i) * D + lane * W;
+        float x[W];
+        if (W == 4)
+            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src);
+        else
+            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src);
+#pragma unroll
+        for (int c = 0; c < W; ++c) f[c] = fmaf(x[c], wgt, f[c]);
+    }
+    const int gr = o.first_row + r, node = gr / P.G, h = o.head * P.G + gr - node * P.G;
+    const int64_t row = o.row0 + node;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(P.out + row * P.o_rs + (int64_t)h * P.o_hs) +
+                    lane * (W / 2);
+#pragma unroll
+    for (int c = 0; c < W / 2; ++c) dst[c] = pack_half<FP16>(f[2 * c] * inv, f[2 * c + 1] * inv);
     if (P.lse && lane == 0)
-        P.lse[row * P.heads + h] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
+        P.lse[row * P.heads + h] = (m + log2f(l) - Range<FP16>::kShift) * 0.6931471805599453f;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn g_encode = nullptr;
+
+template <bool FP16, int D>
+cudaError_t launch(const TreeAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int ctas,
+                   cudaStream_t s) {
+    tree_attn_kernel<FP16, D><<<ctas, kAttnThreads, Shape<D>::kSmem, s>>>(p, mk, mv);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int most = std::min((int64_t)2 * kTile, (int64_t)p.t.max_nodes * p.G);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((most + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<FP16, D>, p);
+}
+
+template <bool FP16, int D>
+cudaError_t prepare() {
+    return cudaFuncSetAttribute(tree_attn_kernel<FP16, D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
 }
 
 }  // namespace
 
-cudaError_t prepare_tree() { return cudaSuccess; }
+bool cache_map(const CacheParams &c, const char *base, int box, CUtensorMap *map) {
+    const cuuint64_t dim[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.kv_heads,
+                               (cuuint64_t)c.num_pages};
+    // the stride of a dimension of one is never used, but has to be a legal one
+    const cuuint64_t stride[3] = {(cuuint64_t)c.ts, (cuuint64_t)(c.kv_heads > 1 ? c.hs : c.ts),
+                                  (cuuint64_t)(c.num_pages > 1 ? c.ps : c.ts)};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+    return g_encode(map,
+                    c.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<char *>(base), dim, stride, boxes, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
-cudaError_t launch_tree_attention(const TreeAttnParams &p, int num_sms, cudaStream_t s) {
-    (void)num_sms;
-    const dim3 grid((p.heads + kRowWarps - 1) / kRowWarps, p.t.max_nodes, p.t.B);
-    if (p.c.fp16 && p.c.d == 128)
-        tree_attn_kernel<true, 128><<<grid, kRowWarps * 32, 0, s>>>(p);
-    else if (p.c.fp16)
-        tree_attn_kernel<true, 64><<<grid, kRowWarps * 32, 0, s>>>(p);
-    else if (p.c.d == 128)
-        tree_attn_kernel<false, 128><<<grid, kRowWarps * 32, 0, s>>>(p);
-    else
-        tree_attn_kernel<false, 64><<<grid, kRowWarps * 32, 0, s>>>(p);
-    return cudaGetLastError();
+int cache_box(int page) {
+    int box = kTile;
+    while (page % box != 0) box /= 2;
+    return box;
+}
+
+size_t attn_workspace(int ctas) {
+    return (size_t)ctas * 2 * 2 * kTile * (128 * sizeof(float) + sizeof(float2)) +
+           (size_t)ctas * sizeof(AttnOwner);
+}
+
+void attn_place(TreeAttnParams &p, void *ws, int ctas) {
+    const int64_t rows = (int64_t)ctas * 2 * 2 * kTile;
+    p.piece_o = static_cast<float *>(ws);
+    p.piece_ml = reinterpret_cast<float2 *>(p.piece_o + rows * 128);
+    p.owner = reinterpret_cast<AttnOwner *>(p.piece_ml + rows);
+}
+
+cudaError_t prepare_tree() {
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                               cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        g_encode = reinterpret_cast<EncodeFn>(fn);
+    }
+    cudaError_t e = prepare<false, 64>();
+    if (e == cudaSuccess) e = prepare<false, 128>();
+    if (e == cudaSuccess) e = prepare<true, 64>();
+    if (e == cudaSuccess) e = prepare<true, 128>();
+    return e;
+}
+
+cudaError_t launch_tree_attention(TreeAttnParams p, int num_sms, cudaStream_t s) {
+    CUtensorMap mk, mv;
+    p.box = cache_box(p.c.page);
+    if (!cache_map(p.c, p.c.k, p.box, &mk) || !cache_map(p.c, p.c.v, p.box, &mv))
+        return cudaErrorInvalidValue;
+    if (p.c.fp16)
+        return p.c.d == 128 ? launch<true, 128>(p, mk, mv, num_sms, s)
+                            : launch<true, 64>(p, mk, mv, num_sms, s);
+    return p.c.d == 128 ? launch<false, 128>(p, mk, mv, num_sms, s)
+                        : launch<false, 64>(p, mk, mv, num_sms, s);
 }
 
 }  // namespace sv
