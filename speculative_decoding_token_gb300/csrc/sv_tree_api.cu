@@ -63,6 +63,9 @@ int check_cache(const specverify_cache *c, int32_t B, bool one_layer) {
     const int64_t most = (int64_t)1 << 38;
     for (const int64_t s : {c->layer_stride, c->page_stride, c->head_stride, c->token_stride})
         if (s < 0 || s % 8 != 0 || s > most) return SPECVERIFY_ERR_INVALID_ARG;
+    if ((c->layers > 1 && c->layer_stride == 0) || (c->num_pages > 1 && c->page_stride == 0) ||
+        (c->kv_heads > 1 && c->head_stride == 0) || c->token_stride == 0)
+        return SPECVERIFY_ERR_INVALID_ARG;
     if (c->max_pages < 1 || c->table_stride < c->max_pages || (B > 0 && !c->page_table) ||
         (int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30))
         return SPECVERIFY_ERR_INVALID_ARG;

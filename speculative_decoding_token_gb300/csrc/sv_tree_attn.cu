@@ -10,8 +10,9 @@
 //   warps 0-3, 4-7  two softmax groups, a row a thread: S from tensor memory,
 //                   P back to it;
 //   warp 8          issues the products (one thread);
-//   warp 9          copies K and V tiles into a ring of shared-memory slots
-//                   (warps 10 and 11 only complete its warpgroup).
+//   warp 9          copies K and V tiles into a ring of shared-memory slots;
+//   warps 10, 11    go ahead of them: the next segment's Q tiles, and the check
+//                   of its pages, parents and node values.
 // The two groups take turns on the tensor core, one's softmax under the
 // other's products. Up to 128 rows share one Q tile and the groups alternate
 // over the slots' tiles (each with its own maximum, sum and O, joined at the
@@ -35,7 +36,7 @@ namespace {
 constexpr int kTile = 128;                 // rows of a Q tile, slots of a K or V tile
 constexpr int kSoftThreads = 256;
 constexpr int kAttnThreads = kSoftThreads + 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kScoutThreads = 64;
 // A softmax thread holds a row of S. A launch of 384 threads gives each 168
 // registers; the groups draw 208 and the last warpgroup keeps 80 (the sum, 496
 // a thread triple, stays below the launch's 504).
@@ -50,24 +51,31 @@ struct Shape {
     static constexpr int kSlots = D == 128 ? 5 : 10;     // ring slots of a K or V tile
     static constexpr int kRing = 2 * kTileBytes;         // after the two Q tiles
     static constexpr int kMisc = kRing + kSlots * kTileBytes;
-    static constexpr int kSmem = kMisc + 2688;
+    static constexpr int kSmem = kMisc + 2944;
     // columns of tensor memory: S of both groups, then O of both; P lies over S
     static constexpr uint32_t kS = 0, kO = 2 * kTile;
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
-struct Misc {
-    uint32_t mask[kMaxNodes][kMaskWords];  // a node's ancestors and itself
+// What the scouts say of a segment.
+struct Scouted {
     int8_t parent[kMaxNodes];
-    uint64_t full[10], empty[10], q_full, s_full[2], p_full[2], o_full[2], drain;
-    uint32_t nonfinite[kMaskWords];        // nodes of this segment whose value has an inf or NaN
+    uint32_t nonfinite[kMaskWords];        // nodes of it whose value has an inf or NaN
+    uint32_t bad;                          // a page or a parent
+};
+
+struct Misc {
+    float2 ml[2][kTile];                   // maxima and sums of both groups' rows
+    Scouted seg[2];                        // of the even and the odd segments
+    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t seg_full[2], seg_empty[2], drain;
+    long long rest0;                       // the CTA's first tile in its first sequence,
+    int32_t b0;                            // and that sequence
     uint32_t tmem;
-    int32_t b0;                            // the CTA's first sequence,
-    long long rest0;                       // and its first tile in it
     long long scan[kAttnThreads / 32];
     int32_t abort;                         // a wait gave up
 };
-static_assert(sizeof(Misc) <= 2688, "Misc");
+static_assert(sizeof(Misc) <= 2944, "Misc");
 
 // What sequence b contributes to the line of tiles; 0 tiles: idle or bad.
 struct Seq {
@@ -161,18 +169,7 @@ __device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity,
     return false;
 }
 
-// Barrier of the two softmax groups; returns whether any thread's v was true.
-__device__ __forceinline__ bool soft_any(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-
+// Barrier of the two softmax groups.
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 
 template <bool FP16>
@@ -222,73 +219,17 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
     const uint32_t ts = tmem + lanes + Sh::kS + w * kTile;
     const float c2 = P.scale_log2;
     const float ninf = -INFINITY;
-    uint32_t s_phase = 0, o_phase[2] = {0, 0};
+    uint32_t s_phase = 0, o_phase[2] = {0, 0}, seg = 0;
     uint32_t base = 0;  // ring uses before this segment
     Segment g;
-    while (walk.next(P, g)) {
-        soft_sync();  // the previous segment's reads of Q, O and the masks are over
-        const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
-        const bool tail = t_end > g.s.L;
-        const int64_t kv_off = (int64_t)g.head * P.c.hs;
-        // Q rows into their tiles, in 16-byte chunks swizzled within 8 rows
-        {
-            const int r_first = g.pair ? w * kTile : 0, r_count = min(kTile, g.rows - r_first);
-            const int t0 = g.pair ? tid & 127 : tid, tn = g.pair ? 128 : 256;
-            char *q = smem + (g.pair ? w * Sh::kTileBytes : 0);
-            constexpr int C = D / 8;
-#pragma unroll 8
-            for (int i = t0; i < r_count * C; i += tn) {
-                const int r = i / C, c = i % C;
-                const int gr = g.block * 2 * kTile + r_first + r;
-                const int node = gr / P.G, hh = gr - node * P.G;
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    P.q + (g.s.row0 + node) * P.q_rs + (int64_t)(g.head * P.G + hh) * P.q_hs + c * 16);
-                *reinterpret_cast<uint4 *>(q + (c >> 3) * Sh::kPanel + r * 128 +
-                                           (((c & 7) ^ (r & 7)) << 4)) = x;
-            }
-        }
-        fence_async_smem();
-        mbar_arrive(smem_u32(&M.q_full));
-        // pages, parents
-        bool bad_page = false, bad_tree = false;
-        for (int i = t_begin / P.c.page + tid; i <= (t_end - 1) / P.c.page; i += kSoftThreads)
-            bad_page |= page_at(P.c, g.b, i) < 0;
-        if (tail) {
-            if (tid < g.s.T) {
-                const int up = P.t.parent[(int64_t)g.b * P.t.max_nodes + tid];
-                bad_tree = tid == 0 ? up != -1 : (up < 0 || up >= tid);
-                M.parent[tid] = (int8_t)(bad_tree ? -1 : up);
-            }
-            if (tid < kMaskWords) M.nonfinite[tid] = 0;
-        }
-        if (bad_page) atomicOr(P.status, SPECVERIFY_STATUS_BAD_CACHE);
-        if (bad_tree) atomicOr(P.status, SPECVERIFY_STATUS_BAD_TREE);
-        const bool bad = soft_any(bad_page || bad_tree);
-        if (tail) {
-            if (tid < g.s.T) {
-                uint32_t m[kMaskWords] = {};
-                for (int i = tid; i >= 0; i = M.parent[i])
-#pragma unroll
-                    for (int q = 0; q < kMaskWords; ++q)
-                        if (i >> 5 == q) m[q] |= 1u << (i & 31);
-#pragma unroll
-                for (int q = 0; q < kMaskWords; ++q) M.mask[tid][q] = m[q];
-            }
-            if (!bad_page && !bad) {
-                constexpr int C = D / 8;
-                const int j0 = max(0, t_begin - g.s.L), j1 = t_end - g.s.L;
-                for (int i = tid; i < (j1 - j0) * C; i += kSoftThreads) {
-                    const int j = j0 + i / C, s = g.s.L + j;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(
-                        P.c.v + kv_off + page_of(P.c, g.b, s) * P.c.ps +
-                        (int64_t)(s % P.c.page) * P.c.ts + i % C * 16);
-                    if (nonfinite_bits<FP16>(x.x) | nonfinite_bits<FP16>(x.y) |
-                        nonfinite_bits<FP16>(x.z) | nonfinite_bits<FP16>(x.w))
-                        atomicOr(&M.nonfinite[j >> 5], 1u << (j & 31));
-                }
-            }
-            soft_sync();
-        }
+    for (; walk.next(P, g); ++seg) {
+        const int t_begin = g.tile0 * kTile;
+        const Scouted &sc = M.seg[seg & 1];
+        bool scouted = false;
+        const auto wait_scout = [&] {
+            if (!scouted) wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P.status);
+            scouted = true;
+        };
         // this thread's row
         const int r_item = (g.pair ? w * kTile : 0) + row;
         const int gr = g.block * 2 * kTile + min(r_item, g.rows - 1);
@@ -309,9 +250,19 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                 for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
                 tmem_wait_ld();
                 if (tail_tile) {
+                    wait_scout();
+                    uint32_t up[kMaskWords] = {};  // the node's ancestors and itself
+                    for (int i = node; i >= 0; i = sc.parent[i])
+#pragma unroll
+                        for (int q = 0; q < kMaskWords; ++q)
+                            if (i >> 5 == q) up[q] |= 1u << (i & 31);
                     const int shift = t0 - g.s.L;  // column c is node c + shift, a token before 0
                     const auto word = [&](int i) -> uint32_t {
-                        return i < 0 ? 0xffffffffu : (i >= kMaskWords ? 0u : M.mask[node][i]);
+                        uint32_t x = i < 0 ? 0xffffffffu : 0u;
+#pragma unroll
+                        for (int q = 0; q < kMaskWords; ++q)
+                            if (i == q) x = up[q];
+                        return x;
                     };
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -414,16 +365,16 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
         float mf = m_ref, lf = l;
         if (!g.pair) {
             // join the groups: each takes half of the columns
-            float2 *ml = reinterpret_cast<float2 *>(smem + Sh::kTileBytes);  // the unused Q tile
-            ml[w * kTile + row] = make_float2(m_ref, l);
+            M.ml[w][row] = make_float2(m_ref, l);
             soft_sync();
-            const float2 a = ml[row], b = ml[kTile + row];
+            const float2 a = M.ml[0][row], b = M.ml[1][row];
             mf = fmaxf(a.x, b.x);
             wgt[0] = a.x == ninf ? 0.0f : fmaxf(ex2_approx(a.x - mf), kTiny);
             wgt[1] = b.x == ninf ? 0.0f : fmaxf(ex2_approx(b.x - mf), kTiny);
             lf = a.y * wgt[0] + (used1 ? b.y * wgt[1] : 0.0f);
         }
-        if (bad) lf = NAN;
+        wait_scout();
+        if (sc.bad) lf = NAN;
         if (warp_on) {
             const bool whole = g.first && g.last;
             const bool mine = r_item < g.rows;
@@ -433,10 +384,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
             const int piece = g.first ? 1 : 0;  // a CTA's first and last segments may be pieces
             const int64_t at = ((int64_t)blockIdx.x * 2 + piece) * (2 * kTile) + r_item;
             bool any_odd = false;
-            if (tail)
 #pragma unroll
-                for (int q = 0; q < kMaskWords; ++q)
-                    any_odd |= (M.nonfinite[q] & M.mask[node][q]) != 0;
+            for (int q = 0; q < kMaskWords; ++q) any_odd |= sc.nonfinite[q] != 0;
 #pragma unroll 1
             for (int c = c_begin; c < c_end; c += 32) {
                 uint32_t o[32];
@@ -453,11 +402,11 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                 }
                 if (any_odd && mine) {
                     // a seen inf or NaN decides its element whatever its weight
-                    for (int j = 0; j < g.s.T; ++j) {
-                        if (!(M.nonfinite[j >> 5] & M.mask[node][j >> 5] & (1u << (j & 31)))) continue;
+                    for (int j = node; j >= 0; j = sc.parent[j]) {
+                        if (!(sc.nonfinite[j >> 5] >> (j & 31) & 1)) continue;
                         const int s = g.s.L + j;
                         const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                            P.c.v + kv_off + page_of(P.c, g.b, s) * P.c.ps +
+                            P.c.v + (int64_t)g.head * P.c.hs + page_of(P.c, g.b, s) * P.c.ps +
                             (int64_t)(s % P.c.page) * P.c.ts + c * 2);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -495,6 +444,82 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
             }
         }
         tc_fence_before();
+        mbar_arrive(smem_u32(&M.seg_empty[seg & 1]));
+        if (!g.pair) soft_sync();  // both have read both groups' O
+    }
+}
+
+// ---------------------------------------------------------------------------
+// scouts: Q tiles, pages, parents and values, a segment ahead
+
+template <bool FP16, int D>
+__device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk) {
+    using Sh = Shape<D>;
+    constexpr int C = D / 8;  // 16-byte chunks of a row
+    const int tid = threadIdx.x - (kAttnThreads - kScoutThreads);
+    const uint32_t q = smem_u32(smem);
+    uint32_t seg = 0, uses[2] = {0, 0}, turn = 0;
+    Segment g;
+    for (; walk.next(P, g); ++seg) {
+        // Q rows into their tiles, 16-byte chunks swizzled within 8 rows
+        for (int i = 0; i < (g.pair ? 2 : 1); ++i) {
+            const int x = g.pair ? i : turn;
+            wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status);
+            const int r_first = i * kTile, r_count = min(kTile, g.rows - r_first);
+            const int c = tid % C;
+            for (int r = tid / C; r < r_count; r += kScoutThreads / C) {
+                const int gr = g.block * 2 * kTile + r_first + r;
+                const int node = gr / P.G, hh = gr - node * P.G;
+                const char *src = P.q + (g.s.row0 + node) * P.q_rs +
+                                  (int64_t)(g.head * P.G + hh) * P.q_hs + c * 16;
+                const uint32_t dst = q + x * Sh::kTileBytes + (c >> 3) * Sh::kPanel + r * 128 +
+                                     (((c & 7) ^ (r & 7)) << 4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            mbar_arrive(smem_u32(&M.q_full[x]));
+        }
+        if (!g.pair) turn ^= 1;
+        // pages and parents
+        wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status);
+        Scouted &sc = M.seg[seg & 1];
+        const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
+        const bool tail = t_end > g.s.L;
+        int bad = 0;
+        for (int i = t_begin / P.c.page + tid; i <= (t_end - 1) / P.c.page; i += kScoutThreads)
+            if (page_at(P.c, g.b, i) < 0) bad |= SPECVERIFY_STATUS_BAD_CACHE;
+        if (tail)
+            for (int j = tid; j < g.s.T; j += kScoutThreads) {
+                const int up = P.t.parent[(int64_t)g.b * P.t.max_nodes + j];
+                const bool no = j == 0 ? up != -1 : (up < 0 || up >= j);
+                sc.parent[j] = (int8_t)(no ? -1 : up);
+                if (no) bad |= SPECVERIFY_STATUS_BAD_TREE;
+            }
+        if (tid < kMaskWords) sc.nonfinite[tid] = 0;
+        if (tid == 0) sc.bad = 0;
+        asm volatile("barrier.cta.sync 2, 64;" ::: "memory");
+        if (bad) {
+            atomicOr(P.status, bad);
+            sc.bad = 1;
+        }
+        if (tail) {
+            const int j0 = max(0, t_begin - g.s.L), j1 = t_end - g.s.L;
+#pragma unroll 4
+            for (int i = tid; i < (j1 - j0) * C; i += kScoutThreads) {
+                const int j = j0 + i / C, s = g.s.L + j;
+                const int64_t page = page_of(P.c, g.b, s);
+                if (page < 0) continue;
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    P.c.v + (int64_t)g.head * P.c.hs + page * P.c.ps +
+                    (int64_t)(s % P.c.page) * P.c.ts + i % C * 16);
+                if (nonfinite_bits<FP16>(x.x) | nonfinite_bits<FP16>(x.y) |
+                    nonfinite_bits<FP16>(x.z) | nonfinite_bits<FP16>(x.w))
+                    atomicOr(&sc.nonfinite[j >> 5], 1u << (j & 31));
+            }
+        }
+        mbar_arrive(smem_u32(&M.seg_full[seg & 1]));
     }
 }
 
@@ -506,22 +531,22 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
     using Sh = Shape<D>;
     constexpr uint32_t dqk = mma_desc(FP16, false, kTile, kTile), dpv = mma_desc(FP16, true, kTile, D);
     const uint32_t q0 = smem_u32(smem), ring = q0 + Sh::kRing;
-    uint32_t base = 0, q_phase = 0, p_phase[2] = {0, 0};
+    uint32_t base = 0, uses[2] = {0, 0}, turn = 0, p_phase[2] = {0, 0};
     Segment g;
     bool ok = true;
     while (ok && walk.next(P, g)) {
-        ok = wait_on(M, M.q_full, q_phase, P.status);
-        q_phase ^= 1;
         const int steps = g.pair ? 2 * g.n : g.n;
         // step t: group t % 2, tile t (or t / 2 when both groups take every tile)
         const auto qk = [&](int t) {
             const int j = g.pair ? t >> 1 : t, w = t & 1;
             const uint32_t use = base + k_at(g, j), slot = use % Sh::kSlots;
+            const int x = g.pair ? w : turn;
+            if (t == 0 || (g.pair && t == 1)) ok = wait_on(M, M.q_full[x], uses[x]++ & 1, P.status);
             if (!g.pair || w == 0)
                 ok = ok && wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t a = q0 + (g.pair ? w * Sh::kTileBytes : 0), b = ring + slot * Sh::kTileBytes;
+            const uint32_t a = q0 + x * Sh::kTileBytes, b = ring + slot * Sh::kTileBytes;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * Sh::kPanel + (k & 3) * 32;
@@ -529,6 +554,7 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
                        k > 0);
             }
             mma_commit(smem_u32(&M.s_full[w]));
+            if (g.pair ? t + 2 >= steps : t + 1 == steps) mma_commit(smem_u32(&M.q_empty[x]));
             if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]));
         };
         if (ok) qk(0);
@@ -552,6 +578,7 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             if (t + 2 < steps) qk(t + 2);
         }
         base += 2 * g.n;
+        if (!g.pair) turn ^= 1;
     }
     if (!ok) {  // no product outlives the CTA
         mma_commit(smem_u32(&M.drain));
@@ -631,8 +658,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(smem_u32(&M.full[i]), 1);
             mbar_init(smem_u32(&M.empty[i]), 1);
         }
-        mbar_init(smem_u32(&M.q_full), kSoftThreads);
         for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&M.q_full[w]), kScoutThreads);
+            mbar_init(smem_u32(&M.q_empty[w]), 1);
+            mbar_init(smem_u32(&M.seg_full[w]), kScoutThreads);
+            mbar_init(smem_u32(&M.seg_empty[w]), kSoftThreads);
             mbar_init(smem_u32(&M.s_full[w]), 1);
             mbar_init(smem_u32(&M.p_full[w]), 128);
             mbar_init(smem_u32(&M.o_full[w]), 1);
@@ -705,6 +735,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == kMmaWarp) {
         if (lane == 0) mma_role<FP16, D>(P, M, smem, walk, tmem);
         __syncwarp();
+    } else if (warp > kLoadWarp) {
+        scout_role<FP16, D>(P, M, smem, walk);
     } else if (warp == kLoadWarp) {
         load_role<D>(P, &mk, &mv, M, smem, walk);
         // the item that this CTA begins and does not end, for the joining kernel

@@ -70,12 +70,17 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _ints(name, t, device, shape=None, dtype=torch.int32):
-    """A contiguous integer tensor on `device`."""
-    _need(t.dtype == dtype and t.is_contiguous(), f"{name} must be a contiguous {dtype} tensor")
-    _need(t.device == device, f"{name} is on {t.device}, not on {device}")
-    _need(shape is None or tuple(t.shape) == shape, f"{name} must have shape {shape}, not {tuple(t.shape)}")
+def _ints(name, t, index, shape, dtype=torch.int32):
+    """The address of a contiguous integer tensor of that shape on CUDA device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _strides(t):
+    """Strides with 0 for dimensions of one, whose stride says nothing."""
+    return tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride()))
 
 
 class KVCache:
@@ -90,7 +95,7 @@ class KVCache:
     def __init__(self, k, v, page_table, mass=None, pos=None):
         _need(k.dim() in (4, 5) and v.shape == k.shape, "k and v must have one shape, [(layers,) pages, heads, page, d]")
         _need(k.dtype in _DTYPES and v.dtype == k.dtype, "k and v must both be bfloat16 or both float16")
-        _need(k.stride() == v.stride() and k.stride(-1) == 1, "k and v must have the same strides and a contiguous head")
+        _need(_strides(k) == _strides(v) and k.stride(-1) == 1, "k and v must have the same strides and a contiguous head")
         _need(k.is_cuda and v.device == k.device, "k and v must be on one CUDA device")
         _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.stride(1) == 1
               and page_table.device == k.device, "page_table must be int32 [B, pages] on the cache's device")
@@ -99,20 +104,24 @@ class KVCache:
         _need(page >= 8 and page % 8 == 0, "the page size must be a multiple of 8")
         _need(pages >= 1 and heads >= 1 and page_table.shape[1] >= 1, "the cache is empty")
         _need(k.dim() == 4 or k.shape[0] >= 1, "the cache has no layers")
-        _need(all(s % 8 == 0 for s in k.stride()[:-1]) and k.data_ptr() % 16 == 0 and v.data_ptr() % 16 == 0,
+        ks = _strides(k)
+        _need(all(s % 8 == 0 for s in ks[:-1]) and k.data_ptr() % 16 == 0 and v.data_ptr() % 16 == 0,
               "k and v must be aligned to 16 bytes, strides and all")
+        _need(all(s > 0 or n == 1 for s, n in zip(ks, k.shape)), "k and v must not be expanded")
         for name, t, dt in (("mass", mass, torch.float32), ("pos", pos, torch.int32)):
             if t is not None:
                 _need(t.dtype == dt and t.shape == k.shape[:-1] and t.device == k.device,
                       f"{name} must be {dt}, of k's shape without the head, on its device")
-        _need(mass is None or pos is None or mass.stride() == pos.stride(), "mass and pos must have the same strides")
+                _need(all(s > 0 or n == 1 for s, n in zip(t.stride(), t.shape)), f"{name} must not be expanded")
+        _need(mass is None or pos is None or _strides(mass) == _strides(pos), "mass and pos must have the same strides")
         self.k, self.v, self.page_table, self.mass, self.pos = k, v, page_table, mass, pos
         self.device, self.dtype, self.head_dim, self.kv_heads = k.device, k.dtype, d, heads
+        self.index = k.get_device()
         self.layers, self.batch = (k.shape[0] if k.dim() == 5 else 1), page_table.shape[0]
         self.capacity = page * page_table.shape[1]
         self.values = next((t for t in (mass, pos) if t is not None), None)
-        ks = (0,) * (5 - k.dim()) + k.stride()
-        ms = (0,) * 4 if self.values is None else (0,) * (5 - k.dim()) + self.values.stride()
+        ks = (0,) * (5 - k.dim()) + ks
+        ms = (0,) * 4 if self.values is None else (0,) * (5 - k.dim()) + _strides(self.values)
         self.struct = SpecverifyCache(
             _DTYPES[k.dtype], self.layers, pages, page, heads, d, k.data_ptr(), v.data_ptr(), *ks[:4],
             None if mass is None else mass.data_ptr(), None if pos is None else pos.data_ptr(), *ms,
@@ -128,13 +137,13 @@ class TokenTree:
     def __init__(self, row_off, nodes, parent, tokens=None):
         _need(parent.dim() == 2 and 1 <= parent.shape[1] <= MAX_NODES, f"parent must be [B, 1 to {MAX_NODES}]")
         _need(parent.is_cuda, "a tree's buffers must be on a CUDA device")
-        B, device = parent.shape[0], parent.device
-        self.batch, self.max_nodes, self.device = B, parent.shape[1], device
+        B, index = parent.shape[0], parent.get_device()
+        self.batch, self.max_nodes, self.device, self.index = B, parent.shape[1], parent.device, index
         self.row_off, self.nodes, self.parent, self.tokens = row_off, nodes, parent, tokens
         self.struct = SpecverifyTree(
-            B, self.max_nodes, _ints("row_off", row_off, device, (B,), torch.int64), _ints("nodes", nodes, device, (B,)),
-            _ints("parent", parent, device),
-            None if tokens is None else _ints("tokens", tokens, device, (B, self.max_nodes)))
+            B, self.max_nodes, _ints("row_off", row_off, index, (B,), torch.int64), _ints("nodes", nodes, index, (B,)),
+            _ints("parent", parent, index, parent.shape),
+            None if tokens is None else _ints("tokens", tokens, index, parent.shape))
         self.ref = ctypes.byref(self.struct)
 
 
@@ -164,11 +173,12 @@ class SpecTree:
             self.close()
 
     def _stream(self, stream):
-        return (torch.cuda.current_stream(self.index) if stream is None else stream).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index) if stream is None else stream.cuda_stream
 
     def _on(self, *described):
         for x in described:
-            _need(x.device == self.device, f"the handle is on {self.device}, the call's buffers on {x.device}")
+            if x.index != self.index:
+                raise ValueError(f"the handle is on {self.device}, the call's buffers on {x.device}")
 
     def _empty(self, stream, shape, dtype):
         if stream is None:
@@ -177,15 +187,21 @@ class SpecTree:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def _rows(self, name, x, cache):
-        _need(x.dim() == 3 and x.dtype == cache.dtype and x.shape[2] == cache.head_dim and x.stride(2) == 1,
-              f"{name} must be [rows, heads, {cache.head_dim}] of the cache's dtype with a contiguous head")
-        _need(x.device == self.device, f"{name} is on {x.device}, not on {self.device}")
-        _need(x.shape[1] % cache.kv_heads == 0 and x.shape[1] > 0, f"{name}: heads must be a multiple of the cache's")
-        return x.data_ptr(), x.stride(0), x.stride(1)
+        """Address, rows, heads and strides of queries or outputs."""
+        rows, heads, d = x.shape
+        if (x.dtype is not cache.dtype or d != cache.head_dim or x.get_device() != self.index or heads < 1
+                or heads % cache.kv_heads):
+            raise ValueError(f"{name} must be [rows, heads, {cache.head_dim}] of {cache.dtype} on {self.device}, heads a "
+                             f"multiple of {cache.kv_heads}, not {x.dtype} {tuple(x.shape)} on {x.device}")
+        a, b, one = x.stride()
+        if one != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+        return x.data_ptr(), rows, heads, a if rows > 1 else 0, b if heads > 1 else 0
 
     def _lse(self, lse, rows, heads):
-        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
-              and lse.shape[0] == rows and lse.shape[1] == heads, "lse must be contiguous float32 [rows, heads]")
+        if (lse.dtype is not torch.float32 or lse.shape != (rows, heads) or lse.get_device() != self.index
+                or not lse.is_contiguous()):
+            raise ValueError(f"lse must be contiguous float32 [{rows}, {heads}] on {self.device}")
         return lse.data_ptr()
 
     def attention(self, q, cache: KVCache, tree: TokenTree, lens, *, scale=None, out=None, lse=None, stream=None):
@@ -194,37 +210,44 @@ class SpecTree:
         ``q`` [rows, heads, head size], ``lens`` int32 [B]: committed tokens; ``scale`` defaults to head size ** -0.5.
         ``out`` and ``lse``: buffers to use. Rows that belong to no sequence are not written."""
         self._on(cache, tree)
-        B, d = tree.batch, cache.head_dim
-        _need(cache.layers == 1, "attention takes one layer's cache")
-        _need(cache.batch == B, "the page table and the tree must have the same sequences")
-        qp, qr, qh = self._rows("q", q, cache)
+        B = tree.batch
+        if cache.layers != 1 or cache.batch != B:
+            raise ValueError("attention takes one layer's cache with a page table row for each sequence of the tree")
+        qp, rows, heads, qr, qh = self._rows("q", q, cache)
         if out is None:
             out = self._empty(stream, q.shape, q.dtype)
-        _need(out.shape == q.shape, "out must have q's shape")
-        op, orow, oh = self._rows("out", out, cache)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        op, _, _, orow, oh = self._rows("out", out, cache)
         if lse is None:
-            lse = self._empty(stream, q.shape[:2], torch.float32)
-        self.check(self.lib.specverify_tree_attention(
-            self.h, cache.ref, tree.ref, _ints("lens", lens, self.device, (B,)), qp, q.shape[0], q.shape[1], qr, qh,
-            d ** -0.5 if scale is None else scale, op, orow, oh, self._lse(lse, q.shape[0], q.shape[1]),
-            self._stream(stream)), "specverify_tree_attention")
+            lse = self._empty(stream, (rows, heads), torch.float32)
+        rc = self.lib.specverify_tree_attention(
+            self.h, cache.ref, tree.ref, _ints("lens", lens, self.index, (B,)), qp, rows, heads, qr, qh,
+            cache.head_dim ** -0.5 if scale is None else scale, op, orow, oh, self._lse(lse, rows, heads),
+            self._stream(stream))
+        if rc:
+            self.check(rc, "specverify_tree_attention")
         return out, lse
 
     def verify(self, tree: TokenTree, target, *, n=None, tokens=None, path=None, stream=None):
         """Greedy verify of the trees against target logits [rows, V] (float32 or bfloat16, rows aligned to 16 bytes);
         returns (n_accepted [B], emitted tokens [B, max nodes], accepted path [B, max nodes]), padded with -1."""
         self._on(tree)
-        _need(tree.tokens is not None, "the tree has no tokens")
-        _need(target.dim() == 2 and target.dtype in _LOGITS and target.stride(1) == 1 and target.device == self.device,
-              "target must be 2-D float32 or bfloat16 logits with unit column stride on the handle's device")
-        B, T = tree.batch, tree.max_nodes
+        if (tree.tokens is None or target.dim() != 2 or target.dtype not in _LOGITS or target.stride(1) != 1
+                or target.get_device() != self.index):
+            raise ValueError("verify takes a tree with tokens and 2-D float32 or bfloat16 logits with unit column stride on "
+                             f"{self.device}")
+        B, T, at = tree.batch, tree.max_nodes, self.index
         n = self._empty(stream, (B,), torch.int32) if n is None else n
         tokens = self._empty(stream, (B, T), torch.int32) if tokens is None else tokens
         path = self._empty(stream, (B, T), torch.int32) if path is None else path
-        self.check(self.lib.specverify_verify_tree(
-            self.h, tree.ref, target.data_ptr(), _LOGITS[target.dtype], target.shape[1], target.stride(0), target.shape[0],
-            _ints("n", n, self.device, (B,)), _ints("tokens", tokens, self.device, (B, T)),
-            _ints("path", path, self.device, (B, T)), self._stream(stream)), "specverify_verify_tree")
+        rows, V = target.shape
+        rc = self.lib.specverify_verify_tree(
+            self.h, tree.ref, target.data_ptr(), _LOGITS[target.dtype], V, target.stride(0) if rows > 1 else -(-V // 8) * 8,
+            rows, _ints("n", n, at, (B,)), _ints("tokens", tokens, at, (B, T)), _ints("path", path, at, (B, T)),
+            self._stream(stream))
+        if rc:
+            self.check(rc, "specverify_verify_tree")
         return n, tokens, path
 
     def commit(self, cache: KVCache, lens, n, path, *, seen=None, new_lens=None, new_seen=None, stream=None):
@@ -232,35 +255,37 @@ class SpecTree:
         (new_lens, new_seen). ``seen`` int32 [B], the tokens of each sequence so far, is needed where the cache has
         ``pos``; new_seen is None without it."""
         self._on(cache)
-        B = cache.batch
-        _need(path.dim() == 2 and 1 <= path.shape[1] <= MAX_NODES, f"path must be [B, 1 to {MAX_NODES}]")
-        _need(seen is not None or cache.pos is None, "a cache with positions needs `seen`")
+        B, at = cache.batch, self.index
+        if path.dim() != 2 or not 1 <= path.shape[1] <= MAX_NODES:
+            raise ValueError(f"path must be [B, 1 to {MAX_NODES}]")
+        if seen is None and cache.pos is not None:
+            raise ValueError("a cache with positions needs `seen`")
         new_lens = self._empty(stream, (B,), torch.int32) if new_lens is None else new_lens
         if seen is not None and new_seen is None:
             new_seen = self._empty(stream, (B,), torch.int32)
-        dev = self.device
-        self.check(self.lib.specverify_tree_commit(
-            self.h, cache.ref, B, path.shape[1], _ints("lens", lens, dev, (B,)),
-            None if seen is None else _ints("seen", seen, dev, (B,)), _ints("n", n, dev, (B,)),
-            _ints("path", path, dev, (B, path.shape[1])), _ints("new_lens", new_lens, dev, (B,)),
-            None if new_seen is None else _ints("new_seen", new_seen, dev, (B,)), self._stream(stream)),
-            "specverify_tree_commit")
+        T = path.shape[1]
+        rc = self.lib.specverify_tree_commit(
+            self.h, cache.ref, B, T, _ints("lens", lens, at, (B,)), None if seen is None else _ints("seen", seen, at, (B,)),
+            _ints("n", n, at, (B,)), _ints("path", path, at, (B, T)), _ints("new_lens", new_lens, at, (B,)),
+            None if new_seen is None else _ints("new_seen", new_seen, at, (B,)), self._stream(stream))
+        if rc:
+            self.check(rc, "specverify_tree_commit")
         return new_lens, new_seen
 
     def accumulate(self, q, lse, cache: KVCache, tree: TokenTree, lens, n, path, *, scale=None, stream=None):
         """Adds to the cache's ``mass`` the attention weight that the accepted nodes gave each slot; ``q`` and ``lse`` are
         those of :meth:`attention`, ``lens`` the lengths before the commit, which has run. Returns the mass."""
         self._on(cache, tree)
-        B = tree.batch
-        _need(cache.layers == 1 and cache.mass is not None, "accumulate takes one layer's cache with its mass")
-        _need(cache.batch == B, "the page table and the tree must have the same sequences")
-        qp, qr, qh = self._rows("q", q, cache)
-        dev = self.device
-        self.check(self.lib.specverify_cache_accumulate(
-            self.h, cache.ref, tree.ref, _ints("lens", lens, dev, (B,)), _ints("n", n, dev, (B,)),
-            _ints("path", path, dev, (B, tree.max_nodes)), qp, q.shape[0], q.shape[1], qr, qh,
-            self._lse(lse, q.shape[0], q.shape[1]), cache.head_dim ** -0.5 if scale is None else scale,
-            self._stream(stream)), "specverify_cache_accumulate")
+        B, at = tree.batch, self.index
+        if cache.layers != 1 or cache.mass is None or cache.batch != B:
+            raise ValueError("accumulate takes one layer's cache, its mass and a page table row for each sequence of the tree")
+        qp, rows, heads, qr, qh = self._rows("q", q, cache)
+        rc = self.lib.specverify_cache_accumulate(
+            self.h, cache.ref, tree.ref, _ints("lens", lens, at, (B,)), _ints("n", n, at, (B,)),
+            _ints("path", path, at, (B, tree.max_nodes)), qp, rows, heads, qr, qh, self._lse(lse, rows, heads),
+            cache.head_dim ** -0.5 if scale is None else scale, self._stream(stream))
+        if rc:
+            self.check(rc, "specverify_cache_accumulate")
         return cache.mass
 
     def evict(self, cache: KVCache, lens, seen, budget: int, *, sink: int = 0, recent: int = 0, mass_out=None, pos_out=None,
@@ -270,18 +295,21 @@ class SpecTree:
         default to the cache's own. Returns (mass_out, pos_out, new_lens). The handle's ``max_moves`` must be at least
         layers * B * kv heads * min(budget, slots of a sequence - budget)."""
         self._on(cache)
-        B, dev = cache.batch, self.device
-        _need(cache.mass is not None and cache.pos is not None, "evict needs the cache's mass and pos")
+        B, at = cache.batch, self.index
+        if cache.mass is None or cache.pos is None:
+            raise ValueError("evict needs the cache's mass and pos")
         mass_out = cache.mass if mass_out is None else mass_out
         pos_out = cache.pos if pos_out is None else pos_out
         for name, t, like in (("mass_out", mass_out, cache.mass), ("pos_out", pos_out, cache.pos)):
-            _need(t.dtype == like.dtype and t.shape == like.shape and t.stride() == like.stride() and t.device == dev,
-                  f"{name} must be laid out as the cache's")
+            if t is not like and (t.dtype is not like.dtype or t.shape != like.shape or t.stride() != like.stride()
+                                  or t.get_device() != at):
+                raise ValueError(f"{name} must be laid out as the cache's")
         new_lens = self._empty(stream, (B,), torch.int32) if new_lens is None else new_lens
-        self.check(self.lib.specverify_cache_evict(
-            self.h, cache.ref, B, _ints("lens", lens, dev, (B,)), _ints("seen", seen, dev, (B,)), budget, sink, recent,
-            mass_out.data_ptr(), pos_out.data_ptr(), _ints("new_lens", new_lens, dev, (B,)), self._stream(stream)),
-            "specverify_cache_evict")
+        rc = self.lib.specverify_cache_evict(
+            self.h, cache.ref, B, _ints("lens", lens, at, (B,)), _ints("seen", seen, at, (B,)), budget, sink, recent,
+            mass_out.data_ptr(), pos_out.data_ptr(), _ints("new_lens", new_lens, at, (B,)), self._stream(stream))
+        if rc:
+            self.check(rc, "specverify_cache_evict")
         return mass_out, pos_out, new_lens
 
     def device_status(self, stream=None) -> int:
