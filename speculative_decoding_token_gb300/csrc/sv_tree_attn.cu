@@ -12,19 +12,20 @@
 //   warp 8          issues the products (one thread);
 //   warp 9          copies K and V tiles into a ring of shared-memory slots;
 //   warps 10, 11    go ahead of them: the next segment's Q tiles, and the check
-//                   of its pages, parents and node values.
+//                   of its pages and parents.
 // The two groups take turns on the tensor core, one's softmax under the
 // other's products. Up to 128 rows share one Q tile and the groups alternate
 // over the slots' tiles (each with its own maximum, sum and O, joined at the
 // end); more rows make two Q tiles, a group each, over the same slots.
 //
-// All (sequence, key head, block of rows) items' tiles of 128 slots form one
-// line that is cut evenly over the CTAs. An item cut in pieces leaves each
+// All (sequence, key head, block of rows) items' tiles of 128 slots, with a
+// constant for each item's start, form one line that is cut evenly over the CTAs. An item cut in pieces leaves each
 // piece's O (not yet divided), maximum and sum in the workspace, and a second
 // kernel joins the pieces; whole items are written directly.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "sv_tcgen05.cuh"
 #include "sv_tree.h"
@@ -57,7 +58,7 @@ struct Shape {
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
-// What the scouts say of a segment.
+// What the scouts say of a segment, and whoever clears its last values.
 struct Scouted {
     int8_t parent[kMaxNodes];
     uint32_t nonfinite[kMaskWords];        // nodes of it whose value has an inf or NaN
@@ -77,10 +78,18 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 2944, "Misc");
 
-// What sequence b contributes to the line of tiles; 0 tiles: idle or bad.
+// An item's place on the line starts with kHead units that are no tiles: what
+// its start and end cost beside its tiles (queries, sums, the output).
+constexpr int kHead = 2;
+
+// What sequence b contributes to the line; 0 tiles: idle or bad.
 struct Seq {
     int L, T, tiles, blocks;
     int64_t row0;
+
+    __device__ long long units(const TreeAttnParams &P) const {
+        return tiles ? (long long)(tiles + kHead) * blocks * P.c.kv_heads : 0;
+    }
 };
 
 __device__ __forceinline__ int seq_error(const TreeAttnParams &P, int nodes, int64_t row0, int L) {
@@ -116,31 +125,35 @@ struct Segment {
 
 struct Walk {
     int b;
-    long long rest;   // next tile within sequence b
-    long long left;   // tiles of this CTA still to do
+    long long rest;   // next unit within sequence b
+    long long left;   // units of this CTA still to do
 
     __device__ bool next(const TreeAttnParams &P, Segment &g) {
-        if (left <= 0) return false;
-        for (;;) {
+        while (left > 0) {
             g.s = seq_of(P, b);
-            const long long all = (long long)g.s.tiles * g.s.blocks * P.c.kv_heads;
-            if (rest < all) break;
-            rest = 0;
-            ++b;
+            if (rest >= g.s.units(P)) {
+                rest = 0;
+                ++b;
+                continue;
+            }
+            const int len = g.s.tiles + kHead;
+            const int item = (int)(rest / len), u = (int)(rest - (long long)item * len);
+            const int end = (int)min((long long)len, u + left);
+            rest += end - u;
+            left -= end - u;
+            g.b = b;
+            g.tile0 = max(u - kHead, 0);
+            g.n = end - kHead - g.tile0;
+            if (g.n <= 0) continue;
+            g.head = item / g.s.blocks;
+            g.block = item - g.head * g.s.blocks;
+            g.rows = min(g.s.T * P.G - g.block * 2 * kTile, 2 * kTile);
+            g.pair = g.rows > kTile;
+            g.first = g.tile0 == 0;
+            g.last = g.tile0 + g.n == g.s.tiles;
+            return true;
         }
-        const int item = (int)(rest / g.s.tiles);
-        g.b = b;
-        g.tile0 = (int)(rest - (long long)item * g.s.tiles);
-        g.head = item / g.s.blocks;
-        g.block = item - g.head * g.s.blocks;
-        g.n = (int)min((long long)(g.s.tiles - g.tile0), left);
-        g.rows = min(g.s.T * P.G - g.block * 2 * kTile, 2 * kTile);
-        g.pair = g.rows > kTile;
-        g.first = g.tile0 == 0;
-        g.last = g.tile0 + g.n == g.s.tiles;
-        rest += g.n;
-        left -= g.n;
-        return true;
+        return false;
     }
 };
 
@@ -195,6 +208,13 @@ __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
     return ((w & e) == e ? 0xffffu : 0u) | (((w >> 16) & e) == e ? 0xffff0000u : 0u);
 }
 
+// 32 bytes, a whole sector of L2.
+__device__ __forceinline__ void st_global_8(float *dst, const float *f) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(f[0]),
+                 "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                 : "memory");
+}
+
 // A weight is rounded to the cache's type relative to a reference maximum that
 // is raised only when the running one passes it by kSlack binades (until then
 // O and the sum need no rescaling). bfloat16 keeps fp32's range; binary16 has
@@ -224,7 +244,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
     Segment g;
     for (; walk.next(P, g); ++seg) {
         const int t_begin = g.tile0 * kTile;
-        const Scouted &sc = M.seg[seg & 1];
+        Scouted &sc = M.seg[seg & 1];
         bool scouted = false;
         const auto wait_scout = [&] {
             if (!scouted) wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P.status);
@@ -323,6 +343,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
             }
             fresh = false;
             if (tail_tile && (!g.pair || w == 0)) {
+                wait_scout();
                 // a slot past the tree, or a node's inf or NaN: 0 in the products
                 // (the latter are added where they are seen, below)
                 const uint32_t use = base + v_at(g, j);
@@ -340,8 +361,11 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                         const uint32_t a = nonfinite_bits<FP16>(x.x), b = nonfinite_bits<FP16>(x.y),
                                        c4 = nonfinite_bits<FP16>(x.z),
                                        d4 = nonfinite_bits<FP16>(x.w);
-                        if (a | b | c4 | d4)
+                        if (a | b | c4 | d4) {
                             *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
+                            const int j = r + t0 - g.s.L;
+                            atomicOr(&sc.nonfinite[j >> 5], 1u << (j & 31));
+                        }
                     }
                 }
                 fence_async_smem();
@@ -374,6 +398,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
             lf = a.y * wgt[0] + (used1 ? b.y * wgt[1] : 0.0f);
         }
         wait_scout();
+        if (g.pair && (g.tile0 + g.n) * kTile > g.s.L) soft_sync();  // group 0's sc.nonfinite
         if (sc.bad) lf = NAN;
         if (warp_on) {
             const bool whole = g.first && g.last;
@@ -428,10 +453,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                                 pack_half<FP16>(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
                                 pack_half<FP16>(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(P.piece_o + at * D + c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        for (int i = 0; i < 4; ++i) st_global_8(P.piece_o + at * D + c + 8 * i, f + 8 * i);
                     }
                 }
             }
@@ -450,7 +473,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
 }
 
 // ---------------------------------------------------------------------------
-// scouts: Q tiles, pages, parents and values, a segment ahead
+// scouts: Q tiles, pages and parents, a segment ahead
 
 template <bool FP16, int D>
 __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk) {
@@ -461,21 +484,39 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
     uint32_t seg = 0, uses[2] = {0, 0}, turn = 0;
     Segment g;
     for (; walk.next(P, g); ++seg) {
+        // the checks' first loads go out before the copies
+        const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
+        const bool tail = t_end > g.s.L;
+        const int pg0 = t_begin / P.c.page, pg1 = (t_end - 1) / P.c.page;
+        const bool page_ok = pg0 + tid > pg1 || page_at(P.c, g.b, pg0 + tid) >= 0;
+        int up[kMaxNodes / kScoutThreads];
+#pragma unroll
+        for (int i = 0; i < kMaxNodes / kScoutThreads; ++i) {
+            const int j = tid + i * kScoutThreads;
+            up[i] = tail && j < g.s.T ? P.t.parent[(int64_t)g.b * P.t.max_nodes + j] : -1;
+        }
         // Q rows into their tiles, 16-byte chunks swizzled within 8 rows
         for (int i = 0; i < (g.pair ? 2 : 1); ++i) {
             const int x = g.pair ? i : turn;
             wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status);
             const int r_first = i * kTile, r_count = min(kTile, g.rows - r_first);
-            const int c = tid % C;
-            for (int r = tid / C; r < r_count; r += kScoutThreads / C) {
-                const int gr = g.block * 2 * kTile + r_first + r;
-                const int node = gr / P.G, hh = gr - node * P.G;
-                const char *src = P.q + (g.s.row0 + node) * P.q_rs +
-                                  (int64_t)(g.head * P.G + hh) * P.q_hs + c * 16;
-                const uint32_t dst = q + x * Sh::kTileBytes + (c >> 3) * Sh::kPanel + r * 128 +
-                                     (((c & 7) ^ (r & 7)) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
+            constexpr int R = kScoutThreads / C;  // rows at a time
+            const int c = tid % C, dn = R / P.G, dh = R - dn * P.G;
+            const int gr = g.block * 2 * kTile + r_first + tid / C;
+            int node = gr / P.G, hh = gr - node * P.G;
+            const uint32_t tile = q + x * Sh::kTileBytes + (c >> 3) * Sh::kPanel;
+            const char *src = P.q + g.s.row0 * P.q_rs + (int64_t)g.head * P.G * P.q_hs + c * 16;
+            for (int r = tid / C; r < r_count; r += R) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                             "l"(src + node * P.q_rs + hh * P.q_hs)
                              : "memory");
+                node += dn;
+                hh += dh;
+                if (hh >= P.G) {
+                    hh -= P.G;
+                    ++node;
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
@@ -485,16 +526,16 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         // pages and parents
         wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status);
         Scouted &sc = M.seg[seg & 1];
-        const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
-        const bool tail = t_end > g.s.L;
-        int bad = 0;
-        for (int i = t_begin / P.c.page + tid; i <= (t_end - 1) / P.c.page; i += kScoutThreads)
+        int bad = page_ok ? 0 : SPECVERIFY_STATUS_BAD_CACHE;
+        for (int i = pg0 + tid + kScoutThreads; i <= pg1; i += kScoutThreads)
             if (page_at(P.c, g.b, i) < 0) bad |= SPECVERIFY_STATUS_BAD_CACHE;
         if (tail)
-            for (int j = tid; j < g.s.T; j += kScoutThreads) {
-                const int up = P.t.parent[(int64_t)g.b * P.t.max_nodes + j];
-                const bool no = j == 0 ? up != -1 : (up < 0 || up >= j);
-                sc.parent[j] = (int8_t)(no ? -1 : up);
+#pragma unroll
+            for (int i = 0; i < kMaxNodes / kScoutThreads; ++i) {
+                const int j = tid + i * kScoutThreads;
+                if (j >= g.s.T) continue;
+                const bool no = j == 0 ? up[i] != -1 : (up[i] < 0 || up[i] >= j);
+                sc.parent[j] = (int8_t)(no ? -1 : up[i]);
                 if (no) bad |= SPECVERIFY_STATUS_BAD_TREE;
             }
         if (tid < kMaskWords) sc.nonfinite[tid] = 0;
@@ -503,21 +544,6 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         if (bad) {
             atomicOr(P.status, bad);
             sc.bad = 1;
-        }
-        if (tail) {
-            const int j0 = max(0, t_begin - g.s.L), j1 = t_end - g.s.L;
-#pragma unroll 4
-            for (int i = tid; i < (j1 - j0) * C; i += kScoutThreads) {
-                const int j = j0 + i / C, s = g.s.L + j;
-                const int64_t page = page_of(P.c, g.b, s);
-                if (page < 0) continue;
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    P.c.v + (int64_t)g.head * P.c.hs + page * P.c.ps +
-                    (int64_t)(s % P.c.page) * P.c.ts + i % C * 16);
-                if (nonfinite_bits<FP16>(x.x) | nonfinite_bits<FP16>(x.y) |
-                    nonfinite_bits<FP16>(x.z) | nonfinite_bits<FP16>(x.w))
-                    atomicOr(&sc.nonfinite[j >> 5], 1u << (j & 31));
-            }
         }
         mbar_arrive(smem_u32(&M.seg_full[seg & 1]));
     }
@@ -679,7 +705,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_of(P, b);
-        mine += (long long)s.tiles * s.blocks * P.c.kv_heads;
+        mine += s.units(P);
         if (s.tiles == 0 && s.T != 0 && b % (int)gridDim.x == (int)blockIdx.x) {
             // a bad sequence: NaN in the rows that it names, if it names rows
             const int bad = seq_error(P, s.T, s.row0, s.L);
@@ -714,7 +740,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             const Seq s = seq_of(P, b);
-            const long long n = (long long)s.tiles * s.blocks * P.c.kv_heads;
+            const long long n = s.units(P);
             if (lo < at + n) {
                 M.b0 = b;
                 M.rest0 = (int)(lo - at);
@@ -744,17 +770,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             AttnOwner o{};
             Walk v = walk;
             Segment g;
-            long long at = lo;
             while (v.next(P, g)) {
-                if (g.first && !g.last) {
-                    const long long end = at + g.s.tiles;  // line position after the item
+                if (g.first && !g.last) {  // the CTA's last segment: the line goes on at hi
+                    const long long end = hi + g.s.tiles - g.n;
                     o.pieces = (int)((end * ctas - 1) / total) - (int)blockIdx.x + 1;
                     o.rows = g.rows;
                     o.first_row = g.block * 2 * kTile;
                     o.head = g.head;
                     o.row0 = g.s.row0;
                 }
-                at += g.n;
             }
             P.owner[blockIdx.x] = o;
         }
@@ -764,48 +788,76 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the pieces of the items that were cut: block (c, i) the rows 8 i .. of
-// the item that CTA c began, a warp a row. Piece 0 is c's last segment, the
-// next CTAs' first segments follow.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of the items that were cut: block (c, y) rows 32 y and up of
+// the item that CTA c began, four a warp. Piece 0 is c's last segment, the next
+// CTAs' first segments follow. Bound by the latency of its loads: the first
+// kAhead pieces are read before anything is known of their weights.
+constexpr int kJoinWarps = 8, kJoinRows = 4, kAhead = 2;
 
 template <bool FP16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const AttnOwner o = P.owner[blockIdx.x];
-    const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (o.pieces == 0 || r >= o.rows) return;
-    const auto at = [&](int i) -> int64_t {
-        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * (2 * kTile) + r;
-    };
-    float m = -INFINITY;
-    for (int i = lane; i < o.pieces; i += 32) m = fmaxf(m, P.piece_ml[at(i)].x);
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     constexpr int W = D / 32;
-    float l = 0.0f, f[W] = {};
-#pragma unroll 4
-    for (int i = 0; i < o.pieces; ++i) {
-        const float2 ml = P.piece_ml[at(i)];
-        const float wgt = ml.x == -INFINITY ? 0.0f : fmaxf(ex2_approx(ml.x - m), kTiny);
-        l = fmaf(ml.y, ml.x == -INFINITY ? 1.0f : wgt, l);  // a NaN sum stays one
-        const float *src = P.piece_o + at(i) * D + lane * W;
-        float x[W];
-        if (W == 4)
-            *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(src);
-        else
-            *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(src);
+    using Vec = typename std::conditional<W == 4, float4, float2>::type;
+    const AttnOwner o = P.owner[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    const int r0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
+    if (o.pieces == 0 || r0 >= o.rows) return;
+    const auto at = [&](int i, int k) -> int64_t {  // rows past the item's are in its slot too
+        return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * (2 * kTile) + r0 + k;
+    };
+    const auto piece = [&](int i, int k, float *x) {
+        *reinterpret_cast<Vec *>(x) = *reinterpret_cast<const Vec *>(P.piece_o + at(i, k) * D + lane * W);
+    };
+    float x[kAhead][kJoinRows][W], m[kJoinRows], l[kJoinRows] = {}, f[kJoinRows][W] = {};
+    float2 ml[kAhead][kJoinRows];
 #pragma unroll
-        for (int c = 0; c < W; ++c) f[c] = fmaf(x[c], wgt, f[c]);
+    for (int i = 0; i < kAhead; ++i)  // a cut item has two pieces at least
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            ml[i][k] = P.piece_ml[at(i, k)];
+            piece(i, k, x[i][k]);
+        }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        m[k] = -INFINITY;
+        for (int i = lane; i < o.pieces; i += 32) m[k] = fmaxf(m[k], P.piece_ml[at(i, k)].x);
     }
-    const int gr = o.first_row + r, node = gr / P.G, h = o.head * P.G + gr - node * P.G;
-    const int64_t row = o.row0 + node;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(P.out + row * P.o_rs + (int64_t)h * P.o_hs) +
-                    lane * (W / 2);
 #pragma unroll
-    for (int c = 0; c < W / 2; ++c) dst[c] = pack_half<FP16>(f[2 * c] * inv, f[2 * c + 1] * inv);
-    if (P.lse && lane == 0)
-        P.lse[row * P.heads + h] = (m + log2f(l) - Range<FP16>::kShift) * 0.6931471805599453f;
+    for (int k = 0; k < kJoinRows; ++k)
+        for (int s = 16; s > 0; s >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], s));
+    const auto add = [&](int k, float2 a, const float *v) {
+        const float wgt = a.x == -INFINITY ? 0.0f : fmaxf(ex2_approx(a.x - m[k]), kTiny);
+        l[k] = fmaf(a.y, a.x == -INFINITY ? 1.0f : wgt, l[k]);  // a NaN sum stays one
+#pragma unroll
+        for (int c = 0; c < W; ++c) f[k][c] = fmaf(v[c], wgt, f[k][c]);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) add(k, ml[i][k], x[i][k]);
+#pragma unroll 2
+    for (int i = kAhead; i < o.pieces; ++i)
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            float v[W];
+            piece(i, k, v);
+            add(k, P.piece_ml[at(i, k)], v);
+        }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        if (r0 + k >= o.rows) break;
+        const int gr = o.first_row + r0 + k, node = gr / P.G, h = o.head * P.G + gr - node * P.G;
+        const int64_t row = o.row0 + node;
+        const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+        uint32_t *dst = reinterpret_cast<uint32_t *>(P.out + row * P.o_rs + (int64_t)h * P.o_hs) +
+                        lane * (W / 2);
+#pragma unroll
+        for (int c = 0; c < W / 2; ++c)
+            dst[c] = pack_half<FP16>(f[k][2 * c] * inv, f[k][2 * c + 1] * inv);
+        if (P.lse && lane == 0)
+            P.lse[row * P.heads + h] = (m[k] + log2f(l[k]) - Range<FP16>::kShift) * 0.6931471805599453f;
+    }
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -822,7 +874,7 @@ cudaError_t launch(const TreeAttnParams &p, const CUtensorMap &mk, const CUtenso
     if (e != cudaSuccess) return e;
     const int most = std::min((int64_t)2 * kTile, (int64_t)p.t.max_nodes * p.G);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((most + kJoinWarps - 1) / kJoinWarps));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((most + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows)));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
