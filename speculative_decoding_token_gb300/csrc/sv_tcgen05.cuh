@@ -11,6 +11,24 @@
 
 namespace sv {
 
+// A wait that gives up after about two seconds, or once another of the CTA has
+// (`abort`, in shared memory): the roles then run through their work without
+// waiting, and the status says so.
+__device__ __forceinline__ bool wait_on(uint64_t &bar, uint32_t parity, int32_t &abort,
+                                        int32_t *status) {
+    const uint32_t at = smem_u32(&bar);
+    if (mbar_try_wait(at, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait(at, parity)) return true;
+        if (*(volatile int32_t *)&abort) return false;
+        if (global_ns() - t0 > 2000000000ull) break;
+    }
+    *(volatile int32_t *)&abort = 1;
+    atomicOr(status, SPECVERIFY_STATUS_TIMEOUT);
+    return false;
+}
+
 // --- tensor memory -----------------------------------------------------------
 // One warp; the address of column 0 goes to shared memory at `dst`.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
@@ -133,5 +151,16 @@ __device__ __forceinline__ void fence_async_smem() {
 __device__ __forceinline__ void mbar_fence_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
+
+// --- host: maps of a cache's keys or values --------------------------------------
+struct CacheParams;
+constexpr int kTile = 128;  // slots of a tile, and its rows of 128 bytes
+
+// Tokens of one copy: the largest power of two that divides the page size and a tile.
+int cache_box(int page);
+
+// A [page][head][token][element] map in boxes of 64 elements by `box` tokens;
+// false where the layout cannot be described.
+bool cache_map(const CacheParams &c, const char *base, int box, CUtensorMap *map);
 
 }  // namespace sv

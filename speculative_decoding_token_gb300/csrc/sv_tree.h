@@ -86,6 +86,7 @@ struct AccumParams {
     int64_t rows;
     int32_t heads, G;
     float scale_log2;
+    int32_t box;              // as of the attention
     int32_t *status;
 };
 
@@ -108,7 +109,8 @@ void attn_place(TreeAttnParams &p, void *ws, int ctas);
 cudaError_t launch_tree_attention(TreeAttnParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_tree_verify(const TreeVerifyParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s);
-cudaError_t launch_accumulate(const AccumParams &p, int num_sms, cudaStream_t s);
+cudaError_t prepare_accumulate();
+cudaError_t launch_accumulate(AccumParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

@@ -34,7 +34,6 @@ namespace sv {
 
 namespace {
 
-constexpr int kTile = 128;                 // rows of a Q tile, slots of a K or V tile
 constexpr int kSoftThreads = 256;
 constexpr int kAttnThreads = kSoftThreads + 128;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kScoutThreads = 64;
@@ -166,20 +165,8 @@ __device__ __forceinline__ uint32_t v_at(const Segment &g, int j) {
     return g.pair ? 2 * j + 1 : min(2 * j + 2, 2 * g.n - 1);
 }
 
-// A wait that gives up after about two seconds, or once another has: the roles
-// then run through their work without waiting, and the status says so.
 __device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, int32_t *status) {
-    const uint32_t at = smem_u32(&bar);
-    if (mbar_try_wait(at, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (;;) {
-        if (mbar_try_wait(at, parity)) return true;
-        if (*(volatile int32_t *)&M.abort) return false;
-        if (global_ns() - t0 > 2000000000ull) break;
-    }
-    *(volatile int32_t *)&M.abort = 1;
-    atomicOr(status, SPECVERIFY_STATUS_TIMEOUT);
-    return false;
+    return ::sv::wait_on(bar, parity, M.abort, status);
 }
 
 // Barrier of the two softmax groups.
