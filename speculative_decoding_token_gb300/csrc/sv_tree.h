@@ -111,6 +111,7 @@ cudaError_t launch_tree_verify(const TreeVerifyParams &p, int dtype, cudaStream_
 cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s);
 cudaError_t prepare_accumulate();
 cudaError_t launch_accumulate(AccumParams p, int num_sms, cudaStream_t s);
+cudaError_t prepare_evict();
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

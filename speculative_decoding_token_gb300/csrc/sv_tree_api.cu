@@ -148,6 +148,7 @@ int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch
     cudaError_t e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, device);
     if (e == cudaSuccess) e = sv::prepare_tree();
     if (e == cudaSuccess) e = sv::prepare_accumulate();
+    if (e == cudaSuccess) e = sv::prepare_evict();
     // an item moves at least one token, so max_moves bounds the items as well
     const size_t lists = sizeof(int32_t) * (size_t)max_moves;
     h->ws_bytes = 256 + 3 * ((lists + 255) / 256 * 256) + sv::attn_workspace(h->num_sms);

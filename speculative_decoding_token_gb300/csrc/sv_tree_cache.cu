@@ -1,5 +1,7 @@
 // sv_tree_cache.cu -- what a paged cache keeps: the commit of an accepted path
 // and the eviction of the tokens that gathered the least attention weight.
+#include <algorithm>
+
 #include "sv_tree.h"
 
 namespace sv {
@@ -86,13 +88,16 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
 }
 
 // ---------------------------------------------------------------------------
-// Eviction, selection: one CTA for each (layer, sequence, key head). The
-// budget-th largest key by a radix select over the keys' bits, most
-// significant first, then the kept slots by counting in slot order.
+// Eviction, selection: one CTA for each (layer, sequence, key head). Every slot
+// becomes a 32-bit key, read once into shared memory while they fit (kKeyCap of
+// them; beyond that the passes read mass and pos again, from L2). The budget-th
+// largest key by a radix select, 11, 11 and 10 bits, most significant first;
+// then the kept slots by counting in slot order. Bound by the passes over the
+// keys and, for a few thousand slots, by the latency of its dozen barriers.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBits = 8;
-constexpr int kSelBins = 1 << kSelBits;
+constexpr int kSelBins = 2048;             // two a thread
+constexpr int kKeyCap = 48 * 1024;         // 192 KiB
 
 // Order-preserving bits of a mass: -0 as +0, a NaN as the least. A protected
 // token's key is above every one of them.
@@ -113,19 +118,20 @@ __device__ __forceinline__ int64_t slot_at(const CacheParams &c, const Item &it,
     return it.base + pg * c.mps + (int64_t)(s % c.page) * c.mts;
 }
 
-__device__ __forceinline__ uint32_t key_of(const EvictParams &P, const Item &it, int s) {
-    const int64_t at = slot_at(P.c, it, s);
+__device__ __forceinline__ uint32_t key_at(const EvictParams &P, const Item &it, int64_t at) {
     const int pos = P.c.pos[at];
-    if (pos < P.sink || pos >= it.seen - P.recent) return 0xffffffffu;
-    return mass_key(P.c.mass[at]);
+    const float m = P.c.mass[at];
+    return pos < P.sink || pos >= it.seen - P.recent ? 0xffffffffu : mass_key(m);
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams P) {
+    extern __shared__ uint32_t s_key[];
     __shared__ uint32_t s_hist[kSelBins];
-    __shared__ uint32_t s_pick[2];
+    __shared__ int s_pick[2];
     __shared__ int s_cnt[3][kSelWarps];
+    asm volatile("griddepcontrol.launch_dependents;");
     const CacheParams &c = P.c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = blockIdx.x;
     Item it;
     it.head = item % c.kv_heads;
@@ -136,11 +142,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     it.base = it.layer * c.mls + it.head * c.mhs;
     int bad = it.len < 0 || !cache_holds(c, it.len);
     if (!bad)
-        for (int i = threadIdx.x; i < (it.len + c.page - 1) / c.page; i += kSelThreads)
+        for (int i = tid; i < (it.len + c.page - 1) / c.page; i += kSelThreads)
             bad |= page_at(c, it.b, i) < 0;
+    for (int i = tid; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
     bad = __syncthreads_or(bad);
     const int N = it.len, keep = min(N, P.budget);
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         if (P.moves > 0 && (N <= P.budget || bad)) P.move_cnt[item] = 0;
         if (it.layer == 0 && it.head == 0) P.new_lens[it.b] = bad ? N : keep;
         if (bad) atomicOr(P.status, SPECVERIFY_STATUS_BAD_CACHE);
@@ -149,127 +156,181 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const bool copy = P.mass_out != c.mass, copy_pos = P.pos_out != c.pos;
     if (N <= P.budget) {
         if (copy || copy_pos)
-            for (int s = threadIdx.x; s < N; s += kSelThreads) {
+            for (int s = tid; s < N; s += kSelThreads) {
                 const int64_t at = slot_at(c, it, s);
                 if (copy) P.mass_out[at] = c.mass[at];
                 if (copy_pos) P.pos_out[at] = c.pos[at];
             }
         return;
     }
-    // the keep-th largest key: `prefix` its leading bits, `need` its rank among those that share them
-    uint32_t prefix = 0, mask = 0;
+    const bool held = N <= kKeyCap;
+    const auto key_of = [&](int s) { return held ? s_key[s] : key_at(P, it, slot_at(c, it, s)); };
+    // the keep-th largest key: `prefix` its leading bits, `need` its rank among
+    // those that share them
+    uint32_t prefix = 0;
     int need = keep;
-    for (int shift = 32 - kSelBits; shift >= 0; shift -= kSelBits) {
-        for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
-        __syncthreads();
-        for (int s = threadIdx.x; s < N; s += kSelThreads) {
-            const uint32_t k = key_of(P, it, s);
-            if ((k & mask) == prefix) atomicAdd(&s_hist[k >> shift & (kSelBins - 1)], 1u);
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const uint32_t bins = pass == 2 ? 1024u : 2048u;
+        if (pass == 0) {
+#pragma unroll 4
+            for (int s = tid; s < N; s += kSelThreads) {
+                const uint32_t k = key_at(P, it, slot_at(c, it, s));
+                if (held) s_key[s] = k;
+                atomicAdd(&s_hist[k >> shift], 1u);
+            }
+        } else {
+            const int above = pass == 1 ? 21 : 10;
+            for (int s = tid; s < N; s += kSelThreads) {
+                const uint32_t k = key_of(s);
+                if (k >> above == prefix >> above) atomicAdd(&s_hist[k >> shift & (bins - 1)], 1u);
+            }
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            int left = need, bin = kSelBins - 1;
-            for (; bin > 0 && (int)s_hist[bin] < left; --bin) left -= (int)s_hist[bin];
-            s_pick[0] = (uint32_t)bin;
-            s_pick[1] = (uint32_t)left;
+        // keys in the bins above this thread's two (thread 0 has the highest)
+        const int hi = (int)bins - 1 - 2 * tid;
+        const int n1 = hi >= 0 ? (int)s_hist[hi] : 0, n0 = hi >= 1 ? (int)s_hist[hi - 1] : 0;
+        int incl = n0 + n1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += up;
         }
+        if (lane == 31) s_cnt[0][warp] = incl;
         __syncthreads();
-        prefix |= s_pick[0] << shift;
-        mask |= (uint32_t)(kSelBins - 1) << shift;
-        need = (int)s_pick[1];
+        int before = incl - n0 - n1;
+        {
+            const int t = s_cnt[0][lane];
+            before += __reduce_add_sync(kAll, lane < warp ? t : 0);
+        }
+        if (before < need && need <= before + n1) {
+            s_pick[0] = hi;
+            s_pick[1] = need - before;
+        } else if (before + n1 < need && need <= before + n1 + n0) {
+            s_pick[0] = hi - 1;
+            s_pick[1] = need - before - n1;
+        }
+        if (hi >= 0) s_hist[hi] = 0;
+        if (hi >= 1) s_hist[hi - 1] = 0;
         __syncthreads();
+        prefix |= (uint32_t)s_pick[0] << shift;
+        need = s_pick[1];
     }
     // kept: keys above it, and the first `need` slots that equal it. Warp w owns
     // a run of slots; counts before it come from the other warps' totals.
     const int run = ((N + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
     const int r0 = min(N, warp * run), r1 = min(N, r0 + run);
-    int eq = 0;
+    int eq = 0, low_above = 0, high_above = 0, low_eq = 0;
     for (int s0 = r0; s0 < r1; s0 += 32) {
         const int s = s0 + lane;
-        eq += __popc(__ballot_sync(kAll, s < r1 && key_of(P, it, s) == prefix));
+        const uint32_t k = s < r1 ? key_of(s) : 0u;
+        eq += s < r1 && k == prefix;
+        low_eq += s < keep && s < r1 && k == prefix;
+        low_above += s < keep && s < r1 && k > prefix;
+        high_above += s >= keep && s < r1 && k > prefix;
     }
+    eq = __reduce_add_sync(kAll, eq);
+    low_eq = __reduce_add_sync(kAll, low_eq);
+    low_above = __reduce_add_sync(kAll, low_above);
+    high_above = __reduce_add_sync(kAll, high_above);
     if (lane == 0) s_cnt[0][warp] = eq;
     __syncthreads();
-    int eq0 = 0;
-    for (int w = 0; w < warp; ++w) eq0 += s_cnt[0][w];
-    int holes = 0, movers = 0;
-    const uint32_t below = (1u << lane) - 1u;
-    for (int pass = 0; pass < 2; ++pass) {
-        int e = eq0, hole = 0, mover = 0;
-        if (pass == 1)
-            for (int w = 0; w < warp; ++w) {
-                hole += s_cnt[1][w];
-                mover += s_cnt[2][w];
-            }
-        for (int s0 = r0; s0 < r1; s0 += 32) {
-            const int s = s0 + lane;
-            const uint32_t k = s < r1 ? key_of(P, it, s) : 0u;
-            const uint32_t same = __ballot_sync(kAll, s < r1 && k == prefix);
-            const bool kept =
-                s < r1 && (k > prefix || (k == prefix && e + __popc(same & below) < need));
-            e += __popc(same);
-            const uint32_t hm = __ballot_sync(kAll, s < keep && s < r1 && !kept);
-            const uint32_t mm = __ballot_sync(kAll, s >= keep && kept);
-            if (pass == 1) {
-                const int64_t list = (int64_t)item * P.moves;
-                if (hm >> lane & 1) P.move_dst[list + hole + __popc(hm & below)] = s;
-                if (mm >> lane & 1) P.move_src[list + mover + __popc(mm & below)] = s;
-                if (kept && s < keep && (copy || copy_pos)) {
-                    const int64_t at = slot_at(c, it, s);
-                    if (copy) P.mass_out[at] = c.mass[at];
-                    if (copy_pos) P.pos_out[at] = c.pos[at];
-                }
-            }
-            hole += __popc(hm);
-            mover += __popc(mm);
-        }
-        if (pass == 0) {
-            if (lane == 0) {
-                s_cnt[1][warp] = hole;
-                s_cnt[2][warp] = mover;
-            }
-            __syncthreads();
-        } else {
-            holes = hole;
-            movers = mover;
-        }
+    const int eq0 = __reduce_add_sync(kAll, lane < warp ? s_cnt[0][lane] : 0);
+    // of this warp's equal slots the first `take` are kept, those below the budget first
+    const int take = max(0, min(eq, need - eq0)), low_take = min(take, low_eq);
+    if (lane == 0) {
+        s_cnt[1][warp] = max(0, min(r1, keep) - r0) - low_above - low_take;  // free slots
+        s_cnt[2][warp] = high_above + take - low_take;                      // movers
     }
-    (void)holes;
-    if (warp == kSelWarps - 1 && lane == 0) P.move_cnt[item] = movers;
+    __syncthreads();
+    int hole = __reduce_add_sync(kAll, lane < warp ? s_cnt[1][lane] : 0);
+    int mover = __reduce_add_sync(kAll, lane < warp ? s_cnt[2][lane] : 0);
+    const uint32_t below = (1u << lane) - 1u;
+    const int64_t list = (int64_t)item * P.moves;
+    int e = eq0;
+    for (int s0 = r0; s0 < r1; s0 += 32) {
+        const int s = s0 + lane;
+        const uint32_t k = s < r1 ? key_of(s) : 0u;
+        const uint32_t same = __ballot_sync(kAll, s < r1 && k == prefix);
+        const bool kept = s < r1 && (k > prefix || (k == prefix && e + __popc(same & below) < need));
+        e += __popc(same);
+        const uint32_t hm = __ballot_sync(kAll, s < keep && s < r1 && !kept);
+        const uint32_t mm = __ballot_sync(kAll, s >= keep && kept);
+        if (hm >> lane & 1) P.move_dst[list + hole + __popc(hm & below)] = s;
+        if (mm >> lane & 1) P.move_src[list + mover + __popc(mm & below)] = s;
+        if (kept && s < keep && (copy || copy_pos)) {
+            const int64_t at = slot_at(c, it, s);
+            if (copy) P.mass_out[at] = c.mass[at];
+            if (copy_pos) P.pos_out[at] = c.pos[at];
+        }
+        hole += __popc(hm);
+        mover += __popc(mm);
+    }
+    if (warp == kSelWarps - 1 && lane == 0) P.move_cnt[item] = mover;
 }
 
-// Eviction, moves: a source lies at or past the budget and a destination
-// below it, so moves never meet. A group of d / 8 threads takes one move.
+// Eviction, moves: a source lies at or past the budget and a destination below
+// it, so moves never meet. d / 8 threads take a group of kMoveGroup moves, all
+// of its rows in flight at once; bound by the bytes of the moved rows.
 constexpr int kMoveThreads = 256;
+constexpr int kMoveGroup = 4;
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const CacheParams &c = P.c;
     const int chunks = c.d / 8, item = blockIdx.x;
     const int head = item % c.kv_heads, b = item / c.kv_heads % P.B,
               layer = item / c.kv_heads / P.B;
     const int cnt = P.move_cnt[item];
     const int part = threadIdx.x % chunks;
-    const int per = kMoveThreads / chunks;
+    const int groups = kMoveThreads / chunks;
     const int64_t base = layer * c.ls + head * c.hs + part * 16;
-    for (int r = blockIdx.y * per + threadIdx.x / chunks; r < cnt; r += gridDim.y * per) {
-        const int64_t list = (int64_t)item * P.moves + r;
-        const int s = P.move_src[list], d = P.move_dst[list];
-        const int64_t ps = __ldg(&c.table[(int64_t)b * c.table_stride + s / c.page]);
-        const int64_t pd = __ldg(&c.table[(int64_t)b * c.table_stride + d / c.page]);
-        const int64_t so = base + ps * c.ps + (int64_t)(s % c.page) * c.ts;
-        const int64_t dof = base + pd * c.ps + (int64_t)(d % c.page) * c.ts;
-        const uint4 k = *reinterpret_cast<const uint4 *>(c.k + so);
-        const uint4 v = *reinterpret_cast<const uint4 *>(c.v + so);
-        *reinterpret_cast<uint4 *>(c.k + dof) = k;
-        *reinterpret_cast<uint4 *>(c.v + dof) = v;
-        if (part < 2) {
-            const int64_t mb = layer * c.mls + head * c.mhs;
-            const int64_t ms = mb + ps * c.mps + (int64_t)(s % c.page) * c.mts;
-            const int64_t md = mb + pd * c.mps + (int64_t)(d % c.page) * c.mts;
-            if (part == 0)
-                P.mass_out[md] = c.mass[ms];
-            else
+    const int64_t mbase = layer * c.mls + head * c.mhs, list = (int64_t)item * P.moves;
+    const int32_t *table = c.table + (int64_t)b * c.table_stride;
+    const int step = gridDim.y * groups * kMoveGroup;
+    for (int r0 = (blockIdx.y * groups + threadIdx.x / chunks) * kMoveGroup; r0 < cnt; r0 += step) {
+        int s[kMoveGroup], d[kMoveGroup];
+        int64_t ps[kMoveGroup], pd[kMoveGroup];
+#pragma unroll
+        for (int i = 0; i < kMoveGroup; ++i) {
+            const int64_t at = list + min(r0 + i, cnt - 1);
+            s[i] = P.move_src[at];
+            d[i] = P.move_dst[at];
+        }
+#pragma unroll
+        for (int i = 0; i < kMoveGroup; ++i) {
+            ps[i] = __ldg(&table[s[i] / c.page]);
+            pd[i] = __ldg(&table[d[i] / c.page]);
+            s[i] %= c.page;
+            d[i] %= c.page;
+        }
+        uint4 k[kMoveGroup], v[kMoveGroup];
+#pragma unroll
+        for (int i = 0; i < kMoveGroup; ++i) {
+            const int64_t so = base + ps[i] * c.ps + s[i] * c.ts;
+            k[i] = *reinterpret_cast<const uint4 *>(c.k + so);
+            v[i] = *reinterpret_cast<const uint4 *>(c.v + so);
+        }
+        // thread `part` also takes mass or pos of one of the moves
+        const int mi = part >> 1;
+        if (mi < kMoveGroup && r0 + mi < cnt) {
+            int64_t ms = 0, md = 0;
+#pragma unroll
+            for (int i = 0; i < kMoveGroup; ++i)
+                if (i == mi) {
+                    ms = mbase + ps[i] * c.mps + s[i] * c.mts;
+                    md = mbase + pd[i] * c.mps + d[i] * c.mts;
+                }
+            if (part & 1)
                 P.pos_out[md] = c.pos[ms];
+            else
+                P.mass_out[md] = c.mass[ms];
+        }
+#pragma unroll
+        for (int i = 0; i < kMoveGroup; ++i) {
+            if (r0 + i >= cnt) break;
+            const int64_t to = base + pd[i] * c.ps + d[i] * c.ts;
+            *reinterpret_cast<uint4 *>(c.k + to) = k[i];
+            *reinterpret_cast<uint4 *>(c.v + to) = v[i];
         }
     }
 }
@@ -281,13 +342,31 @@ cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+cudaError_t prepare_evict() {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kKeyCap * (int)sizeof(uint32_t));
+}
+
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
     const int items = p.c.layers * p.B * p.c.kv_heads;
-    evict_select_kernel<<<items, kSelThreads, 0, s>>>(p);
+    const int64_t capacity = (int64_t)p.c.max_pages * p.c.page;
+    const int keys = (int)std::min<int64_t>(capacity, kKeyCap);
+    evict_select_kernel<<<items, kSelThreads, keys * sizeof(uint32_t), s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.moves == 0) return e;
-    evict_move_kernel<<<dim3(items, 32), kMoveThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    // blocks of an item: enough for its longest list, up to about four waves in all
+    const int per = kMoveThreads / (p.c.d / 8) * kMoveGroup;
+    const int most = (p.moves + per - 1) / per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)items, (unsigned)std::min(most, std::max(1, 8192 / items)));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
 }
 
 }  // namespace sv

@@ -15,8 +15,9 @@ namespace sv {
 namespace {
 
 constexpr int kVtCtas = 8;
-constexpr int kVtThreads = 512;
+constexpr int kVtThreads = 256;
 constexpr int kVtWarps = kVtThreads / 32;
+constexpr int kVtBatch = 5;  // 16-byte loads of a thread in flight
 
 // a before b: the larger value, then the lower index; a NaN before all
 __device__ __forceinline__ void take_first(float &best, int32_t &idx, float ob, int32_t oi) {
@@ -30,7 +31,7 @@ __device__ __forceinline__ void take_first(float &best, int32_t &idx, float ob, 
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVtThreads, 1) tree_verify_kernel(const TreeVerifyParams P) {
+__global__ void __launch_bounds__(kVtThreads, 4) tree_verify_kernel(const TreeVerifyParams P) {
     __shared__ __align__(16) float4 s_slice[2][kVtCtas];
     __shared__ float2 s_warp[kVtWarps];
     __shared__ int32_t s_parent[kMaxNodes], s_token[kMaxNodes], s_path[kMaxNodes];
@@ -85,21 +86,46 @@ __global__ void __launch_bounds__(kVtThreads, 1) tree_verify_kernel(const TreeVe
     bool nan = false;
     for (;;) {  // at most `nodes` steps: each goes to a later node
         const char *row = P.target + (row0 + node) * P.stride_bytes;
+        // the first child's slice on its way to L2: where the walk goes on, it is
+        // usually there
+        if (warp == kVtWarps - 1) {
+            int child = -1;
+            for (int j0 = (node + 1) & ~31; j0 < nodes && child < 0; j0 += 32) {
+                const int j = j0 + lane;
+                const uint32_t hit =
+                    __ballot_sync(0xffffffffu, j > node && j < nodes && s_parent[j] == node);
+                if (hit) child = j0 + __ffs(hit) - 1;
+            }
+            if (child >= 0 && v1 > v0 && lane == 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 P.target + (row0 + child) * P.stride_bytes + v0 * 16),
+                             "r"((uint32_t)min((v1 - v0) * 16, (int64_t)1 << 18))
+                             : "memory");
+        }
         const uint4 *rv = reinterpret_cast<const uint4 *>(row);
         float best = -INFINITY;
         int32_t idx = -1;
-#pragma unroll 8
-        for (int64_t vi = v0 + threadIdx.x; vi < v1; vi += kVtThreads) {
-            const uint4 w = __ldg(rv + vi);
-            const float m = vec_max<DT>(w);
-            if (m != m || m > best || idx < 0) {  // later indexes: a tie keeps the first
-                if (best == best) {
-                    float f[PV];
-                    vec_floats<DT>(w, f);
-                    int e = 0;
-                    while (e < PV - 1 && f[e] != m) ++e;
-                    best = m;
-                    idx = (int32_t)(vi * PV + e);
+        for (int64_t vi0 = v0 + threadIdx.x; vi0 < v1; vi0 += kVtBatch * kVtThreads) {
+            uint4 v[kVtBatch];
+#pragma unroll
+            for (int i = 0; i < kVtBatch; ++i)
+                if (vi0 + i * kVtThreads < v1) v[i] = __ldg(rv + vi0 + i * kVtThreads);
+#pragma unroll
+            for (int i = 0; i < kVtBatch; ++i) {
+                const int64_t vi = vi0 + i * kVtThreads;
+                if (vi >= v1) break;
+                const float m = vec_max<DT>(v[i]);
+                if (m != m || m > best || idx < 0) {  // later indexes: a tie keeps the first
+                    if (best == best) {
+                        float f[PV];
+                        vec_floats<DT>(v[i], f);
+                        int e = 0;
+#pragma unroll
+                        for (int j = PV - 1; j >= 0; --j)
+                            if (f[j] == m) e = j;
+                        best = m;
+                        idx = (int32_t)(vi * PV + e);
+                    }
                 }
             }
         }
