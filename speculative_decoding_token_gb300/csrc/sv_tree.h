@@ -24,7 +24,20 @@ struct CacheParams {
     int64_t num_pages;
     int32_t max_pages, page, kv_heads, d, layers;
     int32_t fp16;             // 1: binary16, 0: bfloat16
+    // s / page for 0 <= s < 2^31: the high word of s * page_mul, shifted right
+    // (Granlund and Montgomery, "Division by invariant integers using
+    // multiplication", with 2^(31 + l) / page rounded up, 2^l >= page)
+    uint32_t page_mul;
+    int32_t page_shift;
 };
+
+inline void set_page(CacheParams &c, int32_t page) {
+    int l = 0;
+    while (((int64_t)1 << l) < page) ++l;
+    c.page = page;
+    c.page_mul = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint32_t)page + 1);
+    c.page_shift = l - 1;
+}
 
 struct TreeParams {
     const int64_t *row_off;
@@ -129,9 +142,19 @@ __device__ __forceinline__ int64_t page_at(const CacheParams &c, int b, int i) {
     return id >= 0 && (int64_t)id < c.num_pages ? (int64_t)id : -1;
 }
 
+// Slot s's place: page `index` of its sequence, token `token` of that page.
+struct Place {
+    int index, token;
+};
+
+__device__ __forceinline__ Place place_of(const CacheParams &c, int s) {
+    const int i = (int)(__umulhi((uint32_t)s, c.page_mul) >> c.page_shift);
+    return {i, s - i * c.page};
+}
+
 // The page that holds slot s of sequence b.
 __device__ __forceinline__ int64_t page_of(const CacheParams &c, int b, int s) {
-    return page_at(c, b, s / c.page);
+    return page_at(c, b, place_of(c, s).index);
 }
 
 #endif

@@ -111,7 +111,7 @@ sv::CacheParams cache_params(const specverify_cache *c) {
     p.table_stride = c->table_stride;
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
-    p.page = c->page_size;
+    sv::set_page(p, c->page_size);
     p.kv_heads = c->kv_heads;
     p.d = c->head_dim;
     p.layers = c->layers;

@@ -419,7 +419,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                         const int s = g.s.L + j;
                         const uint32_t *v = reinterpret_cast<const uint32_t *>(
                             P.c.v + (int64_t)g.head * P.c.hs + page_of(P.c, g.b, s) * P.c.ps +
-                            (int64_t)(s % P.c.page) * P.c.ts + c * 2);
+                            (int64_t)place_of(P.c, s).token * P.c.ts + c * 2);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const uint32_t x = v[i], bits = nonfinite_bits<FP16>(x);
@@ -474,7 +474,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         // the checks' first loads go out before the copies
         const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
         const bool tail = t_end > g.s.L;
-        const int pg0 = t_begin / P.c.page, pg1 = (t_end - 1) / P.c.page;
+        const int pg0 = place_of(P.c, t_begin).index, pg1 = place_of(P.c, t_end - 1).index;
         const bool page_ok = pg0 + tid > pg1 || page_at(P.c, g.b, pg0 + tid) >= 0;
         int up[kMaxNodes / kScoutThreads];
 #pragma unroll
@@ -634,7 +634,7 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
                 const uint32_t dst = ring + slot * Sh::kTileBytes + lane * box * 128;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
-                    tile_load(dst + c * Sh::kPanel, map, c * 64, s % P.c.page, g.head, page, bar);
+                    tile_load(dst + c * Sh::kPanel, map, c * 64, place_of(P.c, s).token, g.head, page, bar);
             }
             __syncwarp();
         };

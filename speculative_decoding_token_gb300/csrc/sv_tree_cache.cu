@@ -40,9 +40,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
             } else {
                 const int64_t ps = page_of(c, b, L + j), pd = page_of(c, b, L + i);
                 if (ps < 0 || pd < 0) bad = SPECVERIFY_STATUS_BAD_CACHE;
-                src = ps * c.ps + (L + j) % c.page * c.ts;
-                dst = pd * c.ps + (L + i) % c.page * c.ts;
-                mass = pd * c.mps + (L + i) % c.page * c.mts;
+                src = ps * c.ps + place_of(c, L + j).token * c.ts;
+                dst = pd * c.ps + place_of(c, L + i).token * c.ts;
+                mass = pd * c.mps + place_of(c, L + i).token * c.mts;
                 s_src[i] = src;
                 s_dst[i] = dst;
                 s_mass[i] = mass;
@@ -114,8 +114,9 @@ struct Item {
 };
 
 __device__ __forceinline__ int64_t slot_at(const CacheParams &c, const Item &it, int s) {
-    const int64_t pg = __ldg(&c.table[(int64_t)it.b * c.table_stride + s / c.page]);
-    return it.base + pg * c.mps + (int64_t)(s % c.page) * c.mts;
+    const Place p = place_of(c, s);
+    const int64_t pg = __ldg(&c.table[(int64_t)it.b * c.table_stride + p.index]);
+    return it.base + pg * c.mps + (int64_t)p.token * c.mts;
 }
 
 __device__ __forceinline__ uint32_t key_at(const EvictParams &P, const Item &it, int64_t at) {
@@ -298,10 +299,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         }
 #pragma unroll
         for (int i = 0; i < kMoveGroup; ++i) {
-            ps[i] = __ldg(&table[s[i] / c.page]);
-            pd[i] = __ldg(&table[d[i] / c.page]);
-            s[i] %= c.page;
-            d[i] %= c.page;
+            const Place a = place_of(c, s[i]), z = place_of(c, d[i]);
+            ps[i] = __ldg(&table[a.index]);
+            pd[i] = __ldg(&table[z.index]);
+            s[i] = a.token;
+            d[i] = z.token;
         }
         uint4 k[kMoveGroup], v[kMoveGroup];
 #pragma unroll

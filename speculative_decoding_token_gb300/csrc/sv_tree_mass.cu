@@ -172,7 +172,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
                 mbar_arrive(smem_u32(&M.s_empty[w]));
                 if (page >= 0 && !M.bad[chunk & 1])
                     atomicAdd(&P.c.mass[page * P.c.mps + g.head * P.c.mhs +
-                                        (int64_t)(s % P.c.page) * P.c.mts],
+                                        (int64_t)place_of(P.c, s).token * P.c.mts],
                               (sum[0] + sum[1]) + (sum[2] + sum[3]));
             }
             if (!ready) wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
@@ -250,7 +250,7 @@ __device__ void load_role(const AccumParams &P, const CUtensorMap *mk, Misc &M, 
                     const uint32_t dst = ring + slot * Sh::kTileBytes + lane * box * 128;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        tile_load(dst + c * Sh::kPanel, mk, c * 64, s % P.c.page, g.head, page, bar);
+                        tile_load(dst + c * Sh::kPanel, mk, c * 64, place_of(P.c, s).token, g.head, page, bar);
                 }
                 __syncwarp();
                 page = next;
@@ -278,7 +278,7 @@ __device__ void scout_role(const AccumParams &P, Misc &M, char *smem, Walk walk)
                 const int j = path[i], prev = i > 0 ? path[i - 1] : -1;
                 if (j <= prev || j >= nodes) bad |= SPECVERIFY_STATUS_BAD_TREE;
             }
-            const int pages = (g.s.L + g.s.n) / P.c.page + 1;
+            const int pages = place_of(P.c, g.s.L + g.s.n).index + 1;
 #pragma unroll 8
             for (int i = tid; i < pages; i += kScoutThreads)
                 if (page_at(P.c, g.b, i) < 0) bad |= SPECVERIFY_STATUS_BAD_CACHE;
