@@ -88,6 +88,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(addr)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t *r) {
+    static_assert(N == 16 || N == 32, "columns of a load");
+    if (N == 32)
+        tmem_ld32(addr, r);
+    else
+        tmem_ld16(addr, r);
+}
+
 // --- matrix products ----------------------------------------------------------
 // Shared-memory matrix descriptor of a tile in 128-byte rows with the 128-byte
 // swizzle, groups of 8 rows 1024 bytes apart. `lead`: for an operand whose

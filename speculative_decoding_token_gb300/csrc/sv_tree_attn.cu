@@ -7,11 +7,11 @@
 // matrix, row r = node r / G, head r % G, so each key is read once for all of
 // them: S = Q K^T and O += P V run on the tensor core in tiles of 128 rows by
 // 128 slots. A persistent CTA per SM:
-//   warps 0-3, 4-7  two softmax groups, a row a thread: S from tensor memory,
-//                   P back to it;
-//   warp 8          issues the products (one thread);
-//   warp 9          copies K and V tiles into a ring of shared-memory slots;
-//   warps 10, 11    go ahead of them: the next segment's Q tiles, and the check
+//   warps 0-7, 8-15 two softmax groups, half a row a thread: S from tensor
+//                   memory, P back to it;
+//   warp 16         issues the products (one thread);
+//   warp 17         copies K and V tiles into a ring of shared-memory slots;
+//   warps 18, 19    go ahead of them: the next segment's Q tiles, and the check
 //                   of its pages and parents.
 // The two groups take turns on the tensor core, one's softmax under the
 // other's products. Up to 128 rows share one Q tile and the groups alternate
@@ -34,13 +34,13 @@ namespace sv {
 
 namespace {
 
-constexpr int kSoftThreads = 256;
+constexpr int kSoftThreads = 512;
 constexpr int kAttnThreads = kSoftThreads + 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kScoutThreads = 64;
-// A softmax thread holds a row of S. A launch of 384 threads gives each 168
-// registers; the groups draw 208 and the last warpgroup keeps 80 (the sum, 496
-// a thread triple, stays below the launch's 504).
-constexpr int kSoftRegs = 208, kOtherRegs = 80;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kScoutThreads = 64;
+// A softmax thread holds half a row of S. A launch of 640 threads gives each 96
+// registers; the groups draw 104 and the last warpgroup keeps 64 (104 * 512 +
+// 64 * 128 registers, the launch's 96 * 640).
+constexpr int kSoftRegs = 104, kOtherRegs = 64;
 constexpr int kTmemCols = 512;
 constexpr float kTiny = 1e-37f;            // least weight of a piece: keeps inf * weight infinite
 
@@ -57,25 +57,6 @@ struct Shape {
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
-// What the scouts say of a segment, and whoever clears its last values.
-struct Scouted {
-    int8_t parent[kMaxNodes];
-    uint32_t nonfinite[kMaskWords];        // nodes of it whose value has an inf or NaN
-    uint32_t bad;                          // a page or a parent
-};
-
-struct Misc {
-    float2 ml[2][kTile];                   // maxima and sums of both groups' rows
-    Scouted seg[2];                        // of the even and the odd segments
-    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
-    uint64_t seg_full[2], seg_empty[2], drain;
-    long long rest0;                       // the CTA's first tile in its first sequence,
-    int32_t b0;                            // and that sequence
-    uint32_t tmem;
-    long long scan[kAttnThreads / 32];
-    int32_t abort;                         // a wait gave up
-};
-static_assert(sizeof(Misc) <= 2944, "Misc");
 
 // An item's place on the line starts with kHead units that are no tiles: what
 // its start and end cost beside its tiles (queries, sums, the output).
@@ -156,6 +137,27 @@ struct Walk {
     }
 };
 
+// What the scouts say of a segment, and whoever clears its last values.
+struct Scouted {
+    Segment g;                             // n = 0: the CTA's work is done
+    int8_t parent[kMaxNodes];
+    uint32_t nonfinite[kMaskWords];        // nodes of it whose value has an inf or NaN
+    uint32_t bad;                          // a page or a parent
+};
+
+struct Misc {
+    float x[4][kTile];                     // what the halves and the groups tell each other of a row
+    Scouted seg[2];                        // of the even and the odd segments
+    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t seg_full[2], seg_empty[2], drain;
+    long long rest0;                       // the CTA's first tile in its first sequence,
+    int32_t b0;                            // and that sequence
+    uint32_t tmem;
+    long long scan[kAttnThreads / 32];
+    int32_t abort;                         // a wait gave up
+};
+static_assert(sizeof(Misc) <= 2944, "Misc");
+
 // Place of a segment's K and V tile j in the order of the ring's uses. Group w
 // needs K of its next tile before V of its current one.
 __device__ __forceinline__ uint32_t k_at(const Segment &g, int j) {
@@ -170,7 +172,43 @@ __device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity,
 }
 
 // Barrier of the two softmax groups.
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+
+// The same; whether every thread's v was true.
+__device__ __forceinline__ bool soft_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 512, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// Barrier of the scouts; whether every thread's v was true.
+__device__ __forceinline__ bool scouts_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 10, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// Barrier of the two warps that share 32 rows; whether any thread's v was true.
+__device__ __forceinline__ bool pair_any(int bar, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
@@ -216,54 +254,53 @@ struct Range {
 // softmax groups
 
 template <bool FP16, int D>
-__device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk,
-                             uint32_t tmem) {
+__device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint32_t tmem) {
     using Sh = Shape<D>;
+    constexpr int H = kTile / 2;               // columns of S that a thread holds
+    constexpr int CW = D / 4;                  // columns of O at a time
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int w = warp >> 2;                   // group
+    const int w = warp >> 3, h = warp >> 2 & 1;  // group, half of its columns
     const int row = (warp & 3) * 32 + lane;    // of the group's Q tile
+    const int pair_bar = 2 + w * 4 + (warp & 3);  // barrier of the two warps that share 32 rows
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + Sh::kS + w * kTile;
     const float c2 = P.scale_log2;
     const float ninf = -INFINITY;
-    uint32_t s_phase = 0, o_phase[2] = {0, 0}, seg = 0;
+    uint32_t s_phase = 0, o_phase = 0, seg = 0;  // o_phase: a bit for each group
     uint32_t base = 0;  // ring uses before this segment
-    Segment g;
-    for (; walk.next(P, g); ++seg) {
-        const int t_begin = g.tile0 * kTile;
+    for (;; ++seg) {
         Scouted &sc = M.seg[seg & 1];
-        bool scouted = false;
-        const auto wait_scout = [&] {
-            if (!scouted) wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P.status);
-            scouted = true;
-        };
+        // (the barrier: all have read the last segment's O and x)
+        if (!soft_all(wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P.status))) break;
+        const Segment &g = sc.g;
+        const int n = g.n;
+        if (n == 0) break;
+        const bool pair = g.pair;
+        const int ahead = g.tile0 * kTile - g.s.L;
         // this thread's row
-        const int r_item = (g.pair ? w * kTile : 0) + row;
+        const int r_item = (pair ? w * kTile : 0) + row;
         const int gr = g.block * 2 * kTile + min(r_item, g.rows - 1);
         const int node = gr / P.G, qh = g.head * P.G + gr - node * P.G;
-        const bool warp_on = (g.pair ? w * kTile : 0) + (row & ~31) < g.rows;
+        const bool warp_on = (pair ? w * kTile : 0) + (row & ~31) < g.rows;
         float m_ref = ninf, l = 0.0f;
-        const int step = g.pair ? 1 : 2;
         bool fresh = true;
-        for (int j = g.pair ? 0 : w; j < g.n; j += step) {
+        for (int j = pair ? 0 : w; j < n; j += pair ? 1 : 2) {
             wait_on(M, M.s_full[w], s_phase, P.status);
             s_phase ^= 1;
             tc_fence_after();
-            const int t0 = t_begin + j * kTile;
-            const bool tail_tile = t0 + kTile > g.s.L;
+            const int shift = ahead + j * kTile;  // column c is node c + shift, a token before 0
+            const bool tail_tile = shift + kTile > 0;
             if (warp_on) {
-                uint32_t s[kTile];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+                uint32_t s[H];
+                tmem_ld32(ts + H * h, s);
+                tmem_ld32(ts + H * h + 32, s + 32);
                 tmem_wait_ld();
                 if (tail_tile) {
-                    wait_scout();
                     uint32_t up[kMaskWords] = {};  // the node's ancestors and itself
                     for (int i = node; i >= 0; i = sc.parent[i])
 #pragma unroll
                         for (int q = 0; q < kMaskWords; ++q)
                             if (i >> 5 == q) up[q] |= 1u << (i & 31);
-                    const int shift = t0 - g.s.L;  // column c is node c + shift, a token before 0
                     const auto word = [&](int i) -> uint32_t {
                         uint32_t x = i < 0 ? 0xffffffffu : 0u;
 #pragma unroll
@@ -272,8 +309,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                         return x;
                     };
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int at = 32 * q + shift;
+                    for (int q = 0; q < H / 32; ++q) {
+                        const int at = H * h + 32 * q + shift;
                         const uint32_t see =
                             __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
 #pragma unroll
@@ -281,63 +318,64 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                             if (!(see >> c & 1)) s[32 * q + c] = __float_as_uint(ninf);
                     }
                 }
-                float mx = ninf;
+                float m4[4] = {ninf, ninf, ninf, ninf};
 #pragma unroll
-                for (int i = 0; i < kTile; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
-                mx *= c2;
-                if (__any_sync(0xffffffffu, mx > m_ref + Range<FP16>::kSlack)) {
-                    const float up = fmaxf(m_ref, mx);
-                    const float f = m_ref == up ? 1.0f : ex2_approx(m_ref - up);
-                    m_ref = up;
+                for (int i = 0; i < H; i += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(s[i + c]), __uint_as_float(s[i + c + 4])));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+                // Both warps have read S when the barrier opens: P may go over it.
+                if (pair_any(pair_bar, mx > m_ref + Range<FP16>::kSlack)) {
+                    M.x[2 * w + h][row] = mx;
+                    pair_any(pair_bar, false);
+                    const float top = fmaxf(m_ref, fmaxf(M.x[2 * w][row], M.x[2 * w + 1][row]));
+                    const float f = m_ref == top ? 1.0f : ex2_approx(m_ref - top);
+                    m_ref = top;
                     l *= f;
                     if (!fresh) {
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
+#pragma unroll 1
+                        for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
+                            uint32_t o[16];
                             const uint32_t at = tmem + lanes + Sh::kO + w * D + c;
-                            tmem_ld32(at, o);
+                            tmem_ld16(at, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 16; ++i)
                                 o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32(at, o);
+                            tmem_st16(at, o);
                         }
                     }
                 }
                 const float off = Range<FP16>::kShift - (m_ref == ninf ? 0.0f : m_ref);
                 const f32x2 c22 = pack2(c2, c2), off2 = pack2(off, off);
                 f32x2 sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+                uint32_t p[H / 2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = 64 * h + 2 * i;
-                        const float2 x = unpack2(
-                            fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c22, off2));
-                        const float a = ex2_approx(x.x), b = ex2_approx(x.y);
-                        if (i & 1)
-                            sum1 = add2(sum1, pack2(a, b));
-                        else
-                            sum0 = add2(sum0, pack2(a, b));
-                        p[i] = pack_half<FP16>(a, b);
-                    }
-                    tmem_st32(ts + 32 * h, p);
+                for (int i = 0; i < H / 2; ++i) {
+                    const float2 x = unpack2(fma2(
+                        pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, off2));
+                    const float a = ex2_approx(x.x), b = ex2_approx(x.y);
+                    if (i & 1)
+                        sum1 = add2(sum1, pack2(a, b));
+                    else
+                        sum0 = add2(sum0, pack2(a, b));
+                    p[i] = pack_half<FP16>(a, b);
                 }
+                tmem_st32(ts + H / 2 * h, p);
                 const float2 sum = unpack2(add2(sum0, sum1));
                 l += sum.x + sum.y;
                 tmem_wait_st();
             }
             fresh = false;
-            if (tail_tile && (!g.pair || w == 0)) {
-                wait_scout();
+            if (tail_tile && (!pair || w == 0)) {
                 // a slot past the tree, or a node's inf or NaN: 0 in the products
                 // (the latter are added where they are seen, below)
                 const uint32_t use = base + v_at(g, j);
                 wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status);
                 char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
-                const int r0 = max(0, g.s.L - t0), gone = g.s.L + g.s.T - t0;
-                for (int i = tid & 127; i < (kTile - r0) * (D / 8); i += 128) {
+                const int r0 = max(0, -shift), gone = g.s.T - shift;
+                for (int i = tid & 255; i < (kTile - r0) * (D / 8); i += 256) {
                     const int r = r0 + i / (D / 8), c = i % (D / 8);
                     uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::kPanel + r * 128 +
                                                           ((c & 7) << 4));
@@ -350,8 +388,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                                        d4 = nonfinite_bits<FP16>(x.w);
                         if (a | b | c4 | d4) {
                             *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
-                            const int j = r + t0 - g.s.L;
-                            atomicOr(&sc.nonfinite[j >> 5], 1u << (j & 31));
+                            const int n = r + shift;
+                            atomicOr(&sc.nonfinite[n >> 5], 1u << (n & 31));
                         }
                     }
                 }
@@ -361,56 +399,58 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
             mbar_arrive(smem_u32(&M.p_full[w]));
         }
         // the item's sums
-        const bool used1 = g.pair || g.n > 1;
-        if (!g.pair || w == 0) {
-            wait_on(M, M.o_full[0], o_phase[0], P.status);
-        }
-        if (used1 && (!g.pair || w == 1)) {
-            wait_on(M, M.o_full[1], o_phase[1], P.status);
-        }
-        o_phase[0] ^= 1;
-        if (used1) o_phase[1] ^= 1;
+        const bool used1 = pair || n > 1;
+        if (!pair || w == 0) wait_on(M, M.o_full[0], o_phase & 1, P.status);
+        if (used1 && (!pair || w == 1)) wait_on(M, M.o_full[1], o_phase >> 1, P.status);
+        o_phase ^= used1 ? 3 : 1;
         tc_fence_after();
-        base += 2 * g.n;
+        base += 2 * n;
         float wgt[2] = {1.0f, 1.0f};
         float mf = m_ref, lf = l;
-        if (!g.pair) {
-            // join the groups: each takes half of the columns
-            M.ml[w][row] = make_float2(m_ref, l);
+        if (!pair) {
+            // join the groups, each of the four warpgroups a quarter of the columns
+            M.x[2 * w][row] = m_ref;  // both halves' is the same
             soft_sync();
-            const float2 a = M.ml[0][row], b = M.ml[1][row];
-            mf = fmaxf(a.x, b.x);
-            wgt[0] = a.x == ninf ? 0.0f : fmaxf(ex2_approx(a.x - mf), kTiny);
-            wgt[1] = b.x == ninf ? 0.0f : fmaxf(ex2_approx(b.x - mf), kTiny);
-            lf = a.y * wgt[0] + (used1 ? b.y * wgt[1] : 0.0f);
+            const float m0 = M.x[0][row], m1 = M.x[2][row];
+            mf = fmaxf(m0, m1);
+            wgt[0] = m0 == ninf ? 0.0f : fmaxf(ex2_approx(m0 - mf), kTiny);
+            wgt[1] = m1 == ninf ? 0.0f : fmaxf(ex2_approx(m1 - mf), kTiny);
+            soft_sync();
+            M.x[2 * w + h][row] = l * wgt[w];
+            soft_sync();
+            lf = M.x[0][row] + M.x[1][row];
+            if (used1) lf += M.x[2][row] + M.x[3][row];
+        } else {
+            M.x[2 * w + h][row] = l;
+            soft_sync();  // of all: group 0's sc.nonfinite, too
+            lf = M.x[2 * w][row] + M.x[2 * w + 1][row];
         }
-        wait_scout();
-        if (g.pair && (g.tile0 + g.n) * kTile > g.s.L) soft_sync();  // group 0's sc.nonfinite
         if (sc.bad) lf = NAN;
         if (warp_on) {
             const bool whole = g.first && g.last;
             const bool mine = r_item < g.rows;
             const float inv = whole ? (lf == 0.0f ? 0.0f : 1.0f / lf) : 1.0f;
             const int64_t orow = g.s.row0 + node;
-            const int c_begin = g.pair ? 0 : w * (D / 2), c_end = g.pair ? D : c_begin + D / 2;
+            const int c_begin = pair ? h * (D / 2) : (2 * w + h) * CW;
+            const int c_end = c_begin + (pair ? D / 2 : CW);
             const int piece = g.first ? 1 : 0;  // a CTA's first and last segments may be pieces
             const int64_t at = ((int64_t)blockIdx.x * 2 + piece) * (2 * kTile) + r_item;
             bool any_odd = false;
 #pragma unroll
             for (int q = 0; q < kMaskWords; ++q) any_odd |= sc.nonfinite[q] != 0;
 #pragma unroll 1
-            for (int c = c_begin; c < c_end; c += 32) {
-                uint32_t o[32];
-                float f[32];
-                tmem_ld32(tmem + lanes + Sh::kO + (g.pair ? w * D : 0) + c, o);
+            for (int c = c_begin; c < c_end; c += CW) {
+                uint32_t o[CW];
+                float f[CW];
+                tmem_ld_n<CW>(tmem + lanes + Sh::kO + (pair ? w * D : 0) + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * wgt[0];
-                if (!g.pair && used1) {
-                    tmem_ld32(tmem + lanes + Sh::kO + D + c, o);
+                for (int i = 0; i < CW; ++i) f[i] = __uint_as_float(o[i]) * wgt[0];
+                if (!pair && used1) {
+                    tmem_ld_n<CW>(tmem + lanes + Sh::kO + D + c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(o[i]), wgt[1], f[i]);
+                    for (int i = 0; i < CW; ++i) f[i] = fmaf(__uint_as_float(o[i]), wgt[1], f[i]);
                 }
                 if (any_odd && mine) {
                     // a seen inf or NaN decides its element whatever its weight
@@ -421,7 +461,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                             P.c.v + (int64_t)g.head * P.c.hs + page_of(P.c, g.b, s) * P.c.ps +
                             (int64_t)place_of(P.c, s).token * P.c.ts + c * 2);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < CW / 2; ++i) {
                             const uint32_t x = v[i], bits = nonfinite_bits<FP16>(x);
                             if (bits & 0xffffu) f[2 * i] += half_at<FP16>(x, 0);
                             if (bits >> 16) f[2 * i + 1] += half_at<FP16>(x, 1);
@@ -433,7 +473,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                         uint4 *dst = reinterpret_cast<uint4 *>(P.out + orow * P.o_rs +
                                                                (int64_t)qh * P.o_hs + c * 2);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < CW / 8; ++i)
                             dst[i] = make_uint4(
                                 pack_half<FP16>(f[8 * i] * inv, f[8 * i + 1] * inv),
                                 pack_half<FP16>(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
@@ -441,11 +481,12 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
                                 pack_half<FP16>(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st_global_8(P.piece_o + at * D + c + 8 * i, f + 8 * i);
+                        for (int i = 0; i < CW / 8; ++i)
+                            st_global_8(P.piece_o + at * D + c + 8 * i, f + 8 * i);
                     }
                 }
             }
-            if (mine && (g.pair || w == 0)) {
+            if (mine && h == 0 && (pair || w == 0)) {
                 if (!whole)
                     P.piece_ml[at] = make_float2(mf, lf);
                 else if (P.lse)
@@ -455,7 +496,6 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, Walk 
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&M.seg_empty[seg & 1]));
-        if (!g.pair) soft_sync();  // both have read both groups' O
     }
 }
 
@@ -470,7 +510,15 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
     const uint32_t q = smem_u32(smem);
     uint32_t seg = 0, uses[2] = {0, 0}, turn = 0;
     Segment g;
-    for (; walk.next(P, g); ++seg) {
+    for (;; ++seg) {
+        if (!walk.next(P, g)) {
+            if (wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status)) {
+                if (tid == 0) M.seg[seg & 1].g.n = 0;
+                mbar_arrive(smem_u32(&M.seg_full[seg & 1]));
+            }
+            break;
+        }
+        bool ok = true;
         // the checks' first loads go out before the copies
         const int t_begin = g.tile0 * kTile, t_end = min((g.tile0 + g.n) * kTile, g.s.L + g.s.T);
         const bool tail = t_end > g.s.L;
@@ -485,7 +533,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         // Q rows into their tiles, 16-byte chunks swizzled within 8 rows
         for (int i = 0; i < (g.pair ? 2 : 1); ++i) {
             const int x = g.pair ? i : turn;
-            wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status);
+            ok = wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status) && ok;
             const int r_first = i * kTile, r_count = min(kTile, g.rows - r_first);
             constexpr int R = kScoutThreads / C;  // rows at a time
             const int c = tid % C, dn = R / P.G, dh = R - dn * P.G;
@@ -511,7 +559,8 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         }
         if (!g.pair) turn ^= 1;
         // pages and parents
-        wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status);
+        ok = wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status) && ok;
+        if (!scouts_all(ok)) break;
         Scouted &sc = M.seg[seg & 1];
         int bad = page_ok ? 0 : SPECVERIFY_STATUS_BAD_CACHE;
         for (int i = pg0 + tid + kScoutThreads; i <= pg1; i += kScoutThreads)
@@ -526,8 +575,11 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
                 if (no) bad |= SPECVERIFY_STATUS_BAD_TREE;
             }
         if (tid < kMaskWords) sc.nonfinite[tid] = 0;
-        if (tid == 0) sc.bad = 0;
-        asm volatile("barrier.cta.sync 2, 64;" ::: "memory");
+        if (tid == 0) {
+            sc.g = g;
+            sc.bad = 0;
+        }
+        scouts_all(true);
         if (bad) {
             atomicOr(P.status, bad);
             sc.bad = 1;
@@ -677,7 +729,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(smem_u32(&M.seg_full[w]), kScoutThreads);
             mbar_init(smem_u32(&M.seg_empty[w]), kSoftThreads);
             mbar_init(smem_u32(&M.s_full[w]), 1);
-            mbar_init(smem_u32(&M.p_full[w]), 128);
+            mbar_init(smem_u32(&M.p_full[w]), kSoftThreads / 2);
             mbar_init(smem_u32(&M.o_full[w]), 1);
         }
         mbar_init(smem_u32(&M.drain), 1);
@@ -741,7 +793,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t tmem = M.tmem;
     if (warp < kSoftThreads / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        softmax_role<FP16, D>(P, M, smem, walk, tmem);
+        softmax_role<FP16, D>(P, M, smem, tmem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     }
