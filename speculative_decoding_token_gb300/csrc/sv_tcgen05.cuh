@@ -134,30 +134,45 @@ __host__ __device__ constexpr uint32_t mma_desc(bool fp16, bool b_mn, int m, int
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D (tensor memory) = A B (+ D), 16 steps of the summed dimension, issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
-                                       bool add) {
+// Whether this lane is the one that issues its warp's products. The warp runs
+// the issuing code as a whole, so that descriptors stay in uniform registers;
+// code under `if (lane == 0)` takes about 100 cycles a product instead of 64.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// D (tensor memory) = A B (+ D), 16 steps of the summed dimension, issued by
+// the lane whose `on` is set.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add,
+                                       bool on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"((uint32_t)on)
         : "memory");
 }
 
 // The same with A in tensor memory, two elements a column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
-                                       bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add,
+                                       bool on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"((uint32_t)on)
         : "memory");
 }
 
-// One arrival on `bar` once every product that this thread issued has completed.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+// One arrival on `bar` once every product that the lane issued has completed.
+__device__ __forceinline__ void mma_commit(uint32_t bar, bool on) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar),
+        "r"((uint32_t)on)
         : "memory");
 }
 

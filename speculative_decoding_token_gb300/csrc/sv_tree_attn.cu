@@ -596,6 +596,7 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
     using Sh = Shape<D>;
     constexpr uint32_t dqk = mma_desc(FP16, false, kTile, kTile), dpv = mma_desc(FP16, true, kTile, D);
     const uint32_t q0 = smem_u32(smem), ring = q0 + Sh::kRing;
+    const bool on = elect_one();
     uint32_t base = 0, uses[2] = {0, 0}, turn = 0, p_phase[2] = {0, 0};
     Segment g;
     bool ok = true;
@@ -616,11 +617,11 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * Sh::kPanel + (k & 3) * 32;
                 mma_ss(tmem + Sh::kS + w * kTile, smem_desc(a + off, 0), smem_desc(b + off, 0), dqk,
-                       k > 0);
+                       k > 0, on);
             }
-            mma_commit(smem_u32(&M.s_full[w]));
-            if (g.pair ? t + 2 >= steps : t + 1 == steps) mma_commit(smem_u32(&M.q_empty[x]));
-            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]));
+            mma_commit(smem_u32(&M.s_full[w]), on);
+            if (g.pair ? t + 2 >= steps : t + 1 == steps) mma_commit(smem_u32(&M.q_empty[x]), on);
+            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]), on);
         };
         if (ok) qk(0);
         if (ok && steps > 1) qk(1);
@@ -637,16 +638,16 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(tmem + Sh::kO + w * D, tmem + Sh::kS + w * kTile + k * 8,
-                       smem_desc(b + k * 2048, Sh::kPanel), dpv, t >= 2 || k > 0);
-            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]));
-            if (t + 2 >= steps) mma_commit(smem_u32(&M.o_full[w]));
+                       smem_desc(b + k * 2048, Sh::kPanel), dpv, t >= 2 || k > 0, on);
+            if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]), on);
+            if (t + 2 >= steps) mma_commit(smem_u32(&M.o_full[w]), on);
             if (t + 2 < steps) qk(t + 2);
         }
         base += 2 * g.n;
         if (!g.pair) turn ^= 1;
     }
     if (!ok) {  // no product outlives the CTA
-        mma_commit(smem_u32(&M.drain));
+        mma_commit(smem_u32(&M.drain), on);
         mbar_wait_bounded(smem_u32(&M.drain), 0);
     }
 }
@@ -798,8 +799,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     }
     if (warp == kMmaWarp) {
-        if (lane == 0) mma_role<FP16, D>(P, M, smem, walk, tmem);
-        __syncwarp();
+        mma_role<FP16, D>(P, M, smem, walk, tmem);
     } else if (warp > kLoadWarp) {
         scout_role<FP16, D>(P, M, smem, walk);
     } else if (warp == kLoadWarp) {

@@ -185,6 +185,7 @@ template <bool FP16, int D>
 __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, uint32_t tmem) {
     using Sh = Shape<D>;
     const uint32_t q0 = smem_u32(smem), ring = q0 + Sh::kRing;
+    const bool on = elect_one();
     uint32_t chunk = 0, turn = 0;
     Segment g;
     bool ok = true;
@@ -204,16 +205,16 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k >> 2) * Sh::kPanel + (k & 3) * 32;
-                    mma_ss(tmem + w * kRows, smem_desc(a + off, 0), smem_desc(b + off, 0), desc, k > 0);
+                    mma_ss(tmem + w * kRows, smem_desc(a + off, 0), smem_desc(b + off, 0), desc, k > 0, on);
                 }
-                mma_commit(smem_u32(&M.s_full[w]));
-                mma_commit(smem_u32(&M.empty[slot]));
+                mma_commit(smem_u32(&M.s_full[w]), on);
+                mma_commit(smem_u32(&M.empty[slot]), on);
             }
-            if (ok) mma_commit(smem_u32(&M.q_empty[chunk & 1]));
+            if (ok) mma_commit(smem_u32(&M.q_empty[chunk & 1]), on);
         }
     }
     if (!ok) {  // no product outlives the CTA
-        mma_commit(smem_u32(&M.drain));
+        mma_commit(smem_u32(&M.drain), on);
         mbar_wait_bounded(smem_u32(&M.drain), 0);
     }
 }
@@ -392,8 +393,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     if (warp < kMmaWarp) {
         sum_role(P, M, walk, tmem);
     } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_role<FP16, D>(P, M, smem, walk, tmem);
-        __syncwarp();
+        mma_role<FP16, D>(P, M, smem, walk, tmem);
     } else if (warp == kLoadWarp) {
         load_role<D>(P, &mk, M, smem, walk);
     } else {
