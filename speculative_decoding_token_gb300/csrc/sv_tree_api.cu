@@ -213,6 +213,10 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
     if (!lens) return SPECVERIFY_ERR_INVALID_ARG;
+    // one sequence's share of the work line is counted in 31 bits
+    const int64_t tiles = (int64_t)cache->max_pages * cache->page_size / 128 + 4;
+    if (tiles * ((int64_t)tree->max_nodes * heads / 256 + cache->kv_heads) > INT32_MAX)
+        return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
     sv::TreeAttnParams p{};

@@ -67,8 +67,9 @@ struct Seq {
     int L, T, tiles, blocks;
     int64_t row0;
 
-    __device__ long long units(const TreeAttnParams &P) const {
-        return tiles ? (long long)(tiles + kHead) * blocks * P.c.kv_heads : 0;
+    // (the host has checked that a sequence's fit 31 bits)
+    __device__ int units(const TreeAttnParams &P) const {
+        return tiles ? (tiles + kHead) * blocks * P.c.kv_heads : 0;
     }
 };
 
@@ -105,7 +106,7 @@ struct Segment {
 
 struct Walk {
     int b;
-    long long rest;   // next unit within sequence b
+    int rest;         // next unit within sequence b
     long long left;   // units of this CTA still to do
 
     __device__ bool next(const TreeAttnParams &P, Segment &g) {
@@ -117,7 +118,7 @@ struct Walk {
                 continue;
             }
             const int len = g.s.tiles + kHead;
-            const int item = (int)(rest / len), u = (int)(rest - (long long)item * len);
+            const int item = rest / len, u = rest - item * len;
             const int end = (int)min((long long)len, u + left);
             rest += end - u;
             left -= end - u;
@@ -148,15 +149,36 @@ struct Scouted {
 struct Misc {
     float x[4][kTile];                     // what the halves and the groups tell each other of a row
     Scouted seg[2];                        // of the even and the odd segments
-    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
     uint64_t seg_full[2], seg_empty[2], drain;
-    long long rest0;                       // the CTA's first tile in its first sequence,
+    int32_t rest0;                         // the CTA's first unit in its first sequence,
     int32_t b0;                            // and that sequence
     uint32_t tmem;
     long long scan[kAttnThreads / 32];
     int32_t abort;                         // a wait gave up
 };
 static_assert(sizeof(Misc) <= 2944, "Misc");
+
+// The line's cut: CTA i has units [cut.at(i), cut.at(i + 1)), the first `more` one
+// more than the others.
+struct Cut {
+    int ctas, more;
+    long long each;
+
+    __device__ Cut(long long total, int grid) {
+        ctas = (int)min((long long)grid, total);
+        each = ctas == 0 ? 0 : (total >> 31 ? total / ctas : (long long)((int)total / ctas));
+        more = (int)(total - each * ctas);
+    }
+    __device__ long long at(int i) const { return i * each + min(i, more); }
+    // The CTA of a unit.
+    __device__ int of(long long unit) const {
+        int i = 0;  // at(i) <= unit < at(i + 1), by halves
+        for (int step = 1 << (31 - __clz(ctas)); step > 0; step >>= 1)
+            if (i + step < ctas && at(i + step) <= unit) i += step;
+        return i;
+    }
+};
 
 // Place of a segment's K and V tile j in the order of the ring's uses. Group w
 // needs K of its next tile before V of its current one.
@@ -290,10 +312,44 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
             tc_fence_after();
             const int shift = ahead + j * kTile;  // column c is node c + shift, a token before 0
             const bool tail_tile = shift + kTile > 0;
+            if (tail_tile && (!pair || w == 0)) {
+                // a slot past the tree, or a node's inf or NaN: 0 in the products
+                // (the latter are added where they are seen, below)
+                const uint32_t use = base + v_at(g, j);
+                wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status);
+                char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
+                const int r0 = max(0, -shift), gone = g.s.T - shift;
+                for (int i = tid & 255; i < (kTile - r0) * (D / 8); i += 256) {
+                    const int r = r0 + i / (D / 8), c = i % (D / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::kPanel + r * 128 +
+                                                          ((c & 7) << 4));
+                    if (r >= gone) {
+                        *at = make_uint4(0, 0, 0, 0);
+                    } else {
+                        uint4 x = *at;
+                        const uint32_t a = nonfinite_bits<FP16>(x.x), b = nonfinite_bits<FP16>(x.y),
+                                       c4 = nonfinite_bits<FP16>(x.z),
+                                       d4 = nonfinite_bits<FP16>(x.w);
+                        if (a | b | c4 | d4) {
+                            *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
+                            const int n = r + shift;
+                            atomicOr(&sc.nonfinite[n >> 5], 1u << (n & 31));
+                        }
+                    }
+                }
+                fence_async_smem();
+            }
+            // P's first half of the slots is complete when both warps of a row have
+            // done theirs of it, and its products start under the second half
+            const auto done = [&](int part) {
+                tc_fence_before();
+                __syncwarp();  // a warp's one arrival: 256 on one barrier take their time
+                if (lane == 0) mbar_arrive(smem_u32(&M.p_full[w][part]));
+            };
             if (warp_on) {
-                uint32_t s[H];
-                tmem_ld32(ts + H * h, s);
-                tmem_ld32(ts + H * h + 32, s + 32);
+                uint32_t s[H];  // columns 32 h and up of each half of S
+                tmem_ld32(ts + 32 * h, s);
+                tmem_ld32(ts + H + 32 * h, s + 32);
                 tmem_wait_ld();
                 if (tail_tile) {
                     uint32_t up[kMaskWords] = {};  // the node's ancestors and itself
@@ -310,7 +366,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                     };
 #pragma unroll
                     for (int q = 0; q < H / 32; ++q) {
-                        const int at = H * h + 32 * q + shift;
+                        const int at = H * q + 32 * h + shift;
                         const uint32_t see =
                             __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
 #pragma unroll
@@ -350,53 +406,32 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                 const float off = Range<FP16>::kShift - (m_ref == ninf ? 0.0f : m_ref);
                 const f32x2 c22 = pack2(c2, c2), off2 = pack2(off, off);
                 f32x2 sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
-                uint32_t p[H / 2];
 #pragma unroll
-                for (int i = 0; i < H / 2; ++i) {
-                    const float2 x = unpack2(fma2(
-                        pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, off2));
-                    const float a = ex2_approx(x.x), b = ex2_approx(x.y);
-                    if (i & 1)
-                        sum1 = add2(sum1, pack2(a, b));
-                    else
-                        sum0 = add2(sum0, pack2(a, b));
-                    p[i] = pack_half<FP16>(a, b);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = 32 * q + 2 * i;
+                        const float2 x = unpack2(fma2(
+                            pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c22, off2));
+                        const float a = ex2_approx(x.x), b = ex2_approx(x.y);
+                        if (i & 1)
+                            sum1 = add2(sum1, pack2(a, b));
+                        else
+                            sum0 = add2(sum0, pack2(a, b));
+                        p[i] = pack_half<FP16>(a, b);
+                    }
+                    tmem_st16(ts + 32 * q + 16 * h, p);
+                    tmem_wait_st();
+                    done(q);
                 }
-                tmem_st32(ts + H / 2 * h, p);
                 const float2 sum = unpack2(add2(sum0, sum1));
                 l += sum.x + sum.y;
-                tmem_wait_st();
+            } else {
+                done(0);
+                done(1);
             }
             fresh = false;
-            if (tail_tile && (!pair || w == 0)) {
-                // a slot past the tree, or a node's inf or NaN: 0 in the products
-                // (the latter are added where they are seen, below)
-                const uint32_t use = base + v_at(g, j);
-                wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status);
-                char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
-                const int r0 = max(0, -shift), gone = g.s.T - shift;
-                for (int i = tid & 255; i < (kTile - r0) * (D / 8); i += 256) {
-                    const int r = r0 + i / (D / 8), c = i % (D / 8);
-                    uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * Sh::kPanel + r * 128 +
-                                                          ((c & 7) << 4));
-                    if (r >= gone) {
-                        *at = make_uint4(0, 0, 0, 0);
-                    } else {
-                        uint4 x = *at;
-                        const uint32_t a = nonfinite_bits<FP16>(x.x), b = nonfinite_bits<FP16>(x.y),
-                                       c4 = nonfinite_bits<FP16>(x.z),
-                                       d4 = nonfinite_bits<FP16>(x.w);
-                        if (a | b | c4 | d4) {
-                            *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
-                            const int n = r + shift;
-                            atomicOr(&sc.nonfinite[n >> 5], 1u << (n & 31));
-                        }
-                    }
-                }
-                fence_async_smem();
-            }
-            tc_fence_before();
-            mbar_arrive(smem_u32(&M.p_full[w]));
         }
         // the item's sums
         const bool used1 = pair || n > 1;
@@ -603,13 +638,15 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
     while (ok && walk.next(P, g)) {
         const int steps = g.pair ? 2 * g.n : g.n;
         // step t: group t % 2, tile t (or t / 2 when both groups take every tile)
+        uint32_t k_slot = 0, k_par = 0;
+        const auto k_ready = [&](int t) { const uint32_t use = base + k_at(g, g.pair ? t >> 1 : t); k_slot = use % Sh::kSlots; k_par = use / Sh::kSlots & 1; };
         const auto qk = [&](int t) {
-            const int j = g.pair ? t >> 1 : t, w = t & 1;
-            const uint32_t use = base + k_at(g, j), slot = use % Sh::kSlots;
+            const int w = t & 1;
+            const uint32_t slot = k_slot, kpar = k_par;
             const int x = g.pair ? w : turn;
             if (t == 0 || (g.pair && t == 1)) ok = wait_on(M, M.q_full[x], uses[x]++ & 1, P.status);
             if (!g.pair || w == 0)
-                ok = ok && wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
+                ok = ok && wait_on(M, M.full[slot], kpar, P.status);
             if (!ok) return;
             tc_fence_after();
             const uint32_t a = q0 + x * Sh::kTileBytes, b = ring + slot * Sh::kTileBytes;
@@ -623,22 +660,28 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             if (g.pair ? t + 2 >= steps : t + 1 == steps) mma_commit(smem_u32(&M.q_empty[x]), on);
             if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]), on);
         };
+        k_ready(0);
         if (ok) qk(0);
+        k_ready(1);
         if (ok && steps > 1) qk(1);
         for (int t = 0; ok && t < steps; ++t) {
             const int j = g.pair ? t >> 1 : t, w = t & 1;
             const uint32_t use = base + v_at(g, j), slot = use % Sh::kSlots;
-            ok = wait_on(M, M.p_full[w], p_phase[w], P.status);
-            p_phase[w] ^= 1;
-            if (ok && (!g.pair || w == 0))
-                ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
-            if (!ok) break;
-            tc_fence_after();
+            k_ready(t + 2);
+            if (!g.pair || w == 0) ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
             const uint32_t b = ring + slot * Sh::kTileBytes;
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(tmem + Sh::kO + w * D, tmem + Sh::kS + w * kTile + k * 8,
-                       smem_desc(b + k * 2048, Sh::kPanel), dpv, t >= 2 || k > 0, on);
+            for (int part = 0; part < 2; ++part) {
+                ok = ok && wait_on(M, M.p_full[w][part], p_phase[w], P.status);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = part * kTile / 32; k < (part + 1) * kTile / 32; ++k)
+                    mma_ts(tmem + Sh::kO + w * D, tmem + Sh::kS + w * kTile + k * 8,
+                           smem_desc(b + k * 2048, Sh::kPanel), dpv, t >= 2 || k > 0, on);
+            }
+            p_phase[w] ^= 1;
+            if (!ok) break;
             if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]), on);
             if (t + 2 >= steps) mma_commit(smem_u32(&M.o_full[w]), on);
             if (t + 2 < steps) qk(t + 2);
@@ -730,7 +773,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(smem_u32(&M.seg_full[w]), kScoutThreads);
             mbar_init(smem_u32(&M.seg_empty[w]), kSoftThreads);
             mbar_init(smem_u32(&M.s_full[w]), 1);
-            mbar_init(smem_u32(&M.p_full[w]), kSoftThreads / 2);
+            mbar_init(smem_u32(&M.p_full[w][0]), kSoftThreads / 64);
+            mbar_init(smem_u32(&M.p_full[w][1]), kSoftThreads / 64);
             mbar_init(smem_u32(&M.o_full[w]), 1);
         }
         mbar_init(smem_u32(&M.drain), 1);
@@ -773,9 +817,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (i < warp) before += M.scan[i];
         total += M.scan[i];
     }
-    const long long ctas = min((long long)gridDim.x, total);
-    const long long lo = (int)blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-    const long long hi = (int)blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
+    const Cut cut(total, gridDim.x);
+    const int cta = min((int)blockIdx.x, cut.ctas);
+    const long long lo = cut.at(cta), hi = cut.at(min(cta + 1, cut.ctas));
     if (lo < hi && before <= lo && lo < before + mine) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
@@ -811,8 +855,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             Segment g;
             while (v.next(P, g)) {
                 if (g.first && !g.last) {  // the CTA's last segment: the line goes on at hi
-                    const long long end = hi + g.s.tiles - g.n;
-                    o.pieces = (int)((end * ctas - 1) / total) - (int)blockIdx.x + 1;
+                    o.pieces = cut.of(hi + g.s.tiles - g.n - 1) - (int)blockIdx.x + 1;
                     o.rows = g.rows;
                     o.first_row = g.block * 2 * kTile;
                     o.head = g.head;
@@ -827,11 +870,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the pieces of the items that were cut: block (c, y) rows 32 y and up of
-// the item that CTA c began, four a warp. Piece 0 is c's last segment, the next
+// Joins the pieces of the items that were cut: block (c, y) rows 8 y and up of
+// the item that CTA c began, two a warp. Piece 0 is c's last segment, the next
 // CTAs' first segments follow. Bound by the latency of its loads: the first
 // kAhead pieces are read before anything is known of their weights.
-constexpr int kJoinWarps = 8, kJoinRows = 4, kAhead = 2;
+constexpr int kJoinWarps = 4, kJoinRows = 2, kAhead = 8;
 
 template <bool FP16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
@@ -851,12 +894,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     float x[kAhead][kJoinRows][W], m[kJoinRows], l[kJoinRows] = {}, f[kJoinRows][W] = {};
     float2 ml[kAhead][kJoinRows];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)  // a cut item has two pieces at least
+    for (int i = 0; i < kAhead; ++i)
+        if (i < o.pieces)
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) {
-            ml[i][k] = P.piece_ml[at(i, k)];
-            piece(i, k, x[i][k]);
-        }
+            for (int k = 0; k < kJoinRows; ++k) {
+                ml[i][k] = P.piece_ml[at(i, k)];
+                piece(i, k, x[i][k]);
+            }
 #pragma unroll
     for (int k = 0; k < kJoinRows; ++k) {
         m[k] = -INFINITY;
@@ -873,16 +917,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
+        if (i < o.pieces)
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) add(k, ml[i][k], x[i][k]);
-#pragma unroll 2
-    for (int i = kAhead; i < o.pieces; ++i)
+            for (int k = 0; k < kJoinRows; ++k) add(k, ml[i][k], x[i][k]);
+    for (int i0 = kAhead; i0 < o.pieces; i0 += kAhead) {
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) {
-            float v[W];
-            piece(i, k, v);
-            add(k, P.piece_ml[at(i, k)], v);
-        }
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < o.pieces)
+#pragma unroll
+                for (int k = 0; k < kJoinRows; ++k) {
+                    ml[i][k] = P.piece_ml[at(i0 + i, k)];
+                    piece(i0 + i, k, x[i][k]);
+                }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < o.pieces)
+#pragma unroll
+                for (int k = 0; k < kJoinRows; ++k) add(k, ml[i][k], x[i][k]);
+    }
 #pragma unroll
     for (int k = 0; k < kJoinRows; ++k) {
         if (r0 + k >= o.rows) break;
