@@ -113,6 +113,7 @@ struct EvictParams {
     int32_t moves;            // list entries of one item: min(budget, capacity - budget)
     int32_t *move_src, *move_dst;  // [items, moves]
     int32_t *move_cnt;        // [items]
+    int32_t inline_moves;     // the selecting CTA makes its item's moves
     int32_t *status;
 };
 
@@ -125,7 +126,7 @@ cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s);
 cudaError_t prepare_accumulate();
 cudaError_t launch_accumulate(AccumParams p, int num_sms, cudaStream_t s);
 cudaError_t prepare_evict();
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+cudaError_t launch_evict(EvictParams p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device helpers

@@ -98,6 +98,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;             // two a thread
 constexpr int kKeyCap = 48 * 1024;         // 192 KiB
+constexpr int kSelBatch = 8;               // slots of a thread read at a time
 
 // Order-preserving bits of a mass: -0 as +0, a NaN as the least. A protected
 // token's key is above every one of them.
@@ -119,10 +120,84 @@ __device__ __forceinline__ int64_t slot_at(const CacheParams &c, const Item &it,
     return it.base + pg * c.mps + (int64_t)p.token * c.mts;
 }
 
-__device__ __forceinline__ uint32_t key_at(const EvictParams &P, const Item &it, int64_t at) {
-    const int pos = P.c.pos[at];
-    const float m = P.c.mass[at];
-    return pos < P.sink || pos >= it.seen - P.recent ? 0xffffffffu : mass_key(m);
+__device__ __forceinline__ uint32_t key_of_token(const EvictParams &P, const Item &it, float mass,
+                                                 int pos) {
+    return pos < P.sink || pos >= it.seen - P.recent ? 0xffffffffu : mass_key(mass);
+}
+
+// Eviction, moves: a source lies at or past the budget and a destination below
+// it, so moves never meet. d / 8 threads take a group of moves, all of its rows
+// in flight at once; bound by the bytes of the moved rows. Four moves a group
+// in the moving kernel (B = 16, 32k to 4k: 119 us a call; two 122, eight 151),
+// two where the selecting CTA moves (its threads have 64 registers).
+constexpr int kMoveThreads = 256;
+constexpr int kMoveGroup = 4, kOwnGroup = 2;
+
+// Moves of an item, groups `first`, `first` + `step`, ... by d / 8 threads, of
+// which this is number `part`.
+template <int M>
+__device__ __forceinline__ void move_tokens(const EvictParams &P, int item, int cnt, int first,
+                                            int step, int part) {
+    const CacheParams &c = P.c;
+    const int head = item % c.kv_heads, b = item / c.kv_heads % P.B,
+              layer = item / c.kv_heads / P.B;
+    const int64_t base = layer * c.ls + head * c.hs + part * 16;
+    const int64_t mbase = layer * c.mls + head * c.mhs, list = (int64_t)item * P.moves;
+    const int32_t *table = c.table + (int64_t)b * c.table_stride;
+    for (int r0 = first * M; r0 < cnt; r0 += step * M) {
+        int s[M], d[M];
+        int64_t ps[M], pd[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int64_t at = list + min(r0 + i, cnt - 1);
+            s[i] = P.move_src[at];
+            d[i] = P.move_dst[at];
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const Place a = place_of(c, s[i]), z = place_of(c, d[i]);
+            ps[i] = __ldg(&table[a.index]);
+            pd[i] = __ldg(&table[z.index]);
+            s[i] = a.token;
+            d[i] = z.token;
+        }
+        uint4 k[M], v[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const int64_t so = base + ps[i] * c.ps + s[i] * c.ts;
+            k[i] = *reinterpret_cast<const uint4 *>(c.k + so);
+            v[i] = *reinterpret_cast<const uint4 *>(c.v + so);
+        }
+        // thread `part` also takes mass or pos of one of the moves
+        const int mi = part >> 1;
+        if (mi < M && r0 + mi < cnt) {
+            int64_t ms = 0, md = 0;
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+                if (i == mi) {
+                    ms = mbase + ps[i] * c.mps + s[i] * c.mts;
+                    md = mbase + pd[i] * c.mps + d[i] * c.mts;
+                }
+            if (part & 1)
+                P.pos_out[md] = c.pos[ms];
+            else
+                P.mass_out[md] = c.mass[ms];
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            if (r0 + i >= cnt) break;
+            const int64_t to = base + pd[i] * c.ps + d[i] * c.ts;
+            *reinterpret_cast<uint4 *>(c.k + to) = k[i];
+            *reinterpret_cast<uint4 *>(c.v + to) = v[i];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int chunks = P.c.d / 8, groups = kMoveThreads / chunks, item = blockIdx.x;
+    move_tokens<kMoveGroup>(P, item, P.move_cnt[item], blockIdx.y * groups + threadIdx.x / chunks,
+                gridDim.y * groups, threadIdx.x % chunks);
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams P) {
@@ -149,7 +224,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     bad = __syncthreads_or(bad);
     const int N = it.len, keep = min(N, P.budget);
     if (tid == 0) {
-        if (P.moves > 0 && (N <= P.budget || bad)) P.move_cnt[item] = 0;
+        if (!P.inline_moves && (N <= P.budget || bad)) P.move_cnt[item] = 0;
         if (it.layer == 0 && it.head == 0) P.new_lens[it.b] = bad ? N : keep;
         if (bad) atomicOr(P.status, SPECVERIFY_STATUS_BAD_CACHE);
     }
@@ -165,7 +240,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         return;
     }
     const bool held = N <= kKeyCap;
-    const auto key_of = [&](int s) { return held ? s_key[s] : key_at(P, it, slot_at(c, it, s)); };
+    const auto key_of = [&](int s) {
+        if (held) return s_key[s];
+        const int64_t at = slot_at(c, it, s);
+        return key_of_token(P, it, c.mass[at], c.pos[at]);
+    };
     // the keep-th largest key: `prefix` its leading bits, `need` its rank among
     // those that share them
     uint32_t prefix = 0;
@@ -174,11 +253,28 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t bins = pass == 2 ? 1024u : 2048u;
         if (pass == 0) {
-#pragma unroll 4
-            for (int s = tid; s < N; s += kSelThreads) {
-                const uint32_t k = key_at(P, it, slot_at(c, it, s));
-                if (held) s_key[s] = k;
-                atomicAdd(&s_hist[k >> shift], 1u);
+            for (int s0 = tid; s0 < N; s0 += kSelThreads * kSelBatch) {
+                float m[kSelBatch];
+                int pos[kSelBatch];
+                int64_t at[kSelBatch];
+#pragma unroll
+                for (int i = 0; i < kSelBatch; ++i) {
+                    at[i] = slot_at(c, it, min(s0 + i * kSelThreads, N - 1));
+                    m[i] = c.mass[at[i]];
+                    pos[i] = c.pos[at[i]];
+                }
+#pragma unroll
+                for (int i = 0; i < kSelBatch; ++i) {
+                    const int s = s0 + i * kSelThreads;
+                    if (s >= N) break;
+                    const uint32_t k = key_of_token(P, it, m[i], pos[i]);
+                    if (held) s_key[s] = k;
+                    atomicAdd(&s_hist[k >> shift], 1u);
+                    if (s < keep) {  // what moves into a freed slot comes after, in the other kernel
+                        if (copy) P.mass_out[at[i]] = m[i];
+                        if (copy_pos) P.pos_out[at[i]] = pos[i];
+                    }
+                }
             }
         } else {
             const int above = pass == 1 ? 21 : 10;
@@ -258,83 +354,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         const uint32_t mm = __ballot_sync(kAll, s >= keep && kept);
         if (hm >> lane & 1) P.move_dst[list + hole + __popc(hm & below)] = s;
         if (mm >> lane & 1) P.move_src[list + mover + __popc(mm & below)] = s;
-        if (kept && s < keep && (copy || copy_pos)) {
-            const int64_t at = slot_at(c, it, s);
-            if (copy) P.mass_out[at] = c.mass[at];
-            if (copy_pos) P.pos_out[at] = c.pos[at];
-        }
         hole += __popc(hm);
         mover += __popc(mm);
     }
-    if (warp == kSelWarps - 1 && lane == 0) P.move_cnt[item] = mover;
-}
-
-// Eviction, moves: a source lies at or past the budget and a destination below
-// it, so moves never meet. d / 8 threads take a group of kMoveGroup moves, all
-// of its rows in flight at once; bound by the bytes of the moved rows.
-constexpr int kMoveThreads = 256;
-constexpr int kMoveGroup = 4;
-
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const CacheParams &c = P.c;
-    const int chunks = c.d / 8, item = blockIdx.x;
-    const int head = item % c.kv_heads, b = item / c.kv_heads % P.B,
-              layer = item / c.kv_heads / P.B;
-    const int cnt = P.move_cnt[item];
-    const int part = threadIdx.x % chunks;
-    const int groups = kMoveThreads / chunks;
-    const int64_t base = layer * c.ls + head * c.hs + part * 16;
-    const int64_t mbase = layer * c.mls + head * c.mhs, list = (int64_t)item * P.moves;
-    const int32_t *table = c.table + (int64_t)b * c.table_stride;
-    const int step = gridDim.y * groups * kMoveGroup;
-    for (int r0 = (blockIdx.y * groups + threadIdx.x / chunks) * kMoveGroup; r0 < cnt; r0 += step) {
-        int s[kMoveGroup], d[kMoveGroup];
-        int64_t ps[kMoveGroup], pd[kMoveGroup];
-#pragma unroll
-        for (int i = 0; i < kMoveGroup; ++i) {
-            const int64_t at = list + min(r0 + i, cnt - 1);
-            s[i] = P.move_src[at];
-            d[i] = P.move_dst[at];
-        }
-#pragma unroll
-        for (int i = 0; i < kMoveGroup; ++i) {
-            const Place a = place_of(c, s[i]), z = place_of(c, d[i]);
-            ps[i] = __ldg(&table[a.index]);
-            pd[i] = __ldg(&table[z.index]);
-            s[i] = a.token;
-            d[i] = z.token;
-        }
-        uint4 k[kMoveGroup], v[kMoveGroup];
-#pragma unroll
-        for (int i = 0; i < kMoveGroup; ++i) {
-            const int64_t so = base + ps[i] * c.ps + s[i] * c.ts;
-            k[i] = *reinterpret_cast<const uint4 *>(c.k + so);
-            v[i] = *reinterpret_cast<const uint4 *>(c.v + so);
-        }
-        // thread `part` also takes mass or pos of one of the moves
-        const int mi = part >> 1;
-        if (mi < kMoveGroup && r0 + mi < cnt) {
-            int64_t ms = 0, md = 0;
-#pragma unroll
-            for (int i = 0; i < kMoveGroup; ++i)
-                if (i == mi) {
-                    ms = mbase + ps[i] * c.mps + s[i] * c.mts;
-                    md = mbase + pd[i] * c.mps + d[i] * c.mts;
-                }
-            if (part & 1)
-                P.pos_out[md] = c.pos[ms];
-            else
-                P.mass_out[md] = c.mass[ms];
-        }
-#pragma unroll
-        for (int i = 0; i < kMoveGroup; ++i) {
-            if (r0 + i >= cnt) break;
-            const int64_t to = base + pd[i] * c.ps + d[i] * c.ts;
-            *reinterpret_cast<uint4 *>(c.k + to) = k[i];
-            *reinterpret_cast<uint4 *>(c.v + to) = v[i];
-        }
+    if (!P.inline_moves) {
+        if (warp == kSelWarps - 1 && lane == 0) P.move_cnt[item] = mover;
+        return;
     }
+    if (warp == kSelWarps - 1 && lane == 0) s_pick[0] = mover;
+    __syncthreads();
+    const int chunks = c.d / 8;
+    move_tokens<kOwnGroup>(P, item, s_pick[0], tid / chunks, kSelThreads / chunks, tid % chunks);
 }
 
 }  // namespace
@@ -349,13 +379,17 @@ cudaError_t prepare_evict() {
                                 kKeyCap * (int)sizeof(uint32_t));
 }
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
+cudaError_t launch_evict(EvictParams p, cudaStream_t s) {
     const int items = p.c.layers * p.B * p.c.kv_heads;
     const int64_t capacity = (int64_t)p.c.max_pages * p.c.page;
     const int keys = (int)std::min<int64_t>(capacity, kKeyCap);
+    // Up to a group of moves for each team of the selecting CTA are its own (B = 4,
+    // 40 over 2048: 9.7 us against 10.8); a second kernel spreads more of them
+    // over the SMs.
+    p.inline_moves = p.moves <= kSelThreads / (p.c.d / 8) * kOwnGroup;
     evict_select_kernel<<<items, kSelThreads, keys * sizeof(uint32_t), s>>>(p);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.moves == 0) return e;
+    if (e != cudaSuccess || p.inline_moves) return e;
     // blocks of an item: enough for its longest list, up to about four waves in all
     const int per = kMoveThreads / (p.c.d / 8) * kMoveGroup;
     const int most = (p.moves + per - 1) / per;

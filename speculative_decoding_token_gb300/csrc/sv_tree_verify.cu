@@ -17,23 +17,38 @@ namespace {
 constexpr int kVtCtas = 8;
 constexpr int kVtThreads = 256;
 constexpr int kVtWarps = kVtThreads / 32;
-constexpr int kVtBatch = 5;  // 16-byte loads of a thread in flight
+constexpr int kVtBatch = 10;  // 16-byte vectors that a thread holds
 
-// a before b: the larger value, then the lower index; a NaN before all
-__device__ __forceinline__ void take_first(float &best, int32_t &idx, float ob, int32_t oi) {
-    const bool take = (ob != ob) ? true
-                      : (best != best) ? false
-                      : (oi >= 0 && (idx < 0 || ob > best || (ob == best && oi < idx)));
-    if (take) {
-        best = ob;
-        idx = oi;
-    }
+// A load that is issued where it stands, ahead of the barriers before its use.
+__device__ __forceinline__ uint4 ld_early(const void *p) {
+    uint4 x;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
+}
+
+// A candidate of the argmax: order-preserving bits of its value (-0 as +0, a NaN
+// above all), and its index. The larger value wins, then the lower index.
+__device__ __forceinline__ uint32_t value_key(float x) {
+    if (x != x) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ void warp_best(uint32_t &key, uint32_t &idx) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    idx = __reduce_min_sync(0xffffffffu, key == top ? idx : 0xffffffffu);
+    key = top;
+}
+
+__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVtThreads, 4) tree_verify_kernel(const TreeVerifyParams P) {
-    __shared__ __align__(16) float4 s_slice[2][kVtCtas];
-    __shared__ float2 s_warp[kVtWarps];
+__global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const TreeVerifyParams P) {
+    __shared__ __align__(16) uint2 s_slice[2][kVtCtas * kVtWarps];  // every warp's candidate
     __shared__ int32_t s_parent[kMaxNodes], s_token[kMaxNodes], s_path[kMaxNodes];
     constexpr int PV = DT == SV_DT_FP32 ? 4 : 8;  // logits in a 16-byte vector
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -84,85 +99,115 @@ __global__ void __launch_bounds__(kVtThreads, 4) tree_verify_kernel(const TreeVe
     int node = 0, n = 0;
     int32_t pick = -1;
     bool nan = false;
+    // Where the target agrees with a draft it is mostly the first child's, so that
+    // child's row is on its way (into registers as far as they reach, the rest
+    // to L2) while the cluster decides the step.
+    uint4 v[kVtBatch];
+    const auto fetch = [&](int to) {
+        const char *row = P.target + (row0 + to) * P.stride_bytes;
+#pragma unroll
+        for (int i = 0; i < kVtBatch; ++i) {
+            const int64_t vi = v0 + threadIdx.x + i * kVtThreads;
+            if (vi < v1) v[i] = ld_early(row + vi * 16);
+        }
+    };
+    const int64_t beyond = v0 + kVtBatch * kVtThreads;  // vectors that registers do not hold
+    fetch(0);
     for (;;) {  // at most `nodes` steps: each goes to a later node
         const char *row = P.target + (row0 + node) * P.stride_bytes;
-        // the first child's slice on its way to L2: where the walk goes on, it is
-        // usually there
-        if (warp == kVtWarps - 1) {
-            int child = -1;
-            for (int j0 = (node + 1) & ~31; j0 < nodes && child < 0; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t hit =
-                    __ballot_sync(0xffffffffu, j > node && j < nodes && s_parent[j] == node);
-                if (hit) child = j0 + __ffs(hit) - 1;
-            }
-            if (child >= 0 && v1 > v0 && lane == 0)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                 P.target + (row0 + child) * P.stride_bytes + v0 * 16),
-                             "r"((uint32_t)min((v1 - v0) * 16, (int64_t)1 << 18))
-                             : "memory");
-        }
         const uint4 *rv = reinterpret_cast<const uint4 *>(row);
-        float best = -INFINITY;
-        int32_t idx = -1;
-        for (int64_t vi0 = v0 + threadIdx.x; vi0 < v1; vi0 += kVtBatch * kVtThreads) {
-            uint4 v[kVtBatch];
-#pragma unroll
-            for (int i = 0; i < kVtBatch; ++i)
-                if (vi0 + i * kVtThreads < v1) v[i] = __ldg(rv + vi0 + i * kVtThreads);
+        uint32_t key = 0, idx = 0xffffffffu;
+        {
+            // the maximum of the held vectors, then the first vector and element of it
+            float m[kVtBatch], best = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kVtBatch; ++i) {
-                const int64_t vi = vi0 + i * kVtThreads;
-                if (vi >= v1) break;
-                const float m = vec_max<DT>(v[i]);
-                if (m != m || m > best || idx < 0) {  // later indexes: a tie keeps the first
-                    if (best == best) {
-                        float f[PV];
-                        vec_floats<DT>(v[i], f);
-                        int e = 0;
+                const int64_t vi = v0 + threadIdx.x + i * kVtThreads;
+                m[i] = vi < v1 ? vec_max<DT>(v[i]) : -INFINITY;
+                best = max_nan(best, m[i]);
+            }
+            uint4 x = v[0];
+            int at = 0;
 #pragma unroll
-                        for (int j = PV - 1; j >= 0; --j)
-                            if (f[j] == m) e = j;
-                        best = m;
-                        idx = (int32_t)(vi * PV + e);
-                    }
+            for (int i = kVtBatch - 1; i >= 0; --i)
+                if (m[i] == best && v0 + threadIdx.x + i * kVtThreads < v1) {
+                    at = i;
+                    x = v[i];
                 }
+            if (v0 + threadIdx.x < v1) {
+                float f[PV];
+                vec_floats<DT>(x, f);
+                int e = 0;
+#pragma unroll
+                for (int j = PV - 1; j >= 0; --j)
+                    if (f[j] == best) e = j;
+                key = value_key(best);
+                idx = (uint32_t)((v0 + threadIdx.x + at * kVtThreads) * PV + e);
             }
         }
-        for (int64_t e = v1 * PV + threadIdx.x; e < c1; e += kVtThreads)  // the ragged end at V
-            take_first(best, idx, load_logit<DT>(row, e), (int32_t)e);
-        const float2 r = warp_combine_greedy(best, idx);
-        if (lane == 0) s_warp[warp] = r;
-        if (n == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-        __syncthreads();
-        if (warp == 0) {
-            best = lane < kVtWarps ? s_warp[lane].x : -INFINITY;
-            idx = lane < kVtWarps ? __float_as_int(s_warp[lane].y) : -1;
-            const float2 c = warp_combine_greedy(best, idx);
-            if (lane < kVtCtas)
-                st_cluster_f4(cluster_addr(&s_slice[n & 1][rank], (uint32_t)lane),
-                              make_float4(c.x, c.y, 0.0f, 0.0f));
+#pragma unroll 4
+        for (int64_t vi = beyond + threadIdx.x; vi < v1; vi += kVtThreads) {
+            const uint4 x = __ldg(rv + vi);
+            const float m = vec_max<DT>(x);
+            if (value_key(m) > key) {  // later indexes: a tie keeps the first
+                float f[PV];
+                vec_floats<DT>(x, f);
+                int e = 0;
+#pragma unroll
+                for (int j = PV - 1; j >= 0; --j)
+                    if (f[j] == m) e = j;
+                key = value_key(m);
+                idx = (uint32_t)(vi * PV + e);
+            }
         }
-        // The barrier orders the slices, and step n + 2 reuses this step's only
+        for (int64_t e = v1 * PV + threadIdx.x; e < c1; e += kVtThreads) {  // the ragged end at V
+            const uint32_t k = value_key(load_logit<DT>(row, e));
+            if (k > key || idx == 0xffffffffu) {
+                key = k;
+                idx = (uint32_t)e;
+            }
+        }
+        // the lowest child (of the token `want`, if that is not -1), every warp for itself
+        const auto child_of = [&](int32_t want) {
+            int found = -1;
+            for (int j0 = (node + 1) & ~31; j0 < nodes && found < 0; j0 += 32) {
+                const int j = j0 + lane;
+                const uint32_t hit =
+                    __ballot_sync(0xffffffffu, j > node && j < nodes && s_parent[j] == node &&
+                                                   (want < 0 || s_token[j] == want));
+                if (hit) found = j0 + __ffs(hit) - 1;
+            }
+            return found;
+        };
+        const int guess = child_of(-1);
+        if (guess >= 0) {
+            fetch(guess);
+            if (beyond < v1 && threadIdx.x == 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 P.target + (row0 + guess) * P.stride_bytes + beyond * 16),
+                             "r"((uint32_t)min((v1 - beyond) * 16, (int64_t)1 << 18))
+                             : "memory");
+        }
+        warp_best(key, idx);
+        if (n == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (lane < kVtCtas)
+            st_cluster_u2(cluster_addr(&s_slice[n & 1][rank * kVtWarps + warp], (uint32_t)lane), key,
+                          idx);
+        // The barrier orders the candidates, and step n + 2 reuses this step's only
         // after every CTA has passed the barrier of step n + 1.
         cluster_sync();
-        best = -INFINITY;
-        idx = -1;
-#pragma unroll
-        for (int c = 0; c < kVtCtas; ++c)
-            take_first(best, idx, s_slice[n & 1][c].x, __float_as_int(s_slice[n & 1][c].y));
-        pick = idx;
-        nan = best != best;
+        static_assert(kVtCtas * kVtWarps == 64, "two candidates a lane");
+        const uint2 a = s_slice[n & 1][lane], z = s_slice[n & 1][lane + 32];
+        const bool second = z.x > a.x || (z.x == a.x && z.y < a.y);
+        key = second ? z.x : a.x;
+        idx = second ? z.y : a.y;
+        warp_best(key, idx);
+        pick = (int32_t)idx;
+        nan = key == 0xffffffffu;
         if (nan) break;
         if (threadIdx.x == 0) s_path[n] = node;
-        // the lowest child with that token (every warp for itself)
-        int next = -1;
-        for (int j0 = (node + 1) & ~31; j0 < nodes && next < 0; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t hit = __ballot_sync(
-                0xffffffffu, j > node && j < nodes && s_parent[j] == node && s_token[j] == pick);
-            if (hit) next = j0 + __ffs(hit) - 1;
-        }
+        const int next = child_of(pick);
+        if (next >= 0 && next != guess) fetch(next);
         if (next < 0) break;
         node = next;
         ++n;
