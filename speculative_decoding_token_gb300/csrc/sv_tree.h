@@ -58,6 +58,7 @@ struct TreeAttnParams {
     int32_t heads, G;
     float scale_log2;         // scale * log2(e)
     int32_t box;              // tokens of one tiled copy: divides the page size and a tile
+    int32_t blocks;           // blocks of 256 rows that a tree can have
     int32_t *status;
     // workspace: the pieces of rows whose slots were split over CTAs
     float *piece_o;           // [CTAs, 2, 256, d]

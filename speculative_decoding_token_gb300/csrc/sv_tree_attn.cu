@@ -19,7 +19,10 @@
 // end); more rows make two Q tiles, a group each, over the same slots.
 //
 // All (sequence, key head, block of rows) items' tiles of 128 slots, with a
-// constant for each item's start, form one line that is cut evenly over the CTAs. An item cut in pieces leaves each
+// constant for each item's start, form one line that is cut evenly over the CTAs,
+// first every sequence's first block of rows, then the second ones: where trees
+// have two blocks, CTAs half the grid apart read the same keys at about the same
+// time, and L2 serves one of them. An item cut in pieces leaves each
 // piece's O (not yet divided), maximum and sum in the workspace, and a second
 // kernel joins the pieces; whole items are written directly.
 #include <algorithm>
@@ -67,9 +70,9 @@ struct Seq {
     int L, T, tiles, blocks;
     int64_t row0;
 
-    // (the host has checked that a sequence's fit 31 bits)
-    __device__ int units(const TreeAttnParams &P) const {
-        return tiles ? (tiles + kHead) * blocks * P.c.kv_heads : 0;
+    // Units of the items of one block of rows (the host has checked that they fit 31 bits).
+    __device__ int units(const TreeAttnParams &P, int block) const {
+        return block < blocks ? (tiles + kHead) * P.c.kv_heads : 0;
     }
 };
 
@@ -105,20 +108,24 @@ struct Segment {
 };
 
 struct Walk {
-    int b;
-    int rest;         // next unit within sequence b
+    int b, block;
+    int rest;         // next unit within sequence b's of that block
     long long left;   // units of this CTA still to do
 
     __device__ bool next(const TreeAttnParams &P, Segment &g) {
         while (left > 0) {
             g.s = seq_of(P, b);
-            if (rest >= g.s.units(P)) {
+            if (rest >= g.s.units(P, block)) {
                 rest = 0;
-                ++b;
+                if (++b == P.t.B) {
+                    b = 0;
+                    ++block;
+                }
                 continue;
             }
             const int len = g.s.tiles + kHead;
-            const int item = rest / len, u = rest - item * len;
+            g.head = rest / len;
+            const int u = rest - g.head * len;
             const int end = (int)min((long long)len, u + left);
             rest += end - u;
             left -= end - u;
@@ -126,8 +133,7 @@ struct Walk {
             g.tile0 = max(u - kHead, 0);
             g.n = end - kHead - g.tile0;
             if (g.n <= 0) continue;
-            g.head = item / g.s.blocks;
-            g.block = item - g.head * g.s.blocks;
+            g.block = block;
             g.rows = min(g.s.T * P.G - g.block * 2 * kTile, 2 * kTile);
             g.pair = g.rows > kTile;
             g.first = g.tile0 == 0;
@@ -152,7 +158,7 @@ struct Misc {
     uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
     uint64_t seg_full[2], seg_empty[2], drain;
     int32_t rest0;                         // the CTA's first unit in its first sequence,
-    int32_t b0;                            // and that sequence
+    int32_t b0, block0;                    // that sequence, and the block of rows
     uint32_t tmem;
     long long scan[kAttnThreads / 32];
     int32_t abort;                         // a wait gave up
@@ -783,13 +789,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (warp == kMmaWarp) tmem_alloc(smem_u32(&M.tmem), kTmemCols);
 
-    // the line of tiles: each thread a run of sequences, a scan over the threads
+    // the line: each thread a run of sequences, a scan over the threads
     const int per = (P.t.B + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min(P.t.B, tid * per), b1 = min(P.t.B, b0 + per);
-    long long mine = 0;
+    long long first = 0, all = 0;  // units of the run: the first block of rows, every block
     for (int b = b0; b < b1; ++b) {
         const Seq s = seq_of(P, b);
-        mine += s.units(P);
+        first += s.units(P, 0);
+        all += (long long)s.units(P, 0) * s.blocks;
         if (s.tiles == 0 && s.T != 0 && b % (int)gridDim.x == (int)blockIdx.x) {
             // a bad sequence: NaN in the rows that it names, if it names rows
             const int bad = seq_error(P, s.T, s.row0, s.L);
@@ -803,38 +810,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
         }
     }
-    long long incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) M.scan[warp] = incl;
+    // units before this thread's, and everybody's
+    const auto scan = [&](long long mine, long long &sum) {
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) M.scan[warp] = incl;
+        __syncthreads();
+        long long before = incl - mine;
+        sum = 0;
+        for (int i = 0; i < kAttnThreads / 32; ++i) {
+            if (i < warp) before += M.scan[i];
+            sum += M.scan[i];
+        }
+        return before;
+    };
     tc_fence_before();
-    __syncthreads();
+    long long total, in_block = 0;
+    long long before = scan(all, total);
     tc_fence_after();
-    long long before = incl - mine, total = 0;
-    for (int i = 0; i < kAttnThreads / 32; ++i) {
-        if (i < warp) before += M.scan[i];
-        total += M.scan[i];
-    }
     const Cut cut(total, gridDim.x);
     const int cta = min((int)blockIdx.x, cut.ctas);
     const long long lo = cut.at(cta), hi = cut.at(min(cta + 1, cut.ctas));
-    if (lo < hi && before <= lo && lo < before + mine) {
-        long long at = before;
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(P, b);
-            const long long n = s.units(P);
-            if (lo < at + n) {
-                M.b0 = b;
-                M.rest0 = (int)(lo - at);
-                break;
-            }
-            at += n;
+    long long start = 0;  // of the block on the line
+    for (int block = 0; block < P.blocks; ++block) {
+        long long mine = first;
+        if (P.blocks > 1) {
+            __syncthreads();
+            mine = 0;
+            for (int b = b0; b < b1; ++b) mine += seq_of(P, b).units(P, block);
+            before = scan(mine, in_block);
         }
+        if (lo < hi && start + before <= lo && lo < start + before + mine) {
+            long long at = start + before;
+            for (int b = b0; b < b1; ++b) {
+                const int n = seq_of(P, b).units(P, block);
+                if (lo < at + n) {
+                    M.b0 = b;
+                    M.block0 = block;
+                    M.rest0 = (int)(lo - at);
+                    break;
+                }
+                at += n;
+            }
+        }
+        start += in_block;
+        if (lo < start) break;
     }
     __syncthreads();
-    Walk walk{M.b0, M.rest0, hi - lo};
+    Walk walk{M.b0, M.block0, M.rest0, hi - lo};
     const uint32_t tmem = M.tmem;
     if (warp < kSoftThreads / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -1037,6 +1063,7 @@ cudaError_t prepare_tree() {
 cudaError_t launch_tree_attention(TreeAttnParams p, int num_sms, cudaStream_t s) {
     CUtensorMap mk, mv;
     p.box = cache_box(p.c.page);
+    p.blocks = (int32_t)(((int64_t)p.t.max_nodes * p.G + 2 * kTile - 1) / (2 * kTile));
     if (!cache_map(p.c, p.c.k, p.box, &mk) || !cache_map(p.c, p.c.v, p.box, &mv))
         return cudaErrorInvalidValue;
     if (p.c.fp16)
