@@ -129,9 +129,39 @@ cudaError_t launch_accumulate(AccumParams p, int num_sms, cudaStream_t s);
 cudaError_t prepare_evict();
 cudaError_t launch_evict(EvictParams p, cudaStream_t s);
 
+#ifdef __CUDACC__
+// A launch that may begin while the stream's kernel before it ends (programmatic
+// dependent launch): the kernel sets itself up and then waits for what came
+// before with after_previous(), ahead of its first access to global memory, in
+// every CTA. A step is a row of short kernels, and this hides their starts.
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         int cluster, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------------------
 // device helpers
-#ifdef __CUDACC__
+
+// Waits until the kernels before this one are done and their writes are seen,
+// then lets the next one set itself up.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Whether tokens [0, count) of sequence b fit its pages.
 __device__ __forceinline__ bool cache_holds(const CacheParams &c, int64_t count) {
@@ -140,7 +170,7 @@ __device__ __forceinline__ bool cache_holds(const CacheParams &c, int64_t count)
 
 // Page i of sequence b, -1 for an id outside the pool.
 __device__ __forceinline__ int64_t page_at(const CacheParams &c, int b, int i) {
-    const int32_t id = __ldg(&c.table[(int64_t)b * c.table_stride + i]);
+    const int32_t id = c.table[(int64_t)b * c.table_stride + i];
     return id >= 0 && (int64_t)id < c.num_pages ? (int64_t)id : -1;
 }
 

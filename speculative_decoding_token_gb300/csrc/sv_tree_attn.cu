@@ -767,7 +767,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     extern __shared__ __align__(1024) char smem[];
     Misc &M = *reinterpret_cast<Misc *>(smem + Sh::kMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(smem_u32(&M.full[i]), 1);
@@ -788,6 +787,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(smem_u32(&M.tmem), kTmemCols);
+    after_previous();
 
     // the line: each thread a run of sequences, a scan over the threads
     const int per = (P.t.B + kAttnThreads - 1) / kAttnThreads;
@@ -904,7 +904,7 @@ constexpr int kJoinWarps = 4, kJoinRows = 2, kAhead = 8;
 
 template <bool FP16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     constexpr int W = D / 32;
     using Vec = typename std::conditional<W == 4, float4, float2>::type;
     const AttnOwner o = P.owner[blockIdx.x];
@@ -986,20 +986,12 @@ EncodeFn g_encode = nullptr;
 template <bool FP16, int D>
 cudaError_t launch(const TreeAttnParams &p, const CUtensorMap &mk, const CUtensorMap &mv, int ctas,
                    cudaStream_t s) {
-    tree_attn_kernel<FP16, D><<<ctas, kAttnThreads, Shape<D>::kSmem, s>>>(p, mk, mv);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(tree_attn_kernel<FP16, D>, dim3((unsigned)ctas), kAttnThreads,
+                                       Shape<D>::kSmem, s, 1, p, mk, mv);
     if (e != cudaSuccess) return e;
-    const int most = std::min((int64_t)2 * kTile, (int64_t)p.t.max_nodes * p.G);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((most + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows)));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<FP16, D>, p);
+    const int64_t most = std::min((int64_t)2 * kTile, (int64_t)p.t.max_nodes * p.G);
+    const unsigned y = (unsigned)((most + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows));
+    return launch_after(tree_join_kernel<FP16, D>, dim3((unsigned)ctas, y), kJoinWarps * 32, 0, s, 1, p);
 }
 
 template <bool FP16, int D>

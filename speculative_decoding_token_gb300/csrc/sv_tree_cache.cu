@@ -18,9 +18,10 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kCommitThreads = 256;
 constexpr int kCommitGroup = 4;
 
-__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams P) {
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_constant__ CommitParams P) {
     __shared__ int64_t s_src[kMaxNodes], s_dst[kMaxNodes];   // byte offset of the slot, head 0
     __shared__ int64_t s_mass[kMaxNodes];                    // element offset of L + i
+    after_previous();
     const int b = blockIdx.x, layer = blockIdx.y;
     const int L = P.lens[b], n = P.n[b];
     const CacheParams &c = P.c;
@@ -116,7 +117,7 @@ struct Item {
 
 __device__ __forceinline__ int64_t slot_at(const CacheParams &c, const Item &it, int s) {
     const Place p = place_of(c, s);
-    const int64_t pg = __ldg(&c.table[(int64_t)it.b * c.table_stride + p.index]);
+    const int64_t pg = c.table[(int64_t)it.b * c.table_stride + p.index];
     return it.base + pg * c.mps + (int64_t)p.token * c.mts;
 }
 
@@ -156,8 +157,8 @@ __device__ __forceinline__ void move_tokens(const EvictParams &P, int item, int 
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             const Place a = place_of(c, s[i]), z = place_of(c, d[i]);
-            ps[i] = __ldg(&table[a.index]);
-            pd[i] = __ldg(&table[z.index]);
+            ps[i] = table[a.index];
+            pd[i] = table[z.index];
             s[i] = a.token;
             d[i] = z.token;
         }
@@ -193,19 +194,19 @@ __device__ __forceinline__ void move_tokens(const EvictParams &P, int item, int 
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams P) {
+    after_previous();
     const int chunks = P.c.d / 8, groups = kMoveThreads / chunks, item = blockIdx.x;
     move_tokens<kMoveGroup>(P, item, P.move_cnt[item], blockIdx.y * groups + threadIdx.x / chunks,
                 gridDim.y * groups, threadIdx.x % chunks);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams P) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams P) {
     extern __shared__ uint32_t s_key[];
     __shared__ uint32_t s_hist[kSelBins];
     __shared__ int s_pick[2];
     __shared__ int s_cnt[3][kSelWarps];
-    asm volatile("griddepcontrol.launch_dependents;");
+    after_previous();
     const CacheParams &c = P.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int item = blockIdx.x;
@@ -370,8 +371,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 }  // namespace
 
 cudaError_t launch_tree_commit(const CommitParams &p, cudaStream_t s) {
-    commit_kernel<<<dim3(p.B, p.c.layers), kCommitThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(commit_kernel, dim3(p.B, p.c.layers), kCommitThreads, 0, s, 1, p);
 }
 
 cudaError_t prepare_evict() {
@@ -387,22 +387,15 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t s) {
     // 40 over 2048: 9.7 us against 10.8); a second kernel spreads more of them
     // over the SMs.
     p.inline_moves = p.moves <= kSelThreads / (p.c.d / 8) * kOwnGroup;
-    evict_select_kernel<<<items, kSelThreads, keys * sizeof(uint32_t), s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(evict_select_kernel, dim3((unsigned)items), kSelThreads,
+                                       keys * sizeof(uint32_t), s, 1, p);
     if (e != cudaSuccess || p.inline_moves) return e;
     // blocks of an item: enough for its longest list, up to about four waves in all
     const int per = kMoveThreads / (p.c.d / 8) * kMoveGroup;
     const int most = (p.moves + per - 1) / per;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)items, (unsigned)std::min(most, std::max(1, 8192 / items)));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    return launch_after(evict_move_kernel,
+                        dim3((unsigned)items, (unsigned)std::min(most, std::max(1, 8192 / items))),
+                        kMoveThreads, 0, s, 1, p);
 }
 
 }  // namespace sv

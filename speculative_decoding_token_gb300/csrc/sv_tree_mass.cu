@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(smem_u32(&M.tmem), kCols);
+    after_previous();
 
     // the line: each thread a run of sequences, a scan over the threads
     const int per = (P.t.B + kMassThreads - 1) / kMassThreads;
@@ -406,8 +407,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 
 template <bool FP16, int D>
 cudaError_t launch(const AccumParams &p, const CUtensorMap &mk, int ctas, cudaStream_t s) {
-    accumulate_kernel<FP16, D><<<ctas, kMassThreads, Shape<D>::kSmem, s>>>(p, mk);
-    return cudaGetLastError();
+    return launch_after(accumulate_kernel<FP16, D>, dim3((unsigned)ctas), kMassThreads,
+                        Shape<D>::kSmem, s, 1, p, mk);
 }
 
 template <bool FP16, int D>

@@ -22,7 +22,7 @@ constexpr int kVtBatch = 10;  // 16-byte vectors that a thread holds
 // A load that is issued where it stands, ahead of the barriers before its use.
 __device__ __forceinline__ uint4 ld_early(const void *p) {
     uint4 x;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                  : "l"(p));
     return x;
@@ -47,10 +47,17 @@ __device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t x, uint32_
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const TreeVerifyParams P) {
+__device__ __forceinline__ float logit_at(const char *row, int64_t v) {
+    if (DT == SV_DT_FP32) return reinterpret_cast<const float *>(row)[v];
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[v] << 16);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid_constant__ TreeVerifyParams P) {
     __shared__ __align__(16) uint2 s_slice[2][kVtCtas * kVtWarps];  // every warp's candidate
     __shared__ int32_t s_parent[kMaxNodes], s_token[kMaxNodes], s_path[kMaxNodes];
     constexpr int PV = DT == SV_DT_FP32 ? 4 : 8;  // logits in a 16-byte vector
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const int b = blockIdx.x / kVtCtas;
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const TreeVe
         }
 #pragma unroll 4
         for (int64_t vi = beyond + threadIdx.x; vi < v1; vi += kVtThreads) {
-            const uint4 x = __ldg(rv + vi);
+            const uint4 x = rv[vi];
             const float m = vec_max<DT>(x);
             if (value_key(m) > key) {  // later indexes: a tie keeps the first
                 float f[PV];
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const TreeVe
             }
         }
         for (int64_t e = v1 * PV + threadIdx.x; e < c1; e += kVtThreads) {  // the ragged end at V
-            const uint32_t k = value_key(load_logit<DT>(row, e));
+            const uint32_t k = value_key(logit_at<DT>(row, e));
             if (k > key || idx == 0xffffffffu) {
                 key = k;
                 idx = (uint32_t)e;
@@ -228,20 +235,10 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const TreeVe
 }  // namespace
 
 cudaError_t launch_tree_verify(const TreeVerifyParams &p, int dtype, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.t.B * kVtCtas));
-    cfg.blockDim = dim3(kVtThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kVtCtas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const dim3 grid((unsigned)(p.t.B * kVtCtas));
     if (dtype == SPECVERIFY_FP32)
-        return cudaLaunchKernelEx(&cfg, tree_verify_kernel<SV_DT_FP32>, p);
-    return cudaLaunchKernelEx(&cfg, tree_verify_kernel<SV_DT_BF16>, p);
+        return launch_after(tree_verify_kernel<SV_DT_FP32>, grid, kVtThreads, 0, s, kVtCtas, p);
+    return launch_after(tree_verify_kernel<SV_DT_BF16>, grid, kVtThreads, 0, s, kVtCtas, p);
 }
 
 }  // namespace sv
