@@ -157,6 +157,27 @@ cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cud
 // ---------------------------------------------------------------------------
 // device helpers
 
+// A line of work units cut over CTAs: CTA i has units [cut.at(i), cut.at(i + 1)), the first `more` one
+// more than the others.
+struct Cut {
+    int ctas, more;
+    long long each;
+
+    __device__ __forceinline__ Cut(long long total, int grid) {
+        ctas = (int)min((long long)grid, total);
+        each = ctas == 0 ? 0 : (total >> 31 ? total / ctas : (long long)((int)total / ctas));
+        more = (int)(total - each * ctas);
+    }
+    __device__ __forceinline__ long long at(int i) const { return i * each + min(i, more); }
+    // The CTA of a unit.
+    __device__ __forceinline__ int of(long long unit) const {
+        int i = 0;  // at(i) <= unit < at(i + 1), by halves
+        for (int step = 1 << (31 - __clz(ctas)); step > 0; step >>= 1)
+            if (i + step < ctas && at(i + step) <= unit) i += step;
+        return i;
+    }
+};
+
 // Waits until the kernels before this one are done and their writes are seen,
 // then lets the next one set itself up.
 __device__ __forceinline__ void after_previous() {

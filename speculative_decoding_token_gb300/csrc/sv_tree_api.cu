@@ -319,6 +319,8 @@ int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cac
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
     if (!lens || !n_accepted || !path || !lse || !cache->mass) return SPECVERIFY_ERR_INVALID_ARG;
+    if (((int64_t)cache->max_pages * cache->page_size / 128 + 4) * cache->kv_heads > INT32_MAX)
+        return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
     sv::AccumParams p{};

@@ -165,27 +165,6 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 2944, "Misc");
 
-// The line's cut: CTA i has units [cut.at(i), cut.at(i + 1)), the first `more` one
-// more than the others.
-struct Cut {
-    int ctas, more;
-    long long each;
-
-    __device__ Cut(long long total, int grid) {
-        ctas = (int)min((long long)grid, total);
-        each = ctas == 0 ? 0 : (total >> 31 ? total / ctas : (long long)((int)total / ctas));
-        more = (int)(total - each * ctas);
-    }
-    __device__ long long at(int i) const { return i * each + min(i, more); }
-    // The CTA of a unit.
-    __device__ int of(long long unit) const {
-        int i = 0;  // at(i) <= unit < at(i + 1), by halves
-        for (int step = 1 << (31 - __clz(ctas)); step > 0; step >>= 1)
-            if (i + step < ctas && at(i + step) <= unit) i += step;
-        return i;
-    }
-};
-
 // Place of a segment's K and V tile j in the order of the ring's uses. Group w
 // needs K of its next tile before V of its current one.
 __device__ __forceinline__ uint32_t k_at(const Segment &g, int j) {

@@ -42,8 +42,7 @@ struct Shape {
 struct Misc {
     float lse[2][kRows];                   // of a chunk's rows, times log2(e)
     uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], s_empty[2], drain;
-    long long rest0;
-    int32_t b0;
+    int32_t b0, rest0;                     // the CTA's first sequence and unit in it
     uint32_t tmem;
     long long scan[kMassThreads / 32];
     int32_t abort;
@@ -55,8 +54,9 @@ struct Seq {
     int L, n, tiles;                       // tiles 0: idle or bad
     int64_t row0;
 
-    __device__ long long units(const AccumParams &P) const {
-        return tiles ? (long long)(tiles + kHead) * P.c.kv_heads : 0;
+    // (the host has checked that they fit 31 bits)
+    __device__ int units(const AccumParams &P) const {
+        return tiles ? (tiles + kHead) * P.c.kv_heads : 0;
     }
 };
 
@@ -88,7 +88,8 @@ struct Segment {
 
 struct Walk {
     int b;
-    long long rest, left;
+    int rest;        // next unit within sequence b
+    long long left;  // units of this CTA still to do
 
     __device__ bool next(const AccumParams &P, Segment &g) {
         while (left > 0) {
@@ -99,8 +100,8 @@ struct Walk {
                 continue;
             }
             const int len = g.s.tiles + kHead;
-            g.head = (int)(rest / len);
-            const int u = (int)(rest - (long long)g.head * len);
+            g.head = rest / len;
+            const int u = rest - g.head * len;
             const int end = (int)min((long long)len, u + left);
             rest += end - u;
             left -= end - u;
@@ -373,16 +374,16 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (i < warp) before += M.scan[i];
         total += M.scan[i];
     }
-    const long long ctas = min((long long)gridDim.x, total);
-    const long long lo = (int)blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-    const long long hi = (int)blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
+    const Cut cut(total, gridDim.x);
+    const int cta = min((int)blockIdx.x, cut.ctas);
+    const long long lo = cut.at(cta), hi = cut.at(min(cta + 1, cut.ctas));
     if (lo < hi && before <= lo && lo < before + mine) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             const long long n = seq_of(P, b).units(P);
             if (lo < at + n) {
                 M.b0 = b;
-                M.rest0 = lo - at;
+                M.rest0 = (int)(lo - at);
                 break;
             }
             at += n;

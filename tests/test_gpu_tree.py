@@ -65,6 +65,9 @@ ATTENTION = {
     "flat": ([900, 400], [6, 20], 4, 2, 64, 16, FP16, {"sharp": 0.0}),
     "many short": ([i * 7 % 90 for i in range(60)], [1 + i % 5 for i in range(60)], 4, 2, 64, 16, BF16, {}),
     "page above tile": ([500, 1030], [3, 9], 4, 4, 64, 1040, BF16, {}),
+    "one head for all": ([260, 9], [5, 3], 64, 1, 128, 16, BF16, {}),
+    "more heads than a tile's rows": ([150], [2], 300, 1, 64, 16, BF16, {}),
+    "blocks of rows": ([400, 20, 300, 0, 700], [64, 3, 33, 0, 128], 16, 2, 64, 16, FP16, {}),
 }
 
 
@@ -91,6 +94,43 @@ def test_attention_long_context_split(st):
         ordered[0, pg] = ramp[0, i]
     bt.k = (bt.k.float() * ordered).to(BF16)
     check_attention(st, bt)
+
+
+def test_attention_of_many_sequences():
+    """More sequences than threads of a CTA."""
+    import speculative_decoding_token_gb300 as sv
+    h = sv.SpecTree(700)
+    check_attention(h, tu.Batch([i % 23 for i in range(700)], [i % 3 for i in range(700)], 2, 1, 64, 8, BF16, seed=4))
+    assert h.device_status() == 0
+    h.close()
+
+
+def test_attention_shared_pages_and_layer_views(st):
+    """Two sequences whose tables share a prefix's pages, one layer of a pool that holds k and v of several layers side by
+    side, and a page table with columns to spare."""
+    import speculative_decoding_token_gb300 as sv
+    bt = tu.Batch([100, 90], [3, 6], 4, 2, 64, 16, BF16, seed=21, poison=False)
+    bt.table[1, :4] = bt.table[0, :4]
+    bt.upload()
+    pool = torch.full((3, 2, *bt.dk.shape), float("nan"), dtype=BF16, device="cuda")  # layers, k and v
+    pool[1, 0], pool[1, 1] = bt.dk, bt.dv
+    wide = torch.full((2, 40), -9, dtype=torch.int32, device="cuda")
+    wide[:, : bt.table.shape[1]] = bt.dev(bt.table)
+    cache = sv.KVCache(pool[1, 0], pool[1, 1], wide)
+    out, lse = st.attention(bt.dq, cache, bt.tree, bt.dlens)
+    want = tu.attention(bt, 0.125)
+    real = ~torch.isnan(want[1][:, 0])
+    near(out[real.cuda()], want[0][real], want[2][real])
+    near(lse[real.cuda()], want[1][real], want[3][real])
+
+
+def test_attention_repeats_bit_for_bit(st):
+    bt = tu.Batch([5000, 700, 3], [30, 2, 9], 8, 2, 128, 16, BF16, seed=13)
+    first = run_attention(st, bt)
+    for _ in range(5):
+        again = run_attention(st, bt)
+        assert torch.equal(first[0].nan_to_num(9.0), again[0].nan_to_num(9.0))
+        assert torch.equal(first[1].nan_to_num(9.0), again[1].nan_to_num(9.0))
 
 
 def test_attention_scale(st):
@@ -485,6 +525,25 @@ def test_evict(st, layers, d, page, dtype, lens, budget, sink, recent, kind, in_
     assert torch.equal(dm.cpu().nan_to_num(77.0), bt.one(m).nan_to_num(77.0))
 
 
+def test_evict_more_slots_than_shared_memory_holds():
+    import speculative_decoding_token_gb300 as sv
+    rng = np.random.default_rng(2)
+    lens, budget = [50011, 49153, 7], 30000
+    bt = tu.Batch(lens, [0, 0, 0], 1, 1, 64, 256, BF16, seed=2, poison=False)
+    shape = bt.k.shape[:-1]
+    mass = torch.randint(0, 4000, shape, generator=bt.gen).float()  # many ties
+    pos, seen = make_positions(rng, bt, shape)
+    bt.upload(mass=mass, pos=pos)
+    h = sv.SpecTree(3, max_moves=3 * 30000)
+    out = torch.zeros_like(bt.dmass)
+    _, p, new_lens = h.evict(bt.cache, bt.dlens, bt.dev(seen, torch.int32), budget, sink=4, recent=100, mass_out=out)
+    want = expected_evict(bt, mass, pos, seen, budget, 4, 100, torch.zeros(shape), pos)
+    assert new_lens.tolist() == [30000, 30000, 7] and h.device_status() == 0
+    for got, w in ((bt.dk, want[0]), (bt.dv, want[1]), (out, want[2]), (p, want[3])):
+        assert torch.equal(got.cpu(), w[0])
+    h.close()
+
+
 def test_evict_bad_input(st):
     import speculative_decoding_token_gb300 as sv
     for change in (lambda t: t.lens.__setitem__(0, -4), lambda t: t.lens.__setitem__(0, 10 ** 8),
@@ -610,6 +669,56 @@ def test_attention_on_another_stream_and_in_graphs(st):
     for h in handles:
         assert h.device_status() == 0
         h.close()
+
+
+def test_cache_calls_in_a_graph_and_on_a_stream():
+    """Commit, accumulation and eviction captured together and replayed on a side stream give what eager calls give."""
+    import speculative_decoding_token_gb300 as sv
+    rng = np.random.default_rng(31)
+    lens, nodes, budget = [200, 90, 64], [12, 9, 1], 60
+    base = tu.Batch(lens, nodes, 4, 2, 64, 16, BF16, seed=31, poison=False)
+    n, path = make_paths(rng, nodes, base.T)
+    shape = base.k.shape[:-1]
+    mass0 = torch.rand(shape, generator=base.gen)
+    pos0, seen0 = make_positions(rng, base, shape)
+    lse = torch.rand(base.rows, 4, generator=base.gen) + 4
+
+    def state():
+        bt = tu.Batch(lens, nodes, 4, 2, 64, 16, BF16, seed=31, poison=False).upload(mass=mass0, pos=pos0)
+        bufs = [torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(3)]
+        moves = 3 * 2 * budget
+        return bt, sv.SpecTree(3, max_moves=moves), bufs, [x.cuda() for x in (
+            torch.tensor(n, dtype=torch.int32), torch.tensor(path, dtype=torch.int32), torch.tensor(seen0, dtype=torch.int32),
+            lse)]
+
+    def step(bt, h, bufs, args):
+        dn, dpath, dseen, dlse = args
+        h.commit(bt.cache, bt.dlens, dn, dpath, seen=dseen, new_lens=bufs[0], new_seen=bufs[1])
+        h.accumulate(bt.dq, dlse, bt.cache, bt.tree, bt.dlens, dn, dpath)
+        h.evict(bt.cache, bufs[0], bufs[1], budget, sink=2, recent=10, new_lens=bufs[2])
+
+    eager, graphed = state(), state()
+    step(*eager)
+    keep = [t.clone() for t in (graphed[0].dk, graphed[0].dv, graphed[0].dmass, graphed[0].dpos)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*graphed)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            for t, k in zip((graphed[0].dk, graphed[0].dv, graphed[0].dmass, graphed[0].dpos), keep):
+                t.copy_(k)
+            g.replay()
+    side.synchronize()
+    torch.cuda.synchronize()
+    a, b = eager[0], graphed[0]
+    for x, y in ((a.dk, b.dk), (a.dv, b.dv), (a.dmass, b.dmass), (a.dpos, b.dpos), *zip(eager[2], graphed[2])):
+        assert torch.equal(x, y)
+    assert eager[2][2].tolist() == [min(x + y + 1, budget) for x, y in zip(lens, n)]
+    for x in (eager, graphed):
+        assert x[1].device_status() == 0
+        x[1].close()
 
 
 def test_steps_of_a_bounded_cache(st):
