@@ -48,11 +48,13 @@ def parse():
     ap.add_argument("--batches", type=int, default=2, choices=[1, 2],
                     help="alternating input batches (2 keeps consecutive steps off L2)")
     ap.add_argument("--mode", default="sampling",
-                    choices=["sampling", "greedy", "lossy", "restricted", "stats", "features"],
+                    choices=["sampling", "greedy", "lossy", "restricted", "stats", "features", "tree"],
                     help="sampling verify (default), the greedy exact-match verify, the lossy "
                          "verify (f_sq lenience, eps 0.5), the restricted verify (top-k 20, "
                          "top-p 0.95 per sequence), or the row diagnostics: per-position "
-                         "acceptance statistics (beta, TVD) or draft features (entropy, top-10)")
+                         "acceptance statistics (beta, TVD) or draft features (entropy, top-10), or "
+                         "a step of drafted token trees over a paged cache (attention, greedy "
+                         "verify, commit, weight accumulation, eviction)")
     ap.add_argument("--config", type=int, default=BENCH_CFG, choices=[0, 1, 2, 3, 4],
                     help="workload (default: the ragged B=256 bf16 batch; the others serve "
                          "profiling and the per-workload table)")
@@ -447,6 +449,122 @@ def run_restricted(args, rank, world, local):
     print(json.dumps(line), flush=True)
 
 
+TREE_LAYERS, TREE_KV_HEADS, TREE_GROUP, TREE_D, TREE_PAGE = 2, 8, 4, 128, 64
+TREE_LENS, TREE_BUDGET = (1000, 2000), 1900
+
+
+def run_tree(args, rank, world, local):
+    """Times a step of drafted token trees on the workload's target rows: sequence
+    b's tree has gamma_b + 1 nodes (its row count), every node below a random
+    earlier one, over a cache of two layers (8 key heads of 128, 4 query heads
+    each, 1000 to 2000 tokens a sequence). Every call of the step, in its order;
+    the eviction writes its masses and positions aside, so that each step evicts
+    the same tokens."""
+    import torch
+
+    import speculative_decoding_token_gb300 as sv
+    from speculative_decoding_token_gb300 import workload
+
+    sv.build()
+    cfg = workload.CONFIGS[args.config]
+    batch = workload.make_batch(args.config, device="cuda", seed=cfg["seed"] + 100 * rank)
+    B, T = cfg["B"], batch.gamma_max + 1
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(17 + rank)
+    nodes = (batch.gamma + 1).to(torch.int32)
+    j = torch.arange(T, device="cuda")
+    parent = torch.where(j > 0, (torch.rand(B, T, generator=gen, device="cuda") * j).floor(), -1.0)
+    tokens = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    tokens[:, 1:] = batch.draft_tokens
+    tree = sv.TokenTree(batch.p_row_off, nodes, parent.to(torch.int32), tokens)
+    lens = torch.randint(*TREE_LENS, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    pages_each = -(-(TREE_LENS[1] + T) // TREE_PAGE)
+    pages = B * pages_each
+    table = torch.randperm(pages, generator=gen, device="cuda").view(B, pages_each).to(torch.int32)
+    shape = (TREE_LAYERS, pages, TREE_KV_HEADS, TREE_PAGE, TREE_D)
+    k = torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    v = torch.randn(shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    mass = torch.zeros(shape[:-1], device="cuda")
+    pos = torch.zeros(shape[:-1], dtype=torch.int32, device="cuda")
+    slots = torch.arange(pages_each * TREE_PAGE, device="cuda", dtype=torch.int32).view(pages_each, 1, TREE_PAGE)
+    pos[:, table.long()] = slots.expand(B, pages_each, TREE_KV_HEADS, TREE_PAGE)
+    mass_out, pos_out = torch.zeros_like(mass), torch.zeros_like(pos)
+    heads = TREE_KV_HEADS * TREE_GROUP
+    rows = batch.target.shape[0]
+    q = torch.randn(TREE_LAYERS, rows, heads, TREE_D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(TREE_LAYERS, rows, heads, device="cuda")
+    cache = sv.KVCache(k, v, table, mass=mass, pos=pos)
+    layers = [sv.KVCache(k[i], v[i], table, mass=mass[i]) for i in range(TREE_LAYERS)]
+    moves = TREE_LAYERS * B * TREE_KV_HEADS * min(TREE_BUDGET, pages_each * TREE_PAGE - TREE_BUDGET)
+    h = sv.SpecTree(B, max_moves=moves)
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    n, emitted, path = i32(B), i32(B, T), i32(B, T)
+    new_lens, new_seen, kept = i32(B), i32(B), i32(B)
+
+    def attention():
+        for i in range(TREE_LAYERS):
+            h.attention(q[i], layers[i], tree, lens, out=out[i], lse=lse[i])
+
+    def verify():
+        h.verify(tree, batch.target, n=n, tokens=emitted, path=path)
+
+    def commit():
+        h.commit(cache, lens, n, path, seen=lens, new_lens=new_lens, new_seen=new_seen)
+
+    def accumulate():
+        for i in range(TREE_LAYERS):
+            h.accumulate(q[i], lse[i], layers[i], tree, lens, n, path)
+
+    def evict():
+        h.evict(cache, new_lens, new_seen, TREE_BUDGET, sink=4, recent=256, mass_out=mass_out, pos_out=pos_out,
+                new_lens=kept)
+
+    calls = (attention, verify, commit, accumulate, evict)
+
+    def timed(which, steps):
+        start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        start.record()
+        for _ in range(steps):
+            for call in which:
+                call()
+        stop.record()
+        torch.cuda.synchronize()
+        return start.elapsed_time(stop)
+
+    timed(calls, max(args.warmup, 3))
+    barrier(world)
+    with ClockSampler(local) as clocks:
+        time.sleep(0.25)
+        ms = timed(calls, args.steps)
+        time.sleep(0.05)
+    barrier(world)
+    ms = max_over_ranks(ms, world)
+    each = {call.__name__: timed((call,), args.steps) / args.steps for call in calls}
+    status = h.device_status()
+    accepted = int(n.clamp(min=0).sum())
+    h.close()
+    if rank != 0:
+        return
+    count = int(nodes.sum())
+    kv_bytes = int((lens + nodes).sum()) * TREE_LAYERS * TREE_KV_HEADS * TREE_D * 2
+    peak, peak_kind = peaks()
+    gbs = 2 * kv_bytes / (each["attention"] / 1e3) / 1e9
+    line = {"metric": "drafted tree nodes/s", "value": world * count * args.steps / (ms / 1e3), "unit": "nodes/s",
+            "n_gpus": world, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms / args.steps,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {**workload_config(cfg, batch, "greedy"), "mode": "tree", "nodes_per_step": count,
+                       "accepted_per_step": accepted, "layers": TREE_LAYERS, "kv_heads": TREE_KV_HEADS,
+                       "heads": heads, "head_dim": TREE_D, "page": TREE_PAGE, "lens": "%d..%d" % TREE_LENS,
+                       "budget": TREE_BUDGET},
+            "roofline": {"bound": "hbm", "kernel": "tree_attn_kernel", "achieved": gbs, "peak": peak,
+                         "peak_kind": peak_kind, "unit": "GB/s", "frac": gbs / peak, "traffic": None,
+                         "algorithmic_bytes": "keys and values of every token and node once"},
+            "ms_per_call_alone": each, "clocks": clocks.summary(),
+            "gpu_launches": (3 * TREE_LAYERS + 4) * args.steps, "device_status": status}
+    print(json.dumps(line), flush=True)
+
+
 def run_native(args, rank, world, local):
     import torch
 
@@ -650,6 +768,8 @@ def main():
             run_diagnostics(args, rank, world, local)
         elif args.mode == "restricted":
             run_restricted(args, rank, world, local)
+        elif args.mode == "tree":
+            run_tree(args, rank, world, local)
         else:
             run_native(args, rank, world, local)
     finally:
