@@ -60,10 +60,11 @@ struct Shape {
 };
 static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory of a CTA");
 
-
 // An item's place on the line starts with kHead units that are no tiles: what
 // its start and end cost beside its tiles (queries, sums, the output).
-constexpr int kHead = 2;
+// Six measured best over ragged batches (B = 16, 300 to 8000 tokens: 57.8 us;
+// four 58.3, two 59.8, one 63.0).
+constexpr int kHead = 6;
 
 // What sequence b contributes to the line; 0 tiles: idle or bad.
 struct Seq {
@@ -692,7 +693,7 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
     const int box = P.box;
     uint32_t use = 0;
     Segment g;
-    bool ok = true;
+    bool ok = true, begun = false;
     while (ok && walk.next(P, g)) {
         const int len = g.s.L + g.s.T;
         const auto page_id = [&](int j) -> int {  // of the lane's box in tile j, -1: none
@@ -702,6 +703,12 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
         const auto copy = [&](const CUtensorMap *map, int j, int page) {
             const uint32_t slot = use % Sh::kSlots, bar = smem_u32(&M.full[slot]);
             ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
+            // the first queries come ahead of a ring's worth of keys, which would
+            // keep them in the memory's queue for microseconds
+            if (use == 2 && !begun) {
+                ok = wait_on(M, M.q_full[0], 0, P.status) && ok;
+                begun = true;
+            }
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 return;
@@ -879,10 +886,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // the item that CTA c began, two a warp. Piece 0 is c's last segment, the next
 // CTAs' first segments follow. Bound by the latency of its loads: the first
 // kAhead pieces are read before anything is known of their weights.
-constexpr int kJoinWarps = 4, kJoinRows = 2, kAhead = 8;
+constexpr int kJoinWarps = 4, kJoinRows = 2;
 
-template <bool FP16, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
+template <bool FP16, int D, int kAhead>
+__global__ void __launch_bounds__(kJoinWarps * 32, kAhead <= 3 ? 8 : 4) tree_join_kernel(const __grid_constant__ TreeAttnParams P) {
     after_previous();
     constexpr int W = D / 32;
     using Vec = typename std::conditional<W == 4, float4, float2>::type;
@@ -970,7 +977,12 @@ cudaError_t launch(const TreeAttnParams &p, const CUtensorMap &mk, const CUtenso
     if (e != cudaSuccess) return e;
     const int64_t most = std::min((int64_t)2 * kTile, (int64_t)p.t.max_nodes * p.G);
     const unsigned y = (unsigned)((most + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows));
-    return launch_after(tree_join_kernel<FP16, D>, dim3((unsigned)ctas, y), kJoinWarps * 32, 0, s, 1, p);
+    const dim3 grid((unsigned)ctas, y);
+    // With an item for every second CTA, cut items have two or three pieces (and
+    // there are many: fewer registers, more rows at once); with few items, more.
+    if ((int64_t)p.t.B * p.c.kv_heads * 2 >= ctas)
+        return launch_after(tree_join_kernel<FP16, D, 3>, grid, kJoinWarps * 32, 0, s, 1, p);
+    return launch_after(tree_join_kernel<FP16, D, 8>, grid, kJoinWarps * 32, 0, s, 1, p);
 }
 
 template <bool FP16, int D>
