@@ -290,6 +290,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
         const int gr = g.block * 2 * kTile + min(r_item, g.rows - 1);
         const int node = gr / P.G, qh = g.head * P.G + gr - node * P.G;
         const bool warp_on = (pair ? w * kTile : 0) + (row & ~31) < g.rows;
+        const bool mine = r_item < g.rows;  // (rows past the item's hold what the tile held before)
         float m_ref = ninf, l = 0.0f;
         bool fresh = true;
         for (int j = pair ? 0 : w; j < n; j += pair ? 1 : 2) {
@@ -368,7 +369,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                         m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(s[i + c]), __uint_as_float(s[i + c + 4])));
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
                 // Both warps have read S when the barrier opens: P may go over it.
-                if (pair_any(pair_bar, mx > m_ref + Range<FP16>::kSlack)) {
+                if (pair_any(pair_bar, mine && mx > m_ref + Range<FP16>::kSlack)) {
                     M.x[2 * w + h][row] = mx;
                     pair_any(pair_bar, false);
                     const float top = fmaxf(m_ref, fmaxf(M.x[2 * w][row], M.x[2 * w + 1][row]));
@@ -449,7 +450,6 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
         if (sc.bad) lf = NAN;
         if (warp_on) {
             const bool whole = g.first && g.last;
-            const bool mine = r_item < g.rows;
             const float inv = whole ? (lf == 0.0f ? 0.0f : 1.0f / lf) : 1.0f;
             const int64_t orow = g.s.row0 + node;
             const int c_begin = pair ? h * (D / 2) : (2 * w + h) * CW;

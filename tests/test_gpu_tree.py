@@ -125,12 +125,63 @@ def test_attention_shared_pages_and_layer_views(st):
 
 
 def test_attention_repeats_bit_for_bit(st):
-    bt = tu.Batch([5000, 700, 3], [30, 2, 9], 8, 2, 128, 16, BF16, seed=13)
+    """Whatever ran before on the SMs: the Q tile's rows past a tree's hold what the last call left there."""
+    bt = tu.Batch([20000, 9000, 3], [26, 16, 9], 8, 2, 128, 16, FP16, seed=13)
+    other = tu.Batch([700, 300], [32, 30], 8, 2, 128, 16, FP16, seed=14, sharp=40.0).upload()
     first = run_attention(st, bt)
-    for _ in range(5):
+    for i in range(8):
+        if i % 2:
+            st.attention(other.dq, other.cache, other.tree, other.dlens)
         again = run_attention(st, bt)
         assert torch.equal(first[0].nan_to_num(9.0), again[0].nan_to_num(9.0))
         assert torch.equal(first[1].nan_to_num(9.0), again[1].nan_to_num(9.0))
+
+
+def test_calls_of_one_handle_back_to_back():
+    """Attention and eviction of several batches through one handle's workspace, with nothing between the calls."""
+    import speculative_decoding_token_gb300 as sv
+    h = sv.SpecTree(8, max_moves=1 << 16)
+    bts = [tu.Batch([3000 + 900 * i, 77], [5 + 9 * i, 20], 8, 2, 128, 16, BF16, seed=40 + i, poison=False) for i in range(3)]
+    rng, budget = np.random.default_rng(3), 600
+    for bt in bts:
+        shape = bt.k.shape[:-1]
+        mass = torch.rand(shape, generator=bt.gen)
+        pos, seen = make_positions(rng, bt, shape)
+        bt.upload(mass=mass, pos=pos)
+        bt.att = (torch.zeros_like(bt.dq), torch.zeros(bt.rows, bt.heads, device="cuda"))
+        bt.ev = (torch.zeros_like(bt.dmass), torch.zeros_like(bt.dpos), torch.zeros(2, dtype=torch.int32, device="cuda"))
+        bt.dseen = bt.dev(seen, torch.int32)
+
+    def attend(bt):
+        h.attention(bt.dq, bt.cache, bt.tree, bt.dlens, out=bt.att[0], lse=bt.att[1])
+
+    def evict(bt):
+        h.evict(bt.cache, bt.dlens, bt.dseen, budget, sink=4, recent=50, mass_out=bt.ev[0], pos_out=bt.ev[1],
+                new_lens=bt.ev[2])
+
+    want = []
+    for bt in bts:
+        keep = bt.dk.clone(), bt.dv.clone()
+        attend(bt)
+        evict(bt)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (*bt.att, *bt.ev, bt.dk, bt.dv)])
+        bt.dk.copy_(keep[0]), bt.dv.copy_(keep[1])
+        bt.keep = keep
+    for _ in range(20):
+        for bt in bts:
+            for t in (*bt.att, *bt.ev):
+                t.zero_()
+            bt.dk.copy_(bt.keep[0]), bt.dv.copy_(bt.keep[1])
+        for bt in bts * 2:
+            attend(bt)
+        for bt in bts:
+            evict(bt)
+        for bt, w in zip(bts, want):
+            for t, x in zip((*bt.att, *bt.ev, bt.dk, bt.dv), w):
+                assert torch.equal(t, x)
+    assert h.device_status() == 0
+    h.close()
 
 
 def test_attention_scale(st):
