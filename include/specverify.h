@@ -312,6 +312,12 @@ int specverify_verify_noalloc(const specverify_batch *in, float temperature, uin
  * captured into a CUDA graph, and check on the device what they read there:
  * a sequence with a bad size, row, parent, path or page id is left alone (see
  * each call), the others are unaffected, and the sticky status word says so.
+ * They launch as programmatic dependents of the kernel before them on the
+ * stream and wait for it before they touch memory. Waits inside the kernels
+ * are bounded (about two seconds): one that runs out sets
+ * SPECVERIFY_STATUS_TIMEOUT and leaves that call's outputs undefined. Results
+ * are the same from run to run on one GPU. Rows of different sequences do not
+ * overlap, and outputs do not overlap inputs unless a call says so.
  */
 
 typedef struct specverify_tree_ctx *specverify_tree_t;

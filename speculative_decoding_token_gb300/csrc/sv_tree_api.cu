@@ -154,6 +154,7 @@ int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch
     h->ws_bytes = 256 + 3 * ((lists + 255) / 256 * 256) + sv::attn_workspace(h->num_sms);
     if (e == cudaSuccess) e = cudaMalloc(&h->ws, h->ws_bytes);
     if (e == cudaSuccess) e = cudaMemset(h->ws, 0, 256);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the caller's streams need not wait for it
     if (e != cudaSuccess) {
         if (h->ws) cudaFree(h->ws);
         delete h;
