@@ -157,18 +157,19 @@ cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cud
 // ---------------------------------------------------------------------------
 // device helpers
 
-// A line of work units cut over CTAs: CTA i has units [cut.at(i), cut.at(i + 1)), the first `more` one
-// more than the others.
+// A line of work units cut over CTAs: CTA i has units [cut.at(i), cut.at(i + 1)),
+// at(i) = floor(i total / ctas), so that halves of the line are halves of the CTAs.
 struct Cut {
     int ctas, more;
     long long each;
 
     __device__ __forceinline__ Cut(long long total, int grid) {
         ctas = (int)min((long long)grid, total);
-        each = ctas == 0 ? 0 : (total >> 31 ? total / ctas : (long long)((int)total / ctas));
+        if (ctas == 0) ctas = 1;  // no units: they all are CTA 0's
+        each = total >> 31 ? total / ctas : (long long)((int)total / ctas);
         more = (int)(total - each * ctas);
     }
-    __device__ __forceinline__ long long at(int i) const { return i * each + min(i, more); }
+    __device__ __forceinline__ long long at(int i) const { return i * each + i * more / ctas; }
     // The CTA of a unit.
     __device__ __forceinline__ int of(long long unit) const {
         int i = 0;  // at(i) <= unit < at(i + 1), by halves
