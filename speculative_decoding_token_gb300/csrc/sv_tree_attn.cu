@@ -8,8 +8,8 @@
 // them: S = Q K^T and O += P V run on the tensor core in tiles of 128 rows by
 // 128 slots. A persistent CTA per SM:
 //   warps 0-7, 8-15 two softmax groups, half a row a thread: S from tensor
-//                   memory, P back to it;
-//   warp 16         issues the products (one thread);
+//                   memory, P back to it, in two parts;
+//   warp 16         issues the products;
 //   warp 17         copies K and V tiles into a ring of shared-memory slots;
 //   warps 18, 19    go ahead of them: the next segment's Q tiles, and the check
 //                   of its pages and parents.
@@ -22,9 +22,16 @@
 // constant for each item's start, form one line that is cut evenly over the CTAs,
 // first every sequence's first block of rows, then the second ones: where trees
 // have two blocks, CTAs half the grid apart read the same keys at about the same
-// time, and L2 serves one of them. An item cut in pieces leaves each
-// piece's O (not yet divided), maximum and sum in the workspace, and a second
-// kernel joins the pieces; whole items are written directly.
+// time, and L2 serves one of them. An item cut in pieces leaves each piece's O
+// (not yet divided), maximum and sum in the workspace, and a second kernel joins
+// the pieces (3 us; the last of an item's CTAs joining them took longer, for its
+// fence and counter); whole items are written directly.
+//
+// Up to 128 rows a key head the keys' bytes bound it: 1.39 us a tile of 64 KiB
+// and CTA, 7.2 TB/s over 152 of them (B = 38, 65 thousand tokens each). With 256
+// rows the products do: 88 cycles for each of nominally 64 (S = Q K^T reads 8 KiB
+// of shared memory a product, all of the SM's bandwidth), 1.37 PFLOP/s (B = 32,
+// 64 nodes, 64 heads over 8, 14 thousand tokens: 689 us).
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,7 +61,7 @@ struct Shape {
     static constexpr int kSlots = D == 128 ? 5 : 10;     // ring slots of a K or V tile
     static constexpr int kRing = 2 * kTileBytes;         // after the two Q tiles
     static constexpr int kMisc = kRing + kSlots * kTileBytes;
-    static constexpr int kSmem = kMisc + 2944;
+    static constexpr int kSmem = kMisc + 3072;
     // columns of tensor memory: S of both groups, then O of both; P lies over S
     static constexpr uint32_t kS = 0, kO = 2 * kTile;
 };
@@ -157,14 +164,14 @@ struct Misc {
     float x[4][kTile];                     // what the halves and the groups tell each other of a row
     Scouted seg[2];                        // of the even and the odd segments
     uint64_t full[10], empty[10], q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
-    uint64_t seg_full[2], seg_empty[2], drain;
+    uint64_t seg_full[2], seg_empty[2], begun, drain;  // begun: the first queries are there
     int32_t rest0;                         // the CTA's first unit in its first sequence,
     int32_t b0, block0;                    // that sequence, and the block of rows
     uint32_t tmem;
     long long scan[kAttnThreads / 32];
     int32_t abort;                         // a wait gave up
 };
-static_assert(sizeof(Misc) <= 2944, "Misc");
+static_assert(sizeof(Misc) <= 3072, "Misc");
 
 // Place of a segment's K and V tile j in the order of the ring's uses. Group w
 // needs K of its next tile before V of its current one.
@@ -319,8 +326,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                                        d4 = nonfinite_bits<FP16>(x.w);
                         if (a | b | c4 | d4) {
                             *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c4, x.w & ~d4);
-                            const int n = r + shift;
-                            atomicOr(&sc.nonfinite[n >> 5], 1u << (n & 31));
+                            const int i = r + shift;
+                            atomicOr(&sc.nonfinite[i >> 5], 1u << (i & 31));
                         }
                     }
                 }
@@ -577,6 +584,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             mbar_arrive(smem_u32(&M.q_full[x]));
+            if (seg == 0 && i == 0) mbar_arrive(smem_u32(&M.begun));
         }
         if (!g.pair) turn ^= 1;
         // pages and parents
@@ -624,15 +632,18 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
     while (ok && walk.next(P, g)) {
         const int steps = g.pair ? 2 * g.n : g.n;
         // step t: group t % 2, tile t (or t / 2 when both groups take every tile)
-        uint32_t k_slot = 0, k_par = 0;
-        const auto k_ready = [&](int t) { const uint32_t use = base + k_at(g, g.pair ? t >> 1 : t); k_slot = use % Sh::kSlots; k_par = use / Sh::kSlots & 1; };
+        uint32_t slot_k = 0, phase_k = 0;  // of the next step's K, found while P is waited for
+        const auto find_k = [&](int t) {
+            const uint32_t use = base + k_at(g, g.pair ? t >> 1 : t);
+            slot_k = use % Sh::kSlots;
+            phase_k = use / Sh::kSlots & 1;
+        };
         const auto qk = [&](int t) {
             const int w = t & 1;
-            const uint32_t slot = k_slot, kpar = k_par;
+            const uint32_t slot = slot_k;
             const int x = g.pair ? w : turn;
             if (t == 0 || (g.pair && t == 1)) ok = wait_on(M, M.q_full[x], uses[x]++ & 1, P.status);
-            if (!g.pair || w == 0)
-                ok = ok && wait_on(M, M.full[slot], kpar, P.status);
+            if (!g.pair || w == 0) ok = ok && wait_on(M, M.full[slot], phase_k, P.status);
             if (!ok) return;
             tc_fence_after();
             const uint32_t a = q0 + x * Sh::kTileBytes, b = ring + slot * Sh::kTileBytes;
@@ -646,14 +657,14 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             if (g.pair ? t + 2 >= steps : t + 1 == steps) mma_commit(smem_u32(&M.q_empty[x]), on);
             if (!g.pair || w == 1) mma_commit(smem_u32(&M.empty[slot]), on);
         };
-        k_ready(0);
+        find_k(0);
         if (ok) qk(0);
-        k_ready(1);
+        find_k(1);
         if (ok && steps > 1) qk(1);
         for (int t = 0; ok && t < steps; ++t) {
             const int j = g.pair ? t >> 1 : t, w = t & 1;
             const uint32_t use = base + v_at(g, j), slot = use % Sh::kSlots;
-            k_ready(t + 2);
+            find_k(t + 2);
             if (!g.pair || w == 0) ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
             const uint32_t b = ring + slot * Sh::kTileBytes;
 #pragma unroll
@@ -693,7 +704,7 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
     const int box = P.box;
     uint32_t use = 0;
     Segment g;
-    bool ok = true, begun = false;
+    bool ok = true;
     while (ok && walk.next(P, g)) {
         const int len = g.s.L + g.s.T;
         const auto page_id = [&](int j) -> int {  // of the lane's box in tile j, -1: none
@@ -705,10 +716,7 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
             ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
             // the first queries come ahead of a ring's worth of keys, which would
             // keep them in the memory's queue for microseconds
-            if (use == 2 && !begun) {
-                ok = wait_on(M, M.q_full[0], 0, P.status) && ok;
-                begun = true;
-            }
+            if (use == 2) ok = wait_on(M, M.begun, 0, P.status) && ok;
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 return;
@@ -768,6 +776,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(smem_u32(&M.p_full[w][1]), kSoftThreads / 64);
             mbar_init(smem_u32(&M.o_full[w]), 1);
         }
+        mbar_init(smem_u32(&M.begun), kScoutThreads);
         mbar_init(smem_u32(&M.drain), 1);
         M.abort = 0;
         mbar_fence_init();

