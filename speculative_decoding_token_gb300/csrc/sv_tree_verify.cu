@@ -5,9 +5,13 @@
 // Only the rows on the accepted path decide, about two of a tree's dozens, so
 // the walk reads those alone, one after another, and is bound by the latency
 // of n + 1 dependent row reads: a cluster of kVtCtas CTAs per sequence reads
-// each row, CTA c the columns [c per, (c + 1) per), every warp tells all of
-// them its first maximum through distributed shared memory, and every CTA takes
-// the same step: 1.8 us (V = 152064; B = 64, 4 to 48 nodes: 21 us a call).
+// each row, CTA c the columns [c per, (c + 1) per), every warp sends all of them
+// its first maximum (stores to distributed shared memory that count themselves
+// on a barrier there: B = 16, V = 152064: 11.4 us a call; with a barrier of the
+// cluster 12.7), and every CTA takes the same step, in about 1.8 us. B = 64, 4 to
+// 48 nodes: 19.4 us; 57 sequences fit the GPU at a time. Loading the first
+// child's row ahead did not pay: where every cluster is at work it is traffic
+// that many steps do not need.
 #include "sv_rows.cuh"
 #include "sv_tree.h"
 
@@ -18,16 +22,7 @@ namespace {
 constexpr int kVtCtas = 8;
 constexpr int kVtThreads = 256;
 constexpr int kVtWarps = kVtThreads / 32;
-constexpr int kVtBatch = 10;  // 16-byte vectors that a thread holds
-
-// A load that is issued where it stands, ahead of the barriers before its use.
-__device__ __forceinline__ uint4 ld_early(const void *p) {
-    uint4 x;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "l"(p));
-    return x;
-}
+constexpr int kVtBatch = 10;  // 16-byte vectors that a thread loads at a time
 
 // A candidate of the argmax: order-preserving bits of its value (-0 as +0, a NaN
 // above all), and its index. The larger value wins, then the lower index.
@@ -43,8 +38,29 @@ __device__ __forceinline__ void warp_best(uint32_t &key, uint32_t &idx) {
     key = top;
 }
 
-__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t x, uint32_t y) {
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+// A store to another CTA's shared memory that counts its bytes on a barrier there.
+__device__ __forceinline__ void send_u2(uint32_t addr, uint32_t bar, uint32_t x, uint32_t y) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+        "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// A wait for what other CTAs of the cluster send; gives up after about two seconds.
+__device__ __forceinline__ bool wait_sent(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (global_ns() - t0 > 2000000000ull) return false;
+    }
 }
 
 template <int DT>
@@ -55,7 +71,9 @@ __device__ __forceinline__ float logit_at(const char *row, int64_t v) {
 
 template <int DT>
 __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid_constant__ TreeVerifyParams P) {
-    __shared__ __align__(16) uint2 s_slice[2][kVtCtas * kVtWarps];  // every warp's candidate
+    // every warp's candidate, and its arrival, of the even and the odd steps
+    __shared__ __align__(16) uint2 s_slice[2][kVtCtas * kVtWarps];
+    __shared__ uint64_t s_bar[2];
     __shared__ int32_t s_parent[kMaxNodes], s_token[kMaxNodes], s_path[kMaxNodes];
     constexpr int PV = DT == SV_DT_FP32 ? 4 : 8;  // logits in a 16-byte vector
     after_previous();
@@ -97,113 +115,74 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
         return;  // every CTA of the cluster leaves here
     }
 
-    // no CTA's shared memory is written before that CTA runs (waited for below)
+    // no CTA's shared memory is written before that CTA has set it up (waited for below)
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&s_bar[0]), 1);
+        mbar_init(smem_u32(&s_bar[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
     // this CTA's columns: whole vectors, the last CTA's ending at V
     const int64_t per = ((P.V + kVtCtas - 1) / kVtCtas + PV - 1) / PV * PV;
     const int64_t c0 = min(P.V, (int64_t)rank * per), c1 = min(P.V, c0 + per);
-    const int64_t v0 = c0 / PV, v1 = c1 / PV;
+    const int v0 = (int)(c0 / PV), v1 = (int)(c1 / PV);
     int node = 0, n = 0;
     int32_t pick = -1;
-    bool nan = false;
-    // Where the target agrees with a draft it is mostly the first child's, so that
-    // child's row is on its way (into registers as far as they reach, the rest
-    // to L2) while the cluster decides the step.
-    uint4 v[kVtBatch];
-    const auto fetch = [&](int to) {
-        const char *row = P.target + (row0 + to) * P.stride_bytes;
-#pragma unroll
-        for (int i = 0; i < kVtBatch; ++i) {
-            const int64_t vi = v0 + threadIdx.x + i * kVtThreads;
-            if (vi < v1) v[i] = ld_early(row + vi * 16);
-        }
-    };
-    const int64_t beyond = v0 + kVtBatch * kVtThreads;  // vectors that registers do not hold
-    fetch(0);
+    bool nan = false, late = false;
     for (;;) {  // at most `nodes` steps: each goes to a later node
         const char *row = P.target + (row0 + node) * P.stride_bytes;
-        const uint4 *rv = reinterpret_cast<const uint4 *>(row);
+        // the thread's first vector of the largest element, then that element
         uint32_t key = 0, idx = 0xffffffffu;
-        {
-            // the maximum of the held vectors, then the first vector and element of it
-            float m[kVtBatch], best = -INFINITY;
+        if (v0 + (int)threadIdx.x < v1) {
+            float best = -INFINITY;
+            int at = v0 + (int)threadIdx.x;
+            bool odd = false;
+            for (int from = at; from < v1; from += kVtBatch * kVtThreads) {
+                uint4 v[kVtBatch];
 #pragma unroll
-            for (int i = 0; i < kVtBatch; ++i) {
-                const int64_t vi = v0 + threadIdx.x + i * kVtThreads;
-                m[i] = vi < v1 ? vec_max<DT>(v[i]) : -INFINITY;
-                best = max_nan(best, m[i]);
-            }
-            uint4 x = v[0];
-            int at = 0;
+                for (int i = 0; i < kVtBatch; ++i)
+                    if (from + i * kVtThreads < v1)
+                        v[i] = *reinterpret_cast<const uint4 *>(row + (int64_t)(from + i * kVtThreads) * 16);
 #pragma unroll
-            for (int i = kVtBatch - 1; i >= 0; --i)
-                if (m[i] == best && v0 + threadIdx.x + i * kVtThreads < v1) {
-                    at = i;
-                    x = v[i];
+                for (int i = 0; i < kVtBatch; ++i) {
+                    if (from + i * kVtThreads >= v1) break;
+                    const float m = vec_max<DT>(v[i]);
+                    odd |= m != m;
+                    if (m > best) {
+                        best = m;
+                        at = from + i * kVtThreads;
+                    }
                 }
-            if (v0 + threadIdx.x < v1) {
-                float f[PV];
-                vec_floats<DT>(x, f);
-                int e = 0;
-#pragma unroll
-                for (int j = PV - 1; j >= 0; --j)
-                    if (f[j] == best) e = j;
-                key = value_key(best);
-                idx = (uint32_t)((v0 + threadIdx.x + at * kVtThreads) * PV + e);
             }
-        }
-#pragma unroll 4
-        for (int64_t vi = beyond + threadIdx.x; vi < v1; vi += kVtThreads) {
-            const uint4 x = rv[vi];
-            const float m = vec_max<DT>(x);
-            if (value_key(m) > key) {  // later indexes: a tie keeps the first
-                float f[PV];
-                vec_floats<DT>(x, f);
-                int e = 0;
+            float f[PV];
+            vec_floats<DT>(*reinterpret_cast<const uint4 *>(row + (int64_t)at * 16), f);
+            int e = 0;
 #pragma unroll
-                for (int j = PV - 1; j >= 0; --j)
-                    if (f[j] == m) e = j;
-                key = value_key(m);
-                idx = (uint32_t)(vi * PV + e);
-            }
+            for (int j = PV - 1; j >= 0; --j)
+                if (f[j] == best) e = j;
+            key = odd ? 0xffffffffu : value_key(best);
+            idx = (uint32_t)(at * PV + e);
         }
-        for (int64_t e = v1 * PV + threadIdx.x; e < c1; e += kVtThreads) {  // the ragged end at V
+        for (int64_t e = (int64_t)v1 * PV + threadIdx.x; e < c1; e += kVtThreads) {  // the ragged end at V
             const uint32_t k = value_key(logit_at<DT>(row, e));
             if (k > key || idx == 0xffffffffu) {
                 key = k;
                 idx = (uint32_t)e;
             }
         }
-        // the lowest child (of the token `want`, if that is not -1), every warp for itself
-        const auto child_of = [&](int32_t want) {
-            int found = -1;
-            for (int j0 = (node + 1) & ~31; j0 < nodes && found < 0; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t hit =
-                    __ballot_sync(0xffffffffu, j > node && j < nodes && s_parent[j] == node &&
-                                                   (want < 0 || s_token[j] == want));
-                if (hit) found = j0 + __ffs(hit) - 1;
-            }
-            return found;
-        };
-        const int guess = child_of(-1);
-        if (guess >= 0) {
-            fetch(guess);
-            if (beyond < v1 && threadIdx.x == 0)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                 P.target + (row0 + guess) * P.stride_bytes + beyond * 16),
-                             "r"((uint32_t)min((v1 - beyond) * 16, (int64_t)1 << 18))
-                             : "memory");
-        }
         warp_best(key, idx);
         if (n == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        // Every CTA sends its candidates to all of them and waits for theirs on its
+        // own barrier. Step n + 2 reuses step n's places: who is there has had this
+        // CTA's candidates of step n + 1, sent after it had read step n's.
+        const uint32_t bar = smem_u32(&s_bar[n & 1]);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, sizeof(s_slice[0]));
         if (lane < kVtCtas)
-            st_cluster_u2(cluster_addr(&s_slice[n & 1][rank * kVtWarps + warp], (uint32_t)lane), key,
-                          idx);
-        // The barrier orders the candidates, and step n + 2 reuses this step's only
-        // after every CTA has passed the barrier of step n + 1.
-        cluster_sync();
+            send_u2(cluster_addr(&s_slice[n & 1][rank * kVtWarps + warp], (uint32_t)lane),
+                    cluster_addr(&s_bar[n & 1], (uint32_t)lane), key, idx);
+        if (!wait_sent(bar, n >> 1 & 1)) late = true;
+        if (late) break;
         static_assert(kVtCtas * kVtWarps == 64, "two candidates a lane");
         const uint2 a = s_slice[n & 1][lane], z = s_slice[n & 1][lane + 32];
         const bool second = z.x > a.x || (z.x == a.x && z.y < a.y);
@@ -214,23 +193,34 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
         nan = key == 0xffffffffu;
         if (nan) break;
         if (threadIdx.x == 0) s_path[n] = node;
-        const int next = child_of(pick);
-        if (next >= 0 && next != guess) fetch(next);
+        // the lowest child with that token (every warp for itself)
+        int next = -1;
+        for (int j0 = (node + 1) & ~31; j0 < nodes && next < 0; j0 += 32) {
+            const int j = j0 + lane;
+            const uint32_t hit = __ballot_sync(
+                0xffffffffu, j > node && j < nodes && s_parent[j] == node && s_token[j] == pick);
+            if (hit) next = j0 + __ffs(hit) - 1;
+        }
         if (next < 0) break;
         node = next;
         ++n;
     }
+    // (nobody leaves while another may still send to it)
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    late = __syncthreads_or(late);
     if (rank == 0) {
-        __syncthreads();
+        const bool none = nan || late;
         for (int i = threadIdx.x; i < mn; i += kVtThreads) {
-            path[i] = !nan && i <= n ? s_path[i] : -1;
-            tok[i] = nan || i > n ? -1 : (i == n ? pick : s_token[s_path[i + 1]]);
+            path[i] = !none && i <= n ? s_path[i] : -1;
+            tok[i] = none || i > n ? -1 : (i == n ? pick : s_token[s_path[i + 1]]);
         }
         if (threadIdx.x == 0) {
-            P.n_out[b] = nan ? -1 : n;
-            if (nan) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
+            P.n_out[b] = none ? -1 : n;
+            if (late) atomicOr(P.status, SPECVERIFY_STATUS_TIMEOUT);
+            else if (nan) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
         }
     }
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 }  // namespace
