@@ -480,8 +480,9 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
 #pragma unroll
                     for (int i = 0; i < CW; ++i) f[i] = fmaf(__uint_as_float(o[i]), wgt[1], f[i]);
                 }
-                if (any_odd && mine) {
-                    // a seen inf or NaN decides its element whatever its weight
+                if (any_odd && mine && !sc.bad) {
+                    // a seen inf or NaN decides its element whatever its weight (a bad
+                    // segment has no page to read: its sum is NaN already)
                     for (int j = node; j >= 0; j = sc.parent[j]) {
                         if (!(sc.nonfinite[j >> 5] >> (j & 31) & 1)) continue;
                         const int s = g.s.L + j;

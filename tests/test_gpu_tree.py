@@ -251,6 +251,25 @@ def test_attention_bad_input_marks_its_sequence(st):
         near(lse, want[1], want[3])
 
 
+def test_attention_bad_pages_under_the_tree(st):
+    """Pages of nodes that lie outside the pool, in tiles whose shared memory still holds other sequences' NaN (slots past
+    their trees): nothing is read there, the rows are NaN, the sequences between them are right."""
+    import speculative_decoding_token_gb300 as sv
+    B = 400
+    lens, nodes = [192 if b % 2 == 0 else 200 for b in range(B)], [1 if b % 2 == 0 else 8 for b in range(B)]
+    bt = tu.Batch(lens, nodes, 4, 2, 128, 16, BF16, seed=71)
+    want = tu.attention(bt, bt.d ** -0.5)
+    for b in range(1, B, 2):
+        bt.table[b, 12] = (-1, -(2 ** 31), bt.k.shape[1], 2 ** 31 - 1)[b // 2 % 4]
+        for w in want[:2]:
+            w[bt.row_off[b]: bt.row_off[b] + nodes[b]] = float("nan")
+    h = sv.SpecTree(B)
+    out, lse = run_attention(h, bt)
+    assert h.device_status() == sv.STATUS_BITS["bad_cache"]
+    near(out, want[0], want[2])
+    near(lse, want[1], want[3])
+
+
 # ---------------------------------------------------------------------------
 # verify
 
