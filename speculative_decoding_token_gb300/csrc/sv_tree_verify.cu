@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
         if (lane < kVtCtas)
             send_u2(cluster_addr(&s_slice[n & 1][rank * kVtWarps + warp], (uint32_t)lane),
                     cluster_addr(&s_bar[n & 1], (uint32_t)lane), key, idx);
-        if (!wait_sent(bar, n >> 1 & 1)) late = true;
+        // (a warp leaves as a whole: its reductions are of all lanes)
+        late = __any_sync(0xffffffffu, !wait_sent(bar, n >> 1 & 1));
         if (late) break;
         static_assert(kVtCtas * kVtWarps == 64, "two candidates a lane");
         const uint2 a = s_slice[n & 1][lane], z = s_slice[n & 1][lane + 32];
