@@ -316,8 +316,9 @@ int specverify_verify_noalloc(const specverify_batch *in, float temperature, uin
  * stream and wait for it before they touch memory. Waits inside the kernels
  * are bounded (about two seconds): one that runs out sets
  * SPECVERIFY_STATUS_TIMEOUT and leaves that call's outputs undefined. Results
- * are the same from run to run on one GPU. Rows of different sequences do not
- * overlap, and outputs do not overlap inputs unless a call says so.
+ * are the same from run to run on one GPU unless a call says otherwise. Rows
+ * of different sequences do not overlap, and outputs do not overlap inputs
+ * unless a call says so.
  */
 
 typedef struct specverify_tree_ctx *specverify_tree_t;
@@ -395,7 +396,8 @@ int specverify_tree_workspace_bytes(specverify_tree_t h, size_t *out);
  *   out = sum_p softmax(s)_p v_p,  lse = ln sum_p exp(s_p).
  * q and out are [rows, heads, head_dim] of the cache's dtype, with their own
  * row and head strides in elements (multiples of 16 bytes, as the bases);
- * heads is a multiple of kv_heads, scale > 0; lse [rows, heads] may be NULL.
+ * heads is a multiple of kv_heads, scale > 0; lse [rows, heads] may be NULL. q
+ * may have strides of 0 (one query for all rows or heads), out may not.
  * The scores, the softmax statistics and the sums over values are fp32; a
  * weight is rounded to the cache's dtype, relative to a running maximum,
  * before it multiplies a value. A slot that a node does not see never reaches
@@ -441,8 +443,9 @@ int specverify_tree_commit(specverify_tree_t h, const specverify_cache *cache, i
  * before it):
  *   mass[p, g] += sum_{i <= n_accepted[b]} sum_{h of key head g} [p <= lens[b] + i]
  *                 exp(scale * <q[row_off[b] + path[b, i], h], k_p> - lse[that row, h]).
- * q and lse are those of specverify_tree_attention. One layer a call. Sums
- * are fp32 in a fixed order; a page that two sequences share gathers both. A
+ * q and lse are those of specverify_tree_attention. One layer a call. A
+ * sequence's sums are fp32 in a fixed order; a page that sequences share gathers
+ * all of theirs, in any order (its last bits may differ from run to run). A
  * sequence with n_accepted[b] = -1 or a bad path, row, length or page adds
  * nothing. */
 int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cache,

@@ -212,6 +212,9 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
         rc = check_rows(cache, out, rows, heads, out_row_stride, out_head_stride);
     if (rc != SPECVERIFY_OK) return rc;
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
+    // queries may be one row for all, outputs not
+    if ((rows > 1 && out_row_stride == 0) || (heads > 1 && out_head_stride == 0))
+        return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
     if (!lens) return SPECVERIFY_ERR_INVALID_ARG;
     // one sequence's share of the work line is counted in 31 bits

@@ -686,6 +686,23 @@ def test_refusals(st):
     assert st.device_status() == 0
 
 
+def test_attention_refuses_an_expanded_output_and_takes_an_expanded_query(st):
+    import speculative_decoding_token_gb300 as sv
+    bt = tu.Batch([40, 7], [5, 3], 4, 2, 64, 8, BF16, seed=6)
+    bt.q = bt.q[:1, :1].expand(bt.rows, 4, 64).contiguous()
+    want = tu.attention(bt, 0.125)
+    bt.upload()
+    one = bt.dq[:1, :1]
+    for out in (torch.zeros_like(bt.dq[:1]).expand(bt.rows, -1, -1), torch.zeros_like(bt.dq[:, :1]).expand(-1, 4, -1)):
+        with pytest.raises(sv.SpecVerifyError) as e:
+            st.attention(bt.dq, bt.cache, bt.tree, bt.dlens, out=out)
+        assert e.value.rc == -1 and not bool(out.any())
+    out, lse = torch.full_like(bt.dq, float("nan")), torch.full((bt.rows, 4), float("nan"), device="cuda")
+    st.attention(one.expand(bt.rows, 4, 64), bt.cache, bt.tree, bt.dlens, out=out, lse=lse)
+    near(out, want[0], want[2])
+    near(lse, want[1], want[3])
+
+
 def test_empty_batch(st):
     import speculative_decoding_token_gb300 as sv
     bt = tu.Batch([3], [2], 2, 1, 64, 8, BF16, poison=False)
