@@ -38,6 +38,7 @@ struct DeviceGuard {
 
 int map_cuda(cudaError_t e) {
     if (e == cudaSuccess) return SPECVERIFY_OK;
+    cudaGetLastError();  // it is reported here: the program's next launch check need not see it
     if (e == cudaErrorMemoryAllocation) return SPECVERIFY_ERR_OOM;
     return SPECVERIFY_ERR_CUDA;
 }

@@ -703,6 +703,14 @@ def test_attention_refuses_an_expanded_output_and_takes_an_expanded_query(st):
     near(lse, want[1], want[3])
 
 
+def test_a_handle_too_large_leaves_no_error_behind(st):
+    import speculative_decoding_token_gb300 as sv
+    with pytest.raises(sv.SpecVerifyError) as e:
+        sv.SpecTree(1, max_moves=1 << 36)  # three lists of 256 GiB
+    assert e.value.rc == sv.ERR_OOM
+    assert float(torch.ones(8, device="cuda").sum()) == 8.0  # a launch that checks for errors before it
+
+
 def test_empty_batch(st):
     import speculative_decoding_token_gb300 as sv
     bt = tu.Batch([3], [2], 2, 1, 64, 8, BF16, poison=False)
