@@ -61,7 +61,7 @@ struct Shape {
     static constexpr int kSlots = D == 128 ? 5 : 10;     // ring slots of a K or V tile
     static constexpr int kRing = 2 * kTileBytes;         // after the two Q tiles
     static constexpr int kMisc = kRing + kSlots * kTileBytes;
-    static constexpr int kSmem = kMisc + 3072;
+    static constexpr int kSmem = kMisc + 3 * 1024;
     // columns of tensor memory: S of both groups, then O of both; P lies over S
     static constexpr uint32_t kS = 0, kO = 2 * kTile;
 };
@@ -171,7 +171,7 @@ struct Misc {
     long long scan[kAttnThreads / 32];
     int32_t abort;                         // a wait gave up
 };
-static_assert(sizeof(Misc) <= 3072, "Misc");
+static_assert(sizeof(Misc) <= 3 * 1024, "Misc");
 
 // Place of a segment's K and V tile j in the order of the ring's uses. Group w
 // needs K of its next tile before V of its current one.
