@@ -6,14 +6,15 @@
 // tensor memory and a row a column, so the sum over the rows stays within a
 // thread and needs no running maximum (the rows' logsumexps are known). A
 // persistent CTA per SM:
-//   warps 0-3, 4-7  two groups over every other tile of 128 slots, a slot a
+//   warps 0-3, 4-7  two groups, every other tile of 128 slots each, a slot a
 //                   thread: exponentials, their sum, one addition to mass;
 //   warp 8          issues the products (one thread);
 //   warp 9          copies K tiles into a ring of shared-memory slots;
 //   warps 10, 11    gather the rows' queries and logsumexps a chunk ahead.
 // (B = 24, 9 to 16 thousand tokens: 103 us, 6.1 TB/s, 90 % of the copy rate.)
-// More than 128 rows are taken in chunks over the same tiles. A slot's chunks
-// are added in order by one thread, so the sum is the same every time.
+// More than 128 rows are taken in chunks over the same tiles. A tile belongs to
+// one group in every chunk, so a slot's chunks are added in order by one thread
+// and the sum is the same every time.
 #include <cuda_fp16.h>
 
 #include "sv_tcgen05.cuh"
@@ -128,7 +129,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
     const int tid = threadIdx.x, w = tid >> 7, lane_row = tid & 127;
     const uint32_t ts = tmem + ((uint32_t)(lane_row & ~31) << 16) + w * kRows;
     const float c2 = P.scale_log2;
-    uint32_t chunk = 0, turn = 0, phase = 0;  // turn: tiles of the CTA so far
+    uint32_t chunk = 0, first = 0, phase = 0;  // first: tiles of the CTA's segments so far
     Segment g;
     while (walk.next(P, g)) {
         const int last = g.s.L + g.s.n;  // the last slot that gathers
@@ -136,8 +137,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
             const int rows = min(kRows, g.rows - q * kRows);
             const float *lse = M.lse[chunk & 1];
             bool ready = false;
-            for (int j = 0; j < g.n; ++j, ++turn) {
-                if ((int)(turn & 1) != w) continue;
+            for (int j = (first ^ w) & 1; j < g.n; j += 2) {  // the same tiles in every chunk
                 const int s = (g.tile0 + j) * kTile + lane_row;
                 const int64_t page = s <= last ? page_of(P.c, g.b, s) : -1;
                 if (!ready) {  // the scouts' lse and verdict
@@ -180,6 +180,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
             if (!ready) wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
             mbar_arrive(smem_u32(&M.q_empty[chunk & 1]));  // its lse is not read again
         }
+        first += g.n;
     }
 }
 
@@ -188,7 +189,7 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
     using Sh = Shape<D>;
     const uint32_t q0 = smem_u32(smem), ring = q0 + Sh::kRing;
     const bool on = elect_one();
-    uint32_t chunk = 0, turn = 0;
+    uint32_t chunk = 0, turn = 0, first = 0, uses[2] = {0, 0};
     Segment g;
     bool ok = true;
     while (ok && walk.next(P, g)) {
@@ -198,9 +199,9 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
             ok = wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
             const uint32_t b = q0 + (chunk & 1) * Sh::kTileBytes;
             for (int j = 0; ok && j < g.n; ++j, ++turn) {
-                const uint32_t slot = turn % Sh::kSlots, w = turn & 1;
+                const uint32_t slot = turn % Sh::kSlots, w = (first + j) & 1;
                 ok = wait_on(M, M.full[slot], turn / Sh::kSlots & 1, P.status) &&
-                     wait_on(M, M.s_empty[w], (turn >> 1 & 1) ^ 1, P.status);
+                     wait_on(M, M.s_empty[w], (uses[w]++ & 1) ^ 1, P.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t a = ring + slot * Sh::kTileBytes;
@@ -214,6 +215,7 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
             }
             if (ok) mma_commit(smem_u32(&M.q_empty[chunk & 1]), on);
         }
+        first += g.n;
     }
     if (!ok) {  // no product outlives the CTA
         mma_commit(smem_u32(&M.drain), on);

@@ -915,3 +915,62 @@ def test_steps_of_a_bounded_cache(st):
                     assert torch.equal(e[0], by_pos[e[3]][0]) and torch.equal(e[1], by_pos[e[3]][1])
         lens, seen = kept, new_seen
     assert evictions > 10
+
+
+def long_paths(bt, nodes):
+    """Every node of every tree accepted."""
+    n = [t - 1 for t in nodes]
+    path = np.full((bt.B, bt.T), -1)
+    for b, t in enumerate(nodes):
+        path[b, :t] = np.arange(t)
+    return bt.dev(n, torch.int32), bt.dev(path, torch.int32)
+
+
+def test_accumulate_adds_the_chunks_of_a_slot_in_order(st):
+    """Three and four chunks of 128 rows over one to three tiles. Every score is 0, so a row weighs exactly 1 (logsumexp 0)
+    or nothing (200, under fp32's least number), and sums next to 2^24 show the order in which the chunks were added."""
+    B, G = 48, 8
+    lens, nodes = [(60, 200, 300, 0)[b % 4] for b in range(B)], [40 + 3 * (b % 5) for b in range(B)]
+    bt = tu.Batch(lens, nodes, 8 * G, 8, 64, 16, BF16, seed=51, kind="chain", poison=False)
+    bt.q.zero_()
+    start = 2.0 ** 24 - 2
+    bt.upload(mass=torch.full(bt.k.shape[:-1], start))
+    weigh = torch.zeros(bt.rows, bt.heads)
+    want = torch.full(bt.k.shape[1:-1], start)
+    for b in range(B):
+        own = torch.zeros(nodes[b], bt.kv_heads, G)  # a node's rows of a key head
+        for i, count in ((0, 3), (17, 1), (34, 1)):  # in chunks 0, 1 and 2
+            own[i, :, :count] = 1
+        weigh[bt.row_off[b]: bt.row_off[b] + nodes[b]] = own.view(nodes[b], -1)
+        pg, at = bt.slots(b, lens[b] + nodes[b])
+        for s in range(lens[b] + nodes[b]):
+            rows = own[max(0, s - lens[b]):, 0].reshape(-1)  # of the nodes that see the slot
+            first = max(0, s - lens[b]) * G
+            total = np.float32(start)
+            for c in range(0, nodes[b] * G, 128):
+                total = np.float32(total + np.float32(float(rows[max(0, c - first): max(0, c + 128 - first)].sum())))
+            want[pg[s], :, at[s]] = float(total)
+    lse = torch.where(weigh > 0, 0.0, 200.0).cuda()
+    n, path = long_paths(bt, nodes)
+    for _ in range(10):
+        bt.dmass.fill_(start)
+        st.accumulate(bt.dq, lse, bt.cache, bt.tree, bt.dlens, n, path)
+        assert torch.equal(bt.dmass.cpu(), want)
+
+
+@pytest.mark.parametrize("lens,nodes,G,d", [([60, 20], [40, 64], 8, 64), ([300, 310, 5], [48, 70, 50], 8, 128),
+                                            ([1000, 333, 90], [128, 100, 33], 4, 64)])
+def test_accumulate_of_many_rows_repeats_bit_for_bit(st, lens, nodes, G, d):
+    bt = tu.Batch(lens, nodes, 4 * G, 4, d, 16, BF16, seed=G + d)
+    mass = torch.rand(bt.k.shape[:-1], generator=bt.gen)
+    bt.upload(mass=mass)
+    lse = (torch.rand(bt.rows, bt.heads, generator=bt.gen) * 3 + 4).cuda()
+    n, path = long_paths(bt, nodes)
+    first = None
+    for _ in range(20):
+        bt.dmass.copy_(mass[0])
+        st.accumulate(bt.dq, lse, bt.cache, bt.tree, bt.dlens, n, path)
+        first = bt.dmass.clone() if first is None else first
+        assert torch.equal(bt.dmass, first)
+    want, tol = tu.accumulate(bt, mass[0], lse.cpu(), n.tolist(), path.cpu().numpy(), d ** -0.5)
+    near(first, want, tol)
