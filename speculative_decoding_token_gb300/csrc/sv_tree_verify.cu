@@ -63,6 +63,41 @@ __device__ __forceinline__ bool wait_sent(uint32_t bar, uint32_t parity) {
     }
 }
 
+// A plain store to another CTA's shared memory, there once both have passed a
+// barrier of the cluster.
+__device__ __forceinline__ void put_u1(uint32_t addr, int32_t x) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Waits for every candidate that was sent to this CTA, where warps of the cluster
+// gave up: a store that counts itself must not meet a CTA that has left. A warp goes
+// past a step only with all of its candidates, so every warp has sent those of the
+// first `all` steps and some those of one step more; sent[w] is warp w's number, of
+// this CTA's warp 0 `mine`. One thread.
+__device__ __noinline__ void drain_sent(const int32_t *sent, int mine, const uint64_t *bars) {
+    int all = sent[0], more = 0;
+    for (int w = 1; w < kVtCtas * kVtWarps; ++w) all = min(all, sent[w]);
+    for (int w = 0; w < kVtCtas * kVtWarps; ++w) more += sent[w] > all;
+    mbar_wait_bounded(smem_u32(&bars[(all - 1) & 1]), (all - 1) >> 1 & 1);
+    if (more == 0) return;
+    const uint32_t bar = smem_u32(&bars[all & 1]), each = sizeof(uint2);
+    if (mine > all)  // the barrier expects every warp's: count those that do not come
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar),
+                     "r"((kVtCtas * kVtWarps - more) * each)
+                     : "memory");
+    else
+        mbar_arrive_expect_tx(bar, more * each);
+    mbar_wait_bounded(bar, all >> 1 & 1);
+}
+
 template <int DT>
 __device__ __forceinline__ float logit_at(const char *row, int64_t v) {
     if (DT == SV_DT_FP32) return reinterpret_cast<const float *>(row)[v];
@@ -74,6 +109,7 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
     // every warp's candidate, and its arrival, of the even and the odd steps
     __shared__ __align__(16) uint2 s_slice[2][kVtCtas * kVtWarps];
     __shared__ uint64_t s_bar[2];
+    __shared__ int32_t s_late, s_sent[kVtCtas * kVtWarps];  // a warp of the cluster gave up; steps that it sent
     __shared__ int32_t s_parent[kMaxNodes], s_token[kMaxNodes], s_path[kMaxNodes];
     constexpr int PV = DT == SV_DT_FP32 ? 4 : 8;  // logits in a 16-byte vector
     after_previous();
@@ -119,9 +155,10 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&s_bar[0]), 1);
         mbar_init(smem_u32(&s_bar[1]), 1);
+        s_late = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    cluster_arrive();
 
     // this CTA's columns: whole vectors, the last CTA's ending at V
     const int64_t per = ((P.V + kVtCtas - 1) / kVtCtas + PV - 1) / PV * PV;
@@ -172,7 +209,7 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
             }
         }
         warp_best(key, idx);
-        if (n == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (n == 0) cluster_wait();
         // Every CTA sends its candidates to all of them and waits for theirs on its
         // own barrier. Step n + 2 reuses step n's places: who is there has had this
         // CTA's candidates of step n + 1, sent after it had read step n's.
@@ -206,8 +243,10 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
         node = next;
         ++n;
     }
-    // (nobody leaves while another may still send to it)
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    // nobody leaves while another may still send to it
+    const int sent = n + 1;
+    if (late && lane < kVtCtas) put_u1(cluster_addr(&s_late, (uint32_t)lane), 1);
+    cluster_arrive();
     late = __syncthreads_or(late);
     if (rank == 0) {
         const bool none = nan || late;
@@ -221,7 +260,13 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
             else if (nan) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
         }
     }
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    cluster_wait();
+    if (*(volatile int32_t *)&s_late) {  // the same in every CTA
+        if (lane < kVtCtas) put_u1(cluster_addr(&s_sent[rank * kVtWarps + warp], (uint32_t)lane), sent);
+        cluster_arrive();
+        cluster_wait();
+        if (threadIdx.x == 0) drain_sent(s_sent, sent, s_bar);
+    }
 }
 
 }  // namespace
