@@ -8,32 +8,20 @@
 #include <new>
 #include <vector>
 
+#include "sv_host.h"
 #include "sv_internal.h"
 #include "sv_rows_params.h"
 #include "sv_small.h"
 
 namespace {
 
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            changed = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
+using sv::DeviceGuard;
+using sv::kDefaultWaitNs;
+using sv::map_cuda;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kNumKernels = 9;  // timing ids, see specverify_set_timing
-constexpr uint64_t kDefaultWaitNs = 2000000000ull;  // about two seconds
 
 struct TimedLaunch {
     cudaEvent_t start, stop;
@@ -63,12 +51,6 @@ struct specverify_ctx {
 };
 
 namespace {
-
-int map_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return SPECVERIFY_OK;
-    if (e == cudaErrorMemoryAllocation) return SPECVERIFY_ERR_OOM;
-    return SPECVERIFY_ERR_CUDA;
-}
 
 cudaEvent_t take_event(specverify_ctx *h) {
     if (!h->pool.empty()) {
@@ -131,7 +113,7 @@ int run_verify(specverify_ctx *h, const specverify_batch *in, bool sampling, flo
     if (in->B == 0) return SPECVERIFY_OK;  // nothing to write: outputs may be NULL
     if (!n_out || !tok_out) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
     sv::Params P = h->base;
@@ -244,10 +226,10 @@ int specverify_create(specverify_t *out, int device, int32_t max_batch, int32_t 
         max_vocab > sv::kMaxVocab)
         return SPECVERIFY_ERR_INVALID_ARG;
     if (device < 0) return SPECVERIFY_ERR_INVALID_ARG;
-    int ndev = 0;
-    if (cudaGetDeviceCount(&ndev) != cudaSuccess || device >= ndev) return SPECVERIFY_ERR_CUDA;
+    const int found = sv::check_device(device);
+    if (found != SPECVERIFY_OK) return found;
     DeviceGuard guard(device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
 
     specverify_ctx *h = new (std::nothrow) specverify_ctx();
     if (!h) return SPECVERIFY_ERR_OOM;
@@ -457,7 +439,7 @@ int specverify_verify_restricted(specverify_t h, const specverify_batch *in,
     const int64_t stages = max_rows * ((in->V * esz0 + 4095) / 4096);
     if (max_rows > INT32_MAX || stages > INT32_MAX) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const int64_t esz = in->dtype == SPECVERIFY_FP32 ? 4 : 2;
     sv::RestrictParams R = h->rbase;
@@ -495,7 +477,7 @@ int specverify_acceptance_stats(specverify_t h, const specverify_batch *in, floa
     if (in->B == 0 || in->gamma_max == 0) return SPECVERIFY_OK;
     if (!beta || !tvd) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     const int64_t esz = in->dtype == SPECVERIFY_FP32 ? 4 : 2;
     sv::FeatParams F{};
     F.rows = static_cast<const char *>(in->target_logits);
@@ -531,7 +513,7 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
         (row_stride * esz) % 16 != 0 || !entropy || (k > 0 && (!topk_prob || !topk_idx)))
         return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     // the row pass splits at most max_rows rows at a time (its pieces fit the workspace)
     sv::FeatParams F = h->fbase;
     F.stride_bytes = row_stride * esz;
@@ -566,7 +548,7 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
 int specverify_device_status(specverify_t h, void *cuda_stream, int32_t *status_out) {
     if (!h || !status_out) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     int32_t v = 0;
     cudaError_t e = cudaMemcpyAsync(&v, h->base.status, sizeof(v), cudaMemcpyDeviceToHost, s);
@@ -613,7 +595,7 @@ int specverify_get_timing(specverify_t h, int kernel, double *total_ms, int64_t 
                           int reset) {
     if (!h || kernel < 0 || kernel >= kNumKernels) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     for (auto &t : h->pending) {
         if (cudaEventSynchronize(t.stop) != cudaSuccess) return SPECVERIFY_ERR_CUDA;
         float ms = 0.0f;

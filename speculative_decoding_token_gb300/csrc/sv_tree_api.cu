@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <new>
 
+#include "sv_host.h"
 #include "sv_tree.h"
 
 struct specverify_tree_ctx {
@@ -20,28 +21,8 @@ struct specverify_tree_ctx {
 
 namespace {
 
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev) {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            changed = err == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
-
-int map_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return SPECVERIFY_OK;
-    cudaGetLastError();  // it is reported here: the program's next launch check need not see it
-    if (e == cudaErrorMemoryAllocation) return SPECVERIFY_ERR_OOM;
-    return SPECVERIFY_ERR_CUDA;
-}
+using sv::DeviceGuard;
+using sv::map_cuda;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -137,10 +118,10 @@ int specverify_tree_create(specverify_tree_t *out, int device, int32_t max_batch
     if (max_batch < 1 || max_batch > 65535 || max_moves < 0 || max_moves > ((int64_t)1 << 36) ||
         device < 0)
         return SPECVERIFY_ERR_INVALID_ARG;
-    int ndev = 0;
-    if (cudaGetDeviceCount(&ndev) != cudaSuccess || device >= ndev) return SPECVERIFY_ERR_CUDA;
+    const int found = sv::check_device(device);
+    if (found != SPECVERIFY_OK) return found;
     DeviceGuard guard(device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     specverify_tree_ctx *h = new (std::nothrow) specverify_tree_ctx();
     if (!h) return SPECVERIFY_ERR_OOM;
     h->device = device;
@@ -185,7 +166,7 @@ int specverify_tree_destroy(specverify_tree_t h) {
 int specverify_tree_status(specverify_tree_t h, void *cuda_stream, int32_t *status_out) {
     if (!h || !status_out) return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     cudaError_t e = cudaMemcpyAsync(status_out, h->status, sizeof(int32_t),
                                     cudaMemcpyDeviceToHost, s);
@@ -223,7 +204,7 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
     if (tiles * ((int64_t)tree->max_nodes * heads / 256 + cache->kv_heads) > INT32_MAX)
         return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     sv::TreeAttnParams p{};
     p.c = cache_params(cache);
     p.t = tree_params(tree);
@@ -259,7 +240,7 @@ int specverify_verify_tree(specverify_tree_t h, const specverify_tree *tree, con
     if ((rows > 0 && (!target || !aligned16(target))) || !n_accepted || !out_tokens || !path)
         return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     sv::TreeVerifyParams p{};
     p.t = tree_params(tree);
     p.target = static_cast<const char *>(target);
@@ -296,7 +277,7 @@ int specverify_tree_commit(specverify_tree_t h, const specverify_cache *cache, i
         (new_seen && overlap(new_lens, n, new_seen, n)))
         return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     sv::CommitParams p{};
     p.c = cache_params(cache);
     p.B = B;
@@ -327,7 +308,7 @@ int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cac
     if (((int64_t)cache->max_pages * cache->page_size / 128 + 4) * cache->kv_heads > INT32_MAX)
         return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     sv::AccumParams p{};
     p.c = cache_params(cache);
     p.t = tree_params(tree);
@@ -366,7 +347,7 @@ int specverify_cache_evict(specverify_tree_t h, const specverify_cache *cache, i
     const int64_t moves = budget < capacity ? std::min((int64_t)budget, capacity - budget) : 0;
     if (items > INT32_MAX || items * moves > h->max_moves) return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
-    if (guard.err != cudaSuccess) return SPECVERIFY_ERR_CUDA;
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
     sv::EvictParams p{};
     p.c = cache_params(cache);
     p.B = B;

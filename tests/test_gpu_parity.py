@@ -518,6 +518,13 @@ def test_wait_limit_times_out_cleanly_and_the_next_call_is_exact(svm):
     h.close()
 
 
+def test_a_handle_too_large_leaves_no_error_behind(svm):
+    with pytest.raises(svm.SpecVerifyError) as e:
+        svm.SpecVerify(1 << 20, 256, 256000)  # hundreds of GB
+    assert e.value.rc == svm.ERR_OOM
+    assert float(torch.ones(8, device="cuda").sum()) == 8.0  # a launch that checks for errors before it
+
+
 def test_flag_budget_over_the_run(svm):
     """Flagged decisions (inside the rounding bands) are fewer than 1e-4 of
     all decisions compared in this run."""
