@@ -687,10 +687,11 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
         base += 2 * g.n;
         if (!g.pair) turn ^= 1;
     }
-    if (!ok) {  // no product outlives the CTA
-        mma_commit(smem_u32(&M.drain), on);
-        mbar_wait_bounded(smem_u32(&M.drain), 0);
-    }
+    // No product, nor the arrival of one, outlives the CTA. Whoever reads the last ones
+    // may have given up waiting for them, also where every wait of this warp was met.
+    __syncwarp();
+    mma_commit(smem_u32(&M.drain), on);
+    mbar_wait_bounded(smem_u32(&M.drain), 0);
 }
 
 // ---------------------------------------------------------------------------
