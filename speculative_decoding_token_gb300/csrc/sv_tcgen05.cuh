@@ -11,18 +11,22 @@
 
 namespace sv {
 
-// A wait that gives up after about two seconds, or once another of the CTA has
-// (`abort`, in shared memory): the roles then run through their work without
-// waiting, and the status says so.
+// A whole warp's wait, the same outcome for every lane (what follows a wait are
+// instructions of whole warps). It gives up after about two seconds, or once
+// another of the CTA has (`abort`, in shared memory), and the status says so. A
+// warp that gave up touches nothing that is shared and arrives at no barrier of
+// this kind any more: whoever needs it gives up in turn, and nobody takes for
+// done what was not.
 __device__ __forceinline__ bool wait_on(uint64_t &bar, uint32_t parity, int32_t &abort,
                                         int32_t *status) {
+    constexpr uint32_t all = 0xffffffffu;
     const uint32_t at = smem_u32(&bar);
-    if (mbar_try_wait(at, parity)) return true;
+    if (__all_sync(all, mbar_try_wait(at, parity))) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
-        if (mbar_try_wait(at, parity)) return true;
-        if (*(volatile int32_t *)&abort) return false;
-        if (global_ns() - t0 > 2000000000ull) break;
+        if (__all_sync(all, mbar_try_wait(at, parity))) return true;
+        if (__any_sync(all, *(volatile int32_t *)&abort)) return false;
+        if (__any_sync(all, global_ns() - t0 > 2000000000ull)) break;
     }
     *(volatile int32_t *)&abort = 1;
     atomicOr(status, SPECVERIFY_STATUS_TIMEOUT);

@@ -300,8 +300,16 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
         const bool mine = r_item < g.rows;  // (rows past the item's hold what the tile held before)
         float m_ref = ninf, l = 0.0f;
         bool fresh = true;
-        for (int j = pair ? 0 : w; j < n; j += pair ? 1 : 2) {
-            wait_on(M, M.s_full[w], s_phase, P.status);
+        int j = pair ? 0 : w;
+        // A warp that gave up only keeps to the barriers of the others, to the next segment's start.
+        const auto leave = [&] {
+            for (; warp_on && j < n; j += pair ? 1 : 2)
+                if (pair_any(pair_bar, false)) pair_any(pair_bar, false);
+            for (int i = pair ? 1 : 3; i > 0; --i) soft_sync();
+            soft_all(false);
+        };
+        for (; j < n; j += pair ? 1 : 2) {
+            if (!wait_on(M, M.s_full[w], s_phase, P.status)) return leave();
             s_phase ^= 1;
             tc_fence_after();
             const int shift = ahead + j * kTile;  // column c is node c + shift, a token before 0
@@ -310,7 +318,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                 // a slot past the tree, or a node's inf or NaN: 0 in the products
                 // (the latter are added where they are seen, below)
                 const uint32_t use = base + v_at(g, j);
-                wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status);
+                if (!wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status)) return leave();
                 char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
                 const int r0 = max(0, -shift), gone = g.s.T - shift;
                 for (int i = tid & 255; i < (kTile - r0) * (D / 8); i += 256) {
@@ -429,8 +437,9 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
         }
         // the item's sums
         const bool used1 = pair || n > 1;
-        if (!pair || w == 0) wait_on(M, M.o_full[0], o_phase & 1, P.status);
-        if (used1 && (!pair || w == 1)) wait_on(M, M.o_full[1], o_phase >> 1, P.status);
+        if ((!pair || w == 0) && !wait_on(M, M.o_full[0], o_phase & 1, P.status)) return leave();
+        if (used1 && (!pair || w == 1) && !wait_on(M, M.o_full[1], o_phase >> 1, P.status))
+            return leave();
         o_phase ^= used1 ? 3 : 1;
         tc_fence_after();
         base += 2 * n;
@@ -562,7 +571,8 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         // Q rows into their tiles, 16-byte chunks swizzled within 8 rows
         for (int i = 0; i < (g.pair ? 2 : 1); ++i) {
             const int x = g.pair ? i : turn;
-            ok = wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status) && ok;
+            ok = ok && wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status);
+            if (!ok) break;
             const int r_first = i * kTile, r_count = min(kTile, g.rows - r_first);
             constexpr int R = kScoutThreads / C;  // rows at a time
             const int c = tid % C, dn = R / P.G, dh = R - dn * P.G;
@@ -589,7 +599,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         }
         if (!g.pair) turn ^= 1;
         // pages and parents
-        ok = wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status) && ok;
+        ok = ok && wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status);
         if (!scouts_all(ok)) break;
         Scouted &sc = M.seg[seg & 1];
         int bad = page_ok ? 0 : SPECVERIFY_STATUS_BAD_CACHE;
@@ -689,7 +699,6 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
     }
     // No product, nor the arrival of one, outlives the CTA. Whoever reads the last ones
     // may have given up waiting for them, also where every wait of this warp was met.
-    __syncwarp();
     mma_commit(smem_u32(&M.drain), on);
     mbar_wait_bounded(smem_u32(&M.drain), 0);
 }
@@ -718,11 +727,8 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
             ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
             // the first queries come ahead of a ring's worth of keys, which would
             // keep them in the memory's queue for microseconds
-            if (use == 2) ok = wait_on(M, M.begun, 0, P.status) && ok;
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                return;
-            }
+            if (use == 2) ok = ok && wait_on(M, M.begun, 0, P.status);
+            if (!ok) return;
             ++use;
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
             if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box * D * 2);

@@ -141,10 +141,10 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
                 const int s = (g.tile0 + j) * kTile + lane_row;
                 const int64_t page = s <= last ? page_of(P.c, g.b, s) : -1;
                 if (!ready) {  // the scouts' lse and verdict
-                    wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
+                    if (!wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status)) return;
                     ready = true;
                 }
-                wait_on(M, M.s_full[w], phase, P.status);
+                if (!wait_on(M, M.s_full[w], phase, P.status)) return;
                 phase ^= 1;
                 tc_fence_after();
                 // a slot that a node wrote is seen by the later ones only
@@ -177,7 +177,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
                                         (int64_t)place_of(P.c, s).token * P.c.mts],
                               (sum[0] + sum[1]) + (sum[2] + sum[3]));
             }
-            if (!ready) wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
+            if (!ready && !wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status)) return;
             mbar_arrive(smem_u32(&M.q_empty[chunk & 1]));  // its lse is not read again
         }
         first += g.n;
@@ -219,7 +219,6 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
     }
     // No product, nor the arrival of one, outlives the CTA. Whoever reads the last ones
     // may have given up waiting for them, also where every wait of this warp was met.
-    __syncwarp();
     mma_commit(smem_u32(&M.drain), on);
     mbar_wait_bounded(smem_u32(&M.drain), 0);
 }
@@ -245,7 +244,6 @@ __device__ void load_role(const AccumParams &P, const CUtensorMap *mk, Misc &M, 
                 const int next = page_id(j + 1);
                 const uint32_t slot = use % Sh::kSlots, bar = smem_u32(&M.full[slot]);
                 ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++use;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
@@ -275,6 +273,7 @@ __device__ void scout_role(const AccumParams &P, Misc &M, char *smem, Walk walk)
     const int tid = threadIdx.x - (kMassThreads - kScoutThreads), c = tid % C;
     uint32_t chunk = 0;
     Segment g;
+    bool ok = true;  // (the two warps meet at every segment, also one that gave up)
     while (walk.next(P, g)) {
         const int32_t *path = P.path + (int64_t)g.b * P.t.max_nodes;
         int bad = 0;
@@ -299,7 +298,8 @@ __device__ void scout_role(const AccumParams &P, Misc &M, char *smem, Walk walk)
             : "memory");
         for (int q = 0; q < g.chunks; ++q, ++chunk) {
             const int x = chunk & 1, rows = min(kRows, g.rows - q * kRows);
-            wait_on(M, M.q_empty[x], (chunk >> 1 & 1) ^ 1, P.status);
+            ok = ok && wait_on(M, M.q_empty[x], (chunk >> 1 & 1) ^ 1, P.status);
+            if (!ok) break;
             const uint32_t tile = smem_u32(smem) + x * Sh::kTileBytes + (c >> 3) * Sh::kPanel;
             // a bad path names no rows: its chunk is left as it is and not added
             const int dn = R / P.G, dh = R - dn * P.G, r0 = q * kRows + tid / C;
