@@ -314,7 +314,7 @@ int specverify_verify_noalloc(const specverify_batch *in, float temperature, uin
  * each call), the others are unaffected, and the sticky status word says so.
  * They launch as programmatic dependents of the kernel before them on the
  * stream and wait for it before they touch memory. Waits inside the kernels
- * are bounded (about two seconds): one that runs out sets
+ * are bounded (specverify_tree_set_wait_limit): one that runs out sets
  * SPECVERIFY_STATUS_TIMEOUT and leaves that call's outputs undefined. Results
  * are the same from run to run on one GPU unless a call says otherwise. Rows
  * of different sequences do not overlap, and outputs do not overlap inputs
@@ -388,6 +388,15 @@ int specverify_tree_destroy(specverify_tree_t h);
 int specverify_tree_status(specverify_tree_t h, void *cuda_stream, int32_t *status_out);
 
 int specverify_tree_workspace_bytes(specverify_tree_t h, size_t *out);
+
+/* Bound, in nanoseconds of GPU wall time, on every wait of the handle's kernels
+ * for another warp or CTA, of the calls that follow; 0 restores the default of
+ * about two seconds. A wait that runs out ends the call early with
+ * SPECVERIFY_STATUS_TIMEOUT; the handle and its next calls are good. The waits
+ * for copies and products in flight before a kernel exits keep their fixed bound.
+ * A limit below a call's duration makes calls time out: this exists for
+ * failure-detection tests and watchdog tuning, as specverify_set_wait_limit. */
+int specverify_tree_set_wait_limit(specverify_tree_t h, uint64_t ns);
 
 /* Attention of the tree's nodes over the cache. For node j, query head h and
  * its key head h / (heads / kv_heads):

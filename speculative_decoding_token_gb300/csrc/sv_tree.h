@@ -60,6 +60,7 @@ struct TreeAttnParams {
     int32_t box;              // tokens of one tiled copy: divides the page size and a tile
     int32_t blocks;           // blocks of 256 rows that a tree can have
     int32_t *status;
+    uint64_t wait_ns;         // bound of a wait inside the kernel
     // workspace: the pieces of rows whose slots were split over CTAs
     float *piece_o;           // [CTAs, 2, 256, d]
     float2 *piece_ml;         // [CTAs, 2, 256]: reference maximum (log2 scale), sum
@@ -80,6 +81,7 @@ struct TreeVerifyParams {
     int64_t stride_bytes, V, rows;
     int32_t *n_out, *tok_out, *path_out;
     int32_t *status;
+    uint64_t wait_ns;
 };
 
 struct CommitParams {
@@ -102,6 +104,7 @@ struct AccumParams {
     float scale_log2;
     int32_t box;              // as of the attention
     int32_t *status;
+    uint64_t wait_ns;
 };
 
 struct EvictParams {

@@ -12,6 +12,7 @@ struct specverify_tree_ctx {
     int num_sms = 0;
     int32_t max_batch = 0;
     int64_t max_moves = 0;
+    uint64_t wait_ns = sv::kDefaultWaitNs;
     void *ws = nullptr;
     size_t ws_bytes = 0;
     int32_t *status = nullptr;
@@ -181,6 +182,12 @@ int specverify_tree_workspace_bytes(specverify_tree_t h, size_t *out) {
     return SPECVERIFY_OK;
 }
 
+int specverify_tree_set_wait_limit(specverify_tree_t h, uint64_t ns) {
+    if (!h) return SPECVERIFY_ERR_INVALID_ARG;
+    h->wait_ns = ns == 0 ? sv::kDefaultWaitNs : ns;
+    return SPECVERIFY_OK;
+}
+
 int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache,
                               const specverify_tree *tree, const int32_t *lens, const void *q,
                               int64_t rows, int32_t heads, int64_t q_row_stride,
@@ -221,6 +228,7 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
     p.G = heads / cache->kv_heads;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
+    p.wait_ns = h->wait_ns;
     sv::attn_place(p, h->attn, h->num_sms);
     return map_cuda(sv::launch_tree_attention(p, h->num_sms,
                                               static_cast<cudaStream_t>(cuda_stream)));
@@ -251,6 +259,7 @@ int specverify_verify_tree(specverify_tree_t h, const specverify_tree *tree, con
     p.tok_out = out_tokens;
     p.path_out = path;
     p.status = h->status;
+    p.wait_ns = h->wait_ns;
     return map_cuda(sv::launch_tree_verify(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
@@ -324,6 +333,7 @@ int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cac
     p.G = heads / cache->kv_heads;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = h->status;
+    p.wait_ns = h->wait_ns;
     return map_cuda(sv::launch_accumulate(p, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 

@@ -182,8 +182,8 @@ __device__ __forceinline__ uint32_t v_at(const Segment &g, int j) {
     return g.pair ? 2 * j + 1 : min(2 * j + 2, 2 * g.n - 1);
 }
 
-__device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, int32_t *status) {
-    return ::sv::wait_on(bar, parity, M.abort, status);
+__device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, const TreeAttnParams &P) {
+    return ::sv::wait_on(bar, parity, M.abort, P.status, P.wait_ns);
 }
 
 // Barrier of the two softmax groups.
@@ -286,7 +286,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
     for (;; ++seg) {
         Scouted &sc = M.seg[seg & 1];
         // (the barrier: all have read the last segment's O and x)
-        if (!soft_all(wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P.status))) break;
+        if (!soft_all(wait_on(M, M.seg_full[seg & 1], seg >> 1 & 1, P))) break;
         const Segment &g = sc.g;
         const int n = g.n;
         if (n == 0) break;
@@ -309,7 +309,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
             soft_all(false);
         };
         for (; j < n; j += pair ? 1 : 2) {
-            if (!wait_on(M, M.s_full[w], s_phase, P.status)) return leave();
+            if (!wait_on(M, M.s_full[w], s_phase, P)) return leave();
             s_phase ^= 1;
             tc_fence_after();
             const int shift = ahead + j * kTile;  // column c is node c + shift, a token before 0
@@ -318,7 +318,7 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
                 // a slot past the tree, or a node's inf or NaN: 0 in the products
                 // (the latter are added where they are seen, below)
                 const uint32_t use = base + v_at(g, j);
-                if (!wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P.status)) return leave();
+                if (!wait_on(M, M.full[use % Sh::kSlots], use / Sh::kSlots & 1, P)) return leave();
                 char *v = smem + Sh::kRing + use % Sh::kSlots * Sh::kTileBytes;
                 const int r0 = max(0, -shift), gone = g.s.T - shift;
                 for (int i = tid & 255; i < (kTile - r0) * (D / 8); i += 256) {
@@ -437,8 +437,8 @@ __device__ void softmax_role(const TreeAttnParams &P, Misc &M, char *smem, uint3
         }
         // the item's sums
         const bool used1 = pair || n > 1;
-        if ((!pair || w == 0) && !wait_on(M, M.o_full[0], o_phase & 1, P.status)) return leave();
-        if (used1 && (!pair || w == 1) && !wait_on(M, M.o_full[1], o_phase >> 1, P.status))
+        if ((!pair || w == 0) && !wait_on(M, M.o_full[0], o_phase & 1, P)) return leave();
+        if (used1 && (!pair || w == 1) && !wait_on(M, M.o_full[1], o_phase >> 1, P))
             return leave();
         o_phase ^= used1 ? 3 : 1;
         tc_fence_after();
@@ -550,7 +550,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
     Segment g;
     for (;; ++seg) {
         if (!walk.next(P, g)) {
-            if (wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status)) {
+            if (wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P)) {
                 if (tid == 0) M.seg[seg & 1].g.n = 0;
                 mbar_arrive(smem_u32(&M.seg_full[seg & 1]));
             }
@@ -571,7 +571,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         // Q rows into their tiles, 16-byte chunks swizzled within 8 rows
         for (int i = 0; i < (g.pair ? 2 : 1); ++i) {
             const int x = g.pair ? i : turn;
-            ok = ok && wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P.status);
+            ok = ok && wait_on(M, M.q_empty[x], (uses[x]++ & 1) ^ 1, P);
             if (!ok) break;
             const int r_first = i * kTile, r_count = min(kTile, g.rows - r_first);
             constexpr int R = kScoutThreads / C;  // rows at a time
@@ -599,7 +599,7 @@ __device__ void scout_role(const TreeAttnParams &P, Misc &M, char *smem, Walk wa
         }
         if (!g.pair) turn ^= 1;
         // pages and parents
-        ok = ok && wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P.status);
+        ok = ok && wait_on(M, M.seg_empty[seg & 1], (seg >> 1 & 1) ^ 1, P);
         if (!scouts_all(ok)) break;
         Scouted &sc = M.seg[seg & 1];
         int bad = page_ok ? 0 : SPECVERIFY_STATUS_BAD_CACHE;
@@ -653,8 +653,8 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             const int w = t & 1;
             const uint32_t slot = slot_k;
             const int x = g.pair ? w : turn;
-            if (t == 0 || (g.pair && t == 1)) ok = wait_on(M, M.q_full[x], uses[x]++ & 1, P.status);
-            if (!g.pair || w == 0) ok = ok && wait_on(M, M.full[slot], phase_k, P.status);
+            if (t == 0 || (g.pair && t == 1)) ok = wait_on(M, M.q_full[x], uses[x]++ & 1, P);
+            if (!g.pair || w == 0) ok = ok && wait_on(M, M.full[slot], phase_k, P);
             if (!ok) return;
             tc_fence_after();
             const uint32_t a = q0 + x * Sh::kTileBytes, b = ring + slot * Sh::kTileBytes;
@@ -676,11 +676,11 @@ __device__ void mma_role(const TreeAttnParams &P, Misc &M, char *smem, Walk walk
             const int j = g.pair ? t >> 1 : t, w = t & 1;
             const uint32_t use = base + v_at(g, j), slot = use % Sh::kSlots;
             find_k(t + 2);
-            if (!g.pair || w == 0) ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P.status);
+            if (!g.pair || w == 0) ok = wait_on(M, M.full[slot], use / Sh::kSlots & 1, P);
             const uint32_t b = ring + slot * Sh::kTileBytes;
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                ok = ok && wait_on(M, M.p_full[w][part], p_phase[w], P.status);
+                ok = ok && wait_on(M, M.p_full[w][part], p_phase[w], P);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -724,10 +724,10 @@ __device__ void load_role(const TreeAttnParams &P, const CUtensorMap *mk, const 
         };
         const auto copy = [&](const CUtensorMap *map, int j, int page) {
             const uint32_t slot = use % Sh::kSlots, bar = smem_u32(&M.full[slot]);
-            ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
+            ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P);
             // the first queries come ahead of a ring's worth of keys, which would
             // keep them in the memory's queue for microseconds
-            if (use == 2) ok = ok && wait_on(M, M.begun, 0, P.status);
+            if (use == 2) ok = ok && wait_on(M, M.begun, 0, P);
             if (!ok) return;
             ++use;
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));

@@ -119,8 +119,8 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, int32_t *status) {
-    return ::sv::wait_on(bar, parity, M.abort, status);
+__device__ __forceinline__ bool wait_on(Misc &M, uint64_t &bar, uint32_t parity, const AccumParams &P) {
+    return ::sv::wait_on(bar, parity, M.abort, P.status, P.wait_ns);
 }
 
 // ---------------------------------------------------------------------------
@@ -141,10 +141,10 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
                 const int s = (g.tile0 + j) * kTile + lane_row;
                 const int64_t page = s <= last ? page_of(P.c, g.b, s) : -1;
                 if (!ready) {  // the scouts' lse and verdict
-                    if (!wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status)) return;
+                    if (!wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P)) return;
                     ready = true;
                 }
-                if (!wait_on(M, M.s_full[w], phase, P.status)) return;
+                if (!wait_on(M, M.s_full[w], phase, P)) return;
                 phase ^= 1;
                 tc_fence_after();
                 // a slot that a node wrote is seen by the later ones only
@@ -177,7 +177,7 @@ __device__ void sum_role(const AccumParams &P, Misc &M, Walk walk, uint32_t tmem
                                         (int64_t)place_of(P.c, s).token * P.c.mts],
                               (sum[0] + sum[1]) + (sum[2] + sum[3]));
             }
-            if (!ready && !wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status)) return;
+            if (!ready && !wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P)) return;
             mbar_arrive(smem_u32(&M.q_empty[chunk & 1]));  // its lse is not read again
         }
         first += g.n;
@@ -196,12 +196,12 @@ __device__ void mma_role(const AccumParams &P, Misc &M, char *smem, Walk walk, u
         for (int q = 0; ok && q < g.chunks; ++q, ++chunk) {
             const int rows = min(kRows, g.rows - q * kRows);
             const uint32_t desc = mma_desc(FP16, false, kTile, (rows + 15) / 16 * 16);
-            ok = wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P.status);
+            ok = wait_on(M, M.q_full[chunk & 1], chunk >> 1 & 1, P);
             const uint32_t b = q0 + (chunk & 1) * Sh::kTileBytes;
             for (int j = 0; ok && j < g.n; ++j, ++turn) {
                 const uint32_t slot = turn % Sh::kSlots, w = (first + j) & 1;
-                ok = wait_on(M, M.full[slot], turn / Sh::kSlots & 1, P.status) &&
-                     wait_on(M, M.s_empty[w], (uses[w]++ & 1) ^ 1, P.status);
+                ok = wait_on(M, M.full[slot], turn / Sh::kSlots & 1, P) &&
+                     wait_on(M, M.s_empty[w], (uses[w]++ & 1) ^ 1, P);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t a = ring + slot * Sh::kTileBytes;
@@ -243,7 +243,7 @@ __device__ void load_role(const AccumParams &P, const CUtensorMap *mk, Misc &M, 
             for (int j = 0; ok && j < g.n; ++j) {
                 const int next = page_id(j + 1);
                 const uint32_t slot = use % Sh::kSlots, bar = smem_u32(&M.full[slot]);
-                ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P.status);
+                ok = wait_on(M, M.empty[slot], (use / Sh::kSlots & 1) ^ 1, P);
                 if (!ok) break;
                 ++use;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
@@ -298,7 +298,7 @@ __device__ void scout_role(const AccumParams &P, Misc &M, char *smem, Walk walk)
             : "memory");
         for (int q = 0; q < g.chunks; ++q, ++chunk) {
             const int x = chunk & 1, rows = min(kRows, g.rows - q * kRows);
-            ok = ok && wait_on(M, M.q_empty[x], (chunk >> 1 & 1) ^ 1, P.status);
+            ok = ok && wait_on(M, M.q_empty[x], (chunk >> 1 & 1) ^ 1, P);
             if (!ok) break;
             const uint32_t tile = smem_u32(smem) + x * Sh::kTileBytes + (c >> 3) * Sh::kPanel;
             // a bad path names no rows: its chunk is left as it is and not added

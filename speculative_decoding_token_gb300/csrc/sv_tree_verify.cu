@@ -46,8 +46,8 @@ __device__ __forceinline__ void send_u2(uint32_t addr, uint32_t bar, uint32_t x,
         : "memory");
 }
 
-// A wait for what other CTAs of the cluster send; gives up after about two seconds.
-__device__ __forceinline__ bool wait_sent(uint32_t bar, uint32_t parity) {
+// A wait for what other CTAs of the cluster send; gives up after `limit` nanoseconds.
+__device__ __forceinline__ bool wait_sent(uint32_t bar, uint32_t parity, uint64_t limit) {
     const uint64_t t0 = global_ns();
     for (;;) {
         uint32_t ok;
@@ -59,7 +59,7 @@ __device__ __forceinline__ bool wait_sent(uint32_t bar, uint32_t parity) {
             : "r"(bar), "r"(parity)
             : "memory");
         if (ok) return true;
-        if (global_ns() - t0 > 2000000000ull) return false;
+        if (global_ns() - t0 > limit) return false;
     }
 }
 
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kVtThreads, 3) tree_verify_kernel(const __grid
             send_u2(cluster_addr(&s_slice[n & 1][rank * kVtWarps + warp], (uint32_t)lane),
                     cluster_addr(&s_bar[n & 1], (uint32_t)lane), key, idx);
         // (a warp leaves as a whole: its reductions are of all lanes)
-        late = __any_sync(0xffffffffu, !wait_sent(bar, n >> 1 & 1));
+        late = __any_sync(0xffffffffu, !wait_sent(bar, n >> 1 & 1, P.wait_ns));
         if (late) break;
         static_assert(kVtCtas * kVtWarps == 64, "two candidates a lane");
         const uint2 a = s_slice[n & 1][lane], z = s_slice[n & 1][lane + 32];

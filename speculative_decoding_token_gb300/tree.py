@@ -55,13 +55,14 @@ def bind(lib):
     lib.specverify_tree_destroy.argtypes = [vp]
     lib.specverify_tree_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
     lib.specverify_tree_workspace_bytes.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.specverify_tree_set_wait_limit.argtypes = [vp, ctypes.c_uint64]
     lib.specverify_tree_attention.argtypes = [vp, vp, vp, vp, vp, i64, i32, i64, i64, f32, vp, i64, i64, vp, vp]
     lib.specverify_verify_tree.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, vp]
     lib.specverify_tree_commit.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
     lib.specverify_cache_accumulate.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, vp, f32, vp]
     lib.specverify_cache_evict.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
-    for name in ("tree_create", "tree_destroy", "tree_status", "tree_workspace_bytes", "tree_attention", "verify_tree",
-                 "tree_commit", "cache_accumulate", "cache_evict"):
+    for name in ("tree_create", "tree_destroy", "tree_status", "tree_workspace_bytes", "tree_set_wait_limit",
+                 "tree_attention", "verify_tree", "tree_commit", "cache_accumulate", "cache_evict"):
         getattr(lib, "specverify_" + name).restype = ctypes.c_int
 
 
@@ -317,6 +318,11 @@ class SpecTree:
         v = ctypes.c_int32()
         self.check(self.lib.specverify_tree_status(self.h, self._stream(stream), ctypes.byref(v)), "specverify_tree_status")
         return v.value
+
+    def set_wait_limit(self, ns: int):
+        """Bounds every wait inside the kernels of the calls that follow, in nanoseconds; 0: the default, about two
+        seconds. A wait that runs out ends its call with the status bit ``timeout`` and its outputs undefined."""
+        self.check(self.lib.specverify_tree_set_wait_limit(self.h, int(ns)), "specverify_tree_set_wait_limit")
 
     def workspace_bytes(self) -> int:
         v = ctypes.c_size_t()

@@ -974,3 +974,85 @@ def test_accumulate_of_many_rows_repeats_bit_for_bit(st, lens, nodes, G, d):
         assert torch.equal(bt.dmass, first)
     want, tol = tu.accumulate(bt, mass[0], lse.cpu(), n.tolist(), path.cpu().numpy(), d ** -0.5)
     near(first, want, tol)
+
+
+# ---------------------------------------------------------------------------
+# waits that run out
+
+def with_short_waits(h, call, check):
+    """Calls whose every wait gives up after a microsecond, until one has timed out: each returns and says so, and the next
+    call with the default limit is right. Whether one timed out."""
+    import speculative_decoding_token_gb300 as sv
+    cold = torch.zeros(1 << 26, device="cuda")  # more than L2 holds
+    for i in range(100):
+        cold.add_(1)
+        h.set_wait_limit(1)
+        call()
+        status = h.device_status()
+        assert status in (0, sv.STATUS_BITS["timeout"])
+        h.set_wait_limit(0)
+        if status or i % 20 == 0:
+            check()
+            assert h.device_status() == 0
+        if status:
+            return True
+    return False
+
+
+def test_attention_whose_waits_run_out():
+    import speculative_decoding_token_gb300 as sv
+    h, late = sv.SpecTree(4), 0
+    for lens, nodes, heads, d in (([20000, 700, 90], [3, 30, 1], 4, 128), ([4000, 9000], [64, 40], 16, 64)):
+        bt = tu.Batch(lens, nodes, heads, 2, d, 16, BF16, seed=d, poison=False)
+        late += with_short_waits(h, lambda: run_attention(h, bt), lambda: check_attention(h, bt))
+    assert late
+    h.close()
+
+
+def test_accumulate_whose_waits_run_out():
+    import speculative_decoding_token_gb300 as sv
+    h, late = sv.SpecTree(4), 0
+    for lens, nodes, G, d in (([9000, 700, 90], [30, 3, 1], 4, 128), ([400, 3000], [64, 40], 8, 64)):
+        bt = tu.Batch(lens, nodes, 2 * G, 2, d, 16, BF16, seed=d, poison=False)
+        n, path = long_paths(bt, nodes)
+        mass = torch.rand(bt.k.shape[:-1], generator=bt.gen)
+        bt.upload(mass=mass)
+        lse = torch.rand(bt.rows, bt.heads, generator=bt.gen) * 3 + 4
+        want, tol = tu.accumulate(bt, mass[0], lse, n.tolist(), path.cpu().numpy(), d ** -0.5)
+        dlse = lse.cuda()
+
+        def call():
+            h.accumulate(bt.dq, dlse, bt.cache, bt.tree, bt.dlens, n, path)
+
+        def check():
+            bt.dmass.copy_(mass[0])
+            call()
+            near(bt.dmass, want, tol)
+
+        late += with_short_waits(h, call, check)
+    assert late
+    h.close()
+
+
+def test_verify_whose_waits_run_out():
+    """A sequence whose waits ran out has no answer; one that was done in time has the right one."""
+    import speculative_decoding_token_gb300 as sv
+    case = make_verify(np.random.default_rng(8), 40, 48, 50257, BF16)
+    want = tu.verify(case[2], case[0], case[3], case[1], case[4])
+    h, late = sv.SpecTree(40), 0
+
+    def call():
+        n, tokens, path = run_verify(h, *case)
+        gone = n == -1
+        assert (tokens[gone] == -1).all() and (path[gone] == -1).all()
+        for g, w in zip((n, tokens, path), want):
+            assert np.array_equal(g[~gone], w[~gone])
+
+    def check():
+        for g, w in zip(run_verify(h, *case), want):
+            assert np.array_equal(g, w)
+
+    for _ in range(5):
+        late += with_short_waits(h, call, check)
+    assert late
+    h.close()
