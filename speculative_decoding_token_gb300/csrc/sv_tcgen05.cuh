@@ -8,6 +8,7 @@
 #include <cuda.h>
 
 #include "sv_stream.cuh"
+#include "sv_tree.h"
 
 namespace sv {
 
@@ -205,8 +206,7 @@ __device__ __forceinline__ void mbar_fence_init() {
 }
 
 // --- host: maps of a cache's keys or values --------------------------------------
-struct CacheParams;
-constexpr int kTile = 128;  // slots of a tile, and its rows of 128 bytes
+constexpr int kTile = kTileSlots;  // of a tile, and its rows of 128 bytes
 
 // Tokens of one copy: the largest power of two that divides the page size and a tile.
 int cache_box(int page);

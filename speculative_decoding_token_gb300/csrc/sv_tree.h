@@ -11,6 +11,18 @@ namespace sv {
 
 constexpr int kMaxNodes = SPECVERIFY_MAX_NODES;
 constexpr int kMaskWords = kMaxNodes / 32;
+constexpr int kTileSlots = 128;  // slots of a tile of keys
+
+// An item's place on the work line of attention or accumulation starts with that
+// many units that are no tiles (what a start costs: see the kernels).
+constexpr int kAttnHead = 6, kMassHead = 1;
+
+// Whether the kernels' 31-bit counts hold: units of a sequence's key heads on the
+// line, and rows (nodes times the heads of a key head) of an item.
+inline bool line_fits(int64_t slots, int64_t kv_heads, int head, int64_t nodes, int64_t group) {
+    return ((slots + kTileSlots - 1) / kTileSlots + head) * kv_heads <= INT32_MAX &&
+           nodes * group <= INT32_MAX - 2 * kTileSlots;
+}
 
 // A paged cache, strides in bytes.
 struct CacheParams {

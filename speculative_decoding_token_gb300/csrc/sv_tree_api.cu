@@ -206,9 +206,8 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
         return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
     if (!lens) return SPECVERIFY_ERR_INVALID_ARG;
-    // one sequence's share of the work line is counted in 31 bits
-    const int64_t tiles = (int64_t)cache->max_pages * cache->page_size / 128 + 4;
-    if (tiles * ((int64_t)tree->max_nodes * heads / 256 + cache->kv_heads) > INT32_MAX)
+    if (!sv::line_fits((int64_t)cache->max_pages * cache->page_size, cache->kv_heads, sv::kAttnHead,
+                       tree->max_nodes, heads / cache->kv_heads))
         return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
@@ -314,7 +313,8 @@ int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cac
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
     if (!lens || !n_accepted || !path || !lse || !cache->mass) return SPECVERIFY_ERR_INVALID_ARG;
-    if (((int64_t)cache->max_pages * cache->page_size / 128 + 4) * cache->kv_heads > INT32_MAX)
+    if (!sv::line_fits((int64_t)cache->max_pages * cache->page_size, cache->kv_heads, sv::kMassHead,
+                       tree->max_nodes, heads / cache->kv_heads))
         return SPECVERIFY_ERR_TOO_LARGE;
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return map_cuda(guard.err);

@@ -71,7 +71,7 @@ static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared
 // its start and end cost beside its tiles (queries, sums, the output).
 // Six measured best over ragged batches (B = 16, 300 to 8000 tokens: 57.8 us;
 // four 58.3, two 59.8, one 63.0).
-constexpr int kHead = 6;
+constexpr int kHead = kAttnHead;
 
 // What sequence b contributes to the line; 0 tiles: idle or bad.
 struct Seq {

@@ -29,7 +29,7 @@ constexpr int kMassThreads = 384;
 constexpr int kGroupThreads = 128;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kScoutThreads = 64;
 constexpr uint32_t kCols = 2 * kRows;      // tensor memory: S of both groups
-constexpr int kHead = 1;                   // units of an item's start on the line (see below)
+constexpr int kHead = kMassHead;           // units of an item's start on the line (see below)
 
 template <int D>
 struct Shape {

@@ -93,3 +93,79 @@ def test_kept_slots_on_worked_cases():
     assert tu.keep_slots(mass, pos, 6, 3, 1, 1).tolist() == [0, 5, 2]  # first and last position stay, then the lower tie
     mass[0] = np.nan
     assert set(tu.keep_slots(mass, pos, 6, 2, 0, 0).tolist()) == {2, 3}
+
+
+# ---------------------------------------------------------------------------
+# checks ahead of the device: a handle whose device does not exist, so that a call that passes them ends there
+
+NO_DEVICE, TOO_LARGE, INVALID = -2, -6, -1
+
+
+class FakeHandle(ctypes.Structure):
+    """The first members of the handle, as the library lays them out."""
+    _fields_ = [("device", ctypes.c_int), ("num_sms", ctypes.c_int), ("max_batch", ctypes.c_int32),
+                ("max_moves", ctypes.c_int64), ("rest", ctypes.c_char * 256)]
+
+
+class HostCalls:
+    """The calls with addresses that are never read: buffers far apart, of a cache of `layers` layers, B = 1."""
+
+    def __init__(self, lib, *, layers=1, pages=4, kv_heads=2, page=16, d=64, max_pages=4, nodes=4):
+        from speculative_decoding_token_gb300 import tree
+        self.lib, self.handle = lib, FakeHandle(device=10 ** 6, num_sms=152, max_batch=4, max_moves=1 << 30)
+        self.h = ctypes.byref(self.handle)
+        token, head = d, page * d
+        self.cache = tree.SpecverifyCache(
+            dtype=1, layers=layers, num_pages=pages, page_size=page, kv_heads=kv_heads, head_dim=d, k=1 << 44, v=1 << 45,
+            layer_stride=pages * kv_heads * head if layers > 1 else 0, page_stride=kv_heads * head, head_stride=head, token_stride=token,
+            mass=1 << 42, pos=1 << 43, mass_layer_stride=pages * kv_heads * page, mass_page_stride=kv_heads * page,
+            mass_head_stride=page, mass_token_stride=1, page_table=4096, table_stride=max_pages, max_pages=max_pages)
+        self.tree = tree.SpecverifyTree(B=1, max_nodes=nodes, row_off=4096, nodes=4096, parent=4096, tokens=4096)
+
+    def attention(self, heads, rows=4, q_strides=None, out_strides=None, q=1 << 40, out=1 << 41, lse=1 << 39):
+        d = self.cache.head_dim
+        q_strides, out_strides = q_strides or (heads * d, d), out_strides or (heads * d, d)
+        return self.lib.specverify_tree_attention(self.h, ctypes.byref(self.cache), ctypes.byref(self.tree), 4096, q, rows,
+                                                  heads, *q_strides, 0.125, out, *out_strides, lse, None)
+
+    def accumulate(self, heads, rows=4):
+        d = self.cache.head_dim
+        return self.lib.specverify_cache_accumulate(self.h, ctypes.byref(self.cache), ctypes.byref(self.tree), 4096, 4096,
+                                                    4096, 1 << 40, rows, heads, heads * d, d, 1 << 41, 0.125, None)
+
+    def commit(self):
+        return self.lib.specverify_tree_commit(self.h, ctypes.byref(self.cache), 1, 4, 4096, 8192, 12288, 16384, 20480,
+                                               24576, None)
+
+    def evict(self, mass_out=None, pos_out=None):
+        return self.lib.specverify_cache_evict(self.h, ctypes.byref(self.cache), 1, 4096, 8192, 8, 0, 0,
+                                               mass_out or self.cache.mass, pos_out or self.cache.pos, 12288, None)
+
+
+def test_plain_calls_pass_the_host_checks(lib):
+    c = HostCalls(lib, layers=1)
+    assert [c.attention(4), c.accumulate(4), c.commit(), c.evict()] == [NO_DEVICE] * 4
+    c = HostCalls(lib, layers=3)
+    assert [c.commit(), c.evict()] == [NO_DEVICE] * 2
+
+
+def test_work_that_does_not_fit_31_bits_is_refused(lib):
+    """The kernels count a sequence's tiles, and what the start of each key head weighs beside them, in 31 bits: six units
+    for the attention, one for the accumulation."""
+    most = 2 ** 31 - 1
+    for head, call in ((6, "attention"), (1, "accumulate")):
+        for slots, tiles in ((128, 1), (136, 2), (8, 1), (128 * 40, 40)):
+            fit = most // (tiles + head)
+            if fit * 8 * 64 > 2 ** 38:  # more heads than a page stride can span
+                continue
+            for kv_heads, want in ((fit, NO_DEVICE), (fit + 1, TOO_LARGE)):
+                c = HostCalls(lib, kv_heads=kv_heads, page=8, max_pages=slots // 8, pages=slots // 8)
+                assert getattr(c, call)(kv_heads) == want, (call, slots, kv_heads)
+
+
+def test_rows_of_a_key_head_that_do_not_fit_31_bits_are_refused(lib):
+    for call in ("attention", "accumulate"):
+        c = HostCalls(lib, kv_heads=1, nodes=128)
+        most = (2 ** 31 - 1 - 256) // 128
+        assert getattr(c, call)(most) == NO_DEVICE
+        assert getattr(c, call)(most + 1) == TOO_LARGE
