@@ -344,7 +344,11 @@ enum {
  * of 16 bytes. Slot s of sequence b is token s % page_size of page
  * page_table[b * table_stride + s / page_size]. Slots past a sequence's tokens
  * may hold anything. Pages that only attention reads may be shared by
- * sequences; a page that a call writes (commit, evict) belongs to one. */
+ * sequences; a page that a call writes (commit, evict) belongs to one. Where a
+ * call writes, k, v, mass and pos keep to memory of their own: of the strides of
+ * dimensions of more than one, sorted, each is at least the extent of what lies
+ * below it (any view that slicing and transposing make), also with the two
+ * buffers' distance as a stride (SPECVERIFY_ERR_INVALID_ARG). */
 typedef struct {
     int32_t dtype;      /* SPECVERIFY_BF16 or SPECVERIFY_FP16 */
     int32_t layers;     /* attention and accumulation take one layer */
@@ -406,7 +410,8 @@ int specverify_tree_set_wait_limit(specverify_tree_t h, uint64_t ns);
  * q and out are [rows, heads, head_dim] of the cache's dtype, with their own
  * row and head strides in elements (multiples of 16 bytes, as the bases);
  * heads is a multiple of kv_heads, scale > 0; lse [rows, heads] may be NULL. q
- * may have strides of 0 (one query for all rows or heads), out may not.
+ * may have strides of 0 (one query for all rows or heads); out keeps its rows and
+ * heads apart, and is not q.
  * The scores, the softmax statistics and the sums over values are fp32; a
  * weight is rounded to the cache's dtype, relative to a running maximum,
  * before it multiplies a value. A slot that a node does not see never reaches

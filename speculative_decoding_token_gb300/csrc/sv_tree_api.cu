@@ -33,6 +33,68 @@ bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
     return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
 }
 
+// A strided layout in bytes, to see whether its elements, or those of two buffers
+// laid out alike, keep to memory of their own: sorted by size, each stride has to be
+// at least the extent of what lies below it. Every view that slicing and transposing
+// make of a plain buffer is such a one.
+struct Layout {
+    struct Dim {
+        int64_t count, stride;
+    } dim[6];
+    int dims = 0;
+    int64_t inner;  // contiguous bytes of an element
+
+    explicit Layout(int64_t bytes) : inner(bytes) {}
+    Layout &add(int64_t count, int64_t stride) {
+        if (count > 1) dim[dims++] = {count, stride};
+        return *this;
+    }
+    bool apart() const {
+        Dim d[6];
+        std::copy(dim, dim + dims, d);
+        std::sort(d, d + dims, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+        __int128 span = inner;
+        for (int i = 0; i < dims; ++i) {
+            if (d[i].stride < span) return false;
+            span += (__int128)d[i].stride * (d[i].count - 1);
+        }
+        return true;
+    }
+    // of a buffer at a and another at b, both of this layout
+    bool apart(const void *a, const void *b) const {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return Layout(*this).add(2, (int64_t)(x < y ? y - x : x - y)).apart();
+    }
+};
+
+Layout rows_layout(int64_t rows, int64_t heads, int64_t d, int64_t rs, int64_t hs) {
+    return Layout(d * 2).add(rows, rs * 2).add(heads, hs * 2);
+}
+
+Layout kv_layout(const specverify_cache *c) {
+    return Layout(c->head_dim * 2)
+        .add(c->layers, c->layer_stride * 2)
+        .add(c->num_pages, c->page_stride * 2)
+        .add(c->kv_heads, c->head_stride * 2)
+        .add(c->page_size, c->token_stride * 2);
+}
+
+Layout mass_layout(const specverify_cache *c) {
+    return Layout(4)
+        .add(c->layers, c->mass_layer_stride * 4)
+        .add(c->num_pages, c->mass_page_stride * 4)
+        .add(c->kv_heads, c->mass_head_stride * 4)
+        .add(c->page_size, c->mass_token_stride * 4);
+}
+
+// Whether a call may write the cache's keys, values, masses and positions.
+bool writable(const specverify_cache *c) {
+    if (!kv_layout(c).apart(c->k, c->v)) return false;
+    const Layout m = mass_layout(c);
+    if (c->mass && c->pos) return m.apart(c->mass, c->pos);
+    return (!c->mass && !c->pos) || m.apart();
+}
+
 int check_cache(const specverify_cache *c, int32_t B, bool one_layer) {
     if (!c) return SPECVERIFY_ERR_INVALID_ARG;
     if (c->dtype != SPECVERIFY_BF16 && c->dtype != SPECVERIFY_FP16)
@@ -201,10 +263,12 @@ int specverify_tree_attention(specverify_tree_t h, const specverify_cache *cache
         rc = check_rows(cache, out, rows, heads, out_row_stride, out_head_stride);
     if (rc != SPECVERIFY_OK) return rc;
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
-    // queries may be one row for all, outputs not
-    if ((rows > 1 && out_row_stride == 0) || (heads > 1 && out_head_stride == 0))
-        return SPECVERIFY_ERR_INVALID_ARG;
+    // queries may be one row for all, outputs keep to themselves
+    const Layout o = rows_layout(rows, heads, cache->head_dim, out_row_stride, out_head_stride);
+    if (!o.apart()) return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
+    if (q == out || (q_row_stride == out_row_stride && q_head_stride == out_head_stride && !o.apart(q, out)))
+        return SPECVERIFY_ERR_INVALID_ARG;
     if (!lens) return SPECVERIFY_ERR_INVALID_ARG;
     if (!sv::line_fits((int64_t)cache->max_pages * cache->page_size, cache->kv_heads, sv::kAttnHead,
                        tree->max_nodes, heads / cache->kv_heads))
@@ -270,7 +334,7 @@ int specverify_tree_commit(specverify_tree_t h, const specverify_cache *cache, i
         return SPECVERIFY_ERR_INVALID_ARG;
     const int rc = check_cache(cache, B, false);
     if (rc != SPECVERIFY_OK) return rc;
-    if (cache->layers > 65535) return SPECVERIFY_ERR_INVALID_ARG;
+    if (cache->layers > 65535 || !writable(cache)) return SPECVERIFY_ERR_INVALID_ARG;
     if (B == 0) return SPECVERIFY_OK;
     if (!lens || !n_accepted || !path || !new_lens || (new_seen && !seen) ||
         (cache->pos && !seen))
@@ -312,7 +376,8 @@ int specverify_cache_accumulate(specverify_tree_t h, const specverify_cache *cac
     if (rc != SPECVERIFY_OK) return rc;
     if (!good_scale(scale)) return SPECVERIFY_ERR_INVALID_ARG;
     if (tree->B == 0 || rows == 0) return SPECVERIFY_OK;
-    if (!lens || !n_accepted || !path || !lse || !cache->mass) return SPECVERIFY_ERR_INVALID_ARG;
+    if (!lens || !n_accepted || !path || !lse || !cache->mass || !mass_layout(cache).apart())
+        return SPECVERIFY_ERR_INVALID_ARG;
     if (!sv::line_fits((int64_t)cache->max_pages * cache->page_size, cache->kv_heads, sv::kMassHead,
                        tree->max_nodes, heads / cache->kv_heads))
         return SPECVERIFY_ERR_TOO_LARGE;
@@ -347,7 +412,13 @@ int specverify_cache_evict(specverify_tree_t h, const specverify_cache *cache, i
     if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
         return SPECVERIFY_ERR_INVALID_ARG;
     if (B == 0) return SPECVERIFY_OK;
-    if (!cache->mass || !cache->pos || !lens || !seen || !mass_out || !pos_out || !new_lens)
+    if (!cache->mass || !cache->pos || !lens || !seen || !mass_out || !pos_out || !new_lens ||
+        !writable(cache))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    const Layout m = mass_layout(cache);
+    if ((mass_out != cache->mass && !m.apart(mass_out, cache->mass)) ||
+        (pos_out != cache->pos && !m.apart(pos_out, cache->pos)) || !m.apart(mass_out, pos_out) ||
+        !m.apart(mass_out, cache->pos) || !m.apart(pos_out, cache->mass))
         return SPECVERIFY_ERR_INVALID_ARG;
     const int64_t n = (int64_t)B * 4;
     if (overlap(lens, n, new_lens, n) || overlap(seen, n, new_lens, n))

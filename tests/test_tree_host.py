@@ -169,3 +169,67 @@ def test_rows_of_a_key_head_that_do_not_fit_31_bits_are_refused(lib):
         most = (2 ** 31 - 1 - 256) // 128
         assert getattr(c, call)(most) == NO_DEVICE
         assert getattr(c, call)(most + 1) == TOO_LARGE
+
+
+def test_attention_refuses_an_output_that_shares_memory(lib):
+    c = HostCalls(lib)
+    d, out = 64, 1 << 41
+    for rows, heads, strides in ((4, 4, (4 * d, 8)), (4, 4, (8, 4 * d)), (4, 4, (2 * d, d)), (4, 4, (0, d)), (4, 4, (4 * d, 0)),
+                                 (4, 4, (4 * d - 8, d)), (5, 4, (d, 4 * d)), (2, 4, (d - 8, 4 * d))):
+        assert c.attention(heads, rows, out_strides=strides) == INVALID, (rows, heads, strides)
+    for rows, heads, strides in ((4, 4, (4 * d, d)), (4, 4, (d, 4 * d)), (4, 4, (12 * d, 3 * d)), (4, 4, (2 * d, 8 * d)),
+                                 (1, 4, (0, d)), (4, 2, (2 * d + 8, d + 8))):
+        assert c.attention(heads, rows, out_strides=strides) == NO_DEVICE, (rows, heads, strides)
+    # queries and outputs: one buffer, buffers that overlap, halves of one row
+    assert c.attention(4, q=out, out=out) == INVALID
+    assert c.attention(4, q=out, out=out, q_strides=(0, 0)) == INVALID
+    assert c.attention(4, q=out + 2 * d, out=out) == INVALID
+    assert c.attention(4, q=out + 2 * 4 * d, out=out) == INVALID
+    assert c.attention(4, q=out + 2 * 16 * d, out=out) == NO_DEVICE
+    wide = (8 * d, d)
+    assert c.attention(4, q=out + 2 * 4 * d, out=out, q_strides=wide, out_strides=wide) == NO_DEVICE
+
+
+def test_caches_that_share_memory_are_read_and_not_written(lib):
+    def calls(**changes):
+        c = HostCalls(lib, layers=2)
+        for name, value in changes.items():
+            setattr(c.cache, name, value)
+        one = HostCalls(lib)
+        for name, value in changes.items():
+            if not name.endswith("layer_stride"):
+                setattr(one.cache, name, value)
+        return one.attention(4), one.accumulate(4), c.commit(), c.evict()
+
+    ok, no = NO_DEVICE, INVALID
+    assert calls() == (ok, ok, ok, ok)
+    # keys and values: overlapping tokens, heads or pages, the same buffer twice, buffers that overlap
+    for change in (dict(token_stride=8), dict(head_stride=8 * 64), dict(page_stride=8), dict(v=1 << 44),
+                   dict(v=(1 << 44) + 64), dict(v=(1 << 44) + 2 * 64)):
+        assert calls(**change) == (ok, ok, no, no), change
+    assert calls(layer_stride=64) == (ok, ok, no, no)
+    # token-major, and keys beside values in one pool: by page, by head, by token
+    assert calls(token_stride=2 * 64, head_stride=64) == (ok, ok, ok, ok)
+    assert calls(page_stride=2 * 2048, layer_stride=4 * 4096, v=(1 << 44) + 2 * 2048) == (ok, ok, ok, ok)
+    assert calls(head_stride=2048, page_stride=4096, layer_stride=4 * 4096, v=(1 << 44) + 2 * 1024) == (ok, ok, ok, ok)
+    assert calls(token_stride=128, head_stride=2048, page_stride=4096, layer_stride=4 * 4096,
+                 v=(1 << 44) + 2 * 64) == (ok, ok, ok, ok)
+    # masses and positions
+    for change in (dict(mass_token_stride=0), dict(mass_token_stride=-1), dict(mass_head_stride=8), dict(mass_page_stride=16),
+                   dict(mass_head_stride=-16)):
+        assert calls(**change) == (ok, no, no, no), change
+    for change in (dict(pos=1 << 42), dict(pos=(1 << 42) + 4), dict(mass_layer_stride=3)):
+        assert calls(**change) == (ok, ok, no, no), change
+    assert calls(mass_token_stride=2, mass_head_stride=2, mass_page_stride=64, mass_layer_stride=256) == (ok, no, no, no)
+    assert calls(mass_token_stride=2, mass_head_stride=32, mass_page_stride=64, mass_layer_stride=256,
+                 pos=(1 << 42) + 4) == (ok, ok, ok, ok)
+    # what the eviction writes: the cache's own, or buffers apart from them
+    c = HostCalls(lib)
+    m, p, far = c.cache.mass, c.cache.pos, 1 << 38
+    assert [c.evict(m, p), c.evict(far, p), c.evict(m, far), c.evict(far, far + (1 << 20))] == [ok] * 4
+    for a, b in ((m + 4, p), (m, p + 4), (far, far), (far, far + 4), (p, m), (p, far), (far, m), (m + 4 * 100, p)):
+        assert c.evict(a, b) == no, (a, b)
+    c.cache.mass = None
+    assert c.commit() == ok
+    c.cache.pos = None
+    assert c.commit() == ok
