@@ -302,7 +302,7 @@ class SpecTree:
         mass_out = cache.mass if mass_out is None else mass_out
         pos_out = cache.pos if pos_out is None else pos_out
         for name, t, like in (("mass_out", mass_out, cache.mass), ("pos_out", pos_out, cache.pos)):
-            if t is not like and (t.dtype is not like.dtype or t.shape != like.shape or t.stride() != like.stride()
+            if t is not like and (t.dtype is not like.dtype or t.shape != like.shape or _strides(t) != _strides(like)
                                   or t.get_device() != at):
                 raise ValueError(f"{name} must be laid out as the cache's")
         new_lens = self._empty(stream, (B,), torch.int32) if new_lens is None else new_lens

@@ -1056,3 +1056,23 @@ def test_verify_whose_waits_run_out():
         late += with_short_waits(h, call, check)
     assert late
     h.close()
+
+
+def test_evict_into_buffers_whose_strides_differ_where_nothing_lies(st):
+    """The stride of a cache's only key head says nothing."""
+    rng = np.random.default_rng(6)
+    bt = tu.Batch([90, 40], [0, 0], 1, 1, 64, 16, BF16, seed=6, poison=False)
+    shape = bt.k.shape[:-1]
+    mass = torch.rand(shape, generator=bt.gen)
+    pos, seen = make_positions(rng, bt, shape)
+    bt.upload(mass=mass, pos=pos)
+    wide = torch.zeros(shape[1], 3, shape[3], device="cuda")  # pages of three heads
+    out = torch.zeros(shape[1], 1, shape[3], device="cuda").as_strided(bt.dmass.shape, (shape[3], 7, 1))
+    assert out.stride() != bt.dmass.stride()
+    _, p, new_lens = st.evict(bt.cache, bt.dlens, bt.dev(seen, torch.int32), 32, sink=1, recent=4, mass_out=out)
+    want = expected_evict(bt, mass, pos, seen, 32, 1, 4, torch.zeros(shape), pos)
+    assert new_lens.tolist() == [32, 32]
+    for got, w in ((bt.dk, want[0]), (bt.dv, want[1]), (out, want[2]), (p, want[3])):
+        assert torch.equal(got.cpu(), w[0])
+    with pytest.raises(ValueError):  # a stride that is used
+        st.evict(bt.cache, bt.dlens, bt.dev(seen, torch.int32), 32, mass_out=wide[:, 1:2])
