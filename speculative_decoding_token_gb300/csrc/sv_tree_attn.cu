@@ -52,7 +52,9 @@ constexpr int kMmaWarp = 16, kLoadWarp = 17, kScoutThreads = 64;
 // 64 * 128 registers, the launch's 96 * 640).
 constexpr int kSoftRegs = 104, kOtherRegs = 64;
 constexpr int kTmemCols = 512;
-constexpr float kTiny = 1e-37f;            // least weight of a piece: keeps inf * weight infinite
+// The least weight of a piece, fp32's least number: keeps inf * weight infinite, and
+// adds under 2^-21 where a finite piece (under 2^128) should count for nothing.
+constexpr float kTiny = 0x1p-149f;
 
 template <int D>
 struct Shape {

@@ -1076,3 +1076,23 @@ def test_evict_into_buffers_whose_strides_differ_where_nothing_lies(st):
         assert torch.equal(got.cpu(), w[0])
     with pytest.raises(ValueError):  # a stride that is used
         st.evict(bt.cache, bt.dlens, bt.dev(seen, torch.int32), 32, mass_out=wide[:, 1:2])
+
+
+@pytest.mark.parametrize("B,high", [(1, 260), (150, 260), (1, 250), (150, 250)])
+def test_attention_of_large_values_whose_weight_vanishes(B, high):
+    """Values of 1e36 with scores 300 under the others': pieces and groups of tiles that hold nothing else count for nothing
+    (one sequence: joined across CTAs; many: within them)."""
+    import speculative_decoding_token_gb300 as sv
+    bt = tu.Batch([400 + b % 3 for b in range(B)], [2] * B, 2, 1, 64, 16, BF16, seed=B)
+    for b in range(B):
+        pg, at = bt.slots(b, 402)
+        bt.k[0, pg, 0, at] = 0.0
+        bt.k[0, pg[130:high], 0, at[130:high], 0] = 150.0
+        bt.v[0, pg[:130], 0, at[:130]] = 1e36
+        bt.v[0, pg[high:400], 0, at[high:400]] = -1e36
+    bt.q.zero_()
+    bt.q[:, :, 0] = 16.0
+    h = sv.SpecTree(B)
+    check_attention(h, bt)
+    assert h.device_status() == 0
+    h.close()
