@@ -456,7 +456,7 @@ TREE_LENS, TREE_BUDGET = (1000, 2000), 1900
 def run_tree(args, rank, world, local):
     """Times a step of drafted token trees on the workload's target rows: sequence
     b's tree has gamma_b + 1 nodes (its row count), every node below a random
-    earlier one, over a cache of two layers (8 key heads of 128, 4 query heads
+    earlier one, three of four first children what the target ranks first, over a cache of two layers (8 key heads of 128, 4 query heads
     each, 1000 to 2000 tokens a sequence). Every call of the step, in its order;
     the eviction writes its masses and positions aside, so that each step evicts
     the same tokens."""
@@ -472,11 +472,8 @@ def run_tree(args, rank, world, local):
     gen = torch.Generator(device="cuda")
     gen.manual_seed(17 + rank)
     nodes = (batch.gamma + 1).to(torch.int32)
-    j = torch.arange(T, device="cuda")
-    parent = torch.where(j > 0, (torch.rand(B, T, generator=gen, device="cuda") * j).floor(), -1.0)
-    tokens = torch.zeros(B, T, dtype=torch.int32, device="cuda")
-    tokens[:, 1:] = batch.draft_tokens
-    tree = sv.TokenTree(batch.p_row_off, nodes, parent.to(torch.int32), tokens)
+    parent, tokens = workload.draft_tree(batch, seed=17 + rank)
+    tree = sv.TokenTree(batch.p_row_off, nodes, parent, tokens)
     lens = torch.randint(*TREE_LENS, (B,), generator=gen, device="cuda", dtype=torch.int32)
     pages_each = -(-(TREE_LENS[1] + T) // TREE_PAGE)
     pages = B * pages_each

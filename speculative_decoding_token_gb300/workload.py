@@ -177,6 +177,33 @@ def make_batch(cfg, device="cpu", *, B=None, V=None, gamma=None, seed=None,
                  dtype=cfg["dtype"], gamma_max=gamma_max, meta=meta)
 
 
+def draft_tree(batch: Batch, *, agree=0.75, chain=False, seed=0):
+    """Drafted trees over a batch's target rows: (parent, tokens), int32 [B, gamma_max + 1],
+    sequence b's tree of gamma[b] + 1 nodes in its target rows. Node j > 0 hangs below a uniform
+    earlier node (with `chain`, below node j - 1). A share `agree` of the first children hold the
+    token that the target ranks first after their parent (the lowest such), so that a greedy walk
+    takes steps; the other nodes hold the batch's draft tokens."""
+    B, T, dev = batch.B, batch.gamma_max + 1, batch.target.device
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    j = torch.arange(T, device=dev)
+    u, pick = torch.rand(2, B, T, generator=gen, device=dev)
+    up = torch.minimum((u * j).long(), (j - 1).clamp(min=0)) if not chain else (j - 1).expand(B, T)
+    parent = torch.where(j > 0, up, -1)
+    tokens = torch.zeros(B, T, device=dev, dtype=torch.int32)
+    tokens[:, 1:] = batch.draft_tokens
+    first = (parent[:, :, None] == parent[:, None, :]).tril(-1).sum(2) == 0
+    good = first & (j > 0) & (j <= batch.gamma[:, None]) & (pick < agree)
+    b, node = good.nonzero(as_tuple=True)
+    rows = batch.target[batch.p_row_off[b] + parent[b, node]]
+    col = torch.arange(batch.V, device=dev, dtype=torch.int32)
+    for r0 in range(0, len(b), 256):
+        x = rows[r0:r0 + 256]
+        best = torch.where(x == x.amax(1, keepdim=True), col, batch.V).amin(1)
+        tokens[b[r0:r0 + 256], node[r0:r0 + 256]] = best
+    return parent.to(torch.int32).contiguous(), tokens
+
+
 def to_numpy_logits(t: torch.Tensor) -> np.ndarray:
     """Host numpy view of logit rows: float32, or uint16 bit patterns for bf16."""
     t = t.detach().cpu().contiguous()

@@ -233,3 +233,27 @@ def test_caches_that_share_memory_are_read_and_not_written(lib):
     assert c.commit() == ok
     c.cache.pos = None
     assert c.commit() == ok
+
+
+@pytest.mark.parametrize("config,kw", [(1, {}), (3, dict(B=24, V=1001)), (3, dict(B=30, V=5))])
+def test_drafted_trees_take_steps(config, kw):
+    from speculative_decoding_token_gb300 import workload
+    batch = workload.make_batch(config, **kw)
+    nodes, rows = (batch.gamma + 1).tolist(), batch.p_row_off.tolist()
+    for chain in (False, True):
+        parent, tokens = workload.draft_tree(batch, chain=chain, seed=3)
+        assert parent.dtype == tokens.dtype == torch.int32 and parent.shape == tokens.shape == (batch.B, batch.gamma_max + 1)
+        for b in range(batch.B):
+            up = parent[b, : nodes[b]].tolist()
+            assert up[0] == -1 and all(0 <= p < j for j, p in enumerate(up) if j)
+            assert not chain or up == list(range(-1, nodes[b] - 1))
+        assert bool(((tokens >= 0) & (tokens < batch.V)).all())
+        n = tu.verify(parent.numpy(), nodes, tokens.numpy(), rows, batch.target)[0]
+        assert (n > 0).sum() > batch.B // 3
+        # every first child agrees: the walk ends in a leaf; no child does but by chance
+        parent, tokens = workload.draft_tree(batch, agree=1.0, chain=chain, seed=4)
+        n, _, path = tu.verify(parent.numpy(), nodes, tokens.numpy(), rows, batch.target)
+        for b in range(batch.B):
+            assert int(path[b, n[b]]) not in parent[b, : nodes[b]].tolist()
+        assert not chain or n.tolist() == batch.gamma.tolist()
+    assert torch.equal(workload.draft_tree(batch, agree=0.0)[1][:, 1:], batch.draft_tokens)
