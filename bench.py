@@ -453,21 +453,22 @@ TREE_LAYERS, TREE_KV_HEADS, TREE_GROUP, TREE_D, TREE_PAGE = 2, 8, 4, 128, 64
 TREE_LENS, TREE_BUDGET = (1000, 2000), 1900
 
 
-def run_tree(args, rank, world, local):
-    """Times a step of drafted token trees on the workload's target rows: sequence
+def tree_step(cfg, batch, rank=0):
+    """A step of drafted token trees on the workload's target rows: sequence
     b's tree has gamma_b + 1 nodes (its row count), every node below a random
     earlier one, three of four first children what the target ranks first, over a cache of two layers (8 key heads of 128, 4 query heads
-    each, 1000 to 2000 tokens a sequence). Every call of the step, in its order;
-    the eviction writes its masses and positions aside, so that each step evicts
-    the same tokens."""
+    each, 1000 to 2000 tokens a sequence). Every call of the step, in its order.
+    Lengths and positions stay as they are from step to step, and the eviction
+    ranks masses that no call changes, so each step commits and evicts the same
+    slots (the keys and values in them are moved about in place). Returns the
+    calls and what they work on."""
+    import types
+
     import torch
 
     import speculative_decoding_token_gb300 as sv
     from speculative_decoding_token_gb300 import workload
 
-    sv.build()
-    cfg = workload.CONFIGS[args.config]
-    batch = workload.make_batch(args.config, device="cuda", seed=cfg["seed"] + 100 * rank)
     B, T = cfg["B"], batch.gamma_max + 1
     gen = torch.Generator(device="cuda")
     gen.manual_seed(17 + rank)
@@ -485,12 +486,14 @@ def run_tree(args, rank, world, local):
     pos = torch.zeros(shape[:-1], dtype=torch.int32, device="cuda")
     slots = torch.arange(pages_each * TREE_PAGE, device="cuda", dtype=torch.int32).view(pages_each, 1, TREE_PAGE)
     pos[:, table.long()] = slots.expand(B, pages_each, TREE_KV_HEADS, TREE_PAGE)
+    ranked = torch.randn(shape[:-1], generator=gen, device="cuda").exp()
     mass_out, pos_out = torch.zeros_like(mass), torch.zeros_like(pos)
     heads = TREE_KV_HEADS * TREE_GROUP
     rows = batch.target.shape[0]
     q = torch.randn(TREE_LAYERS, rows, heads, TREE_D, generator=gen, device="cuda", dtype=torch.bfloat16)
     out, lse = torch.empty_like(q), torch.empty(TREE_LAYERS, rows, heads, device="cuda")
     cache = sv.KVCache(k, v, table, mass=mass, pos=pos)
+    bounded = sv.KVCache(k, v, table, mass=ranked, pos=pos)
     layers = [sv.KVCache(k[i], v[i], table, mass=mass[i]) for i in range(TREE_LAYERS)]
     moves = TREE_LAYERS * B * TREE_KV_HEADS * min(TREE_BUDGET, pages_each * TREE_PAGE - TREE_BUDGET)
     h = sv.SpecTree(B, max_moves=moves)
@@ -513,10 +516,26 @@ def run_tree(args, rank, world, local):
             h.accumulate(q[i], lse[i], layers[i], tree, lens, n, path)
 
     def evict():
-        h.evict(cache, new_lens, new_seen, TREE_BUDGET, sink=4, recent=256, mass_out=mass_out, pos_out=pos_out,
+        h.evict(bounded, new_lens, new_seen, TREE_BUDGET, sink=4, recent=256, mass_out=mass_out, pos_out=pos_out,
                 new_lens=kept)
 
-    calls = (attention, verify, commit, accumulate, evict)
+    return types.SimpleNamespace(calls=(attention, verify, commit, accumulate, evict), handle=h, nodes=nodes, lens=lens, n=n,
+                                 path=path, emitted=emitted, new_lens=new_lens, kept=kept, mass=mass, mass_out=mass_out,
+                                 pos_out=pos_out, heads=heads)
+
+
+def run_tree(args, rank, world, local):
+    """Times tree_step's calls, together and each by itself."""
+    import torch
+
+    import speculative_decoding_token_gb300 as sv
+    from speculative_decoding_token_gb300 import workload
+
+    sv.build()
+    cfg = workload.CONFIGS[args.config]
+    batch = workload.make_batch(args.config, device="cuda", seed=cfg["seed"] + 100 * rank)
+    step = tree_step(cfg, batch, rank)
+    calls, h = step.calls, step.handle
 
     def timed(which, steps):
         start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -539,12 +558,12 @@ def run_tree(args, rank, world, local):
     ms = max_over_ranks(ms, world)
     each = {call.__name__: timed((call,), args.steps) / args.steps for call in calls}
     status = h.device_status()
-    accepted = int(n.clamp(min=0).sum())
+    accepted = int(step.n.clamp(min=0).sum())
     h.close()
     if rank != 0:
         return
-    count = int(nodes.sum())
-    kv_bytes = int((lens + nodes).sum()) * TREE_LAYERS * TREE_KV_HEADS * TREE_D * 2
+    count = int(step.nodes.sum())
+    kv_bytes = int((step.lens + step.nodes).sum()) * TREE_LAYERS * TREE_KV_HEADS * TREE_D * 2
     peak, peak_kind = peaks()
     gbs = 2 * kv_bytes / (each["attention"] / 1e3) / 1e9
     line = {"metric": "drafted tree nodes/s", "value": world * count * args.steps / (ms / 1e3), "unit": "nodes/s",
@@ -552,7 +571,7 @@ def run_tree(args, rank, world, local):
             "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
             "config": {**workload_config(cfg, batch, "greedy"), "mode": "tree", "nodes_per_step": count,
                        "accepted_per_step": accepted, "layers": TREE_LAYERS, "kv_heads": TREE_KV_HEADS,
-                       "heads": heads, "head_dim": TREE_D, "page": TREE_PAGE, "lens": "%d..%d" % TREE_LENS,
+                       "heads": step.heads, "head_dim": TREE_D, "page": TREE_PAGE, "lens": "%d..%d" % TREE_LENS,
                        "budget": TREE_BUDGET},
             "roofline": {"bound": "hbm", "kernel": "tree_attn_kernel", "achieved": gbs, "peak": peak,
                          "peak_kind": peak_kind, "unit": "GB/s", "frac": gbs / peak, "traffic": None,

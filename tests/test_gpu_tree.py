@@ -1096,3 +1096,25 @@ def test_attention_of_large_values_whose_weight_vanishes(B, high):
     check_attention(h, bt)
     assert h.device_status() == 0
     h.close()
+
+
+def test_benchmark_step_does_the_same_work_every_time():
+    """The benchmark's step accepts drafts, moves tokens, and commits and evicts the same slots however often it has run."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    import bench
+    from speculative_decoding_token_gb300 import workload
+    batch = workload.make_batch(1, device="cuda", B=24)
+    step = bench.tree_step({**workload.CONFIGS[1], "B": 24}, batch)
+    first = None
+    for _ in range(4):
+        for call in step.calls:
+            call()
+        now = [t.clone() for t in (step.n, step.path, step.emitted, step.new_lens, step.kept, step.mass_out, step.pos_out)]
+        first = now if first is None else first
+        for a, b in zip(now, first):
+            assert torch.equal(a, b)
+    assert int((step.n > 0).sum()) > 4 and int((step.kept < step.new_lens).sum()) > 0
+    assert float(step.mass.max()) > 0 and step.handle.device_status() == 0
+    step.handle.close()
