@@ -71,6 +71,12 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _fits(bits=32, **values):
+    """Whole numbers that the call would cut to their lowest bits are refused here."""
+    for name, x in values.items():
+        _need(-(1 << (bits - 1)) <= x < 1 << (bits - 1), f"{name} must fit {bits} bits, not {x}")
+
+
 def _ints(name, t, index, shape, dtype=torch.int32):
     """The address of a contiguous integer tensor of that shape on CUDA device `index`."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
@@ -159,6 +165,8 @@ class SpecTree:
         self.lib, self.check = load(), _check
         self.index = torch.cuda.current_device() if device is None else int(device)
         self.device = torch.device("cuda", self.index)
+        _fits(max_batch=max_batch, device=self.index)
+        _fits(64, max_moves=max_moves)
         h = ctypes.c_void_p()
         _check(self.lib.specverify_tree_create(ctypes.byref(h), self.index, max_batch, max_moves), "specverify_tree_create")
         self.h = h
@@ -305,6 +313,7 @@ class SpecTree:
             if t is not like and (t.dtype is not like.dtype or t.shape != like.shape or _strides(t) != _strides(like)
                                   or t.get_device() != at):
                 raise ValueError(f"{name} must be laid out as the cache's")
+        _fits(budget=budget, sink=sink, recent=recent)
         new_lens = self._empty(stream, (B,), torch.int32) if new_lens is None else new_lens
         rc = self.lib.specverify_cache_evict(
             self.h, cache.ref, B, _ints("lens", lens, at, (B,)), _ints("seen", seen, at, (B,)), budget, sink, recent,
@@ -322,6 +331,7 @@ class SpecTree:
     def set_wait_limit(self, ns: int):
         """Bounds every wait inside the kernels of the calls that follow, in nanoseconds; 0: the default, about two
         seconds. A wait that runs out ends its call with the status bit ``timeout`` and its outputs undefined."""
+        _need(0 <= ns < 1 << 63, f"a wait's limit must be a number of nanoseconds, not {ns}")
         self.check(self.lib.specverify_tree_set_wait_limit(self.h, int(ns)), "specverify_tree_set_wait_limit")
 
     def workspace_bytes(self) -> int:

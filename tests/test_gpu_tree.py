@@ -1118,3 +1118,22 @@ def test_benchmark_step_does_the_same_work_every_time():
     assert int((step.n > 0).sum()) > 4 and int((step.kept < step.new_lens).sum()) > 0
     assert float(step.mass.max()) > 0 and step.handle.device_status() == 0
     step.handle.close()
+
+
+def test_numbers_that_do_not_fit_are_refused(st):
+    """Not cut to their lowest bits: a budget of 2^32 + 4 is not one of 4."""
+    import speculative_decoding_token_gb300 as sv
+    bt = tu.Batch([20], [0], 2, 2, 64, 8, BF16, poison=False)
+    shape = bt.k.shape[:-1]
+    pos = torch.arange(bt.k.shape[1] * 8, dtype=torch.int32).view(1, -1, 1, 8).expand(shape).contiguous()
+    bt.upload(mass=torch.rand(shape, generator=bt.gen), pos=pos)
+    big = 1 << 32
+    k, m = bt.dk.clone(), bt.dmass.clone()
+    for bad in (lambda: st.evict(bt.cache, bt.dlens, bt.dlens, big + 4), lambda: st.evict(bt.cache, bt.dlens, bt.dlens, 4, sink=big),
+                lambda: st.evict(bt.cache, bt.dlens, bt.dlens, 4, recent=big + 1), lambda: st.evict(bt.cache, bt.dlens, bt.dlens, -big),
+                lambda: sv.SpecTree(big + 1), lambda: sv.SpecTree(1, max_moves=1 << 64), lambda: sv.SpecTree(1, device=big),
+                lambda: st.set_wait_limit(-1), lambda: st.set_wait_limit(1 << 64)):
+        with pytest.raises(ValueError):
+            bad()
+    assert torch.equal(bt.dk, k) and torch.equal(bt.dmass, m)
+    assert st.device_status() == 0
