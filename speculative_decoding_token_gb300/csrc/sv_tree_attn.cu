@@ -29,9 +29,12 @@
 //
 // Up to 128 rows a key head the keys' bytes bound it: 1.39 us a tile of 64 KiB
 // and CTA, 7.2 TB/s over 152 of them (B = 38, 65 thousand tokens each). With 256
-// rows the products do: 88 cycles for each of nominally 64 (S = Q K^T reads 8 KiB
-// of shared memory a product, all of the SM's bandwidth), 1.37 PFLOP/s (B = 32,
-// 64 nodes, 64 heads over 8, 14 thousand tokens: 689 us).
+// rows the products do: 88 cycles for each of nominally 64 in a trace (S = Q K^T
+// reads 8 KiB of shared memory a product, all of the SM's bandwidth). B = 32, 64
+// nodes, 64 heads over 8, 14 thousand tokens: 648 us in short bursts, 1.46 PFLOP/s;
+// 726 us, 1.30 PFLOP/s, where calls follow one another for long and the 1400 W cap
+// holds the clock at 1.70 GHz. Waits whose outcome is the whole warp's, and the
+// uniform branches after them, are worth 5 % of that (683 us with a branch a lane).
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -257,7 +260,13 @@ __device__ __forceinline__ void st_global_8(float *dst, const float *f) {
                  : "memory");
 }
 
-// A weight is rounded to the cache's type relative to a reference maximum that
+// A weight is rounded to the cache's type (the product takes P in the type of V; as
+// two terms, the rounding and the rest, P would double the products), off by at most
+// half a step, 2^-8 or 2^-11 of itself. So an output is within that of the mean of
+// |v| from the one of exact weights, before its own rounding of the same size: the
+// error against 64 bits is 2.2e-3 of the outputs' size with bfloat16 (1.7e-3 for
+// exact weights) and 2.2e-4 with binary16 (2.1e-4). The weight counts in the sum as
+// it was before the rounding. It is relative to a reference maximum that
 // is raised only when the running one passes it by kSlack binades (until then
 // O and the sum need no rescaling). bfloat16 keeps fp32's range; binary16 has
 // weights from 2^-24 to 2^16, so the reference's weight is 2^kShift there.

@@ -9,7 +9,8 @@
 // its first maximum (stores to distributed shared memory that count themselves
 // on a barrier there: B = 16, V = 152064: 11.4 us a call; with a barrier of the
 // cluster 12.7), and every CTA takes the same step, in about 1.8 us. B = 64, 4 to
-// 48 nodes: 19.4 us; 57 sequences fit the GPU at a time. Loading the first
+// 48 nodes: 19.4 us; 57 sequences fit the GPU at a time. (Plain stores with a
+// releasing arrival, which need no care where a wait runs out: 22.3 us.) Loading the first
 // child's row ahead did not pay: where every cluster is at work it is traffic
 // that many steps do not need.
 #include "sv_rows.cuh"
