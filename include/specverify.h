@@ -309,7 +309,8 @@ int specverify_verify_noalloc(const specverify_batch *in, float temperature, uin
  * bounded cache specverify_cache_accumulate and specverify_cache_evict.
  *
  * All calls are asynchronous on `cuda_stream`, allocate nothing, may be
- * captured into a CUDA graph, and check on the device what they read there:
+ * captured into a CUDA graph, take inputs that stay as they are until the call
+ * has run, and check on the device what they read there:
  * a sequence with a bad size, row, parent, path or page id is left alone (see
  * each call), the others are unaffected, and the sticky status word says so.
  * They launch as programmatic dependents of the kernel before them on the

@@ -132,7 +132,7 @@ struct Walk {
                 rest = 0;
                 if (++b == P.t.B) {
                     b = 0;
-                    ++block;
+                    if (++block >= P.blocks) left = 0;  // (sizes that changed meanwhile)
                 }
                 continue;
             }

@@ -98,7 +98,7 @@ struct Walk {
             g.s = seq_of(P, b);
             if (rest >= g.s.units(P)) {
                 rest = 0;
-                ++b;
+                if (++b >= P.t.B) left = 0;  // (sizes that changed meanwhile)
                 continue;
             }
             const int len = g.s.tiles + kHead;
