@@ -229,6 +229,116 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
                             float *entropy, float *topk_prob, int32_t *topk_idx,
                             void *cuda_stream);
 
+/* ==========================================================================
+ * Log-probabilities of given tokens and distillation of a draft, on rows of
+ * logits as in specverify_row_features: `logits` of dtype SPECVERIFY_FP32 or
+ * SPECVERIFY_BF16, `rows` rows of V logits (V < 2^31), row_stride elements
+ * apart, 16-byte aligned; one temperature T > 0 (1 / T a normal float). x = row / T, lse =
+ * ln sum_v exp(x_v). A logit of -inf is a masked token, of probability 0. The
+ * calls use the handle's device and its sticky status word and no workspace:
+ * unlike the others, they may run beside one another and inside captured graphs
+ * that do. Sums are fp32, results the same from run to run. A bad row (a NaN or
+ * +inf logit, every logit -inf, a bad token, list or row number) gets NaN for
+ * each of its floats and -1 for its whole numbers, and sets its status bit.
+ */
+
+#define SPECVERIFY_MAX_ALTERNATIVES 128 /* top tokens of a row, specverify_token_logprobs */
+#define SPECVERIFY_MAX_LIST 256         /* listed tokens of a row, specverify_distill_* */
+#define SPECVERIFY_MAX_GRAD_ROW (1 << 21) /* bytes of a row's logits in the calls with gradients */
+
+/* Log-probabilities of given tokens: what a server returns of the tokens that a
+ * verify step emitted, or a sequence's likelihood. Entry (b, m), b < B, m < M,
+ * asks for token y = tokens[b * M + m] under the row
+ *   row_off[b] + m, or row_off[b] + path[b * M + m] where path is given (a tree's
+ *   accepted path); b * M + m where row_off is NULL (path is then NULL as well).
+ * out_tokens of a verify call with its p_row_off, or of a tree verify with its
+ * path, are such entries. Outputs [B, M], each but logprob may be NULL:
+ *   logprob   x_y - lse;
+ *   entropy   -sum_v p_v ln p_v (nats), p = softmax(x);
+ *   lse       natural-log logsumexp of x;
+ *   rank      tokens before y in the order of larger logit, then lower index (0: y is the argmax);
+ *   topk_logprob, topk_idx [B, M, k]  the first k <= SPECVERIFY_MAX_ALTERNATIVES tokens of
+ *             that order and their log-probabilities; past V -inf and -1. NULL for k = 0.
+ * An entry of token -1 asks for nothing: its row is not read, its floats and its
+ * rank are 0, its top tokens -1 of log-probability -inf. Any other token outside
+ * [0, V) is bad. Each row asked for is read once. */
+int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                              int64_t V, int64_t row_stride, float temperature, int32_t B,
+                              int32_t M, const int32_t *tokens, const int64_t *row_off,
+                              const int32_t *path, int32_t k, float *logprob, float *entropy,
+                              float *lse, int32_t *rank, float *topk_logprob, int32_t *topk_idx,
+                              void *cuda_stream);
+
+/* Gradient of sum_r grad_logprob[r] logprob_r + grad_entropy[r] entropy_r with
+ * respect to the logits, row r with token y = tokens[r]:
+ *   grad[r, v] = (1/T) (g ([v = y] - p_v) - h p_v (ln p_v + entropy_r)),
+ * g = grad_logprob[r], h = grad_entropy[r] (0 where grad_entropy is NULL). grad has the
+ * logits' dtype, rows grad_stride elements apart, 16-byte aligned; it may be the
+ * logits themselves (same address and stride), and else shares no memory with
+ * the inputs. Rows of token -1 get a gradient of 0 and are not read. What lies
+ * between rows stays as it was. logprob and entropy [rows] may be NULL. Each row
+ * is read once and written once; V * element size is at most
+ * SPECVERIFY_MAX_GRAD_ROW (SPECVERIFY_ERR_TOO_LARGE). */
+int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                                   int64_t V, int64_t row_stride, float temperature,
+                                   const int32_t *tokens, const float *grad_logprob,
+                                   const float *grad_entropy, void *grad, int64_t grad_stride,
+                                   float *logprob, float *entropy, void *cuda_stream);
+
+/* Divergence of a draft's distribution from its target's top tokens ("DistillSpec:
+ * ..." App. A.1, Eq. A.1-A.4: FKL, RKL, JSD[beta], TVD with the missing 1/2).
+ * Row r has a list of the K columns k <= SPECVERIFY_MAX_LIST: token ids[r, k]
+ * (-1: unused, anywhere in the list; no id twice) and target[r, k], fp32 or bf16
+ * (target_dtype):
+ *   SPECVERIFY_TARGET_LOGPROBS  the target's log-probability p_k = exp(target) at the
+ *       call's temperature (specverify_token_logprobs' alternatives are such lists); what the list
+ *       leaves of one, p_rest = max(0, 1 - sum_k p_k), is the rest of the vocabulary's;
+ *   SPECVERIFY_TARGET_LOGITS    its logit: p = softmax(target / T) over the list,
+ *       p_rest = 0 (refused for RKL, which is infinite then).
+ * The draft's q = softmax(x) over the whole vocabulary is taken over the same
+ * outcomes, the listed tokens and the rest; q_rest is summed over the unlisted
+ * tokens. loss[r] is, over these outcomes (0 ln 0 = 0),
+ *   FKL sum p ln(p/q);   RKL sum q ln(q/p), p_rest at least 2^-20 in the logarithm;
+ *   JSD beta KL(p|m) + (1 - beta) KL(q|m), m = beta p + (1 - beta) q, 0 < beta < 1;
+ *   TVD 1/2 sum |p - q|.
+ * A row with no list (every id -1) is not read: its loss is 0. A list with an id outside [-1, V) or one
+ * twice, or with a NaN or +inf target, is bad. */
+enum {
+    SPECVERIFY_FKL = 0,
+    SPECVERIFY_RKL = 1,
+    SPECVERIFY_JSD = 2,
+    SPECVERIFY_TVD = 3
+};
+
+enum {
+    SPECVERIFY_TARGET_LOGPROBS = 0,
+    SPECVERIFY_TARGET_LOGITS = 1
+};
+
+typedef struct {
+    int32_t K;
+    int32_t target_dtype;   /* SPECVERIFY_FP32 or SPECVERIFY_BF16 */
+    int32_t form;           /* SPECVERIFY_TARGET_* */
+    int32_t divergence;     /* SPECVERIFY_FKL .. SPECVERIFY_TVD */
+    float beta;             /* of the JSD */
+    const int32_t *ids;     /* [rows, K] */
+    const void *target;     /* [rows, K] */
+} specverify_lists;
+
+int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                            int64_t V, int64_t row_stride, float temperature,
+                            const specverify_lists *lists, float *loss, void *cuda_stream);
+
+/* The divergence and its gradient: grad[r, v] = weight[r] dloss[r] / dlogits[r, v]
+ * (weight NULL: 1), for a list's token (h_k - q_k C) / T and for the others
+ * (h_rest - q_rest C) q_v / (q_rest T) with h = q dloss/dq of each outcome, C = sum h. grad, its
+ * layout, its sizes and rows without a list: as in specverify_token_logprobs_grad.
+ * Each row is read once and written once. loss [rows] is the unweighted one. */
+int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                            int64_t V, int64_t row_stride, float temperature,
+                            const specverify_lists *lists, const float *weight, void *grad,
+                            int64_t grad_stride, float *loss, void *cuda_stream);
+
 /* Synchronise `cuda_stream`, return the sticky status bits accumulated since
  * the last call in *status_out (0 = clean) and clear them. */
 int specverify_device_status(specverify_t h, void *cuda_stream, int32_t *status_out);

@@ -19,6 +19,7 @@ import os
 import threading
 
 from . import _build
+from .losses import RowLosses, TokenLogprobs
 
 __all__ = ["SpecVerify", "SpecVerifyError", "build", "load", "specverify_create",
            "specverify_destroy", "specverify_verify", "specverify_verify_greedy",
@@ -27,7 +28,7 @@ __all__ = ["SpecVerify", "SpecVerifyError", "build", "load", "specverify_create"
            "specverify_device_status", "specverify_status_string", "specverify_workspace_bytes",
            "specverify_set_timing", "specverify_get_timing", "specverify_set_wait_limit",
            "specverify_acceptance_stats", "specverify_row_features", "STATUS_BITS",
-           "SpecTree", "KVCache", "TokenTree"]
+           "TokenLogprobs", "SpecTree", "KVCache", "TokenTree"]
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -125,7 +126,8 @@ def load():
                   "specverify_get_timing", "specverify_set_wait_limit",
                   "specverify_acceptance_stats", "specverify_row_features"):
             getattr(lib, f).restype = ctypes.c_int
-        from . import tree
+        from . import losses, tree
+        losses.bind(lib)
         tree.bind(lib)
         _lib = lib
         return lib
@@ -297,8 +299,9 @@ def specverify_get_timing(h, kernel: int, reset: bool = False):
 
 # ---------------------------------------------------------------------------
 
-class SpecVerify:
-    """A handle on one CUDA device with workspace for batches up to the given sizes."""
+class SpecVerify(RowLosses):
+    """A handle on one CUDA device with workspace for batches up to the given sizes. The calls on the log-probabilities of
+    tokens and on distillation are :class:`losses.RowLosses`'; they use no workspace and take any sizes."""
 
     def __init__(self, max_batch: int, max_gamma: int, max_vocab: int, device: int | None = None):
         import torch

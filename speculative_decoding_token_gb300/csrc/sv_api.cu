@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <new>
 #include <vector>
 
@@ -12,12 +13,14 @@
 #include "sv_internal.h"
 #include "sv_rows_params.h"
 #include "sv_small.h"
+#include "sv_token.h"
 
 namespace {
 
 using sv::DeviceGuard;
 using sv::kDefaultWaitNs;
 using sv::map_cuda;
+using sv::overlap;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -212,6 +215,75 @@ int run_verify(specverify_ctx *h, const specverify_batch *in, bool sampling, flo
     if (e != cudaSuccess) return map_cuda(e);
     e = timed(h, 3, s, [&] { return sv::launch_accept(P, in->dtype, s); });
     return map_cuda(e);
+}
+
+// Rows of logits of a token log-probability or distillation call; with a
+// gradient, its rows too.
+int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int64_t rows,
+                 int64_t V, int64_t row_stride, float T, sv::TokenParams &p) {
+    if (!h || rows < 0 || rows > (int64_t)1 << 40 || V < 1 || V > INT32_MAX)
+        return SPECVERIFY_ERR_INVALID_ARG;
+    if (dtype != SPECVERIFY_FP32 && dtype != SPECVERIFY_BF16) return SPECVERIFY_ERR_INVALID_ARG;
+    // log2(e) / T has to be a number as well
+    if (!(T >= 4 * std::numeric_limits<float>::min() && T <= 0.25f / std::numeric_limits<float>::min()))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    const int64_t esz = dtype == SPECVERIFY_FP32 ? 4 : 2;
+    if (rows > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & 15) != 0 || row_stride < V ||
+                     row_stride > INT64_MAX / (8 * rows) || (row_stride * esz) % 16 != 0))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    p = sv::TokenParams{};
+    p.logits = static_cast<const char *>(logits);
+    p.stride_bytes = row_stride * esz;
+    p.rows = rows;
+    p.V = (int32_t)V;
+    p.c = (float)(1.4426950408889634073599 / (double)T);
+    p.inv_hi = (float)(1.0 / (double)T);
+    p.inv_lo = (float)(1.0 / (double)T - (double)p.inv_hi);
+    p.status = h->base.status;
+    p.entries = rows;
+    p.M = 1;
+    return SPECVERIFY_OK;
+}
+
+int grad_params(sv::TokenParams &p, int32_t dtype, void *grad, int64_t grad_stride) {
+    const int64_t esz = dtype == SPECVERIFY_FP32 ? 4 : 2;
+    if (!grad || (reinterpret_cast<uintptr_t>(grad) & 15) != 0 || grad_stride < p.V ||
+        grad_stride > INT64_MAX / (8 * p.rows) || (grad_stride * esz) % 16 != 0)
+        return SPECVERIFY_ERR_INVALID_ARG;
+    p.grad = static_cast<char *>(grad);
+    p.grad_stride_bytes = grad_stride * esz;
+    const int64_t row = p.V * esz;
+    const bool in_place = p.grad == p.logits && p.grad_stride_bytes == p.stride_bytes;
+    if (!in_place && overlap(p.grad, (p.rows - 1) * p.grad_stride_bytes + row, p.logits,
+                             (p.rows - 1) * p.stride_bytes + row))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    return row > SPECVERIFY_MAX_GRAD_ROW ? SPECVERIFY_ERR_TOO_LARGE : SPECVERIFY_OK;
+}
+
+// Whether the gradient's rows keep away from a small array.
+bool grad_clear(const sv::TokenParams &p, int64_t esz, const void *a, int64_t bytes) {
+    return !a || !overlap(p.grad, (p.rows - 1) * p.grad_stride_bytes + p.V * esz, a, bytes);
+}
+
+int list_params(sv::TokenParams &p, const specverify_lists *lists) {
+    if (!lists || lists->K < 1 || lists->K > SPECVERIFY_MAX_LIST ||
+        (lists->target_dtype != SPECVERIFY_FP32 && lists->target_dtype != SPECVERIFY_BF16) ||
+        (lists->form != SPECVERIFY_TARGET_LOGPROBS && lists->form != SPECVERIFY_TARGET_LOGITS) ||
+        lists->divergence < SPECVERIFY_FKL || lists->divergence > SPECVERIFY_TVD)
+        return SPECVERIFY_ERR_INVALID_ARG;
+    if (lists->divergence == SPECVERIFY_RKL && lists->form == SPECVERIFY_TARGET_LOGITS)
+        return SPECVERIFY_ERR_INVALID_ARG;
+    if (lists->divergence == SPECVERIFY_JSD && !(lists->beta > 0.0f && lists->beta < 1.0f))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    if (p.rows > 0 && (!lists->ids || !lists->target)) return SPECVERIFY_ERR_INVALID_ARG;
+    p.K = lists->K;
+    p.target_bf16 = lists->target_dtype == SPECVERIFY_BF16;
+    p.form = lists->form;
+    p.divergence = lists->divergence;
+    p.beta = lists->beta;
+    p.ids = lists->ids;
+    p.target = static_cast<const char *>(lists->target);
+    return SPECVERIFY_OK;
 }
 
 }  // namespace
@@ -543,6 +615,99 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
         if (e != cudaSuccess) return map_cuda(e);
     }
     return SPECVERIFY_OK;
+}
+
+int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                              int64_t V, int64_t row_stride, float temperature, int32_t B,
+                              int32_t M, const int32_t *tokens, const int64_t *row_off,
+                              const int32_t *path, int32_t k, float *logprob, float *entropy,
+                              float *lse, int32_t *rank, float *topk_logprob, int32_t *topk_idx,
+                              void *cuda_stream) {
+    sv::TokenParams p;
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    if (rc != SPECVERIFY_OK) return rc;
+    if (B < 0 || M < 0 || k < 0 || k > SPECVERIFY_MAX_ALTERNATIVES || (path && !row_off))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    p.entries = (int64_t)B * M;
+    if (p.entries == 0) return SPECVERIFY_OK;
+    if (!tokens || !logprob || (k > 0 && (!topk_logprob || !topk_idx)))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
+    p.M = M;
+    p.tokens = tokens;
+    p.row_off = row_off;
+    p.path = path;
+    p.k = k;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.lse = lse;
+    p.rank = rank;
+    p.top_logprob = topk_logprob;
+    p.top_idx = topk_idx;
+    return map_cuda(sv::launch_token_logprobs(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                                   int64_t V, int64_t row_stride, float temperature,
+                                   const int32_t *tokens, const float *grad_logprob,
+                                   const float *grad_entropy, void *grad, int64_t grad_stride,
+                                   float *logprob, float *entropy, void *cuda_stream) {
+    sv::TokenParams p;
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    if (rc != SPECVERIFY_OK || rows == 0) return rc;
+    if (!tokens || !grad_logprob) return SPECVERIFY_ERR_INVALID_ARG;
+    rc = grad_params(p, dtype, grad, grad_stride);
+    if (rc != SPECVERIFY_OK) return rc;
+    const int64_t esz = dtype == SPECVERIFY_FP32 ? 4 : 2;
+    for (const void *a : {(const void *)tokens, (const void *)grad_logprob, (const void *)grad_entropy,
+                          (const void *)logprob, (const void *)entropy})
+        if (!grad_clear(p, esz, a, rows * 4)) return SPECVERIFY_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
+    p.tokens = tokens;
+    p.g_logprob = grad_logprob;
+    p.g_entropy = grad_entropy;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    return map_cuda(sv::launch_token_logprobs_grad(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                            int64_t V, int64_t row_stride, float temperature,
+                            const specverify_lists *lists, float *loss, void *cuda_stream) {
+    sv::TokenParams p;
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    if (rc == SPECVERIFY_OK) rc = list_params(p, lists);
+    if (rc != SPECVERIFY_OK || rows == 0) return rc;
+    if (!loss) return SPECVERIFY_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
+    p.loss = loss;
+    return map_cuda(sv::launch_distill(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
+                            int64_t V, int64_t row_stride, float temperature,
+                            const specverify_lists *lists, const float *weight, void *grad,
+                            int64_t grad_stride, float *loss, void *cuda_stream) {
+    sv::TokenParams p;
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    if (rc == SPECVERIFY_OK) rc = list_params(p, lists);
+    if (rc != SPECVERIFY_OK || rows == 0) return rc;
+    if (!loss) return SPECVERIFY_ERR_INVALID_ARG;
+    rc = grad_params(p, dtype, grad, grad_stride);
+    if (rc != SPECVERIFY_OK) return rc;
+    const int64_t esz = dtype == SPECVERIFY_FP32 ? 4 : 2, n = rows * lists->K;
+    if (!grad_clear(p, esz, weight, rows * 4) || !grad_clear(p, esz, loss, rows * 4) ||
+        !grad_clear(p, esz, lists->ids, n * 4) ||
+        !grad_clear(p, esz, lists->target, n * (p.target_bf16 ? 2 : 4)))
+        return SPECVERIFY_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    if (guard.err != cudaSuccess) return map_cuda(guard.err);
+    p.weight = weight;
+    p.loss = loss;
+    return map_cuda(sv::launch_distill(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_device_status(specverify_t h, void *cuda_stream, int32_t *status_out) {

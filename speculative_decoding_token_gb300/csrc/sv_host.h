@@ -41,4 +41,10 @@ inline int check_device(int device) {
     return rc == SPECVERIFY_OK && device >= ndev ? SPECVERIFY_ERR_CUDA : rc;
 }
 
+// Whether [a, a + n) and [b, b + m) share a byte.
+inline bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
 }  // namespace sv

@@ -1,0 +1,52 @@
+// sv_token.h -- types shared by the host library and the kernels of the token
+// log-probability and distillation calls (not part of the public C ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "specverify.h"
+
+namespace sv {
+
+constexpr int kMaxAlternatives = SPECVERIFY_MAX_ALTERNATIVES;
+constexpr int kMaxList = SPECVERIFY_MAX_LIST;
+
+// A call over rows of logits. Row r is at logits + r * stride_bytes.
+struct TokenParams {
+    const char *logits;
+    int64_t stride_bytes, rows;
+    int32_t V;
+    float c;             // log2(e) / T
+    float inv_hi, inv_lo;  // 1 / T
+    int32_t *status;
+    // entries: rows with a token (log-probabilities) or with a list (distillation)
+    int64_t entries;
+    int32_t M;           // entries of a sequence (log-probabilities)
+    const int32_t *tokens;
+    const int64_t *row_off;
+    const int32_t *path;
+    int32_t k;
+    float *logprob, *entropy, *lse;
+    int32_t *rank;
+    float *top_logprob;
+    int32_t *top_idx;
+    // gradients
+    char *grad;
+    int64_t grad_stride_bytes;
+    const float *g_logprob, *g_entropy;
+    // distillation
+    int32_t K;
+    const int32_t *ids;
+    const char *target;
+    int32_t target_bf16, form, divergence;
+    float beta;
+    const float *weight;
+    float *loss;
+};
+
+cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_distill(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);  // grad: nullable
+
+}  // namespace sv

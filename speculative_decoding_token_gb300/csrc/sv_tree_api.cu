@@ -24,14 +24,9 @@ namespace {
 
 using sv::DeviceGuard;
 using sv::map_cuda;
+using sv::overlap;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Whether [a, a + n) and [b, b + m) share a byte.
-bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)m && y < x + (uintptr_t)n;
-}
 
 // A strided layout in bytes, to see whether its elements, or those of two buffers
 // laid out alike, keep to memory of their own: sorted by size, each stride has to be

@@ -1,0 +1,127 @@
+"""Host-side checks of the token log-probability and distillation calls (no GPU needed): refusals before any CUDA call,
+and the restatement in 64 bits that the GPU tests compare against, pinned by worked cases and by differences."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import token_util as tu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import speculative_decoding_token_gb300 as sv
+    sv.build()
+    return sv.load()
+
+
+def test_refusals_without_a_handle(lib):
+    from speculative_decoding_token_gb300 import losses
+    li = losses.SpecverifyLists(K=1)
+    rows = (None, None, 0, 1, 8, 8, 1.0)
+    assert lib.specverify_token_logprobs(*rows, 1, 1, None, None, None, 0, *[None] * 7) == -1
+    assert lib.specverify_token_logprobs_grad(*rows, None, None, None, None, 8, None, None, None) == -1
+    assert lib.specverify_distill_loss(*rows, ctypes.byref(li), None, None) == -1
+    assert lib.specverify_distill_grad(*rows, ctypes.byref(li), None, None, 8, None, None) == -1
+
+
+def test_struct_matches_the_header(lib):
+    from speculative_decoding_token_gb300 import losses
+    assert ctypes.sizeof(losses.SpecverifyLists) == 4 * 4 + 4 + 4 + 2 * 8
+
+
+def test_importing_the_package_needs_no_torch():
+    import subprocess
+    import sys
+    code = "import sys, speculative_decoding_token_gb300 as sv; assert 'torch' not in sys.modules; sv.TokenLogprobs"
+    subprocess.run([sys.executable, "-c", code], check=True)
+
+
+def test_binding_refuses_host_tensors_and_bad_shapes(lib):
+    import speculative_decoding_token_gb300 as sv
+    h = object.__new__(sv.SpecVerify)  # no CUDA here: a handle that every call refuses before using it
+    h.h, h.device = None, 0
+    z = torch.zeros(2, 8)
+    with pytest.raises(ValueError):
+        h.token_logprobs(z, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        h.distill_grad(z, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1))
+
+
+# -- the restatement
+
+def test_log_probabilities_of_worked_rows():
+    s = tu.Soft(torch.tensor([0.0, math.log(3.0)]), 1.0)
+    # ln 3 in fp32 is off by up to 2^-24, a log-probability by three quarters of that
+    assert abs(float(s.lp[0]) - math.log(0.25)) < 2.0 ** -24 and abs(float(s.lse) - math.log(4.0)) < 1e-7
+    assert abs(float(s.entropy) - (math.log(4) - 0.75 * math.log(3))) < 1e-7
+    s = tu.Soft(torch.tensor([1.0, 5.0, 5.0, -math.inf]), 2.0)
+    assert [s.rank(i) for i in range(4)] == [2, 0, 1, 3] and s.top(3).tolist() == [1, 2, 0]
+    u = tu.Soft(torch.full((7,), tu.LOWEST[torch.float32]), 1.0)  # masked by the lowest value, all of it: uniform
+    assert abs(float(u.entropy) - math.log(7)) < 1e-12 and abs(float(u.lp[3]) + math.log(7)) < 1e-12
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.75])
+def test_log_probability_gradient_by_differences(T):
+    z = tu.logits(1, 37, torch.float32, 3)[0].double()
+    for y, g, h in ((5, 1.0, 0.0), (0, -0.3, 0.7), (36, 0.0, 1.0)):
+        f = lambda x: g * tu.Soft(x, T).lp[y] + h * tu.Soft(x, T).entropy  # noqa: E731, B023
+        want, step = tu.Soft(z, T).grad(y, g, h)[0], 1e-5
+        for v in (0, 5, 17, 36):
+            e = torch.zeros_like(z)
+            e[v] = step
+            assert abs(float((f(z + e) - f(z - e)) / (2 * step)) - float(want[v])) < 1e-8
+
+
+@pytest.mark.parametrize("kind", ["fkl", "rkl", "jsd", "tvd"])
+@pytest.mark.parametrize("form", ["logprobs", "logits"])
+def test_divergence_gradient_by_differences(kind, form):
+    if kind == "rkl" and form == "logits":
+        pytest.skip("infinite")
+    z = tu.logits(2, 41, torch.float32, 5).double()
+    ids, t = tu.lists(z, 6, 5, form, 1.25)
+    for r in range(2):
+        f = lambda x: tu.Divergence(x, ids[r], t[r], 1.25, kind, form, 0.3)  # noqa: E731, B023
+        want, step = f(z[r]).grad, 1e-5
+        for v in list(range(8)) + ids[r][ids[r] >= 0].tolist():
+            e = torch.zeros(41, dtype=torch.float64)
+            e[v] = step
+            assert abs(float((f(z[r] + e).loss - f(z[r] - e).loss) / (2 * step)) - float(want[v])) < 1e-8
+
+
+def test_divergences_of_worked_rows():
+    # a draft of 1/2, 1/4, 1/4; the target lists the first token alone, with 3/4
+    z, ids = torch.tensor([math.log(2.0), 0.0, 0.0], dtype=torch.float64), torch.tensor([0])
+    t = torch.tensor([math.log(0.75)], dtype=torch.float64)
+    D = lambda kind, **k: float(tu.Divergence(z, ids, t, 1.0, kind, **k).loss)  # noqa: E731
+    assert abs(D("tvd") - 0.25) < 1e-9
+    assert abs(D("fkl") - (0.75 * math.log(1.5) + 0.25 * math.log(0.5))) < 1e-9
+    assert abs(D("rkl") - (0.5 * math.log(2 / 3) + 0.5 * math.log(2))) < 1e-9
+    m = (0.625, 0.375)
+    want = 0.5 * (0.75 * math.log(0.75 / m[0]) + 0.25 * math.log(0.25 / m[1])
+                  + 0.5 * math.log(0.5 / m[0]) + 0.5 * math.log(0.5 / m[1]))
+    assert abs(D("jsd") - want) < 1e-9
+    # over the list alone the target is the first token: -ln 1/2
+    assert abs(D("fkl", form="logits") - math.log(2)) < 1e-9
+    # the draft's own distribution, complete or not, is at no distance
+    lp = tu.Soft(z, 1.0).lp
+    for kind in ("fkl", "rkl", "jsd", "tvd"):
+        assert abs(float(tu.Divergence(z, torch.tensor([0, 2]), lp[[0, 2]], 1.0, kind).loss)) < 1e-9
+
+
+def test_a_planted_mistake_fails_the_differences():
+    """The gradient without the rest's share, or with the temperature left out, is not the difference quotient's."""
+    z = tu.logits(1, 20, torch.float32, 8).double()
+    ids, t = tu.lists(z, 4, 8, "logprobs", 2.0, short=False)
+    d = tu.Divergence(z[0], ids[0], t[0], 2.0, "fkl")
+    step, e = 1e-5, torch.zeros(20, dtype=torch.float64)
+    v = next(v for v in range(20) if v not in ids[0])
+    e[v] = step
+    diff = float((tu.Divergence(z[0] + e, ids[0], t[0], 2.0, "fkl").loss
+                  - tu.Divergence(z[0] - e, ids[0], t[0], 2.0, "fkl").loss) / (2 * step))
+    q = float(d.soft.p[v])
+    for wrong in (q / 2.0, float(d.grad[v]) * 2.0):
+        assert abs(diff - wrong) > 1e-4 * q
+    assert np.isclose(diff, float(d.grad[v]), rtol=1e-4)
