@@ -240,6 +240,7 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     p.inv_hi = (float)(1.0 / (double)T);
     p.inv_lo = (float)(1.0 / (double)T - (double)p.inv_hi);
     p.status = h->base.status;
+    p.wait_ns = h->wait_ns;
     p.entries = rows;
     p.M = 1;
     return SPECVERIFY_OK;
@@ -316,6 +317,7 @@ int specverify_create(specverify_t *out, int device, int32_t max_batch, int32_t 
     if (e == cudaSuccess) e = sv::prepare_features();
     if (e == cudaSuccess) e = sv::prepare_restricted();
     if (e == cudaSuccess) e = sv::prepare_small();
+    if (e == cudaSuccess) e = sv::prepare_token();
     if (e != cudaSuccess) {
         delete h;
         return map_cuda(e);

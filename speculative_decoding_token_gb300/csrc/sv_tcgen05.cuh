@@ -12,32 +12,6 @@
 
 namespace sv {
 
-// What a look at a barrier takes that does not open meanwhile (measured: 1.0 us,
-// whatever time it is asked to take).
-constexpr uint64_t kLookNs = 1000;
-
-// A whole warp's wait, the same outcome for every lane (what follows a wait are
-// instructions of whole warps). It gives up after `limit` nanoseconds, or once
-// another of the CTA has (`abort`, in shared memory), and the status says so. A
-// warp that gave up touches nothing that is shared and arrives at no barrier of
-// this kind any more: whoever needs it gives up in turn, and nobody takes for
-// done what was not. What a CTA waits for before it exits (its copies and products
-// in flight) has the fixed bound of mbar_wait_bounded.
-__device__ __forceinline__ bool wait_on(uint64_t &bar, uint32_t parity, int32_t &abort,
-                                        int32_t *status, uint64_t limit) {
-    constexpr uint32_t all = 0xffffffffu;
-    const uint32_t at = smem_u32(&bar);
-    if (__all_sync(all, mbar_try_wait(at, parity))) return true;
-    const uint64_t t0 = global_ns() - kLookNs;
-    while (!__any_sync(all, global_ns() - t0 > limit)) {
-        if (__all_sync(all, mbar_try_wait(at, parity))) return true;
-        if (__any_sync(all, *(volatile int32_t *)&abort)) return false;
-    }
-    *(volatile int32_t *)&abort = 1;
-    atomicOr(status, SPECVERIFY_STATUS_TIMEOUT);
-    return false;
-}
-
 // --- tensor memory -----------------------------------------------------------
 // One warp; the address of column 0 goes to shared memory at `dst`.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {

@@ -20,6 +20,7 @@ struct TokenParams {
     float c;             // log2(e) / T
     float inv_hi, inv_lo;  // 1 / T
     int32_t *status;
+    uint64_t wait_ns;    // bound of a wait inside the kernel
     // entries: rows with a token (log-probabilities) or with a list (distillation)
     int64_t entries;
     int32_t M;           // entries of a sequence (log-probabilities)
@@ -45,6 +46,7 @@ struct TokenParams {
     float *loss;
 };
 
+cudaError_t prepare_token();
 cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
 cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
 cudaError_t launch_distill(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);  // grad: nullable
