@@ -233,7 +233,7 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
  * Log-probabilities of given tokens and distillation of a draft, on rows of
  * logits as in specverify_row_features: `logits` of dtype SPECVERIFY_FP32 or
  * SPECVERIFY_BF16, `rows` rows of V logits (V < 2^31), row_stride elements
- * apart, 16-byte aligned; one temperature T > 0 (1 / T a normal float). x = row / T, lse =
+ * apart, 16-byte aligned; one temperature T, 2^-20 <= T <= 2^20. x = row / T, lse =
  * ln sum_v exp(x_v). A logit of -inf is a masked token, of probability 0. The
  * calls use the handle's device and its sticky status word and no workspace:
  * unlike the others, they may run beside one another and inside captured graphs

@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
-#include <limits>
 #include <new>
 #include <vector>
 
@@ -224,9 +223,7 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     if (!h || rows < 0 || rows > (int64_t)1 << 40 || V < 1 || V > INT32_MAX)
         return SPECVERIFY_ERR_INVALID_ARG;
     if (dtype != SPECVERIFY_FP32 && dtype != SPECVERIFY_BF16) return SPECVERIFY_ERR_INVALID_ARG;
-    // log2(e) / T has to be a number as well
-    if (!(T >= 4 * std::numeric_limits<float>::min() && T <= 0.25f / std::numeric_limits<float>::min()))
-        return SPECVERIFY_ERR_INVALID_ARG;
+    if (!(T >= 0x1p-20f && T <= 0x1p20f)) return SPECVERIFY_ERR_INVALID_ARG;
     const int64_t esz = dtype == SPECVERIFY_FP32 ? 4 : 2;
     if (rows > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & 15) != 0 || row_stride < V ||
                      row_stride > INT64_MAX / (8 * rows) || (row_stride * esz) % 16 != 0))
@@ -317,7 +314,9 @@ int specverify_create(specverify_t *out, int device, int32_t max_batch, int32_t 
     if (e == cudaSuccess) e = sv::prepare_features();
     if (e == cudaSuccess) e = sv::prepare_restricted();
     if (e == cudaSuccess) e = sv::prepare_small();
-    if (e == cudaSuccess) e = sv::prepare_token();
+    if (e == cudaSuccess) e = sv::prepare_logprobs();
+    if (e == cudaSuccess) e = sv::prepare_logprobs_grad();
+    if (e == cudaSuccess) e = sv::prepare_distill();
     if (e != cudaSuccess) {
         delete h;
         return map_cuda(e);
@@ -647,7 +646,7 @@ int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype,
     p.rank = rank;
     p.top_logprob = topk_logprob;
     p.top_idx = topk_idx;
-    return map_cuda(sv::launch_token_logprobs(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_token_logprobs(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -672,7 +671,7 @@ int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t d
     p.g_entropy = grad_entropy;
     p.logprob = logprob;
     p.entropy = entropy;
-    return map_cuda(sv::launch_token_logprobs_grad(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_token_logprobs_grad(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -686,7 +685,7 @@ int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, i
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
     p.loss = loss;
-    return map_cuda(sv::launch_distill(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_distill(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -709,7 +708,7 @@ int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, i
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
     p.weight = weight;
     p.loss = loss;
-    return map_cuda(sv::launch_distill(p, dtype, h->num_sms, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_distill(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_device_status(specverify_t h, void *cuda_stream, int32_t *status_out) {

@@ -1,4 +1,5 @@
-// sv_token.cu -- log-probabilities of given tokens (with entropy, rank and top
+// sv_token.cuh -- the kernel of the calls on log-probabilities and distillation:
+// log-probabilities of given tokens (with entropy, rank and top
 // alternatives), the divergence of a draft's rows from its target's top tokens,
 // and the gradients of both: one pass over rows of logits.
 //
@@ -18,6 +19,8 @@
 //                  tokens, writes the results, and hands the consumers what a
 //                  gradient's second reading needs.
 // No warp waits for the end of a row but the consumers of a gradient.
+#pragma once
+
 #include "sv_token.h"
 #include "sv_rows.cuh"
 #include "sv_tree.h"
@@ -31,19 +34,29 @@ namespace token {
 constexpr int kConsumers = 8;                     // warps
 constexpr int kScout = kConsumers, kProducer = kScout + 1, kPatcher = kProducer + 1, kEpilogue = kPatcher + 1;
 constexpr int kThreads = (kEpilogue + 1) * 32;
-constexpr int kVecs = 2;                          // 16-byte vectors of a chunk that a thread takes
-constexpr int kChunkVecs = kConsumers * 32 * kVecs;
-constexpr int kChunkBytes = kChunkVecs * 16;
+constexpr int kTeam = kConsumers * 32;            // a thread takes every kTeam-th 16-byte vector of a chunk
 constexpr int kMaxSlots = 26;
 constexpr int kDepth = 4;                         // rows between the scout and the epilogue at most
 constexpr int kTopDepth = 2;                      // the same where top tokens are asked for (their buffers are large)
 constexpr int kMaxCluster = 16;
-constexpr int kCandidates = kChunkVecs + 128;     // vectors that may hold top tokens: a chunk of ties, and more
+constexpr int kCandidates = 1536;                 // vectors that may hold top tokens: a chunk of ties, and more
 constexpr int kKeys = 1024;                       // tokens among them
 constexpr int kGathered = 512;                    // keys that a cluster's CTAs send to its first
 constexpr int kHash = 1024;
 
-enum State { kLive = 0, kSkip = 1, kBad = 2 };
+enum State { kLive = 0, kSkip = 1, kBad = 2, kEnd = 3 };
+
+// What a kernel is compiled for.
+template <int kDtype, bool kIsList, bool kIsGrad, bool kHasEntropy, bool kHasTop, bool kHasRank>
+struct Kind {
+    static constexpr int DT = kDtype;
+    static constexpr bool List = kIsList, Grad = kIsGrad, Ent = kHasEntropy, Top = kHasTop, Rank = kHasRank;
+    static constexpr int kSize = DT == SV_DT_FP32 ? 4 : 2;
+    static constexpr int kPer = 16 / kSize;  // logits of a vector
+    static constexpr uint32_t kNegInf = DT == SV_DT_FP32 ? 0xff800000u : 0xff80ff80u;
+    static constexpr int kVecs = Grad ? 2 : 4;  // of a chunk, a thread
+    static constexpr int kChunkVecs = kTeam * kVecs, kChunkBytes = kChunkVecs * 16;
+};
 
 // What the scout knows of a row.
 struct Row {
@@ -56,8 +69,8 @@ struct Row {
     float g, h;    // what the gradient is multiplied by
 };
 
-// Sums over part of a row: s and t relative to m (see above); n tokens before
-// the given one, -1: a bad logit.
+// Sums over part of a row: s of 2^x and t of 2^x x, x = (z - m) c; n tokens
+// before the given one, -1: a bad logit.
 struct Part {
     float m, s, t;
     int n;
@@ -66,11 +79,13 @@ struct Part {
 struct Shared {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots];
     uint64_t row_full[kDepth], row_free[kDepth], summed[kDepth], known[kDepth], stored[kDepth], bounded[kDepth];
-    uint64_t exchanged[2];
+    uint64_t exchanged[2], granted;
+    uint4 grant;          // the answer to a request for another row
     Row row[kDepth];
     Part part[kDepth][kConsumers];
     Part others[2][kMaxCluster];
-    float4 coef[kDepth];  // of the gradient: reference, factor, slope
+    float4 coef[kDepth];  // of the gradient: reference, factor, slope; what the epilogue puts right in it
+    int fix[kDepth];
     int32_t abort;
 };
 
@@ -78,12 +93,11 @@ struct Shared {
 // token's, inverted: keys fall in the order of alternatives, and 0 is none.
 struct SharedTop {
     unsigned long long bound[kTopDepth][kConsumers];  // that many tokens are at least so large; chunk
-    uint4 vec[kTopDepth][kCandidates];
-    int32_t at[kTopDepth][kCandidates];
+    int32_t at[kTopDepth][kCandidates];            // vectors of the row with a token that reaches the bound of its time
     unsigned long long keys[kKeys];
     unsigned long long best[kMaxAlternatives];
     unsigned long long gathered[kGathered];
-    unsigned count[kTopDepth];
+    unsigned count[kTopDepth], found;
 };
 
 struct SharedList {
@@ -99,6 +113,7 @@ struct Plan {
     int32_t slots;        // of a ring
     int32_t slice_vecs;   // vectors of a slice, but the last's
     int32_t lag;          // rows between the two readings of a gradient
+    int32_t dynamic;      // a CTA takes its next row when it is free for it (else rows are dealt out)
     int32_t depth_log;    // rows between the scout and the epilogue
     int32_t clusters;
     int32_t smem;
@@ -153,13 +168,6 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-
-template <int DT>
-struct Type {
-    static constexpr int kSize = DT == SV_DT_FP32 ? 4 : 2;
-    static constexpr int kPer = 16 / kSize;  // logits of a vector
-    static constexpr uint32_t kNegInf = DT == SV_DT_FP32 ? 0xff800000u : 0xff80ff80u;
-};
 
 // Pair i of a vector's logits.
 template <int DT>
@@ -224,9 +232,16 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
-// The least exponent argument that is told from -inf: a weight of 0 either way,
-// and its product with the argument is 0 and not NaN.
+// Logits are told from -inf down to here: a weight of 0 either way (T >= 2^-20),
+// and its product with the exponent is 0 and not NaN.
 constexpr float kFar = -0x1p100f;
+constexpr uint32_t kFarBf16x2 = 0xf180f180u;
+// Rows of a larger maximum than this, either way, take exponents (z - m) c, with
+// the difference first; the others z c - R with R = m c rounded: one FMA, whose
+// product is exact, and what R's rounding shifts is made good in the sum.
+constexpr float kPlain = 0x1p90f;
+
+__device__ __forceinline__ bool plain(float m) { return fabsf(m) < kPlain; }
 
 __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
     a.n = a.n < 0 || b.n < 0 ? -1 : a.n + b.n;
@@ -238,9 +253,9 @@ __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
         return;
     }
     const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf(a.m - m, kFar), db = fmaxf(b.m - m, kFar);
-    const float fa = ex2_approx(da * c), fb = ex2_approx(db * c);
-    a.t = fa * fmaf(da, a.s, a.t) + fb * fmaf(db, b.s, b.t);
+    const float xa = fmaxf(a.m - m, kFar) * c, xb = fmaxf(b.m - m, kFar) * c;
+    const float fa = ex2_approx(xa), fb = ex2_approx(xb);
+    a.t = fa * fmaf(xa, a.s, a.t) + fb * fmaf(xb, b.s, b.t);
     a.s = fa * a.s + fb * b.s;
     a.m = m;
 }
@@ -276,10 +291,19 @@ __device__ __forceinline__ void cluster_arrive(const uint64_t &bar, uint32_t ran
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(&bar, rank)) : "memory");
 }
 
-// wait_on for what other CTAs of the cluster have sent
-__device__ __forceinline__ bool wait_on_cluster(uint64_t &bar, uint32_t parity, int32_t &abort, int32_t *status,
-                                                uint64_t limit) {
-    if (!wait_on(bar, parity, abort, status, limit)) return false;
+// The wait of every role: see wait_on. Most are over at the first look.
+__device__ __noinline__ bool wait_longer(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
+    return wait_on(bar, parity, S.abort, P.status, P.wait_ns);
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
+    return wait_longer(bar, parity, S, P);
+}
+
+// The same for what other CTAs of the cluster have sent
+__device__ __forceinline__ bool wait_on_cluster(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
+    if (!wait_bar(bar, parity, S, P)) return false;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     return true;
 }
@@ -287,7 +311,7 @@ __device__ __forceinline__ bool wait_on_cluster(uint64_t &bar, uint32_t parity, 
 // A CTA's view of the call.
 struct Cta {
     int rank, cluster;
-    long long first, step;   // entries
+    long long first;         // entry
     int slice0, slice_vecs;  // vectors of the row
     int chunks;
     int lane;
@@ -300,57 +324,129 @@ struct Cta {
 // ---------------------------------------------------------------------------
 // consumers
 
-// The sums of a row's slice, vectors of chunk after chunk. G: its chunks stay for the gradient.
-template <int DT, bool LIST, bool G>
+// The logits of the row's ragged end, which no copy brings, with -inf behind them.
+template <class Kd>
+__device__ __forceinline__ uint4 ragged_end(const char *row, int whole, int rest) {
+    uint32_t x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        x[q] = Kd::kNegInf;
+#pragma unroll
+        for (int e = 0; e < 4 / Kd::kSize; ++e) {
+            const int at = q * (4 / Kd::kSize) + e;
+            if (at >= rest) continue;
+            const char *p = row + ((int64_t)whole * Kd::kPer + at) * Kd::kSize;
+            if (Kd::DT == SV_DT_FP32) x[q] = *reinterpret_cast<const volatile uint32_t *>(p);
+            else x[q] = (x[q] & ~(0xffffu << (16 * e))) | (uint32_t)*reinterpret_cast<const volatile uint16_t *>(p) << (16 * e);
+        }
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The maximum of a vector, NaN if there is one: bf16 as a pair of them, still packed.
+template <int DT>
+__device__ __forceinline__ uint32_t packed_max(const uint4 &w) {
+    if (DT == SV_DT_FP32) return __float_as_uint(vec_max<DT>(w));
+    return max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t packed_max(uint32_t a, uint32_t b) {
+    if (DT == SV_DT_FP32) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    return max_nan_bf16x2(a, b);
+}
+
+template <int DT>
+__device__ __forceinline__ float from_packed_max(uint32_t x) {
+    return DT == SV_DT_FP32 ? __uint_as_float(x) : max_nan(bf16_lo(x), bf16_hi(x));
+}
+
+// Word i of a vector, or pair i of fp32 logits, as two floats; with the entropy, no less than kFar.
+template <class Kd>
+__device__ __forceinline__ f32x2 logits2(const uint4 &w, int i) {
+    if (Kd::DT == SV_DT_FP32) {
+        float lo = __uint_as_float(i == 0 ? w.x : w.z), hi = __uint_as_float(i == 0 ? w.y : w.w);
+        if (Kd::Ent) {
+            lo = fmaxf(lo, kFar);
+            hi = fmaxf(hi, kFar);
+        }
+        return pack2(lo, hi);
+    }
+    uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    if (Kd::Ent) x = max_bf16x2(x, kFarBf16x2);
+    return pack2(bf16_lo(x), bf16_hi(x));
+}
+
+// The exponents of pair i where the row's maximum is not a plain number.
+template <class Kd>
+__device__ __forceinline__ f32x2 far_exponents2(const uint4 &w, int i, float m, float c) {
+    const float2 z = pair_of<Kd::DT>(w, i);
+    return pack2(fmaxf(z.x - m, kFar) * c, fmaxf(z.y - m, kFar) * c);
+}
+
+// Tokens of a vector before the given one (logit zy, token y): those larger, and equal ones of a lower index. first: the
+// vector's first token.
+template <class Kd>
+__device__ __forceinline__ int count_before(const uint4 &w, float zy, int y, int first) {
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < Kd::kPer / 2; ++q) {
+        const float2 z = pair_of<Kd::DT>(w, q);
+        n += (z.x > zy || (z.x == zy && first + 2 * q < y)) ? 1 : 0;
+        n += (z.y > zy || (z.y == zy && first + 2 * q + 1 < y)) ? 1 : 0;
+    }
+    return n;
+}
+
+// The sums of a row's slice, chunk after chunk. A gradient's chunks stay for its second reading.
+template <class Kd>
 __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
                                           const Cta &cta, int d, uint32_t row_parity, int &slot, uint32_t &phase) {
-    using Ty = Type<DT>;
+    constexpr int kVecs = Kd::kVecs, kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane, warp = tid >> 5;
-    const Row &row = S.row[d];
-    const bool ent = !LIST && (P.entropy || P.g_entropy);
-    const bool rank = !LIST && !G && P.rank;
-    const int k = LIST || G ? 0 : P.k;
-    const int nth = (k + kConsumers - 1) / kConsumers;
-    const int whole = P.V / Ty::kPer, rest = P.V - whole * Ty::kPer;
-    float m = -INFINITY;
+    const int nth = Kd::Top ? (P.k + kConsumers - 1) / kConsumers : 1;
+    const int whole = P.V / kPer, rest = P.V - whole * kPer;
+    float m = -INFINITY, R = 0.0f;
     f32x2 s0 = 0ull, s1 = 0ull, t0 = 0ull, t1 = 0ull;
     bool bad = false;
     int before = 0;
-    uint32_t bound = 0;     // order bits that a vector has to reach
-    int bound_chunk = 0;    // and pass, in later chunks than this one
-    const f32x2 c2 = pack2(P.c, P.c);
+    float least = -INFINITY;  // what a vector has to reach to hold a top token,
+    int least_chunk = 0;      // and in later chunks than this one to pass
+    const float c = P.c;
+    const f32x2 c2 = pack2(c, c);
     for (int i = 0; i < cta.chunks; ++i) {
-        if (!wait_on(S.full[slot], phase, S.abort, P.status, P.wait_ns)) return false;
-        if (LIST && !wait_on(S.ready[slot], phase, S.abort, P.status, P.wait_ns)) return false;
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * kChunkBytes);
-        const int n = min(kChunkVecs, cta.slice_vecs - i * kChunkVecs);
-        const int v0 = cta.slice0 + i * kChunkVecs;  // of the row
+        if (!wait_bar(S.full[slot], phase, S, P)) return false;
+        if (Kd::List && !wait_bar(S.ready[slot], phase, S, P)) return false;
+        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * Kd::kChunkBytes);
+        const int v0 = i * Kd::kChunkVecs;  // of the slice
+        const int n = cta.slice_vecs - v0;
         uint4 w[kVecs];
-        float vm[kVecs];
+        if (n >= Kd::kChunkVecs && cta.slice0 + v0 + Kd::kChunkVecs <= whole) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int v = tid + j * kConsumers * 32;
-            if (v < n) w[j] = chunk[v];
-            else w[j] = make_uint4(Ty::kNegInf, Ty::kNegInf, Ty::kNegInf, Ty::kNegInf);
-            if (!LIST && rest && v < n && v0 + v == whole) {  // the ragged end of the row, which no copy brings
-                uint32_t x[4];
+            for (int j = 0; j < kVecs; ++j) w[j] = chunk[tid + j * kTeam];
+        } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    x[q] = Ty::kNegInf;
-#pragma unroll
-                    for (int e = 0; e < 4 / Ty::kSize; ++e) {
-                        const int at = q * (4 / Ty::kSize) + e;
-                        if (at >= rest) continue;
-                        const char *p = row.z + ((int64_t)whole * Ty::kPer + at) * Ty::kSize;
-                        if (DT == SV_DT_FP32) x[q] = *reinterpret_cast<const volatile uint32_t *>(p);
-                        else x[q] = (x[q] & ~(0xffffu << (16 * e))) |
-                                    (uint32_t)*reinterpret_cast<const volatile uint16_t *>(p) << (16 * e);
-                    }
-                }
-                w[j] = make_uint4(x[0], x[1], x[2], x[3]);
+            for (int j = 0; j < kVecs; ++j) {
+                const int v = tid + j * kTeam;
+                w[j] = make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
+                if (v >= n) continue;
+                if (!Kd::List && cta.slice0 + v0 + v == whole) w[j] = ragged_end<Kd>(S.row[d].z, whole, rest);
+                else w[j] = chunk[v];
             }
         }
-        if (!G) {
+        if (!Kd::Grad) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
         }
@@ -358,108 +454,114 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             slot = 0;
             phase ^= 1u;
         }
-        float cm = -INFINITY;
+        uint32_t pm[kVecs], all = 0;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            vm[j] = vec_max<DT>(w[j]);
-            cm = max_nan(cm, vm[j]);
+            pm[j] = packed_max<Kd::DT>(w[j]);
+            all = j == 0 ? pm[0] : packed_max<Kd::DT>(all, pm[j]);
         }
+        float cm = from_packed_max<Kd::DT>(all);
         if (!(cm < INFINITY)) {
             bad = true;
             cm = -INFINITY;
         }
         if (cm > m) {
+            const float next = cm * c;
             if (m != -INFINITY) {
-                const float dm = fmaxf(m - cm, kFar), f = ex2_approx(dm * P.c);
-                const f32x2 f2 = pack2(f, f), d2 = pack2(dm, dm);
-                if (ent) {
-                    t0 = mul2(f2, fma2(d2, s0, t0));
-                    t1 = mul2(f2, fma2(d2, s1, t1));
+                const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
+                const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
+                if (Kd::Ent) {
+                    t0 = mul2(f2, fma2(x2, s0, t0));
+                    t1 = mul2(f2, fma2(x2, s1, t1));
                 }
                 s0 = mul2(f2, s0);
                 s1 = mul2(f2, s1);
             }
             m = cm;
+            R = next;
         }
-        if (m != -INFINITY) {
-            const f32x2 nm = pack2(-m, -m);
+        if (plain(m)) {
+            const f32x2 nR = pack2(-R, -R);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-                for (int q = 0; q < Ty::kPer / 2; ++q) {
-                    const float2 z = pair_of<DT>(w[j], q);
-                    float2 dz = unpack2(add2(pack2(z.x, z.y), nm));
-                    if (ent) {
-                        dz.x = fmaxf(dz.x, kFar);
-                        dz.y = fmaxf(dz.y, kFar);
-                    }
-                    const f32x2 d2 = pack2(dz.x, dz.y);
-                    const float2 x = unpack2(mul2(d2, c2));
+                for (int q = 0; q < kPer / 2; ++q) {
+                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q), c2, nR);
+                    const float2 x = unpack2(x2);
                     const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
                     if (q & 1) {
                         s1 = add2(s1, e2);
-                        if (ent) t1 = fma2(e2, d2, t1);
+                        if (Kd::Ent) t1 = fma2(e2, x2, t1);
                     } else {
                         s0 = add2(s0, e2);
-                        if (ent) t0 = fma2(e2, d2, t0);
+                        if (Kd::Ent) t0 = fma2(e2, x2, t0);
                     }
                 }
-        }
-        if (rank) {
-            const float zy = row.zy;
-            const int y = row.y;
-#pragma unroll
+        } else if (m != -INFINITY) {
+#pragma unroll 1
             for (int j = 0; j < kVecs; ++j) {
-                const int v = tid + j * kConsumers * 32;
-                // the indexes of what fills a short chunk belong to the next slice
-                const int e0 = v < n ? (v0 + v) * Ty::kPer : P.V;
+                const uint4 v = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2 % kVecs] : w[3 % kVecs];
 #pragma unroll
-                for (int q = 0; q < Ty::kPer / 2; ++q) {
-                    const float2 z = pair_of<DT>(w[j], q);
-                    before += (z.x > zy || (z.x == zy && e0 + 2 * q < y)) ? 1 : 0;
-                    before += (z.y > zy || (z.y == zy && e0 + 2 * q + 1 < y)) ? 1 : 0;
+                for (int q = 0; q < kPer / 2; ++q) {
+                    const f32x2 x2 = far_exponents2<Kd>(v, q, m, c);
+                    const float2 x = unpack2(x2);
+                    const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
+                    s0 = add2(s0, e2);
+                    if (Kd::Ent) t0 = fma2(e2, x2, t0);
                 }
             }
         }
-        if (k > 0) {
+        if (Kd::Rank) {
+            const float zy = S.row[d].zy;
+            const int y = S.row[d].y;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int v = v0 + tid + j * kTeam;
+                // the indexes of what fills a short chunk belong to the next slice
+                before += count_before<Kd>(w[j], zy, y, v < cta.slice_vecs ? (cta.slice0 + v) * kPer : P.V);
+            }
+        }
+        if (Kd::Top) {
             // Each warp bounds the k-th largest logit by the nth largest of its lanes' maxima: 8 warps have 8 nth >= k
             // tokens that large. The bound of the first chunk is everybody's; it then rises at chunks 1, 3, 7, ...
-            const bool last = i + 1 == cta.chunks;
-            if ((i & (i + 1)) == 0 || last) {
+            if ((i & (i + 1)) == 0 || i + 1 == cta.chunks) {
                 const uint32_t mine = warp_nth(order_bits(m), nth, lane);
                 if (lane == 0)
                     *(volatile unsigned long long *)&top->bound[d][warp] = ((unsigned long long)mine << 32) | (uint32_t)i;
                 if (i == 0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
-                    if (!wait_on(S.bounded[d], row_parity, S.abort, P.status, P.wait_ns)) return false;
+                    if (!wait_bar(S.bounded[d], row_parity, S, P)) return false;
                 }
             }
             if ((i & (i - 1)) == 0) {
                 const unsigned long long b = lane < kConsumers ? *(volatile unsigned long long *)&top->bound[d][lane] : ~0ull << 32;
-                bound = __reduce_min_sync(0xffffffffu, (uint32_t)(b >> 32));
-                bound_chunk = (int)__reduce_max_sync(0xffffffffu, (uint32_t)b);
+                least = from_order_bits(__reduce_min_sync(0xffffffffu, (uint32_t)(b >> 32)));
+                least_chunk = (int)__reduce_max_sync(0xffffffffu, (uint32_t)b);
             }
             // Tokens that equal the bound come after the ones that made it, once these lie in earlier chunks.
-            const float least = from_order_bits(bound);
-            const bool strict = i > bound_chunk;
+            const bool strict = i > least_chunk;
+            if (cm >= least && (!strict || cm > least)) {
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int v = tid + j * kConsumers * 32;
-                if (v < n && (strict ? vm[j] > least : vm[j] >= least)) {
-                    const unsigned at = atomicAdd(&top->count[d], 1u);
-                    if (at < kCandidates) {
-                        top->vec[d][at] = w[j];
-                        top->at[d][at] = v0 + v;
+                for (int j = 0; j < kVecs; ++j) {
+                    const float x = from_packed_max<Kd::DT>(pm[j]);
+                    if (tid + j * kTeam < n && (strict ? x > least : x >= least)) {
+                        const unsigned at = atomicAdd(&top->count[d], 1u);
+                        if (at < kCandidates) top->at[d][at] = cta.slice0 + v0 + tid + j * kTeam;
                     }
                 }
             }
         }
     }
-    if (k > 0 && cta.chunks == 0 && lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
+    if (Kd::Top && cta.chunks == 0 && lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
     Part p{m, (a.x + a.y) + (b.x + b.y), (e.x + e.y) + (f.x + f.y), bad ? -1 : before};
-    p = warp_merge(p, P.c);
+    if (plain(m)) {  // what R was off by
+        const float r = fmaf(m, c, -R), g = ex2_approx(-r);
+        p.t = g * fmaf(-r, p.s, p.t);
+        p.s *= g;
+    }
+    p = warp_merge(p, c);
     if (lane == 0) {
         S.part[d][warp] = p;
         mbar_arrive(smem_u32(&S.summed[d]));
@@ -467,76 +569,70 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     return true;
 }
 
-// The gradient of a row's slice.
-template <int DT, bool LIST>
+// The gradient of a row's slice: 2^x (a + b x) for x = (z - m) c.
+template <class Kd>
 __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &plan, Shared &S, const uint8_t *ring, const Cta &cta,
                                             int d, uint32_t row_parity, int &slot) {
-    using Ty = Type<DT>;
+    constexpr int kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane;
-    const int whole = P.V / Ty::kPer, rest = P.V - whole * Ty::kPer;
+    const int whole = P.V / kPer, rest = P.V - whole * kPer;
     const int state = S.row[d].state;
-    char *out = P.grad + S.row[d].entry * P.grad_stride_bytes;
-    float4 cf = make_float4(0.0f, state == kBad ? NAN : 0.0f, 0.0f, 0.0f);
+    char *out = P.grad + S.row[d].entry * P.grad_stride_bytes + (int64_t)cta.slice0 * 16;
+    float m = 0.0f, fa = state == kBad ? NAN : 0.0f, fb = 0.0f;
     if (state == kLive) {
-        if (!wait_on(S.known[d], row_parity, S.abort, P.status, P.wait_ns)) return false;
-        cf = S.coef[d];
+        if (!wait_bar(S.known[d], row_parity, S, P)) return false;
+        const float4 cf = S.coef[d];
+        m = cf.x;
+        fa = cf.y;
+        fb = cf.z;
     }
-    const bool ent = !LIST && P.g_entropy;
-    const f32x2 nm = pack2(-cf.x, -cf.x), c2 = pack2(P.c, P.c), a2 = pack2(cf.y, cf.y), b2 = pack2(cf.z, cf.z);
+    const float c = P.c, R = m * c;
+    const bool near = plain(m);
+    if (near) {
+        const float r = fmaf(m, c, -R), g = ex2_approx(-r);
+        fa = g * fmaf(-r, fb, fa);
+        fb *= g;
+    }
+    const f32x2 nR = pack2(-R, -R), c2 = pack2(c, c), a2 = pack2(fa, fa), b2 = pack2(fb, fb);
     for (int i = 0; i < cta.chunks; ++i) {
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * kChunkBytes);
-        const int n = min(kChunkVecs, cta.slice_vecs - i * kChunkVecs);
-        const int v0 = cta.slice0 + i * kChunkVecs;
+        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * Kd::kChunkBytes);
+        const int v0 = i * Kd::kChunkVecs;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int v = tid + j * kConsumers * 32;
-            if (v >= n) continue;
-            float g[Ty::kPer];
+        for (int j = 0; j < Kd::kVecs; ++j) {
+            const int v = v0 + tid + j * kTeam;  // of the slice
+            if (v >= cta.slice_vecs) continue;
+            const bool end = cta.slice0 + v >= whole;
+            f32x2 g[kPer / 2];
             if (state == kLive) {
-                uint4 w = chunk[v];
-                if (!LIST && rest && v0 + v == whole) {
-                    uint32_t x[4] = {0, 0, 0, 0};
+                uint4 w = chunk[tid + j * kTeam];
+                if (!Kd::List && end) w = ragged_end<Kd>(S.row[d].z, whole, rest);
 #pragma unroll
-                    for (int q = 0; q < Ty::kPer; ++q) {
-                        if (q >= rest) continue;
-                        const char *p = S.row[d].z + ((int64_t)whole * Ty::kPer + q) * Ty::kSize;
-                        if (DT == SV_DT_FP32) x[q & 3] = *reinterpret_cast<const volatile uint32_t *>(p);
-                        else x[(q >> 1) & 3] |= (uint32_t)*reinterpret_cast<const volatile uint16_t *>(p) << (16 * (q & 1));
-                    }
-                    w = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-#pragma unroll
-                for (int q = 0; q < Ty::kPer / 2; ++q) {
-                    const float2 z = pair_of<DT>(w, q);
-                    float2 dz = unpack2(add2(pack2(z.x, z.y), nm));
-                    if (ent) {
-                        dz.x = fmaxf(dz.x, kFar);
-                        dz.y = fmaxf(dz.y, kFar);
-                    }
-                    const f32x2 d2 = pack2(dz.x, dz.y);
-                    const float2 x = unpack2(mul2(d2, c2));
-                    const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
-                    const float2 r = unpack2(mul2(e2, ent ? fma2(b2, d2, a2) : a2));
-                    g[2 * q] = r.x;
-                    g[2 * q + 1] = r.y;
+                for (int q = 0; q < kPer / 2; ++q) {
+                    const f32x2 x2 = near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c);
+                    const float2 x = unpack2(x2);
+                    g[q] = mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
                 }
             } else {
 #pragma unroll
-                for (int q = 0; q < Ty::kPer; ++q) g[q] = cf.y;
+                for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
             }
-            char *to = out + (int64_t)(v0 + v) * 16;
-            if (v0 + v < whole) {
+            char *to = out + (int64_t)v * 16;
+            if (!end) {
                 uint4 r;
-                if (DT == SV_DT_FP32)
-                    r = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
-                else
-                    r = make_uint4(to_bf16x2(g[0], g[1]), to_bf16x2(g[2], g[3]), to_bf16x2(g[4 % Ty::kPer], g[5 % Ty::kPer]),
-                                   to_bf16x2(g[6 % Ty::kPer], g[7 % Ty::kPer]));
+                const float2 x = unpack2(g[0]), y = unpack2(g[1]);
+                if (Kd::DT == SV_DT_FP32) {
+                    r = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+                } else {
+                    const float2 z = unpack2(g[2 % (kPer / 2)]), u = unpack2(g[3 % (kPer / 2)]);
+                    r = make_uint4(to_bf16x2(x.x, x.y), to_bf16x2(y.x, y.y), to_bf16x2(z.x, z.y), to_bf16x2(u.x, u.y));
+                }
                 *reinterpret_cast<uint4 *>(to) = r;
             } else {
 #pragma unroll
-                for (int q = 0; q < Ty::kPer; ++q)
-                    if (q < rest) store_logit<DT>(to, q, g[q]);
+                for (int q = 0; q < kPer; ++q) {
+                    const float2 x = unpack2(g[q / 2]);
+                    if (q < rest) store_logit<Kd::DT>(to, q, q & 1 ? x.y : x.x);
+                }
             }
         }
         if (state == kLive) {
@@ -550,80 +646,171 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
     return true;
 }
 
-template <int DT, bool LIST, bool G>
+template <class Kd>
 __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
                                         const Cta &cta) {
     int slot = 0, gslot = 0, r = 0;
     uint32_t phase = 0;
     auto store = [&](int g) {
         const int d = cta.place(g);
-        if (!store_slice<DT, LIST>(P, plan, S, ring, cta, d, cta.parity(g), gslot)) return false;
+        if (!store_slice<Kd>(P, plan, S, ring, cta, d, cta.parity(g), gslot)) return false;
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
         return true;
     };
-    for (long long e = cta.first; e < P.entries; e += cta.step, ++r) {
+    for (;; ++r) {
         const int d = cta.place(r);
-        if (!wait_on(S.row_full[d], cta.parity(r), S.abort, P.status, P.wait_ns)) return;
+        if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
+        if (S.row[d].state == kEnd) break;
         if (S.row[d].state == kLive) {
-            if (!sum_slice<DT, LIST, G>(P, plan, S, top, ring, cta, d, cta.parity(r), slot, phase)) return;
+            if (!sum_slice<Kd>(P, plan, S, top, ring, cta, d, cta.parity(r), slot, phase)) return;
         } else if (cta.lane == 0) {
-            if (top) mbar_arrive(smem_u32(&S.bounded[d]));
+            if (Kd::Top) mbar_arrive(smem_u32(&S.bounded[d]));
             mbar_arrive(smem_u32(&S.summed[d]));
         }
-        if (!G) {
+        if (!Kd::Grad) {
             __syncwarp();
             if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
         } else if (r >= plan.lag && !store(r - plan.lag)) {
             return;
         }
     }
-    if (G && plan.lag && r > 0) store(r - 1);
+    if (Kd::Grad && plan.lag && r > 0) store(r - 1);
 }
 
 // ---------------------------------------------------------------------------
 // scout
 
+// The rows of a CTA (or cluster), one after another. Dynamic: the grid has a CTA for every row, and a CTA that runs takes
+// over, one at a time, the rows of those that have not begun (cluster launch control).
+struct Entries {
+    long long e;
+    uint32_t phase;
+    bool asked;
+
+    __device__ __forceinline__ void ask(Shared &S, int lane) {
+        if (lane == 0) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive_expect_tx(smem_u32(&S.granted), 16);
+            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                             smem_u32(&S.grant)),
+                         "r"(smem_u32(&S.granted))
+                         : "memory");
+        }
+        asked = true;
+    }
+    __device__ __forceinline__ void begin(const Plan &plan, Shared &S, const Cta &cta) {
+        e = cta.first;
+        phase = 0;
+        asked = false;
+        if (plan.dynamic) ask(S, cta.lane);
+    }
+    // e < 0 after the last one; false: gave up
+    __device__ __forceinline__ bool next(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta) {
+        if (!plan.dynamic) {
+            e += plan.clusters;
+            if (e >= P.entries) e = -1;
+            return true;
+        }
+        if (!wait_bar(S.granted, phase, S, P)) return false;
+        phase ^= 1u;
+        asked = false;
+        uint32_t more, x;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+            "ld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+            : "=r"(more), "=r"(x)
+            : "r"(smem_u32(&S.grant))
+            : "memory");
+        __syncwarp();
+        e = more ? (long long)x : -1;
+        if (more) ask(S, cta.lane);
+        return true;
+    }
+    // No answer outlives its CTA, also where the scout gave up.
+    __device__ __forceinline__ void end(Shared &S) {
+        if (asked) mbar_wait_bounded(smem_u32(&S.granted), phase);
+    }
+};
+
+// What is fetched of an entry ahead of its turn.
+struct Asked {
+    int y;
+    int64_t row;
+    float g, h;
+    int id[kMaxList / 32];
+    float t[kMaxList / 32];
+};
+
+template <bool LIST>
+__device__ __forceinline__ void fetch(const TokenParams &P, long long e, int lane, Asked &a) {
+    if (LIST) {
+#pragma unroll
+        for (int i = 0; i < kMaxList / 32; ++i) {
+            const int j = lane + 32 * i;
+            if (j >= P.K) continue;
+            a.id[i] = P.ids[e * P.K + j];
+            a.t[i] = P.target_bf16 ? plain_logit<SV_DT_BF16>(P.target, e * P.K + j) : plain_logit<SV_DT_FP32>(P.target, e * P.K + j);
+        }
+        a.g = P.weight ? P.weight[e] : 1.0f;
+    } else {
+        a.y = P.tokens[e];
+        a.row = e;
+        if (P.row_off) a.row = P.row_off[e / P.M] + (P.path ? (int64_t)P.path[e] : (int64_t)(e % P.M));
+        if (P.grad) {
+            a.g = P.g_logprob[e];
+            a.h = P.g_entropy ? P.g_entropy[e] : 0.0f;
+        }
+    }
+}
+
 template <int DT>
-__device__ __forceinline__ void scout_token(const TokenParams &P, Row &row, long long e) {
-    const int y = P.tokens[e];
-    int64_t r = e;
+__device__ __forceinline__ void scout_token(const TokenParams &P, Row &row, long long e, const Asked &a) {
     int bits = 0;
-    if (y != -1) {
-        if (P.row_off) r = P.row_off[e / P.M] + (P.path ? (int64_t)P.path[e] : (int64_t)(e % P.M));
-        if (y < 0 || y >= P.V) bits = SPECVERIFY_STATUS_BAD_TOKEN;
-        else if (r < 0 || r >= P.rows) bits = SPECVERIFY_STATUS_BAD_ROW;
+    if (a.y != -1) {
+        if (a.y < 0 || a.y >= P.V) bits = SPECVERIFY_STATUS_BAD_TOKEN;
+        else if (a.row < 0 || a.row >= P.rows) bits = SPECVERIFY_STATUS_BAD_ROW;
     }
-    row.z = P.logits + r * P.stride_bytes;
+    row.z = P.logits + a.row * P.stride_bytes;
     row.entry = e;
-    row.y = y;
-    row.state = y == -1 ? kSkip : bits ? kBad : kLive;
-    row.zy = row.state == kLive ? plain_logit<DT>(row.z, y) : 0.0f;
-    if (P.grad) {
-        row.g = P.g_logprob[e];
-        row.h = P.g_entropy ? P.g_entropy[e] : 0.0f;
-    }
+    row.y = a.y;
+    row.state = a.y == -1 ? kSkip : bits ? kBad : kLive;
+    row.zy = row.state == kLive ? plain_logit<DT>(row.z, a.y) : 0.0f;
+    row.g = a.g;
+    row.h = a.h;
     if (bits) atomicOr(P.status, bits);
 }
 
 // A list: its ids, the draft's logits of them, the target's log-probabilities.
 template <int DT>
-__device__ void scout_list(const TokenParams &P, Row &row, SharedList &L, int d, long long e, int lane) {
+__device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, SharedList &L, int d, long long e, int lane, const Asked &a) {
     constexpr uint32_t all = 0xffffffffu;
     const char *z = P.logits + e * P.stride_bytes;
     int bits = 0;
     bool any = false;
     float top = -INFINITY;
-    for (int j = lane; j < P.K; j += 32) {
-        int id = P.ids[e * P.K + j];
-        float zk = -INFINITY, t = -INFINITY;
+    float zk[kMaxList / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxList / 32; ++i) {
+        zk[i] = -INFINITY;
+        if (lane + 32 * i < P.K && a.id[i] >= 0 && a.id[i] < P.V) zk[i] = plain_logit<DT>(z, a.id[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxList / 32; ++i) {
+        const int j = lane + 32 * i;
+        if (j >= P.K) continue;
+        int id = a.id[i];
+        float t = -INFINITY;
         if (id < -1 || id >= P.V) {
             bits |= SPECVERIFY_STATUS_BAD_TOKEN;
             id = -1;
         } else if (id >= 0) {
             any = true;
-            zk = plain_logit<DT>(z, id);
-            t = P.target_bf16 ? plain_logit<SV_DT_BF16>(P.target, e * P.K + j) : plain_logit<SV_DT_FP32>(P.target, e * P.K + j);
-            if (!(zk < INFINITY) || !(t < INFINITY)) bits |= SPECVERIFY_STATUS_BAD_LOGIT;
+            t = a.t[i];
+            if (!(zk[i] < INFINITY) || !(t < INFINITY)) bits |= SPECVERIFY_STATUS_BAD_LOGIT;
             // twice the same id: one of its entries finds the other in the table
             uint32_t at = (uint32_t)id * 2654435761u >> 22;
             for (int tries = 0; tries < kHash; ++tries, at = (at + 1) % kHash) {
@@ -633,7 +820,7 @@ __device__ void scout_list(const TokenParams &P, Row &row, SharedList &L, int d,
             }
         }
         L.ids[d][j] = id;
-        L.z[d][j] = zk;
+        L.z[d][j] = zk[i];
         L.lp[d][j] = t;
         top = fmaxf(top, t);
     }
@@ -675,58 +862,67 @@ __device__ void scout_list(const TokenParams &P, Row &row, SharedList &L, int d,
         row.entry = e;
         row.state = bits ? kBad : any ? kLive : kSkip;
         row.p_rest = p_rest;
-        row.g = P.weight ? P.weight[e] : 1.0f;
+        row.g = a.g;
         if (bits) atomicOr(P.status, bits);
     }
 }
 
-template <int DT, bool LIST>
-__device__ __forceinline__ void scout(const TokenParams &P, Shared &S, SharedTop *top, SharedList *list, const Cta &cta) {
-    int r = 0;
-    for (long long e = cta.first; e < P.entries; e += cta.step, ++r) {
+template <class Kd>
+__device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, SharedList *list,
+                                      const Cta &cta) {
+    Entries at;
+    Asked a;
+    at.begin(plan, S, cta);
+    fetch<Kd::List>(P, at.e, cta.lane, a);
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
-        if (!wait_on(S.row_free[d], cta.parity(r) ^ 1u, S.abort, P.status, P.wait_ns)) return;
-        if (LIST) {
-            scout_list<DT>(P, S.row[d], *list, d, e, cta.lane);
+        if (!wait_bar(S.row_free[d], cta.parity(r) ^ 1u, S, P)) break;
+        if (at.e < 0) {
+            if (cta.lane == 0) S.row[d].state = kEnd;
+        } else if (Kd::List) {
+            scout_list<Kd::DT>(P, S.row[d], *list, d, at.e, cta.lane, a);
         } else if (cta.lane == 0) {
-            scout_token<DT>(P, S.row[d], e);
-            if (top) top->count[d] = 0;
+            scout_token<Kd::DT>(P, S.row[d], at.e, a);
+            if (Kd::Top) top->count[d] = 0;
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_full[d]));
+        if (at.e < 0 || !at.next(P, plan, S, cta)) break;
+        if (at.e >= 0) fetch<Kd::List>(P, at.e, cta.lane, a);
     }
+    at.end(S);
 }
 
 // ---------------------------------------------------------------------------
 // producer and patcher
 
-template <int DT>
+template <class Kd>
 __device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, Shared &S, uint8_t *ring, const Cta &cta) {
-    const int64_t row_bytes = (int64_t)P.V * Type<DT>::kSize & ~15ll;
+    const int64_t row_bytes = (int64_t)P.V * Kd::kSize & ~15ll;
     int slot = 0, r = 0;
     uint32_t phase = 0;
     long long issued = 0;
     bool ok = true;
-    for (long long e = cta.first; e < P.entries && ok; e += cta.step, ++r) {
+    for (; ok; ++r) {
         const int d = cta.place(r);
-        ok = wait_on(S.row_full[d], cta.parity(r), S.abort, P.status, P.wait_ns);
-        if (!ok) break;
+        ok = wait_bar(S.row_full[d], cta.parity(r), S, P);
+        if (!ok || S.row[d].state == kEnd) break;
         const char *z = S.row[d].z;
         const bool live = S.row[d].state == kLive;
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
         if (!live) continue;
         for (int i = 0; i < cta.chunks && ok; ++i) {
-            ok = wait_on(S.empty[slot], phase ^ 1u, S.abort, P.status, P.wait_ns);
+            ok = wait_bar(S.empty[slot], phase ^ 1u, S, P);
             if (!ok) break;
             if (cta.lane == 0) {
-                const int64_t off = ((int64_t)cta.slice0 + (int64_t)i * kChunkVecs) * 16;
-                const int n = min(kChunkVecs, cta.slice_vecs - i * kChunkVecs) * 16;
+                const int64_t off = ((int64_t)cta.slice0 + (int64_t)i * Kd::kChunkVecs) * 16;
+                const int n = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs) * 16;
                 const int bytes = (int)min((int64_t)n, row_bytes - off);
                 const uint32_t bar = smem_u32(&S.full[slot]);
                 if (bytes > 0) {
                     mbar_arrive_expect_tx(bar, (uint32_t)bytes);
-                    bulk_load(smem_u32(ring + (size_t)slot * kChunkBytes), z + off, (uint32_t)bytes, bar);
+                    bulk_load(smem_u32(ring + (size_t)slot * Kd::kChunkBytes), z + off, (uint32_t)bytes, bar);
                 } else {
                     mbar_arrive(bar);
                 }
@@ -743,31 +939,31 @@ __device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, 
         mbar_wait_bounded(smem_u32(&S.full[u % plan.slots]), u / plan.slots & 1);
 }
 
-template <int DT>
+template <class Kd>
 __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Shared &S, const SharedList &L, uint8_t *ring,
                                       const Cta &cta) {
-    using Ty = Type<DT>;
-    const int whole = P.V / Ty::kPer, rest = P.V - whole * Ty::kPer;
+    const int whole = P.V / Kd::kPer, rest = P.V - whole * Kd::kPer;
     int slot = 0, r = 0;
     uint32_t phase = 0;
-    for (long long e = cta.first; e < P.entries; e += cta.step, ++r) {
+    for (;; ++r) {
         const int d = cta.place(r);
-        if (!wait_on(S.row_full[d], cta.parity(r), S.abort, P.status, P.wait_ns)) return;
+        if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
+        if (S.row[d].state == kEnd) return;
         for (int i = 0; i < (S.row[d].state == kLive ? cta.chunks : 0); ++i) {
-            if (!wait_on(S.full[slot], phase, S.abort, P.status, P.wait_ns)) return;
-            uint8_t *chunk = ring + (size_t)slot * kChunkBytes;
-            const int v0 = cta.slice0 + i * kChunkVecs;
-            const int n = min(kChunkVecs, cta.slice_vecs - i * kChunkVecs);
+            if (!wait_bar(S.full[slot], phase, S, P)) return;
+            uint8_t *chunk = ring + (size_t)slot * Kd::kChunkBytes;
+            const int v0 = cta.slice0 + i * Kd::kChunkVecs;
+            const int n = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs);
             if (rest && v0 <= whole && whole < v0 + n) {  // the ragged end of the row, which no copy brings
-                if (cta.lane < Ty::kPer) {
-                    const float x = cta.lane < rest ? plain_logit<DT>(S.row[d].z, (int64_t)whole * Ty::kPer + cta.lane) : -INFINITY;
-                    store_logit<DT>(reinterpret_cast<char *>(chunk + (whole - v0) * 16), cta.lane, x);
+                if (cta.lane < Kd::kPer) {
+                    const float x = cta.lane < rest ? plain_logit<Kd::DT>(S.row[d].z, (int64_t)whole * Kd::kPer + cta.lane) : -INFINITY;
+                    store_logit<Kd::DT>(reinterpret_cast<char *>(chunk + (whole - v0) * 16), cta.lane, x);
                 }
                 __syncwarp();
             }
             for (int j = cta.lane; j < P.K; j += 32) {
-                const int at = L.ids[d][j] - v0 * Ty::kPer;
-                if (at >= 0 && at < n * Ty::kPer) store_logit<DT>(reinterpret_cast<char *>(chunk), at, -INFINITY);
+                const int at = L.ids[d][j] - v0 * Kd::kPer;
+                if (at >= 0 && at < n * Kd::kPer) store_logit<Kd::DT>(reinterpret_cast<char *>(chunk), at, -INFINITY);
             }
             // the next copy into this slot comes after these stores
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -786,43 +982,47 @@ __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Sh
 // ---------------------------------------------------------------------------
 // epilogue
 
-// Calls f with the keys of the n candidates' tokens, or (n < 0) of the whole slice, read once more from memory.
+// Calls f with the keys of the n candidates' tokens, or (n < 0) of the whole slice's, read once more from memory (L2).
 template <int DT, class F>
-__device__ __forceinline__ void each_key(const TokenParams &P, const Row &row, const SharedTop &T, int d, int n, const Cta &cta, F &&f) {
-    using Ty = Type<DT>;
-    auto vector = [&](const uint4 &w, int at) {
-        float x[Ty::kPer];
-        vec_floats<DT>(w, x);
-#pragma unroll
-        for (int q = 0; q < Ty::kPer; ++q)
-            if (at * Ty::kPer + q < P.V) f(order_key(x[q], at * Ty::kPer + q));
-    };
-    if (n >= 0) {
-        for (int i = cta.lane; i < n; i += 32) vector(T.vec[d][i], T.at[d][i]);
-        return;
-    }
-    const int whole = P.V / Ty::kPer, end = min(whole, cta.slice0 + cta.slice_vecs);
-    const uint4 *z = reinterpret_cast<const uint4 *>(row.z);
-    for (int v = cta.slice0 + cta.lane; v < end; v += 128) {
+__device__ __forceinline__ void each_key(const TokenParams &P, const char *row, const int32_t *at, int n, const Cta &cta, F &&f) {
+    constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2);
+    const int whole = P.V / kPer, first = n < 0 ? cta.slice0 : 0;
+    const int end = n < 0 ? min(whole, cta.slice0 + cta.slice_vecs) : n;
+    const uint4 *z = reinterpret_cast<const uint4 *>(row);
+    bool ragged = n < 0 && cta.slice0 + cta.slice_vecs > whole;
+    for (int i = first + cta.lane; i < end; i += 128) {
         uint4 w[4];
+        int v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (v + 32 * q < end) w[q] = __ldg(z + v + 32 * q);
+        for (int q = 0; q < 4; ++q) {
+            v[q] = i + 32 * q < end ? (n < 0 ? i + 32 * q : at[i + 32 * q]) : -1;
+            if (v[q] == whole) {
+                ragged = true;
+                v[q] = -1;
+            }
+            if (v[q] >= 0) w[q] = __ldg(z + v[q]);
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (v + 32 * q < end) vector(w[q], v + 32 * q);
+        for (int q = 0; q < 4; ++q) {
+            if (v[q] < 0) continue;
+            float x[kPer];
+            vec_floats<DT>(w[q], x);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) f(order_key(x[u], v[q] * kPer + u));
+        }
     }
-    const int at = whole * Ty::kPer + cta.lane;  // the ragged end
-    if (cta.slice0 + cta.slice_vecs > whole && at < P.V) f(order_key(load_logit<DT>(row.z, at), at));
+    ragged = __any_sync(0xffffffffu, ragged);
+    const int t = whole * kPer + cta.lane;  // the row's ragged end
+    if (ragged && t < P.V) f(order_key(load_logit<DT>(row, t), t));
 }
 
 // The k best keys of the CTA's slice, in order, in T.best (0 where there are none).
 template <int DT>
-__device__ void select_top(const TokenParams &P, const Row &row, SharedTop &T, int d, const Cta &cta) {
+__device__ __noinline__ void select_top(const TokenParams &P, const char *row, SharedTop &T, int d, const Cta &cta) {
     constexpr uint32_t all = 0xffffffffu;
     const int lane = cta.lane, k = P.k;
-    const unsigned found = *(volatile unsigned *)&T.count[d];
-    int n = found <= kCandidates ? (int)found : -1;
+    const unsigned met = *(volatile unsigned *)&T.count[d];
+    int n = met <= kCandidates ? (int)met : -1;
     // the last bound: k tokens are at least so large, or there are not that many
     const unsigned long long b = lane < kConsumers ? T.bound[d][lane] : ~0ull;
     unsigned long long least = (unsigned long long)__reduce_min_sync(all, (uint32_t)(b >> 32)) << 32;
@@ -830,44 +1030,39 @@ __device__ void select_top(const TokenParams &P, const Row &row, SharedTop &T, i
         least = 0;
         n = 0;
     }
-    auto count = [&](unsigned long long key) {
-        int c = 0;
-        each_key<DT>(P, row, T, d, n, cta, [&](unsigned long long x) { c += x >= key ? 1 : 0; });
-        return (int)__reduce_add_sync(all, (unsigned)c);
-    };
-    // More than fit (many equal logits, or rows that rise): the largest key that k tokens reach, a bit at a time.
-    if (count(least) > kKeys) {
-        unsigned long long key = 0;
-        for (int bit = 63; bit >= 0; --bit)
-            if (count(key | 1ull << bit) >= k) key |= 1ull << bit;
-        least = max(least, key);
-    }
-    int m = 0;
-    {
-        // keys into one list, each lane's behind those of the lanes before it
-        int mine = 0;
-        each_key<DT>(P, row, T, d, n, cta, [&](unsigned long long x) { mine += x >= least ? 1 : 0; });
-        int incl = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(all, incl, off);
-            if (lane >= off) incl += y;
-        }
-        m = __shfl_sync(all, incl, 31);
-        int at = incl - mine;
-        each_key<DT>(P, row, T, d, n, cta, [&](unsigned long long x) {
-            if (x >= least) T.keys[at++] = x;
-        });
-    }
     for (int i = lane; i < k; i += 32) T.best[i] = 0;
-    __syncwarp();
+    auto collect = [&]() {
+        if (lane == 0) T.found = 0;
+        __syncwarp();
+        each_key<DT>(P, row, T.at[d], n, cta, [&](unsigned long long x) {
+            if (x >= least) {
+                const unsigned at = atomicAdd(&T.found, 1u);
+                if (at < kKeys) T.keys[at] = x;
+            }
+        });
+        __syncwarp();
+        return *(volatile unsigned *)&T.found;
+    };
+    unsigned m = collect();
+    if (m > kKeys) {
+        // many equal logits: the largest key that k tokens reach, a bit at a time
+        unsigned long long key = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+            const unsigned long long next = key | 1ull << bit;
+            int c = 0;
+            each_key<DT>(P, row, T.at[d], n, cta, [&](unsigned long long x) { c += x >= next ? 1 : 0; });
+            if ((int)__reduce_add_sync(all, (unsigned)c) >= k) key = next;
+        }
+        least = max(least, key);
+        m = min(collect(), (unsigned)kKeys);
+    }
     // a key's place is the number of larger ones
-    for (int i0 = 0; i0 < m; i0 += 128) {
+    for (unsigned i0 = 0; i0 < m; i0 += 128) {
         unsigned long long x[4];
         int place[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[q] = i0 + 32 * q + lane < m ? T.keys[i0 + 32 * q + lane] : 0;
-        for (int i = 0; i < m; ++i) {
+        for (unsigned i = 0; i < m; ++i) {
             const unsigned long long o = T.keys[i];
 #pragma unroll
             for (int q = 0; q < 4; ++q) place[q] += o > x[q] ? 1 : 0;
@@ -899,22 +1094,22 @@ __device__ __forceinline__ bool exchange(const TokenParams &P, Shared &S, const 
         st_cluster_f4(cluster_addr(&S.others[set][cta.rank], lane), make_float4(p.m, p.s, p.t, __int_as_float(p.n)));
         cluster_arrive(S.exchanged[set], lane);
     }
-    if (!wait_on_cluster(S.exchanged[set], x >> 1 & 1, S.abort, P.status, P.wait_ns)) return false;
+    if (!wait_on_cluster(S.exchanged[set], x >> 1 & 1, S, P)) return false;
     p = lane < cta.cluster ? S.others[set][lane] : Part{-INFINITY, 0.0f, 0.0f, 0};
     p = warp_merge(p, P.c);
     return true;
 }
 
-template <int DT, bool G>
-__device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, SharedTop *T, const Cta &cta, int d, uint32_t parity,
-                                             Part p, int &x) {
+template <class Kd>
+__device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, SharedTop *T, const Cta &cta, int d, Part p,
+                                             int &x) {
     const Row &row = S.row[d];
     const long long e = row.entry;
-    const int lane = cta.lane, k = G ? 0 : P.k;
+    const int lane = cta.lane, k = Kd::Top ? P.k : 0;
     const bool alone = cta.cluster == 1;
     if (row.state == kLive) {
         if (k) {
-            select_top<DT>(P, row, *T, d, cta);
+            select_top<Kd::DT>(P, row.z, *T, d, cta);
             if (!alone)
                 for (int i = lane; i < k; i += 32)
                     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(&T->gathered[cta.rank * k + i], 0)),
@@ -936,7 +1131,7 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
         ff_log(p.s, lh, ll);
         ff_logprob(P, row.zy, p.m, lh, ll, lp, lo);
         const float mean = p.t / p.s;
-        H = lh - fmaf(mean, P.inv_hi, mean * P.inv_lo);
+        H = lh - fmaf(mean, kLn2Hi, fmaf(mean, kLn2Lo, -ll));
         float xh, xl;
         over_T(P, p.m, 0.0f, xh, xl);
         if (fabsf(xh) < INFINITY) ff_add(xh, xl, lh, ll, xh, xl);
@@ -947,20 +1142,20 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
     if (lane == 0 && cta.rank == 0) {
         if (P.logprob) P.logprob[e] = lp;
         if (P.entropy) P.entropy[e] = H;
-        if (!G && P.lse) P.lse[e] = lse;
-        if (!G && P.rank) P.rank[e] = bad ? -1 : p.n;
+        if (!Kd::Grad && P.lse) P.lse[e] = lse;
+        if (Kd::Rank) P.rank[e] = bad ? -1 : p.n;
     }
-    if constexpr (!G) if (k && cta.rank == 0) {
+    if constexpr (Kd::Top) if (cta.rank == 0) {
         if (!good) {
             for (int i = lane; i < k; i += 32) {
                 P.top_logprob[e * k + i] = bad ? NAN : -INFINITY;
                 P.top_idx[e * k + i] = -1;
             }
         } else if (alone) {
-            for (int i = lane; i < k; i += 32) write_top<DT>(P, e, i, T->best[i], p.m, lh, ll);
+            for (int i = lane; i < k; i += 32) write_top<Kd::DT>(P, e, i, T->best[i], p.m, lh, ll);
         } else {
             // each CTA's keys fall: a key's place is how many of each list are larger, found by halves
-            for (int i = lane; i < k; i += 32) write_top<DT>(P, e, i, 0, p.m, lh, ll);
+            for (int i = lane; i < k; i += 32) write_top<Kd::DT>(P, e, i, 0, p.m, lh, ll);
             __syncwarp();
             for (int i = lane; i < cta.cluster * k; i += 32) {
                 const unsigned long long key = T->gathered[i];
@@ -976,35 +1171,51 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
                     }
                     place += lo_;
                 }
-                if (place < k) write_top<DT>(P, e, place, key, p.m, lh, ll);
+                if (place < k) write_top<Kd::DT>(P, e, place, key, p.m, lh, ll);
             }
         }
     }
-    if (G) {
+    if (Kd::Grad) {
         const float g = row.g, h = row.h;
-        // p_v (-(g + h (ln p_v + H)) / T) with p_v = w / s and ln p_v = d / T - ln s
+        // p_v (-(g + h (ln p_v + H)) / T) with p_v = 2^x / s and ln p_v = x ln 2 - ln s
         const float inv_s = 1.0f / p.s;
-        const float a = -(g + h * (H - lh)) * P.inv_hi * inv_s, b = -h * P.inv_hi * P.inv_hi * inv_s;
+        const float a = -(g + h * (H - lh)) * P.inv_hi * inv_s, b = -h * P.inv_hi * kLn2Hi * inv_s;
         if (lane == 0) {
-            S.coef[d] = good ? make_float4(p.m, a, b, 0.0f) : make_float4(0.0f, NAN, NAN, 0.0f);
-            mbar_arrive(smem_u32(&S.known[d]));
-        }
-        if (!wait_on(S.stored[d], parity, S.abort, P.status, P.wait_ns)) return false;
-        const int y = row.y / Type<DT>::kPer;
-        if (good && lane == 0 && y >= cta.slice0 && y < cta.slice0 + cta.slice_vecs) {
             const float py = ff_exp(lp, lo);
             const float s = py > 0.0f ? h * py * (lp + H) : 0.0f;
-            store_logit<DT>(P.grad + e * P.grad_stride_bytes, row.y, (g * (1.0f - py) - s) * P.inv_hi);
+            S.coef[d] = good ? make_float4(p.m, a, b, (g * (1.0f - py) - s) * P.inv_hi) : make_float4(0.0f, NAN, NAN, 0.0f);
+            S.fix[d] = good;
+            mbar_arrive(smem_u32(&S.known[d]));
         }
     }
     return true;
 }
 
+// Puts the given token's gradient in its place, once the consumers have stored the others'.
+template <class Kd>
+__device__ __forceinline__ void fix_token(const TokenParams &P, const Shared &S, const Cta &cta, int d) {
+    const int y = S.row[d].y, v = y / Kd::kPer;
+    if (S.fix[d] && cta.lane == 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
+        store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, y, S.coef[d].w);
+}
+
+// The same for a list's tokens.
+template <class Kd>
+__device__ __forceinline__ void fix_list(const TokenParams &P, const Shared &S, const SharedList &L, const Cta &cta, int d) {
+    if (!S.fix[d]) return;
+    const float w = S.row[d].g * P.inv_hi, C = S.coef[d].w;
+    for (int j = cta.lane; j < P.K; j += 32) {
+        const int id = L.ids[d][j], v = id / Kd::kPer;
+        if (id >= 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
+            store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, id, w * (L.lp[d][j] - L.z[d][j] * C));
+    }
+}
+
 // The divergence over the list's tokens and the rest, see include/specverify.h. Logarithms are pairs of floats up to their
 // differences: a small divergence is a difference of much larger terms.
-template <int DT, bool G>
-__device__ __forceinline__ bool finish_list(const TokenParams &P, Shared &S, SharedList &L, const Cta &cta, int d, uint32_t parity,
-                                            Part p, int &x) {
+template <class Kd>
+__device__ __forceinline__ bool finish_list(const TokenParams &P, Shared &S, SharedList &L, const Cta &cta, int d, Part p,
+                                            int &x) {
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane, K = P.K, kind = P.divergence;
@@ -1074,71 +1285,78 @@ __device__ __forceinline__ bool finish_list(const TokenParams &P, Shared &S, Sha
         }
         loss = warp_sum(f);
         C = warp_sum(h);
-        if (G) {
+        if (Kd::Grad) {
             h_rest = __shfl_sync(0xffffffffu, h_rest, K & 31);
             q_rest = __shfl_sync(0xffffffffu, q_rest, K & 31);
             factor = some ? row.g * P.inv_hi * (h_rest - q_rest * C) / p.s : 0.0f;
         }
     }
     if (lane == 0 && cta.rank == 0) P.loss[e] = loss;
-    if (G) {
+    if (Kd::Grad) {
         if (lane == 0) {
-            S.coef[d] = bad ? make_float4(0.0f, NAN, 0.0f, 0.0f) : make_float4(some ? p.m : 0.0f, factor, 0.0f, 0.0f);
+            S.coef[d] = bad ? make_float4(0.0f, NAN, 0.0f, 0.0f) : make_float4(some ? p.m : 0.0f, factor, 0.0f, C);
+            S.fix[d] = good;
             mbar_arrive(smem_u32(&S.known[d]));
         }
-        if (!wait_on(S.stored[d], parity, S.abort, P.status, P.wait_ns)) return false;
-        if (good)
-            for (int j = lane; j < K; j += 32) {
-                const int id = L.ids[d][j], v = id / Type<DT>::kPer;
-                if (id >= 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
-                    store_logit<DT>(P.grad + e * P.grad_stride_bytes, id, row.g * P.inv_hi * (L.lp[d][j] - L.z[d][j] * C));
-            }
     }
     return true;
 }
 
-template <int DT, bool LIST, bool G>
-__device__ __forceinline__ void finish(const TokenParams &P, Shared &S, SharedTop *T, SharedList *L, const Cta &cta) {
+template <class Kd>
+__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, SharedList *L, const Cta &cta) {
     int r = 0, x = 0;
-    for (long long e = cta.first; e < P.entries; e += cta.step, ++r) {
+    auto fix = [&](int g) {
+        const int d = cta.place(g);
+        if (!wait_bar(S.stored[d], cta.parity(g), S, P)) return false;
+        if (Kd::List) fix_list<Kd>(P, S, *L, cta, d);
+        else fix_token<Kd>(P, S, cta, d);
+        __syncwarp();
+        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
+        return true;
+    };
+    for (;; ++r) {
         const int d = cta.place(r);
         const uint32_t parity = cta.parity(r);
-        if (!wait_on(S.row_full[d], parity, S.abort, P.status, P.wait_ns) ||
-            !wait_on(S.summed[d], parity, S.abort, P.status, P.wait_ns))
-            return;
+        if (!wait_bar(S.row_full[d], parity, S, P)) return;
+        if (S.row[d].state == kEnd) break;
+        if (!wait_bar(S.summed[d], parity, S, P)) return;
         Part p{-INFINITY, 0.0f, 0.0f, 0};
         if (S.row[d].state == kLive) {
             if (cta.lane < kConsumers) p = S.part[d][cta.lane];
             p = warp_merge(p, P.c);
         }
-        if (LIST ? !finish_list<DT, G>(P, S, *L, cta, d, parity, p, x) : !finish_token<DT, G>(P, S, T, cta, d, parity, p, x)) return;
+        if (Kd::List ? !finish_list<Kd>(P, S, *L, cta, d, p, x) : !finish_token<Kd>(P, S, T, cta, d, p, x)) return;
         __syncwarp();
-        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
+        // A gradient's next row is not kept waiting for the stores of this one.
+        if (Kd::Grad) {
+            if (r >= plan.lag && !fix(r - plan.lag)) return;
+        } else if (cta.lane == 0) {
+            mbar_arrive(smem_u32(&S.row_free[d]));
+        }
     }
+    if (Kd::Grad && plan.lag && r > 0) fix(r - 1);
 }
-
 // ---------------------------------------------------------------------------
 
-template <int DT, bool LIST, bool G>
+template <class Kd>
 __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constant__ TokenParams P, const __grid_constant__ Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
-    Shared &S = *reinterpret_cast<Shared *>(smem + (size_t)plan.slots * kChunkBytes);
+    Shared &S = *reinterpret_cast<Shared *>(smem + (size_t)plan.slots * Kd::kChunkBytes);
     constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
     void *more = reinterpret_cast<uint8_t *>(&S) + kFixed;
-    SharedTop *top = !LIST && !G && P.k > 0 ? static_cast<SharedTop *>(more) : nullptr;
-    SharedList *list = LIST ? static_cast<SharedList *>(more) : nullptr;
+    SharedTop *top = Kd::Top ? static_cast<SharedTop *>(more) : nullptr;
+    SharedList *list = Kd::List ? static_cast<SharedList *>(more) : nullptr;
     const int tid = threadIdx.x, warp = tid >> 5;
 
     Cta cta;
     cta.cluster = plan.cluster;
     cta.rank = plan.cluster > 1 ? (int)cluster_rank() : 0;
     cta.first = blockIdx.x / plan.cluster;
-    cta.step = plan.clusters;
-    const int vecs = (int)(((int64_t)P.V * Type<DT>::kSize + 15) / 16);
+    const int vecs = (int)(((int64_t)P.V * Kd::kSize + 15) / 16);
     cta.slice0 = min(vecs, cta.rank * plan.slice_vecs);
     cta.slice_vecs = min(vecs - cta.slice0, plan.slice_vecs);
-    cta.chunks = (cta.slice_vecs + kChunkVecs - 1) / kChunkVecs;
+    cta.chunks = (cta.slice_vecs + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
     cta.lane = tid & 31;
     cta.depth_log = plan.depth_log;
 
@@ -1150,28 +1368,29 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
         }
         for (int i = 0; i < kDepth; ++i) {
             mbar_init(smem_u32(&S.row_full[i]), 1);
-            mbar_init(smem_u32(&S.row_free[i]), kConsumers + (LIST ? 3 : 2));
+            mbar_init(smem_u32(&S.row_free[i]), kConsumers + (Kd::List ? 3 : 2));
             mbar_init(smem_u32(&S.summed[i]), kConsumers);
             mbar_init(smem_u32(&S.known[i]), 1);
             mbar_init(smem_u32(&S.stored[i]), kConsumers);
             mbar_init(smem_u32(&S.bounded[i]), kConsumers);
         }
+        mbar_init(smem_u32(&S.granted), 1);
         mbar_init(smem_u32(&S.exchanged[0]), plan.cluster);
         mbar_init(smem_u32(&S.exchanged[1]), plan.cluster);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (LIST)
+    if (Kd::List)
         for (int i = tid; i < kHash; i += kThreads) list->hash[i] = -1;
     __syncthreads();
     if (plan.cluster > 1) cluster_sync();
     after_previous();
 
-    if (warp < kConsumers) consume<DT, LIST, G>(P, plan, S, top, ring, cta);
-    else if (warp == kScout) scout<DT, LIST>(P, S, top, list, cta);
-    else if (warp == kProducer) produce<DT>(P, plan, S, ring, cta);
-    else if (LIST && warp == kPatcher) patch<DT>(P, plan, S, *list, ring, cta);
-    else if (warp == kEpilogue) finish<DT, LIST, G>(P, S, top, list, cta);
+    if (warp < kConsumers) consume<Kd>(P, plan, S, top, ring, cta);
+    else if (warp == kScout) scout<Kd>(P, plan, S, top, list, cta);
+    else if (warp == kProducer) produce<Kd>(P, plan, S, ring, cta);
+    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, *list, ring, cta);
+    else if (warp == kEpilogue) finish<Kd>(P, plan, S, top, list, cta);
     __syncwarp();
     // sums of other CTAs may still be on their way here where somebody gave up
     if (plan.cluster > 1) cluster_sync();
@@ -1180,76 +1399,72 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 // host
 
-size_t fixed_bytes(bool list, bool top) {
-    return (sizeof(Shared) + 15) / 16 * 16 + (list ? sizeof(SharedList) : top ? sizeof(SharedTop) : 0);
-}
-
 constexpr int kHalfSmem = 113 * 1024, kFullSmem = 226 * 1024;  // of a CTA, two or one on an SM
+
+// What fits the GPU of a kernel: clusters of 2^i CTAs at once, two CTAs an SM (0) or one (1).
+template <class Kd>
+struct Room {
+    static inline int clusters[2][5];
+};
 
 // Rows over the GPU. The sums alone: one CTA a row where that fills the GPU, else as many as do (a power of two). With a
 // gradient: the fewest that hold a row in their rings.
-Plan make_plan(const TokenParams &P, int elem, bool list, bool grad, int num_sms) {
-    const bool top = !list && !grad && P.k > 0;
-    const int64_t vecs = ((int64_t)P.V * elem + 15) / 16;
-    const int room = 2 * num_sms;
-    Plan p{};
-    p.depth_log = top ? 1 : 2;
-    const int fixed = (int)fixed_bytes(list, top);
-    const int half = (kHalfSmem - fixed) / kChunkBytes, full = std::min(kMaxSlots, (kFullSmem - fixed) / kChunkBytes);
-    auto chunks = [&](int s) {
-        const int64_t slice = ((vecs + s - 1) / s + 31) / 32 * 32;
-        return (slice + kChunkVecs - 1) / kChunkVecs;
+template <class Kd>
+Plan make_plan(const TokenParams &P) {
+    const int64_t vecs = ((int64_t)P.V * Kd::kSize + 15) / 16;
+    const int fixed = (int)((sizeof(Shared) + 15) / 16 * 16 + (Kd::List ? sizeof(SharedList) : Kd::Top ? sizeof(SharedTop) : 0));
+    const int half = std::min(kMaxSlots, (kHalfSmem - fixed) / Kd::kChunkBytes);
+    const int full = std::min(kMaxSlots, (kFullSmem - fixed) / Kd::kChunkBytes);
+    auto chunks = [&](int log) {
+        const int64_t slice = ((vecs + (1 << log) - 1 >> log) + 31) / 32 * 32;
+        return (slice + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
     };
-    int S = 1;
-    if (grad)
-        while (S < kMaxCluster && 2 * chunks(S) > half) S *= 2;
-    while (S < kMaxCluster && P.entries * S * 2 <= room && vecs >= 256 * S && (!top || P.k * S * 2 <= kGathered)) S *= 2;
-    p.lag = grad && 2 * chunks(S) <= half;
-    p.slots = !grad ? std::min(half, 8) : chunks(S) <= half ? half : full;
-    p.cluster = S;
-    p.slice_vecs = (int32_t)(((vecs + S - 1) / S + 31) / 32 * 32);
-    const int resident = (p.slots > half ? num_sms : room) / S;
-    p.clusters = (int32_t)std::min<int64_t>(P.entries, std::max(1, resident));
-    p.smem = p.slots * kChunkBytes + fixed;
+    const auto &room = Room<Kd>::clusters;
+    int log = 0;
+    if (Kd::Grad)
+        while (log < 4 && 2 * chunks(log) > half) ++log;
+    while (log < 4 && P.entries <= room[0][log + 1] && vecs >> log >= 256 && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
+    Plan p{};
+    p.depth_log = Kd::Top ? 1 : 2;
+    p.cluster = 1 << log;
+    p.slice_vecs = (int32_t)(((vecs + p.cluster - 1 >> log) + 31) / 32 * 32);
+    p.lag = Kd::Grad && 2 * chunks(log) <= half;
+    const bool whole_sm = Kd::Grad && chunks(log) > half;
+    p.slots = whole_sm ? full : half;
+    p.dynamic = log == 0 && P.entries <= INT32_MAX;
+    p.clusters = (int32_t)(p.dynamic ? P.entries : std::min<int64_t>(P.entries, std::max(1, room[whole_sm][log])));
+    p.smem = p.slots * Kd::kChunkBytes + fixed;
     return p;
 }
 
-template <int DT, bool LIST, bool G>
-cudaError_t launch(const TokenParams &P, int num_sms, cudaStream_t s) {
-    const Plan plan = make_plan(P, DT == SV_DT_FP32 ? 4 : 2, LIST, G, num_sms);
-    return launch_after(token_kernel<DT, LIST, G>, dim3((unsigned)(plan.clusters * plan.cluster)), kThreads, plan.smem, s,
-                        plan.cluster, P, plan);
+template <class Kd>
+cudaError_t launch(const TokenParams &P, cudaStream_t s) {
+    const Plan plan = make_plan<Kd>(P);
+    return launch_after(token_kernel<Kd>, dim3((unsigned)(plan.clusters * plan.cluster)), kThreads, plan.smem, s, plan.cluster, P,
+                        plan);
 }
 
-template <int DT, bool LIST, bool G>
+template <class Kd>
 cudaError_t prepare() {
-    cudaError_t e = cudaFuncSetAttribute(token_kernel<DT, LIST, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFullSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(token_kernel<DT, LIST, G>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFullSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int whole = 0; whole < 2; ++whole)
+        for (int log = 0; log < 5 && e == cudaSuccess; ++log) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << log;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(1u << log);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = whole ? kFullSmem : kHalfSmem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&Room<Kd>::clusters[whole][log], token_kernel<Kd>, &cfg);
+        }
     return e;
 }
 
 }  // namespace
-
-cudaError_t prepare_token() {
-    cudaError_t e = cudaSuccess;
-    for (cudaError_t (*f)() : {prepare<SV_DT_FP32, false, false>, prepare<SV_DT_BF16, false, false>, prepare<SV_DT_FP32, false, true>,
-                               prepare<SV_DT_BF16, false, true>, prepare<SV_DT_FP32, true, false>, prepare<SV_DT_BF16, true, false>,
-                               prepare<SV_DT_FP32, true, true>, prepare<SV_DT_BF16, true, true>})
-        if (e == cudaSuccess) e = f();
-    return e;
-}
-
-cudaError_t launch_token_logprobs(const TokenParams &P, int dtype, int num_sms, cudaStream_t s) {
-    return dtype == SV_DT_FP32 ? launch<SV_DT_FP32, false, false>(P, num_sms, s) : launch<SV_DT_BF16, false, false>(P, num_sms, s);
-}
-
-cudaError_t launch_token_logprobs_grad(const TokenParams &P, int dtype, int num_sms, cudaStream_t s) {
-    return dtype == SV_DT_FP32 ? launch<SV_DT_FP32, false, true>(P, num_sms, s) : launch<SV_DT_BF16, false, true>(P, num_sms, s);
-}
-
-cudaError_t launch_distill(const TokenParams &P, int dtype, int num_sms, cudaStream_t s) {
-    if (P.grad) return dtype == SV_DT_FP32 ? launch<SV_DT_FP32, true, true>(P, num_sms, s) : launch<SV_DT_BF16, true, true>(P, num_sms, s);
-    return dtype == SV_DT_FP32 ? launch<SV_DT_FP32, true, false>(P, num_sms, s) : launch<SV_DT_BF16, true, false>(P, num_sms, s);
-}
 
 }  // namespace sv

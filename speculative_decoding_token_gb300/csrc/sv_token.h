@@ -46,9 +46,11 @@ struct TokenParams {
     float *loss;
 };
 
-cudaError_t prepare_token();
-cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
-cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);
-cudaError_t launch_distill(const TokenParams &p, int dtype, int num_sms, cudaStream_t s);  // grad: nullable
+cudaError_t prepare_logprobs();
+cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, cudaStream_t s);
+cudaError_t prepare_logprobs_grad();
+cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, cudaStream_t s);
+cudaError_t prepare_distill();
+cudaError_t launch_distill(const TokenParams &p, int dtype, cudaStream_t s);  // p.grad may be NULL
 
 }  // namespace sv
