@@ -54,7 +54,9 @@ struct Kind {
     static constexpr int kSize = DT == SV_DT_FP32 ? 4 : 2;
     static constexpr int kPer = 16 / kSize;  // logits of a vector
     static constexpr uint32_t kNegInf = DT == SV_DT_FP32 ? 0xff800000u : 0xff80ff80u;
-    static constexpr int kVecs = Grad ? 2 : 4;  // of a chunk, a thread
+    static constexpr int kVecs = 4;  // of a chunk, a thread
+    // numbers of a Part that a cluster's CTAs send one another
+    static constexpr int kWords = 2 + (Ent ? 1 : 0) + (Rank ? 1 : 0);
     static constexpr int kChunkVecs = kTeam * kVecs, kChunkBytes = kChunkVecs * 16;
 };
 
@@ -65,7 +67,8 @@ struct Row {
     int state;
     int y;
     float zy;
-    float p_rest;  // of a list: what it leaves of one
+    float p_rest, p_sum;  // of a list: what it leaves of one, what it has
+    float zmax, zsum;     // of a list: the draft's largest logit, and the sum of 2^((z - zmax) c)
     float g, h;    // what the gradient is multiplied by
 };
 
@@ -79,13 +82,13 @@ struct Part {
 struct Shared {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots];
     uint64_t row_full[kDepth], row_free[kDepth], summed[kDepth], known[kDepth], stored[kDepth], bounded[kDepth];
-    uint64_t exchanged[2], granted;
+    uint64_t gathered, granted;
     uint4 grant;          // the answer to a request for another row
     Row row[kDepth];
-    Part part[kDepth][kConsumers];
-    Part others[2][kMaxCluster];
-    float4 coef[kDepth];  // of the gradient: reference, factor, slope; what the epilogue puts right in it
-    int fix[kDepth];
+    Part part[kDepth][kConsumers];  // of the CTA's warps where a row is one CTA's
+    float4 coef[kDepth];  // of the gradient: m, a, b (see store_slice)
+    float fix[kDepth];    // the given token's gradient, or what a list's needs
+    int good[kDepth];
     int32_t abort;
 };
 
@@ -100,12 +103,17 @@ struct SharedTop {
     unsigned count[kTopDepth], found;
 };
 
-struct SharedList {
-    int32_t ids[kDepth][kMaxList];
-    float z[kDepth][kMaxList];
-    float lp[kDepth][kMaxList];  // the target's log-probability
-    int32_t hash[kHash];
+// Lists of kDepth rows, `stride` entries each, in shared memory.
+struct Lists {
+    int32_t *ids;
+    float *z;    // the draft's logits of them
+    float *lp;   // the target's log-probabilities
+    float *p;    // and probabilities
+    int32_t *hash;
+    int stride;
 };
+
+constexpr int kListBytes = kDepth * 16, kHashBytes = kHash * 4;  // an entry of a list in every row; the table
 
 // How a call's rows are laid out over the GPU.
 struct Plan {
@@ -115,6 +123,8 @@ struct Plan {
     int32_t lag;          // rows between the two readings of a gradient
     int32_t dynamic;      // a CTA takes its next row when it is free for it (else rows are dealt out)
     int32_t depth_log;    // rows between the scout and the epilogue
+    int32_t list_stride;  // entries of a list
+    int32_t words_at;     // where in shared memory the words of a cluster are
     int32_t clusters;
     int32_t smem;
 };
@@ -260,17 +270,23 @@ __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
     a.m = m;
 }
 
-__device__ __forceinline__ Part warp_merge(Part a, float c) {
+// The warp's lanes' sums in one, in every lane.
+template <class Kd>
+__device__ __forceinline__ Part warp_fold(Part a, float c) {
+    constexpr uint32_t all = 0xffffffffu;
+    Part r;
+    r.m = from_order_bits(__reduce_max_sync(all, order_bits(a.m)));
+    const float x = fmaxf(a.m - r.m, kFar) * c, f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
+    r.s = f * a.s;
+    r.t = Kd::Ent && f > 0.0f ? f * fmaf(x, a.s, a.t) : 0.0f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        Part b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
-        b.t = __shfl_xor_sync(0xffffffffu, a.t, off);
-        b.n = __shfl_xor_sync(0xffffffffu, a.n, off);
-        merge(a, b, c);
+        r.s += __shfl_xor_sync(all, r.s, off);
+        if (Kd::Ent) r.t += __shfl_xor_sync(all, r.t, off);
     }
-    return a;
+    r.n = Kd::Rank ? (int)__reduce_add_sync(all, (unsigned)max(a.n, 0)) : 0;
+    if (__any_sync(all, a.n < 0)) r.n = -1;
+    return r;
 }
 
 // The j-th largest of the warp's values (j from 1).
@@ -301,13 +317,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t &bar, uint32_t parity, Shared 
     return wait_longer(bar, parity, S, P);
 }
 
-// The same for what other CTAs of the cluster have sent
-__device__ __forceinline__ bool wait_on_cluster(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
-    if (!wait_bar(bar, parity, S, P)) return false;
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return true;
-}
-
 // A CTA's view of the call.
 struct Cta {
     int rank, cluster;
@@ -316,10 +325,77 @@ struct Cta {
     int chunks;
     int lane;
     int depth_log;
+    unsigned long long *words;  // what the cluster's warps have sent
 
     __device__ __forceinline__ int place(int r) const { return r & ((1 << depth_log) - 1); }
     __device__ __forceinline__ uint32_t parity(int r) const { return (uint32_t)r >> depth_log & 1u; }
 };
+
+// Sums between the CTAs of a cluster: each number goes with the row's number (of live rows, from 1) in one 8-byte word, so
+// that whoever reads it knows that it has come; no barrier, no fence. A warp's words have kDepth places. Row x's replace those
+// of row x - 4, which their reader has read: sums of x are sent behind the stores of x - 2 at the latest, these take sums of
+// x - 2 from every CTA, and a CTA sends those behind its own stores of x - 4.
+template <class Kd>
+__device__ __forceinline__ unsigned long long *words_of(const Cta &cta, int warp, int live) {
+    return cta.words + ((size_t)(live & (kDepth - 1)) * cta.cluster * kConsumers + warp) * Kd::kWords;
+}
+
+template <class Kd>
+__device__ __forceinline__ void send(const Cta &cta, int warp, int live, const Part &p) {
+    if (cta.lane >= cta.cluster) return;
+    const uint32_t at = cluster_addr(words_of<Kd>(cta, warp, live), cta.lane);
+    auto put = [&](int i, uint32_t x) {
+        asm volatile("st.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(at + 8 * i),
+                     "l"((unsigned long long)(uint32_t)(live + 1) << 32 | x)
+                     : "memory");
+    };
+    put(0, __float_as_uint(p.m));
+    put(1, __float_as_uint(p.n < 0 ? NAN : p.s));  // a bad logit
+    if (Kd::Ent) put(2, __float_as_uint(p.t));
+    if (Kd::Rank) put(2 + Kd::Ent, (uint32_t)p.n);
+}
+
+// The cluster's sums of its live-th live row.
+template <class Kd>
+__device__ bool receive(const TokenParams &P, Shared &S, const Cta &cta, int live, Part &p) {
+    p = Part{-INFINITY, 0.0f, 0.0f, 0};
+    const uint64_t t0 = global_ns();
+    for (int warp = cta.lane; warp - cta.lane < cta.cluster * kConsumers; warp += 32) {
+        const uint32_t at = smem_u32(words_of<Kd>(cta, warp, live));
+        uint32_t x[Kd::kWords];
+        for (;;) {
+            bool here = true;
+            if (warp < cta.cluster * kConsumers) {
+#pragma unroll
+                for (int i = 0; i < Kd::kWords; ++i) {
+                    unsigned long long w;
+                    asm volatile("ld.relaxed.cluster.shared::cta.b64 %0, [%1];" : "=l"(w) : "r"(at + 8 * i) : "memory");
+                    x[i] = (uint32_t)w;
+                    here = here && (uint32_t)(w >> 32) == (uint32_t)(live + 1);
+                }
+            }
+            if (__all_sync(0xffffffffu, here)) break;
+            if (__any_sync(0xffffffffu, *(volatile int32_t *)&S.abort)) return false;
+            if (__any_sync(0xffffffffu, global_ns() - t0 > P.wait_ns)) {
+                *(volatile int32_t *)&S.abort = 1;
+                atomicOr(P.status, SPECVERIFY_STATUS_TIMEOUT);
+                return false;
+            }
+        }
+        if (warp < cta.cluster * kConsumers) {
+            Part q{__uint_as_float(x[0]), __uint_as_float(x[1]), 0.0f, 0};
+            if (Kd::Ent) q.t = __uint_as_float(x[Kd::kWords - 1 - Kd::Rank]);
+            if (Kd::Rank) q.n = (int)x[Kd::kWords - 1];
+            if (q.s != q.s) {
+                q.s = 0.0f;
+                q.n = -1;
+            }
+            merge(p, q, P.c);
+        }
+    }
+    p = warp_fold<Kd>(p, P.c);
+    return true;
+}
 
 // ---------------------------------------------------------------------------
 // consumers
@@ -413,7 +489,7 @@ __device__ __forceinline__ int count_before(const uint4 &w, float zy, int y, int
 // The sums of a row's slice, chunk after chunk. A gradient's chunks stay for its second reading.
 template <class Kd>
 __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
-                                          const Cta &cta, int d, uint32_t row_parity, int &slot, uint32_t &phase) {
+                                          const Cta &cta, int d, uint32_t row_parity, int live, int &slot, uint32_t &phase) {
     constexpr int kVecs = Kd::kVecs, kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane, warp = tid >> 5;
     const int nth = Kd::Top ? (P.k + kConsumers - 1) / kConsumers : 1;
@@ -561,10 +637,14 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         p.t = g * fmaf(-r, p.s, p.t);
         p.s *= g;
     }
-    p = warp_merge(p, c);
-    if (lane == 0) {
-        S.part[d][warp] = p;
-        mbar_arrive(smem_u32(&S.summed[d]));
+    p = warp_fold<Kd>(p, c);
+    if (cta.cluster == 1) {
+        if (lane == 0) {
+            S.part[d][warp] = p;
+            mbar_arrive(smem_u32(&S.summed[d]));
+        }
+    } else {
+        send<Kd>(cta, cta.rank * kConsumers + warp, live, p);
     }
     return true;
 }
@@ -594,44 +674,61 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
         fb *= g;
     }
     const f32x2 nR = pack2(-R, -R), c2 = pack2(c, c), a2 = pack2(fa, fa), b2 = pack2(fb, fb);
+    auto gradients = [&](const uint4 &w, f32x2 (&g)[kPer / 2]) {
+        if (state != kLive) {
+#pragma unroll
+            for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
+            return;
+        }
+#pragma unroll
+        for (int q = 0; q < kPer / 2; ++q) {
+            const f32x2 x2 = near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c);
+            const float2 x = unpack2(x2);
+            g[q] = mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
+        }
+    };
+    auto packed = [&](const f32x2 (&g)[kPer / 2]) {
+        const float2 x = unpack2(g[0]), y = unpack2(g[1]);
+        if (Kd::DT == SV_DT_FP32)
+            return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+        const float2 z = unpack2(g[2 % (kPer / 2)]), u = unpack2(g[3 % (kPer / 2)]);
+        return make_uint4(to_bf16x2(x.x, x.y), to_bf16x2(y.x, y.y), to_bf16x2(z.x, z.y), to_bf16x2(u.x, u.y));
+    };
     for (int i = 0; i < cta.chunks; ++i) {
         const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * Kd::kChunkBytes);
         const int v0 = i * Kd::kChunkVecs;
+        uint4 *to = reinterpret_cast<uint4 *>(out) + v0 + tid;
+        if (state == kLive && near && v0 + Kd::kChunkVecs <= cta.slice_vecs && cta.slice0 + v0 + Kd::kChunkVecs <= whole) {
+            uint4 w[Kd::kVecs];
 #pragma unroll
-        for (int j = 0; j < Kd::kVecs; ++j) {
-            const int v = v0 + tid + j * kTeam;  // of the slice
-            if (v >= cta.slice_vecs) continue;
-            const bool end = cta.slice0 + v >= whole;
-            f32x2 g[kPer / 2];
-            if (state == kLive) {
-                uint4 w = chunk[tid + j * kTeam];
-                if (!Kd::List && end) w = ragged_end<Kd>(S.row[d].z, whole, rest);
+            for (int j = 0; j < Kd::kVecs; ++j) w[j] = chunk[tid + j * kTeam];
+#pragma unroll
+            for (int j = 0; j < Kd::kVecs; ++j) {
+                f32x2 g[kPer / 2];
 #pragma unroll
                 for (int q = 0; q < kPer / 2; ++q) {
-                    const f32x2 x2 = near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c);
+                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q), c2, nR);
                     const float2 x = unpack2(x2);
                     g[q] = mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
                 }
-            } else {
-#pragma unroll
-                for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
+                to[j * kTeam] = packed(g);
             }
-            char *to = out + (int64_t)v * 16;
-            if (!end) {
-                uint4 r;
-                const float2 x = unpack2(g[0]), y = unpack2(g[1]);
-                if (Kd::DT == SV_DT_FP32) {
-                    r = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < Kd::kVecs; ++j) {
+                const int v = v0 + tid + j * kTeam;  // of the slice
+                if (v >= cta.slice_vecs) break;
+                const bool end = cta.slice0 + v >= whole;
+                f32x2 g[kPer / 2];
+                gradients(!Kd::List && end && state == kLive ? ragged_end<Kd>(S.row[d].z, whole, rest) : chunk[tid + j * kTeam], g);
+                if (!end) {
+                    to[j * kTeam] = packed(g);
                 } else {
-                    const float2 z = unpack2(g[2 % (kPer / 2)]), u = unpack2(g[3 % (kPer / 2)]);
-                    r = make_uint4(to_bf16x2(x.x, x.y), to_bf16x2(y.x, y.y), to_bf16x2(z.x, z.y), to_bf16x2(u.x, u.y));
-                }
-                *reinterpret_cast<uint4 *>(to) = r;
-            } else {
 #pragma unroll
-                for (int q = 0; q < kPer; ++q) {
-                    const float2 x = unpack2(g[q / 2]);
-                    if (q < rest) store_logit<Kd::DT>(to, q, q & 1 ? x.y : x.x);
+                    for (int q = 0; q < kPer; ++q) {
+                        const float2 x = unpack2(g[q / 2]);
+                        if (q < rest) store_logit<Kd::DT>(reinterpret_cast<char *>(to + j * kTeam), q, q & 1 ? x.y : x.x);
+                    }
                 }
             }
         }
@@ -649,7 +746,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
 template <class Kd>
 __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
                                         const Cta &cta) {
-    int slot = 0, gslot = 0, r = 0;
+    int slot = 0, gslot = 0, r = 0, live = 0;
     uint32_t phase = 0;
     auto store = [&](int g) {
         const int d = cta.place(g);
@@ -662,10 +759,10 @@ __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, 
         if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
         if (S.row[d].state == kEnd) break;
         if (S.row[d].state == kLive) {
-            if (!sum_slice<Kd>(P, plan, S, top, ring, cta, d, cta.parity(r), slot, phase)) return;
+            if (!sum_slice<Kd>(P, plan, S, top, ring, cta, d, cta.parity(r), live++, slot, phase)) return;
         } else if (cta.lane == 0) {
             if (Kd::Top) mbar_arrive(smem_u32(&S.bounded[d]));
-            mbar_arrive(smem_u32(&S.summed[d]));
+            if (cta.cluster == 1) mbar_arrive(smem_u32(&S.summed[d]));
         }
         if (!Kd::Grad) {
             __syncwarp();
@@ -786,12 +883,14 @@ __device__ __forceinline__ void scout_token(const TokenParams &P, Row &row, long
 
 // A list: its ids, the draft's logits of them, the target's log-probabilities.
 template <int DT>
-__device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, SharedList &L, int d, long long e, int lane, const Asked &a) {
+__device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const Lists &L, int d, long long e, int lane, const Asked &a) {
     constexpr uint32_t all = 0xffffffffu;
     const char *z = P.logits + e * P.stride_bytes;
+    int32_t *ids = L.ids + d * L.stride;
+    float *lz = L.z + d * L.stride, *llp = L.lp + d * L.stride, *lpr = L.p + d * L.stride;
     int bits = 0;
     bool any = false;
-    float top = -INFINITY;
+    float top = -INFINITY, zmax = -INFINITY;
     float zk[kMaxList / 32];
 #pragma unroll
     for (int i = 0; i < kMaxList / 32; ++i) {
@@ -819,56 +918,72 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, Share
                 if (was == -1 || was == id) break;
             }
         }
-        L.ids[d][j] = id;
-        L.z[d][j] = zk[i];
-        L.lp[d][j] = t;
+        ids[j] = id;
+        lz[j] = zk[i];
+        llp[j] = t;
         top = fmaxf(top, t);
+        zmax = fmaxf(zmax, zk[i]);
     }
     __syncwarp();
     for (int j = lane; j < kHash / 4; j += 32) reinterpret_cast<int4 *>(L.hash)[j] = make_int4(-1, -1, -1, -1);
     bits = __reduce_or_sync(all, bits);
     any = __any_sync(all, any);
-    float p_rest = 0.0f;
+    float p_rest = 0.0f, p_sum = 0.0f, zsum = 0.0f;
+    zmax = warp_max(zmax);
     if (!bits && any) {
         if (P.form == SPECVERIFY_TARGET_LOGITS) {
             top = warp_max(top);
             float sum = 0.0f, lh = 0.0f, ll = 0.0f;
             for (int j = lane; j < P.K; j += 32) {
                 float h, l;
-                ff_logprob(P, L.lp[d][j], top, 0.0f, 0.0f, h, l);
-                sum += L.lp[d][j] == -INFINITY ? 0.0f : ff_exp(h, l);
+                ff_logprob(P, llp[j], top, 0.0f, 0.0f, h, l);
+                sum += llp[j] == -INFINITY ? 0.0f : ff_exp(h, l);
             }
             sum = warp_sum(sum);
             if (top == -INFINITY) bits = SPECVERIFY_STATUS_BAD_LOGIT;  // a target of nothing
             else ff_log(sum, lh, ll);
             for (int j = lane; j < P.K; j += 32) {
                 float h, l;
-                ff_logprob(P, L.lp[d][j], top, lh, ll, h, l);
-                L.lp[d][j] = L.lp[d][j] == -INFINITY ? -INFINITY : h;
+                ff_logprob(P, llp[j], top, lh, ll, h, l);
+                if (llp[j] == -INFINITY) h = -INFINITY;
+                llp[j] = h;
+                lpr[j] = ff_exp(h, 0.0f);
+                p_sum += lpr[j];
             }
+            p_sum = warp_sum(p_sum);
         } else {
             // One less a sum close to it: in 64 bits, or little would be left of it. (Off everybody's way: the scout is rows
             // ahead.)
             double sum = 0.0;
-            for (int j = lane; j < P.K; j += 32)
-                if (L.lp[d][j] > -INFINITY) sum += exp((double)L.lp[d][j]);
+            for (int j = lane; j < P.K; j += 32) {
+                const double x = llp[j] > -INFINITY ? exp((double)llp[j]) : 0.0;
+                lpr[j] = (float)x;
+                sum += x;
+            }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(all, sum, off);
             p_rest = (float)fmax(1.0 - sum, 0.0);
+            p_sum = (float)sum;
         }
+        if (zmax > -INFINITY)
+            for (int j = lane; j < P.K; j += 32) zsum += ex2_approx(fmaxf(lz[j] - zmax, kFar) * P.c);
+        zsum = warp_sum(zsum);
     }
     if (lane == 0) {
         row.z = z;
         row.entry = e;
         row.state = bits ? kBad : any ? kLive : kSkip;
         row.p_rest = p_rest;
+        row.p_sum = p_sum;
+        row.zmax = zmax;
+        row.zsum = zsum;
         row.g = a.g;
         if (bits) atomicOr(P.status, bits);
     }
 }
 
 template <class Kd>
-__device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, SharedList *list,
+__device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const Lists &list,
                                       const Cta &cta) {
     Entries at;
     Asked a;
@@ -880,7 +995,7 @@ __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Sh
         if (at.e < 0) {
             if (cta.lane == 0) S.row[d].state = kEnd;
         } else if (Kd::List) {
-            scout_list<Kd::DT>(P, S.row[d], *list, d, at.e, cta.lane, a);
+            scout_list<Kd::DT>(P, S.row[d], list, d, at.e, cta.lane, a);
         } else if (cta.lane == 0) {
             scout_token<Kd::DT>(P, S.row[d], at.e, a);
             if (Kd::Top) top->count[d] = 0;
@@ -940,7 +1055,7 @@ __device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, 
 }
 
 template <class Kd>
-__device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Shared &S, const SharedList &L, uint8_t *ring,
+__device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Shared &S, const Lists &L, uint8_t *ring,
                                       const Cta &cta) {
     const int whole = P.V / Kd::kPer, rest = P.V - whole * Kd::kPer;
     int slot = 0, r = 0;
@@ -962,7 +1077,7 @@ __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Sh
                 __syncwarp();
             }
             for (int j = cta.lane; j < P.K; j += 32) {
-                const int at = L.ids[d][j] - v0 * Kd::kPer;
+                const int at = L.ids[d * L.stride + j] - v0 * Kd::kPer;
                 if (at >= 0 && at < n * Kd::kPer) store_logit<Kd::DT>(reinterpret_cast<char *>(chunk), at, -INFINITY);
             }
             // the next copy into this slot comes after these stores
@@ -1086,66 +1201,66 @@ __device__ __forceinline__ void write_top(const TokenParams &P, long long e, int
     P.top_idx[e * P.k + i] = idx;
 }
 
-// The cluster's sums from each CTA's. Rows of a gradient follow one another through two sets of slots: a CTA sends a row's
-// sums once it has read those of the row before, so a slot is free again when its next sums arrive.
-__device__ __forceinline__ bool exchange(const TokenParams &P, Shared &S, const Cta &cta, int x, Part &p) {
-    const int lane = cta.lane, set = x & 1;
-    if (lane < cta.cluster) {
-        st_cluster_f4(cluster_addr(&S.others[set][cta.rank], lane), make_float4(p.m, p.s, p.t, __int_as_float(p.n)));
-        cluster_arrive(S.exchanged[set], lane);
-    }
-    if (!wait_on_cluster(S.exchanged[set], x >> 1 & 1, S, P)) return false;
-    p = lane < cta.cluster ? S.others[set][lane] : Part{-INFINITY, 0.0f, 0.0f, 0};
-    p = warp_merge(p, P.c);
-    return true;
-}
-
 template <class Kd>
-__device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, SharedTop *T, const Cta &cta, int d, Part p,
-                                             int &x) {
+__device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, SharedTop *T, const Cta &cta, int d, const Part &p) {
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane, k = Kd::Top ? P.k : 0;
     const bool alone = cta.cluster == 1;
-    if (row.state == kLive) {
-        if (k) {
+    const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || p.m == -INFINITY));
+    const bool good = row.state == kLive && !bad;
+    if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
+    float lh = 0.0f, ll = 0.0f, lp = 0.0f, lo = 0.0f, H = 0.0f;
+    const float inv_s = 1.0f / p.s;
+    // p_v (-(g + h (ln p_v + H)) / T) with p_v = 2^x / s and ln p_v = x ln 2 - ln s
+    if (Kd::Grad && !Kd::Ent && lane == 0) {
+        S.coef[d] = good ? make_float4(p.m, -row.g * P.inv_hi * inv_s, 0.0f, 0.0f) : make_float4(0.0f, NAN, 0.0f, 0.0f);
+        mbar_arrive(smem_u32(&S.known[d]));
+    }
+    if (good) {
+        ff_log(p.s, lh, ll);
+        if (Kd::Ent) {
+            const float mean = p.t / p.s;
+            H = lh - fmaf(mean, kLn2Hi, fmaf(mean, kLn2Lo, -ll));
+        }
+    }
+    if (Kd::Grad && Kd::Ent && lane == 0) {
+        const float a = -(row.g + row.h * (H - lh)) * P.inv_hi * inv_s, b = -row.h * P.inv_hi * kLn2Hi * inv_s;
+        S.coef[d] = good ? make_float4(p.m, a, b, 0.0f) : make_float4(0.0f, NAN, NAN, 0.0f);
+        mbar_arrive(smem_u32(&S.known[d]));
+    }
+    if (good) ff_logprob(P, row.zy, p.m, lh, ll, lp, lo);
+    else if (bad) lp = H = NAN;
+    if (lane == 0 && cta.rank == 0) {
+        if (P.logprob) P.logprob[e] = lp;
+        if (P.entropy) P.entropy[e] = H;
+        if (!Kd::Grad && P.lse) {
+            float xh = 0.0f, xl = 0.0f;
+            if (good) {
+                over_T(P, p.m, 0.0f, xh, xl);
+                if (fabsf(xh) < INFINITY) ff_add(xh, xl, lh, ll, xh, xl);
+            }
+            P.lse[e] = bad ? NAN : xh;
+        }
+        if (Kd::Rank) P.rank[e] = bad ? -1 : p.n;
+    }
+    if constexpr (Kd::Top) {
+        if (row.state == kLive) {
             select_top<Kd::DT>(P, row.z, *T, d, cta);
-            if (!alone)
+            if (!alone) {
                 for (int i = lane; i < k; i += 32)
                     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(&T->gathered[cta.rank * k + i], 0)),
                                  "l"(T->best[i])
                                  : "memory");
-            __syncwarp();
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) cluster_arrive(S.gathered, 0);
+                if (cta.rank != 0) return true;
+                if (!wait_bar(S.gathered, 0, S, P)) return false;  // a cluster of such rows has one
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            }
         }
-        if (!alone) {
-            if (k) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-            __syncwarp();
-            if (!exchange(P, S, cta, x++, p)) return false;
-        }
-    }
-    const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || p.m == -INFINITY));
-    if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
-    const bool good = row.state == kLive && !bad;
-    float lh = 0.0f, ll = 0.0f, lp = 0.0f, lo = 0.0f, H = 0.0f, lse = 0.0f;
-    if (good) {
-        ff_log(p.s, lh, ll);
-        ff_logprob(P, row.zy, p.m, lh, ll, lp, lo);
-        const float mean = p.t / p.s;
-        H = lh - fmaf(mean, kLn2Hi, fmaf(mean, kLn2Lo, -ll));
-        float xh, xl;
-        over_T(P, p.m, 0.0f, xh, xl);
-        if (fabsf(xh) < INFINITY) ff_add(xh, xl, lh, ll, xh, xl);
-        lse = xh;
-    } else if (bad) {
-        lp = H = lse = NAN;
-    }
-    if (lane == 0 && cta.rank == 0) {
-        if (P.logprob) P.logprob[e] = lp;
-        if (P.entropy) P.entropy[e] = H;
-        if (!Kd::Grad && P.lse) P.lse[e] = lse;
-        if (Kd::Rank) P.rank[e] = bad ? -1 : p.n;
-    }
-    if constexpr (Kd::Top) if (cta.rank == 0) {
+        if (cta.rank != 0) return true;
         if (!good) {
             for (int i = lane; i < k; i += 32) {
                 P.top_logprob[e * k + i] = bad ? NAN : -INFINITY;
@@ -1163,30 +1278,23 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
                 int place = i % k;
                 for (int c = 0; c < cta.cluster && place < k; ++c) {
                     if (c == i / k) continue;
-                    int lo_ = 0, hi_ = k;  // keys [0, lo_) are larger, [hi_, k) are not
-                    while (lo_ < hi_) {
-                        const int mid = (lo_ + hi_) >> 1;
-                        if (T->gathered[c * k + mid] > key) lo_ = mid + 1;
-                        else hi_ = mid;
+                    int from = 0, to = k;  // keys [0, from) are larger, [to, k) are not
+                    while (from < to) {
+                        const int mid = (from + to) >> 1;
+                        if (T->gathered[c * k + mid] > key) from = mid + 1;
+                        else to = mid;
                     }
-                    place += lo_;
+                    place += from;
                 }
                 if (place < k) write_top<Kd::DT>(P, e, place, key, p.m, lh, ll);
             }
         }
     }
-    if (Kd::Grad) {
-        const float g = row.g, h = row.h;
-        // p_v (-(g + h (ln p_v + H)) / T) with p_v = 2^x / s and ln p_v = x ln 2 - ln s
-        const float inv_s = 1.0f / p.s;
-        const float a = -(g + h * (H - lh)) * P.inv_hi * inv_s, b = -h * P.inv_hi * kLn2Hi * inv_s;
-        if (lane == 0) {
-            const float py = ff_exp(lp, lo);
-            const float s = py > 0.0f ? h * py * (lp + H) : 0.0f;
-            S.coef[d] = good ? make_float4(p.m, a, b, (g * (1.0f - py) - s) * P.inv_hi) : make_float4(0.0f, NAN, NAN, 0.0f);
-            S.fix[d] = good;
-            mbar_arrive(smem_u32(&S.known[d]));
-        }
+    if (Kd::Grad && lane == 0) {
+        const float py = ff_exp(lp, lo);
+        const float s = Kd::Ent && py > 0.0f ? row.h * py * (lp + H) : 0.0f;
+        S.fix[d] = (row.g * (1.0f - py) - s) * P.inv_hi;
+        S.good[d] = good;
     }
     return true;
 }
@@ -1195,68 +1303,70 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
 template <class Kd>
 __device__ __forceinline__ void fix_token(const TokenParams &P, const Shared &S, const Cta &cta, int d) {
     const int y = S.row[d].y, v = y / Kd::kPer;
-    if (S.fix[d] && cta.lane == 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
-        store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, y, S.coef[d].w);
+    if (cta.lane == 0 && S.good[d] && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
+        store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, y, S.fix[d]);
 }
 
 // The same for a list's tokens.
 template <class Kd>
-__device__ __forceinline__ void fix_list(const TokenParams &P, const Shared &S, const SharedList &L, const Cta &cta, int d) {
-    if (!S.fix[d]) return;
-    const float w = S.row[d].g * P.inv_hi, C = S.coef[d].w;
+__device__ __forceinline__ void fix_list(const TokenParams &P, const Shared &S, const Lists &L, const Cta &cta, int d) {
+    if (!S.good[d]) return;
+    const float w = S.row[d].g * P.inv_hi, C = S.fix[d];
     for (int j = cta.lane; j < P.K; j += 32) {
-        const int id = L.ids[d][j], v = id / Kd::kPer;
+        const int at = d * L.stride + j, id = L.ids[at], v = id / Kd::kPer;
         if (id >= 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
-            store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, id, w * (L.lp[d][j] - L.z[d][j] * C));
+            store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, id, w * (L.lp[at] - L.z[at] * C));
     }
 }
 
 // The divergence over the list's tokens and the rest, see include/specverify.h. Logarithms are pairs of floats up to their
 // differences: a small divergence is a difference of much larger terms.
 template <class Kd>
-__device__ __forceinline__ bool finish_list(const TokenParams &P, Shared &S, SharedList &L, const Cta &cta, int d, Part p,
-                                            int &x) {
+__device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, const Lists &L, const Cta &cta, int d, const Part &p) {
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane, K = P.K, kind = P.divergence;
-    if (row.state == kLive && cta.cluster > 1 && !exchange(P, S, cta, x++, p)) return false;
-    float zmax = -INFINITY;
-    if (row.state == kLive)
-        for (int j = lane; j < K; j += 32) zmax = fmaxf(zmax, L.z[d][j]);
-    zmax = warp_max(zmax);
-    const float M = fmaxf(p.m, zmax);
+    const float M = fmaxf(p.m, row.zmax);
     const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || M == -INFINITY));
     const bool good = row.state == kLive && !bad;
-    if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
-    float loss = bad ? NAN : 0.0f, factor = 0.0f, C = 0.0f;
     const bool some = p.m > -INFINITY;  // the rest has mass
+    if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
+    float loss = bad ? NAN : 0.0f, C = 0.0f, Z = 0.0f;
     if (good) {
-        float Z = 0.0f;
-        for (int j = lane; j < K; j += 32) Z += ex2_approx(fmaxf(L.z[d][j] - M, kFar) * P.c);
-        Z = warp_sum(Z);
+        if (row.zmax > -INFINITY) Z = row.zsum * ex2_approx(fmaxf(row.zmax - M, kFar) * P.c);
         if (some) Z = fmaf(p.s, ex2_approx(fmaxf(p.m - M, kFar) * P.c), Z);
+    }
+    // the others' share of a gradient, (h_rest - q_rest C) / (s T) times 2^((z - m) c)
+    auto known = [&](float h_rest, float q_rest) {
+        if (lane == 0) {
+            const float f = some ? row.g * P.inv_hi * (h_rest - q_rest * C) / p.s : 0.0f;
+            S.coef[d] = bad ? make_float4(0.0f, NAN, 0.0f, 0.0f) : make_float4(some ? p.m : 0.0f, f, 0.0f, 0.0f);
+            mbar_arrive(smem_u32(&S.known[d]));
+        }
+    };
+    if (Kd::Grad && (!good || kind == SPECVERIFY_FKL)) {  // here sum h = -sum p is known beforehand
+        C = -(row.p_sum + row.p_rest);
+        known(-row.p_rest, good && some ? p.s * ex2_approx(fmaxf(p.m - M, kFar) * P.c) / Z : 0.0f);
+    }
+    if (good) {
         float zh, zl;
         ff_log(Z, zh, zl);
         float f = 0.0f, h = 0.0f, h_rest = 0.0f, q_rest = 0.0f;
         // outcome K is the rest
         for (int j = lane; j <= K; j += 32) {
             const bool rest = j == K;
-            if (!rest && L.ids[d][j] < 0) continue;
-            float qh, ql, lp = rest ? -INFINITY : L.lp[d][j];
-            ff_logprob(P, rest ? p.m : L.z[d][j], M, zh, zl, qh, ql);
+            const int at = d * L.stride + j;
+            if (!rest && L.ids[at] < 0) continue;
+            float qh, ql;
+            ff_logprob(P, rest ? p.m : L.z[at], M, zh, zl, qh, ql);
             if (rest && some) {
                 float sh, sl;
                 ff_log(p.s, sh, sl);
                 if (qh > -INFINITY) ff_add(qh, ql, sh, sl, qh, ql);
             }
             const float q = ff_exp(qh, ql);
-            float pr;
-            if (rest) {
-                pr = row.p_rest;
-                lp = logf(kind == SPECVERIFY_RKL ? fmaxf(pr, 0x1p-20f) : pr);
-            } else {
-                pr = ff_exp(lp, 0.0f);
-            }
+            const float pr = rest ? row.p_rest : L.p[at];
+            const float lp = rest ? logf(kind == SPECVERIFY_RKL ? fmaxf(pr, 0x1p-20f) : pr) : L.lp[at];
             float fj = 0.0f, hj = 0.0f;
             if (kind == SPECVERIFY_FKL) {
                 if (pr > 0.0f) fj = pr * ((lp - qh) - ql);
@@ -1278,37 +1388,31 @@ __device__ __forceinline__ bool finish_list(const TokenParams &P, Shared &S, Sha
             if (rest) {
                 h_rest = hj;
                 q_rest = q;
-            } else {
-                L.lp[d][j] = hj;  // what the gradient needs of it
-                L.z[d][j] = q;
+            } else if (Kd::Grad) {
+                L.lp[at] = hj;
+                L.z[at] = q;
             }
         }
         loss = warp_sum(f);
-        C = warp_sum(h);
-        if (Kd::Grad) {
-            h_rest = __shfl_sync(0xffffffffu, h_rest, K & 31);
-            q_rest = __shfl_sync(0xffffffffu, q_rest, K & 31);
-            factor = some ? row.g * P.inv_hi * (h_rest - q_rest * C) / p.s : 0.0f;
+        if (Kd::Grad && kind != SPECVERIFY_FKL) {
+            C = warp_sum(h);
+            known(__shfl_sync(0xffffffffu, h_rest, K & 31), __shfl_sync(0xffffffffu, q_rest, K & 31));
         }
     }
     if (lane == 0 && cta.rank == 0) P.loss[e] = loss;
-    if (Kd::Grad) {
-        if (lane == 0) {
-            S.coef[d] = bad ? make_float4(0.0f, NAN, 0.0f, 0.0f) : make_float4(some ? p.m : 0.0f, factor, 0.0f, C);
-            S.fix[d] = good;
-            mbar_arrive(smem_u32(&S.known[d]));
-        }
+    if (Kd::Grad && lane == 0) {
+        S.fix[d] = C;
+        S.good[d] = good;
     }
-    return true;
 }
 
 template <class Kd>
-__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, SharedList *L, const Cta &cta) {
-    int r = 0, x = 0;
+__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Lists &L, const Cta &cta) {
+    int r = 0, live = 0;
     auto fix = [&](int g) {
         const int d = cta.place(g);
         if (!wait_bar(S.stored[d], cta.parity(g), S, P)) return false;
-        if (Kd::List) fix_list<Kd>(P, S, *L, cta, d);
+        if (Kd::List) fix_list<Kd>(P, S, L, cta, d);
         else fix_token<Kd>(P, S, cta, d);
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
@@ -1318,14 +1422,20 @@ __device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, S
         const int d = cta.place(r);
         const uint32_t parity = cta.parity(r);
         if (!wait_bar(S.row_full[d], parity, S, P)) return;
-        if (S.row[d].state == kEnd) break;
-        if (!wait_bar(S.summed[d], parity, S, P)) return;
+        const int state = S.row[d].state;
+        if (state == kEnd) break;
         Part p{-INFINITY, 0.0f, 0.0f, 0};
-        if (S.row[d].state == kLive) {
-            if (cta.lane < kConsumers) p = S.part[d][cta.lane];
-            p = warp_merge(p, P.c);
+        if (cta.cluster == 1) {
+            if (!wait_bar(S.summed[d], parity, S, P)) return;
+            if (state == kLive) {
+                if (cta.lane < kConsumers) p = S.part[d][cta.lane];
+                p = warp_fold<Kd>(p, P.c);
+            }
+        } else if (state == kLive && !receive<Kd>(P, S, cta, live++, p)) {
+            return;
         }
-        if (Kd::List ? !finish_list<Kd>(P, S, *L, cta, d, p, x) : !finish_token<Kd>(P, S, T, cta, d, p, x)) return;
+        if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
+        else if (!finish_token<Kd>(P, S, T, cta, d, p)) return;
         __syncwarp();
         // A gradient's next row is not kept waiting for the stores of this one.
         if (Kd::Grad) {
@@ -1336,6 +1446,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, S
     }
     if (Kd::Grad && plan.lag && r > 0) fix(r - 1);
 }
+
 // ---------------------------------------------------------------------------
 
 template <class Kd>
@@ -1346,7 +1457,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
     void *more = reinterpret_cast<uint8_t *>(&S) + kFixed;
     SharedTop *top = Kd::Top ? static_cast<SharedTop *>(more) : nullptr;
-    SharedList *list = Kd::List ? static_cast<SharedList *>(more) : nullptr;
+    Lists list{};
+    if (Kd::List) {
+        list.stride = plan.list_stride;
+        list.hash = static_cast<int32_t *>(more);
+        list.ids = list.hash + kHash;
+        list.z = reinterpret_cast<float *>(list.ids + kDepth * list.stride);
+        list.lp = list.z + kDepth * list.stride;
+        list.p = list.lp + kDepth * list.stride;
+    }
     const int tid = threadIdx.x, warp = tid >> 5;
 
     Cta cta;
@@ -1359,6 +1478,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     cta.chunks = (cta.slice_vecs + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
     cta.lane = tid & 31;
     cta.depth_log = plan.depth_log;
+    cta.words = reinterpret_cast<unsigned long long *>(smem + plan.words_at);
 
     if (tid == 0) {
         for (int i = 0; i < plan.slots; ++i) {
@@ -1375,13 +1495,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
             mbar_init(smem_u32(&S.bounded[i]), kConsumers);
         }
         mbar_init(smem_u32(&S.granted), 1);
-        mbar_init(smem_u32(&S.exchanged[0]), plan.cluster);
-        mbar_init(smem_u32(&S.exchanged[1]), plan.cluster);
+        mbar_init(smem_u32(&S.gathered), plan.cluster);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (Kd::List)
-        for (int i = tid; i < kHash; i += kThreads) list->hash[i] = -1;
+        for (int i = tid; i < kHash; i += kThreads) list.hash[i] = -1;
+    if (plan.cluster > 1)
+        for (int i = tid; i < kDepth * plan.cluster * kConsumers * Kd::kWords; i += kThreads) cta.words[i] = 0;
     __syncthreads();
     if (plan.cluster > 1) cluster_sync();
     after_previous();
@@ -1389,7 +1510,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     if (warp < kConsumers) consume<Kd>(P, plan, S, top, ring, cta);
     else if (warp == kScout) scout<Kd>(P, plan, S, top, list, cta);
     else if (warp == kProducer) produce<Kd>(P, plan, S, ring, cta);
-    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, *list, ring, cta);
+    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, list, ring, cta);
     else if (warp == kEpilogue) finish<Kd>(P, plan, S, top, list, cta);
     __syncwarp();
     // sums of other CTAs may still be on their way here where somebody gave up
@@ -1412,9 +1533,13 @@ struct Room {
 template <class Kd>
 Plan make_plan(const TokenParams &P) {
     const int64_t vecs = ((int64_t)P.V * Kd::kSize + 15) / 16;
-    const int fixed = (int)((sizeof(Shared) + 15) / 16 * 16 + (Kd::List ? sizeof(SharedList) : Kd::Top ? sizeof(SharedTop) : 0));
-    const int half = std::min(kMaxSlots, (kHalfSmem - fixed) / Kd::kChunkBytes);
-    const int full = std::min(kMaxSlots, (kFullSmem - fixed) / Kd::kChunkBytes);
+    Plan p{};
+    p.depth_log = Kd::Top ? 1 : 2;
+    p.list_stride = Kd::List ? (P.K + 31) / 32 * 32 : 0;
+    const int fixed = (int)((sizeof(Shared) + 15) / 16 * 16) +
+                      (Kd::List ? kHashBytes + p.list_stride * kListBytes : Kd::Top ? (int)((sizeof(SharedTop) + 15) / 16 * 16) : 0);
+    auto words = [&](int log) { return log ? (kDepth * kConsumers * Kd::kWords * 8) << log : 0; };
+    auto slots = [&](int log, int smem) { return std::min(kMaxSlots, (smem - fixed - words(log)) / Kd::kChunkBytes); };
     auto chunks = [&](int log) {
         const int64_t slice = ((vecs + (1 << log) - 1 >> log) + 31) / 32 * 32;
         return (slice + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
@@ -1422,18 +1547,17 @@ Plan make_plan(const TokenParams &P) {
     const auto &room = Room<Kd>::clusters;
     int log = 0;
     if (Kd::Grad)
-        while (log < 4 && 2 * chunks(log) > half) ++log;
+        while (log < 4 && 2 * chunks(log) > slots(log, kHalfSmem)) ++log;
     while (log < 4 && P.entries <= room[0][log + 1] && vecs >> log >= 256 && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
-    Plan p{};
-    p.depth_log = Kd::Top ? 1 : 2;
     p.cluster = 1 << log;
     p.slice_vecs = (int32_t)(((vecs + p.cluster - 1 >> log) + 31) / 32 * 32);
-    p.lag = Kd::Grad && 2 * chunks(log) <= half;
-    const bool whole_sm = Kd::Grad && chunks(log) > half;
-    p.slots = whole_sm ? full : half;
+    const bool whole_sm = Kd::Grad && chunks(log) > slots(log, kHalfSmem);
+    p.slots = slots(log, whole_sm ? kFullSmem : kHalfSmem);
+    p.lag = Kd::Grad && 2 * chunks(log) <= p.slots;
     p.dynamic = log == 0 && P.entries <= INT32_MAX;
     p.clusters = (int32_t)(p.dynamic ? P.entries : std::min<int64_t>(P.entries, std::max(1, room[whole_sm][log])));
-    p.smem = p.slots * Kd::kChunkBytes + fixed;
+    p.words_at = p.slots * Kd::kChunkBytes + fixed;
+    p.smem = p.words_at + words(log);
     return p;
 }
 
