@@ -244,7 +244,6 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
 
 #define SPECVERIFY_MAX_ALTERNATIVES 128 /* top tokens of a row, specverify_token_logprobs */
 #define SPECVERIFY_MAX_LIST 256         /* listed tokens of a row, specverify_distill_* */
-#define SPECVERIFY_MAX_GRAD_ROW (1 << 21) /* bytes of a row's logits in the calls with gradients */
 
 /* Log-probabilities of given tokens: what a server returns of the tokens that a
  * verify step emitted, or a sequence's likelihood. Entry (b, m), b < B, m < M,
@@ -277,8 +276,7 @@ int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype,
  * logits themselves (same address and stride), and else shares no memory with
  * the inputs. Rows of token -1 get a gradient of 0 and are not read. What lies
  * between rows stays as it was. logprob and entropy [rows] may be NULL. Each row
- * is read once and written once; V * element size is at most
- * SPECVERIFY_MAX_GRAD_ROW (SPECVERIFY_ERR_TOO_LARGE). */
+ * is read (a second time from L2) and written once. */
 int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
                                    int64_t V, int64_t row_stride, float temperature,
                                    const int32_t *tokens, const float *grad_logprob,
@@ -332,8 +330,8 @@ int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, i
 /* The divergence and its gradient: grad[r, v] = weight[r] dloss[r] / dlogits[r, v]
  * (weight NULL: 1), for a list's token (h_k - q_k C) / T and for the others
  * (h_rest - q_rest C) q_v / (q_rest T) with h = q dloss/dq of each outcome, C = sum h. grad, its
- * layout, its sizes and rows without a list: as in specverify_token_logprobs_grad.
- * Each row is read once and written once. loss [rows] is the unweighted one. */
+ * layout and rows without a list: as in specverify_token_logprobs_grad. loss
+ * [rows] is the unweighted one. */
 int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
                             int64_t V, int64_t row_stride, float temperature,
                             const specverify_lists *lists, const float *weight, void *grad,

@@ -4,26 +4,30 @@
 // and the gradients of both: one pass over rows of logits.
 //
 // A row is taken by a cluster of S CTAs, each a slice of it; S = 1 where there
-// are rows enough. Slices come in chunks of 8 KiB by bulk copies into a ring of
-// shared memory. The warps of a CTA:
-//   consumers (8)  a chunk's vectors, two a thread: the running maximum m, the
-//                  sum s of 2^((z - m) c) and t of 2^((z - m) c) (z - m), c =
-//                  log2(e) / T; for a gradient, once the row's sums are known,
-//                  again over the same chunks, to store it;
-//   scout          what a row's entry asks for (its token, or its list with
-//                  the logits and probabilities of it), up to kDepth rows ahead;
+// are rows enough. Slices come in chunks of 16 KiB by bulk copies into a ring of
+// shared memory; a gradient's slice comes twice, the second time backwards and
+// from L2. The warps of a CTA:
+//   consumers (8)  a chunk's vectors, four a thread: the running maximum m, the
+//                  sums s of 2^x and t of 2^x x, x = (z - m) log2(e) / T; on the
+//                  second reading, with the row's sums known, the gradient;
+//   scout          the next row, and what its entry asks for (its token, or its
+//                  list with the logits and probabilities of it);
 //   producer       the copies;
 //   patcher        (lists) takes the listed tokens out of a chunk that has
 //                  arrived (-inf), so that the sums are over the rest alone;
 //   epilogue       merges the warps' sums (and the cluster's), picks the top
 //                  tokens, writes the results, and hands the consumers what a
 //                  gradient's second reading needs.
-// No warp waits for the end of a row but the consumers of a gradient.
+// No warp waits for the end of a row but the consumers of a gradient. Rows are
+// taken over from CTAs (clusters) that have not begun, one at a time, when the
+// copies of the row before are on their way: CTAs differ by a sixth in speed.
 #pragma once
 
 #include "sv_token.h"
 #include "sv_rows.cuh"
 #include "sv_tree.h"
+
+#include <cuda_bf16.h>
 
 #include <algorithm>
 
@@ -39,7 +43,7 @@ constexpr int kMaxSlots = 26;
 constexpr int kDepth = 4;                         // rows between the scout and the epilogue at most
 constexpr int kTopDepth = 2;                      // the same where top tokens are asked for (their buffers are large)
 constexpr int kMaxCluster = 16;
-constexpr int kCandidates = 1536;                 // vectors that may hold top tokens: a chunk of ties, and more
+constexpr int kCandidates = 192;                  // a warp's vectors that may hold top tokens: its share of a chunk of ties, and more
 constexpr int kKeys = 1024;                       // tokens among them
 constexpr int kGathered = 512;                    // keys that a cluster's CTAs send to its first
 constexpr int kHash = 1024;
@@ -81,14 +85,17 @@ struct Part {
 
 struct Shared {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots];
-    uint64_t row_full[kDepth], row_free[kDepth], summed[kDepth], known[kDepth], stored[kDepth], bounded[kDepth];
-    uint64_t gathered, granted;
+    // of a row: asked for and checked; done with; its copies issued; the CTA's sums there, its bounds (top tokens); of a
+    // gradient: what the second reading needs, all stored
+    uint64_t row_full[kDepth], row_free[kDepth], sent[kDepth], summed[kDepth], bounded[kDepth], known[kDepth], stored[kDepth];
+    uint64_t gathered, granted, acked;
     uint4 grant;          // the answer to a request for another row
     Row row[kDepth];
     Part part[kDepth][kConsumers];  // of the CTA's warps where a row is one CTA's
     float4 coef[kDepth];  // of the gradient: m, a, b (see store_slice)
     float fix[kDepth];    // the given token's gradient, or what a list's needs
     int good[kDepth];
+    int asked;            // requests made (the first CTA's)
     int32_t abort;
 };
 
@@ -96,11 +103,11 @@ struct Shared {
 // token's, inverted: keys fall in the order of alternatives, and 0 is none.
 struct SharedTop {
     unsigned long long bound[kTopDepth][kConsumers];  // that many tokens are at least so large; chunk
-    int32_t at[kTopDepth][kCandidates];            // vectors of the row with a token that reaches the bound of its time
+    int32_t at[kTopDepth][kConsumers][kCandidates];   // vectors of the row with a token that reaches the bound of its time
+    int count[kTopDepth][kConsumers];
     unsigned long long keys[kKeys];
     unsigned long long best[kMaxAlternatives];
     unsigned long long gathered[kGathered];
-    unsigned count[kTopDepth], found;
 };
 
 // Lists of kDepth rows, `stride` entries each, in shared memory.
@@ -118,14 +125,14 @@ constexpr int kListBytes = kDepth * 16, kHashBytes = kHash * 4;  // an entry of 
 // How a call's rows are laid out over the GPU.
 struct Plan {
     int32_t cluster;      // CTAs of a row
+    int32_t clusters;     // of the grid
+    int32_t dynamic;      // a cluster takes its next row when it is free for it (else every clusters-th)
+    int32_t eager;        // and at once, rows being short
     int32_t slots;        // of a ring
     int32_t slice_vecs;   // vectors of a slice, but the last's
-    int32_t lag;          // rows between the two readings of a gradient
-    int32_t dynamic;      // a CTA takes its next row when it is free for it (else rows are dealt out)
     int32_t depth_log;    // rows between the scout and the epilogue
     int32_t list_stride;  // entries of a list
     int32_t words_at;     // where in shared memory the words of a cluster are
-    int32_t clusters;
     int32_t smem;
 };
 
@@ -227,6 +234,40 @@ __device__ __forceinline__ void ff_logprob(const TokenParams &P, float z, float 
 
 __device__ __forceinline__ float ff_exp(float h, float l) { return h == -INFINITY ? 0.0f : expf(h) * (1.0f + l); }
 
+// 2^(j / 8) as pairs of floats
+__device__ const float2 kExp8[8] = {
+    {0x1p+0f, 0.0f},
+    {0x1.172b84p+0f, -0x1.c15742p-27f},
+    {0x1.306fe0p+0f, 0x1.4636e2p-25f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f},
+    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f},
+    {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f},
+    {0x1.d5818ep+0f, -0x1.822dbcp-27f},
+};
+
+// e^v of v <= 88 as a pair of floats, to about 2^-40 of itself (0 below e^-86): v = n ln 2 / 8 + x, |x| <= ln 2 / 16, the
+// series of e^x with its first three terms as pairs, and 2^(n / 8) from the table (Tang's method, see sv_common.cuh).
+__device__ __forceinline__ void ff_exp_near(float v, float &h, float &l) {
+    h = l = 0.0f;
+    if (!(v > -86.0f)) return;
+    const float n = rintf(v * 11.5415603f);
+    float ph, pl, xh, xl;
+    ff_mul(n * 0.125f, 0.0f, kLn2Hi, kLn2Lo, ph, pl);
+    ff_add(v, 0.0f, -ph, -pl, xh, xl);
+    const float sq = xh * xh, sl = fmaf(xh, xh, -sq) + 2.0f * xh * xl;
+    const float tail = sq * xh * fmaf(xh, fmaf(xh, fmaf(xh, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f), 1.0f / 6.0f);
+    float eh, el;
+    ff_add(xh, xl, 0.5f * sq, fmaf(0.5f, sl, tail), eh, el);
+    ff_add(1.0f, 0.0f, eh, el, eh, el);
+    const int i = (int)n;
+    const float2 t = kExp8[i & 7];
+    ff_mul(eh, el, t.x, t.y, h, l);
+    const float scale = __uint_as_float((uint32_t)((i >> 3) + 127) << 23);
+    h *= scale;
+    l *= scale;
+}
+
 // ln(1 + b (e^r - 1)), good where r is small; 0 < b < 1
 __device__ __forceinline__ float ln_mixed(float b, float r) { return r > 40.0f ? r + logf(b) : log1pf(b * expm1f(r)); }
 
@@ -308,13 +349,23 @@ __device__ __forceinline__ void cluster_arrive(const uint64_t &bar, uint32_t ran
 }
 
 // The wait of every role: see wait_on. Most are over at the first look.
-__device__ __noinline__ bool wait_longer(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
-    return wait_on(bar, parity, S.abort, P.status, P.wait_ns);
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, Shared &S, const TokenParams &P) {
+    return wait_on(*static_cast<uint64_t *>(__cvta_shared_to_generic(bar)), parity, S.abort, P.status, P.wait_ns);
+}
+
+__device__ __forceinline__ bool wait_at(uint32_t bar, uint32_t parity, Shared &S, const TokenParams &P) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_longer(bar, parity, S, P);
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t &bar, uint32_t parity, Shared &S, const TokenParams &P) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
-    return wait_longer(bar, parity, S, P);
+    return wait_at(smem_u32(&bar), parity, S, P);
+}
+
+__device__ __forceinline__ uint4 load_vec(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
 }
 
 // A CTA's view of the call.
@@ -322,22 +373,35 @@ struct Cta {
     int rank, cluster;
     long long first;         // entry
     int slice0, slice_vecs;  // vectors of the row
-    int chunks;
+    int chunks, whole_chunks;  // of the slice; those of nothing but whole vectors, all of them there
     int lane;
     int depth_log;
+    uint32_t ring, full, ready, empty;  // in shared memory
     unsigned long long *words;  // what the cluster's warps have sent
 
     __device__ __forceinline__ int place(int r) const { return r & ((1 << depth_log) - 1); }
     __device__ __forceinline__ uint32_t parity(int r) const { return (uint32_t)r >> depth_log & 1u; }
 };
 
+// A place in the ring, and the parity of its barriers' phase.
+struct Cursor {
+    uint32_t slot = 0, phase = 0;
+
+    __device__ __forceinline__ void step(const Plan &plan) {
+        if (++slot == (uint32_t)plan.slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // Sums between the CTAs of a cluster: each number goes with the row's number (of live rows, from 1) in one 8-byte word, so
-// that whoever reads it knows that it has come; no barrier, no fence. A warp's words have kDepth places. Row x's replace those
-// of row x - 4, which their reader has read: sums of x are sent behind the stores of x - 2 at the latest, these take sums of
-// x - 2 from every CTA, and a CTA sends those behind its own stores of x - 4.
+// that whoever reads it knows that it has come; no barrier, no fence. A warp's words have two places. Row x's replace those
+// of row x - 2, which their reader has read: sums of x are sent behind the stores of x - 1, these take sums of x - 1 from
+// every CTA, and a CTA sends those behind its own stores of x - 2. (Sums alone: a cluster has one row.)
 template <class Kd>
 __device__ __forceinline__ unsigned long long *words_of(const Cta &cta, int warp, int live) {
-    return cta.words + ((size_t)(live & (kDepth - 1)) * cta.cluster * kConsumers + warp) * Kd::kWords;
+    return cta.words + ((size_t)(live & 1) * cta.cluster * kConsumers + warp) * Kd::kWords;
 }
 
 template <class Kd>
@@ -475,7 +539,7 @@ __device__ __forceinline__ f32x2 far_exponents2(const uint4 &w, int i, float m, 
 // Tokens of a vector before the given one (logit zy, token y): those larger, and equal ones of a lower index. first: the
 // vector's first token.
 template <class Kd>
-__device__ __forceinline__ int count_before(const uint4 &w, float zy, int y, int first) {
+__device__ __noinline__ int count_before(uint4 w, float zy, int y, int first) {
     int n = 0;
 #pragma unroll
     for (int q = 0; q < Kd::kPer / 2; ++q) {
@@ -486,50 +550,88 @@ __device__ __forceinline__ int count_before(const uint4 &w, float zy, int y, int
     return n;
 }
 
-// The sums of a row's slice, chunk after chunk. A gradient's chunks stay for its second reading.
+// The next lower number of the logits' type; of -inf NaN, which nothing is larger than.
+template <int DT>
+__device__ __forceinline__ float next_below(float x) {
+    constexpr int kShift = DT == SV_DT_FP32 ? 0 : 16;
+    const uint32_t b = __float_as_uint(x) >> kShift, sign = 0x80000000u >> kShift;
+    const uint32_t r = (b & ~sign) == 0 ? sign | 1u : b & sign ? b + 1 : b - 1;
+    return __uint_as_float(r << kShift);
+}
+
+// Logits of a vector larger than a bound (bf16: a pair of it). bf16 counts both halves of a word at once: a true half is
+// 0xffff, so that a words' sum is 65536 (lo - hi) - lo of the counts of their low and high halves.
+template <int DT>
+__device__ __forceinline__ uint32_t count_above(const uint4 &w, uint32_t bound) {
+    if (DT == SV_DT_FP32) {
+        const float t = __uint_as_float(bound);
+        return (__uint_as_float(w.x) > t) + (__uint_as_float(w.y) > t) + (__uint_as_float(w.z) > t) + (__uint_as_float(w.w) > t);
+    }
+    auto above = [&](uint32_t x) {
+        return __hgt2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&bound));
+    };
+    return (above(w.x) + above(w.y)) + (above(w.z) + above(w.w));
+}
+
+template <int DT>
+__device__ __forceinline__ int counted(uint32_t sum) {
+    if (DT == SV_DT_FP32) return (int)sum;
+    const uint32_t lo = 0u - sum & 0xffffu;
+    return (int)(lo + ((lo - ((sum + lo) >> 16)) & 0xffffu));
+}
+
+// The sums of a row's slice, chunk after chunk.
 template <class Kd>
-__device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
-                                          const Cta &cta, int d, uint32_t row_parity, int live, int &slot, uint32_t &phase) {
+__device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const Cta &cta, int d,
+                                          uint32_t row_parity, int live, Cursor &cur) {
     constexpr int kVecs = Kd::kVecs, kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane, warp = tid >> 5;
     const int nth = Kd::Top ? (P.k + kConsumers - 1) / kConsumers : 1;
-    const int whole = P.V / kPer, rest = P.V - whole * kPer;
     float m = -INFINITY, R = 0.0f;
     f32x2 s0 = 0ull, s1 = 0ull, t0 = 0ull, t1 = 0ull;
     bool bad = false;
     int before = 0;
+    uint32_t above = 0, bound_before = 0, bound_after = 0;
+    int y_vec = 0;
+    if (Kd::Rank) {  // a token equal to the given one comes before it where its index is lower
+        const float zy = S.row[d].zy, below = next_below<Kd::DT>(zy);
+        y_vec = S.row[d].y / kPer;
+        bound_after = __float_as_uint(zy);
+        bound_before = __float_as_uint(below);
+        if (Kd::DT == SV_DT_BF16) {
+            bound_after |= bound_after >> 16;
+            bound_before |= bound_before >> 16;
+        }
+        if (zy == -INFINITY) bound_before = bound_after;  // and the equal ones one by one, below
+    }
     float least = -INFINITY;  // what a vector has to reach to hold a top token,
     int least_chunk = 0;      // and in later chunks than this one to pass
+    int found = 0;
     const float c = P.c;
     const f32x2 c2 = pack2(c, c);
+    const uint32_t mine = cta.ring + tid * 16;
     for (int i = 0; i < cta.chunks; ++i) {
-        if (!wait_bar(S.full[slot], phase, S, P)) return false;
-        if (Kd::List && !wait_bar(S.ready[slot], phase, S, P)) return false;
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * Kd::kChunkBytes);
-        const int v0 = i * Kd::kChunkVecs;  // of the slice
-        const int n = cta.slice_vecs - v0;
+        if (!wait_at(cta.full + 8 * cur.slot, cur.phase, S, P)) return false;
+        if (Kd::List && !wait_at(cta.ready + 8 * cur.slot, cur.phase, S, P)) return false;
+        const uint32_t at = mine + cur.slot * Kd::kChunkBytes;
         uint4 w[kVecs];
-        if (n >= Kd::kChunkVecs && cta.slice0 + v0 + Kd::kChunkVecs <= whole) {
+        if (i < cta.whole_chunks) {
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) w[j] = chunk[tid + j * kTeam];
+            for (int j = 0; j < kVecs; ++j) w[j] = load_vec(at + j * kTeam * 16);
         } else {
+            const int whole = P.V / kPer, rest = P.V - whole * kPer;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int v = tid + j * kTeam;
+                const int v = i * Kd::kChunkVecs + tid + j * kTeam;  // of the slice
                 w[j] = make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
-                if (v >= n) continue;
-                if (!Kd::List && cta.slice0 + v0 + v == whole) w[j] = ragged_end<Kd>(S.row[d].z, whole, rest);
-                else w[j] = chunk[v];
+                if (v >= cta.slice_vecs) continue;
+                if (!Kd::List && cta.slice0 + v == whole) w[j] = ragged_end<Kd>(S.row[d].z, whole, rest);
+                else w[j] = load_vec(at + j * kTeam * 16);
             }
         }
-        if (!Kd::Grad) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
-        }
-        if (++slot == plan.slots) {
-            slot = 0;
-            phase ^= 1u;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
+        cur.step(plan);
         uint32_t pm[kVecs], all = 0;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
@@ -537,24 +639,25 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             all = j == 0 ? pm[0] : packed_max<Kd::DT>(all, pm[j]);
         }
         float cm = from_packed_max<Kd::DT>(all);
-        if (!(cm < INFINITY)) {
-            bad = true;
-            cm = -INFINITY;
-        }
-        if (cm > m) {
-            const float next = cm * c;
-            if (m != -INFINITY) {
-                const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
-                const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
-                if (Kd::Ent) {
-                    t0 = mul2(f2, fma2(x2, s0, t0));
-                    t1 = mul2(f2, fma2(x2, s1, t1));
+        if (!(cm <= m)) {
+            if (!(cm < INFINITY)) {
+                bad = true;
+                cm = -INFINITY;
+            } else {
+                const float next = cm * c;
+                if (m != -INFINITY) {
+                    const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
+                    const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
+                    if (Kd::Ent) {
+                        t0 = mul2(f2, fma2(x2, s0, t0));
+                        t1 = mul2(f2, fma2(x2, s1, t1));
+                    }
+                    s0 = mul2(f2, s0);
+                    s1 = mul2(f2, s1);
                 }
-                s0 = mul2(f2, s0);
-                s1 = mul2(f2, s1);
+                m = cm;
+                R = next;
             }
-            m = cm;
-            R = next;
         }
         if (plain(m)) {
             const f32x2 nR = pack2(-R, -R);
@@ -576,7 +679,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         } else if (m != -INFINITY) {
 #pragma unroll 1
             for (int j = 0; j < kVecs; ++j) {
-                const uint4 v = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2 % kVecs] : w[3 % kVecs];
+                const uint4 v = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
 #pragma unroll
                 for (int q = 0; q < kPer / 2; ++q) {
                     const f32x2 x2 = far_exponents2<Kd>(v, q, m, c);
@@ -588,22 +691,29 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             }
         }
         if (Kd::Rank) {
-            const float zy = S.row[d].zy;
-            const int y = S.row[d].y;
+            const int v0 = cta.slice0 + i * Kd::kChunkVecs + tid;
+            const bool inf = bound_before == bound_after;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const int v = v0 + tid + j * kTeam;
-                // the indexes of what fills a short chunk belong to the next slice
-                before += count_before<Kd>(w[j], zy, y, v < cta.slice_vecs ? (cta.slice0 + v) * kPer : P.V);
+                const int v = v0 + j * kTeam;
+                if (v == y_vec || (inf && v < y_vec)) {
+                    if (v < cta.slice0 + cta.slice_vecs) before += count_before<Kd>(w[j], S.row[d].zy, S.row[d].y, v * kPer);
+                } else {
+                    above += count_above<Kd::DT>(w[j], v < y_vec ? bound_before : bound_after);
+                }
+            }
+            if ((i & 1023) == 1023) {  // what is packed into half a word does not overflow
+                before += counted<Kd::DT>(above);
+                above = 0;
             }
         }
         if (Kd::Top) {
             // Each warp bounds the k-th largest logit by the nth largest of its lanes' maxima: 8 warps have 8 nth >= k
             // tokens that large. The bound of the first chunk is everybody's; it then rises at chunks 1, 3, 7, ...
             if ((i & (i + 1)) == 0 || i + 1 == cta.chunks) {
-                const uint32_t mine = warp_nth(order_bits(m), nth, lane);
+                const uint32_t nth_max = warp_nth(order_bits(m), nth, lane);
                 if (lane == 0)
-                    *(volatile unsigned long long *)&top->bound[d][warp] = ((unsigned long long)mine << 32) | (uint32_t)i;
+                    *(volatile unsigned long long *)&top->bound[d][warp] = ((unsigned long long)nth_max << 32) | (uint32_t)i;
                 if (i == 0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
@@ -617,20 +727,28 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             }
             // Tokens that equal the bound come after the ones that made it, once these lie in earlier chunks.
             const bool strict = i > least_chunk;
-            if (cm >= least && (!strict || cm > least)) {
+            if (__any_sync(0xffffffffu, strict ? cm > least : cm >= least)) {
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
+                    const int v = i * Kd::kChunkVecs + tid + j * kTeam;
                     const float x = from_packed_max<Kd::DT>(pm[j]);
-                    if (tid + j * kTeam < n && (strict ? x > least : x >= least)) {
-                        const unsigned at = atomicAdd(&top->count[d], 1u);
-                        if (at < kCandidates) top->at[d][at] = cta.slice0 + v0 + tid + j * kTeam;
+                    const bool pass = v < cta.slice_vecs && (strict ? x > least : x >= least);
+                    const uint32_t who = __ballot_sync(0xffffffffu, pass);
+                    if (pass) {
+                        const int to = found + __popc(who & ((1u << lane) - 1u));
+                        if (to < kCandidates) top->at[d][warp][to] = cta.slice0 + v;
                     }
+                    found += __popc(who);
                 }
             }
         }
     }
-    if (Kd::Top && cta.chunks == 0 && lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
+    if (Kd::Top) {
+        if (lane == 0) top->count[d][warp] = found;
+        if (cta.chunks == 0 && lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
+    }
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
+    if (Kd::Rank) before += counted<Kd::DT>(above);
     Part p{m, (a.x + a.y) + (b.x + b.y), (e.x + e.y) + (f.x + f.y), bad ? -1 : before};
     if (plain(m)) {  // what R was off by
         const float r = fmaf(m, c, -R), g = ex2_approx(-r);
@@ -638,26 +756,21 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         p.s *= g;
     }
     p = warp_fold<Kd>(p, c);
-    if (cta.cluster == 1) {
-        if (lane == 0) {
-            S.part[d][warp] = p;
-            mbar_arrive(smem_u32(&S.summed[d]));
-        }
-    } else {
-        send<Kd>(cta, cta.rank * kConsumers + warp, live, p);
-    }
+    if (cta.cluster > 1) send<Kd>(cta, cta.rank * kConsumers + warp, live, p);
+    else if (lane == 0) S.part[d][warp] = p;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&S.summed[d]));
     return true;
 }
 
-// The gradient of a row's slice: 2^x (a + b x) for x = (z - m) c.
+// The gradient of a row's slice, 2^x (a + b x) for x = (z - m) c, the last chunk first.
 template <class Kd>
-__device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &plan, Shared &S, const uint8_t *ring, const Cta &cta,
-                                            int d, uint32_t row_parity, int &slot) {
-    constexpr int kPer = Kd::kPer;
+__device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta, int d,
+                                            uint32_t row_parity, Cursor &cur) {
+    constexpr int kPer = Kd::kPer, kVecs = Kd::kVecs;
     const int tid = threadIdx.x, lane = cta.lane;
-    const int whole = P.V / kPer, rest = P.V - whole * kPer;
     const int state = S.row[d].state;
-    char *out = P.grad + S.row[d].entry * P.grad_stride_bytes + (int64_t)cta.slice0 * 16;
+    uint4 *out = reinterpret_cast<uint4 *>(P.grad + S.row[d].entry * P.grad_stride_bytes) + cta.slice0 + tid;
     float m = 0.0f, fa = state == kBad ? NAN : 0.0f, fb = 0.0f;
     if (state == kLive) {
         if (!wait_bar(S.known[d], row_parity, S, P)) return false;
@@ -674,18 +787,9 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
         fb *= g;
     }
     const f32x2 nR = pack2(-R, -R), c2 = pack2(c, c), a2 = pack2(fa, fa), b2 = pack2(fb, fb);
-    auto gradients = [&](const uint4 &w, f32x2 (&g)[kPer / 2]) {
-        if (state != kLive) {
-#pragma unroll
-            for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
-            return;
-        }
-#pragma unroll
-        for (int q = 0; q < kPer / 2; ++q) {
-            const f32x2 x2 = near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c);
-            const float2 x = unpack2(x2);
-            g[q] = mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
-        }
+    auto weigh = [&](f32x2 x2) {
+        const float2 x = unpack2(x2);
+        return mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
     };
     auto packed = [&](const f32x2 (&g)[kPer / 2]) {
         const float2 x = unpack2(g[0]), y = unpack2(g[1]);
@@ -694,33 +798,45 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
         const float2 z = unpack2(g[2 % (kPer / 2)]), u = unpack2(g[3 % (kPer / 2)]);
         return make_uint4(to_bf16x2(x.x, x.y), to_bf16x2(y.x, y.y), to_bf16x2(z.x, z.y), to_bf16x2(u.x, u.y));
     };
-    for (int i = 0; i < cta.chunks; ++i) {
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(ring + (size_t)slot * Kd::kChunkBytes);
-        const int v0 = i * Kd::kChunkVecs;
-        uint4 *to = reinterpret_cast<uint4 *>(out) + v0 + tid;
-        if (state == kLive && near && v0 + Kd::kChunkVecs <= cta.slice_vecs && cta.slice0 + v0 + Kd::kChunkVecs <= whole) {
-            uint4 w[Kd::kVecs];
+    const uint32_t mine = cta.ring + tid * 16;
+    for (int i = cta.chunks - 1; i >= 0; --i) {
+        uint32_t at = mine;
+        if (state == kLive) {
+            if (!wait_at(cta.full + 8 * cur.slot, cur.phase, S, P)) return false;
+            if (Kd::List && !wait_at(cta.ready + 8 * cur.slot, cur.phase, S, P)) return false;
+            at += cur.slot * Kd::kChunkBytes;
+        }
+        uint4 *to = out + i * Kd::kChunkVecs;
+        if (state == kLive && near && i < cta.whole_chunks) {
+            uint4 w[kVecs];
 #pragma unroll
-            for (int j = 0; j < Kd::kVecs; ++j) w[j] = chunk[tid + j * kTeam];
+            for (int j = 0; j < kVecs; ++j) w[j] = load_vec(at + j * kTeam * 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
 #pragma unroll
-            for (int j = 0; j < Kd::kVecs; ++j) {
+            for (int j = 0; j < kVecs; ++j) {
                 f32x2 g[kPer / 2];
 #pragma unroll
-                for (int q = 0; q < kPer / 2; ++q) {
-                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q), c2, nR);
-                    const float2 x = unpack2(x2);
-                    g[q] = mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
-                }
+                for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(fma2(logits2<Kd>(w[j], q), c2, nR));
                 to[j * kTeam] = packed(g);
             }
         } else {
+            const int whole = P.V / kPer, rest = P.V - whole * kPer;
 #pragma unroll 1
-            for (int j = 0; j < Kd::kVecs; ++j) {
-                const int v = v0 + tid + j * kTeam;  // of the slice
+            for (int j = 0; j < kVecs; ++j) {
+                const int v = i * Kd::kChunkVecs + tid + j * kTeam;  // of the slice
                 if (v >= cta.slice_vecs) break;
                 const bool end = cta.slice0 + v >= whole;
                 f32x2 g[kPer / 2];
-                gradients(!Kd::List && end && state == kLive ? ragged_end<Kd>(S.row[d].z, whole, rest) : chunk[tid + j * kTeam], g);
+                if (state == kLive) {
+                    const uint4 w = end ? ragged_end<Kd>(S.row[d].z, whole, rest) : load_vec(at + j * kTeam * 16);
+#pragma unroll
+                    for (int q = 0; q < kPer / 2; ++q)
+                        g[q] = weigh(near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
+                }
                 if (!end) {
                     to[j * kTeam] = packed(g);
                 } else {
@@ -731,12 +847,12 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
                     }
                 }
             }
+            if (state == kLive) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
+            }
         }
-        if (state == kLive) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.empty[slot]));
-            if (++slot == plan.slots) slot = 0;
-        }
+        if (state == kLive) cur.step(plan);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&S.stored[d]));
@@ -744,63 +860,36 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
 }
 
 template <class Kd>
-__device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const uint8_t *ring,
-                                        const Cta &cta) {
-    int slot = 0, gslot = 0, r = 0, live = 0;
-    uint32_t phase = 0;
-    auto store = [&](int g) {
-        const int d = cta.place(g);
-        if (!store_slice<Kd>(P, plan, S, ring, cta, d, cta.parity(g), gslot)) return false;
-        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
-        return true;
-    };
-    for (;; ++r) {
+__device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const Cta &cta) {
+    Cursor cur;
+    int live = 0;
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
         if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
-        if (S.row[d].state == kEnd) break;
-        if (S.row[d].state == kLive) {
-            if (!sum_slice<Kd>(P, plan, S, top, ring, cta, d, cta.parity(r), live++, slot, phase)) return;
+        const int state = S.row[d].state;
+        if (state == kEnd) return;
+        if (state == kLive) {
+            if (!sum_slice<Kd>(P, plan, S, top, cta, d, cta.parity(r), live++, cur)) return;
         } else if (cta.lane == 0) {
             if (Kd::Top) mbar_arrive(smem_u32(&S.bounded[d]));
-            if (cta.cluster == 1) mbar_arrive(smem_u32(&S.summed[d]));
+            mbar_arrive(smem_u32(&S.summed[d]));
         }
-        if (!Kd::Grad) {
-            __syncwarp();
-            if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
-        } else if (r >= plan.lag && !store(r - plan.lag)) {
-            return;
-        }
+        if (Kd::Grad && !store_slice<Kd>(P, plan, S, cta, d, cta.parity(r), cur)) return;
+        __syncwarp();
+        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
     }
-    if (Kd::Grad && plan.lag && r > 0) store(r - 1);
 }
 
 // ---------------------------------------------------------------------------
 // scout
 
-// The rows of a CTA (or cluster), one after another. Dynamic: the grid has a CTA for every row, and a CTA that runs takes
-// over, one at a time, the rows of those that have not begun (cluster launch control).
+// The rows of a cluster, one after another. Dynamic: the grid has a cluster for every row, and one that runs takes over, one
+// at a time, the rows of those that have not begun (cluster launch control). The first CTA asks, the answer goes to all of
+// them, and the next is asked for when they all have read it.
 struct Entries {
     long long e;
-    uint32_t phase;
-    bool asked;
+    int answers;
 
-    __device__ __forceinline__ void ask(Shared &S, int lane) {
-        if (lane == 0) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive_expect_tx(smem_u32(&S.granted), 16);
-            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                             smem_u32(&S.grant)),
-                         "r"(smem_u32(&S.granted))
-                         : "memory");
-        }
-        asked = true;
-    }
-    __device__ __forceinline__ void begin(const Plan &plan, Shared &S, const Cta &cta) {
-        e = cta.first;
-        phase = 0;
-        asked = false;
-        if (plan.dynamic) ask(S, cta.lane);
-    }
     // e < 0 after the last one; false: gave up
     __device__ __forceinline__ bool next(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta) {
         if (!plan.dynamic) {
@@ -808,9 +897,27 @@ struct Entries {
             if (e >= P.entries) e = -1;
             return true;
         }
-        if (!wait_bar(S.granted, phase, S, P)) return false;
-        phase ^= 1u;
-        asked = false;
+        if (cta.rank == 0) {
+            if (cta.cluster > 1 && answers > 0 && !wait_bar(S.acked, (uint32_t)(answers - 1) & 1u, S, P)) return false;
+            if (cta.lane == 0) {
+                S.asked = answers + 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (cta.cluster == 1)
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                                     smem_u32(&S.grant)),
+                                 "r"(smem_u32(&S.granted))
+                                 : "memory");
+                else
+                    asm volatile(
+                        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+                        "[%0], [%1];" ::"r"(smem_u32(&S.grant)),
+                        "r"(smem_u32(&S.granted))
+                        : "memory");
+            }
+        }
+        if (cta.lane == 0) mbar_arrive_expect_tx(smem_u32(&S.granted), 16);
+        if (!wait_bar(S.granted, (uint32_t)answers & 1u, S, P)) return false;
+        ++answers;
         uint32_t more, x;
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
@@ -822,14 +929,14 @@ struct Entries {
             : "=r"(more), "=r"(x)
             : "r"(smem_u32(&S.grant))
             : "memory");
+        if (cta.cluster > 1) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next answer comes after this one was read
+            __syncwarp();
+            if (cta.lane == 0) cluster_arrive(S.acked, 0);
+        }
         __syncwarp();
-        e = more ? (long long)x : -1;
-        if (more) ask(S, cta.lane);
+        e = more ? (long long)(x / (uint32_t)cta.cluster) : -1;
         return true;
-    }
-    // No answer outlives its CTA, also where the scout gave up.
-    __device__ __forceinline__ void end(Shared &S) {
-        if (asked) mbar_wait_bounded(smem_u32(&S.granted), phase);
     }
 };
 
@@ -952,18 +1059,20 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
             }
             p_sum = warp_sum(p_sum);
         } else {
-            // One less a sum close to it: in 64 bits, or little would be left of it. (Off everybody's way: the scout is rows
-            // ahead.)
-            double sum = 0.0;
+            // One less a sum close to it: in pairs of floats, or little would be left of it.
+            float sh = 0.0f, sl = 0.0f;
             for (int j = lane; j < P.K; j += 32) {
-                const double x = llp[j] > -INFINITY ? exp((double)llp[j]) : 0.0;
-                lpr[j] = (float)x;
-                sum += x;
+                float h, l;
+                ff_exp_near(llp[j], h, l);
+                lpr[j] = h;
+                ff_add(sh, sl, h, l, sh, sl);
             }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(all, sum, off);
-            p_rest = (float)fmax(1.0 - sum, 0.0);
-            p_sum = (float)sum;
+            for (int off = 16; off > 0; off >>= 1)
+                ff_add(sh, sl, __shfl_xor_sync(all, sh, off), __shfl_xor_sync(all, sl, off), sh, sl);
+            p_sum = sh;
+            ff_add(1.0f, 0.0f, -sh, -sl, sh, sl);
+            p_rest = fmaxf(sh + sl, 0.0f);
         }
         if (zmax > -INFINITY)
             for (int j = lane; j < P.K; j += 32) zsum += ex2_approx(fmaxf(lz[j] - zmax, kFar) * P.c);
@@ -983,111 +1092,109 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
 }
 
 template <class Kd>
-__device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *top, const Lists &list,
-                                      const Cta &cta) {
-    Entries at;
+__device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, const Lists &list, const Cta &cta,
+                                      Entries &at) {
     Asked a;
-    at.begin(plan, S, cta);
-    fetch<Kd::List>(P, at.e, cta.lane, a);
     for (int r = 0;; ++r) {
         const int d = cta.place(r);
-        if (!wait_bar(S.row_free[d], cta.parity(r) ^ 1u, S, P)) break;
+        if (at.e >= 0) fetch<Kd::List>(P, at.e, cta.lane, a);
+        if (!wait_bar(S.row_free[d], cta.parity(r) ^ 1u, S, P)) return;
         if (at.e < 0) {
             if (cta.lane == 0) S.row[d].state = kEnd;
         } else if (Kd::List) {
             scout_list<Kd::DT>(P, S.row[d], list, d, at.e, cta.lane, a);
         } else if (cta.lane == 0) {
             scout_token<Kd::DT>(P, S.row[d], at.e, a);
-            if (Kd::Top) top->count[d] = 0;
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_full[d]));
-        if (at.e < 0 || !at.next(P, plan, S, cta)) break;
-        if (at.e >= 0) fetch<Kd::List>(P, at.e, cta.lane, a);
+        if (at.e < 0) return;
+        // The next row is asked for when this one's copies have all been issued: not sooner than it is needed.
+        if (!plan.eager && !wait_bar(S.sent[d], cta.parity(r), S, P)) return;
+        if (!at.next(P, plan, S, cta)) return;
     }
-    at.end(S);
 }
 
 // ---------------------------------------------------------------------------
 // producer and patcher
 
 template <class Kd>
-__device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, Shared &S, uint8_t *ring, const Cta &cta) {
+__device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta) {
     const int64_t row_bytes = (int64_t)P.V * Kd::kSize & ~15ll;
-    int slot = 0, r = 0;
-    uint32_t phase = 0;
+    Cursor cur;
     long long issued = 0;
     bool ok = true;
-    for (; ok; ++r) {
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
         ok = wait_bar(S.row_full[d], cta.parity(r), S, P);
         if (!ok || S.row[d].state == kEnd) break;
         const char *z = S.row[d].z;
-        const bool live = S.row[d].state == kLive;
-        __syncwarp();
-        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
-        if (!live) continue;
-        for (int i = 0; i < cta.chunks && ok; ++i) {
-            ok = wait_bar(S.empty[slot], phase ^ 1u, S, P);
+        const int n = S.row[d].state != kLive ? 0 : Kd::Grad ? 2 * cta.chunks : cta.chunks;
+        for (int j = 0; j < n; ++j) {
+            ok = wait_at(cta.empty + 8 * cur.slot, cur.phase ^ 1u, S, P);
             if (!ok) break;
             if (cta.lane == 0) {
+                const int i = j < cta.chunks ? j : 2 * cta.chunks - 1 - j;  // backwards the second time
                 const int64_t off = ((int64_t)cta.slice0 + (int64_t)i * Kd::kChunkVecs) * 16;
-                const int n = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs) * 16;
-                const int bytes = (int)min((int64_t)n, row_bytes - off);
-                const uint32_t bar = smem_u32(&S.full[slot]);
+                const int most = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs) * 16;
+                const int bytes = (int)min((int64_t)most, row_bytes - off);
+                const uint32_t bar = cta.full + 8 * cur.slot;
                 if (bytes > 0) {
                     mbar_arrive_expect_tx(bar, (uint32_t)bytes);
-                    bulk_load(smem_u32(ring + (size_t)slot * Kd::kChunkBytes), z + off, (uint32_t)bytes, bar);
+                    bulk_load(cta.ring + cur.slot * Kd::kChunkBytes, z + off, (uint32_t)bytes, bar);
                 } else {
                     mbar_arrive(bar);
                 }
             }
             ++issued;
-            if (++slot == plan.slots) {
-                slot = 0;
-                phase ^= 1u;
-            }
+            cur.step(plan);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (cta.lane == 0) {
+            mbar_arrive(smem_u32(&S.sent[d]));
+            mbar_arrive(smem_u32(&S.row_free[d]));
         }
     }
     // no copy outlives its CTA, also where those who needed it gave up
     for (long long u = max(0ll, issued - plan.slots); u < issued; ++u)
-        mbar_wait_bounded(smem_u32(&S.full[u % plan.slots]), u / plan.slots & 1);
+        mbar_wait_bounded(cta.full + 8 * (uint32_t)(u % plan.slots), u / plan.slots & 1);
 }
 
 template <class Kd>
 __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Shared &S, const Lists &L, uint8_t *ring,
                                       const Cta &cta) {
     const int whole = P.V / Kd::kPer, rest = P.V - whole * Kd::kPer;
-    int slot = 0, r = 0;
-    uint32_t phase = 0;
-    for (;; ++r) {
+    Cursor cur;
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
         if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
         if (S.row[d].state == kEnd) return;
-        for (int i = 0; i < (S.row[d].state == kLive ? cta.chunks : 0); ++i) {
-            if (!wait_bar(S.full[slot], phase, S, P)) return;
-            uint8_t *chunk = ring + (size_t)slot * Kd::kChunkBytes;
-            const int v0 = cta.slice0 + i * Kd::kChunkVecs;
-            const int n = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs);
-            if (rest && v0 <= whole && whole < v0 + n) {  // the ragged end of the row, which no copy brings
-                if (cta.lane < Kd::kPer) {
-                    const float x = cta.lane < rest ? plain_logit<Kd::DT>(S.row[d].z, (int64_t)whole * Kd::kPer + cta.lane) : -INFINITY;
-                    store_logit<Kd::DT>(reinterpret_cast<char *>(chunk + (whole - v0) * 16), cta.lane, x);
+        const int n = S.row[d].state != kLive ? 0 : Kd::Grad ? 2 * cta.chunks : cta.chunks;
+        for (int i = 0; i < n; ++i) {
+            if (!wait_at(cta.full + 8 * cur.slot, cur.phase, S, P)) return;
+            if (i < cta.chunks) {  // the gradient's second reading takes the chunk as it is
+                uint8_t *chunk = ring + (size_t)cur.slot * Kd::kChunkBytes;
+                const int v0 = cta.slice0 + i * Kd::kChunkVecs;
+                const int vecs = min(Kd::kChunkVecs, cta.slice_vecs - i * Kd::kChunkVecs);
+                if (rest && v0 <= whole && whole < v0 + vecs) {  // the ragged end of the row, which no copy brings
+                    if (cta.lane < Kd::kPer) {
+                        const float x =
+                            cta.lane < rest ? plain_logit<Kd::DT>(S.row[d].z, (int64_t)whole * Kd::kPer + cta.lane) : -INFINITY;
+                        store_logit<Kd::DT>(reinterpret_cast<char *>(chunk + (whole - v0) * 16), cta.lane, x);
+                    }
+                    __syncwarp();
                 }
+                for (int j = cta.lane; j < P.K; j += 32) {
+                    const int at = L.ids[d * L.stride + j] - v0 * Kd::kPer;
+                    if (at >= 0 && at < vecs * Kd::kPer) store_logit<Kd::DT>(reinterpret_cast<char *>(chunk), at, -INFINITY);
+                }
+                // the next copy into this slot comes after these stores
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
-            for (int j = cta.lane; j < P.K; j += 32) {
-                const int at = L.ids[d * L.stride + j] - v0 * Kd::kPer;
-                if (at >= 0 && at < n * Kd::kPer) store_logit<Kd::DT>(reinterpret_cast<char *>(chunk), at, -INFINITY);
-            }
-            // the next copy into this slot comes after these stores
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (cta.lane == 0) mbar_arrive(smem_u32(&S.ready[slot]));
-            if (++slot == plan.slots) {
-                slot = 0;
-                phase ^= 1u;
-            }
+            if (cta.lane == 0) mbar_arrive(cta.ready + 8 * cur.slot);
+            cur.step(plan);
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
@@ -1097,20 +1204,39 @@ __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Sh
 // ---------------------------------------------------------------------------
 // epilogue
 
-// Calls f with the keys of the n candidates' tokens, or (n < 0) of the whole slice's, read once more from memory (L2).
+// The vectors that may hold a row's top tokens: the warps' lists one behind another, or (n < 0) the whole slice.
+struct Candidates {
+    const int32_t *at;  // [kConsumers][kCandidates]
+    int n;
+    int ends[kConsumers];
+
+    __device__ __forceinline__ int vector(int i) const {
+        int w = 0, from = 0;
+#pragma unroll
+        for (int q = 0; q + 1 < kConsumers; ++q)
+            if (i >= ends[q]) {
+                w = q + 1;
+                from = ends[q];
+            }
+        return at[w * kCandidates + i - from];
+    }
+};
+
+// Calls f with the keys of the candidates' tokens, read once more from memory (L2), one for every lane at a time; 0 is none.
 template <int DT, class F>
-__device__ __forceinline__ void each_key(const TokenParams &P, const char *row, const int32_t *at, int n, const Cta &cta, F &&f) {
+__device__ __forceinline__ void each_key(const TokenParams &P, const char *row, const Candidates &c, const Cta &cta, F &&f) {
     constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2);
-    const int whole = P.V / kPer, first = n < 0 ? cta.slice0 : 0;
-    const int end = n < 0 ? min(whole, cta.slice0 + cta.slice_vecs) : n;
+    const int whole = P.V / kPer, first = c.n < 0 ? cta.slice0 : 0;
+    const int end = c.n < 0 ? min(whole, cta.slice0 + cta.slice_vecs) : c.n;
     const uint4 *z = reinterpret_cast<const uint4 *>(row);
-    bool ragged = n < 0 && cta.slice0 + cta.slice_vecs > whole;
-    for (int i = first + cta.lane; i < end; i += 128) {
+    bool ragged = c.n < 0 && cta.slice0 + cta.slice_vecs > whole;
+    for (int i = first; i < end; i += 128) {
         uint4 w[4];
         int v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            v[q] = i + 32 * q < end ? (n < 0 ? i + 32 * q : at[i + 32 * q]) : -1;
+            const int j = i + 32 * q + cta.lane;
+            v[q] = j < end ? (c.n < 0 ? j : c.vector(j)) : -1;
             if (v[q] == whole) {
                 ragged = true;
                 v[q] = -1;
@@ -1119,16 +1245,16 @@ __device__ __forceinline__ void each_key(const TokenParams &P, const char *row, 
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (v[q] < 0) continue;
             float x[kPer];
             vec_floats<DT>(w[q], x);
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) f(order_key(x[u], v[q] * kPer + u));
+            for (int u = 0; u < kPer; ++u) f(v[q] < 0 ? 0ull : order_key(x[u], v[q] * kPer + u));
         }
     }
-    ragged = __any_sync(0xffffffffu, ragged);
-    const int t = whole * kPer + cta.lane;  // the row's ragged end
-    if (ragged && t < P.V) f(order_key(load_logit<DT>(row, t), t));
+    if (__any_sync(0xffffffffu, ragged)) {  // the row's ragged end
+        const int t = whole * kPer + cta.lane;
+        f(t < P.V ? order_key(load_logit<DT>(row, t), t) : 0ull);
+    }
 }
 
 // The k best keys of the CTA's slice, in order, in T.best (0 where there are none).
@@ -1136,48 +1262,58 @@ template <int DT>
 __device__ __noinline__ void select_top(const TokenParams &P, const char *row, SharedTop &T, int d, const Cta &cta) {
     constexpr uint32_t all = 0xffffffffu;
     const int lane = cta.lane, k = P.k;
-    const unsigned met = *(volatile unsigned *)&T.count[d];
-    int n = met <= kCandidates ? (int)met : -1;
+    Candidates c{&T.at[d][0][0], 0, {}};
+    bool over = false;
+#pragma unroll
+    for (int q = 0; q < kConsumers; ++q) {
+        const int n = T.count[d][q];
+        over = over || n > kCandidates;
+        c.n += n;
+        c.ends[q] = c.n;
+    }
     // the last bound: k tokens are at least so large, or there are not that many
     const unsigned long long b = lane < kConsumers ? T.bound[d][lane] : ~0ull;
     unsigned long long least = (unsigned long long)__reduce_min_sync(all, (uint32_t)(b >> 32)) << 32;
     if (cta.chunks == 0) {
-        least = 0;
-        n = 0;
+        c.n = 0;
+        over = false;
     }
+    if (over) c.n = -1;
     for (int i = lane; i < k; i += 32) T.best[i] = 0;
     auto collect = [&]() {
-        if (lane == 0) T.found = 0;
-        __syncwarp();
-        each_key<DT>(P, row, T.at[d], n, cta, [&](unsigned long long x) {
-            if (x >= least) {
-                const unsigned at = atomicAdd(&T.found, 1u);
-                if (at < kKeys) T.keys[at] = x;
-            }
+        int n = 0;
+        each_key<DT>(P, row, c, cta, [&](unsigned long long x) {
+            const bool in = x != 0 && x >= least;
+            const uint32_t who = __ballot_sync(all, in);
+            if (!who) return;
+            const int to = n + __popc(who & ((1u << lane) - 1u));
+            if (in && to < kKeys) T.keys[to] = x;
+            n += __popc(who);
         });
         __syncwarp();
-        return *(volatile unsigned *)&T.found;
+        return n;
     };
-    unsigned m = collect();
+    int m = collect();
     if (m > kKeys) {
         // many equal logits: the largest key that k tokens reach, a bit at a time
         unsigned long long key = 0;
         for (int bit = 63; bit >= 0; --bit) {
             const unsigned long long next = key | 1ull << bit;
-            int c = 0;
-            each_key<DT>(P, row, T.at[d], n, cta, [&](unsigned long long x) { c += x >= next ? 1 : 0; });
-            if ((int)__reduce_add_sync(all, (unsigned)c) >= k) key = next;
+            int n = 0;
+            each_key<DT>(P, row, c, cta, [&](unsigned long long x) { n += x >= next ? 1 : 0; });
+            if ((int)__reduce_add_sync(all, (unsigned)n) >= k) key = next;
         }
         least = max(least, key);
-        m = min(collect(), (unsigned)kKeys);
+        m = min(collect(), kKeys);
     }
     // a key's place is the number of larger ones
-    for (unsigned i0 = 0; i0 < m; i0 += 128) {
+    for (int i0 = 0; i0 < m; i0 += 128) {
         unsigned long long x[4];
         int place[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[q] = i0 + 32 * q + lane < m ? T.keys[i0 + 32 * q + lane] : 0;
-        for (unsigned i = 0; i < m; ++i) {
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
             const unsigned long long o = T.keys[i];
 #pragma unroll
             for (int q = 0; q < 4; ++q) place[q] += o > x[q] ? 1 : 0;
@@ -1407,44 +1543,33 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
 }
 
 template <class Kd>
-__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Lists &L, const Cta &cta) {
-    int r = 0, live = 0;
-    auto fix = [&](int g) {
-        const int d = cta.place(g);
-        if (!wait_bar(S.stored[d], cta.parity(g), S, P)) return false;
-        if (Kd::List) fix_list<Kd>(P, S, L, cta, d);
-        else fix_token<Kd>(P, S, cta, d);
-        __syncwarp();
-        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
-        return true;
-    };
-    for (;; ++r) {
+__device__ __forceinline__ void finish(const TokenParams &P, Shared &S, SharedTop *T, const Lists &L, const Cta &cta) {
+    int live = 0;
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
         const uint32_t parity = cta.parity(r);
         if (!wait_bar(S.row_full[d], parity, S, P)) return;
         const int state = S.row[d].state;
-        if (state == kEnd) break;
+        if (state == kEnd) return;
         Part p{-INFINITY, 0.0f, 0.0f, 0};
-        if (cta.cluster == 1) {
-            if (!wait_bar(S.summed[d], parity, S, P)) return;
-            if (state == kLive) {
-                if (cta.lane < kConsumers) p = S.part[d][cta.lane];
-                p = warp_fold<Kd>(p, P.c);
-            }
-        } else if (state == kLive && !receive<Kd>(P, S, cta, live++, p)) {
-            return;
+        if (!wait_bar(S.summed[d], parity, S, P)) return;
+        if (state == kLive && cta.cluster > 1) {
+            if (!receive<Kd>(P, S, cta, live++, p)) return;
+        } else if (state == kLive) {
+            if (cta.lane < kConsumers) p = S.part[d][cta.lane];
+            p = warp_fold<Kd>(p, P.c);
         }
         if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
         else if (!finish_token<Kd>(P, S, T, cta, d, p)) return;
         __syncwarp();
-        // A gradient's next row is not kept waiting for the stores of this one.
         if (Kd::Grad) {
-            if (r >= plan.lag && !fix(r - plan.lag)) return;
-        } else if (cta.lane == 0) {
-            mbar_arrive(smem_u32(&S.row_free[d]));
+            if (!wait_bar(S.stored[d], parity, S, P)) return;
+            if (Kd::List) fix_list<Kd>(P, S, L, cta, d);
+            else fix_token<Kd>(P, S, cta, d);
+            __syncwarp();
         }
+        if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
     }
-    if (Kd::Grad && plan.lag && r > 0) fix(r - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -1452,10 +1577,8 @@ __device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, S
 template <class Kd>
 __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constant__ TokenParams P, const __grid_constant__ Plan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *ring = smem;
     Shared &S = *reinterpret_cast<Shared *>(smem + (size_t)plan.slots * Kd::kChunkBytes);
-    constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
-    void *more = reinterpret_cast<uint8_t *>(&S) + kFixed;
+    void *more = reinterpret_cast<uint8_t *>(&S) + (sizeof(Shared) + 15) / 16 * 16;
     SharedTop *top = Kd::Top ? static_cast<SharedTop *>(more) : nullptr;
     Lists list{};
     if (Kd::List) {
@@ -1472,12 +1595,17 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     cta.cluster = plan.cluster;
     cta.rank = plan.cluster > 1 ? (int)cluster_rank() : 0;
     cta.first = blockIdx.x / plan.cluster;
-    const int vecs = (int)(((int64_t)P.V * Kd::kSize + 15) / 16);
+    const int vecs = (int)(((int64_t)P.V * Kd::kSize + 15) / 16), whole = P.V / Kd::kPer;
     cta.slice0 = min(vecs, cta.rank * plan.slice_vecs);
     cta.slice_vecs = min(vecs - cta.slice0, plan.slice_vecs);
     cta.chunks = (cta.slice_vecs + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
+    cta.whole_chunks = max(0, min(cta.slice_vecs, whole - cta.slice0)) / Kd::kChunkVecs;
     cta.lane = tid & 31;
     cta.depth_log = plan.depth_log;
+    cta.ring = smem_u32(smem);
+    cta.full = smem_u32(S.full);
+    cta.ready = smem_u32(S.ready);
+    cta.empty = smem_u32(S.empty);
     cta.words = reinterpret_cast<unsigned long long *>(smem + plan.words_at);
 
     if (tid == 0) {
@@ -1489,47 +1617,59 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
         for (int i = 0; i < kDepth; ++i) {
             mbar_init(smem_u32(&S.row_full[i]), 1);
             mbar_init(smem_u32(&S.row_free[i]), kConsumers + (Kd::List ? 3 : 2));
+            mbar_init(smem_u32(&S.sent[i]), 1);
             mbar_init(smem_u32(&S.summed[i]), kConsumers);
             mbar_init(smem_u32(&S.known[i]), 1);
             mbar_init(smem_u32(&S.stored[i]), kConsumers);
             mbar_init(smem_u32(&S.bounded[i]), kConsumers);
         }
         mbar_init(smem_u32(&S.granted), 1);
+        mbar_init(smem_u32(&S.acked), plan.cluster);
         mbar_init(smem_u32(&S.gathered), plan.cluster);
+        S.asked = 0;
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (Kd::List)
         for (int i = tid; i < kHash; i += kThreads) list.hash[i] = -1;
     if (plan.cluster > 1)
-        for (int i = tid; i < kDepth * plan.cluster * kConsumers * Kd::kWords; i += kThreads) cta.words[i] = 0;
+        for (int i = tid; i < 2 * plan.cluster * kConsumers * Kd::kWords; i += kThreads) cta.words[i] = 0;
     __syncthreads();
     if (plan.cluster > 1) cluster_sync();
     after_previous();
 
-    if (warp < kConsumers) consume<Kd>(P, plan, S, top, ring, cta);
-    else if (warp == kScout) scout<Kd>(P, plan, S, top, list, cta);
-    else if (warp == kProducer) produce<Kd>(P, plan, S, ring, cta);
-    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, list, ring, cta);
-    else if (warp == kEpilogue) finish<Kd>(P, plan, S, top, list, cta);
+    Entries at{cta.first, 0};
+    if (warp < kConsumers) consume<Kd>(P, plan, S, top, cta);
+    else if (warp == kScout) scout<Kd>(P, plan, S, list, cta, at);
+    else if (warp == kProducer) produce<Kd>(P, plan, S, cta);
+    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, list, smem, cta);
+    else if (warp == kEpilogue) finish<Kd>(P, S, top, list, cta);
     __syncwarp();
-    // sums of other CTAs may still be on their way here where somebody gave up
+    // What other CTAs send may still be on its way here where somebody gave up.
+    if (plan.cluster > 1) cluster_sync();
+    // The same of an answer to a request.
+    if (warp == kScout && plan.dynamic) {
+        int asked;
+        asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(asked) : "r"(cluster_addr(&S.asked, 0)) : "memory");
+        if (asked > at.answers && S.abort) mbar_wait_bounded(smem_u32(&S.granted), (uint32_t)at.answers & 1u);
+    }
     if (plan.cluster > 1) cluster_sync();
 }
 
 // ---------------------------------------------------------------------------
 // host
 
-constexpr int kHalfSmem = 113 * 1024, kFullSmem = 226 * 1024;  // of a CTA, two or one on an SM
+constexpr int kHalfSmem = 113 * 1024;  // of a CTA, two on an SM
+constexpr int64_t kRereadBytes = 80 << 20;
 
-// What fits the GPU of a kernel: clusters of 2^i CTAs at once, two CTAs an SM (0) or one (1).
+// What fits the GPU of a kernel: clusters of 2^i CTAs at once.
 template <class Kd>
 struct Room {
-    static inline int clusters[2][5];
+    static inline int clusters[5];
 };
 
-// Rows over the GPU. The sums alone: one CTA a row where that fills the GPU, else as many as do (a power of two). With a
-// gradient: the fewest that hold a row in their rings.
+// Rows over the GPU. One CTA a row where there are rows for every CTA that fits, else as many as do (a power of two). A
+// gradient's rows go through L2 between their readings: no more of them at once than it holds well.
 template <class Kd>
 Plan make_plan(const TokenParams &P) {
     const int64_t vecs = ((int64_t)P.V * Kd::kSize + 15) / 16;
@@ -1538,26 +1678,21 @@ Plan make_plan(const TokenParams &P) {
     p.list_stride = Kd::List ? (P.K + 31) / 32 * 32 : 0;
     const int fixed = (int)((sizeof(Shared) + 15) / 16 * 16) +
                       (Kd::List ? kHashBytes + p.list_stride * kListBytes : Kd::Top ? (int)((sizeof(SharedTop) + 15) / 16 * 16) : 0);
-    auto words = [&](int log) { return log ? (kDepth * kConsumers * Kd::kWords * 8) << log : 0; };
-    auto slots = [&](int log, int smem) { return std::min(kMaxSlots, (smem - fixed - words(log)) / Kd::kChunkBytes); };
-    auto chunks = [&](int log) {
-        const int64_t slice = ((vecs + (1 << log) - 1 >> log) + 31) / 32 * 32;
-        return (slice + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
-    };
     const auto &room = Room<Kd>::clusters;
     int log = 0;
     if (Kd::Grad)
-        while (log < 4 && 2 * chunks(log) > slots(log, kHalfSmem)) ++log;
-    while (log < 4 && P.entries <= room[0][log + 1] && vecs >> log >= 256 && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
+        while (log < 4 && (int64_t)room[log] * vecs * 16 > kRereadBytes) ++log;
+    while (log < 4 && P.entries <= room[log + 1] && vecs >> log >= 256 && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
     p.cluster = 1 << log;
     p.slice_vecs = (int32_t)(((vecs + p.cluster - 1 >> log) + 31) / 32 * 32);
-    const bool whole_sm = Kd::Grad && chunks(log) > slots(log, kHalfSmem);
-    p.slots = slots(log, whole_sm ? kFullSmem : kHalfSmem);
-    p.lag = Kd::Grad && 2 * chunks(log) <= p.slots;
-    p.dynamic = log == 0 && P.entries <= INT32_MAX;
-    p.clusters = (int32_t)(p.dynamic ? P.entries : std::min<int64_t>(P.entries, std::max(1, room[whole_sm][log])));
+    const int words = log ? (2 * kConsumers * Kd::kWords * 8) << log : 0;
+    p.slots = std::min(kMaxSlots, (kHalfSmem - fixed - words) / Kd::kChunkBytes);
+    // (the sums of a cluster's rows have no way to keep one another apart: it has one row)
+    p.dynamic = (Kd::Grad || log == 0) && P.entries <= INT32_MAX >> log;
+    p.eager = vecs * 16 >> log <= p.slots * Kd::kChunkBytes;
+    p.clusters = (int32_t)(p.dynamic ? P.entries : std::min<int64_t>(P.entries, std::max(1, room[log])));
     p.words_at = p.slots * Kd::kChunkBytes + fixed;
-    p.smem = p.words_at + words(log);
+    p.smem = p.words_at + words;
     return p;
 }
 
@@ -1570,22 +1705,21 @@ cudaError_t launch(const TokenParams &P, cudaStream_t s) {
 
 template <class Kd>
 cudaError_t prepare() {
-    cudaError_t e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFullSmem);
+    cudaError_t e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHalfSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    for (int whole = 0; whole < 2; ++whole)
-        for (int log = 0; log < 5 && e == cudaSuccess; ++log) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << log;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(1u << log);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = whole ? kFullSmem : kHalfSmem;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&Room<Kd>::clusters[whole][log], token_kernel<Kd>, &cfg);
-        }
+    for (int log = 0; log < 5 && e == cudaSuccess; ++log) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << log;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(1u << log);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kHalfSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&Room<Kd>::clusters[log], token_kernel<Kd>, &cfg);
+    }
     return e;
 }
 
