@@ -43,9 +43,10 @@ constexpr int kMaxSlots = 26;
 constexpr int kDepth = 4;                         // rows between the scout and the epilogue at most
 constexpr int kTopDepth = 2;                      // the same where top tokens are asked for (their buffers are large)
 constexpr int kMaxCluster = 16;
-constexpr int kCandidates = 192;                  // a warp's vectors that may hold top tokens: its share of a chunk of ties, and more
-constexpr int kKeys = 512;                        // vectors that still do at the end, and tokens among them
-constexpr int kGathered = 512;                    // keys that a cluster's CTAs send to its first
+constexpr int kGroupRows = 20;                    // groups of a thread's vectors in a slice whose maxima are kept
+constexpr int kKept = 512;                        // groups that may hold top tokens
+constexpr int kKeys = 1024;                       // tokens among them
+constexpr int kGathered = 256;                    // keys that a cluster's CTAs send to its first
 constexpr int kHash = 1024;
 
 enum State { kLive = 0, kSkip = 1, kBad = 2, kEnd = 3 };
@@ -71,6 +72,7 @@ struct Row {
     long long entry;
     int state;
     int y;
+    int bad;       // what was found wrong with its list
     float zy;
     float p_rest, p_sum;  // of a list: what it leaves of one, what it has
     float zmax, zsum;     // of a list: the draft's largest logit, and the sum of 2^((z - zmax) c)
@@ -88,9 +90,9 @@ struct Part {
 
 struct Shared {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots];
-    // of a row: asked for and checked; done with; its copies issued; the CTA's sums there, its bounds (top tokens); of a
-    // gradient: what the second reading needs, all stored
-    uint64_t row_full[kDepth], row_free[kDepth], sent[kDepth], summed[kDepth], bounded[kDepth], known[kDepth], stored[kDepth];
+    // of a row: known; done with; all known of its entry; its copies issued; the CTA's sums there; of a gradient: what the
+    // second reading needs, all stored
+    uint64_t row_full[kDepth], row_free[kDepth], scouted[kDepth], sent[kDepth], summed[kDepth], known[kDepth], stored[kDepth];
     uint64_t gathered, granted, acked;
     uint4 grant;          // the answer to a request for another row
     Row row[kDepth];
@@ -105,13 +107,10 @@ struct Shared {
 // Top tokens: a key is a logit's bits, made to order as it does, over its
 // token's, inverted: keys fall in the order of alternatives, and 0 is none.
 struct SharedTop {
-    unsigned long long bound[kTopDepth][kConsumers];  // that many tokens are at least so large; chunk
-    // vectors of the row with a token that reaches the bound of its time, and their maxima
-    int2 at[kTopDepth][kConsumers][kCandidates];
-    int count[kTopDepth][kConsumers];
-    int32_t kept[kTopDepth][kKeys];                   // those that reach the last bound
+    uint16_t most[kTopDepth][kGroupRows][kTeam];  // upper halves of the order bits of the groups' maxima
+    uint32_t bound[kTopDepth][kConsumers];        // that many of the warp's tokens are at least so large
+    uint16_t kept[kTopDepth][kKept];
     unsigned long long keys[kTopDepth][kKeys];
-    unsigned long long best[kTopDepth][kMaxAlternatives];
     unsigned long long gathered[kGathered];
 };
 
@@ -137,6 +136,7 @@ struct Plan {
     int32_t slice_vecs;   // vectors of a slice, but the last's
     int32_t depth_log;    // rows between the scout and the epilogue
     int32_t list_stride;  // entries of a list
+    int32_t group_log;    // chunks of a group of top tokens
     int32_t words_at;     // where in shared memory the words of a cluster are
     int32_t smem;
 };
@@ -596,14 +596,15 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                                           uint32_t row_parity, int live, Cursor &cur) {
     constexpr int kVecs = Kd::kVecs, kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane, warp = tid >> 5;
-    const int nth = Kd::Top ? (P.k + kConsumers - 1) / kConsumers : 1;
-    float m = -INFINITY, R = -INFINITY, most = -INFINITY;
+    float m = -INFINITY, R = -INFINITY, most = -INFINITY, group = -INFINITY;
     f32x2 s0 = 0ull, s1 = 0ull, t0 = 0ull, t1 = 0ull;
     bool bad = false;
     int before = 0;
     uint32_t above = 0, bound_before = 0, bound_after = 0;
     int y_vec = 0;
-    if (Kd::Rank) {  // a token equal to the given one comes before it where its index is lower
+    if (Kd::Rank) {
+        if (!wait_bar(S.scouted[d], row_parity, S, P)) return false;
+        // a token equal to the given one comes before it where its index is lower
         const float zy = S.row[d].zy, below = next_below<Kd::DT>(zy);
         y_vec = S.row[d].y / kPer;
         bound_after = __float_as_uint(zy);
@@ -614,9 +615,6 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         }
         if (zy == -INFINITY) bound_before = bound_after;  // and the equal ones one by one, below
     }
-    float least = -INFINITY;  // what a vector has to reach to hold a top token,
-    int least_chunk = 0;      // and in later chunks than this one to pass
-    int found = 0;
     const float c = P.c;
     const f32x2 c2 = pack2(c, c);
     const uint32_t mine = cta.ring + tid * 16;
@@ -672,7 +670,12 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             m = cm;
             R = next;
         }
-        if (Kd::Top) most = fmaxf(most, cm);
+        if (Kd::Top) {
+            // all that the top tokens need of a chunk (lists of the vectors that pass a rising bound took 70 instructions more)
+            group = (i & ((1 << plan.group_log) - 1)) == 0 ? cm : fmaxf(group, cm);
+            most = fmaxf(most, cm);
+            top->most[d][i >> plan.group_log][tid] = (uint16_t)(order_bits(group) >> 16);
+        }
         if (plain(m)) {
             const f32x2 nR = pack2(-R, -R);
 #pragma unroll
@@ -721,45 +724,12 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                 above = 0;
             }
         }
-        if (Kd::Top) {
-            // Each warp bounds the k-th largest logit by the nth largest of its lanes' maxima: 8 warps have 8 nth >= k
-            // tokens that large. The bound of the first chunk is everybody's; it then rises at chunks 1, 3, 7, ...
-            if ((i & (i + 1)) == 0 || i + 1 == cta.chunks) {
-                const uint32_t nth_max = warp_nth(order_bits(most), nth, lane);
-                if (lane == 0)
-                    *(volatile unsigned long long *)&top->bound[d][warp] = ((unsigned long long)nth_max << 32) | (uint32_t)i;
-                if (i == 0) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
-                    if (!wait_bar(S.bounded[d], row_parity, S, P)) return false;
-                }
-            }
-            if ((i & (i - 1)) == 0) {
-                const unsigned long long b = lane < kConsumers ? *(volatile unsigned long long *)&top->bound[d][lane] : ~0ull << 32;
-                least = from_order_bits(__reduce_min_sync(0xffffffffu, (uint32_t)(b >> 32)));
-                least_chunk = (int)__reduce_max_sync(0xffffffffu, (uint32_t)b);
-            }
-            // Tokens that equal the bound come after the ones that made it, once these lie in earlier chunks.
-            const bool strict = i > least_chunk;
-            if (__any_sync(0xffffffffu, strict ? cm > least : cm >= least)) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    const int v = i * Kd::kChunkVecs + tid + j * kTeam;
-                    const float x = from_packed_max<Kd::DT>(pm[j]);
-                    const bool pass = v < cta.slice_vecs && (strict ? x > least : x >= least);
-                    const uint32_t who = __ballot_sync(0xffffffffu, pass);
-                    if (pass) {
-                        const int to = found + __popc(who & ((1u << lane) - 1u));
-                        if (to < kCandidates) top->at[d][warp][to] = make_int2(cta.slice0 + v, __float_as_int(x));
-                    }
-                    found += __popc(who);
-                }
-            }
-        }
     }
     if (Kd::Top) {
-        if (lane == 0) top->count[d][warp] = found;
-        if (cta.chunks == 0 && lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
+        // Each warp bounds the k-th largest logit by the nth largest of its lanes' maxima: 8 warps have 8 nth >= k tokens that
+        // large.
+        const uint32_t nth = warp_nth(order_bits(most), (P.k + kConsumers - 1) / kConsumers, lane);
+        if (lane == 0) top->bound[d][warp] = nth;
     }
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
     if (Kd::Rank) before += counted<Kd::DT>(above);
@@ -770,6 +740,8 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         p.s *= g;
     }
     p = warp_fold<Kd>(p, c);
+    // (a list's or a token's logits are read before any CTA can overwrite the row)
+    if (Kd::Grad && cta.cluster > 1 && !wait_bar(S.scouted[d], row_parity, S, P)) return false;
     if (cta.cluster > 1) send<Kd>(cta, cta.rank * kConsumers + warp, live, p);
     else if (lane == 0) S.part[d][warp] = p;
     __syncwarp();
@@ -885,7 +857,6 @@ __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, 
         if (state == kLive) {
             if (!sum_slice<Kd>(P, plan, S, top, cta, d, cta.parity(r), live++, cur)) return;
         } else if (cta.lane == 0) {
-            if (Kd::Top) mbar_arrive(smem_u32(&S.bounded[d]));
             mbar_arrive(smem_u32(&S.summed[d]));
         }
         if (Kd::Grad && !store_slice<Kd>(P, plan, S, cta, d, cta.parity(r), cur)) return;
@@ -985,8 +956,8 @@ __device__ __forceinline__ void fetch(const TokenParams &P, long long e, int lan
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void scout_token(const TokenParams &P, Row &row, long long e, const Asked &a) {
+// What a row is: one lane's work.
+__device__ __forceinline__ void scout_row(const TokenParams &P, Row &row, long long e, const Asked &a) {
     int bits = 0;
     if (a.y != -1) {
         if (a.y < 0 || a.y >= P.V) bits = SPECVERIFY_STATUS_BAD_TOKEN;
@@ -996,39 +967,58 @@ __device__ __forceinline__ void scout_token(const TokenParams &P, Row &row, long
     row.entry = e;
     row.y = a.y;
     row.state = a.y == -1 ? kSkip : bits ? kBad : kLive;
-    row.zy = row.state == kLive ? plain_logit<DT>(row.z, a.y) : 0.0f;
     row.g = a.g;
     row.h = a.h;
     if (bits) atomicOr(P.status, bits);
 }
 
-// A list: its ids, the draft's logits of them, the target's log-probabilities.
+// The same of a list, the warp's work: its ids, where they are tokens.
+__device__ __forceinline__ void scout_ids(const TokenParams &P, Row &row, const Lists &L, int d, long long e, int lane, const Asked &a) {
+    constexpr uint32_t all = 0xffffffffu;
+    bool bad = false, any = false;
+#pragma unroll
+    for (int i = 0; i < kMaxList / 32; ++i) {
+        const int j = lane + 32 * i;
+        if (j >= P.K) continue;
+        const int id = a.id[i];
+        const bool token = id >= 0 && id < P.V;
+        bad = bad || (!token && id != -1);
+        any = any || token;
+        L.ids[d * L.stride + j] = token ? id : -1;
+    }
+    bad = __any_sync(all, bad);
+    any = __any_sync(all, any);
+    if (lane == 0) {
+        row.z = P.logits + e * P.stride_bytes;
+        row.entry = e;
+        row.state = bad ? kBad : any ? kLive : kSkip;
+        row.g = a.g;
+        if (bad) atomicOr(P.status, SPECVERIFY_STATUS_BAD_TOKEN);
+    }
+}
+
+// The rest of a list: the draft's logits of it, the target's log-probabilities, what can be summed of both.
 template <int DT>
 __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const Lists &L, int d, long long e, int lane, const Asked &a) {
     constexpr uint32_t all = 0xffffffffu;
     const char *z = P.logits + e * P.stride_bytes;
-    int32_t *ids = L.ids + d * L.stride;
+    const int32_t *ids = L.ids + d * L.stride;
     float *lz = L.z + d * L.stride, *llp = L.lp + d * L.stride, *lpr = L.p + d * L.stride;
     int bits = 0;
-    bool any = false;
     float top = -INFINITY, zmax = -INFINITY;
     float zk[kMaxList / 32];
 #pragma unroll
     for (int i = 0; i < kMaxList / 32; ++i) {
-        zk[i] = -INFINITY;
-        if (lane + 32 * i < P.K && a.id[i] >= 0 && a.id[i] < P.V) zk[i] = plain_logit<DT>(z, a.id[i]);
+        const int j = lane + 32 * i;
+        zk[i] = j < P.K && ids[j] >= 0 ? plain_logit<DT>(z, ids[j]) : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < kMaxList / 32; ++i) {
         const int j = lane + 32 * i;
         if (j >= P.K) continue;
-        int id = a.id[i];
+        const int id = ids[j];
         float t = -INFINITY;
-        if (id < -1 || id >= P.V) {
-            bits |= SPECVERIFY_STATUS_BAD_TOKEN;
-            id = -1;
-        } else if (id >= 0) {
-            any = true;
+        if (id >= 0) {
             t = a.t[i];
             if (!(zk[i] < INFINITY) || !(t < INFINITY)) bits |= SPECVERIFY_STATUS_BAD_LOGIT;
             // twice the same id: one of its entries finds the other in the table
@@ -1039,7 +1029,6 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
                 if (was == -1 || was == id) break;
             }
         }
-        ids[j] = id;
         lz[j] = zk[i];
         llp[j] = t;
         top = fmaxf(top, t);
@@ -1048,10 +1037,9 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
     __syncwarp();
     for (int j = lane; j < kHash / 4; j += 32) reinterpret_cast<int4 *>(L.hash)[j] = make_int4(-1, -1, -1, -1);
     bits = __reduce_or_sync(all, bits);
-    any = __any_sync(all, any);
     float p_rest = 0.0f, p_sum = 0.0f, zsum = 0.0f, cross = 0.0f;
     zmax = warp_max(zmax);
-    if (!bits && any) {
+    if (!bits) {
         if (P.form == SPECVERIFY_TARGET_LOGITS) {
             top = warp_max(top);
             float sum = 0.0f, lh = 0.0f, ll = 0.0f;
@@ -1098,15 +1086,12 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
         cross = warp_sum(cross);
     }
     if (lane == 0) {
-        row.z = z;
-        row.entry = e;
-        row.state = bits ? kBad : any ? kLive : kSkip;
+        row.bad = bits;
         row.p_rest = p_rest;
         row.p_sum = p_sum;
         row.zmax = zmax;
         row.zsum = zsum;
         row.cross = cross;
-        row.g = a.g;
         if (bits) atomicOr(P.status, bits);
     }
 }
@@ -1123,9 +1108,9 @@ __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Sh
         if (at.e < 0) {
             if (cta.lane == 0) S.row[d].state = kEnd;
         } else if (Kd::List) {
-            scout_list<Kd::DT>(P, S.row[d], list, d, at.e, cta.lane, a);
+            scout_ids(P, S.row[d], list, d, at.e, cta.lane, a);
         } else if (cta.lane == 0) {
-            scout_token<Kd::DT>(P, S.row[d], at.e, a);
+            scout_row(P, S.row[d], at.e, a);
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_full[d]));
@@ -1133,6 +1118,13 @@ __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Sh
             if (++ends == Kd::kEpilogues) return;
             continue;
         }
+        // The copies can begin; what else there is to know of the entry
+        if (S.row[d].state == kLive) {
+            if (Kd::List) scout_list<Kd::DT>(P, S.row[d], list, d, at.e, cta.lane, a);
+            else if (cta.lane == 0) S.row[d].zy = plain_logit<Kd::DT>(S.row[d].z, a.y);
+        }
+        __syncwarp();
+        if (cta.lane == 0) mbar_arrive(smem_u32(&S.scouted[d]));
         // The next row is asked for when (nearly) all of this one's copies have been issued: not sooner than it is needed.
         if (!plan.eager && !wait_bar(S.sent[d], cta.parity(r), S, P)) return;
         if (!at.next(P, plan, S, cta)) return;
@@ -1154,7 +1146,7 @@ __device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, 
         if (!ok || S.row[d].state == kEnd) break;
         const char *z = S.row[d].z;
         const int n = S.row[d].state != kLive ? 0 : Kd::Grad ? 2 * cta.chunks : cta.chunks;
-        // A list takes the scout five microseconds, three dependent loads and their answer; a token two.
+        // (a list takes the scout some five microseconds to its publication, a token two)
         const int ask = n == 0 ? -1 : Kd::List ? max(0, n - 1 - plan.slots) : n - 1;
         for (int j = 0; j < n; ++j) {
             ok = wait_at(cta.empty + 8 * cur.slot, cur.phase ^ 1u, S, P);
@@ -1231,163 +1223,259 @@ __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Sh
 // ---------------------------------------------------------------------------
 // epilogue
 
-// Calls f with the keys of the tokens of n vectors, or (n < 0) of the whole slice, read once more from memory (L2), one for
-// every lane at a time; 0 is none.
-template <int DT, class F>
-__device__ __forceinline__ void each_key(const TokenParams &P, const char *row, const int32_t *at, int n, const Cta &cta, F &&f) {
-    constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2);
-    const int whole = P.V / kPer, first = n < 0 ? cta.slice0 : 0;
-    const int end = n < 0 ? min(whole, cta.slice0 + cta.slice_vecs) : n;
-    const uint4 *z = reinterpret_cast<const uint4 *>(row);
-    bool ragged = n < 0 && cta.slice0 + cta.slice_vecs > whole;
-    for (int i = first; i < end; i += 128) {
-        uint4 w[4];
-        int v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int j = i + 32 * q + cta.lane;
-            v[q] = j < end ? (n < 0 ? j : at[j]) : -1;
-            if (v[q] == whole) {
-                ragged = true;
-                v[q] = -1;
-            }
-            if (v[q] >= 0) w[q] = __ldg(z + v[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (i + 32 * q >= end) break;
-            float x[kPer];
-            vec_floats<DT>(w[q], x);
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) f(v[q] < 0 ? 0ull : order_key(x[u], v[q] * kPer + u));
-        }
-    }
-    if (__any_sync(0xffffffffu, ragged)) {  // the row's ragged end
-        const int t = whole * kPer + cta.lane;
-        f(t < P.V ? order_key(load_logit<DT>(row, t), t) : 0ull);
-    }
-}
-
-// Sorts 32 N keys, the largest first; element 32 q + i is x[q] of lane i (a bitonic network).
+// Sorts 32 N keys, the largest first; element 32 q + i is x[q] of lane i (a bitonic network, rolled up: it runs once a row, and
+// its instructions would not stay in the cache).
 template <int N>
 __device__ __forceinline__ void sort_keys(unsigned long long (&x)[N], int lane) {
-#pragma unroll
+#pragma unroll 1
     for (int k = 2; k <= 32 * N; k <<= 1) {
-#pragma unroll
+#pragma unroll 1
         for (int j = k >> 1; j > 0; j >>= 1) {
-            if (j >= 32) {
-#pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    const int o = q ^ (j >> 5);
-                    if (o < q) continue;
-                    const bool falls = ((32 * q) & k) == 0;
-                    const unsigned long long a = max(x[q], x[o]), b = min(x[q], x[o]);
-                    x[q] = falls ? a : b;
-                    x[o] = falls ? b : a;
-                }
-            } else {
+            if (j < 32) {
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
                     const unsigned long long o = __shfl_xor_sync(0xffffffffu, x[q], j);
                     const bool larger = (((32 * q + lane) & k) == 0) == ((lane & j) == 0);
                     x[q] = larger ? max(x[q], o) : min(x[q], o);
                 }
+                continue;
+            }
+#pragma unroll
+            for (int step = 1; step < N; step <<= 1) {
+                if (j != 32 * step) continue;
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    if (q & step) continue;
+                    const bool falls = ((32 * q) & k) == 0;
+                    const unsigned long long a = max(x[q], x[q ^ step]), b = min(x[q], x[q ^ step]);
+                    x[q] = falls ? a : b;
+                    x[q ^ step] = falls ? b : a;
+                }
             }
         }
     }
 }
 
-// The k best keys of the CTA's slice, in order, in T.best[d] (0 where there are none). One warp's work beside the next row's
-// sums, so it counts: a list of 514 vectors of a row of 152064 bf16 logits (k = 64) is cut by their maxima to the 115 that
-// reach the last bound before any of them is read, and 120 keys are sorted in registers (a place by counting larger ones
-// took 7 us).
-template <int DT>
-__device__ __noinline__ void select_top(const TokenParams &P, const char *row, SharedTop &T, int d, const Cta &cta) {
-    constexpr uint32_t all = 0xffffffffu;
-    const int lane = cta.lane, k = P.k;
-    const uint32_t below = (1u << lane) - 1u;
-    unsigned long long *keys = T.keys[d];
-    // the last bound: k tokens are at least so large, or there are not that many
-    const unsigned long long b = lane < kConsumers ? T.bound[d][lane] : ~0ull;
-    unsigned long long least = cta.chunks ? (unsigned long long)__reduce_min_sync(all, (uint32_t)(b >> 32)) << 32 : 0ull;
-    const float least_logit = from_order_bits((uint32_t)(least >> 32));
-    int n = 0;
-    bool over = false;
-    for (int w = 0; w < (cta.chunks ? kConsumers : 0); ++w) {
-        const int count = T.count[d][w];
-        over = over || count > kCandidates;
-        for (int i = 0; i < min(count, kCandidates); i += 32) {
-            const int2 a = i + lane < min(count, kCandidates) ? T.at[d][w][i + lane] : make_int2(-1, 0);
-            const bool in = a.x >= 0 && __int_as_float(a.y) >= least_logit;
-            const uint32_t who = __ballot_sync(all, in);
-            const int to = n + __popc(who & below);
-            if (in && to < kKeys) T.kept[d][to] = a.x;
-            n += __popc(who);
-        }
-    }
+// The first k of n keys, in order, to the start of them (0 where there are no more); n <= kKeys, k <= 32 N.
+template <int N>
+__device__ __forceinline__ void sort_front(unsigned long long *keys, int n, int k, int lane) {
+    unsigned long long x[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] = 32 * q + lane < n ? keys[32 * q + lane] : 0;
+    sort_keys<N>(x, lane);
     __syncwarp();
-    if (over || n > kKeys) n = -1;
-    for (int i = lane; i < k; i += 32) T.best[d][i] = 0;
-    auto collect = [&]() {
-        int m = 0;
-        each_key<DT>(P, row, T.kept[d], n, cta, [&](unsigned long long x) {
-            const bool in = x != 0 && x >= least;
-            const uint32_t who = __ballot_sync(all, in);
-            if (!who) return;
-            const int to = m + __popc(who & below);
-            if (in && to < kKeys) keys[to] = x;
-            m += __popc(who);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (32 * q + lane < k) keys[32 * q + lane] = x[q];
+    __syncwarp();
+}
+
+__device__ __noinline__ void first_keys(unsigned long long *keys, int n, int k, int lane) {
+    if (n <= 128) sort_front<4>(keys, n, k, lane);
+    else if (n <= 256) sort_front<8>(keys, n, k, lane);
+    else sort_front<32>(keys, n, k, lane);
+}
+
+// Calls f(vector, its index, whether there is one) over n vectors, index(i) the i-th, eight of a lane at a time: read once
+// more from memory (L2). The row's ragged end comes from its logits, with -inf behind them.
+template <int DT, class Index, class F>
+__device__ __forceinline__ void each_batch(const TokenParams &P, const char *row, int n, int lane, Index &&index, F &&f) {
+    using Kd = Kind<DT, false, false, true, true, false>;
+    const int whole = P.V / Kd::kPer, rest = P.V - whole * Kd::kPer;
+    const uint4 *z = reinterpret_cast<const uint4 *>(row);
+    for (int i = 0; i < n; i += 256) {
+        uint4 w[8];
+        int v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int j = i + 32 * q + lane;
+            v[q] = j < n ? index(j) : -1;
+            w[q] = make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
+            if (v[q] == whole) w[q] = ragged_end<Kd>(row, whole, rest);
+            else if (v[q] >= 0) w[q] = __ldg(z + v[q]);
+        }
+        if (!f(w, v, i)) return;
+    }
+}
+
+// The k best keys of the CTA's slice, in order, to the start of T.keys[d] (0 where there are none). One warp's work beside the
+// next row's sums (two warps take rows in turn): of a row of 152064 bf16 logits and k = 64 some 115 of 4864 groups reach the
+// bound, their 460 vectors are read again, and some 120 keys are sorted in registers.
+//
+// The bound's class are the logits whose order bits share its upper 16: one value of bf16, 2^-7 of a value of fp32. Tokens
+// above the class are in groups above it. Only if they are fewer than k, tokens of the class are needed, of bf16 those of the
+// lowest indexes: groups with one, chunk after chunk, until there are enough.
+template <int DT>
+__device__ __noinline__ void select_top(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta) {
+    constexpr uint32_t all = 0xffffffffu;
+    constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2), kPart = kTeam * 4;  // vectors of a chunk
+    const int lane = cta.lane, k = P.k, log = plan.group_log;
+    unsigned long long *keys = T.keys[d];
+    const int rows = (cta.chunks + (1 << log) - 1) >> log;
+    const uint32_t bound = __reduce_min_sync(all, lane < kConsumers ? T.bound[d][lane] : ~0u) >> 16;
+    const uint32_t bound2 = bound | bound << 16;
+    const float high = from_order_bits(bound << 16 | 0xffffu);
+    float low = from_order_bits(bound << 16);
+    if (low != low) low = -INFINITY;
+    // exclusive sums over the lanes
+    auto before = [&](int c, int &total) {
+        int incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(all, incl, off);
+            if (lane >= off) incl += y;
+        }
+        total = __shfl_sync(all, incl, 31);
+        return incl - c;
+    };
+    // groups of row r among the lane's eight: halves of words that are above the bound, or equal to it
+    auto above = [&](int r, bool equal, uint32_t (&m)[4]) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][lane * 8]);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            m[q] = equal ? __vcmpeq2(x[q], bound2) : __vcmpgtu2(x[q], bound2);
+            c += __popc(m[q]);
+        }
+        return c >> 4;
+    };
+    auto keep = [&](int r, const uint32_t (&m)[4], int to) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (m[q >> 1] >> (16 * (q & 1)) & 1u) {
+                if (to < kKept) T.kept[d][to] = (uint16_t)(r * kTeam + lane * 8 + q);
+                ++to;
+            }
+    };
+    // vector j of the kept groups
+    auto kept = [&](int j) {
+        const int g = T.kept[d][j >> (2 + log)], part = j & ((4 << log) - 1);
+        const int v = (((g / kTeam) << log) + (part >> 2)) * kPart + (part & 3) * kTeam + g % kTeam;
+        return v < cta.slice_vecs ? cta.slice0 + v : -1;
+    };
+    // tokens of the first n kept vectors above the class, or in it, behind the `from` keys that are there; false: too many
+    auto collect = [&](int n, bool equal, int &from) {
+        bool fits = true;
+        each_batch<DT>(P, row, n, lane, kept, [&](const uint4 (&w)[8], const int (&v)[8], int) {
+            uint64_t in = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float x[kPer];
+                vec_floats<DT>(w[q], x);
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    if (v[q] >= 0 && v[q] * kPer + u < P.V && (equal ? x[u] >= low && x[u] <= high : x[u] > high))
+                        in |= 1ull << (8 * q + u);
+            }
+            int total, to = before(__popcll(in), total) + from;
+            from += total;
+            fits = from <= kKeys;
+            if (!fits) return false;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (!(in >> (8 * q) & 0xffu)) continue;
+                float x[kPer];
+                vec_floats<DT>(w[q], x);
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    if (in >> (8 * q + u) & 1u) keys[to++] = order_key(x[u], v[q] * kPer + u);
+            }
+            return true;
         });
         __syncwarp();
-        return m;
+        return fits;
     };
-    int m = collect();
-    if (m > kKeys) {
-        // many equal logits: the largest key that k tokens reach, a bit at a time
-        unsigned long long key = 0;
-        for (int bit = 63; bit >= 0; --bit) {
-            const unsigned long long next = key | 1ull << bit;
-            int c = 0;
-            each_key<DT>(P, row, T.kept[d], n, cta, [&](unsigned long long x) { c += x >= next ? 1 : 0; });
-            if ((int)__reduce_add_sync(all, (unsigned)c) >= k) key = next;
-        }
-        least = max(least, key);
-        m = min(collect(), kKeys);
-    }
-    auto sorted = [&](auto &x) {
-        constexpr int N = sizeof(x) / 8;
-#pragma unroll
-        for (int q = 0; q < N; ++q) x[q] = 32 * q + lane < m ? keys[32 * q + lane] : 0;
-        sort_keys<N>(x, lane);
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-            if (32 * q + lane < k) T.best[d][32 * q + lane] = x[q];
-    };
-    if (m <= 32) {
-        unsigned long long x[1];
-        sorted(x);
-    } else if (m <= 128) {
-        unsigned long long x[4];
-        sorted(x);
-    } else {
-        // a key's place is the number of larger ones
-        for (int i0 = 0; i0 < m; i0 += 128) {
-            unsigned long long x[4];
-            int place[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = i0 + 32 * q + lane < m ? keys[i0 + 32 * q + lane] : 0;
-#pragma unroll 4
-            for (int i = 0; i < m; ++i) {
-                const unsigned long long o = keys[i];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) place[q] += o > x[q] ? 1 : 0;
+
+    int groups = 0, found = 0;
+    {
+        int mine = 0;
+        uint32_t m[4];
+        for (int r = 0; r < rows; ++r) mine += above(r, false, m);
+        int to = before(mine, groups);
+        if (groups <= kKept)
+            for (int r = 0; r < rows; ++r) {
+                const int c = above(r, false, m);
+                if (c) keep(r, m, to);
+                to += c;
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (x[q] && place[q] < k) T.best[d][place[q]] = x[q];
-        }
     }
     __syncwarp();
+    bool ok = groups <= kKept && collect(groups << (2 + log), false, found);
+    if (ok && found < k) {
+        int equal = 0;
+        for (int r = 0; r < rows && (DT == SV_DT_FP32 || equal < k - found); ++r) {
+            uint32_t m[4];
+            int total;
+            const int c = above(r, true, m), to = before(c, total) + groups + equal;
+            if (c) keep(r, m, to);
+            equal += total;
+        }
+        __syncwarp();
+        const int larger = found;
+        ok = groups + equal <= kKept && collect((groups + equal) << (2 + log), true, found);
+        if (!ok && DT == SV_DT_BF16) {
+            // the slice's first tokens that equal the bound, from its start
+            found = larger;
+            ok = true;
+            each_batch<DT>(P, row, cta.slice_vecs, lane, [&](int j) { return cta.slice0 + j; },
+                           [&](const uint4 (&w)[8], const int (&v)[8], int) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float x[kPer];
+                    vec_floats<DT>(w[q], x);
+                    uint32_t in = 0;
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u)
+                        if (v[q] >= 0 && v[q] * kPer + u < P.V && x[u] >= low && x[u] <= high) in |= 1u << u;
+                    int total, to = before(__popc(in), total) + found;
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u)
+                        if (in >> u & 1u) {
+                            if (to < k) keys[to] = order_key(x[u], v[q] * kPer + u);
+                            ++to;
+                        }
+                    found = min(k, found + total);
+                }
+                return found < k;
+            });
+            __syncwarp();
+        }
+    }
+    if (!ok) {
+        // Many tokens within a hair of the bound: the largest key that k of them reach, a bit at a time over the whole slice.
+        unsigned long long key = 0;
+        for (int bit = 63; bit >= -1; --bit) {
+            const unsigned long long next = bit < 0 ? key : key | 1ull << bit;
+            int c = 0;
+            found = 0;
+            each_batch<DT>(P, row, cta.slice_vecs, lane, [&](int j) { return cta.slice0 + j; },
+                           [&](const uint4 (&w)[8], const int (&v)[8], int) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float x[kPer];
+                    vec_floats<DT>(w[q], x);
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) {
+                        const unsigned long long mine = order_key(x[u], v[q] * kPer + u);
+                        const bool in = v[q] >= 0 && v[q] * kPer + u < P.V && mine >= next;
+                        if (bit >= 0) {
+                            c += in ? 1 : 0;
+                        } else {
+                            const uint32_t who = __ballot_sync(all, in);
+                            if (in && found + __popc(who & ((1u << lane) - 1u)) < kKeys) keys[found + __popc(who & ((1u << lane) - 1u))] = mine;
+                            found += __popc(who);
+                        }
+                    }
+                }
+                return true;
+            });
+            if (bit >= 0 && (int)__reduce_add_sync(all, (unsigned)c) >= k) key = next;
+        }
+        found = min(found, kKeys);
+        __syncwarp();
+    }
+    first_keys(keys, found, k, lane);
 }
 
 template <int DT>
@@ -1403,7 +1491,7 @@ __device__ __forceinline__ void write_top(const TokenParams &P, long long e, int
 }
 
 template <class Kd>
-__device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, SharedTop *T, const Cta &cta, int d, const Part &p) {
+__device__ __forceinline__ bool finish_token(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Cta &cta, int d, const Part &p) {
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane, k = Kd::Top ? P.k : 0;
@@ -1447,11 +1535,11 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
     }
     if constexpr (Kd::Top) {
         if (row.state == kLive) {
-            select_top<Kd::DT>(P, row.z, *T, d, cta);
+            select_top<Kd::DT>(P, plan, row.z, *T, d, cta);
             if (!alone) {
                 for (int i = lane; i < k; i += 32)
                     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(&T->gathered[cta.rank * k + i], 0)),
-                                 "l"(T->best[d][i])
+                                 "l"(T->keys[d][i])
                                  : "memory");
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 __syncwarp();
@@ -1459,35 +1547,17 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, Shared &S, Sh
                 if (cta.rank != 0) return true;
                 if (!wait_bar(S.gathered, 0, S, P)) return false;  // a cluster of such rows has one
                 asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                first_keys(T->gathered, cta.cluster * k, k, lane);
             }
         }
         if (cta.rank != 0) return true;
-        if (!good) {
-            for (int i = lane; i < k; i += 32) {
+        const unsigned long long *best = alone ? T->keys[d] : T->gathered;
+        for (int i = lane; i < k; i += 32) {
+            if (good) {
+                write_top<Kd::DT>(P, e, i, best[i], p.m, lh, ll);
+            } else {
                 P.top_logprob[e * k + i] = bad ? NAN : -INFINITY;
                 P.top_idx[e * k + i] = -1;
-            }
-        } else if (alone) {
-            for (int i = lane; i < k; i += 32) write_top<Kd::DT>(P, e, i, T->best[d][i], p.m, lh, ll);
-        } else {
-            // each CTA's keys fall: a key's place is how many of each list are larger, found by halves
-            for (int i = lane; i < k; i += 32) write_top<Kd::DT>(P, e, i, 0, p.m, lh, ll);
-            __syncwarp();
-            for (int i = lane; i < cta.cluster * k; i += 32) {
-                const unsigned long long key = T->gathered[i];
-                if (!key) continue;
-                int place = i % k;
-                for (int c = 0; c < cta.cluster && place < k; ++c) {
-                    if (c == i / k) continue;
-                    int from = 0, to = k;  // keys [0, from) are larger, [to, k) are not
-                    while (from < to) {
-                        const int mid = (from + to) >> 1;
-                        if (T->gathered[c * k + mid] > key) from = mid + 1;
-                        else to = mid;
-                    }
-                    place += from;
-                }
-                if (place < k) write_top<Kd::DT>(P, e, place, key, p.m, lh, ll);
             }
         }
     }
@@ -1528,10 +1598,10 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
     const long long e = row.entry;
     const int lane = cta.lane, K = P.K, kind = P.divergence;
     const float M = fmaxf(p.m, row.zmax);
-    const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || M == -INFINITY));
+    const bool bad = row.state == kBad || (row.state == kLive && (row.bad || p.n < 0 || M == -INFINITY));
     const bool good = row.state == kLive && !bad;
     const bool some = p.m > -INFINITY;  // the rest has mass
-    if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
+    if (row.state == kLive && bad && !row.bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
     float loss = bad ? NAN : 0.0f, C = 0.0f, Z = 0.0f;
     if (good) {
         if (row.zmax > -INFINITY) Z = row.zsum * ex2_approx(fmaxf(row.zmax - M, kFar) * P.c);
@@ -1622,7 +1692,7 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
 }
 
 template <class Kd>
-__device__ __forceinline__ void finish(const TokenParams &P, Shared &S, SharedTop *T, const Lists &L, const Cta &cta, int first) {
+__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Lists &L, const Cta &cta, int first) {
     int live = 0;
     for (int r = first;; r += Kd::kEpilogues) {
         const int d = cta.place(r);
@@ -1631,7 +1701,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, Shared &S, SharedTo
         const int state = S.row[d].state;
         if (state == kEnd) return;
         Part p{-INFINITY, 0.0f, 0.0f, 0};
-        if (!wait_bar(S.summed[d], parity, S, P)) return;
+        if (!wait_bar(S.scouted[d], parity, S, P) || !wait_bar(S.summed[d], parity, S, P)) return;
         if (state == kLive && cta.cluster > 1) {
             if (!receive<Kd>(P, S, cta, live++, p)) return;
         } else if (state == kLive) {
@@ -1639,7 +1709,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, Shared &S, SharedTo
             p = warp_fold<Kd>(p, P.c);
         }
         if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
-        else if (!finish_token<Kd>(P, S, T, cta, d, p)) return;
+        else if (!finish_token<Kd>(P, plan, S, T, cta, d, p)) return;
         __syncwarp();
         if (Kd::Grad) {
             if (!wait_bar(S.stored[d], parity, S, P)) return;
@@ -1700,7 +1770,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
             mbar_init(smem_u32(&S.summed[i]), kConsumers);
             mbar_init(smem_u32(&S.known[i]), 1);
             mbar_init(smem_u32(&S.stored[i]), kConsumers);
-            mbar_init(smem_u32(&S.bounded[i]), kConsumers);
+            mbar_init(smem_u32(&S.scouted[i]), 1);
         }
         mbar_init(smem_u32(&S.granted), 1);
         mbar_init(smem_u32(&S.acked), plan.cluster);
@@ -1722,13 +1792,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     else if (warp == kScout) scout<Kd>(P, plan, S, list, cta, at);
     else if (warp == kProducer) produce<Kd>(P, plan, S, cta);
     else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, list, smem, cta);
-    else if (warp == kEpilogue) finish<Kd>(P, S, top, list, cta, 0);
-    else if (Kd::kEpilogues == 2) finish<Kd>(P, S, top, list, cta, 1);
+    else if (warp == kEpilogue) finish<Kd>(P, plan, S, top, list, cta, 0);
+    else if (Kd::kEpilogues == 2) finish<Kd>(P, plan, S, top, list, cta, 1);
     __syncwarp();
     // What other CTAs send may still be on its way here where somebody gave up.
     if (plan.cluster > 1) cluster_sync();
+    if (!plan.dynamic) return;
     // The same of an answer to a request.
-    if (warp == kScout && plan.dynamic) {
+    if (warp == kScout) {
         int asked;
         asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(asked) : "r"(cluster_addr(&S.asked, 0)) : "memory");
         if (asked > at.answers && S.abort) mbar_wait_bounded(smem_u32(&S.granted), (uint32_t)at.answers & 1u);
@@ -1771,6 +1842,7 @@ Plan make_plan(const TokenParams &P) {
     p.dynamic = (Kd::Grad || log == 0) && P.entries <= INT32_MAX >> log;
     p.eager = vecs * 16 >> log <= p.slots * Kd::kChunkBytes;
     p.clusters = (int32_t)(p.dynamic ? P.entries : std::min<int64_t>(P.entries, std::max(1, room[log])));
+    while (((((p.slice_vecs + Kd::kChunkVecs - 1) / Kd::kChunkVecs) + (1 << p.group_log) - 1) >> p.group_log) > kGroupRows) ++p.group_log;
     p.words_at = p.slots * Kd::kChunkBytes + fixed;
     p.smem = p.words_at + words;
     return p;
