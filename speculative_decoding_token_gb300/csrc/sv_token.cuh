@@ -44,8 +44,9 @@ constexpr int kDepth = 4;                         // rows between the scout and 
 constexpr int kTopDepth = 2;                      // the same where top tokens are asked for (their buffers are large)
 constexpr int kMaxCluster = 16;
 constexpr int kGroupRows = 20;                    // groups of a thread's vectors in a slice whose maxima are kept
-constexpr int kKept = 512;                        // groups that may hold top tokens
-constexpr int kKeys = 1024;                       // tokens among them
+constexpr int kMine = 256, kKept = 512;           // groups that may hold top tokens, a warp's and all
+constexpr unsigned kLost = 1u << 24;
+constexpr int kKeys = 512;                        // tokens among them
 constexpr int kGathered = 256;                    // keys that a cluster's CTAs send to its first
 constexpr int kHash = 1024;
 
@@ -90,9 +91,9 @@ struct Part {
 
 struct Shared {
     uint64_t full[kMaxSlots], ready[kMaxSlots], empty[kMaxSlots];
-    // of a row: known; done with; all known of its entry; its copies issued; the CTA's sums there; of a gradient: what the
-    // second reading needs, all stored
-    uint64_t row_full[kDepth], row_free[kDepth], scouted[kDepth], sent[kDepth], summed[kDepth], known[kDepth], stored[kDepth];
+    // of a row: known; done with; all known of its entry; its copies issued; the CTA's sums there, its bounds (top
+    // tokens); of a gradient: what the second reading needs, all stored
+    uint64_t row_full[kDepth], row_free[kDepth], scouted[kDepth], sent[kDepth], summed[kDepth], bounded[kDepth], known[kDepth], stored[kDepth];
     uint64_t gathered, granted, acked;
     uint4 grant;          // the answer to a request for another row
     Row row[kDepth];
@@ -107,11 +108,13 @@ struct Shared {
 // Top tokens: a key is a logit's bits, made to order as it does, over its
 // token's, inverted: keys fall in the order of alternatives, and 0 is none.
 struct SharedTop {
-    uint16_t most[kTopDepth][kGroupRows][kTeam];  // upper halves of the order bits of the groups' maxima
-    uint32_t bound[kTopDepth][kConsumers];        // that many of the warp's tokens are at least so large
-    uint16_t kept[kTopDepth][kKept];
+    uint16_t most[kTopDepth][kGroupRows][kTeam];  // the groups' maxima, upper halves of their bits
+    uint32_t bound[kTopDepth][kConsumers];        // the order bits of a number that enough of the warp's tokens reach
+    uint16_t mine[kConsumers][kMine];             // groups of a warp's share that may hold top tokens
+    uint16_t kept[kTopDepth][kKept];              // and of all of them, where that was not enough
     unsigned long long keys[kTopDepth][kKeys];
     unsigned long long gathered[kGathered];
+    unsigned found[kTopDepth];                    // keys; kLost and more: not all of them
 };
 
 // Lists of kDepth rows, `stride` entries each, in shared memory.
@@ -471,9 +474,6 @@ __device__ bool receive(const TokenParams &P, Shared &S, const Cta &cta, int liv
     return true;
 }
 
-// ---------------------------------------------------------------------------
-// consumers
-
 // The logits of the row's ragged end, which no copy brings, with -inf behind them.
 template <class Kd>
 __device__ __forceinline__ uint4 ragged_end(const char *row, int whole, int rest) {
@@ -492,6 +492,352 @@ __device__ __forceinline__ uint4 ragged_end(const char *row, int whole, int rest
     }
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
+
+// ---------------------------------------------------------------------------
+// top tokens
+
+// Sorts 32 N keys, the largest first; element 32 q + i is x[q] of lane i (a bitonic network, rolled up: it runs once a row, and
+// its instructions would not stay in the cache).
+template <int N>
+__device__ __forceinline__ void sort_keys(unsigned long long (&x)[N], int lane) {
+#pragma unroll 1
+    for (int k = 2; k <= 32 * N; k <<= 1) {
+#pragma unroll 1
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            if (j < 32) {
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, x[q], j);
+                    const bool larger = (((32 * q + lane) & k) == 0) == ((lane & j) == 0);
+                    x[q] = larger ? max(x[q], o) : min(x[q], o);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int step = 1; step < N; step <<= 1) {
+                if (j != 32 * step) continue;
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    if (q & step) continue;
+                    const bool falls = ((32 * q) & k) == 0;
+                    const unsigned long long a = max(x[q], x[q ^ step]), b = min(x[q], x[q ^ step]);
+                    x[q] = falls ? a : b;
+                    x[q ^ step] = falls ? b : a;
+                }
+            }
+        }
+    }
+}
+
+// The first k of n keys, in order, to the start of them (0 where there are no more); n <= kKeys, k <= 32 N.
+template <int N>
+__device__ __forceinline__ void sort_front(unsigned long long *keys, int n, int k, int lane) {
+    unsigned long long x[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] = 32 * q + lane < n ? keys[32 * q + lane] : 0;
+    sort_keys<N>(x, lane);
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (32 * q + lane < k) keys[32 * q + lane] = x[q];
+    __syncwarp();
+}
+
+__device__ __noinline__ void first_keys(unsigned long long *keys, int n, int k, int lane) {
+    if (n <= 64 && k <= 64) sort_front<2>(keys, n, k, lane);
+    else if (n <= 128) sort_front<4>(keys, n, k, lane);
+    else if (n <= 256) sort_front<8>(keys, n, k, lane);
+    else sort_front<kKeys / 32>(keys, n, k, lane);
+}
+
+// exclusive sums over the lanes, and the total
+__device__ __forceinline__ int lanes_before(int c, int lane, int &total) {
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    return incl - c;
+}
+
+__device__ __forceinline__ uint32_t gt_mask(uint32_t a, uint32_t b) {
+    return __hgt2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+}
+
+__device__ __forceinline__ uint32_t eq_mask(uint32_t a, uint32_t b) {
+    return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+}
+
+// What top tokens are chosen from. 8 warps have 8 nth >= k tokens no smaller than the least of their bounds. The bound's class
+// are the logits whose upper 16 bits are its own: one value of bf16, 2^-7 of a value of fp32. Tokens above the class are in
+// groups above it. Only if they are fewer than k, tokens of the class are needed, of bf16 those of the lowest indexes.
+template <int DT>
+struct Chooser {
+    static constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2);
+    using Kd = Kind<DT, false, false, true, true, false>;
+    const TokenParams &P;
+    const char *row;
+    const Cta &cta;
+    int log;
+    uint32_t bound2, high2;
+    float low, high;
+
+    __device__ __forceinline__ Chooser(const TokenParams &P_, const Plan &plan, const char *row_, const SharedTop &T, int d, const Cta &cta_)
+        : P(P_), row(row_), cta(cta_), log(plan.group_log) {
+        const float least = from_order_bits(__reduce_min_sync(0xffffffffu, cta.lane < kConsumers ? T.bound[d][cta.lane] : ~0u));
+        const uint32_t bound = __float_as_uint(least) >> 16;
+        bound2 = bound | bound << 16;
+        low = high = __uint_as_float(bound << 16);
+        if (DT == SV_DT_FP32 && fabsf(low) < INFINITY) {
+            const float far = __uint_as_float(bound << 16 | 0xffffu);
+            if (least < 0.0f) low = far;
+            else high = far;
+            if ((bound & 0x7fffu) == 0) {  // both zeros' classes are one
+                low = __uint_as_float(0x8000ffffu);
+                high = __uint_as_float(0x0000ffffu);
+            }
+        }
+        high2 = __float_as_uint(high) >> 16 | (__float_as_uint(high) & 0xffff0000u);
+    }
+
+    // Eight groups' maxima: bit 16 (i & 1) + i / 2 for group i above the class, or in it.
+    __device__ __forceinline__ uint32_t groups(const uint4 &w, bool equal) const {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        uint32_t in = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) in |= (equal ? eq_mask(x[q], bound2) : gt_mask(x[q], bound2)) & 0x00010001u << q;
+        return in;
+    }
+    static __device__ __forceinline__ int group_of(uint32_t in) {
+        const int bit = __ffs(in) - 1;
+        return 2 * (bit & 15) + (bit >> 4);
+    }
+
+    // Vector `part` of group g of the slice, -1 past its end.
+    __device__ __forceinline__ int vector(int g, int part) const {
+        const int v = (((g / kTeam) << log) + (part >> 2)) * Kd::kChunkVecs + (part & 3) * kTeam + g % kTeam;
+        return v < cta.slice_vecs ? cta.slice0 + v : -1;
+    }
+
+    __device__ __forceinline__ uint4 load(int v) const {
+        const int whole = P.V / kPer;
+        if (v >= 0 && v < whole) return __ldg(reinterpret_cast<const uint4 *>(row) + v);
+        if (v == whole) return ragged_end<Kd>(row, whole, P.V - whole * kPer);
+        return make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
+    }
+
+    // A vector's tokens above the class, or in it: bit u for token u.
+    __device__ __forceinline__ uint32_t tokens(const uint4 &w, int v, bool equal) const {
+        uint32_t in = 0;
+        if (DT == SV_DT_BF16) {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) in |= (equal ? eq_mask(x[q], high2) : gt_mask(x[q], high2)) & 0x00020001u << (2 * q);
+            in = (in | in >> 16) & 0xffu;
+        } else {
+            const float x[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) in |= (equal ? x[u] >= low && x[u] <= high : x[u] > high) ? 1u << u : 0u;
+        }
+        if (equal) {  // (what stands in for tokens that are not there is -inf)
+            if (v < 0) in = 0;
+            else if (P.V - v * kPer < kPer) in &= (1u << (P.V - v * kPer)) - 1u;
+        }
+        return in;
+    }
+
+    // Their keys, from keys[to] on, to keys[end] at most.
+    __device__ __forceinline__ void put(unsigned long long *keys, const uint4 &w, int v, uint32_t in, int to, int end) const {
+        for (; in; in &= in - 1, ++to) {
+            const int u = __ffs(in) - 1;
+            const uint32_t x = DT == SV_DT_FP32 ? (u == 0 ? w.x : u == 1 ? w.y : u == 2 ? w.z : w.w)
+                                                : (u < 2 ? w.x : u < 4 ? w.y : u < 6 ? w.z : w.w) >> (16 * (u & 1)) << 16;
+            if (to < end) keys[to] = order_key(__uint_as_float(x), v * kPer + u);
+        }
+    }
+
+    // Calls f(vectors, their indexes) over vector index(0) .. index(n - 1), four of a lane at a time, while it says so: read
+    // once more from memory (L2).
+    template <class Index, class F>
+    __device__ __forceinline__ void each(int n, Index &&index, F &&f) const {
+        for (int i = 0; i < n; i += 128) {
+            uint4 w[4];
+            int v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = i + 32 * q + cta.lane;
+                v[q] = j < n ? index(j) : -1;
+                w[q] = load(v[q]);
+            }
+            if (!f(w, v)) return;
+        }
+    }
+};
+
+// A consumer warp's share of a row's top tokens, once all warps have said their bounds: an eighth of the groups' maxima, and
+// the vectors of those above the bound's class read again (of a row of 152064 bf16 logits and k = 64, 115 of 4864 groups and
+// 460 vectors; one warp alone took 15 us for it, beside the next row's sums).
+template <int DT>
+__device__ __noinline__ void gather_top(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta cta,
+                                        int warp) {
+    const Chooser<DT> choose(P, plan, row, T, d, cta);
+    const int lane = cta.lane, log = plan.group_log;
+    const int pieces = ((cta.chunks + (1 << log) - 1) >> log) * (kTeam / 8);
+    uint16_t *mine = T.mine[warp];
+    int n = 0;
+    for (int i = warp * 32; i < pieces; i += kTeam) {
+        uint32_t in = 0;
+        if (i + lane < pieces) in = choose.groups(*reinterpret_cast<const uint4 *>(&T.most[d][0][(i + lane) * 8]), false);
+        int total, to = lanes_before(__popc(in), lane, total) + n;
+        for (; in; in &= in - 1, ++to)
+            if (to < kMine) mine[to] = (uint16_t)((i + lane) * 8 + choose.group_of(in));
+        n += total;
+    }
+    __syncwarp();
+    if (n > kMine) {
+        if (lane == 0) atomicAdd(&T.found[d], kLost);
+        return;
+    }
+    choose.each(n << (2 + log), [&](int j) { return choose.vector(mine[j >> (2 + log)], j & ((4 << log) - 1)); },
+                [&](const uint4 (&w)[4], const int (&v)[4]) {
+        uint32_t in[4];
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            in[q] = choose.tokens(w[q], v[q], false);
+            c += __popc(in[q]);
+        }
+        int total, to = lanes_before(c, lane, total);
+        if (total == 0) return true;
+        unsigned from = 0;
+        if (lane == 0) from = atomicAdd(&T.found[d], (unsigned)total);
+        to += (int)(__shfl_sync(0xffffffffu, from, 0) & (kLost - 1));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            choose.put(T.keys[d], w[q], v[q], in[q], to, kKeys);
+            to += __popc(in[q]);
+        }
+        return true;
+    });
+}
+
+// The rest of the choice where the class is needed, or too many tokens are above it: keys to T.keys[d], in any order, and how
+// many.
+template <int DT>
+__device__ __noinline__ int choose_more(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta cta,
+                                        unsigned found_) {
+    const Chooser<DT> choose(P, plan, row, T, d, cta);
+    constexpr int kPer = Chooser<DT>::kPer;
+    const int lane = cta.lane, k = P.k, log = plan.group_log;
+    const int rows = (cta.chunks + (1 << log) - 1) >> log;
+    unsigned long long *keys = T.keys[d];
+    auto slice = [&](int j) { return cta.slice0 + j; };
+    if (found_ < (unsigned)k) {
+        // Groups above the class and, chunk after chunk, those in it until there are enough (of fp32: all).
+        const int larger = (int)found_;
+        int found = larger, groups = 0, equal = 0;
+        for (int r = 0; r < rows; ++r) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][lane * 8]);
+            const bool more = DT == SV_DT_FP32 || equal < k - larger;
+            uint32_t in = choose.groups(w, false);
+            if (more) {
+                const uint32_t same = choose.groups(w, true);
+                equal += (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(same));
+                in |= same;
+            }
+            int total, to = lanes_before(__popc(in), lane, total) + groups;
+            for (; in; in &= in - 1, ++to)
+                if (to < kKept) T.kept[d][to] = (uint16_t)(r * kTeam + lane * 8 + choose.group_of(in));
+            groups += total;
+        }
+        __syncwarp();
+        bool ok = groups <= kKept;
+        if (ok)
+            choose.each(groups << (2 + log), [&](int j) { return choose.vector(T.kept[d][j >> (2 + log)], j & ((4 << log) - 1)); },
+                        [&](const uint4 (&w)[4], const int (&v)[4]) {
+                uint32_t in[4];
+                int c = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    in[q] = choose.tokens(w[q], v[q], true);
+                    c += __popc(in[q]);
+                }
+                int total, to = lanes_before(c, lane, total) + found;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    choose.put(keys, w[q], v[q], in[q], to, kKeys);
+                    to += __popc(in[q]);
+                }
+                found += total;
+                return found <= kKeys;
+            });
+        __syncwarp();
+        if (ok && found <= kKeys) return found;
+        if (DT == SV_DT_BF16) {
+            // the slice's first tokens that equal the bound, from its start
+            found = larger;
+            choose.each(cta.slice_vecs, slice, [&](const uint4 (&w)[4], const int (&v)[4]) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t in = choose.tokens(w[q], v[q], true);
+                    int total;
+                    const int to = lanes_before(__popc(in), lane, total) + found;
+                    choose.put(keys, w[q], v[q], in, to, k);
+                    found = min(k, found + total);
+                }
+                return found < k;
+            });
+            __syncwarp();
+            return found;
+        }
+    }
+    // Many tokens within a hair of the bound: the largest key that k of them reach, a bit at a time over the whole slice.
+    unsigned long long key = 0;
+    int found = 0;
+    for (int bit = 63; bit >= -1; --bit) {
+        const unsigned long long next = bit < 0 ? key : key | 1ull << bit;
+        int c = 0;
+        choose.each(cta.slice_vecs, slice, [&](const uint4 (&w)[4], const int (&v)[4]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x[kPer];
+                vec_floats<DT>(w[q], x);
+                uint32_t in = 0;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    if (v[q] >= 0 && v[q] * kPer + u < P.V && order_key(x[u], v[q] * kPer + u) >= next) in |= 1u << u;
+                if (bit >= 0) {
+                    c += __popc(in);
+                } else {
+                    int total;
+                    const int to = lanes_before(__popc(in), lane, total) + found;
+                    choose.put(keys, w[q], v[q], in, to, kKeys);
+                    found += total;
+                }
+            }
+            return true;
+        });
+        if (bit >= 0 && (int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= k) key = next;
+    }
+    __syncwarp();
+    return min(found, kKeys);
+}
+
+// The k best keys of the CTA's slice, in order, to the start of T.keys[d] (0 where there are none).
+template <int DT>
+__device__ __forceinline__ void select_top(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta) {
+    const unsigned found = *(volatile unsigned *)&T.found[d];
+    int n = (int)found;
+    if (found < (unsigned)P.k || found > (unsigned)kKeys) n = choose_more<DT>(P, plan, row, T, d, cta, found);
+    __syncwarp();
+    first_keys(T.keys[d], n, P.k, cta.lane);
+    if (cta.lane == 0) T.found[d] = 0;  // for the row after the next
+}
+
+// ---------------------------------------------------------------------------
+// consumers
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -674,7 +1020,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             // all that the top tokens need of a chunk (lists of the vectors that pass a rising bound took 70 instructions more)
             group = (i & ((1 << plan.group_log) - 1)) == 0 ? cm : fmaxf(group, cm);
             most = fmaxf(most, cm);
-            top->most[d][i >> plan.group_log][tid] = (uint16_t)(order_bits(group) >> 16);
+            top->most[d][i >> plan.group_log][tid] = (uint16_t)(__float_as_uint(group) >> 16);
         }
         if (plain(m)) {
             const f32x2 nR = pack2(-R, -R);
@@ -730,6 +1076,8 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         // large.
         const uint32_t nth = warp_nth(order_bits(most), (P.k + kConsumers - 1) / kConsumers, lane);
         if (lane == 0) top->bound[d][warp] = nth;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
     }
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
     if (Kd::Rank) before += counted<Kd::DT>(above);
@@ -740,6 +1088,10 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         p.s *= g;
     }
     p = warp_fold<Kd>(p, c);
+    if constexpr (Kd::Top) {
+        if (!wait_bar(S.bounded[d], row_parity, S, P)) return false;
+        gather_top<Kd::DT>(P, plan, S.row[d].z, *top, d, cta, warp);
+    }
     // (a list's or a token's logits are read before any CTA can overwrite the row)
     if (Kd::Grad && cta.cluster > 1 && !wait_bar(S.scouted[d], row_parity, S, P)) return false;
     if (cta.cluster > 1) send<Kd>(cta, cta.rank * kConsumers + warp, live, p);
@@ -857,6 +1209,7 @@ __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, 
         if (state == kLive) {
             if (!sum_slice<Kd>(P, plan, S, top, cta, d, cta.parity(r), live++, cur)) return;
         } else if (cta.lane == 0) {
+            if (Kd::Top) mbar_arrive(smem_u32(&S.bounded[d]));
             mbar_arrive(smem_u32(&S.summed[d]));
         }
         if (Kd::Grad && !store_slice<Kd>(P, plan, S, cta, d, cta.parity(r), cur)) return;
@@ -1223,261 +1576,6 @@ __device__ __forceinline__ void patch(const TokenParams &P, const Plan &plan, Sh
 // ---------------------------------------------------------------------------
 // epilogue
 
-// Sorts 32 N keys, the largest first; element 32 q + i is x[q] of lane i (a bitonic network, rolled up: it runs once a row, and
-// its instructions would not stay in the cache).
-template <int N>
-__device__ __forceinline__ void sort_keys(unsigned long long (&x)[N], int lane) {
-#pragma unroll 1
-    for (int k = 2; k <= 32 * N; k <<= 1) {
-#pragma unroll 1
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            if (j < 32) {
-#pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, x[q], j);
-                    const bool larger = (((32 * q + lane) & k) == 0) == ((lane & j) == 0);
-                    x[q] = larger ? max(x[q], o) : min(x[q], o);
-                }
-                continue;
-            }
-#pragma unroll
-            for (int step = 1; step < N; step <<= 1) {
-                if (j != 32 * step) continue;
-#pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    if (q & step) continue;
-                    const bool falls = ((32 * q) & k) == 0;
-                    const unsigned long long a = max(x[q], x[q ^ step]), b = min(x[q], x[q ^ step]);
-                    x[q] = falls ? a : b;
-                    x[q ^ step] = falls ? b : a;
-                }
-            }
-        }
-    }
-}
-
-// The first k of n keys, in order, to the start of them (0 where there are no more); n <= kKeys, k <= 32 N.
-template <int N>
-__device__ __forceinline__ void sort_front(unsigned long long *keys, int n, int k, int lane) {
-    unsigned long long x[N];
-#pragma unroll
-    for (int q = 0; q < N; ++q) x[q] = 32 * q + lane < n ? keys[32 * q + lane] : 0;
-    sort_keys<N>(x, lane);
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (32 * q + lane < k) keys[32 * q + lane] = x[q];
-    __syncwarp();
-}
-
-__device__ __noinline__ void first_keys(unsigned long long *keys, int n, int k, int lane) {
-    if (n <= 128) sort_front<4>(keys, n, k, lane);
-    else if (n <= 256) sort_front<8>(keys, n, k, lane);
-    else sort_front<32>(keys, n, k, lane);
-}
-
-// Calls f(vector, its index, whether there is one) over n vectors, index(i) the i-th, eight of a lane at a time: read once
-// more from memory (L2). The row's ragged end comes from its logits, with -inf behind them.
-template <int DT, class Index, class F>
-__device__ __forceinline__ void each_batch(const TokenParams &P, const char *row, int n, int lane, Index &&index, F &&f) {
-    using Kd = Kind<DT, false, false, true, true, false>;
-    const int whole = P.V / Kd::kPer, rest = P.V - whole * Kd::kPer;
-    const uint4 *z = reinterpret_cast<const uint4 *>(row);
-    for (int i = 0; i < n; i += 256) {
-        uint4 w[8];
-        int v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int j = i + 32 * q + lane;
-            v[q] = j < n ? index(j) : -1;
-            w[q] = make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
-            if (v[q] == whole) w[q] = ragged_end<Kd>(row, whole, rest);
-            else if (v[q] >= 0) w[q] = __ldg(z + v[q]);
-        }
-        if (!f(w, v, i)) return;
-    }
-}
-
-// The k best keys of the CTA's slice, in order, to the start of T.keys[d] (0 where there are none). One warp's work beside the
-// next row's sums (two warps take rows in turn): of a row of 152064 bf16 logits and k = 64 some 115 of 4864 groups reach the
-// bound, their 460 vectors are read again, and some 120 keys are sorted in registers.
-//
-// The bound's class are the logits whose order bits share its upper 16: one value of bf16, 2^-7 of a value of fp32. Tokens
-// above the class are in groups above it. Only if they are fewer than k, tokens of the class are needed, of bf16 those of the
-// lowest indexes: groups with one, chunk after chunk, until there are enough.
-template <int DT>
-__device__ __noinline__ void select_top(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta) {
-    constexpr uint32_t all = 0xffffffffu;
-    constexpr int kPer = 16 / (DT == SV_DT_FP32 ? 4 : 2), kPart = kTeam * 4;  // vectors of a chunk
-    const int lane = cta.lane, k = P.k, log = plan.group_log;
-    unsigned long long *keys = T.keys[d];
-    const int rows = (cta.chunks + (1 << log) - 1) >> log;
-    const uint32_t bound = __reduce_min_sync(all, lane < kConsumers ? T.bound[d][lane] : ~0u) >> 16;
-    const uint32_t bound2 = bound | bound << 16;
-    const float high = from_order_bits(bound << 16 | 0xffffu);
-    float low = from_order_bits(bound << 16);
-    if (low != low) low = -INFINITY;
-    // exclusive sums over the lanes
-    auto before = [&](int c, int &total) {
-        int incl = c;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(all, incl, off);
-            if (lane >= off) incl += y;
-        }
-        total = __shfl_sync(all, incl, 31);
-        return incl - c;
-    };
-    // groups of row r among the lane's eight: halves of words that are above the bound, or equal to it
-    auto above = [&](int r, bool equal, uint32_t (&m)[4]) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][lane * 8]);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        int c = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            m[q] = equal ? __vcmpeq2(x[q], bound2) : __vcmpgtu2(x[q], bound2);
-            c += __popc(m[q]);
-        }
-        return c >> 4;
-    };
-    auto keep = [&](int r, const uint32_t (&m)[4], int to) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (m[q >> 1] >> (16 * (q & 1)) & 1u) {
-                if (to < kKept) T.kept[d][to] = (uint16_t)(r * kTeam + lane * 8 + q);
-                ++to;
-            }
-    };
-    // vector j of the kept groups
-    auto kept = [&](int j) {
-        const int g = T.kept[d][j >> (2 + log)], part = j & ((4 << log) - 1);
-        const int v = (((g / kTeam) << log) + (part >> 2)) * kPart + (part & 3) * kTeam + g % kTeam;
-        return v < cta.slice_vecs ? cta.slice0 + v : -1;
-    };
-    // tokens of the first n kept vectors above the class, or in it, behind the `from` keys that are there; false: too many
-    auto collect = [&](int n, bool equal, int &from) {
-        bool fits = true;
-        each_batch<DT>(P, row, n, lane, kept, [&](const uint4 (&w)[8], const int (&v)[8], int) {
-            uint64_t in = 0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                float x[kPer];
-                vec_floats<DT>(w[q], x);
-#pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    if (v[q] >= 0 && v[q] * kPer + u < P.V && (equal ? x[u] >= low && x[u] <= high : x[u] > high))
-                        in |= 1ull << (8 * q + u);
-            }
-            int total, to = before(__popcll(in), total) + from;
-            from += total;
-            fits = from <= kKeys;
-            if (!fits) return false;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (!(in >> (8 * q) & 0xffu)) continue;
-                float x[kPer];
-                vec_floats<DT>(w[q], x);
-#pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    if (in >> (8 * q + u) & 1u) keys[to++] = order_key(x[u], v[q] * kPer + u);
-            }
-            return true;
-        });
-        __syncwarp();
-        return fits;
-    };
-
-    int groups = 0, found = 0;
-    {
-        int mine = 0;
-        uint32_t m[4];
-        for (int r = 0; r < rows; ++r) mine += above(r, false, m);
-        int to = before(mine, groups);
-        if (groups <= kKept)
-            for (int r = 0; r < rows; ++r) {
-                const int c = above(r, false, m);
-                if (c) keep(r, m, to);
-                to += c;
-            }
-    }
-    __syncwarp();
-    bool ok = groups <= kKept && collect(groups << (2 + log), false, found);
-    if (ok && found < k) {
-        int equal = 0;
-        for (int r = 0; r < rows && (DT == SV_DT_FP32 || equal < k - found); ++r) {
-            uint32_t m[4];
-            int total;
-            const int c = above(r, true, m), to = before(c, total) + groups + equal;
-            if (c) keep(r, m, to);
-            equal += total;
-        }
-        __syncwarp();
-        const int larger = found;
-        ok = groups + equal <= kKept && collect((groups + equal) << (2 + log), true, found);
-        if (!ok && DT == SV_DT_BF16) {
-            // the slice's first tokens that equal the bound, from its start
-            found = larger;
-            ok = true;
-            each_batch<DT>(P, row, cta.slice_vecs, lane, [&](int j) { return cta.slice0 + j; },
-                           [&](const uint4 (&w)[8], const int (&v)[8], int) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float x[kPer];
-                    vec_floats<DT>(w[q], x);
-                    uint32_t in = 0;
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u)
-                        if (v[q] >= 0 && v[q] * kPer + u < P.V && x[u] >= low && x[u] <= high) in |= 1u << u;
-                    int total, to = before(__popc(in), total) + found;
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u)
-                        if (in >> u & 1u) {
-                            if (to < k) keys[to] = order_key(x[u], v[q] * kPer + u);
-                            ++to;
-                        }
-                    found = min(k, found + total);
-                }
-                return found < k;
-            });
-            __syncwarp();
-        }
-    }
-    if (!ok) {
-        // Many tokens within a hair of the bound: the largest key that k of them reach, a bit at a time over the whole slice.
-        unsigned long long key = 0;
-        for (int bit = 63; bit >= -1; --bit) {
-            const unsigned long long next = bit < 0 ? key : key | 1ull << bit;
-            int c = 0;
-            found = 0;
-            each_batch<DT>(P, row, cta.slice_vecs, lane, [&](int j) { return cta.slice0 + j; },
-                           [&](const uint4 (&w)[8], const int (&v)[8], int) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float x[kPer];
-                    vec_floats<DT>(w[q], x);
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u) {
-                        const unsigned long long mine = order_key(x[u], v[q] * kPer + u);
-                        const bool in = v[q] >= 0 && v[q] * kPer + u < P.V && mine >= next;
-                        if (bit >= 0) {
-                            c += in ? 1 : 0;
-                        } else {
-                            const uint32_t who = __ballot_sync(all, in);
-                            if (in && found + __popc(who & ((1u << lane) - 1u)) < kKeys) keys[found + __popc(who & ((1u << lane) - 1u))] = mine;
-                            found += __popc(who);
-                        }
-                    }
-                }
-                return true;
-            });
-            if (bit >= 0 && (int)__reduce_add_sync(all, (unsigned)c) >= k) key = next;
-        }
-        found = min(found, kKeys);
-        __syncwarp();
-    }
-    first_keys(keys, found, k, lane);
-}
-
 template <int DT>
 __device__ __forceinline__ void write_top(const TokenParams &P, long long e, int i, unsigned long long key, float m, float lh, float ll) {
     float lp = -INFINITY, lo = 0.0f;
@@ -1771,12 +1869,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
             mbar_init(smem_u32(&S.known[i]), 1);
             mbar_init(smem_u32(&S.stored[i]), kConsumers);
             mbar_init(smem_u32(&S.scouted[i]), 1);
+            mbar_init(smem_u32(&S.bounded[i]), kConsumers);
         }
         mbar_init(smem_u32(&S.granted), 1);
         mbar_init(smem_u32(&S.acked), plan.cluster);
         mbar_init(smem_u32(&S.gathered), plan.cluster);
         S.asked = 0;
         S.abort = 0;
+        if (Kd::Top)
+            for (int i = 0; i < kTopDepth; ++i) top->found[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (Kd::List)
