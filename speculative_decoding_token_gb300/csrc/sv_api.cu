@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -216,6 +217,20 @@ int run_verify(specverify_ctx *h, const specverify_batch *in, bool sampling, flo
     return map_cuda(e);
 }
 
+// The kernels of the token log-probability and distillation calls, set up once a
+// device (they ask what fits it, which takes longer than the rest of a handle).
+cudaError_t prepare_token(int device) {
+    static std::mutex lock;
+    static std::vector<int> done;
+    std::lock_guard<std::mutex> hold(lock);
+    if (std::find(done.begin(), done.end(), device) != done.end()) return cudaSuccess;
+    cudaError_t e = sv::prepare_logprobs();
+    if (e == cudaSuccess) e = sv::prepare_logprobs_grad();
+    if (e == cudaSuccess) e = sv::prepare_distill();
+    if (e == cudaSuccess) done.push_back(device);
+    return e;
+}
+
 // Rows of logits of a token log-probability or distillation call; with a
 // gradient, its rows too.
 int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int64_t rows,
@@ -314,9 +329,7 @@ int specverify_create(specverify_t *out, int device, int32_t max_batch, int32_t 
     if (e == cudaSuccess) e = sv::prepare_features();
     if (e == cudaSuccess) e = sv::prepare_restricted();
     if (e == cudaSuccess) e = sv::prepare_small();
-    if (e == cudaSuccess) e = sv::prepare_logprobs();
-    if (e == cudaSuccess) e = sv::prepare_logprobs_grad();
-    if (e == cudaSuccess) e = sv::prepare_distill();
+    if (e == cudaSuccess) e = prepare_token(device);
     if (e != cudaSuccess) {
         delete h;
         return map_cuda(e);

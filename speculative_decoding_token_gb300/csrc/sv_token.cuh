@@ -47,7 +47,7 @@ constexpr int kGroupRows = 20;                    // groups of a thread's vector
 constexpr int kMine = 256, kKept = 512;           // groups that may hold top tokens, a warp's and all
 constexpr unsigned kLost = 1u << 24;
 constexpr int kKeys = 512;                        // tokens among them
-constexpr int kGathered = 256;                    // keys that a cluster's CTAs send to its first
+constexpr int kGathered = 128;                    // keys that a cluster's CTAs send to its first
 constexpr int kHash = 1024;
 
 enum State { kLive = 0, kSkip = 1, kBad = 2, kEnd = 3 };

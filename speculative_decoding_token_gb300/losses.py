@@ -25,7 +25,7 @@ MAX_ALTERNATIVES, MAX_LIST = 128, 256
 DIVERGENCES = {"fkl": 0, "rkl": 1, "jsd": 2, "tvd": 3}
 FORMS = {"logprobs": 0, "logits": 1}
 
-_DTYPES = {}  # filled by bind()
+_DTYPES, _lib, _check = {}, None, None  # filled by bind()
 
 
 class SpecverifyLists(ctypes.Structure):
@@ -47,8 +47,10 @@ class TokenLogprobs(NamedTuple):
 
 
 def bind(lib):
-    global torch
+    global torch, _lib, _check
     import torch
+    from . import _check
+    _lib = lib
     _DTYPES.update({torch.float32: FP32, torch.bfloat16: BF16})
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     rows = [vp, vp, i32, i64, i64, i64, f32]
@@ -79,18 +81,18 @@ def _one_of(name, x, among):
 class RowLosses:
     """The methods; the class that takes them has a handle ``h`` on CUDA device ``device``."""
 
-    def _call(self, name, *args):
-        from . import _check, load
-        _check(getattr(load(), name)(self.h, *args), name)
-
     def _rows(self, name, x):
         """Address, dtype, rows, V and row stride of logits or of their gradient."""
-        if x.dim() != 2 or x.dtype not in _DTYPES or x.get_device() != self.device or x.stride(1) != 1 and x.shape[1] != 1:
-            raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor with unit column stride on "
-                             f"cuda:{self.device}, not {x.dtype} {tuple(x.shape)} on {x.device}")
+        dt = _DTYPES.get(x.dtype)
+        if dt is None or x.dim() != 2 or x.get_device() != self.device:
+            raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor on cuda:{self.device}, not {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
         rows, V = x.shape
+        stride, one = x.stride()
+        if one != 1 and V != 1:
+            raise ValueError(f"{name} must have unit column stride")
         # a single row's stride says nothing; the library wants whole 16-byte pieces
-        return x.data_ptr(), _DTYPES[x.dtype], rows, V, x.stride(0) if rows > 1 else -(-V // 8) * 8
+        return x.data_ptr(), dt, rows, V, stride if rows > 1 else -(-V // 8) * 8
 
     def _raw(self, stream):
         return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
@@ -106,7 +108,7 @@ class RowLosses:
         if grad is None:
             rows, V = logits.shape
             grad = self._new(stream, (rows, -(-V // 8) * 8), logits.dtype)[:, :V]
-        elif grad.shape != logits.shape or grad.dtype != logits.dtype:
+        elif grad.shape != logits.shape or grad.dtype is not logits.dtype:
             raise ValueError("grad must have the logits' shape and dtype")
         at, _, _, _, stride = self._rows("grad", grad)
         return grad, at, stride
@@ -143,13 +145,15 @@ class RowLosses:
             raise ValueError("out must have buffers for the top tokens where k > 0, and only there")
         d, f32, i32 = self.device, torch.float32, torch.int32
         top = (*shape, k)
-        self._call(
-            "specverify_token_logprobs", at, dt, rows, V, stride, temperature, B, M, _array("tokens", tokens, d, shape, i32),
+        rc = _lib.specverify_token_logprobs(
+            self.h, at, dt, rows, V, stride, temperature, B, M, _array("tokens", tokens, d, shape, i32),
             _array("row_off", row_off, d, (B,), torch.int64), _array("path", path, d, shape, i32), k,
             _array("logprob", out.logprob, d, shape, f32), _array("entropy", out.entropy, d, shape, f32),
             _array("lse", out.lse, d, shape, f32), _array("rank", out.rank, d, shape, i32),
             _array("topk_logprob", out.topk_logprob, d, top, f32), _array("topk_idx", out.topk_idx, d, top, i32),
             self._raw(stream))
+        if rc:
+            _check(rc, "specverify_token_logprobs")
         return out
 
     def token_logprobs_grad(self, logits, tokens, grad_logprob, grad_entropy=None, temperature=1.0, *, grad=None,
@@ -162,21 +166,23 @@ class RowLosses:
         logprob = self._new(stream, (rows,)) if logprob is None else logprob
         entropy = self._new(stream, (rows,)) if entropy is None else entropy
         d, f32, one = self.device, torch.float32, (rows,)
-        self._call(
-            "specverify_token_logprobs_grad", at, dt, rows, V, stride, temperature,
+        rc = _lib.specverify_token_logprobs_grad(
+            self.h, at, dt, rows, V, stride, temperature,
             _array("tokens", tokens, d, one, torch.int32), _array("grad_logprob", grad_logprob, d, one, f32),
             _array("grad_entropy", grad_entropy, d, one, f32), gat, gstride, _array("logprob", logprob, d, one, f32),
             _array("entropy", entropy, d, one, f32), self._raw(stream))
+        if rc:
+            _check(rc, "specverify_token_logprobs_grad")
         return grad, logprob, entropy
 
-    def _lists(self, logits, ids, target, divergence, form, beta):
-        rows, d = logits.shape[0], self.device
-        if ids.dim() != 2 or not 1 <= ids.shape[1] <= MAX_LIST or target.dtype not in _DTYPES:
+    def _lists(self, rows, ids, target, divergence, form, beta):
+        shape, dt = ids.shape, _DTYPES.get(target.dtype)
+        if len(shape) != 2 or shape[0] != rows or not 1 <= shape[1] <= MAX_LIST or dt is None:
             raise ValueError(f"ids must be [rows, 1 to {MAX_LIST}], and target of its shape, float32 or bfloat16")
-        K = ids.shape[1]
         return ctypes.byref(SpecverifyLists(
-            K, _DTYPES[target.dtype], _one_of("form", form, FORMS), _one_of("divergence", divergence, DIVERGENCES), beta,
-            _array("ids", ids, d, (rows, K), torch.int32), _array("target", target, d, (rows, K), target.dtype)))
+            shape[1], dt, _one_of("form", form, FORMS), _one_of("divergence", divergence, DIVERGENCES), beta,
+            _array("ids", ids, self.device, shape, torch.int32),
+            _array("target", target, self.device, shape, target.dtype)))
 
     def distill_loss(self, draft, ids, target, temperature=1.0, divergence="fkl", *, form="logprobs", beta=0.5, loss=None,
                      stream=None):
@@ -188,9 +194,11 @@ class RowLosses:
         vocabulary's), or their logits (``form="logits"``: softmax over the list)."""
         at, dt, rows, V, stride = self._rows("draft", draft)
         loss = self._new(stream, (rows,)) if loss is None else loss
-        self._call("specverify_distill_loss", at, dt, rows, V, stride, temperature,
-                   self._lists(draft, ids, target, divergence, form, beta),
-                   _array("loss", loss, self.device, (rows,), torch.float32), self._raw(stream))
+        rc = _lib.specverify_distill_loss(
+            self.h, at, dt, rows, V, stride, temperature, self._lists(rows, ids, target, divergence, form, beta),
+            _array("loss", loss, self.device, (rows,), torch.float32), self._raw(stream))
+        if rc:
+            _check(rc, "specverify_distill_loss")
         return loss
 
     def distill_grad(self, draft, ids, target, weight=None, temperature=1.0, divergence="fkl", *, form="logprobs", beta=0.5,
@@ -201,7 +209,10 @@ class RowLosses:
         grad, gat, gstride = self._grad_rows(draft, grad, stream)
         loss = self._new(stream, (rows,)) if loss is None else loss
         d, one = self.device, (rows,)
-        self._call("specverify_distill_grad", at, dt, rows, V, stride, temperature,
-                   self._lists(draft, ids, target, divergence, form, beta), _array("weight", weight, d, one, torch.float32),
-                   gat, gstride, _array("loss", loss, d, one, torch.float32), self._raw(stream))
+        rc = _lib.specverify_distill_grad(
+            self.h, at, dt, rows, V, stride, temperature, self._lists(rows, ids, target, divergence, form, beta),
+            _array("weight", weight, d, one, torch.float32), gat, gstride, _array("loss", loss, d, one, torch.float32),
+            self._raw(stream))
+        if rc:
+            _check(rc, "specverify_distill_grad")
         return grad, loss
