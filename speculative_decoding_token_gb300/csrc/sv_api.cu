@@ -254,7 +254,6 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     p.status = h->base.status;
     p.wait_ns = h->wait_ns;
     p.entries = rows;
-    p.M = 1;
     return SPECVERIFY_OK;
 }
 
@@ -648,6 +647,7 @@ int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype,
         return SPECVERIFY_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
+    p.B = B;
     p.M = M;
     p.tokens = tokens;
     p.row_off = row_off;

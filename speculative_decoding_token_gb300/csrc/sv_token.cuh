@@ -1280,6 +1280,7 @@ struct Entries {
 
 // What is fetched of an entry ahead of its turn.
 struct Asked {
+    long long entry;
     int y;
     int64_t row;
     float g, h;
@@ -1299,9 +1300,16 @@ __device__ __forceinline__ void fetch(const TokenParams &P, long long e, int lan
         }
         a.g = P.weight ? P.weight[e] : 1.0f;
     } else {
-        a.y = P.tokens[e];
+        a.entry = e;
         a.row = e;
-        if (P.row_off) a.row = P.row_off[e / P.M] + (P.path ? (int64_t)P.path[e] : (int64_t)(e % P.M));
+        if (P.row_off) {
+            // first tokens first: the ends of short sequences, which ask for nothing, come together at the end (in the
+            // sequences' order a CTA met several of them, 1.7 us each, before its first row)
+            const int b = (int)(e % P.B), m = (int)(e / P.B);
+            a.entry = (long long)b * P.M + m;
+            a.row = P.row_off[b] + (P.path ? P.path[a.entry] : m);
+        }
+        a.y = P.tokens[a.entry];
         if (P.grad) {
             a.g = P.g_logprob[e];
             a.h = P.g_entropy ? P.g_entropy[e] : 0.0f;
@@ -1310,14 +1318,14 @@ __device__ __forceinline__ void fetch(const TokenParams &P, long long e, int lan
 }
 
 // What a row is: one lane's work.
-__device__ __forceinline__ void scout_row(const TokenParams &P, Row &row, long long e, const Asked &a) {
+__device__ __forceinline__ void scout_row(const TokenParams &P, Row &row, const Asked &a) {
     int bits = 0;
     if (a.y != -1) {
         if (a.y < 0 || a.y >= P.V) bits = SPECVERIFY_STATUS_BAD_TOKEN;
         else if (a.row < 0 || a.row >= P.rows) bits = SPECVERIFY_STATUS_BAD_ROW;
     }
     row.z = P.logits + a.row * P.stride_bytes;
-    row.entry = e;
+    row.entry = a.entry;
     row.y = a.y;
     row.state = a.y == -1 ? kSkip : bits ? kBad : kLive;
     row.g = a.g;
@@ -1463,7 +1471,7 @@ __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Sh
         } else if (Kd::List) {
             scout_ids(P, S.row[d], list, d, at.e, cta.lane, a);
         } else if (cta.lane == 0) {
-            scout_row(P, S.row[d], at.e, a);
+            scout_row(P, S.row[d], a);
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_full[d]));

@@ -23,7 +23,7 @@ struct TokenParams {
     uint64_t wait_ns;    // bound of a wait inside the kernel
     // entries: rows with a token (log-probabilities) or with a list (distillation)
     int64_t entries;
-    int32_t M;           // entries of a sequence (log-probabilities)
+    int32_t B, M;        // sequences, and entries of one (log-probabilities)
     const int32_t *tokens;
     const int64_t *row_off;
     const int32_t *path;
