@@ -42,6 +42,10 @@ constexpr int kTeam = kConsumers * 32;            // a thread takes every kTeam-
 constexpr int kMaxSlots = 26;
 constexpr int kDepth = 4;                         // rows between the scout and the epilogue at most
 constexpr int kTopDepth = 2;                      // the same where top tokens are asked for (their buffers are large)
+// Chunks that a row has left to copy when the next is asked for: 2 to 5 us pass until that one's first copy. Gradients of
+// 512 rows of 256000 fp32 logits: 197 us for none, 184 for two; rows of 152064 bf16: 200, 199 and, for five, 206 (the sooner a
+// row is taken the worse the rows are balanced).
+constexpr int kLead = 2;
 constexpr int kMaxCluster = 16;
 constexpr int kGroupRows = 20;                    // groups of a thread's vectors in a slice whose maxima are kept
 constexpr int kMine = 256, kKept = 512;           // groups that may hold top tokens, a warp's and all
@@ -302,10 +306,9 @@ constexpr float kPlain = 0x1p90f;
 
 __device__ __forceinline__ bool plain(float m) { return fabsf(m) < kPlain; }
 
-// A thread's reference m is its warp's maximum in the first chunk, and moves when a logit is this many binades above it: the
-// sums are good whatever m is, and moving it for every new maximum costs 30 instructions in nearly every chunk (one of 32
-// lanes has a new maximum). What entropies lose by it is 8 2^-24.
-constexpr float kLag = 8.0f;
+// A thread's reference m is its warp's maximum in the first chunk, and moves when a logit is 8 binades above it
+// (TokenParams::lag): the sums are good whatever m is, and moving it for every new maximum costs 30 instructions in nearly
+// every chunk (one of 32 lanes has a new maximum). What entropies lose by it is 8 2^-24.
 
 __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
     a.n = a.n < 0 || b.n < 0 ? -1 : a.n + b.n;
@@ -869,6 +872,23 @@ __device__ __forceinline__ float from_packed_max(uint32_t x) {
     return DT == SV_DT_FP32 ? __uint_as_float(x) : max_nan(bf16_lo(x), bf16_hi(x));
 }
 
+// The largest logit that leaves a reference m where it is (bf16: a pair of it); of one that is no plain number, itself.
+template <int DT>
+__device__ __forceinline__ uint32_t packed_limit(float m, float lag) {
+    const float x = plain(m) ? m + lag : m;
+    if (DT == SV_DT_FP32) return __float_as_uint(x);
+    // toward zero or not, within 2^-7 of it
+    const uint32_t b = __float_as_uint(x) >> 16;
+    return b | b << 16;
+}
+
+// Whether any of them is larger, or no number.
+template <int DT>
+__device__ __forceinline__ bool beyond(uint32_t all, uint32_t limit) {
+    if (DT == SV_DT_FP32) return !(__uint_as_float(all) <= __uint_as_float(limit));
+    return !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&all), *reinterpret_cast<const __nv_bfloat162 *>(&limit));
+}
+
 // Word i of a vector, or pair i of fp32 logits, as two floats; with the entropy, no less than kFar.
 template <class Kd>
 __device__ __forceinline__ f32x2 logits2(const uint4 &w, int i) {
@@ -942,7 +962,8 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                                           uint32_t row_parity, int live, Cursor &cur) {
     constexpr int kVecs = Kd::kVecs, kPer = Kd::kPer;
     const int tid = threadIdx.x, lane = cta.lane, warp = tid >> 5;
-    float m = -INFINITY, R = -INFINITY, most = -INFINITY, group = -INFINITY;
+    float m = -INFINITY, R = -INFINITY;
+    uint32_t most = Kd::kNegInf, group = Kd::kNegInf, limit = 0;
     f32x2 s0 = 0ull, s1 = 0ull, t0 = 0ull, t1 = 0ull;
     bool bad = false;
     int before = 0;
@@ -986,41 +1007,42 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         __syncwarp();
         if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
         cur.step(plan);
-        uint32_t pm[kVecs], all = 0;
+        uint32_t all = packed_max<Kd::DT>(w[0]);
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            pm[j] = packed_max<Kd::DT>(w[j]);
-            all = j == 0 ? pm[0] : packed_max<Kd::DT>(all, pm[j]);
-        }
-        float cm = from_packed_max<Kd::DT>(all);
-        const bool stays = plain(m) ? fmaf(cm, c, -R) <= kLag : cm <= m;
-        if (!stays && !(cm < INFINITY)) {
-            bad = true;
-            cm = -INFINITY;
-        }
-        if (i == 0) {
-            m = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(cm)));
-            R = m == -INFINITY ? -INFINITY : m * c;
-        } else if (!stays && cm != -INFINITY) {
-            const float next = cm * c;
-            if (m != -INFINITY) {
-                const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
-                const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
-                if (Kd::Ent) {
-                    t0 = mul2(f2, fma2(x2, s0, t0));
-                    t1 = mul2(f2, fma2(x2, s1, t1));
-                }
-                s0 = mul2(f2, s0);
-                s1 = mul2(f2, s1);
+        for (int j = 1; j < kVecs; ++j) all = packed_max<Kd::DT>(all, packed_max<Kd::DT>(w[j]));
+        if (i == 0 || beyond<Kd::DT>(all, limit)) {
+            float cm = from_packed_max<Kd::DT>(all);
+            if (!(cm < INFINITY)) {
+                bad = true;
+                cm = -INFINITY;
+                all = Kd::kNegInf;
             }
-            m = cm;
-            R = next;
+            if (i == 0) {
+                m = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(cm)));
+                R = m == -INFINITY ? -INFINITY : m * c;
+            } else if (cm > m) {
+                const float next = cm * c;
+                if (m != -INFINITY) {
+                    const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
+                    const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
+                    if (Kd::Ent) {
+                        t0 = mul2(f2, fma2(x2, s0, t0));
+                        t1 = mul2(f2, fma2(x2, s1, t1));
+                    }
+                    s0 = mul2(f2, s0);
+                    s1 = mul2(f2, s1);
+                }
+                m = cm;
+                R = next;
+            }
+            limit = packed_limit<Kd::DT>(m, P.lag);
         }
         if (Kd::Top) {
             // all that the top tokens need of a chunk (lists of the vectors that pass a rising bound took 70 instructions more)
-            group = (i & ((1 << plan.group_log) - 1)) == 0 ? cm : fmaxf(group, cm);
-            most = fmaxf(most, cm);
-            top->most[d][i >> plan.group_log][tid] = (uint16_t)(__float_as_uint(group) >> 16);
+            group = (i & ((1 << plan.group_log) - 1)) == 0 ? all : packed_max<Kd::DT>(group, all);
+            most = i == 0 ? all : packed_max<Kd::DT>(most, all);
+            top->most[d][i >> plan.group_log][tid] =
+                (uint16_t)((Kd::DT == SV_DT_FP32 ? group : max_bf16x2(group, group << 16)) >> 16);
         }
         if (plain(m)) {
             const f32x2 nR = pack2(-R, -R);
@@ -1074,7 +1096,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     if (Kd::Top) {
         // Each warp bounds the k-th largest logit by the nth largest of its lanes' maxima: 8 warps have 8 nth >= k tokens that
         // large.
-        const uint32_t nth = warp_nth(order_bits(most), (P.k + kConsumers - 1) / kConsumers, lane);
+        const uint32_t nth = warp_nth(order_bits(from_packed_max<Kd::DT>(most)), (P.k + kConsumers - 1) / kConsumers, lane);
         if (lane == 0) top->bound[d][warp] = nth;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&S.bounded[d]));
@@ -1507,8 +1529,7 @@ __device__ __forceinline__ void produce(const TokenParams &P, const Plan &plan, 
         if (!ok || S.row[d].state == kEnd) break;
         const char *z = S.row[d].z;
         const int n = S.row[d].state != kLive ? 0 : Kd::Grad ? 2 * cta.chunks : cta.chunks;
-        // (a list takes the scout some five microseconds to its publication, a token two)
-        const int ask = n == 0 ? -1 : Kd::List ? max(0, n - 1 - plan.slots) : n - 1;
+        const int ask = n == 0 ? -1 : max(0, n - 1 - kLead);
         for (int j = 0; j < n; ++j) {
             ok = wait_at(cta.empty + 8 * cur.slot, cur.phase ^ 1u, S, P);
             if (!ok) break;
@@ -1920,7 +1941,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
 // host
 
 constexpr int kHalfSmem = 113 * 1024;  // of a CTA, two on an SM
-constexpr int64_t kRereadBytes = 80 << 20;
+constexpr int64_t kRereadBytes = 48 << 20;
 
 // What fits the GPU of a kernel: clusters of 2^i CTAs at once.
 template <class Kd>
