@@ -48,13 +48,15 @@ def parse():
     ap.add_argument("--batches", type=int, default=2, choices=[1, 2],
                     help="alternating input batches (2 keeps consecutive steps off L2)")
     ap.add_argument("--mode", default="sampling",
-                    choices=["sampling", "greedy", "lossy", "restricted", "stats", "features", "tree"],
+                    choices=["sampling", "greedy", "lossy", "restricted", "stats", "features", "tree", "distill"],
                     help="sampling verify (default), the greedy exact-match verify, the lossy "
                          "verify (f_sq lenience, eps 0.5), the restricted verify (top-k 20, "
                          "top-p 0.95 per sequence), or the row diagnostics: per-position "
                          "acceptance statistics (beta, TVD) or draft features (entropy, top-10), or "
                          "a step of drafted token trees over a paged cache (attention, greedy "
-                         "verify, commit, weight accumulation, eviction)")
+                         "verify, commit, weight accumulation, eviction), or a distillation step of "
+                         "the draft's rows (the target's 64 best tokens of every row, the forward "
+                         "divergence from them and its gradient)")
     ap.add_argument("--config", type=int, default=BENCH_CFG, choices=[0, 1, 2, 3, 4],
                     help="workload (default: the ragged B=256 bf16 batch; the others serve "
                          "profiling and the per-workload table)")
@@ -581,6 +583,80 @@ def run_tree(args, rank, world, local):
     print(json.dumps(line), flush=True)
 
 
+DISTILL_K = 64
+
+
+def run_distill(args, rank, world, local):
+    """Times a distillation step on the workload's draft rows: the target's DISTILL_K best tokens of each position, the
+    forward divergence of the draft's rows from them and its gradient; together and each by itself."""
+    import torch
+
+    import speculative_decoding_token_gb300 as sv
+    from speculative_decoding_token_gb300 import workload
+
+    sv.build()
+    cfg = workload.CONFIGS[args.config]
+    batch = workload.make_batch(args.config, device="cuda", seed=cfg["seed"] + 100 * rank)
+    h = sv.SpecVerify(1, 1, cfg["V"])
+    draft = batch.draft
+    rows = draft.shape[0]
+    gamma = batch.gamma.tolist()
+    # the target's rows of the drafted positions: every row of a sequence but its last
+    at = torch.cat([torch.arange(g) + off for g, off in zip(gamma, batch.p_row_off.tolist())]).cuda()
+    target = torch.empty(rows, draft.stride(0), dtype=draft.dtype, device="cuda")[:, :cfg["V"]]
+    target.copy_(batch.target[at])
+    drafted = torch.cat([batch.draft_tokens[b, :g] for b, g in enumerate(gamma)]).contiguous()
+    top = h.token_logprobs_buffers(rows, k=DISTILL_K)
+    weight = torch.full((rows,), 1.0 / rows, device="cuda")
+    grad, loss = torch.empty_strided(draft.shape, draft.stride(), dtype=draft.dtype, device="cuda"), torch.empty(rows, device="cuda")
+
+    def alternatives():
+        h.token_logprobs(target, drafted, cfg["T"], k=DISTILL_K, out=top)
+
+    def gradient():
+        h.distill_grad(draft, top.topk_idx, top.topk_logprob, weight, cfg["T"], "fkl", grad=grad, loss=loss)
+
+    calls = (alternatives, gradient)
+
+    def timed(which, steps):
+        start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        start.record()
+        for _ in range(steps):
+            for call in which:
+                call()
+        stop.record()
+        torch.cuda.synchronize()
+        return start.elapsed_time(stop)
+
+    timed(calls, max(args.warmup, 3))
+    barrier(world)
+    with ClockSampler(local) as clocks:
+        time.sleep(0.25)
+        ms = timed(calls, args.steps)
+        time.sleep(0.05)
+    barrier(world)
+    ms = max_over_ranks(ms, world)
+    each = {call.__name__: timed((call,), args.steps) / args.steps for call in calls}
+    status = h.device_status()
+    h.close()
+    if rank != 0:
+        return
+    logits = rows * cfg["V"] * draft.element_size()
+    peak, peak_kind = peaks()
+    gbs = 2 * logits / (each["gradient"] / 1e3) / 1e9
+    line = {"metric": "distilled draft positions/s", "value": world * rows * args.steps / (ms / 1e3), "unit": "positions/s",
+            "n_gpus": world, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms / args.steps,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": cfg["dtype"], "data": "synthetic",
+            "config": {**workload_config(cfg, batch, "sampling"), "mode": "distill", "positions": rows,
+                       "l2": "inputs larger than L2: %.2f GB of logits each" % (logits / 1e9), "listed_tokens": DISTILL_K, "divergence": "fkl"},
+            "roofline": {"bound": "hbm", "kernel": "token_kernel (gradient)", "achieved": gbs, "peak": peak,
+                         "peak_kind": peak_kind, "unit": "GB/s", "frac": gbs / peak, "traffic": None,
+                         "algorithmic_bytes": "the draft's logits once, their gradient once"},
+            "ms_per_call_alone": each, "clocks": clocks.summary(), "gpu_launches": 2 * args.steps, "device_status": status}
+    print(json.dumps(line), flush=True)
+
+
 def run_native(args, rank, world, local):
     import torch
 
@@ -784,6 +860,8 @@ def main():
             run_diagnostics(args, rank, world, local)
         elif args.mode == "restricted":
             run_restricted(args, rank, world, local)
+        elif args.mode == "distill":
+            run_distill(args, rank, world, local)
         elif args.mode == "tree":
             run_tree(args, rank, world, local)
         else:

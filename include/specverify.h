@@ -366,7 +366,10 @@ int specverify_get_timing(specverify_t h, int kernel, double *total_ms, int64_t 
 
 /* Bound, in nanoseconds of GPU wall time, on every wait of specverify_verify's
  * fused kernel for another warp (a position's chunk partials, an idle task
- * loop); 0 restores the default of about two seconds. A wait that runs out
+ * loop), and of the token log-probability and distillation kernels for a warp,
+ * a CTA or a copy; 0 restores the default of about two seconds. There a wait that
+ * runs out ends its call early with SPECVERIFY_STATUS_TIMEOUT and its outputs
+ * undefined. In specverify_verify one that runs out
  * sets SPECVERIFY_STATUS_TIMEOUT, every other wait of that call then returns
  * at once, and the kernel returns with the sequences it had not decided left
  * at n_accepted[b] = -1 (tokens -1). A warp's waits on its own bulk copies

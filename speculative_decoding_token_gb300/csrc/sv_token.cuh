@@ -1251,7 +1251,7 @@ __device__ __forceinline__ void consume(const TokenParams &P, const Plan &plan, 
 // them, and the next is asked for when they all have read it.
 struct Entries {
     long long e;
-    int answers;
+    int answers, awaited;
 
     // e < 0 after the last one; false: gave up
     __device__ __forceinline__ bool next(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta) {
@@ -1279,6 +1279,7 @@ struct Entries {
             }
         }
         if (cta.lane == 0) mbar_arrive_expect_tx(smem_u32(&S.granted), 16);
+        ++awaited;
         if (!wait_bar(S.granted, (uint32_t)answers & 1u, S, P)) return false;
         ++answers;
         uint32_t more, x;
@@ -1920,7 +1921,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     if (plan.cluster > 1) cluster_sync();
     after_previous();
 
-    Entries at{cta.first, 0};
+    Entries at{cta.first, 0, 0};
     if (warp < kConsumers) consume<Kd>(P, plan, S, top, cta);
     else if (warp == kScout) scout<Kd>(P, plan, S, list, cta, at);
     else if (warp == kProducer) produce<Kd>(P, plan, S, cta);
@@ -1935,7 +1936,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     if (warp == kScout) {
         int asked;
         asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(asked) : "r"(cluster_addr(&S.asked, 0)) : "memory");
-        if (asked > at.answers && S.abort) mbar_wait_bounded(smem_u32(&S.granted), (uint32_t)at.answers & 1u);
+        if (asked > at.answers) {
+            if (asked > at.awaited && cta.lane == 0) mbar_arrive_expect_tx(smem_u32(&S.granted), 16);
+            mbar_wait_bounded(smem_u32(&S.granted), (uint32_t)at.answers & 1u);
+        }
     }
     if (plan.cluster > 1) cluster_sync();
 }

@@ -586,3 +586,37 @@ def test_exploring_gradients_by_differences(h):
         assert ((moved[0][0] - moved[1][0]) / (2 * step) - grad[:, v]).abs().max() <= lim
         assert ((moved[0][1] - moved[1][1]) / (2 * step) - dgrad[:, v]).abs().max() <= lim
     clean(h)
+
+
+# ---------------------------------------------------------------------------
+# waits that run out
+
+@pytest.mark.parametrize("rows", [3, 60], ids=["clusters", "rows"])
+def test_waits_that_run_out(svm, rows):
+    """With a limit of a nanosecond a call gives up at the first wait that lasts a microsecond, and says so; the next call,
+    with the default limit, is right. (Not every call has such a wait every time.)"""
+    h = svm.SpecVerify(1, 1, 1000)
+    z, y, ids, t = inputs(31, rows=rows, V=50001)
+    one = torch.ones(rows, device="cuda")
+    cold, late = torch.zeros(1 << 26, device="cuda"), 0  # more than L2 holds
+    for run in (lambda: [x for x in h.token_logprobs(z, y, rank=True) if x is not None],
+                lambda: [x for x in h.token_logprobs(z, y, k=9) if x is not None],
+                lambda: h.token_logprobs_grad(z, y, one, one), lambda: [h.distill_loss(z, ids, t)],
+                lambda: h.distill_grad(z, ids, t)):
+        want = [x.clone() for x in run()]
+        clean(h)
+        for _ in range(20):
+            cold.add_(1)
+            h.set_wait_limit(1)
+            run()
+            status = h.device_status()
+            assert status in (0, svm.STATUS_BITS["timeout"])
+            h.set_wait_limit(0)
+            got = run()
+            clean(h)
+            assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(want, got))
+            late += status != 0
+            if status:
+                break
+    assert late
+    h.close()
