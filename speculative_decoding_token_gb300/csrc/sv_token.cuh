@@ -1007,9 +1007,6 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                 else w[j] = load_vec(at + j * kTeam * 16);
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
-        cur.step(plan);
         uint32_t all = packed_max<Kd::DT>(w[0]);
 #pragma unroll
         for (int j = 1; j < kVecs; ++j) all = packed_max<Kd::DT>(all, packed_max<Kd::DT>(w[j]));
@@ -1040,6 +1037,12 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             }
             limit = packed_limit<Kd::DT>(m, P.lag);
         }
+        // The slot is free. Not before the branch above has used all that was loaded: an arrival overtakes loads of shared memory
+        // that are queued (behind a gradient's stores), and the slot's next copy with them. (Seen: in gradients of fp32 rows, warps'
+        // shares of a chunk from the copy after. A proxy fence instead costs up to 2.5 us of 195.)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
+        cur.step(plan);
         if (Kd::Top) {
             // all that the top tokens need of a chunk (lists of the vectors that pass a rising bound took 70 instructions more)
             group = (i & ((1 << plan.group_log) - 1)) == 0 ? all : packed_max<Kd::DT>(group, all);
@@ -1174,8 +1177,6 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
             uint4 w[kVecs];
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) w[j] = load_vec(at + j * kTeam * 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
                 f32x2 g[kPer / 2];
@@ -1183,6 +1184,8 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
                 for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(fma2(logits2<Kd>(w[j], q), c2, nR));
                 to[j * kTeam] = packed(g);
             }
+            __syncwarp();  // (after the stores, which have used the loads: see sum_slice)
+            if (lane == 0) mbar_arrive(cta.empty + 8 * cur.slot);
         } else {
             const int whole = P.V / kPer, rest = P.V - whole * kPer;
 #pragma unroll 1

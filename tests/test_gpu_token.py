@@ -588,6 +588,30 @@ def test_exploring_gradients_by_differences(h):
     clean(h)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,kind", [(64000, "rkl"), (256000, "fkl"), (262144, "jsd"), (128000, "tvd")])
+def test_gradients_under_load_repeat(h, dtype, V, kind):
+    """Rows enough to keep the memory busy: every element is the same in every run, and right."""
+    rows, K = 200, 128
+    z = torch.randn(rows, V, device="cuda").mul_(2).to(dtype)
+    v, i = z.float().topk(K, 1)
+    ids, t = i.to(torch.int32), v - z.float().logsumexp(1, keepdim=True) - 0.01
+    y, one = ids[:, 5].contiguous(), torch.ones(rows, device="cuda")
+    first = None
+    for _ in range(5):
+        got = (*h.distill_grad(z, ids, t, divergence=kind), *h.token_logprobs_grad(z, y, one, one))
+        if first is None:
+            first = [x.clone() for x in got]
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
+    clean(h)
+    for r in range(0, rows, 9):
+        d = tu.Divergence(z[r], ids[r], t[r], 1.0, kind)
+        assert tu.close(first[0][r], d.grad, d.grad_err, dtype) and tu.close(first[1][r], d.loss, d.loss_err)
+        want, err = tu.Soft(z[r], 1.0).grad(int(y[r]), 1.0, 1.0)
+        assert tu.close(first[2][r], want, err, dtype)
+
+
 # ---------------------------------------------------------------------------
 # waits that run out
 
