@@ -880,8 +880,8 @@ template <int DT>
 __device__ __forceinline__ uint32_t packed_limit(float m, float lag) {
     const float x = plain(m) ? m + lag : m;
     if (DT == SV_DT_FP32) return __float_as_uint(x);
-    // toward zero or not, within 2^-7 of it
-    const uint32_t b = __float_as_uint(x) >> 16;
+    // rounded down: a step of bf16 can be hundreds of binades of weight
+    const uint32_t b = (__float_as_uint(x) >> 16) + (x < 0.0f && (__float_as_uint(x) & 0xffffu) ? 1u : 0u);
     return b | b << 16;
 }
 

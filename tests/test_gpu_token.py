@@ -613,6 +613,53 @@ def test_gradients_under_load_repeat(h, dtype, V, kind):
 
 
 # ---------------------------------------------------------------------------
+# far from zero: logits whose neighbours in the type are many binades of weight apart, and whose products with log2(e) / T
+# are rounded by as much
+
+def steps(dtype, base, step, V=20001, rising=False):
+    """Rows of base + j step: j = 0 in a row's first half and 0 or 1, or 0 to 7, behind it; or rising."""
+    g = torch.Generator().manual_seed(77)
+    j = torch.randint(0, 8, (3, V), generator=g).double()
+    j[0] = j[0].clamp(max=1)
+    j[:2, : V // 2] = 0
+    if rising:
+        j = torch.sort(torch.randint(0, 160, (3, V), generator=g).double(), 1)[0]
+    x = base + j * step
+    z = x.to(dtype)
+    assert torch.equal(z.double(), x)  # the type has them all
+    return torch.nn.functional.pad(z, (0, -V % 8)).cuda()[:, :V]
+
+
+BF16_LAG = [(-32768.0, 128.0, 1.0), (-100.0, 0.5, 2.0 ** -7), (-100.0, 0.5, 0.25), (-1.0, 2.0 ** -8, 2.0 ** -20)]
+
+
+def check_far(h, z, T):
+    y = torch.tensor([7, z.shape[1] - 1, z.shape[1] // 2], dtype=torch.int32, device="cuda")
+    for rows in (3, 180):
+        many = torch.as_strided(z, (3, z.stride(0)), (z.stride(0), 1)).repeat(rows // 3, 1)[:, : z.shape[1]]
+        for k in (0, 20):
+            r = h.token_logprobs(many, y.repeat(rows // 3), T, k=k, rank=True)
+            clean(h)
+            for i in (0, 1, 2, rows - 1):
+                check_entry(z[i % 3], T, int(y[i % 3]), r, i, k)
+        g, e = torch.tensor([1.0, -0.5, 2.0], device="cuda"), torch.tensor([0.5, 1.0, -1.0], device="cuda")
+        grad, _, _ = h.token_logprobs_grad(many, y.repeat(rows // 3), g.repeat(rows // 3), e.repeat(rows // 3), T)
+        clean(h)
+        for i in (0, 1, 2, rows - 1):
+            want, err = tu.Soft(z[i % 3], T).grad(int(y[i % 3]), float(g[i % 3]), float(e[i % 3]))
+            assert tu.close(grad[i], want, err, z.dtype), i
+    ids, t = tu.lists(z, 9, 3, T=T)
+    for kind in ("fkl", "jsd", "tvd"):
+        check_distill(h, z, ids, t, T, kind, "logprobs")
+
+
+@pytest.mark.parametrize("base,step,T", BF16_LAG)
+def test_bf16_rows_below_zero(h, base, step, T):
+    """Negative logits a step of the type above what came before them."""
+    check_far(h, steps(BF, base, step), T)
+
+
+# ---------------------------------------------------------------------------
 # waits that run out
 
 @pytest.mark.parametrize("rows", [3, 60], ids=["clusters", "rows"])
