@@ -250,6 +250,7 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     p.V = (int32_t)V;
     p.c = (float)(1.4426950408889634073599 / (double)T);
     p.lag = 8.0f / p.c;
+    p.near = 0x1p24f / p.c;
     p.inv_hi = (float)(1.0 / (double)T);
     p.inv_lo = (float)(1.0 / (double)T - (double)p.inv_hi);
     p.status = h->base.status;

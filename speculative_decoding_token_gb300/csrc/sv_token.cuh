@@ -301,12 +301,15 @@ __device__ __forceinline__ float warp_max(float x) {
 // and its product with the exponent is 0 and not NaN.
 constexpr float kFar = -0x1p100f;
 constexpr uint32_t kFarBf16x2 = 0xf180f180u;
-// Rows of a larger maximum than this, either way, take exponents (z - m) c, with
-// the difference first; the others z c - R with R = m c rounded: one FMA, whose
-// product is exact, and what R's rounding shifts is made good in the sum.
-constexpr float kPlain = 0x1p90f;
+// Of a reference nearer to zero than this, exponents are z c - R with R = m c rounded: one FMA, whose product is exact. |R| <
+// 2^24, so that R is off by a half at most, and that is made good in the sum. Others take (z - m) c, with the difference first.
+__device__ __forceinline__ bool plain(const TokenParams &P, float m) { return fabsf(m) < P.near; }
 
-__device__ __forceinline__ bool plain(float m) { return fabsf(m) < kPlain; }
+// R (rounded: no sum takes the product exactly)
+__device__ __forceinline__ float scaled(const TokenParams &P, float m) { return __fmul_rn(m, P.c); }
+
+// What m c is more than the R that is taken of it.
+__device__ __forceinline__ float off_by(const TokenParams &P, float m) { return plain(P, m) ? fmaf(m, P.c, -scaled(P, m)) : 0.0f; }
 
 // A thread's reference m is its warp's maximum in the first chunk, and moves when a logit is 8 binades above it
 // (TokenParams::lag): the sums are good whatever m is, and moving it for every new maximum costs 30 instructions in nearly
@@ -877,8 +880,8 @@ __device__ __forceinline__ float from_packed_max(uint32_t x) {
 
 // The largest logit that leaves a reference m where it is (bf16: a pair of it); of one that is no plain number, itself.
 template <int DT>
-__device__ __forceinline__ uint32_t packed_limit(float m, float lag) {
-    const float x = plain(m) ? m + lag : m;
+__device__ __forceinline__ uint32_t packed_limit(const TokenParams &P, float m) {
+    const float x = plain(P, m) ? m + P.lag : m;
     if (DT == SV_DT_FP32) return __float_as_uint(x);
     // rounded down: a step of bf16 can be hundreds of binades of weight
     const uint32_t b = (__float_as_uint(x) >> 16) + (x < 0.0f && (__float_as_uint(x) & 0xffffu) ? 1u : 0u);
@@ -1019,11 +1022,12 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             }
             if (i == 0) {
                 m = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(cm)));
-                R = m == -INFINITY ? -INFINITY : m * c;
+                R = m == -INFINITY ? -INFINITY : scaled(P, m);
             } else if (cm > m) {
-                const float next = cm * c;
+                const float next = scaled(P, cm);
                 if (m != -INFINITY) {
-                    const float x = plain(m) && plain(cm) ? R - next : fmaxf(m - cm, kFar) * c, f = ex2_approx(x);
+                    const float x = plain(P, m) && plain(P, cm) ? R - next : fmaxf(m - cm, kFar) * c - off_by(P, m) + off_by(P, cm);
+                    const float f = ex2_approx(x);
                     const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
                     if (Kd::Ent) {
                         t0 = mul2(f2, fma2(x2, s0, t0));
@@ -1035,7 +1039,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                 m = cm;
                 R = next;
             }
-            limit = packed_limit<Kd::DT>(m, P.lag);
+            limit = packed_limit<Kd::DT>(P, m);
         }
         // The slot is free. Not before the branch above has used all that was loaded: an arrival overtakes loads of shared memory
         // that are queued (behind a gradient's stores), and the slot's next copy with them. (Seen: in gradients of fp32 rows, warps'
@@ -1050,7 +1054,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             top->most[d][i >> plan.group_log][tid] =
                 (uint16_t)((Kd::DT == SV_DT_FP32 ? group : max_bf16x2(group, group << 16)) >> 16);
         }
-        if (plain(m)) {
+        if (plain(P, m)) {
             const f32x2 nR = pack2(-R, -R);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
@@ -1110,7 +1114,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
     if (Kd::Rank) before += counted<Kd::DT>(above);
     Part p{m, (a.x + a.y) + (b.x + b.y), (e.x + e.y) + (f.x + f.y), bad ? -1 : before};
-    if (plain(m)) {  // what R was off by
+    if (plain(P, m)) {  // what R was off by
         const float r = fmaf(m, c, -R), g = ex2_approx(-r);
         p.t = g * fmaf(-r, p.s, p.t);
         p.s *= g;
@@ -1145,8 +1149,8 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
         fa = cf.y;
         fb = cf.z;
     }
-    const float c = P.c, R = m * c;
-    const bool near = plain(m);
+    const float c = P.c, R = scaled(P, m);
+    const bool near = plain(P, m);
     if (near) {
         const float r = fmaf(m, c, -R), g = ex2_approx(-r);
         fa = g * fmaf(-r, fb, fa);

@@ -659,6 +659,25 @@ def test_bf16_rows_below_zero(h, base, step, T):
     check_far(h, steps(BF, base, step), T)
 
 
+# T = 1: |z| log2(e) = 2^24 between 11629080 and 11629081
+FAR = [(BF, 2.0 ** 100, 2.0 ** 93, 1.0), (BF, -2.0 ** 40, 2.0 ** 33, 2.0 ** 20), (BF, -2.0 ** 40, 2.0 ** 32, 1.0),
+       (FP, 2.0 ** 40, 2.0 ** 17, 1.0), (FP, -2.0 ** 40, 2.0 ** 16, 2.0 ** 12), (FP, -2.0 ** 60, 2.0 ** 36, 2.0 ** 20),
+       (FP, 2.0 ** 127, 2.0 ** 104, 1.0), (FP, -2.0 ** 127, 2.0 ** 103, 2.0 ** 20), (FP, -1.0, 2.0 ** -24, 2.0 ** -20),
+       (FP, 0.0, 2.0 ** -149, 1.0), (BF, 0.0, 2.0 ** -133, 1.0), (FP, 0.0, 2.0 ** -149, 2.0 ** -20),
+       (FP, 20000.0, 2.0 ** -9, 2.0 ** -10)]
+RISING = [(11629000.0, 1.0, 1.0), (-11629160.0, 1.0, 1.0), (11629000.0, 1.0, 1.5), (-2.0 ** 24, 1.0, 1.0)]
+
+
+@pytest.mark.parametrize("dtype,base,step,T", FAR)
+def test_rows_far_from_zero(h, dtype, base, step, T):
+    check_far(h, steps(dtype, base, step), T)
+
+
+@pytest.mark.parametrize("base,step,T", RISING)
+def test_rows_that_rise_far_from_zero(h, base, step, T):
+    check_far(h, steps(FP, base, step, rising=True), T)
+
+
 # ---------------------------------------------------------------------------
 # waits that run out
 
