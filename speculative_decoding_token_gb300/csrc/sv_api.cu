@@ -251,6 +251,11 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     p.c = (float)(1.4426950408889634073599 / (double)T);
     p.lag = 8.0f / p.c;
     p.near = 0x1p24f / p.c;
+    const float far = -0x1p25f / p.c;
+    uint32_t bits;
+    std::memcpy(&bits, &far, 4);
+    bits &= 0xffff0000u;
+    std::memcpy(&p.far, &bits, 4);
     p.inv_hi = (float)(1.0 / (double)T);
     p.inv_lo = (float)(1.0 / (double)T - (double)p.inv_hi);
     p.status = h->base.status;

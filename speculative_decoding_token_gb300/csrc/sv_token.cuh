@@ -297,10 +297,9 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
-// Logits are told from -inf down to here: a weight of 0 either way (T >= 2^-20),
-// and its product with the exponent is 0 and not NaN.
-constexpr float kFar = -0x1p100f;
-constexpr uint32_t kFarBf16x2 = 0xf180f180u;
+// Logits, and differences of them, are told from -inf down to P.far, -2^25 / c: of no weight either way (with |R| < 2^24), and
+// a weight's product with its exponent is 0 and not NaN, also with an entropy's factor between them (below 2^100).
+
 // Of a reference nearer to zero than this, exponents are z c - R with R = m c rounded: one FMA, whose product is exact. |R| <
 // 2^24, so that R is off by a half at most, and that is made good in the sum. Others take (z - m) c, with the difference first.
 __device__ __forceinline__ bool plain(const TokenParams &P, float m) { return fabsf(m) < P.near; }
@@ -315,7 +314,14 @@ __device__ __forceinline__ float off_by(const TokenParams &P, float m) { return 
 // (TokenParams::lag): the sums are good whatever m is, and moving it for every new maximum costs 30 instructions in nearly
 // every chunk (one of 32 lanes has a new maximum). What entropies lose by it is 8 2^-24.
 
-__device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
+// P.far as logits2 takes it
+template <int DT>
+__device__ __forceinline__ uint32_t far_bits(const TokenParams &P) {
+    const uint32_t b = __float_as_uint(P.far);
+    return DT == SV_DT_FP32 ? b : b | b >> 16;
+}
+
+__device__ __forceinline__ void merge(const TokenParams &P, Part &a, const Part &b) {
     a.n = a.n < 0 || b.n < 0 ? -1 : a.n + b.n;
     if (b.m == -INFINITY) return;
     if (a.m == -INFINITY) {
@@ -325,7 +331,7 @@ __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
         return;
     }
     const float m = fmaxf(a.m, b.m);
-    const float xa = fmaxf(a.m - m, kFar) * c, xb = fmaxf(b.m - m, kFar) * c;
+    const float xa = fmaxf(a.m - m, P.far) * P.c, xb = fmaxf(b.m - m, P.far) * P.c;
     const float fa = ex2_approx(xa), fb = ex2_approx(xb);
     a.t = fa * fmaf(xa, a.s, a.t) + fb * fmaf(xb, b.s, b.t);
     a.s = fa * a.s + fb * b.s;
@@ -334,11 +340,11 @@ __device__ __forceinline__ void merge(Part &a, const Part &b, float c) {
 
 // The warp's lanes' sums in one, in every lane.
 template <class Kd>
-__device__ __forceinline__ Part warp_fold(Part a, float c) {
+__device__ __forceinline__ Part warp_fold(const TokenParams &P, Part a) {
     constexpr uint32_t all = 0xffffffffu;
     Part r;
     r.m = from_order_bits(__reduce_max_sync(all, order_bits(a.m)));
-    const float x = fmaxf(a.m - r.m, kFar) * c, f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
+    const float x = fmaxf(a.m - r.m, P.far) * P.c, f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
     r.s = f * a.s;
     r.t = Kd::Ent && f > 0.0f ? f * fmaf(x, a.s, a.t) : 0.0f;
 #pragma unroll
@@ -475,10 +481,10 @@ __device__ bool receive(const TokenParams &P, Shared &S, const Cta &cta, int liv
                 q.s = 0.0f;
                 q.n = -1;
             }
-            merge(p, q, P.c);
+            merge(P, p, q);
         }
     }
-    p = warp_fold<Kd>(p, P.c);
+    p = warp_fold<Kd>(P, p);
     return true;
 }
 
@@ -895,27 +901,27 @@ __device__ __forceinline__ bool beyond(uint32_t all, uint32_t limit) {
     return !__hble2(*reinterpret_cast<const __nv_bfloat162 *>(&all), *reinterpret_cast<const __nv_bfloat162 *>(&limit));
 }
 
-// Word i of a vector, or pair i of fp32 logits, as two floats; with the entropy, no less than kFar.
+// Word i of a vector, or pair i of fp32 logits, as two floats; with the entropy, no less than far (bf16: a pair of it).
 template <class Kd>
-__device__ __forceinline__ f32x2 logits2(const uint4 &w, int i) {
+__device__ __forceinline__ f32x2 logits2(const uint4 &w, int i, uint32_t far) {
     if (Kd::DT == SV_DT_FP32) {
         float lo = __uint_as_float(i == 0 ? w.x : w.z), hi = __uint_as_float(i == 0 ? w.y : w.w);
         if (Kd::Ent) {
-            lo = fmaxf(lo, kFar);
-            hi = fmaxf(hi, kFar);
+            lo = fmaxf(lo, __uint_as_float(far));
+            hi = fmaxf(hi, __uint_as_float(far));
         }
         return pack2(lo, hi);
     }
     uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-    if (Kd::Ent) x = max_bf16x2(x, kFarBf16x2);
+    if (Kd::Ent) x = max_bf16x2(x, far);
     return pack2(bf16_lo(x), bf16_hi(x));
 }
 
 // The exponents of pair i where the row's maximum is not a plain number.
 template <class Kd>
-__device__ __forceinline__ f32x2 far_exponents2(const uint4 &w, int i, float m, float c) {
+__device__ __forceinline__ f32x2 far_exponents2(const TokenParams &P, const uint4 &w, int i, float m) {
     const float2 z = pair_of<Kd::DT>(w, i);
-    return pack2(fmaxf(z.x - m, kFar) * c, fmaxf(z.y - m, kFar) * c);
+    return pack2(fmaxf(z.x - m, P.far) * P.c, fmaxf(z.y - m, P.far) * P.c);
 }
 
 // Tokens of a vector before the given one (logit zy, token y): those larger, and equal ones of a lower index. first: the
@@ -990,7 +996,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     }
     const float c = P.c;
     const f32x2 c2 = pack2(c, c);
-    const uint32_t mine = cta.ring + tid * 16;
+    const uint32_t far = far_bits<Kd::DT>(P), mine = cta.ring + tid * 16;
     for (int i = 0; i < cta.chunks; ++i) {
         if (!wait_at(cta.full + 8 * cur.slot, cur.phase, S, P)) return false;
         if (Kd::List && !wait_at(cta.ready + 8 * cur.slot, cur.phase, S, P)) return false;
@@ -1026,7 +1032,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             } else if (cm > m) {
                 const float next = scaled(P, cm);
                 if (m != -INFINITY) {
-                    const float x = plain(P, m) && plain(P, cm) ? R - next : fmaxf(m - cm, kFar) * c - off_by(P, m) + off_by(P, cm);
+                    const float x = plain(P, m) && plain(P, cm) ? R - next : fmaxf(m - cm, P.far) * c - off_by(P, m) + off_by(P, cm);
                     const float f = ex2_approx(x);
                     const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
                     if (Kd::Ent) {
@@ -1060,7 +1066,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             for (int j = 0; j < kVecs; ++j)
 #pragma unroll
                 for (int q = 0; q < kPer / 2; ++q) {
-                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q), c2, nR);
+                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q, far), c2, nR);
                     const float2 x = unpack2(x2);
                     const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
                     if (q & 1) {
@@ -1077,7 +1083,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                 const uint4 v = j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3];
 #pragma unroll
                 for (int q = 0; q < kPer / 2; ++q) {
-                    const f32x2 x2 = far_exponents2<Kd>(v, q, m, c);
+                    const f32x2 x2 = far_exponents2<Kd>(P, v, q, m);
                     const float2 x = unpack2(x2);
                     const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
                     s0 = add2(s0, e2);
@@ -1119,7 +1125,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         p.t = g * fmaf(-r, p.s, p.t);
         p.s *= g;
     }
-    p = warp_fold<Kd>(p, c);
+    p = warp_fold<Kd>(P, p);
     if constexpr (Kd::Top) {
         if (!wait_bar(S.bounded[d], row_parity, S, P)) return false;
         gather_top<Kd::DT>(P, plan, S.row[d].z, *top, d, cta, warp);
@@ -1168,7 +1174,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
         const float2 z = unpack2(g[2 % (kPer / 2)]), u = unpack2(g[3 % (kPer / 2)]);
         return make_uint4(to_bf16x2(x.x, x.y), to_bf16x2(y.x, y.y), to_bf16x2(z.x, z.y), to_bf16x2(u.x, u.y));
     };
-    const uint32_t mine = cta.ring + tid * 16;
+    const uint32_t far = far_bits<Kd::DT>(P), mine = cta.ring + tid * 16;
     for (int i = cta.chunks - 1; i >= 0; --i) {
         uint32_t at = mine;
         if (state == kLive) {
@@ -1185,7 +1191,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
             for (int j = 0; j < kVecs; ++j) {
                 f32x2 g[kPer / 2];
 #pragma unroll
-                for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(fma2(logits2<Kd>(w[j], q), c2, nR));
+                for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(fma2(logits2<Kd>(w[j], q, far), c2, nR));
                 to[j * kTeam] = packed(g);
             }
             __syncwarp();  // (after the stores, which have used the loads: see sum_slice)
@@ -1202,7 +1208,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
                     const uint4 w = end ? ragged_end<Kd>(S.row[d].z, whole, rest) : load_vec(at + j * kTeam * 16);
 #pragma unroll
                     for (int q = 0; q < kPer / 2; ++q)
-                        g[q] = weigh(near ? fma2(logits2<Kd>(w, q), c2, nR) : far_exponents2<Kd>(w, q, m, c));
+                        g[q] = weigh(near ? fma2(logits2<Kd>(w, q, far), c2, nR) : far_exponents2<Kd>(P, w, q, m));
                 } else {
 #pragma unroll
                     for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
@@ -1472,7 +1478,7 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
         }
         if (zmax > -INFINITY)
             for (int j = lane; j < P.K; j += 32) {
-                const float dz = fmaxf(lz[j] - zmax, kFar), w = ex2_approx(dz * P.c);
+                const float dz = fmaxf(lz[j] - zmax, P.far), w = ex2_approx(dz * P.c);
                 zsum += w;
                 if (w > 0.0f && P.divergence == SPECVERIFY_RKL) cross += w * (dz * P.inv_hi - llp[j]);
             }
@@ -1742,8 +1748,8 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
     if (row.state == kLive && bad && !row.bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
     float loss = bad ? NAN : 0.0f, C = 0.0f, Z = 0.0f;
     if (good) {
-        if (row.zmax > -INFINITY) Z = row.zsum * ex2_approx(fmaxf(row.zmax - M, kFar) * P.c);
-        if (some) Z = fmaf(p.s, ex2_approx(fmaxf(p.m - M, kFar) * P.c), Z);
+        if (row.zmax > -INFINITY) Z = row.zsum * ex2_approx(fmaxf(row.zmax - M, P.far) * P.c);
+        if (some) Z = fmaf(p.s, ex2_approx(fmaxf(p.m - M, P.far) * P.c), Z);
     }
     // the others' share of a gradient, (h_rest - q_rest C) / (s T) times 2^((z - m) c)
     auto known = [&](float h_rest, float q_rest) {
@@ -1757,7 +1763,7 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
     if (Kd::Grad && early) {
         // Here sum h is known without a look at the list: -sum p, and sum q ln(q / p) by the scout's sums. The stores need
         // not wait for the divergence (2.5 us for a list of 128).
-        const float q_rest = good && some ? p.s * ex2_approx(fmaxf(p.m - M, kFar) * P.c) / Z : 0.0f;
+        const float q_rest = good && some ? p.s * ex2_approx(fmaxf(p.m - M, P.far) * P.c) / Z : 0.0f;
         float h_rest = -row.p_rest;
         C = -(row.p_sum + row.p_rest);
         if (good && kind == SPECVERIFY_RKL) {
@@ -1765,7 +1771,7 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
             h_rest = q_rest > 0.0f ? q_rest * (logf(q_rest) - logf(fmaxf(row.p_rest, 0x1p-20f))) : 0.0f;
             C = h_rest;
             if (row.zmax > -INFINITY) {
-                const float dz = fmaxf(row.zmax - M, kFar), w = ex2_approx(dz * P.c) / Z;
+                const float dz = fmaxf(row.zmax - M, P.far), w = ex2_approx(dz * P.c) / Z;
                 if (w > 0.0f) C += w * fmaf(row.zsum, dz * P.inv_hi - ln_z, row.cross);
             }
         }
@@ -1844,7 +1850,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, S
             if (!receive<Kd>(P, S, cta, live++, p)) return;
         } else if (state == kLive) {
             if (cta.lane < kConsumers) p = S.part[d][cta.lane];
-            p = warp_fold<Kd>(p, P.c);
+            p = warp_fold<Kd>(P, p);
         }
         if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
         else if (!finish_token<Kd>(P, plan, S, T, cta, d, p)) return;

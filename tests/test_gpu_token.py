@@ -678,6 +678,28 @@ def test_rows_that_rise_far_from_zero(h, base, step, T):
     check_far(h, steps(FP, base, step, rising=True), T)
 
 
+@pytest.mark.parametrize("T", [2.0 ** -20, 0.01, 1.0, 2.0 ** 20])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_exploring_gradients_of_masked_rows_at_every_temperature(h, dtype, T):
+    """Large weights of the entropy, masked tokens, cold rows: nothing times nothing's logarithm stays nothing."""
+    V = 9001
+    z = tu.logits(3, V, dtype, 5, "plain", device="cuda")
+    z *= min(T, 1.0)
+    z[:, ::3], z[:, 1::3] = -math.inf, tu.LOWEST[dtype]
+    y = torch.tensor([0, 2, 8], dtype=torch.int32, device="cuda")
+    g, e = torch.tensor([1.0, 0.0, 2.0 ** 16], device="cuda"), torch.tensor([2.0 ** 16, -1.0, 2.0 ** 30], device="cuda")
+    for rows in (3, 180):
+        many = torch.as_strided(z, (3, z.stride(0)), (z.stride(0), 1)).repeat(rows // 3, 1)[:, :V]
+        grad, lp, H = h.token_logprobs_grad(many, y.repeat(rows // 3), g.repeat(rows // 3), e.repeat(rows // 3), T)
+        clean(h)
+        for i in (0, 1, 2, rows - 1):
+            s = tu.Soft(z[i % 3], T)
+            at = int(y[i % 3])
+            assert tu.close(lp[i], s.lp[at], s.lp_err(s.lp[at])) and tu.close(H[i], s.entropy, s.entropy_err())
+            want, err = s.grad(at, float(g[i % 3]), float(e[i % 3]))
+            assert tu.close(grad[i], want, err, dtype), i
+
+
 # ---------------------------------------------------------------------------
 # waits that run out
 
