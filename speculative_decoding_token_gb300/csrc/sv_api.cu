@@ -231,10 +231,10 @@ cudaError_t prepare_token(int device) {
     return e;
 }
 
-// Rows of logits of a token log-probability or distillation call; with a
-// gradient, its rows too.
+// Rows of logits of a token log-probability or distillation call; fine: with
+// log2(e) / T in two floats, the second positive (times -inf it is no NaN).
 int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int64_t rows,
-                 int64_t V, int64_t row_stride, float T, sv::TokenParams &p) {
+                 int64_t V, int64_t row_stride, float T, bool fine, sv::TokenParams &p) {
     if (!h || rows < 0 || rows > (int64_t)1 << 40 || V < 1 || V > INT32_MAX)
         return SPECVERIFY_ERR_INVALID_ARG;
     if (dtype != SPECVERIFY_FP32 && dtype != SPECVERIFY_BF16) return SPECVERIFY_ERR_INVALID_ARG;
@@ -248,7 +248,12 @@ int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int
     p.stride_bytes = row_stride * esz;
     p.rows = rows;
     p.V = (int32_t)V;
-    p.c = (float)(1.4426950408889634073599 / (double)T);
+    const double c = 1.4426950408889634073599 / (double)T;
+    p.c = (float)c;
+    if (fine) {
+        if (p.c >= c) p.c = std::nextafterf(p.c, 0.0f);
+        p.c_lo = (float)(c - p.c);
+    }
     p.lag = 8.0f / p.c;
     p.near = 0x1p24f / p.c;
     const float far = -0x1p25f / p.c;
@@ -644,7 +649,7 @@ int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype,
                               float *lse, int32_t *rank, float *topk_logprob, int32_t *topk_idx,
                               void *cuda_stream) {
     sv::TokenParams p;
-    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, false, p);
     if (rc != SPECVERIFY_OK) return rc;
     if (B < 0 || M < 0 || k < 0 || k > SPECVERIFY_MAX_ALTERNATIVES || (path && !row_off))
         return SPECVERIFY_ERR_INVALID_ARG;
@@ -675,7 +680,7 @@ int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t d
                                    const float *grad_entropy, void *grad, int64_t grad_stride,
                                    float *logprob, float *entropy, void *cuda_stream) {
     sv::TokenParams p;
-    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, false, p);
     if (rc != SPECVERIFY_OK || rows == 0) return rc;
     if (!tokens || !grad_logprob) return SPECVERIFY_ERR_INVALID_ARG;
     rc = grad_params(p, dtype, grad, grad_stride);
@@ -698,7 +703,7 @@ int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, i
                             int64_t V, int64_t row_stride, float temperature,
                             const specverify_lists *lists, float *loss, void *cuda_stream) {
     sv::TokenParams p;
-    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, true, p);
     if (rc == SPECVERIFY_OK) rc = list_params(p, lists);
     if (rc != SPECVERIFY_OK || rows == 0) return rc;
     if (!loss) return SPECVERIFY_ERR_INVALID_ARG;
@@ -713,7 +718,7 @@ int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, i
                             const specverify_lists *lists, const float *weight, void *grad,
                             int64_t grad_stride, float *loss, void *cuda_stream) {
     sv::TokenParams p;
-    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, p);
+    int rc = token_params(h, logits, dtype, rows, V, row_stride, temperature, true, p);
     if (rc == SPECVERIFY_OK) rc = list_params(p, lists);
     if (rc != SPECVERIFY_OK || rows == 0) return rc;
     if (!loss) return SPECVERIFY_ERR_INVALID_ARG;

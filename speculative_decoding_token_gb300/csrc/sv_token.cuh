@@ -81,9 +81,11 @@ struct Row {
     int y;
     int bad;       // what was found wrong with its list
     float zy;
-    float p_rest, p_sum;  // of a list: what it leaves of one, what it has
-    float zmax, zsum;     // of a list: the draft's largest logit, and the sum of 2^((z - zmax) c)
-    float cross;          // and (RKL) of 2^((z - zmax) c) ((z - zmax) / T - ln p)
+    // of a list: what it leaves of one, the logarithm, and what all of p is more than one
+    float p_rest, p_rest_l, rest_h, rest_l, over;
+    // the draft's largest logit z of it and (RKL) its p and ln p, the sum of e^((z_k - z) / T), and (RKL) of that times (z_k - z) / T -
+    // (ln p_k - ln p)
+    float zmax, p0, p0_l, lp0, zsum, zsum_l, cross;
     float g, h;    // what the gradient is multiplied by
 };
 
@@ -282,6 +284,30 @@ __device__ __forceinline__ void ff_exp_near(float v, float &h, float &l) {
     l *= scale;
 }
 
+// e^(h + l) as a pair
+__device__ __forceinline__ void ff_exp_pair(float h, float l, float &rh, float &rl) {
+    ff_exp_near(h, rh, rl);
+    rl = fmaf(rh, l, rl);
+}
+
+// ln(x + xl), xl a rounding's worth of x, as a pair of floats good to 2^-40: ff_log's head y, and what x e^-y is more than 1.
+__device__ __forceinline__ void ff_log_near(float x, float xl, float &h, float &l) {
+    float eh, el;
+    ff_log(x, h, l);
+    ff_exp_near(-h, eh, el);
+    l = fmaf(x, eh, -1.0f) + fmaf(x, el, xl * eh);
+}
+
+// a ln(a / b) - a + b, none of it negative, with x = ln(a / b): sums of these have no large terms that cancel. a, b >= 0
+__device__ __forceinline__ float divergence_of(float a, float b, float x) {
+    if (!(a > 0.0f)) return b;
+    if (fabsf(x) > 0.5f) return fmaf(a, x - 1.0f, b);
+    // x - 1 + e^-x
+    const float c = fmaf(x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, -1.0f / 362880.0f, 1.0f / 40320.0f), -1.0f / 5040.0f),
+                                                   1.0f / 720.0f), -1.0f / 120.0f), 1.0f / 24.0f), -1.0f / 6.0f);
+    return a * (x * x) * fmaf(x, c, 0.5f);
+}
+
 // ln(1 + b (e^r - 1)), good where r is small; 0 < b < 1
 __device__ __forceinline__ float ln_mixed(float b, float r) { return r > 40.0f ? r + logf(b) : log1pf(b * expm1f(r)); }
 
@@ -308,11 +334,17 @@ __device__ __forceinline__ bool plain(const TokenParams &P, float m) { return fa
 __device__ __forceinline__ float scaled(const TokenParams &P, float m) { return __fmul_rn(m, P.c); }
 
 // What m c is more than the R that is taken of it.
-__device__ __forceinline__ float off_by(const TokenParams &P, float m) { return plain(P, m) ? fmaf(m, P.c, -scaled(P, m)) : 0.0f; }
+__device__ __forceinline__ float off_by(const TokenParams &P, float m) { return plain(P, m) ? fmaf(m, P.c, -scaled(P, m)) + m * P.c_lo : 0.0f; }
 
 // A thread's reference m is its warp's maximum in the first chunk, and moves when a logit is 8 binades above it
 // (TokenParams::lag): the sums are good whatever m is, and moving it for every new maximum costs 30 instructions in nearly
 // every chunk (one of 32 lanes has a new maximum). What entropies lose by it is 8 2^-24.
+
+// (z - m) log2(e) / T of a difference
+__device__ __forceinline__ float exponent(const TokenParams &P, float d) {
+    d = fmaxf(d, P.far);
+    return fmaf(d, P.c_lo, d * P.c);
+}
 
 // P.far as logits2 takes it
 template <int DT>
@@ -331,7 +363,7 @@ __device__ __forceinline__ void merge(const TokenParams &P, Part &a, const Part 
         return;
     }
     const float m = fmaxf(a.m, b.m);
-    const float xa = fmaxf(a.m - m, P.far) * P.c, xb = fmaxf(b.m - m, P.far) * P.c;
+    const float xa = exponent(P, a.m - m), xb = exponent(P, b.m - m);
     const float fa = ex2_approx(xa), fb = ex2_approx(xb);
     a.t = fa * fmaf(xa, a.s, a.t) + fb * fmaf(xb, b.s, b.t);
     a.s = fa * a.s + fb * b.s;
@@ -344,7 +376,7 @@ __device__ __forceinline__ Part warp_fold(const TokenParams &P, Part a) {
     constexpr uint32_t all = 0xffffffffu;
     Part r;
     r.m = from_order_bits(__reduce_max_sync(all, order_bits(a.m)));
-    const float x = fmaxf(a.m - r.m, P.far) * P.c, f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
+    const float x = exponent(P, a.m - r.m), f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
     r.s = f * a.s;
     r.t = Kd::Ent && f > 0.0f ? f * fmaf(x, a.s, a.t) : 0.0f;
 #pragma unroll
@@ -921,7 +953,7 @@ __device__ __forceinline__ f32x2 logits2(const uint4 &w, int i, uint32_t far) {
 template <class Kd>
 __device__ __forceinline__ f32x2 far_exponents2(const TokenParams &P, const uint4 &w, int i, float m) {
     const float2 z = pair_of<Kd::DT>(w, i);
-    return pack2(fmaxf(z.x - m, P.far) * P.c, fmaxf(z.y - m, P.far) * P.c);
+    return pack2(exponent(P, z.x - m), exponent(P, z.y - m));
 }
 
 // Tokens of a vector before the given one (logit zy, token y): those larger, and equal ones of a lower index. first: the
@@ -1032,7 +1064,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             } else if (cm > m) {
                 const float next = scaled(P, cm);
                 if (m != -INFINITY) {
-                    const float x = plain(P, m) && plain(P, cm) ? R - next : fmaxf(m - cm, P.far) * c - off_by(P, m) + off_by(P, cm);
+                    const float x = plain(P, m) && plain(P, cm) ? R - next : exponent(P, m - cm) - off_by(P, m) + off_by(P, cm);
                     const float f = ex2_approx(x);
                     const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
                     if (Kd::Ent) {
@@ -1066,7 +1098,9 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             for (int j = 0; j < kVecs; ++j)
 #pragma unroll
                 for (int q = 0; q < kPer / 2; ++q) {
-                    const f32x2 x2 = fma2(logits2<Kd>(w[j], q, far), c2, nR);
+                    const f32x2 z2 = logits2<Kd>(w[j], q, far);
+                    f32x2 x2 = fma2(z2, c2, nR);
+                    if (Kd::List) x2 = fma2(z2, pack2(P.c_lo, P.c_lo), x2);
                     const float2 x = unpack2(x2);
                     const f32x2 e2 = pack2(ex2_approx(x.x), ex2_approx(x.y));
                     if (q & 1) {
@@ -1121,7 +1155,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     if (Kd::Rank) before += counted<Kd::DT>(above);
     Part p{m, (a.x + a.y) + (b.x + b.y), (e.x + e.y) + (f.x + f.y), bad ? -1 : before};
     if (plain(P, m)) {  // what R was off by
-        const float r = fmaf(m, c, -R), g = ex2_approx(-r);
+        const float r = off_by(P, m), g = ex2_approx(-r);
         p.t = g * fmaf(-r, p.s, p.t);
         p.s *= g;
     }
@@ -1157,12 +1191,17 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
     }
     const float c = P.c, R = scaled(P, m);
     const bool near = plain(P, m);
+    constexpr bool kFine = Kd::List && Kd::DT == SV_DT_FP32;  // bf16 gradients have no use for c_lo
     if (near) {
-        const float r = fmaf(m, c, -R), g = ex2_approx(-r);
+        const float r = kFine ? off_by(P, m) : fmaf(m, c, -R), g = ex2_approx(-r);
         fa = g * fmaf(-r, fb, fa);
         fb *= g;
     }
     const f32x2 nR = pack2(-R, -R), c2 = pack2(c, c), a2 = pack2(fa, fa), b2 = pack2(fb, fb);
+    auto exponents = [&](f32x2 z2) {
+        const f32x2 x2 = fma2(z2, c2, nR);
+        return kFine ? fma2(z2, pack2(P.c_lo, P.c_lo), x2) : x2;
+    };
     auto weigh = [&](f32x2 x2) {
         const float2 x = unpack2(x2);
         return mul2(pack2(ex2_approx(x.x), ex2_approx(x.y)), Kd::Ent ? fma2(b2, x2, a2) : a2);
@@ -1191,7 +1230,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
             for (int j = 0; j < kVecs; ++j) {
                 f32x2 g[kPer / 2];
 #pragma unroll
-                for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(fma2(logits2<Kd>(w[j], q, far), c2, nR));
+                for (int q = 0; q < kPer / 2; ++q) g[q] = weigh(exponents(logits2<Kd>(w[j], q, far)));
                 to[j * kTeam] = packed(g);
             }
             __syncwarp();  // (after the stores, which have used the loads: see sum_slice)
@@ -1208,7 +1247,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
                     const uint4 w = end ? ragged_end<Kd>(S.row[d].z, whole, rest) : load_vec(at + j * kTeam * 16);
 #pragma unroll
                     for (int q = 0; q < kPer / 2; ++q)
-                        g[q] = weigh(near ? fma2(logits2<Kd>(w, q, far), c2, nR) : far_exponents2<Kd>(P, w, q, m));
+                        g[q] = weigh(near ? exponents(logits2<Kd>(w, q, far)) : far_exponents2<Kd>(P, w, q, m));
                 } else {
 #pragma unroll
                     for (int q = 0; q < kPer / 2; ++q) g[q] = a2;
@@ -1437,7 +1476,8 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
     __syncwarp();
     for (int j = lane; j < kHash / 4; j += 32) reinterpret_cast<int4 *>(L.hash)[j] = make_int4(-1, -1, -1, -1);
     bits = __reduce_or_sync(all, bits);
-    float p_rest = 0.0f, p_sum = 0.0f, zsum = 0.0f, cross = 0.0f;
+    float p_rest = 0.0f, p_rest_l = 0.0f, rest_h = -INFINITY, rest_l = 0.0f, over = 0.0f, p0 = 0.0f, p0_l = 0.0f, lp0 = 0.0f, zsum = 0.0f, zsum_l = 0.0f, cross = 0.0f;
+    const bool rkl = P.divergence == SPECVERIFY_RKL;
     zmax = warp_max(zmax);
     if (!bits) {
         if (P.form == SPECVERIFY_TARGET_LOGITS) {
@@ -1457,9 +1497,7 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
                 if (llp[j] == -INFINITY) h = -INFINITY;
                 llp[j] = h;
                 lpr[j] = ff_exp(h, 0.0f);
-                p_sum += lpr[j];
             }
-            p_sum = warp_sum(p_sum);
         } else {
             // One less a sum close to it: in pairs of floats, or little would be left of it.
             float sh = 0.0f, sl = 0.0f;
@@ -1472,25 +1510,55 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
                 ff_add(sh, sl, __shfl_xor_sync(all, sh, off), __shfl_xor_sync(all, sl, off), sh, sl);
-            p_sum = sh;
             ff_add(1.0f, 0.0f, -sh, -sl, sh, sl);
             p_rest = fmaxf(sh + sl, 0.0f);
+            const float least = rkl ? fmaxf(p_rest, 0x1p-20f) : p_rest;
+            const bool kept = least == sh + sl;
+            p_rest_l = kept ? (sh - least) + sl : 0.0f;
+            if (least > 0.0f) ff_log_near(least, p_rest_l, rest_h, rest_l);
+            over = kept ? 0.0f : (least - sh) - sl;
         }
-        if (zmax > -INFINITY)
-            for (int j = lane; j < P.K; j += 32) {
-                const float dz = fmaxf(lz[j] - zmax, P.far), w = ex2_approx(dz * P.c);
-                zsum += w;
-                if (w > 0.0f && P.divergence == SPECVERIFY_RKL) cross += w * (dz * P.inv_hi - llp[j]);
+        if (zmax > -INFINITY) {
+            if (rkl) {
+                float mine = -INFINITY;  // ln p of a token with the largest logit
+                for (int j = lane; j < P.K; j += 32)
+                    if (lz[j] == zmax) mine = fmaxf(mine, llp[j]);
+                lp0 = warp_max(mine);
+                if (!(lp0 > -80.0f)) lp0 = 0.0f;  // (any number would do)
+                ff_exp_near(lp0, p0, p0_l);
             }
-        zsum = warp_sum(zsum);
-        cross = warp_sum(cross);
+            for (int j = lane; j < P.K; j += 32) {
+                float d, e, xh, xl, wh, wl;
+                two_sum(lz[j], -zmax, d, e);
+                if (!(d > P.far)) continue;
+                over_T(P, d, e, xh, xl);
+                ff_exp_pair(xh, xl, wh, wl);
+                ff_add(zsum, zsum_l, wh, wl, zsum, zsum_l);
+                if (wh > 0.0f && rkl) {
+                    two_sum(llp[j], -lp0, d, e);
+                    if (!(fabsf(d) < INFINITY)) e = 0.0f;
+                    cross += wh * ((xh - d) + (xl - e));
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            ff_add(zsum, zsum_l, __shfl_xor_sync(all, zsum, off), __shfl_xor_sync(all, zsum_l, off), zsum, zsum_l);
+        if (rkl) cross = warp_sum(cross);
     }
     if (lane == 0) {
         row.bad = bits;
         row.p_rest = p_rest;
-        row.p_sum = p_sum;
+        row.p_rest_l = p_rest_l;
+        row.rest_h = rest_h;
+        row.rest_l = rest_l;
+        row.over = over;
         row.zmax = zmax;
+        row.p0 = p0;
+        row.p0_l = p0_l;
+        row.lp0 = lp0;
         row.zsum = zsum;
+        row.zsum_l = zsum_l;
         row.cross = cross;
         if (bits) atomicOr(P.status, bits);
     }
@@ -1734,10 +1802,12 @@ __device__ __forceinline__ void fix_list(const TokenParams &P, const Shared &S, 
     }
 }
 
-// The divergence over the list's tokens and the rest, see include/specverify.h. Logarithms are pairs of floats up to their
-// differences: a small divergence is a difference of much larger terms.
+// The divergence over the list's tokens and the rest, see include/specverify.h, as a sum of divergence_of's. Logarithms are pairs
+// of floats up to their differences, and so is the normaliser: a small divergence or gradient is the difference of much larger
+// terms.
 template <class Kd>
 __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, const Lists &L, const Cta &cta, int d, const Part &p) {
+    constexpr uint32_t all = 0xffffffffu;
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane, K = P.K, kind = P.divergence;
@@ -1746,86 +1816,117 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
     const bool good = row.state == kLive && !bad;
     const bool some = p.m > -INFINITY;  // the rest has mass
     if (row.state == kLive && bad && !row.bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
-    float loss = bad ? NAN : 0.0f, C = 0.0f, Z = 0.0f;
-    if (good) {
-        if (row.zmax > -INFINITY) Z = row.zsum * ex2_approx(fmaxf(row.zmax - M, P.far) * P.c);
-        if (some) Z = fmaf(p.s, ex2_approx(fmaxf(p.m - M, P.far) * P.c), Z);
-    }
+    const bool early = !good || kind == SPECVERIFY_FKL || kind == SPECVERIFY_RKL;
+    float loss = bad ? NAN : 0.0f, C = 0.0f;
     // the others' share of a gradient, (h_rest - q_rest C) / (s T) times 2^((z - m) c)
-    auto known = [&](float h_rest, float q_rest) {
-        if (lane == 0) {
-            const float f = some ? row.g * P.inv_hi * (h_rest - q_rest * C) / p.s : 0.0f;
+    auto known = [&](float d_rest) {  // (lane 1's)
+        if (lane == 1) {
+            const float f = some ? row.g * P.inv_hi * d_rest / p.s : 0.0f;
             S.coef[d] = bad ? make_float4(0.0f, NAN, 0.0f, 0.0f) : make_float4(some ? p.m : 0.0f, f, 0.0f, 0.0f);
             mbar_arrive(smem_u32(&S.known[d]));
         }
     };
-    const bool early = !good || kind == SPECVERIFY_FKL || kind == SPECVERIFY_RKL;
-    if (Kd::Grad && early) {
-        // Here sum h is known without a look at the list: -sum p, and sum q ln(q / p) by the scout's sums. The stores need
-        // not wait for the divergence (2.5 us for a list of 128).
-        const float q_rest = good && some ? p.s * ex2_approx(fmaxf(p.m - M, P.far) * P.c) / Z : 0.0f;
-        float h_rest = -row.p_rest;
-        C = -(row.p_sum + row.p_rest);
-        if (good && kind == SPECVERIFY_RKL) {
-            const float ln_z = logf(Z);
-            h_rest = q_rest > 0.0f ? q_rest * (logf(q_rest) - logf(fmaxf(row.p_rest, 0x1p-20f))) : 0.0f;
-            C = h_rest;
-            if (row.zmax > -INFINITY) {
-                const float dz = fmaxf(row.zmax - M, P.far), w = ex2_approx(dz * P.c) / Z;
-                if (w > 0.0f) C += w * fmaf(row.zsum, dz * P.inv_hi - ln_z, row.cross);
+    // The weights e^((z - M) / T) of the list's largest logit (even lanes) and of the rest's reference (odd lanes), and the
+    // normaliser.
+    float Zh = 1.0f, Zl = 0.0f;
+    if (good) {
+        float dh, dl, wh = 0.0f, wl = 0.0f, mh, ml;
+        two_sum(lane & 1 ? p.m : row.zmax, -M, dh, dl);
+        if (dh > P.far) {
+            float xh, xl;
+            over_T(P, dh, dl, xh, xl);
+            ff_exp_pair(xh, xl, wh, wl);
+        }
+        ff_mul(wh, wl, lane & 1 ? p.s : row.zsum, lane & 1 ? 0.0f : row.zsum_l, mh, ml);
+        ff_add(mh, ml, __shfl_xor_sync(all, mh, 1), __shfl_xor_sync(all, ml, 1), Zh, Zl);
+        if (Kd::Grad && early) {
+            // Here sum h is known without a look at the list: -sum p, and sum q ln(q / p) by the scout's sums. The stores need
+            // not wait for the divergence (2.5 us for a list of 128). q of that logit and of the rest, and ln(q / p):
+            float qh, ql;
+            ff_div(lane & 1 ? mh : wh, lane & 1 ? ml : wl, Zh, Zl, qh, ql);
+            if (kind == SPECVERIFY_FKL) {
+                known(fmaf(qh, row.over, (qh - row.p_rest) + (ql - row.p_rest_l)));
+            } else {
+                const float ph = lane & 1 ? fmaxf(row.p_rest, 0x1p-20f) : row.p0, more = ((qh - ph) + (ql - (lane & 1 ? row.p_rest_l : row.p0_l))) / ph;
+                const float t = fabsf(more) < 0.5f ? log1pf(more) : logf(qh) - (lane & 1 ? row.rest_h : row.lp0);
+                const float part = qh > 0.0f ? lane & 1 ? qh * t : qh * fmaf(row.zsum, t, row.cross) : 0.0f;
+                C = part + __shfl_xor_sync(all, part, 1);
+                known(qh > 0.0f ? qh * (t - C) : 0.0f);
             }
         }
-        known(h_rest, q_rest);
+    } else if (Kd::Grad) {
+        known(0.0f);
     }
+    // the normaliser's logarithm; of q of the rest the logarithm, itself, and ln(p / q) of it
+    float zh = 0.0f, zl = 0.0f, q_rest = 0.0f, r_rest = 0.0f;
     if (good) {
-        float zh, zl;
-        ff_log(Z, zh, zl);
-        float f = 0.0f, h = 0.0f, h_rest = 0.0f, q_rest = 0.0f;
+        float sh, sl, qh = -INFINITY, ql = 0.0f;
+        ff_log_near(lane & 1 ? fmaxf(p.s, 0x1p-100f) : Zh, lane & 1 ? 0.0f : Zl, sh, sl);
+        zh = __shfl_sync(all, sh, 0);
+        zl = __shfl_sync(all, sl, 0);
+        sh = __shfl_sync(all, sh, 1);
+        sl = __shfl_sync(all, sl, 1);
+        if (some) {
+            ff_logprob(P, p.m, M, zh, zl, qh, ql);
+            if (qh > -INFINITY) ff_add(qh, ql, sh, sl, qh, ql);
+            q_rest = ff_exp(qh, ql);
+        }
+        r_rest = (row.rest_h - qh) + (row.rest_l - ql);
+    }
+    // h - q C where sum h = -sum p: q (1 + over) - p
+    auto missing = [&](float pr, float q, float r) {
+        return fmaf(q, row.over, fabsf(r) < 0.5f ? pr * expm1f(-r) : q - pr);
+    };
+    if (good) {
+        float f = 0.0f, h = 0.0f, h_rest = 0.0f;
         // outcome K is the rest
         for (int j = lane; j <= K; j += 32) {
             const bool rest = j == K;
             const int at = d * L.stride + j;
             if (!rest && L.ids[at] < 0) continue;
-            float qh, ql;
-            ff_logprob(P, rest ? p.m : L.z[at], M, zh, zl, qh, ql);
-            if (rest && some) {
-                float sh, sl;
-                ff_log(p.s, sh, sl);
-                if (qh > -INFINITY) ff_add(qh, ql, sh, sl, qh, ql);
+            float q = q_rest, pr = row.p_rest, r = r_rest;  // r = ln(p / q)
+            if (!rest) {
+                float h, l;
+                ff_logprob(P, L.z[at], M, zh, zl, h, l);
+                q = ff_exp(h, l);
+                pr = L.p[at];
+                r = (L.lp[at] - h) - l;
             }
-            const float q = ff_exp(qh, ql);
-            const float pr = rest ? row.p_rest : L.p[at];
-            const float lp = rest ? logf(kind == SPECVERIFY_RKL ? fmaxf(pr, 0x1p-20f) : pr) : L.lp[at];
-            float fj = 0.0f, hj = 0.0f;
+            float fj, hj;
             if (kind == SPECVERIFY_FKL) {
-                if (pr > 0.0f) fj = pr * ((lp - qh) - ql);
-                hj = -pr;
+                fj = divergence_of(pr, q, r);
+                hj = missing(pr, q, r);  // (with q C)
             } else if (kind == SPECVERIFY_RKL) {
-                if (q > 0.0f) fj = hj = q * ((qh - lp) + ql);
+                fj = divergence_of(q, rest ? fmaxf(pr, 0x1p-20f) : pr, -r);
+                hj = q > 0.0f ? q * (-r - C) : 0.0f;  // (with q C)
             } else if (kind == SPECVERIFY_TVD) {
-                fj = 0.5f * fabsf(pr - q);
-                hj = 0.5f * q * (q > pr ? 1.0f : q < pr ? -1.0f : 0.0f);
+                const bool near = fabsf(r) < 0.5f;
+                fj = 0.5f * fabsf(near ? pr * expm1f(-r) : pr - q);
+                hj = 0.5f * q * ((near ? r < 0.0f : q > pr) ? 1.0f : (near ? r > 0.0f : q < pr) ? -1.0f : 0.0f);
             } else {
-                // ln(m / q) = ln(1 + b (p / q - 1)), and the other way round
-                const float b = P.beta, r = (lp - qh) - ql;  // ln(p / q)
-                if (q > 0.0f) hj = -(1.0f - b) * q * ln_mixed(b, pr > 0.0f ? r : -INFINITY);
-                fj = hj;
-                if (pr > 0.0f) fj -= b * pr * ln_mixed(1.0f - b, q > 0.0f ? -r : -INFINITY);
+                // ln(m / q) = ln(1 + b (p / q - 1)), and the other way round; each has a p, a q that is 0 or neither
+                const float b = P.beta, m = b * pr + (1.0f - b) * q;
+                const float u = q > 0.0f ? ln_mixed(b, pr > 0.0f ? r : -INFINITY) : 0.0f;
+                const float v = pr > 0.0f ? ln_mixed(1.0f - b, q > 0.0f ? -r : -INFINITY) : 0.0f;
+                hj = -(1.0f - b) * q * u;
+                fj = b * divergence_of(pr, m, -v) + (1.0f - b) * divergence_of(q, m, -u);
             }
             f += fj;
             h += hj;
             if (rest) {
                 h_rest = hj;
-                q_rest = q;
             } else if (Kd::Grad) {
                 L.lp[at] = hj;
                 L.z[at] = q;
             }
         }
         loss = warp_sum(f);
+        if (kind == SPECVERIFY_FKL) loss += row.over;
+        if (kind == SPECVERIFY_RKL) loss -= row.over;
+        if (Kd::Grad && early) C = 0.0f;
         if (Kd::Grad && !early) {
             C = warp_sum(h);
-            known(__shfl_sync(0xffffffffu, h_rest, K & 31), __shfl_sync(0xffffffffu, q_rest, K & 31));
+            known(__shfl_sync(all, h_rest, K & 31) - q_rest * C);
         }
     }
     if (lane == 0 && cta.rank == 0) P.loss[e] = loss;

@@ -17,7 +17,7 @@ struct TokenParams {
     const char *logits;
     int64_t stride_bytes, rows;
     int32_t V;
-    float c;             // log2(e) / T
+    float c, c_lo;       // log2(e) / T; c_lo is 0, or (lists) more than 0
     float lag, near, far;  // 8 / c, 2^24 / c, about -2^25 / c (a bf16 number): see sv_token.cuh
     float inv_hi, inv_lo;  // 1 / T
     int32_t *status;

@@ -701,6 +701,32 @@ def test_exploring_gradients_of_masked_rows_at_every_temperature(h, dtype, T):
 
 
 # ---------------------------------------------------------------------------
+# a draft that agrees with its target
+
+@pytest.mark.parametrize("kind", ["fkl", "rkl", "jsd", "tvd"])
+@pytest.mark.parametrize("K,T", [(1, 1.9), (20, 1.9), (100, 0.7)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_small_divergences(h, kind, K, T, dtype):
+    """Divergences far below one are as good as larger ones. What is off is the sum over the rest, by a share e of it: q of the
+    rest is e (1 - q) q more, the others less by as much in all. Of the first three the derivative is p less q (of the rest,
+    times no more than 1, 2 where a logarithm's half percent is counted in); of the TVD it is that change. The terms are
+    of one sign: each a few roundings off, and by what a logarithm is (2^-37) times p less q."""
+    z = tu.logits(24, 30000, dtype, 8, device="cuda")
+    ids, t = tu.lists(z, K, 8, T=T, noise=0.02, short=False)
+    loss = h.distill_loss(z, ids, t, T, kind)
+    _, same = h.distill_grad(z, ids, t, None, T, kind)
+    clean(h)
+    for i in range(24):
+        d = tu.Divergence(z[i], ids[i], t[i], T, kind)
+        p_rest = 1.0 - float(torch.exp(t[i].double()).sum())
+        q_rest = 1.0 - float(d.soft.p[ids[i].long()].sum())
+        off = d.soft.sum_err * (q_rest * (1 - q_rest) if kind == "tvd" else 2 * abs(q_rest - p_rest))
+        lim = off + 2.0 ** -20 * float(d.loss) + 2.0 ** -37 * 2 * (2 * float(d.loss)) ** 0.5
+        assert abs(float(loss[i]) - float(d.loss)) <= lim, (i, float(loss[i]), float(d.loss), lim)
+        assert abs(float(same[i]) - float(d.loss)) <= lim
+
+
+# ---------------------------------------------------------------------------
 # waits that run out
 
 @pytest.mark.parametrize("rows", [3, 60], ids=["clusters", "rows"])
