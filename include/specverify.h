@@ -260,7 +260,7 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
  *             that order and their log-probabilities; past V -inf and -1. NULL for k = 0.
  * An entry of token -1 asks for nothing: its row is not read, its floats and its
  * rank are 0, its top tokens -1 of log-probability -inf. Any other token outside
- * [0, V) is bad. Each row asked for is read once. */
+ * [0, V), any path below 0 with a token and any row outside the buffer is bad. Each row asked for is read once. */
 int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
                               int64_t V, int64_t row_stride, float temperature, int32_t B,
                               int32_t M, const int32_t *tokens, const int64_t *row_off,

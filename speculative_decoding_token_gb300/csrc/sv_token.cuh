@@ -668,11 +668,19 @@ struct Chooser {
         return v < cta.slice_vecs ? cta.slice0 + v : -1;
     }
 
+    // Vector v of the row; -inf for what is not there. (No read-only load: the row may have been written while this kernel
+    // waited for the one before. Four of them are in flight, past L1: 2000 rows take 138.6 us,
+    // 140.6 through it; the ragged end comes after.)
     __device__ __forceinline__ uint4 load(int v) const {
+        uint4 w = make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
+        asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+            : "l"(row + (int64_t)v * 16), "r"((uint32_t)(v >= 0 && v < P.V / kPer)));
+        return w;
+    }
+    __device__ __forceinline__ void load_end(uint4 &w, int v) const {
         const int whole = P.V / kPer;
-        if (v >= 0 && v < whole) return __ldg(reinterpret_cast<const uint4 *>(row) + v);
-        if (v == whole) return ragged_end<Kd>(row, whole, P.V - whole * kPer);
-        return make_uint4(Kd::kNegInf, Kd::kNegInf, Kd::kNegInf, Kd::kNegInf);
+        if (v == whole) w = ragged_end<Kd>(row, whole, P.V - whole * kPer);
     }
 
     // A vector's tokens above the class, or in it: bit u for token u.
@@ -718,6 +726,8 @@ struct Chooser {
                 v[q] = j < n ? index(j) : -1;
                 w[q] = load(v[q]);
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_end(w[q], v[q]);
             if (!f(w, v)) return;
         }
     }
@@ -1385,7 +1395,8 @@ __device__ __forceinline__ void fetch(const TokenParams &P, long long e, int lan
             // sequences' order a CTA met several of them, 1.7 us each, before its first row)
             const int b = (int)(e % P.B), m = (int)(e / P.B);
             a.entry = (long long)b * P.M + m;
-            a.row = P.row_off[b] + (P.path ? P.path[a.entry] : m);
+            const int at = P.path ? P.path[a.entry] : m;
+            a.row = at < 0 ? -1 : P.row_off[b] + at;
         }
         a.y = P.tokens[a.entry];
         if (P.grad) {

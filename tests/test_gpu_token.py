@@ -151,6 +151,11 @@ def test_logprobs_bad_entries_fail_alone(svm, h):
     assert r.logprob.isnan().tolist() == [[True, False], [False, False], [False, True], [False, False]]
     check_entry(z[0], 1.0, 0, r, (0, 1), 2)
     check_entry(z[11], 1.0, 0, r, (3, 0), 2)
+    # no row is before a sequence's first
+    path = torch.tensor([[0, -1], [-1, 3]], device="cuda", dtype=torch.int32)
+    r = h.token_logprobs(z, torch.zeros(2, 2, device="cuda", dtype=torch.int32), row_off=off[1:3], path=path)
+    assert h.device_status() == svm.STATUS_BITS["bad_row"]
+    assert r.logprob.isnan().tolist() == [[False, True], [True, True]]  # (row 14 of 12)
 
 
 def test_logprobs_past_two_to_the_31(h):
