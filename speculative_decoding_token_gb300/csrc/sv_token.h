@@ -18,7 +18,7 @@ struct TokenParams {
     int64_t stride_bytes, rows;
     int32_t V;
     float c, c_lo;       // log2(e) / T; c_lo is 0, or (lists) more than 0
-    float lag, near, far;  // 8 / c, 2^24 / c, about -2^25 / c (a bf16 number): see sv_token.cuh
+    float lag, near, far;  // 8 / c, 2^24 / c, about -2^25 / c (a bf16 number): see sv_token_math.cuh
     float inv_hi, inv_lo;  // 1 / T
     int32_t *status;
     uint64_t wait_ns;    // bound of a wait inside the kernel
