@@ -15,9 +15,10 @@
 //   producer       the copies;
 //   patcher        (lists) takes the listed tokens out of a chunk that has
 //                  arrived (-inf), so that the sums are over the rest alone;
-//   epilogue       merges the warps' sums (and the cluster's), picks the top
-//                  tokens, writes the results, and hands the consumers what a
-//                  gradient's second reading needs.
+//   top tokens     (the same warp, rows have one or the other) puts what the
+//                  consumers have gathered in order;
+//   epilogue       merges the warps' sums (and the cluster's), writes the results,
+//                  and hands the consumers what a gradient's second reading needs.
 // No warp waits for the end of a row but the consumers of a gradient. Rows are
 // taken over from CTAs (clusters) that have not begun, one at a time, when the
 // copies of the row before are on their way: CTAs differ by a sixth in speed.
@@ -560,7 +561,6 @@ template <class Kd>
 __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Shared &S, const Lists &list, const Cta &cta,
                                       Entries &at) {
     Asked a;
-    int ends = 0;
     for (int r = 0;; ++r) {
         const int d = cta.place(r);
         if (at.e >= 0) fetch<Kd::List>(P, at.e, cta.lane, a);
@@ -574,10 +574,7 @@ __device__ __forceinline__ void scout(const TokenParams &P, const Plan &plan, Sh
         }
         __syncwarp();
         if (cta.lane == 0) mbar_arrive(smem_u32(&S.row_full[d]));
-        if (at.e < 0) {
-            if (++ends == Kd::kEpilogues) return;
-            continue;
-        }
+        if (at.e < 0) return;
         // The copies can begin; what else there is to know of the entry
         if (S.row[d].state == kLive) {
             if (Kd::List) scout_list<Kd::DT>(P, S.row[d], list, d, at.e, cta.lane, a);
@@ -695,11 +692,10 @@ __device__ __forceinline__ void write_top(const TokenParams &P, long long e, int
 }
 
 template <class Kd>
-__device__ __forceinline__ bool finish_token(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Cta &cta, int d, const Part &p) {
+__device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, const Cta &cta, int d, const Part &p) {
     const Row &row = S.row[d];
     const long long e = row.entry;
-    const int lane = cta.lane, k = Kd::Top ? P.k : 0;
-    const bool alone = cta.cluster == 1;
+    const int lane = cta.lane;
     const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || p.m == -INFINITY));
     const bool good = row.state == kLive && !bad;
     if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
@@ -737,41 +733,64 @@ __device__ __forceinline__ bool finish_token(const TokenParams &P, const Plan &p
         }
         if (Kd::Rank) P.rank[e] = bad ? -1 : p.n;
     }
-    if constexpr (Kd::Top) {
-        if (row.state == kLive) {
-            select_top<Kd::DT>(P, plan, row.z, *T, d, cta);
-            if (!alone) {
-                for (int i = lane; i < k; i += 32)
-                    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(&T->gathered[cta.rank * k + i], 0)),
-                                 "l"(T->keys[d][i])
-                                 : "memory");
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) cluster_arrive(S.gathered, 0);
-                if (cta.rank != 0) return true;
-                if (!wait_bar(S.gathered, 0, S, P)) return false;  // a cluster of such rows has one
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                first_keys(T->gathered, cta.cluster * k, k, lane);
-            }
-        }
-        if (cta.rank != 0) return true;
-        const unsigned long long *best = alone ? T->keys[d] : T->gathered;
-        for (int i = lane; i < k; i += 32) {
-            if (good) {
-                write_top<Kd::DT>(P, e, i, best[i], p.m, lh, ll);
-            } else {
-                P.top_logprob[e * k + i] = bad ? NAN : -INFINITY;
-                P.top_idx[e * k + i] = -1;
-            }
-        }
-    }
     if (Kd::Grad && lane == 0) {
         const float py = ff_exp(lp, lo);
         const float s = Kd::Ent && py > 0.0f ? row.h * py * (lp + H) : 0.0f;
         S.fix[d] = (row.g * (1.0f - py) - s) * P.inv_hi;
         S.good[d] = good;
     }
-    return true;
+}
+
+// The top tokens of every row, beside the epilogue.
+template <class Kd>
+__device__ __forceinline__ void finish_top(const TokenParams &P, const Plan &plan, Shared &S, SharedTop &T, const Cta &cta) {
+    const int lane = cta.lane, k = P.k;
+    int live = 0;
+    for (int r = 0;; ++r) {
+        const int d = cta.place(r);
+        if (!wait_bar(S.row_full[d], cta.parity(r), S, P)) return;
+        const Row &row = S.row[d];
+        const int state = row.state;
+        if (state == kEnd) return;
+        if (!wait_bar(S.summed[d], cta.parity(r), S, P)) return;
+        if (state == kLive) {
+            select_top<Kd::DT>(P, plan, row.z, T, d, cta);
+            if (cta.cluster > 1) {
+                for (int i = lane; i < k; i += 32)
+                    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(&T.gathered[cta.rank * k + i], 0)),
+                                 "l"(T.best[i])
+                                 : "memory");
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) cluster_arrive(S.gathered, 0);
+            }
+        }
+        if (cta.rank == 0) {
+            Part p{-INFINITY, 0.0f, 0.0f, 0};
+            if (state == kLive && cta.cluster > 1) {
+                if (!wait_bar(S.gathered, 0, S, P)) return;  // a cluster of such rows has one
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                first_keys(T.gathered, cta.cluster * k, k, T.best, lane);
+                if (!receive<Kd>(P, S, cta, live++, p)) return;
+            } else if (state == kLive) {
+                if (lane < kConsumers) p = S.part[d][lane];
+                p = warp_fold<Kd>(P, p);
+            }
+            const bool good = state == kLive && p.n >= 0 && p.m > -INFINITY;
+            float lh = 0.0f, ll = 0.0f;
+            if (good) ff_log(p.s, lh, ll);
+            for (int i = lane; i < k; i += 32) {
+                if (good) {
+                    write_top<Kd::DT>(P, row.entry, i, T.best[i], p.m, lh, ll);
+                } else {
+                    P.top_logprob[row.entry * k + i] = state == kSkip ? -INFINITY : NAN;
+                    P.top_idx[row.entry * k + i] = -1;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.row_free[d]));
+    }
 }
 
 // Puts the given token's gradient in its place, once the consumers have stored the others'.
@@ -783,9 +802,9 @@ __device__ __forceinline__ void fix_token(const TokenParams &P, const Shared &S,
 }
 
 template <class Kd>
-__device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, Shared &S, SharedTop *T, const Lists &L, const Cta &cta, int first) {
+__device__ __forceinline__ void finish(const TokenParams &P, Shared &S, const Lists &L, const Cta &cta) {
     int live = 0;
-    for (int r = first;; r += Kd::kEpilogues) {
+    for (int r = 0;; ++r) {
         const int d = cta.place(r);
         const uint32_t parity = cta.parity(r);
         if (!wait_bar(S.row_full[d], parity, S, P)) return;
@@ -800,7 +819,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, const Plan &plan, S
             p = warp_fold<Kd>(P, p);
         }
         if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
-        else if (!finish_token<Kd>(P, plan, S, T, cta, d, p)) return;
+        else finish_token<Kd>(P, S, cta, d, p);
         __syncwarp();
         if (Kd::Grad) {
             if (!wait_bar(S.stored[d], parity, S, P)) return;
@@ -856,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
         }
         for (int i = 0; i < kDepth; ++i) {
             mbar_init(smem_u32(&S.row_full[i]), 1);
-            mbar_init(smem_u32(&S.row_free[i]), kConsumers + (Kd::List ? 3 : 2));
+            mbar_init(smem_u32(&S.row_free[i]), kConsumers + (Kd::List || Kd::Top ? 3 : 2));
             mbar_init(smem_u32(&S.sent[i]), 1);
             mbar_init(smem_u32(&S.summed[i]), kConsumers);
             mbar_init(smem_u32(&S.known[i]), 1);
@@ -885,9 +904,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
     if (warp < kConsumers) consume<Kd>(P, plan, S, top, cta);
     else if (warp == kScout) scout<Kd>(P, plan, S, list, cta, at);
     else if (warp == kProducer) produce<Kd>(P, plan, S, cta);
-    else if (Kd::List && warp == kPatcher) patch<Kd>(P, plan, S, list, smem, cta);
-    else if (warp == kEpilogue) finish<Kd>(P, plan, S, top, list, cta, 0);
-    else if (Kd::kEpilogues == 2) finish<Kd>(P, plan, S, top, list, cta, 1);
+    else if (Kd::List && warp == kBeside) patch<Kd>(P, plan, S, list, smem, cta);
+    else if (warp == kEpilogue) finish<Kd>(P, S, list, cta);
+    else if constexpr (Kd::Top) finish_top<Kd>(P, plan, S, *top, cta);
     __syncwarp();
     // What other CTAs send may still be on its way here where somebody gave up.
     if (plan.cluster > 1) cluster_sync();
@@ -930,7 +949,8 @@ Plan make_plan(const TokenParams &P) {
     int log = 0;
     if (Kd::Grad)
         while (log < 4 && (int64_t)room[log] * vecs * 16 > kRereadBytes) ++log;
-    while (log < 4 && P.entries <= room[log + 1] && vecs >> log >= 256 && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
+    const int64_t least = Kd::Top ? kLeastTop : 128;  // vectors of a slice
+    while (log < 4 && P.entries <= room[log + 1] && vecs >> (log + 1) >= least && (!Kd::Top || P.k << (log + 1) <= kGathered)) ++log;
     p.cluster = 1 << log;
     p.slice_vecs = (int32_t)(((vecs + p.cluster - 1 >> log) + 31) / 32 * 32);
     const int words = log ? (2 * kConsumers * Kd::kWords * 8) << log : 0;

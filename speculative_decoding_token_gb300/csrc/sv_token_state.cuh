@@ -10,7 +10,7 @@ namespace sv {
 namespace token {
 
 constexpr int kConsumers = 8;                     // warps
-constexpr int kScout = kConsumers, kProducer = kScout + 1, kPatcher = kProducer + 1, kEpilogue = kPatcher + 1;  // (patcher: lists)
+constexpr int kScout = kConsumers, kProducer = kScout + 1, kBeside = kProducer + 1, kEpilogue = kBeside + 1;  // (beside: patcher or top tokens)
 constexpr int kThreads = (kEpilogue + 1) * 32;
 constexpr int kTeam = kConsumers * 32;            // a thread takes every kTeam-th 16-byte vector of a chunk
 constexpr int kMaxSlots = 26;
@@ -25,9 +25,11 @@ constexpr int kGroupRows = 20;                    // groups of a thread's vector
 constexpr int kMine = 256, kKept = 512;           // groups that may hold top tokens, a warp's and all
 constexpr unsigned kLost = 1u << 24;
 constexpr int kKeys = 512;                        // tokens among them
-// Keys that a cluster's CTAs send to its first at most: more than a key a lane costs more to put in order than more CTAs save
-// (five rows of 32000 fp32 logits, k = 5: 12.8 us in clusters of 4, 13.7 of 8, 16.7 of 16).
-constexpr int kGathered = 32;
+// Where top tokens are asked for, a cluster's slices have this many vectors at least, and its CTAs send its first this many keys
+// at most: that one has to put them in order too (in a graph, us for clusters of 1, 2, 4, 8, 16: a row of 152064 bf16 logits and
+// k = 5: 13.9, 11.0, 8.7, 8.6, 10.4; five of 128256, k = 20: 13.4, 11.1, 10.5, 14.0, 24; twelve of 152064, k = 64: 16.0, 17.4, 21;
+// 20 of 32000, k = 20: 8.1, 10.0, 12.7).
+constexpr int kLeastTop = 4096, kGathered = 64;
 constexpr int kHash = 1024;
 
 enum State { kLive = 0, kSkip = 1, kBad = 2, kEnd = 3 };
@@ -41,7 +43,6 @@ struct Kind {
     static constexpr int kPer = 16 / kSize;  // logits of a vector
     static constexpr uint32_t kNegInf = DT == SV_DT_FP32 ? 0xff800000u : 0xff80ff80u;
     static constexpr int kVecs = 4;  // of a chunk, a thread
-    static constexpr int kEpilogues = Top ? 2 : 1;  // warps that take rows in turn (top tokens take one longer than short sums)
     // numbers of a Part that a cluster's CTAs send one another
     static constexpr int kWords = 2 + (Ent ? 1 : 0) + (Rank ? 1 : 0);
     static constexpr int kChunkVecs = kTeam * kVecs, kChunkBytes = kChunkVecs * 16;
@@ -93,9 +94,10 @@ struct SharedTop {
     uint16_t most[kTopDepth][kGroupRows][kTeam];  // the groups' maxima, upper halves of their bits
     uint32_t bound[kTopDepth][kConsumers];        // the order bits of a number that enough of the warp's tokens reach
     uint16_t mine[kConsumers][kMine];             // groups of a warp's share that may hold top tokens
-    uint16_t kept[kTopDepth][kKept];              // and of all of them, where that was not enough
-    unsigned long long keys[kTopDepth][kKeys];
-    unsigned long long gathered[kGathered];
+    uint16_t kept[kKept];                         // and of all of them, where that was not enough
+    alignas(16) unsigned long long keys[kTopDepth][kKeys];
+    alignas(16) unsigned long long gathered[kGathered];
+    unsigned long long best[kMaxAlternatives];    // the first k of a row, in order
     unsigned found[kTopDepth];                    // keys; kLost and more: not all of them
 };
 

@@ -10,59 +10,43 @@ namespace sv {
 
 namespace {
 
-// Sorts 32 N keys, the largest first; element 32 q + i is x[q] of lane i (a bitonic network, rolled up: it runs once a row, and
-// its instructions would not stay in the cache).
+// Puts those of n keys that are among the first k in their places in `best`: a key's place is how many are larger, counted by
+// 32 N keys' lanes at a time over all n, two at a load. (64 keys take N = 2 some 250 cycles of independent instructions. A bitonic
+// network has 21 steps of two shuffles that wait on one another: 2.3 us for k = 20,
+// here 1.5; 6.7 us for k = 64, 5.9 beside other work.)
 template <int N>
-__device__ __forceinline__ void sort_keys(unsigned long long (&x)[N], int lane) {
-#pragma unroll 1
-    for (int k = 2; k <= 32 * N; k <<= 1) {
-#pragma unroll 1
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            if (j < 32) {
+__device__ __forceinline__ void place_keys(const unsigned long long *keys, int n, int k, unsigned long long *best, int lane) {
+    int there = 0;
+    for (int b = 0; b < n; b += 32 * N) {
+        unsigned long long x[N];
+        int before[N];
 #pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    const unsigned long long o = __shfl_xor_sync(0xffffffffu, x[q], j);
-                    const bool larger = (((32 * q + lane) & k) == 0) == ((lane & j) == 0);
-                    x[q] = larger ? max(x[q], o) : min(x[q], o);
-                }
-                continue;
-            }
+        for (int q = 0; q < N; ++q) {
+            x[q] = b + 32 * q + lane < n ? keys[b + 32 * q + lane] : 0;
+            before[q] = 0;
+        }
+#pragma unroll 4
+        for (int i = 0; i < n; i += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(keys + i);
+            const unsigned long long second = i + 1 < n ? o.y : 0;
 #pragma unroll
-            for (int step = 1; step < N; step <<= 1) {
-                if (j != 32 * step) continue;
+            for (int q = 0; q < N; ++q) before[q] += (o.x > x[q] ? 1 : 0) + (second > x[q] ? 1 : 0);
+        }
 #pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    if (q & step) continue;
-                    const bool falls = ((32 * q) & k) == 0;
-                    const unsigned long long a = max(x[q], x[q ^ step]), b = min(x[q], x[q ^ step]);
-                    x[q] = falls ? a : b;
-                    x[q ^ step] = falls ? b : a;
-                }
-            }
+        for (int q = 0; q < N; ++q) {
+            if (x[q] && before[q] < k) best[before[q]] = x[q];
+            there += __popc(__ballot_sync(0xffffffffu, x[q] != 0));
         }
     }
-}
-
-// The first k of n keys, in order, to the start of them (0 where there are no more); n <= kKeys, k <= 32 N.
-template <int N>
-__device__ __forceinline__ void sort_front(unsigned long long *keys, int n, int k, int lane) {
-    unsigned long long x[N];
-#pragma unroll
-    for (int q = 0; q < N; ++q) x[q] = 32 * q + lane < n ? keys[32 * q + lane] : 0;
-    sort_keys<N>(x, lane);
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (32 * q + lane < k) keys[32 * q + lane] = x[q];
+    for (int i = there + lane; i < k; i += 32) best[i] = 0;
     __syncwarp();
 }
 
-__device__ __noinline__ void first_keys(unsigned long long *keys, int n, int k, int lane) {
-    if (n <= 32 && k <= 32) sort_front<1>(keys, n, k, lane);
-    else if (n <= 64 && k <= 64) sort_front<2>(keys, n, k, lane);
-    else if (n <= 128) sort_front<4>(keys, n, k, lane);
-    else if (n <= 256) sort_front<8>(keys, n, k, lane);
-    else sort_front<kKeys / 32>(keys, n, k, lane);
+// The first k of n keys, all of them different (but 0, which is none), in order; 0 where there are no more.
+__device__ __noinline__ void first_keys(const unsigned long long *keys, int n, int k, unsigned long long *best, int lane) {
+    if (n <= 32) place_keys<1>(keys, n, k, best, lane);
+    else if (n <= 64) place_keys<2>(keys, n, k, best, lane);
+    else place_keys<4>(keys, n, k, best, lane);
 }
 
 // exclusive sums over the lanes, and the total
@@ -274,13 +258,13 @@ __device__ __noinline__ int choose_more(const TokenParams &P, const Plan &plan, 
             }
             int total, to = lanes_before(__popc(in), lane, total) + groups;
             for (; in; in &= in - 1, ++to)
-                if (to < kKept) T.kept[d][to] = (uint16_t)(r * kTeam + lane * 8 + choose.group_of(in));
+                if (to < kKept) T.kept[to] = (uint16_t)(r * kTeam + lane * 8 + choose.group_of(in));
             groups += total;
         }
         __syncwarp();
         bool ok = groups <= kKept;
         if (ok)
-            choose.each(groups << (2 + log), [&](int j) { return choose.vector(T.kept[d][j >> (2 + log)], j & ((4 << log) - 1)); },
+            choose.each(groups << (2 + log), [&](int j) { return choose.vector(T.kept[j >> (2 + log)], j & ((4 << log) - 1)); },
                         [&](const uint4 (&w)[4], const int (&v)[4]) {
                 uint32_t in[4];
                 int c = 0;
@@ -350,14 +334,14 @@ __device__ __noinline__ int choose_more(const TokenParams &P, const Plan &plan, 
     return min(found, kKeys);
 }
 
-// The k best keys of the CTA's slice, in order, to the start of T.keys[d] (0 where there are none).
+// The k best keys of the CTA's slice, in order, to T.best (0 where there are none).
 template <int DT>
 __device__ __forceinline__ void select_top(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta) {
     const unsigned found = *(volatile unsigned *)&T.found[d];
     int n = (int)found;
     if (found < (unsigned)P.k || found > (unsigned)kKeys) n = choose_more<DT>(P, plan, row, T, d, cta, found);
     __syncwarp();
-    first_keys(T.keys[d], n, P.k, cta.lane);
+    first_keys(T.keys[d], n, P.k, T.best, cta.lane);
     if (cta.lane == 0) T.found[d] = 0;  // for the row after the next
 }
 
