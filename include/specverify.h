@@ -300,7 +300,7 @@ int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t d
  *   JSD beta KL(p|m) + (1 - beta) KL(q|m), m = beta p + (1 - beta) q, 0 < beta < 1;
  *   TVD 1/2 sum |p - q|.
  * A row with no list (every id -1) is not read: its loss is 0. A list with an id outside [-1, V) or one
- * twice, or with a NaN or +inf target, is bad. */
+ * twice, with a NaN or +inf target or a log-probability of 80 or more, is bad. */
 enum {
     SPECVERIFY_FKL = 0,
     SPECVERIFY_RKL = 1,

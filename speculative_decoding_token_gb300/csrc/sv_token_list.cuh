@@ -56,7 +56,7 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
         float t = -INFINITY;
         if (id >= 0) {
             t = a.t[i];
-            if (!(zk[i] < INFINITY) || !(t < INFINITY)) bits |= SPECVERIFY_STATUS_BAD_LOGIT;
+            if (!(zk[i] < INFINITY) || !(t < (P.form == SPECVERIFY_TARGET_LOGITS ? INFINITY : 80.0f))) bits |= SPECVERIFY_STATUS_BAD_LOGIT;
             // twice the same id: one of its entries finds the other in the table
             uint32_t at = (uint32_t)id * 2654435761u >> 22;
             for (int tries = 0; tries < kHash; ++tries, at = (at + 1) % kHash) {

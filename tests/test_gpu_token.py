@@ -391,6 +391,28 @@ def test_distill_bad_rows_fail_alone(svm, h):
         assert tu.close(grad[i], d.grad, d.grad_err, BF) and tu.close(loss[i], d.loss, d.loss_err)
 
 
+@pytest.mark.parametrize("kind", ["fkl", "rkl", "jsd", "tvd"])
+def test_distill_lists_of_more_than_one(svm, h, kind):
+    """Log-probabilities that leave less than nothing of one: the rest has none, and the formulas hold for what is there."""
+    z = tu.logits(4, 3001, FP, 5, device="cuda")
+    ids, t = tu.lists(z, 6, 5, short=False)
+    t[0] += 0.3 - t[0].logsumexp(0)   # 1.35 in all
+    t[1, 2] = 3.0
+    t[2] -= t[2].logsumexp(0)         # one, to a rounding
+    t[3, 0] = 81.0
+    keep = [3]
+    loss = h.distill_loss(z, ids, t, 1.0, kind)
+    grad, same = h.distill_grad(z, ids, t, None, 1.0, kind)
+    assert h.device_status() == svm.STATUS_BITS["bad_logit"]
+    assert loss.isnan().tolist() == same.isnan().tolist() == [False, False, False, True]
+    for i in range(3):
+        d = tu.Divergence(z[i], ids[i], t[i], 1.0, kind)
+        assert tu.close(loss[i], d.loss, d.loss_err), (i, float(loss[i]), float(d.loss))
+        assert tu.close(same[i], d.loss, d.loss_err)
+        assert tu.close(grad[i], d.grad, d.grad_err, FP), i
+    assert grad[keep].isnan().all()
+
+
 # ---------------------------------------------------------------------------
 # as a program runs them
 
@@ -615,6 +637,23 @@ def test_gradients_under_load_repeat(h, dtype, V, kind):
         assert tu.close(first[0][r], d.grad, d.grad_err, dtype) and tu.close(first[1][r], d.loss, d.loss_err)
         want, err = tu.Soft(z[r], 1.0).grad(int(y[r]), 1.0, 1.0)
         assert tu.close(first[2][r], want, err, dtype)
+
+
+def test_rows_under_load_repeat(h):
+    rows, V = 900, 128256
+    z = torch.randn(rows, V, device="cuda").mul_(2).to(BF)
+    y = torch.randint(0, V, (rows,), device="cuda", dtype=torch.int32)
+    top = h.token_logprobs(z, y, k=64)
+    first = None
+    for _ in range(5):
+        got = [x for k in (0, 64) for x in h.token_logprobs(z, y, k=k, rank=k == 0) if x is not None]
+        got.append(h.distill_loss(z, top.topk_idx, top.topk_logprob - 0.01, divergence="jsd"))
+        if first is None:
+            first = [x.clone() for x in got]
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    clean(h)
+    for i in range(0, rows, 90):
+        check_entry(z[i], 1.0, int(y[i]), top, i, 64)
 
 
 # ---------------------------------------------------------------------------
