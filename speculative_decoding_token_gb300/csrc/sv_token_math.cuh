@@ -136,10 +136,23 @@ __device__ __forceinline__ void ff_exp_near(float v, float &h, float &l) {
     l *= scale;
 }
 
-// e^(h + l) as a pair
+// e^(h + l), h <= 0 and l a rounding's worth of it, as a pair good to 2^-31: the same with two constants for ln 2 / 8, the first of
+// 13 bits (its products with n are exact), and one pair kept. Half the instructions that wait on one another: a gradient's stores
+// wait for this.
 __device__ __forceinline__ void ff_exp_pair(float h, float l, float &rh, float &rl) {
-    ff_exp_near(h, rh, rl);
-    rl = fmaf(rh, l, rl);
+    rh = rl = 0.0f;
+    if (!(h > -86.0f)) return;
+    const float n = rintf(h * 11.5415603f);
+    const float d = fmaf(n, -0x1.62ep-4f, h), x = fmaf(n, -0x1.0bfbe8p-18f, d), xl = fmaf(n, -0x1.0bfbe8p-18f, d - x) + l;
+    const float tail = fmaf(x * x, fmaf(x, fmaf(x, fmaf(x, 1.0f / 120.0f, 1.0f / 24.0f), 1.0f / 6.0f), 0.5f), xl);
+    const float eh = 1.0f + x, el = (x - (eh - 1.0f)) + tail;
+    const int i = (int)n;
+    const float2 t = kExp8[i & 7];
+    const float p = eh * t.x, e = fmaf(el, t.x, fmaf(eh, t.y, fmaf(eh, t.x, -p)));
+    const float scale = __uint_as_float((uint32_t)((i >> 3) + 127) << 23);
+    rh = p + e;
+    rl = (e - (rh - p)) * scale;
+    rh *= scale;
 }
 
 // ln(x + xl), xl a rounding's worth of x, as a pair of floats good to 2^-40: ff_log's head y, and what x e^-y is more than 1.
