@@ -214,7 +214,11 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
             // Here sum h is known without a look at the list: -sum p, and sum q ln(q / p) by the scout's sums. The stores need
             // not wait for the divergence (2.5 us for a list of 128). q of that logit and of the rest, and ln(q / p):
             float qh, ql;
-            ff_div(lane & 1 ? mh : wh, lane & 1 ? ml : wl, Zh, Zl, qh, ql);
+            {
+                const float nh = lane & 1 ? mh : wh, nl = lane & 1 ? ml : wl, inv = 1.0f / Zh;
+                qh = nh * inv;
+                ql = (fmaf(-qh, Zh, nh) + fmaf(-qh, Zl, nl)) * inv;
+            }
             if (kind == SPECVERIFY_FKL) {
                 known(fmaf(qh, row.over, (qh - row.p_rest) + (ql - row.p_rest_l)));
             } else {
