@@ -7,9 +7,10 @@
 // are rows enough. Slices come in chunks of 16 KiB by bulk copies into a ring of
 // shared memory; a gradient's slice comes twice, the second time backwards and
 // from L2. The warps of a CTA:
-//   consumers (8)  a chunk's vectors, four a thread: the running maximum m, the
-//                  sums s of 2^x and t of 2^x x, x = (z - m) log2(e) / T; on the
-//                  second reading, with the row's sums known, the gradient;
+//   consumers (8)  a chunk's vectors, four a thread: a reference m near the
+//                  maximum, the sums s of 2^x and t of 2^x x, x = z log2(e) / T
+//                  relative to it; on the second reading, with the row's sums
+//                  known, the gradient;
 //   scout          the next row, and what its entry asks for (its token, or its
 //                  list with the logits and probabilities of it);
 //   producer       the copies;
@@ -219,8 +220,8 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             } else if (cm > m) {
                 const float next = scaled(P, cm);
                 if (m != -INFINITY) {
-                    const float x = plain(P, m) && plain(P, cm) ? R - next : exponent(P, m - cm) - off_by(P, m) + off_by(P, cm);
-                    const float f = ex2_approx(x);
+                    float f;
+                    const float x = between(P, m, cm, f);
                     const f32x2 f2 = pack2(f, f), x2 = pack2(x, x);
                     if (Kd::Ent) {
                         t0 = mul2(f2, fma2(x2, s0, t0));
@@ -309,11 +310,6 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     const float2 a = unpack2(s0), b = unpack2(s1), e = unpack2(t0), f = unpack2(t1);
     if (Kd::Rank) before += counted<Kd::DT>(above);
     Part p{m, (a.x + a.y) + (b.x + b.y), (e.x + e.y) + (f.x + f.y), bad ? -1 : before};
-    if (plain(P, m)) {  // what R was off by
-        const float r = off_by(P, m), g = ex2_approx(-r);
-        p.t = g * fmaf(-r, p.s, p.t);
-        p.s *= g;
-    }
     p = warp_fold<Kd>(P, p);
     if constexpr (Kd::Top) {
         if (!wait_bar(S.bounded[d], row_parity, S, P)) return false;
@@ -328,7 +324,7 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
     return true;
 }
 
-// The gradient of a row's slice, 2^x (a + b x) for x = (z - m) c, the last chunk first.
+// The gradient of a row's slice, 2^x (a + b x) with the sums' x, the last chunk first.
 template <class Kd>
 __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &plan, Shared &S, const Cta &cta, int d,
                                             uint32_t row_parity, Cursor &cur) {
@@ -347,11 +343,7 @@ __device__ __forceinline__ bool store_slice(const TokenParams &P, const Plan &pl
     const float c = P.c, R = scaled(P, m);
     const bool near = plain(P, m);
     constexpr bool kFine = Kd::List && Kd::DT == SV_DT_FP32;  // bf16 gradients have no use for c_lo
-    if (near) {
-        const float r = kFine ? off_by(P, m) : fmaf(m, c, -R), g = ex2_approx(-r);
-        fa = g * fmaf(-r, fb, fa);
-        fb *= g;
-    }
+    if (near && Kd::List && !kFine) fa *= ex2_approx(m * P.c_lo);
     const f32x2 nR = pack2(-R, -R), c2 = pack2(c, c), a2 = pack2(fa, fa), b2 = pack2(fb, fb);
     auto exponents = [&](f32x2 z2) {
         const f32x2 x2 = fma2(z2, c2, nR);
@@ -718,8 +710,15 @@ __device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, co
         S.coef[d] = good ? make_float4(p.m, a, b, 0.0f) : make_float4(0.0f, NAN, NAN, 0.0f);
         mbar_arrive(smem_u32(&S.known[d]));
     }
-    if (good) ff_logprob(P, row.zy, p.m, lh, ll, lp, lo);
-    else if (bad) lp = H = NAN;
+    float mh = lh, ml = ll;  // of the sum relative to p.m
+    if (good) {
+        float oh, ol;
+        ff_off_by(P, p.m, oh, ol);
+        ff_add(lh, ll, -oh, -ol, mh, ml);
+        ff_logprob(P, row.zy, p.m, mh, ml, lp, lo);
+    } else if (bad) {
+        lp = H = NAN;
+    }
     if (lane == 0 && cta.rank == 0) {
         if (P.logprob) P.logprob[e] = lp;
         if (P.entropy) P.entropy[e] = H;
@@ -727,7 +726,7 @@ __device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, co
             float xh = 0.0f, xl = 0.0f;
             if (good) {
                 over_T(P, p.m, 0.0f, xh, xl);
-                if (fabsf(xh) < INFINITY) ff_add(xh, xl, lh, ll, xh, xl);
+                if (fabsf(xh) < INFINITY) ff_add(xh, xl, mh, ml, xh, xl);
             }
             P.lse[e] = bad ? NAN : xh;
         }
@@ -778,7 +777,12 @@ __device__ __forceinline__ void finish_top(const TokenParams &P, const Plan &pla
             }
             const bool good = state == kLive && p.n >= 0 && p.m > -INFINITY;
             float lh = 0.0f, ll = 0.0f;
-            if (good) ff_log(p.s, lh, ll);
+            if (good) {
+                float oh, ol;
+                ff_off_by(P, p.m, oh, ol);
+                ff_log(p.s, lh, ll);
+                ff_add(lh, ll, -oh, -ol, lh, ll);
+            }
             for (int i = lane; i < k; i += 32) {
                 if (good) {
                     write_top<Kd::DT>(P, row.entry, i, T.best[i], p.m, lh, ll);

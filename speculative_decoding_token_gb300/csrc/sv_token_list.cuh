@@ -75,25 +75,28 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
     bits = __reduce_or_sync(all, bits);
     float p_rest = 0.0f, p_rest_l = 0.0f, rest_h = -INFINITY, rest_l = 0.0f, over = 0.0f, p0 = 0.0f, p0_l = 0.0f, lp0 = 0.0f, zsum = 0.0f, zsum_l = 0.0f, cross = 0.0f;
     const bool rkl = P.divergence == SPECVERIFY_RKL;
+    float lh = 0.0f, ll = 0.0f;
     zmax = warp_max(zmax);
     if (!bits) {
         if (P.form == SPECVERIFY_TARGET_LOGITS) {
             top = warp_max(top);
-            float sum = 0.0f, lh = 0.0f, ll = 0.0f;
+            float sum = 0.0f, suml = 0.0f;
             for (int j = lane; j < P.K; j += 32) {
-                float h, l;
+                float h, l, wh, wl;
+                if (llp[j] == -INFINITY) continue;
                 ff_logprob(P, llp[j], top, 0.0f, 0.0f, h, l);
-                sum += llp[j] == -INFINITY ? 0.0f : ff_exp(h, l);
+                ff_exp_pair(h, l, wh, wl);
+                ff_add(sum, suml, wh, wl, sum, suml);
             }
-            sum = warp_sum(sum);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                ff_add(sum, suml, __shfl_xor_sync(all, sum, off), __shfl_xor_sync(all, suml, off), sum, suml);
             if (top == -INFINITY) bits = SPECVERIFY_STATUS_BAD_LOGIT;  // a target of nothing
-            else ff_log(sum, lh, ll);
+            else ff_log_near(sum, suml, lh, ll);  // (the epilogue makes log-probabilities of them once more, in pairs)
             for (int j = lane; j < P.K; j += 32) {
                 float h, l;
                 ff_logprob(P, llp[j], top, lh, ll, h, l);
-                if (llp[j] == -INFINITY) h = -INFINITY;
-                llp[j] = h;
-                lpr[j] = ff_exp(h, 0.0f);
+                lpr[j] = llp[j] == -INFINITY ? 0.0f : ff_exp(h, l);
             }
         } else {
             // One less a sum close to it: in pairs of floats, or little would be left of it.
@@ -154,6 +157,9 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
         row.p0 = p0;
         row.p0_l = p0_l;
         row.lp0 = lp0;
+        row.tmax = top;
+        row.t_h = lh;
+        row.t_l = ll;
         row.zsum = zsum;
         row.zsum_l = zsum_l;
         row.cross = cross;
@@ -165,11 +171,11 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
 template <class Kd>
 __device__ __forceinline__ void fix_list(const TokenParams &P, const Shared &S, const Lists &L, const Cta &cta, int d) {
     if (!S.good[d]) return;
-    const float w = S.row[d].g * P.inv_hi, C = S.fix[d];
+    const float w = S.row[d].g * P.inv_hi;
     for (int j = cta.lane; j < P.K; j += 32) {
         const int at = d * L.stride + j, id = L.ids[at], v = id / Kd::kPer;
         if (id >= 0 && v >= cta.slice0 && v < cta.slice0 + cta.slice_vecs)
-            store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, id, w * (L.lp[at] - L.z[at] * C));
+            store_logit<Kd::DT>(P.grad + S.row[d].entry * P.grad_stride_bytes, id, w * L.lp[at]);
     }
 }
 
@@ -199,13 +205,15 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
     };
     // The weights e^((z - M) / T) of the list's largest logit (even lanes) and of the rest's reference (odd lanes), and the
     // normaliser.
-    float Zh = 1.0f, Zl = 0.0f;
+    float Zh = 1.0f, Zl = 0.0f, oh = 0.0f, ol = 0.0f, t0 = 0.0f;
     if (good) {
         float dh, dl, wh = 0.0f, wl = 0.0f, mh, ml;
+        ff_off_by(P, p.m, oh, ol);
         two_sum(lane & 1 ? p.m : row.zmax, -M, dh, dl);
         if (dh > P.far) {
             float xh, xl;
             over_T(P, dh, dl, xh, xl);
+            if (lane & 1) ff_add(xh, xl, -oh, -ol, xh, xl);
             ff_exp_pair(xh, xl, wh, wl);
         }
         ff_mul(wh, wl, lane & 1 ? p.s : row.zsum, lane & 1 ? 0.0f : row.zsum_l, mh, ml);
@@ -224,9 +232,13 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
             } else {
                 const float ph = lane & 1 ? fmaxf(row.p_rest, 0x1p-20f) : row.p0, more = ((qh - ph) + (ql - (lane & 1 ? row.p_rest_l : row.p0_l))) / ph;
                 const float t = fabsf(more) < 0.5f ? log1pf(more) : logf(qh) - (lane & 1 ? row.rest_h : row.lp0);
-                const float part = qh > 0.0f ? lane & 1 ? qh * t : qh * fmaf(row.zsum, t, row.cross) : 0.0f;
-                C = part + __shfl_xor_sync(all, part, 1);
-                known(qh > 0.0f ? qh * (t - C) : 0.0f);
+                // All relative to that logit's ln(q / p), t0, or gradients of a draft that is sure would be lost in it.
+                const float q0 = __shfl_sync(all, qh, 0), qr = __shfl_sync(all, qh, 1), t1 = __shfl_sync(all, t, 1);
+                t0 = __shfl_sync(all, t, 0);
+                if (!(q0 > 0.0f)) t0 = 0.0f;
+                const float gap = qr > 0.0f ? t1 - t0 : 0.0f, listed = q0 > 0.0f ? q0 * row.cross : 0.0f;
+                C = fmaf(qr, gap, listed);
+                known(qr > 0.0f ? qr * fmaf(gap, q0 * row.zsum, -listed) : 0.0f);
             }
         }
     } else if (Kd::Grad) {
@@ -243,7 +255,10 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
         sl = __shfl_sync(all, sl, 1);
         if (some) {
             ff_logprob(P, p.m, M, zh, zl, qh, ql);
-            if (qh > -INFINITY) ff_add(qh, ql, sh, sl, qh, ql);
+            if (qh > -INFINITY) {
+                ff_add(sh, sl, -oh, -ol, sh, sl);
+                ff_add(qh, ql, sh, sl, qh, ql);
+            }
             q_rest = ff_exp(qh, ql);
         }
         r_rest = (row.rest_h - qh) + (row.rest_l - ql);
@@ -253,7 +268,7 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
         return fmaf(q, row.over, fabsf(r) < 0.5f ? pr * expm1f(-r) : q - pr);
     };
     if (good) {
-        float f = 0.0f, h = 0.0f, h_rest = 0.0f;
+        float f = 0.0f, h = 0.0f, up = 0.0f, h_rest = 0.0f;
         // outcome K is the rest
         for (int j = lane; j <= K; j += 32) {
             const bool rest = j == K;
@@ -265,7 +280,9 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
                 ff_logprob(P, L.z[at], M, zh, zl, h, l);
                 q = ff_exp(h, l);
                 pr = L.p[at];
-                r = (L.lp[at] - h) - l;
+                float ph = L.lp[at], pl = 0.0f;
+                if (P.form == SPECVERIFY_TARGET_LOGITS) ff_logprob(P, ph, row.tmax, row.t_h, row.t_l, ph, pl);
+                r = (ph - h) + (pl - l);
             }
             float fj, hj;
             if (kind == SPECVERIFY_FKL) {
@@ -273,7 +290,7 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
                 hj = missing(pr, q, r);  // (with q C)
             } else if (kind == SPECVERIFY_RKL) {
                 fj = divergence_of(q, rest ? fmaxf(pr, 0x1p-20f) : pr, -r);
-                hj = q > 0.0f ? q * (-r - C) : 0.0f;  // (with q C)
+                hj = q > 0.0f ? q * ((-r - t0) - C) : 0.0f;  // (with q C)
             } else if (kind == SPECVERIFY_TVD) {
                 const bool near = fabsf(r) < 0.5f;
                 fj = 0.5f * fabsf(near ? pr * expm1f(-r) : pr - q);
@@ -283,11 +300,16 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
                 const float b = P.beta, m = b * pr + (1.0f - b) * q;
                 const float u = q > 0.0f ? ln_mixed(b, pr > 0.0f ? r : -INFINITY) : 0.0f;
                 const float v = pr > 0.0f ? ln_mixed(1.0f - b, q > 0.0f ? -r : -INFINITY) : 0.0f;
-                hj = -(1.0f - b) * q * u;
+                hj = -(1.0f - b) * u;  // (less q C, and times q, below)
                 fj = b * divergence_of(pr, m, -v) + (1.0f - b) * divergence_of(q, m, -u);
             }
             f += fj;
-            h += hj;
+            if (kind == SPECVERIFY_TVD) {  // what C is less than a half (h > 0), and more than minus a half (h < 0)
+                h += hj < 0.0f ? q : hj == 0.0f ? 0.5f * q : 0.0f;
+                up += hj > 0.0f ? q : hj == 0.0f ? 0.5f * q : 0.0f;
+            } else {
+                h += hj;
+            }
             if (rest) {
                 h_rest = hj;
             } else if (Kd::Grad) {
@@ -298,17 +320,41 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
         loss = warp_sum(f);
         if (kind == SPECVERIFY_FKL) loss += row.over;
         if (kind == SPECVERIFY_RKL) loss -= row.over;
-        if (Kd::Grad && early) C = 0.0f;
         if (Kd::Grad && !early) {
             C = warp_sum(h);
-            known(__shfl_sync(all, h_rest, K & 31) - q_rest * C);
+            h_rest = __shfl_sync(all, h_rest, K & 31);
+            if (kind == SPECVERIFY_TVD) {
+                up = warp_sum(up);
+                auto left = [&](float hj, float q) { return hj > 0.0f ? q * C : hj < 0.0f ? -q * up : 0.5f * q * (C - up); };
+                known(left(h_rest, q_rest));
+                for (int j = lane; j < K; j += 32) L.lp[d * L.stride + j] = left(L.lp[d * L.stride + j], L.z[d * L.stride + j]);
+            } else {
+                // Relative to the likeliest outcome's, or gradients of a draft that is sure would be lost in it.
+                float most = lane == 0 ? q_rest : 0.0f, ref = h_rest;
+                for (int j = lane; j < K; j += 32) {
+                    const int at = d * L.stride + j;
+                    if (L.ids[at] >= 0 && L.z[at] > most) {
+                        most = L.z[at];
+                        ref = L.lp[at];
+                    }
+                }
+                const unsigned who = __ballot_sync(all, most == warp_max(most));
+                ref = __shfl_sync(all, ref, __ffs(who) - 1);
+                C = lane == 0 ? q_rest * (h_rest - ref) : 0.0f;
+                for (int j = lane; j < K; j += 32) {
+                    const int at = d * L.stride + j;
+                    if (L.ids[at] < 0) continue;
+                    L.lp[at] -= ref;
+                    C = fmaf(L.z[at], L.lp[at], C);
+                }
+                C = warp_sum(C);
+                known(q_rest * ((h_rest - ref) - C));
+                for (int j = lane; j < K; j += 32) L.lp[d * L.stride + j] = L.z[d * L.stride + j] * (L.lp[d * L.stride + j] - C);
+            }
         }
     }
     if (lane == 0 && cta.rank == 0) P.loss[e] = loss;
-    if (Kd::Grad && lane == 0) {
-        S.fix[d] = C;
-        S.good[d] = good;
-    }
+    if (Kd::Grad && lane == 0) S.good[d] = good;
 }
 
 }  // namespace

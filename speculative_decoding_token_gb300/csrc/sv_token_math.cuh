@@ -191,20 +191,42 @@ __device__ __forceinline__ float warp_max(float x) {
 // Logits, and differences of them, are told from -inf down to P.far, -2^25 / c: of no weight either way (with |R| < 2^24), and
 // a weight's product with its exponent is 0 and not NaN, also with an entropy's factor between them (below 2^100).
 
-// Of a reference nearer to zero than this, exponents are z c - R with R = m c rounded: one FMA, whose product is exact. |R| <
-// 2^24, so that R is off by a half at most, and that is made good in the sum. Others take (z - m) c, with the difference first.
-__device__ __forceinline__ bool plain(const TokenParams &P, float m) { return fabsf(m) < P.near; }
-
-// R (rounded: no sum takes the product exactly)
-__device__ __forceinline__ float scaled(const TokenParams &P, float m) { return __fmul_rn(m, P.c); }
-
-// What m c is more than the R that is taken of it.
-__device__ __forceinline__ float off_by(const TokenParams &P, float m) { return plain(P, m) ? fmaf(m, P.c, -scaled(P, m)) + m * P.c_lo : 0.0f; }
-
 // (z - m) log2(e) / T of a difference
 __device__ __forceinline__ float exponent(const TokenParams &P, float d) {
     d = fmaxf(d, P.far);
     return fmaf(d, P.c_lo, d * P.c);
+}
+
+// Of a reference nearer to zero than this, exponents are z c - R with R = m c rounded down to a whole number: one FMA, whose product
+// is exact, and going from one reference to another multiplies by a power of two. |R| <= 2^24. Others take (z - m) c, with the
+// difference first.
+__device__ __forceinline__ bool plain(const TokenParams &P, float m) { return fabsf(m) < P.near; }
+__device__ __forceinline__ float scaled(const TokenParams &P, float m) { return floorf(__fmul_rn(m, P.c)); }
+
+// What m c is more than R; 0 of others.
+__device__ __forceinline__ float off_by(const TokenParams &P, float m) { return plain(P, m) ? fmaf(m, P.c, -scaled(P, m)) + m * P.c_lo : 0.0f; }
+
+// The same times ln 2, as a pair: what the logarithm of a sum is less where it is taken relative to m.
+__device__ __forceinline__ void ff_off_by(const TokenParams &P, float m, float &h, float &l) {
+    h = l = 0.0f;
+    if (!plain(P, m)) return;
+    const float p = __fmul_rn(m, P.c);
+    float oh, ol;
+    ff_add(p - floorf(p), 0.0f, fmaf(m, P.c, -p), m * P.c_lo, oh, ol);
+    ff_mul(oh, ol, kLn2Hi, kLn2Lo, h, l);
+}
+
+// The exponent x by which sums relative to `from` become sums relative to `to`, not less than it, and 2^x.
+__device__ __forceinline__ float between(const TokenParams &P, float from, float to, float &f) {
+    float x;
+    if (plain(P, from) && plain(P, to)) {
+        x = scaled(P, from) - scaled(P, to);
+        f = __uint_as_float((uint32_t)(127 + (int)fmaxf(x, -127.0f)) << 23);
+    } else {
+        x = exponent(P, from - to) - off_by(P, from) + off_by(P, to);
+        f = ex2_approx(x);
+    }
+    return x;
 }
 
 // P.far as logits2 takes it

@@ -61,12 +61,12 @@ struct Row {
     // the draft's largest logit z of it and (RKL) its p and ln p, the sum of e^((z_k - z) / T), and (RKL) of that times (z_k - z) / T -
     // (ln p_k - ln p)
     float zmax, p0, p0_l, lp0, zsum, zsum_l, cross;
+    float tmax, t_h, t_l;  // the target's largest logit, and the logarithm of the sum relative to it
     float g, h;    // what the gradient is multiplied by
 };
 
-// Sums over part of a row: s of 2^x and t of 2^x x, x = (z - m) c, m a logit
-// near the largest (-inf where there is none but -inf); n tokens before the given
-// one, -1: a bad logit.
+// Sums over part of a row: s of 2^x and t of 2^x x, x = z c - R, or (z - m) c (see plain), m a logit near the largest (-inf where
+// there is none but -inf); n tokens before the given one, -1: a bad logit.
 struct Part {
     float m, s, t;
     int n;
@@ -82,7 +82,7 @@ struct Shared {
     Row row[kDepth];
     Part part[kDepth][kConsumers];  // of the CTA's warps where a row is one CTA's
     float4 coef[kDepth];  // of the gradient: m, a, b (see store_slice)
-    float fix[kDepth];    // the given token's gradient, or what a list's needs
+    float fix[kDepth];    // the given token's gradient (a list's tokens': Lists::lp)
     int good[kDepth];
     int asked;            // requests made (the first CTA's)
     int32_t abort;
@@ -105,7 +105,7 @@ struct SharedTop {
 struct Lists {
     int32_t *ids;
     float *z;    // the draft's logits of them
-    float *lp;   // the target's log-probabilities
+    float *lp;   // the target's log-probabilities, or its logits
     float *p;    // and probabilities
     int32_t *hash;
     int stride;
@@ -144,8 +144,8 @@ __device__ __forceinline__ void merge(const TokenParams &P, Part &a, const Part 
         return;
     }
     const float m = fmaxf(a.m, b.m);
-    const float xa = exponent(P, a.m - m), xb = exponent(P, b.m - m);
-    const float fa = ex2_approx(xa), fb = ex2_approx(xb);
+    float fa, fb;
+    const float xa = between(P, a.m, m, fa), xb = between(P, b.m, m, fb);
     a.t = fa * fmaf(xa, a.s, a.t) + fb * fmaf(xb, b.s, b.t);
     a.s = fa * a.s + fb * b.s;
     a.m = m;
@@ -157,7 +157,8 @@ __device__ __forceinline__ Part warp_fold(const TokenParams &P, Part a) {
     constexpr uint32_t all = 0xffffffffu;
     Part r;
     r.m = from_order_bits(__reduce_max_sync(all, order_bits(a.m)));
-    const float x = exponent(P, a.m - r.m), f = a.m == -INFINITY ? 0.0f : ex2_approx(x);
+    float f = 0.0f, x = 0.0f;
+    if (a.m > -INFINITY) x = between(P, a.m, r.m, f);
     r.s = f * a.s;
     r.t = Kd::Ent && f > 0.0f ? f * fmaf(x, a.s, a.t) : 0.0f;
 #pragma unroll

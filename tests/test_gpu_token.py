@@ -770,6 +770,39 @@ def test_small_divergences(h, kind, K, T, dtype):
         assert abs(float(same[i]) - float(d.loss)) <= lim
 
 
+@pytest.mark.parametrize("kind,form", FORMS)
+@pytest.mark.parametrize("on", [0, None], ids=["listed", "rest"])
+def test_gradients_of_sure_drafts(h, kind, form, on):
+    """A draft with all but 2^-14 of its mass on one outcome: gradients and losses are of that size, and good to a few roundings
+    of it (each term's logarithms to 2^-22 of themselves and 2^-36 of one, its factors to 2^-21) and to the share that the rest's sum is off
+    by, which moves that much mass times the other's."""
+    V, K = 40000, 7
+    z = tu.logits(6, V, FP, 14, device="cuda") * 0.25
+    ids, t = tu.lists(z, K, 14, form, noise=0.3, short=False)
+    for r in range(6):
+        free = next(v for v in range(V) if not (ids[r] == v).any())
+        v = int(ids[r, 0]) if on == 0 else free
+        others = torch.logsumexp(z[r].double(), 0)
+        z[r, v] = float(others) + 9.7
+        if form == "logprobs":  # the target is sure of the same
+            small = torch.rand(K, device="cuda").mul_(2.0 ** -16).add_(2.0 ** -18)
+            t[r] = torch.log(small)
+            if on == 0:
+                t[r, 0] = torch.log1p(-small[1:].sum() - 2.0 ** -15)
+        elif on == 0:
+            t[r] = torch.tensor([12.0] + [0.5 * k for k in range(K - 1)], device="cuda")
+    grad, loss = h.distill_grad(z, ids, t, None, 1.0, kind, form=form)
+    clean(h)
+    for r in range(6):
+        d = tu.Divergence(z[r], ids[r], t[r], 1.0, kind, form)
+        q_rest = 1 - float(d.soft.p[ids[r].long()].sum())
+        moved = d.soft.sum_err * q_rest * (1 - q_rest) + 2.0 ** -36
+        size = d.grad.abs()
+        lim = 2.0 ** -19 * size + 4 * moved * d.soft.p.clamp(min=2.0 ** -40) ** 0.5 + 2.0 ** -20 * size.max() * d.soft.p ** 0.5
+        assert ((grad[r].double() - d.grad).abs() <= lim).all(), (r, float(((grad[r].double() - d.grad).abs() - lim).max()))
+        assert abs(float(loss[r]) - float(d.loss)) <= 2.0 ** -20 * float(d.loss) + 16 * moved
+
+
 # ---------------------------------------------------------------------------
 # waits that run out
 
