@@ -774,8 +774,8 @@ def test_small_divergences(h, kind, K, T, dtype):
 @pytest.mark.parametrize("on", [0, None], ids=["listed", "rest"])
 def test_gradients_of_sure_drafts(h, kind, form, on):
     """A draft with all but 2^-14 of its mass on one outcome: gradients and losses are of that size, and good to a few roundings
-    of it (each term's logarithms to 2^-22 of themselves and 2^-36 of one, its factors to 2^-21) and to the share that the rest's sum is off
-    by, which moves that much mass times the other's."""
+    of it (each term's logarithms to 2^-22 of themselves and 2^-36 of one, its factors to 2^-21) and to the share that the
+    rest's sum is off by, which moves that much mass times the other's."""
     V, K = 40000, 7
     z = tu.logits(6, V, FP, 14, device="cuda") * 0.25
     ids, t = tu.lists(z, K, 14, form, noise=0.3, short=False)
