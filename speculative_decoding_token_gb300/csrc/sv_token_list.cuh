@@ -157,6 +157,10 @@ __device__ __forceinline__ void scout_list(const TokenParams &P, Row &row, const
         row.p0 = p0;
         row.p0_l = p0_l;
         row.lp0 = lp0;
+        if (rkl) {
+            row.p0_inv = 1.0f / p0;
+            row.rest_inv = 1.0f / fmaxf(p_rest, 0x1p-20f);
+        }
         row.tmax = top;
         row.t_h = lh;
         row.t_l = ll;
@@ -230,7 +234,8 @@ __device__ __forceinline__ void finish_list(const TokenParams &P, Shared &S, con
             if (kind == SPECVERIFY_FKL) {
                 known(fmaf(qh, row.over, (qh - row.p_rest) + (ql - row.p_rest_l)));
             } else {
-                const float ph = lane & 1 ? fmaxf(row.p_rest, 0x1p-20f) : row.p0, more = ((qh - ph) + (ql - (lane & 1 ? row.p_rest_l : row.p0_l))) / ph;
+                const float ph = lane & 1 ? fmaxf(row.p_rest, 0x1p-20f) : row.p0;
+                const float more = ((qh - ph) + (ql - (lane & 1 ? row.p_rest_l : row.p0_l))) * (lane & 1 ? row.rest_inv : row.p0_inv);
                 const float t = fabsf(more) < 0.5f ? log1pf(more) : logf(qh) - (lane & 1 ? row.rest_h : row.lp0);
                 // All relative to that logit's ln(q / p), t0, or gradients of a draft that is sure would be lost in it.
                 const float q0 = __shfl_sync(all, qh, 0), qr = __shfl_sync(all, qh, 1), t1 = __shfl_sync(all, t, 1);

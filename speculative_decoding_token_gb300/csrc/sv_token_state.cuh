@@ -61,6 +61,7 @@ struct Row {
     // the draft's largest logit z of it and (RKL) its p and ln p, the sum of e^((z_k - z) / T), and (RKL) of that times (z_k - z) / T -
     // (ln p_k - ln p)
     float zmax, p0, p0_l, lp0, zsum, zsum_l, cross;
+    float p0_inv, rest_inv;  // (RKL) 1 / p of it and 1 / p of the rest, no less than 2^-20
     float tmax, t_h, t_l;  // the target's largest logit, and the logarithm of the sum relative to it
     float g, h;    // what the gradient is multiplied by
 };
