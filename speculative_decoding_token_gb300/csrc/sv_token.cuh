@@ -23,6 +23,12 @@
 // No warp waits for the end of a row but the consumers of a gradient. Rows are
 // taken over from CTAs (clusters) that have not begun, one at a time, when the
 // copies of the row before are on their way: CTAs differ by a sixth in speed.
+//
+// Bound by HBM: a row's logits once (twice and a gradient for gradients, one of
+// the readings from L2). Measured, rows of 152064 bf16 logits: 2000 rows' log-
+// probabilities and entropies 91 us (6.7 TB/s), with ranks 107, with 64 top
+// tokens 125 (both by instructions); 2048 rows' gradients 198 (5.9 TB/s); 1111
+// rows of 128256, divergences from lists of 64, 47.7 (5.4 TB/s).
 #pragma once
 
 #include "sv_token_list.cuh"
@@ -248,6 +254,33 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
             top->most[d][i >> plan.group_log][tid] =
                 (uint16_t)((Kd::DT == SV_DT_FP32 ? group : max_bf16x2(group, group << 16)) >> 16);
         }
+        if (Kd::Rank) {
+            const int first = cta.slice0 + i * Kd::kChunkVecs;
+            const bool inf = bound_before == bound_after;
+            if (y_vec < first || (y_vec >= first + Kd::kChunkVecs && !inf)) {
+                // One bound for the chunk, and nothing to count where no logit is larger. (2000 rows of 152064 bf16: 107 us for any
+                // tokens, 104 for likely ones, 91 without ranks; 121 with a bound for each vector, and behind the exponentials.)
+                const uint32_t bound = y_vec < first ? bound_after : bound_before;
+                if (beyond<Kd::DT>(all, bound)) {
+#pragma unroll
+                    for (int j = 0; j < kVecs; ++j) above += count_above<Kd::DT>(w[j], bound);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const int v = first + tid + j * kTeam;
+                    if (v == y_vec || (inf && v < y_vec)) {
+                        if (v < cta.slice0 + cta.slice_vecs) before += count_before<Kd>(w[j], S.row[d].zy, S.row[d].y, v * kPer);
+                    } else {
+                        above += count_above<Kd::DT>(w[j], v < y_vec ? bound_before : bound_after);
+                    }
+                }
+            }
+            if ((i & 1023) == 1023) {  // what is packed into half a word does not overflow
+                before += counted<Kd::DT>(above);
+                above = 0;
+            }
+        }
         if (plain(P, m)) {
             const f32x2 nR = pack2(-R, -R);
 #pragma unroll
@@ -279,23 +312,6 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                     s0 = add2(s0, e2);
                     if (Kd::Ent) t0 = fma2(e2, x2, t0);
                 }
-            }
-        }
-        if (Kd::Rank) {
-            const int v0 = cta.slice0 + i * Kd::kChunkVecs + tid;
-            const bool inf = bound_before == bound_after;
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int v = v0 + j * kTeam;
-                if (v == y_vec || (inf && v < y_vec)) {
-                    if (v < cta.slice0 + cta.slice_vecs) before += count_before<Kd>(w[j], S.row[d].zy, S.row[d].y, v * kPer);
-                } else {
-                    above += count_above<Kd::DT>(w[j], v < y_vec ? bound_before : bound_after);
-                }
-            }
-            if ((i & 1023) == 1023) {  // what is packed into half a word does not overflow
-                before += counted<Kd::DT>(above);
-                above = 0;
             }
         }
     }
