@@ -83,6 +83,24 @@ def test_logprobs_values(h, kind, dtype, V, k, T):
         check_entry(z[i], T, int(y[i]), r, i, k)
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "rising", "masked"])
+@pytest.mark.parametrize("dtype,V,k", [(BF, 152064, 5), (BF, 150001, 16), (FP, 256000, 8), (FP, 131077, 3), (BF, 131072, 32)])
+def test_alternatives_of_few_long_rows(svm, h, kind, dtype, V, k):
+    """Rows that clusters share, each CTA's own top tokens put in order once more; one that asks for nothing, one that is bad."""
+    z = tu.logits(5, V, dtype, V + k, kind, device="cuda")
+    y = torch.tensor([0, V - 1, -1, V // 2, 1], device="cuda", dtype=torch.int32)
+    z[3, V - 2] = math.nan
+    r = h.token_logprobs(z, y, 0.5, k=k, rank=True)
+    assert h.device_status() == svm.STATUS_BITS["bad_logit"]
+    for i in (0, 1, 4):
+        check_entry(z[i], 0.5, int(y[i]), r, i, k)
+    assert (r.topk_idx[2:4] == -1).all() and (r.topk_logprob[2] == -math.inf).all() and r.topk_logprob[3].isnan().all()
+    assert float(r.logprob[2]) == 0 and r.logprob[3].isnan() and r.rank.tolist()[2:4] == [0, -1]
+    one = h.token_logprobs(z[4:], y[4:], 0.5, k=k, rank=True)
+    clean(h)
+    check_entry(z[4], 0.5, 1, one, 0, k)
+
+
 @pytest.mark.parametrize("k,entropy,lse,rank", [(0, True, True, False), (0, False, False, False), (0, False, False, True),
                                                 (5, False, True, False), (5, True, False, True)])
 def test_logprobs_outputs_not_asked_for(h, k, entropy, lse, rank):
@@ -806,12 +824,12 @@ def test_gradients_of_sure_drafts(h, kind, form, on):
 # ---------------------------------------------------------------------------
 # waits that run out
 
-@pytest.mark.parametrize("rows", [3, 60], ids=["clusters", "rows"])
-def test_waits_that_run_out(svm, rows):
+@pytest.mark.parametrize("rows,V", [(3, 50001), (60, 50001), (3, 140001)], ids=["clusters", "rows", "long"])
+def test_waits_that_run_out(svm, rows, V):
     """With a limit of a nanosecond a call gives up at the first wait that lasts a microsecond, and says so; the next call,
     with the default limit, is right. (Not every call has such a wait every time.)"""
     h = svm.SpecVerify(1, 1, 1000)
-    z, y, ids, t = inputs(31, rows=rows, V=50001)
+    z, y, ids, t = inputs(31, rows=rows, V=V)
     one = torch.ones(rows, device="cuda")
     cold, late = torch.zeros(1 << 26, device="cuda"), 0  # more than L2 holds
     for run in (lambda: [x for x in h.token_logprobs(z, y, rank=True) if x is not None],
