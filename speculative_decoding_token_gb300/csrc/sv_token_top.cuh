@@ -80,20 +80,25 @@ struct Chooser {
     const char *row;
     const Cta &cta;
     int log;
+    float bound;           // a number that k tokens reach
     uint32_t bound2, high2;
-    float low, high;
+    float low, high;       // its class
 
     __device__ __forceinline__ Chooser(const TokenParams &P_, const Plan &plan, const char *row_, const SharedTop &T, int d, const Cta &cta_)
         : P(P_), row(row_), cta(cta_), log(plan.group_log) {
-        const float least = from_order_bits(__reduce_min_sync(0xffffffffu, cta.lane < kConsumers ? T.bound[d][cta.lane] : ~0u));
-        const uint32_t bound = __float_as_uint(least) >> 16;
-        bound2 = bound | bound << 16;
-        low = high = __uint_as_float(bound << 16);
+        set(from_order_bits(__reduce_min_sync(0xffffffffu, cta.lane < kConsumers ? T.bound[d][cta.lane] : ~0u)));
+    }
+
+    __device__ __forceinline__ void set(float x) {
+        bound = x;
+        const uint32_t upper = __float_as_uint(x) >> 16;
+        bound2 = upper | upper << 16;
+        low = high = __uint_as_float(upper << 16);
         if (DT == SV_DT_FP32 && fabsf(low) < INFINITY) {
-            const float far = __uint_as_float(bound << 16 | 0xffffu);
-            if (least < 0.0f) low = far;
+            const float far = __uint_as_float(upper << 16 | 0xffffu);
+            if (x < 0.0f) low = far;
             else high = far;
-            if ((bound & 0x7fffu) == 0) {  // both zeros' classes are one
+            if ((upper & 0x7fffu) == 0) {  // both zeros' classes are one
                 low = __uint_as_float(0x8000ffffu);
                 high = __uint_as_float(0x0000ffffu);
             }
@@ -183,7 +188,71 @@ struct Chooser {
             if (!f(w, v)) return;
         }
     }
+
+    __device__ __forceinline__ int rows() const { return (cta.chunks + (1 << log) - 1) >> log; }
+
+    // A row of the groups' maxima, eight a lane: those above the class, or in it too.
+    __device__ __forceinline__ uint32_t groups_of(const SharedTop &T, int d, int r, bool equal) const {
+        const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][cta.lane * 8]);
+        return groups(w, false) | (equal ? groups(w, true) : 0u);
+    }
+
+    // A vector's tokens larger than the bound itself, or equal to it: bit u for token u. (What stands in for tokens that are
+    // not there is -inf.)
+    __device__ __forceinline__ uint32_t past_bound(const uint4 &w, int v, bool equal) const {
+        float x[kPer];
+        vec_floats<DT>(w, x);
+        uint32_t in = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) in |= (equal ? x[u] == bound && v >= 0 && v * kPer + u < P.V : x[u] > bound) ? 1u << u : 0u;
+        return in;
+    }
+
+    // Calls f(vectors, their indexes) over the vectors of all groups that may hold tokens larger than the bound.
+    template <class F>
+    __device__ __forceinline__ void each_past_bound(SharedTop &T, int d, F &&f) const {
+        const bool equal = bound < high;
+        for (int r = 0, n = rows(); r < n; ++r) {
+            uint32_t in = groups_of(T, d, r, equal);
+            int total, to = lanes_before(__popc(in), cta.lane, total);
+            for (; in; in &= in - 1, ++to) T.kept[to] = (uint16_t)(r * kTeam + cta.lane * 8 + group_of(in));
+            __syncwarp();
+            each(total << (2 + log), [&](int j) { return vector(T.kept[j >> (2 + log)], j & ((4 << log) - 1)); }, f);
+            __syncwarp();
+        }
+    }
 };
+
+// The k-th largest (k from 1) of the order bits that visit(f) calls f with, down to bit `last`, a digit of eight bits at a time
+// by counting; false where there are fewer.
+template <class Visit>
+__device__ __forceinline__ bool nth_of(unsigned *bins, int k, int last, int lane, uint32_t &nth, Visit &&visit) {
+    constexpr uint32_t all = 0xffffffffu;
+    uint32_t mask = 0;
+    nth = 0;
+    for (int shift = 24; shift >= last; shift -= 8) {
+        for (int i = lane; i < 256; i += 32) bins[i] = 0;
+        __syncwarp();
+        visit([&](uint32_t u) {
+            if ((u & mask) == nth) atomicAdd(&bins[u >> shift & 255u], 1u);
+        });
+        __syncwarp();
+        // lane l has digits 255 - 8 l and the seven below it
+        int digit = 255 - 8 * lane, mine = 0, total;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) mine += (int)bins[digit - q];
+        int left = k - lanes_before(mine, lane, total);
+        if (total < k) return false;
+        const unsigned who = __ballot_sync(all, left > 0 && left <= mine);
+        if (left > 0 && left <= mine)
+            while (left > (int)bins[digit]) left -= (int)bins[digit--];
+        k = __shfl_sync(all, left, __ffs(who) - 1);
+        nth |= (uint32_t)__shfl_sync(all, digit, __ffs(who) - 1) << shift;
+        mask |= 255u << shift;
+        __syncwarp();
+    }
+    return true;
+}
 
 // A consumer warp's share of a row's top tokens, once all warps have said their bounds: an eighth of the groups' maxima, and
 // the vectors of those above the bound's class read again (of a row of 152064 bf16 logits and k = 64, 115 of 4864 groups and
@@ -232,106 +301,152 @@ __device__ __noinline__ void gather_top(const TokenParams &P, const Plan &plan, 
     });
 }
 
-// The rest of the choice where the class is needed, or too many tokens are above it: keys to T.keys[d], in any order, and how
-// many.
+// The choice where the class is needed: `larger` keys above it are there, keys to T.keys[d], in any order, and how
+// many; -1: too many groups, or tokens.
 template <int DT>
-__device__ __noinline__ int choose_more(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta cta,
-                                        unsigned found_) {
+__device__ __forceinline__ int choose_near(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta,
+                                           int larger) {
     const Chooser<DT> choose(P, plan, row, T, d, cta);
-    constexpr int kPer = Chooser<DT>::kPer;
-    const int lane = cta.lane, k = P.k, log = plan.group_log;
-    const int rows = (cta.chunks + (1 << log) - 1) >> log;
-    unsigned long long *keys = T.keys[d];
-    auto slice = [&](int j) { return cta.slice0 + j; };
-    if (found_ < (unsigned)k) {
-        // Groups above the class and, chunk after chunk, those in it until there are enough (of fp32: all).
-        const int larger = (int)found_;
-        int found = larger, groups = 0, equal = 0;
-        for (int r = 0; r < rows; ++r) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][lane * 8]);
-            const bool more = DT == SV_DT_FP32 || equal < k - larger;
-            uint32_t in = choose.groups(w, false);
-            if (more) {
-                const uint32_t same = choose.groups(w, true);
-                equal += (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(same));
-                in |= same;
-            }
-            int total, to = lanes_before(__popc(in), lane, total) + groups;
-            for (; in; in &= in - 1, ++to)
-                if (to < kKept) T.kept[to] = (uint16_t)(r * kTeam + lane * 8 + choose.group_of(in));
-            groups += total;
+    const int lane = cta.lane, k = P.k, log = plan.group_log, rows = choose.rows();
+    // Groups above the class and, chunk after chunk, those in it until there are enough (of fp32: all).
+    int found = larger, groups = 0, equal = 0;
+    for (int r = 0; r < rows; ++r) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(&T.most[d][r][lane * 8]);
+        const bool more = DT == SV_DT_FP32 || equal < k - larger;
+        uint32_t in = choose.groups(w, false);
+        if (more) {
+            const uint32_t same = choose.groups(w, true);
+            equal += (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(same));
+            in |= same;
         }
-        __syncwarp();
-        bool ok = groups <= kKept;
-        if (ok)
-            choose.each(groups << (2 + log), [&](int j) { return choose.vector(T.kept[j >> (2 + log)], j & ((4 << log) - 1)); },
-                        [&](const uint4 (&w)[4], const int (&v)[4]) {
-                uint32_t in[4];
-                int c = 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    in[q] = choose.tokens(w[q], v[q], true);
-                    c += __popc(in[q]);
-                }
-                int total, to = lanes_before(c, lane, total) + found;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    choose.put(keys, w[q], v[q], in[q], to, kKeys);
-                    to += __popc(in[q]);
-                }
-                found += total;
-                return found <= kKeys;
-            });
-        __syncwarp();
-        if (ok && found <= kKeys) return found;
-        if (DT == SV_DT_BF16) {
-            // the slice's first tokens that equal the bound, from its start
-            found = larger;
-            choose.each(cta.slice_vecs, slice, [&](const uint4 (&w)[4], const int (&v)[4]) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t in = choose.tokens(w[q], v[q], true);
-                    int total;
-                    const int to = lanes_before(__popc(in), lane, total) + found;
-                    choose.put(keys, w[q], v[q], in, to, k);
-                    found = min(k, found + total);
-                }
-                return found < k;
-            });
-            __syncwarp();
-            return found;
-        }
-    }
-    // Many tokens within a hair of the bound: the largest key that k of them reach, a bit at a time over the whole slice.
-    unsigned long long key = 0;
-    int found = 0;
-    for (int bit = 63; bit >= -1; --bit) {
-        const unsigned long long next = bit < 0 ? key : key | 1ull << bit;
-        int c = 0;
-        choose.each(cta.slice_vecs, slice, [&](const uint4 (&w)[4], const int (&v)[4]) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[kPer];
-                vec_floats<DT>(w[q], x);
-                uint32_t in = 0;
-#pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    if (v[q] >= 0 && v[q] * kPer + u < P.V && order_key(x[u], v[q] * kPer + u) >= next) in |= 1u << u;
-                if (bit >= 0) {
-                    c += __popc(in);
-                } else {
-                    int total;
-                    const int to = lanes_before(__popc(in), lane, total) + found;
-                    choose.put(keys, w[q], v[q], in, to, kKeys);
-                    found += total;
-                }
-            }
-            return true;
-        });
-        if (bit >= 0 && (int)__reduce_add_sync(0xffffffffu, (unsigned)c) >= k) key = next;
+        int total, to = lanes_before(__popc(in), lane, total) + groups;
+        for (; in; in &= in - 1, ++to)
+            if (to < kKept) T.kept[to] = (uint16_t)(r * kTeam + lane * 8 + choose.group_of(in));
+        groups += total;
     }
     __syncwarp();
-    return min(found, kKeys);
+    if (groups > kKept) return -1;
+    choose.each(groups << (2 + log), [&](int j) { return choose.vector(T.kept[j >> (2 + log)], j & ((4 << log) - 1)); },
+                [&](const uint4 (&w)[4], const int (&v)[4]) {
+        uint32_t in[4];
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            in[q] = choose.tokens(w[q], v[q], true);
+            c += __popc(in[q]);
+        }
+        int total, to = lanes_before(c, lane, total) + found;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            choose.put(T.keys[d], w[q], v[q], in[q], to, kKeys);
+            to += __popc(in[q]);
+        }
+        found += total;
+        return found <= kKeys;
+    });
+    __syncwarp();
+    return found <= kKeys ? found : -1;
+}
+
+// The choice where neither the groups above the bound's class nor those and the class's do: few tokens are left of the row, or
+// left in few warps' vectors (the bound is -inf), or thousands are near it. Other warps wait for this one, and their waits have a
+// limit: it raises the bound by the groups' maxima, and reads groups that reach it, not the row, six times at most (to count
+// the order bits digit by digit where more than kKeys tokens are past the bound). Rows of 152064 logits, 256 at once, k = 20:
+// fp32 with 4 tokens left 45 us (20.9 ms by the keys' bits over the whole row), 1024 neighbours 43, of bf16 50 (14 ms); fp32
+// logits that are all the same 287 us, and 2.2 ms where all are in the bound's class and thousands past the bound. Unmasked: 37 and 31.
+template <int DT>
+__device__ __forceinline__ int choose_far(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta &cta,
+                                          unsigned found) {
+    constexpr uint32_t all = 0xffffffffu;
+    Chooser<DT> choose(P, plan, row, T, d, cta);
+    using Kd = typename Chooser<DT>::Kd;
+    const int lane = cta.lane, k = P.k, log = plan.group_log, rows = choose.rows();
+    unsigned long long *keys = T.keys[d];
+    unsigned *bins = reinterpret_cast<unsigned *>(T.best);  // (which is written later)
+    static_assert(sizeof T.best >= 256 * sizeof *bins, "");
+    uint32_t u;
+    if (found >= (unsigned)k &&
+        nth_of(bins, k, 16, lane, u, [&](auto &&f) {
+            for (int r = 0; r < rows; ++r)
+                for (uint32_t in = choose.groups_of(T, d, r, false); in; in &= in - 1)
+                    f(order_bits(__uint_as_float((uint32_t)T.most[d][r][lane * 8 + choose.group_of(in)] << 16)));
+        })) {
+        // k groups reach a class above: its least number is a bound
+        choose.set(from_order_bits(u >> 31 ? u : u | 0xffffu));
+        choose.bound = choose.low;
+    }
+    auto collect = [&]() {  // the tokens larger than the bound, kKeys of them at most, and how many there are
+        int n = 0;
+        choose.each_past_bound(T, d, [&](const uint4 (&w)[4], const int (&v)[4]) {
+            uint32_t in[4];
+            int c = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                in[q] = choose.past_bound(w[q], v[q], false);
+                c += __popc(in[q]);
+            }
+            int total, to = lanes_before(c, lane, total) + n;
+            if (total == 0) return true;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                choose.put(keys, w[q], v[q], in[q], to, kKeys);
+                to += __popc(in[q]);
+            }
+            n += total;
+            return true;
+        });
+        __syncwarp();
+        return n;
+    };
+    // (they are there already where none of the class are larger)
+    int n = found < (unsigned)k && choose.bound == choose.high ? (int)found : collect();
+    if (n > kKeys) {
+        nth_of(bins, k, DT == SV_DT_FP32 ? 0 : 16, lane, u, [&](auto &&f) {
+            choose.each_past_bound(T, d, [&](const uint4 (&w)[4], const int (&)[4]) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float x[Chooser<DT>::kPer];
+                    vec_floats<DT>(w[q], x);
+#pragma unroll
+                    for (int i = 0; i < Chooser<DT>::kPer; ++i)
+                        if (x[i] > choose.bound) f(order_bits(x[i]));
+                }
+                return true;
+            });
+        });
+        choose.set(from_order_bits(DT == SV_DT_FP32 || u >> 31 ? u : u | 0xffffu));
+        n = min(collect(), k);
+    }
+    // the first tokens that equal the bound, from the slice's start
+    for (int r = 0; r < rows && n < k; ++r) {
+        if (!__any_sync(all, choose.groups_of(T, d, r, true) != 0)) continue;
+        const int first = (r << log) * Kd::kChunkVecs;
+        choose.each(min(Kd::kChunkVecs << log, cta.slice_vecs - first), [&](int j) { return cta.slice0 + first + j; },
+                    [&](const uint4 (&w)[4], const int (&v)[4]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t in = choose.past_bound(w[q], v[q], true);
+                int total;
+                const int to = lanes_before(__popc(in), lane, total) + n;
+                choose.put(keys, w[q], v[q], in, to, k);
+                n = min(k, n + total);
+            }
+            return n < k;
+        });
+    }
+    __syncwarp();
+    return n;
+}
+
+// The rest of the choice where too few tokens are above the class, or too many. (One function: with a second call in it the
+// epilogue's registers go to the stack, 26.2 us against 25.4 for 276 rows with 20 alternatives.)
+template <int DT>
+__device__ __noinline__ int choose_more(const TokenParams &P, const Plan &plan, const char *row, SharedTop &T, int d, const Cta cta,
+                                        unsigned found) {
+    int n = -1;
+    if (found < (unsigned)P.k) n = choose_near<DT>(P, plan, row, T, d, cta, (int)found);
+    if (n < 0) n = choose_far<DT>(P, plan, row, T, d, cta, found);
+    return n;
 }
 
 // The k best keys of the CTA's slice, in order, to T.best (0 where there are none).

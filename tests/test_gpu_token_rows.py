@@ -1,0 +1,123 @@
+"""Token log-probabilities and distillation on rows that leave little to choose from, or nothing between their logits, and
+the kernel's promises about time."""
+import math
+
+import pytest
+import torch
+
+import token_util as tu
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def svm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_token_gb300 as sv
+    sv.build()
+    sv.load()
+    return sv
+
+
+@pytest.fixture(scope="module")
+def h(svm):
+    h = svm.SpecVerify(1, 1, 1000)
+    yield h
+    h.close()
+
+
+def clean(h):
+    torch.cuda.synchronize()
+    assert h.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# the choice of top tokens
+
+# tokens that a grammar, a choice of answers or a codebook leaves; logits with nothing or next to nothing between them
+LEFT = ["few3", "few16", "few40", "side513", "side700", "side1024", "side1800", "side5000", "sides900", "equal", "ties", "zeros",
+        "band_up", "band_down", "band", "sunk", "spike"]
+
+
+def few_left(kind, rows, V, dtype, seed=0):
+    """[rows, V] logits in rows of whole 16-byte pieces, of that kind."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.randn(rows, V, device="cuda", generator=g) * 2
+    left = None
+    if kind.startswith("few"):  # this many tokens anywhere
+        left = torch.zeros(rows, V, dtype=torch.bool, device="cuda")
+        left.scatter_(1, torch.rand(rows, V, device="cuda", generator=g).topk(int(kind[3:]), 1)[1], True)
+    elif kind.startswith("sides"):  # two runs of neighbours, the second at the row's end
+        n = int(kind[5:])
+        left = torch.zeros(rows, V, dtype=torch.bool, device="cuda")
+        left[:, 3:3 + n] = left[:, V - n:] = True
+    elif kind.startswith("side"):  # this many neighbours
+        n = min(int(kind[4:]), V)
+        at = (V - n) * torch.arange(1, rows + 1, device="cuda")[:, None] // (rows + 1)
+        column = torch.arange(V, device="cuda")
+        left = (column >= at) & (column < at + n)
+    elif kind == "equal":
+        z = torch.full_like(z, -2.5)
+    elif kind == "ties":
+        z = torch.randint(-3, 3, (rows, V), device="cuda", generator=g).float()
+    elif kind == "zeros":  # of both signs, with denormals between
+        z = torch.randint(-2, 3, (rows, V), device="cuda", generator=g).float() * (2.0 ** -133 if dtype is BF else 2.0 ** -149)
+        z = torch.where(torch.rand(rows, V, device="cuda", generator=g) < 0.3, -0.0, z)
+        z[:, ::3] = z[:, ::3].clamp(max=0.0)
+    elif kind.startswith("band"):  # thousands of fp32 logits within one value of bf16, below and above zero
+        z = 1 + torch.rand(rows, V, device="cuda", generator=g) * 2.0 ** -7
+        z[::2].neg_()
+        if kind != "band":
+            z = torch.sort(z, 1, descending=kind == "band_down")[0]
+    elif kind == "sunk":  # the same under a few better ones
+        z = 1 + torch.rand(rows, V, device="cuda", generator=g) * 2.0 ** -8
+        z[:, 5::V // 7] = 3.0
+    elif kind == "spike":  # all of one chunk's better than the rest
+        z[:, V // 2: V // 2 + 3000] += 40.0
+    if left is not None:
+        z = z.masked_fill(~left, -math.inf)
+    return torch.nn.functional.pad(z.to(dtype), (0, -V % 8))[:, :V]
+
+
+def check_top(z, T, y, r, at, k):
+    s = tu.Soft(z, T)
+    assert tu.close(r.logprob[at], s.lp[y], s.lp_err(s.lp[y])) and int(r.rank[at]) == s.rank(y)
+    n = min(k, len(z))
+    i = s.top(n)
+    assert torch.equal(r.topk_idx[at][:n].long(), i), (at, r.topk_idx[at][:n].tolist(), i.tolist())
+    assert (r.topk_idx[at][n:] == -1).all()
+    assert tu.close(r.topk_logprob[at][:n], s.lp[i], s.lp_err(s.lp[i]))
+
+
+@pytest.mark.parametrize("kind", LEFT)
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,rows,ks", [(152064, 5, (1, 5, 20, 128)), (33001, 700, (3, 64)), (262147, 310, (20, 100)), (6001, 4, (128,))])
+def test_top_tokens_of_what_is_left(h, kind, dtype, V, rows, ks):
+    z = few_left(kind, rows, V, dtype, V)
+    y = z.float().argmax(1).to(torch.int32)
+    for k in ks:
+        r = h.token_logprobs(z, y, 0.75, k=k, rank=True)
+        clean(h)
+        for i in sorted({0, 1, rows // 2, rows - 2, rows - 1}):
+            check_top(z[i], 0.75, int(y[i]), r, i, k)
+
+
+@pytest.mark.parametrize("kind", ["few16", "side700", "side1024", "side1800", "equal", "ties", "sunk", "band_up", "band"])
+@pytest.mark.parametrize("dtype,k", [(BF, 5), (BF, 64), (FP, 20), (FP, 64)])
+@pytest.mark.parametrize("rows", [5, 1000])
+def test_rows_with_little_left_keep_to_a_wait_limit(h, kind, dtype, k, rows):
+    """A limit of 4 ms is for what hangs: no row of a vocabulary takes that long, whatever is left of it, and rows that wait for
+    one another (three and more a CTA) do not run into it."""
+    z = few_left(kind, rows, 152064, dtype, 3)
+    y = z.float().argmax(1).to(torch.int32)
+    h.set_wait_limit(4_000_000)
+    try:
+        r = h.token_logprobs(z, y, k=k, rank=True)
+        clean(h)
+    finally:
+        h.set_wait_limit(0)
+    for i in (0, rows - 1):
+        check_top(z[i], 1.0, int(y[i]), r, i, k)
