@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 #include <new>
 #include <vector>
 
@@ -47,6 +46,7 @@ struct specverify_ctx {
     int timing = 0;
     std::vector<TimedLaunch> pending;
     std::vector<cudaEvent_t> pool;
+    sv::TokenRooms rooms;        // of the token log-probability and distillation kernels
     uint32_t epoch = 0;  // flag value of the last fused call
     uint64_t wait_ns = kDefaultWaitNs;  // bound of a fused-kernel wait on another warp
     double total_ms[kNumKernels] = {};
@@ -217,20 +217,6 @@ int run_verify(specverify_ctx *h, const specverify_batch *in, bool sampling, flo
     return map_cuda(e);
 }
 
-// The kernels of the token log-probability and distillation calls, set up once a
-// device (they ask what fits it, which takes longer than the rest of a handle).
-cudaError_t prepare_token(int device) {
-    static std::mutex lock;
-    static std::vector<int> done;
-    std::lock_guard<std::mutex> hold(lock);
-    if (std::find(done.begin(), done.end(), device) != done.end()) return cudaSuccess;
-    cudaError_t e = sv::prepare_logprobs();
-    if (e == cudaSuccess) e = sv::prepare_logprobs_grad();
-    if (e == cudaSuccess) e = sv::prepare_distill();
-    if (e == cudaSuccess) done.push_back(device);
-    return e;
-}
-
 // Rows of logits of a token log-probability or distillation call; fine: with
 // log2(e) / T in two floats, the second positive (times -inf it is no NaN).
 int token_params(const specverify_ctx *h, const void *logits, int32_t dtype, int64_t rows,
@@ -340,7 +326,6 @@ int specverify_create(specverify_t *out, int device, int32_t max_batch, int32_t 
     if (e == cudaSuccess) e = sv::prepare_features();
     if (e == cudaSuccess) e = sv::prepare_restricted();
     if (e == cudaSuccess) e = sv::prepare_small();
-    if (e == cudaSuccess) e = prepare_token(device);
     if (e != cudaSuccess) {
         delete h;
         return map_cuda(e);
@@ -671,7 +656,7 @@ int specverify_token_logprobs(specverify_t h, const void *logits, int32_t dtype,
     p.rank = rank;
     p.top_logprob = topk_logprob;
     p.top_idx = topk_idx;
-    return map_cuda(sv::launch_token_logprobs(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_token_logprobs(p, dtype, h->rooms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -696,7 +681,7 @@ int specverify_token_logprobs_grad(specverify_t h, const void *logits, int32_t d
     p.g_entropy = grad_entropy;
     p.logprob = logprob;
     p.entropy = entropy;
-    return map_cuda(sv::launch_token_logprobs_grad(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_token_logprobs_grad(p, dtype, h->rooms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -710,7 +695,7 @@ int specverify_distill_loss(specverify_t h, const void *logits, int32_t dtype, i
     DeviceGuard guard(h->device);
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
     p.loss = loss;
-    return map_cuda(sv::launch_distill(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_distill(p, dtype, h->rooms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, int64_t rows,
@@ -733,7 +718,7 @@ int specverify_distill_grad(specverify_t h, const void *logits, int32_t dtype, i
     if (guard.err != cudaSuccess) return map_cuda(guard.err);
     p.weight = weight;
     p.loss = loss;
-    return map_cuda(sv::launch_distill(p, dtype, static_cast<cudaStream_t>(cuda_stream)));
+    return map_cuda(sv::launch_distill(p, dtype, h->rooms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int specverify_device_status(specverify_t h, void *cuda_stream, int32_t *status_out) {

@@ -11,17 +11,9 @@ using List = Kind<DT, true, GRAD, false, false, false>;
 
 }  // namespace
 
-cudaError_t prepare_distill() {
-    cudaError_t e = prepare<List<SV_DT_FP32, false>>();
-    if (e == cudaSuccess) e = prepare<List<SV_DT_BF16, false>>();
-    if (e == cudaSuccess) e = prepare<List<SV_DT_FP32, true>>();
-    if (e == cudaSuccess) e = prepare<List<SV_DT_BF16, true>>();
-    return e;
-}
-
-cudaError_t launch_distill(const TokenParams &P, int dtype, cudaStream_t s) {
-    if (P.grad) return dtype == SV_DT_FP32 ? launch<List<SV_DT_FP32, true>>(P, s) : launch<List<SV_DT_BF16, true>>(P, s);
-    return dtype == SV_DT_FP32 ? launch<List<SV_DT_FP32, false>>(P, s) : launch<List<SV_DT_BF16, false>>(P, s);
+cudaError_t launch_distill(const TokenParams &P, int dtype, TokenRooms &rooms, cudaStream_t s) {
+    if (P.grad) return dtype == SV_DT_FP32 ? launch<List<SV_DT_FP32, true>>(P, rooms, s) : launch<List<SV_DT_BF16, true>>(P, rooms, s);
+    return dtype == SV_DT_FP32 ? launch<List<SV_DT_FP32, false>>(P, rooms, s) : launch<List<SV_DT_BF16, false>>(P, rooms, s);
 }
 
 }  // namespace sv

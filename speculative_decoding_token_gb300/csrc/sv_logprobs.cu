@@ -19,26 +19,16 @@ template <int DT>
 using Both = Kind<DT, false, false, true, true, true>;
 
 template <int DT>
-cudaError_t run(const TokenParams &P, cudaStream_t s) {
-    if (P.k > 0) return P.rank ? launch<Both<DT>>(P, s) : launch<Top<DT>>(P, s);
-    if (P.rank) return launch<Rank<DT>>(P, s);
-    return P.entropy ? launch<Ent<DT>>(P, s) : launch<Plain<DT>>(P, s);
+cudaError_t run(const TokenParams &P, TokenRooms &rooms, cudaStream_t s) {
+    if (P.k > 0) return P.rank ? launch<Both<DT>>(P, rooms, s) : launch<Top<DT>>(P, rooms, s);
+    if (P.rank) return launch<Rank<DT>>(P, rooms, s);
+    return P.entropy ? launch<Ent<DT>>(P, rooms, s) : launch<Plain<DT>>(P, rooms, s);
 }
 
 }  // namespace
 
-cudaError_t prepare_logprobs() {
-    for (cudaError_t (*f)() : {prepare<Plain<SV_DT_FP32>>, prepare<Plain<SV_DT_BF16>>, prepare<Ent<SV_DT_FP32>>, prepare<Ent<SV_DT_BF16>>,
-                               prepare<Top<SV_DT_FP32>>, prepare<Top<SV_DT_BF16>>, prepare<Rank<SV_DT_FP32>>, prepare<Rank<SV_DT_BF16>>,
-                               prepare<Both<SV_DT_FP32>>, prepare<Both<SV_DT_BF16>>}) {
-        const cudaError_t e = f();
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
-cudaError_t launch_token_logprobs(const TokenParams &P, int dtype, cudaStream_t s) {
-    return dtype == SV_DT_FP32 ? run<SV_DT_FP32>(P, s) : run<SV_DT_BF16>(P, s);
+cudaError_t launch_token_logprobs(const TokenParams &P, int dtype, TokenRooms &rooms, cudaStream_t s) {
+    return dtype == SV_DT_FP32 ? run<SV_DT_FP32>(P, rooms, s) : run<SV_DT_BF16>(P, rooms, s);
 }
 
 }  // namespace sv

@@ -10,18 +10,10 @@ using Grad = Kind<DT, false, true, ENT, false, false>;
 
 }  // namespace
 
-cudaError_t prepare_logprobs_grad() {
-    cudaError_t e = prepare<Grad<SV_DT_FP32, false>>();
-    if (e == cudaSuccess) e = prepare<Grad<SV_DT_BF16, false>>();
-    if (e == cudaSuccess) e = prepare<Grad<SV_DT_FP32, true>>();
-    if (e == cudaSuccess) e = prepare<Grad<SV_DT_BF16, true>>();
-    return e;
-}
-
-cudaError_t launch_token_logprobs_grad(const TokenParams &P, int dtype, cudaStream_t s) {
+cudaError_t launch_token_logprobs_grad(const TokenParams &P, int dtype, TokenRooms &rooms, cudaStream_t s) {
     if (P.g_entropy || P.entropy)
-        return dtype == SV_DT_FP32 ? launch<Grad<SV_DT_FP32, true>>(P, s) : launch<Grad<SV_DT_BF16, true>>(P, s);
-    return dtype == SV_DT_FP32 ? launch<Grad<SV_DT_FP32, false>>(P, s) : launch<Grad<SV_DT_BF16, false>>(P, s);
+        return dtype == SV_DT_FP32 ? launch<Grad<SV_DT_FP32, true>>(P, rooms, s) : launch<Grad<SV_DT_BF16, true>>(P, rooms, s);
+    return dtype == SV_DT_FP32 ? launch<Grad<SV_DT_FP32, false>>(P, rooms, s) : launch<Grad<SV_DT_BF16, false>>(P, rooms, s);
 }
 
 }  // namespace sv

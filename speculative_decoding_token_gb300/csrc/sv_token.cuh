@@ -949,23 +949,17 @@ __global__ void __launch_bounds__(kThreads, 2) token_kernel(const __grid_constan
 constexpr int kHalfSmem = 113 * 1024;  // of a CTA, two on an SM
 constexpr int64_t kRereadBytes = 48 << 20;
 
-// What fits the GPU of a kernel: clusters of 2^i CTAs at once.
-template <class Kd>
-struct Room {
-    static inline int clusters[5];
-};
-
 // Rows over the GPU. One CTA a row where there are rows for every CTA that fits, else as many as do (a power of two). A
-// gradient's rows go through L2 between their readings: no more of them at once than it holds well.
+// gradient's rows go through L2 between their readings: no more of them at once than it holds well. room: the clusters of 2^i
+// CTAs that fit at once.
 template <class Kd>
-Plan make_plan(const TokenParams &P) {
+Plan make_plan(const TokenParams &P, const int (&room)[5]) {
     const int64_t vecs = ((int64_t)P.V * Kd::kSize + 15) / 16;
     Plan p{};
     p.depth_log = Kd::Top ? 1 : 2;
     p.list_stride = Kd::List ? (P.K + 31) / 32 * 32 : 0;
     const int fixed = (int)((sizeof(Shared) + 15) / 16 * 16) +
                       (Kd::List ? kHashBytes + p.list_stride * kListBytes : Kd::Top ? (int)((sizeof(SharedTop) + 15) / 16 * 16) : 0);
-    const auto &room = Room<Kd>::clusters;
     int log = 0;
     if (Kd::Grad)
         while (log < 4 && (int64_t)room[log] * vecs * 16 > kRereadBytes) ++log;
@@ -985,15 +979,11 @@ Plan make_plan(const TokenParams &P) {
     return p;
 }
 
+// A kernel's set-up on the current device, at a handle's first call that takes it. Not at the handle's making (18 kernels of five
+// questions each: a program's first handle took 3.8 ms instead of 2.4, also where it only verifies), and not once for a process:
+// another device has other room.
 template <class Kd>
-cudaError_t launch(const TokenParams &P, cudaStream_t s) {
-    const Plan plan = make_plan<Kd>(P);
-    return launch_after(token_kernel<Kd>, dim3((unsigned)(plan.clusters * plan.cluster)), kThreads, plan.smem, s, plan.cluster, P,
-                        plan);
-}
-
-template <class Kd>
-cudaError_t prepare() {
+cudaError_t prepare(TokenRoom &room) {
     cudaError_t e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHalfSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(token_kernel<Kd>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int log = 0; log < 5 && e == cudaSuccess; ++log) {
@@ -1007,9 +997,26 @@ cudaError_t prepare() {
         cfg.dynamicSmemBytes = kHalfSmem;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&Room<Kd>::clusters[log], token_kernel<Kd>, &cfg);
+        int fit = 0;
+        e = cudaOccupancyMaxActiveClusters(&fit, token_kernel<Kd>, &cfg);
+        room.clusters[log].store(fit, std::memory_order_relaxed);
     }
+    if (e == cudaSuccess) room.known.store(true, std::memory_order_release);
     return e;
+}
+
+template <class Kd>
+cudaError_t launch(const TokenParams &P, TokenRooms &rooms, cudaStream_t s) {
+    TokenRoom &room = rooms.of[Kd::kId];
+    if (!room.known.load(std::memory_order_acquire)) {
+        const cudaError_t e = prepare<Kd>(room);
+        if (e != cudaSuccess) return e;
+    }
+    int clusters[5];
+    for (int log = 0; log < 5; ++log) clusters[log] = room.clusters[log].load(std::memory_order_relaxed);
+    const Plan plan = make_plan<Kd>(P, clusters);
+    return launch_after(token_kernel<Kd>, dim3((unsigned)(plan.clusters * plan.cluster)), kThreads, plan.smem, s, plan.cluster, P,
+                        plan);
 }
 
 }  // namespace

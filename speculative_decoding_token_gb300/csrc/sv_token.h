@@ -2,6 +2,7 @@
 // log-probability and distillation calls (not part of the public C ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -47,11 +48,19 @@ struct TokenParams {
     float *loss;
 };
 
-cudaError_t prepare_logprobs();
-cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, cudaStream_t s);
-cudaError_t prepare_logprobs_grad();
-cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, cudaStream_t s);
-cudaError_t prepare_distill();
-cudaError_t launch_distill(const TokenParams &p, int dtype, cudaStream_t s);  // p.grad may be NULL
+// What a handle knows of one of the kernels on its device, from its first call that takes it on: the clusters of 2^i CTAs that
+// fit the GPU at once. (Calls on one handle may run beside one another: two that find nothing known write the same.)
+struct TokenRoom {
+    std::atomic<bool> known{false};
+    std::atomic<int> clusters[5] = {};
+};
+
+struct TokenRooms {
+    TokenRoom of[18];
+};
+
+cudaError_t launch_token_logprobs(const TokenParams &p, int dtype, TokenRooms &rooms, cudaStream_t s);
+cudaError_t launch_token_logprobs_grad(const TokenParams &p, int dtype, TokenRooms &rooms, cudaStream_t s);
+cudaError_t launch_distill(const TokenParams &p, int dtype, TokenRooms &rooms, cudaStream_t s);  // p.grad may be NULL
 
 }  // namespace sv

@@ -43,6 +43,7 @@ struct Kind {
     static constexpr int kPer = 16 / kSize;  // logits of a vector
     static constexpr uint32_t kNegInf = DT == SV_DT_FP32 ? 0xff800000u : 0xff80ff80u;
     static constexpr int kVecs = 4;  // of a chunk, a thread
+    static constexpr int kId = DT + 2 * (List ? 7 + Grad : Grad ? 5 + Ent : Rank ? 3 + Top : Top ? 2 : Ent);  // in TokenRooms
     // numbers of a Part that a cluster's CTAs send one another
     static constexpr int kWords = 2 + (Ent ? 1 : 0) + (Rank ? 1 : 0);
     static constexpr int kChunkVecs = kTeam * kVecs, kChunkBytes = kChunkVecs * 16;

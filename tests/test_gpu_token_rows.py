@@ -121,3 +121,101 @@ def test_rows_with_little_left_keep_to_a_wait_limit(h, kind, dtype, k, rows):
         h.set_wait_limit(0)
     for i in (0, rows - 1):
         check_top(z[i], 1.0, int(y[i]), r, i, k)
+
+
+# ---------------------------------------------------------------------------
+# handles
+
+RESET = r"""
+import ctypes, sys
+import speculative_decoding_token_gb300 as sv
+lib, cuda = sv.load(), ctypes.CDLL(%r)
+def bytes_of(n):
+    p = ctypes.c_void_p()
+    assert cuda.cudaMalloc(ctypes.byref(p), ctypes.c_size_t(n)) == 0
+    return p
+def ask(k):
+    h = sv.specverify_create(0, 1, 1, 100)
+    z, y, lp, H, lse, top, idx = (bytes_of(1 << 20) for _ in range(7))
+    for p in (z, y):
+        assert cuda.cudaMemset(p, 0, ctypes.c_size_t(1 << 20)) == 0
+    assert lib.specverify_token_logprobs(h, z, 0, 4, 1000, 1000, 1.0, 4, 1, y, None, None, k, lp, H, lse, None, top, idx, None) == 0
+    assert sv.specverify_device_status(h) == 0
+    out = (ctypes.c_float * 4)()
+    assert cuda.cudaMemcpy(out, lp, ctypes.c_size_t(16), 2) == 0
+    sv.specverify_destroy(h)
+    return list(out)
+first = [ask(0), ask(3)]
+assert cuda.cudaDeviceReset() == 0
+assert [ask(0), ask(3)] == first, first
+assert abs(first[0][0] + 6.907755) < 1e-6, first
+"""
+
+
+def test_handles_after_a_device_reset(svm):
+    """A reset ends a program's own context; a new handle works as the first did."""
+    import os
+    import subprocess
+    import sys
+    lib = next(l.split()[-1] for l in open("/proc/self/maps") if "libcudart.so" in l)
+    r = subprocess.run([sys.executable, "-c", RESET % lib], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+CAPTURED = r"""
+import torch
+import speculative_decoding_token_gb300 as sv
+h = sv.SpecVerify(1, 1, 1000)
+z = torch.zeros(3, 1000, device="cuda")
+y, g = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.ones(3, device="cuda")
+ids, t = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.full((3, 1), -1.0, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = [h.token_logprobs(z, y, k=2, rank=True).logprob, h.token_logprobs(z, y).logprob, *h.token_logprobs_grad(z, y, g),
+           h.distill_loss(z, ids, t), *h.distill_grad(z, ids, t)]
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+assert h.device_status() == 0
+want = [h.token_logprobs(z, y, k=2, rank=True).logprob, h.token_logprobs(z, y).logprob, *h.token_logprobs_grad(z, y, g),
+        h.distill_loss(z, ids, t), *h.distill_grad(z, ids, t)]
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+assert h.device_status() == 0
+"""
+
+
+def test_a_first_call_may_be_captured(svm):
+    """A handle's first calls, in a program's first graph."""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_make_a_handles_first_calls(svm):
+    import threading
+    z = torch.zeros(40, 5000, device="cuda")
+    y = torch.zeros(40, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(10):
+        h, got = svm.SpecVerify(1, 1, 1000), []
+        go = threading.Barrier(2)
+
+        def first(h=h, got=got, go=go):
+            s = torch.cuda.Stream()
+            go.wait()
+            got.append(h.token_logprobs(z, y, k=3, stream=s).logprob)
+            s.synchronize()
+
+        threads = [threading.Thread(target=first) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        clean(h)
+        assert len(got) == 2 and torch.equal(got[0], got[1])
+        assert (got[0] + math.log(5000)).abs().max() < 1e-5
+        h.close()

@@ -125,3 +125,76 @@ def test_a_planted_mistake_fails_the_differences():
     for wrong in (q / 2.0, float(d.grad[v]) * 2.0):
         assert abs(diff - wrong) > 1e-4 * q
     assert np.isclose(diff, float(d.grad[v]), rtol=1e-4)
+
+
+# -- plans
+
+PLANS = r"""
+#include <cstdio>
+#include <random>
+#include "sv_token.cuh"
+
+using namespace sv;
+
+// What a plan has to keep to, whatever fits the device.
+template <class Kd>
+int check(const TokenParams &P, const int (&room)[5], Plan &p) {
+    p = make_plan<Kd>(P, room);
+    const int64_t vecs = ((int64_t)P.V * Kd::kSize + 15) / 16;
+    const int chunks = (p.slice_vecs + Kd::kChunkVecs - 1) / Kd::kChunkVecs;
+    if (p.cluster < 1 || p.cluster > kMaxCluster || p.clusters < 1 || p.slots < 2 || p.slots > kMaxSlots) return 1;
+    if ((int64_t)p.slice_vecs * p.cluster < vecs || p.smem > kHalfSmem) return 2;
+    if ((int64_t)p.clusters * p.cluster > INT32_MAX || (!p.dynamic && p.clusters > P.entries)) return 3;
+    if (Kd::Top && (p.cluster > 1 ? P.k * p.cluster > kGathered : P.k > kMaxAlternatives)) return 4;
+    if (Kd::Top && ((chunks + (1 << p.group_log) - 1) >> p.group_log) > kGroupRows) return 5;
+    if (!Kd::Grad && p.cluster > 1 && p.clusters < P.entries) return 6;  // sums alone: a cluster has one row
+    if (Kd::kId < 0 || Kd::kId >= 18) return 7;
+    return 0;
+}
+
+int main() {
+    std::mt19937_64 rng(1);
+    auto spread = [&](double lo, double hi) { return (int64_t)std::exp(std::uniform_real_distribution<>(std::log(lo), std::log(hi))(rng)); };
+    const int large[5] = {304, 152, 72, 36, 16}, small[5] = {60, 30, 14, 6, 2}, one[5] = {8, 4, 2, 1, 1};
+    int unlike = 0;
+    for (int i = 0; i < 20000; ++i) {
+        TokenParams P{};
+        P.V = (int32_t)(i % 50 == 0 ? INT32_MAX - i : spread(1, 400000));
+        P.entries = P.rows = i % 70 == 0 ? 1ll << 34 : spread(1, 5000);
+        P.k = (int32_t)spread(1, 128.9);
+        P.K = (int32_t)spread(1, 256.9);
+        Plan a, b;
+        for (const int (*rooms)[5] : {&large, &small, &one}) {
+            const int (&room)[5] = *rooms;
+            const int bad[] = {check<Kind<0, false, false, false, false, false>>(P, room, a), check<Kind<1, false, false, true, false, true>>(P, room, a),
+                               check<Kind<0, false, false, true, true, true>>(P, room, a), check<Kind<1, false, false, true, true, false>>(P, room, a),
+                               check<Kind<0, false, true, true, false, false>>(P, room, a), check<Kind<1, false, true, false, false, false>>(P, room, a),
+                               check<Kind<1, true, false, false, false, false>>(P, room, a), check<Kind<0, true, true, false, false, false>>(P, room, a)};
+            for (int j = 0; j < 8; ++j)
+                if (bad[j]) {
+                    std::printf("kind %d: %d (V %d, entries %lld, k %d, K %d, room %d)\n", j, bad[j], P.V, (long long)P.entries, P.k, P.K, room[0]);
+                    return 1;
+                }
+        }
+        check<Kind<1, false, true, false, false, false>>(P, large, a);
+        check<Kind<1, false, true, false, false, false>>(P, small, b);
+        unlike += a.cluster != b.cluster;
+    }
+    std::printf("%d\n", unlike);
+    return 0;
+}
+"""
+
+
+def test_plans_are_a_devices_own(lib, tmp_path):
+    """Every plan keeps to the kernel's limits, over the range of sizes and for large and small devices, and is made for the
+    device that it is told of, not for the last that a handle was made on."""
+    import subprocess
+
+    from speculative_decoding_token_gb300 import _build
+    src, exe = tmp_path / "plans.cu", tmp_path / "plans"
+    src.write_text(PLANS)
+    subprocess.run([_build.nvcc(), *_build.NVCC_FLAGS, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    assert int(r.stdout) > 100
