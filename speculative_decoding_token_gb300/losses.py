@@ -22,6 +22,7 @@ torch = None  # imported by bind(), when the library is loaded: this module, lik
 
 FP32, BF16 = 0, 1
 MAX_ALTERNATIVES, MAX_LIST = 128, 256
+MAX_INT32 = 2 ** 31 - 1
 DIVERGENCES = {"fkl": 0, "rkl": 1, "jsd": 2, "tvd": 3}
 FORMS = {"logprobs": 0, "logits": 1}
 
@@ -137,6 +138,8 @@ class RowLosses:
             raise ValueError("tokens with row_off must be [B, M]")
         else:
             B, M = shape
+        if max(B, M) > MAX_INT32:
+            raise ValueError(f"no more than {MAX_INT32} rows a call, or sequences, or tokens of one")
         if not 0 <= k <= MAX_ALTERNATIVES:
             raise ValueError(f"k must be 0 to {MAX_ALTERNATIVES}, not {k}")
         if out is None:

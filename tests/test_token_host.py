@@ -198,3 +198,17 @@ def test_plans_are_a_devices_own(lib, tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
     assert int(r.stdout) > 100
+
+
+def test_binding_refuses_more_rows_than_the_call_counts(lib):
+    """2^32 rows of a token each would be none in 32 bits."""
+    import speculative_decoding_token_gb300 as sv
+    h = object.__new__(sv.SpecVerify)
+    h.h, h.device = None, -1  # tensors on the host, as far as the check
+    for rows in (2 ** 31, 2 ** 32, 2 ** 32 + 3):
+        z = torch.zeros(8).as_strided((rows, 8), (0, 1))
+        tokens = torch.zeros(1, dtype=torch.int32)
+        for y, off in ((tokens.expand(rows), None), (tokens.expand(rows, 1), torch.zeros(1, dtype=torch.int64).expand(rows)),
+                       (tokens.expand(1, rows), torch.zeros(1, dtype=torch.int64))):
+            with pytest.raises(ValueError, match="no more than 2147483647 rows"):
+                h.token_logprobs(z, y, row_off=off)
