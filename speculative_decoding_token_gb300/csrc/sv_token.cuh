@@ -160,7 +160,18 @@ __device__ __forceinline__ int counted(uint32_t sum) {
     return (int)(lo + ((lo - ((sum + lo) >> 16)) & 0xffffu));
 }
 
-// The sums of a row's slice, chunk after chunk. A thread's reference m is its warp's maximum in the first chunk, and moves when
+// A vector without its token e.
+template <class Kd>
+__device__ __forceinline__ uint4 without(const uint4 &w, int e) {
+    auto word = [&](uint32_t x, int q) {
+        if (Kd::DT == SV_DT_FP32) return q == e ? Kd::kNegInf : x;
+        return q != e >> 1 ? x : e & 1 ? (x & 0xffffu) | 0xff800000u : (x & 0xffff0000u) | 0xff80u;
+    };
+    return make_uint4(word(w.x, 0), word(w.y, 1), word(w.z, 2), word(w.w, 3));
+}
+
+// The sums of a row's slice, chunk after chunk (a gradient's without the given token, which the epilogue adds: what the others
+// have is 1 - p of it, also where that is 2^-40. 37 rows of 50257 with entropies 8.5 -> 8.8 us, 2048 of 152064 198.0 -> 198.4). A thread's reference m is its warp's maximum in the first chunk, and moves when
 // a logit is 8 binades above it (TokenParams::lag): the sums are good whatever m is, and moving it for every new maximum costs
 // 30 instructions in nearly every chunk (one of 32 lanes has a new maximum). What entropies lose by it is 8 2^-24.
 template <class Kd>
@@ -188,6 +199,11 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
         }
         if (zy == -INFINITY) bound_before = bound_after;  // and the equal ones one by one, below
     }
+    int own = -1;  // the chunk that has the given token, of the thread that does
+    if (Kd::Grad && !Kd::List) {
+        const int v = S.row[d].y / kPer - cta.slice0;
+        if (v >= 0 && v % kTeam == tid) own = v / Kd::kChunkVecs;
+    }
     const float c = P.c;
     const f32x2 c2 = pack2(c, c);
     const uint32_t far = far_bits<Kd::DT>(P), mine = cta.ring + tid * 16;
@@ -209,6 +225,12 @@ __device__ __forceinline__ bool sum_slice(const TokenParams &P, const Plan &plan
                 if (!Kd::List && cta.slice0 + v == whole) w[j] = ragged_end<Kd>(S.row[d].z, whole, rest);
                 else w[j] = load_vec(at + j * kTeam * 16);
             }
+        }
+        if (Kd::Grad && !Kd::List && i == own) {
+            const int y = S.row[d].y, at = (y / kPer - cta.slice0) % Kd::kChunkVecs / kTeam;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (j == at) w[j] = without<Kd>(w[j], y % kPer);
         }
         uint32_t all = packed_max<Kd::DT>(w[0]);
 #pragma unroll
@@ -700,10 +722,19 @@ __device__ __forceinline__ void write_top(const TokenParams &P, long long e, int
 }
 
 template <class Kd>
-__device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, const Cta &cta, int d, const Part &p) {
+__device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, const Cta &cta, int d, Part p, const Part &own) {
     const Row &row = S.row[d];
     const long long e = row.entry;
     const int lane = cta.lane;
+    float so = 0.0f, to = 0.0f;  // (a gradient's) sums of the others
+    if (Kd::Grad) {
+        const float m = fmaxf(p.m, own.m);
+        float fo, fy;
+        const float xo = between(P, p.m, m, fo), xy = between(P, own.m, m, fy);
+        so = fo * p.s;
+        to = fo * fmaf(xo, p.s, p.t);
+        p = Part{m, fmaf(fy, own.s, so), fmaf(fy, fmaf(xy, own.s, own.t), to), min(p.n, own.n)};
+    }
     const bool bad = row.state == kBad || (row.state == kLive && (p.n < 0 || p.m == -INFINITY));
     const bool good = row.state == kLive && !bad;
     if (row.state == kLive && bad && lane == 0 && cta.rank == 0) atomicOr(P.status, SPECVERIFY_STATUS_BAD_LOGIT);
@@ -749,9 +780,15 @@ __device__ __forceinline__ void finish_token(const TokenParams &P, Shared &S, co
         if (Kd::Rank) P.rank[e] = bad ? -1 : p.n;
     }
     if (Kd::Grad && lane == 0) {
-        const float py = ff_exp(lp, lo);
-        const float s = Kd::Ent && py > 0.0f ? row.h * py * (lp + H) : 0.0f;
-        S.fix[d] = (row.g * (1.0f - py) - s) * P.inv_hi;
+        // g (1 - p) - h p (ln p + H), where 1 - p is the others' share and ln p + H that times (ln p - the mean of their ln p_v):
+        // of a likely token the differences would leave little
+        const float share = so * inv_s;
+        float s = row.g;
+        if (Kd::Ent) {
+            const float ln = share < 0.5f ? log1pf(-share) : lp, mean = fmaf(__fdividef(to, so), kLn2Hi, -lh);
+            if (share > 0.0f && lp > -INFINITY) s = fmaf(-row.h * ff_exp(lp, lo), ln - mean, s);
+        }
+        S.fix[d] = s * share * P.inv_hi;
         S.good[d] = good;
     }
 }
@@ -831,7 +868,18 @@ __device__ __forceinline__ void finish(const TokenParams &P, Shared &S, const Li
         const int state = S.row[d].state;
         if (state == kEnd) return;
         Part p{-INFINITY, 0.0f, 0.0f, 0};
-        if (!wait_bar(S.scouted[d], parity, S, P) || !wait_bar(S.summed[d], parity, S, P)) return;
+        if (!wait_bar(S.scouted[d], parity, S, P)) return;
+        Part own{-INFINITY, 0.0f, 0.0f, 0};  // (a gradient's) given token, as a sum relative to it
+        if (Kd::Grad && !Kd::List && state == kLive) {
+            const float z = S.row[d].zy;
+            if (z < INFINITY) {
+                const float x = plain(P, z) ? fmaf(z, P.c, -scaled(P, z)) : 0.0f, w = ex2_approx(x);
+                if (z > -INFINITY) own = Part{z, w, w * x, 0};
+            } else {
+                own.n = -1;  // a bad one
+            }
+        }
+        if (!wait_bar(S.summed[d], parity, S, P)) return;
         if (state == kLive && cta.cluster > 1) {
             if (!receive<Kd>(P, S, cta, live++, p)) return;
         } else if (state == kLive) {
@@ -839,7 +887,7 @@ __device__ __forceinline__ void finish(const TokenParams &P, Shared &S, const Li
             p = warp_fold<Kd>(P, p);
         }
         if (Kd::List) finish_list<Kd>(P, S, L, cta, d, p);
-        else finish_token<Kd>(P, S, cta, d, p);
+        else finish_token<Kd>(P, S, cta, d, p, own);
         __syncwarp();
         if (Kd::Grad) {
             if (!wait_bar(S.stored[d], parity, S, P)) return;

@@ -219,3 +219,48 @@ def test_two_threads_make_a_handles_first_calls(svm):
         assert len(got) == 2 and torch.equal(got[0], got[1])
         assert (got[0] + math.log(5000)).abs().max() < 1e-5
         h.close()
+
+
+# ---------------------------------------------------------------------------
+# a given token that has nearly all of the mass
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,many,T", [(40000, 1, 1.0), (40000, 40, 1.5), (152061, 1, 1.0), (1003, 30, 0.5), (13, 1, 1.0)])
+@pytest.mark.parametrize("ent", [False, True], ids=["", "ent"])
+def test_gradients_of_sure_tokens(h, dtype, V, many, T, ent):
+    """The given token's gradient is w (g - h p (ln p - m)) / T with w = 1 - p what the others have and m the mean of their
+    logarithms: as good as w, also where w is 2^-18 or 2^-40 and no fp32 p shows it.
+
+    w is a sum of the others' weights, of one sign: exponents to D binades (the scale and the product rounded, each D and the 8 by
+    which references lag times half a step), exponentials to 2^-22, chains of V / 1024 additions (256 threads with four sums each)
+    and a tree of 32, and eight roundings on the way. ln p is good to w's error, m to its own (terms of one sign, and the sum's
+    logarithm)."""
+    gaps = [0.0, 4.0, 9.0, 12.5, 12.5, 12.5, 16.0, 28.0, 60.0, 120.0]
+    rows = len(gaps)
+    z = tu.logits(rows, V, FP, V, device="cuda")
+    y = torch.tensor([0, V - 1, V // 2, 0, V - 1, min(V - 1, 8191), V // 3, 1, V - 2, 5], dtype=torch.int32, device="cuda")
+    for r, gap in enumerate(gaps):
+        v = int(y[r])
+        z[r, v] = -math.inf
+        z[r, v] = float(T * (torch.logsumexp(z[r].double() / T, 0) + gap))
+    z = torch.nn.functional.pad(z.to(dtype), (0, -V % 8)).repeat(many, 1)[:, :V]
+    g = torch.linspace(-2.0, 1.5, rows, device="cuda")
+    e = torch.linspace(0.25, -1.0, rows, device="cuda") if ent else None
+    grad, lp, H = h.token_logprobs_grad(z, y.repeat(many), g.repeat(many), None if e is None else e.repeat(many), T)
+    clean(h)
+    for i in [*range(rows), rows * many - 4]:
+        r = i % rows
+        s, at = tu.Soft(z[i], T), int(y[r])
+        want, err = s.grad(at, float(g[r]), float(e[r]) if ent else 0.0)
+        assert tu.close(grad[i], want, err, dtype), i
+        others = torch.ones(V, dtype=torch.bool, device="cuda")
+        others[at] = False
+        x = s.z[others] / s.T
+        lse = torch.logsumexp(x, 0)
+        w = float(torch.exp(lse - s.lse))
+        m = float((torch.exp(x - lse) * (x - s.lse)).sum())
+        own = float(g[r]) * w - (float(e[r]) * float(s.p[at]) * w * (math.log1p(-w) - m) if ent else 0.0)
+        D = float(s.z[at] - s.z[others].min()) / s.T * math.log2(math.e)
+        rel = math.log(2) * (2 * D + 16) * 2.0 ** -24 + 2.0 ** -22 + (V / 1024 + 32) * 2.0 ** -24 + 2.0 ** -21
+        lim = w * rel * (abs(float(g[r])) + (abs(float(e[r])) * (4 * abs(m) + 4) if ent else 0.0))
+        assert tu.close(grad[i, at], own / s.T, lim / s.T, dtype), (i, float(grad[i, at]), own / s.T, lim / s.T)
