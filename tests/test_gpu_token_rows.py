@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import token_exact as te
 import token_util as tu
 
 pytestmark = pytest.mark.gpu
@@ -264,3 +265,62 @@ def test_gradients_of_sure_tokens(h, dtype, V, many, T, ent):
         rel = math.log(2) * (2 * D + 16) * 2.0 ** -24 + 2.0 ** -22 + (V / 1024 + 32) * 2.0 ** -24 + 2.0 ** -21
         lim = w * rel * (abs(float(g[r])) + (abs(float(e[r])) * (4 * abs(m) + 4) if ent else 0.0))
         assert tu.close(grad[i, at], own / s.T, lim / s.T, dtype), (i, float(grad[i, at]), own / s.T, lim / s.T)
+
+
+# ---------------------------------------------------------------------------
+# sums that are known exactly: every token counts once
+
+EXACT = [(1, 3), (5, 9), (1003, 400), (8193, 30), (33001, 5), (128256, 3), (152064, 330), (262144, 5), (262139, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,rows", EXACT)
+@pytest.mark.parametrize("top", [0, 5])
+def test_sums_count_every_token_once(h, dtype, V, rows, top):
+    z, w = te.counted(min(rows, 6), V, dtype, V, "cuda", top)
+    n = z.shape[0]
+    many = torch.as_strided(z, (n, z.stride(0)), (z.stride(0), 1)).repeat(-(-rows // n), 1)[:, :V]
+    rows = many.shape[0]
+    y = torch.arange(n, dtype=torch.int32, device="cuda") * 31 % V
+    y[-1] = V // 2
+    y = y.repeat(rows // n)
+    check = sorted({*range(n), rows // 2, rows - 1})
+    for k, rank in ((0, False), (0, True), (20, True)):
+        r = h.token_logprobs(many, y, te.T2, k=k, rank=rank)
+        clean(h)
+        for i in check:
+            assert te.right(z[i % n], w[i % n], int(y[i]), r.lse[i], r.logprob[i], r.entropy[i]), (i, k)
+    g = torch.linspace(-1.0, 0.5, rows, device="cuda")
+    for e in (None, torch.zeros(rows, device="cuda")):
+        grad, lp, H = h.token_logprobs_grad(many, y, g, e, te.T2)
+        clean(h)
+        for i in check:
+            assert te.right(z[i % n], w[i % n], int(y[i]), torch.logsumexp(z[i % n].double() / te.T2, 0), lp[i], H[i]), i
+            assert te.right_gradient(grad[i], w[i % n], int(y[i]), float(g[i]), te.T2, dtype), i
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,rows", [x for x in EXACT if x[0] > 100])
+def test_the_rest_of_a_list_counts_every_token_once(h, dtype, V, rows):
+    """Rows of n equal tokens, one of them listed with a half: the forward divergence is ln(n / 2) / 2 + ln(n / (2 n - 2)) / 2 and
+    an unlisted token's gradient (1 / 2 - 1 / n) / (n - 1) / T. Of the loss, two terms of a few roundings; a lost token is 1 / (2 n)."""
+    z, w = te.counted(min(rows, 6), V, dtype, V + 1, "cuda")
+    n = z.shape[0]
+    many = torch.as_strided(z, (n, z.stride(0)), (z.stride(0), 1)).repeat(-(-rows // n), 1)[:, :V]
+    rows = many.shape[0]
+    ids = torch.full((rows, 3), -1, dtype=torch.int32, device="cuda")
+    ids[:, 1] = V // 2
+    t = torch.full((rows, 3), -math.log(2.0), device="cuda")
+    loss = h.distill_loss(many, ids, t, te.T2)
+    grad, same = h.distill_grad(many, ids, t, None, te.T2)
+    clean(h)
+    for i in sorted({*range(n), rows // 2, rows - 1}):
+        count = float(w[i % n].sum())
+        p = math.exp(float(t[i, 1].double()))
+        want = p * math.log(p * count) + (1 - p) * math.log((1 - p) * count / (count - 1))
+        lim = 2.0 ** -24 * (2 * want + 8)
+        assert lim < 0.4 / count
+        assert abs(float(loss[i]) - want) <= lim and abs(float(same[i]) - want) <= lim, (i, float(loss[i]), want)
+        d = torch.where(w[i % n] > 0, (p - 1 / count) / (count - 1), 0.0)
+        d[V // 2] = -(p - 1 / count)
+        assert tu.close(grad[i], d / te.T2, d.abs() / te.T2 * 2.0 ** -21, dtype), i

@@ -212,3 +212,40 @@ def test_binding_refuses_more_rows_than_the_call_counts(lib):
                        (tokens.expand(1, rows), torch.zeros(1, dtype=torch.int64))):
             with pytest.raises(ValueError, match="no more than 2147483647 rows"):
                 h.token_logprobs(z, y, row_off=off)
+
+
+# -- rows of exact sums
+
+@pytest.mark.parametrize("top", [0, 5])
+@pytest.mark.parametrize("V", [1001, 128256, 262144])
+def test_a_lost_vector_is_seen_in_exact_sums(V, top):
+    """The limits of rows with exact sums let right outputs through, and no vector lost or counted twice; where all weights are one,
+    no token."""
+    import token_exact as te
+    z, w = te.counted(2, V, torch.float32, V, top=top)
+    for r in range(2):
+        y = V // 2
+        x = torch.where(w[r] > 0, torch.log(w[r].clamp(min=1)), 0.0)
+        total, spread = w[r].sum(), (w[r] * x).sum()
+
+        def says(sum_, t, r=r, x=x, y=y):
+            lse = torch.log(sum_)
+            return te.right(z[r], w[r], y, lse.float(), (x[y] - lse).float(), (lse - t / sum_).float())
+
+        assert says(total, spread)
+        at = torch.nonzero(w[r])[:, 0]
+        vectors = [(int(v), int(v) // step * step, step) for v in (at[0], at[len(at) // 3], at[-1]) for step in (4, 8)]
+        for v, first, step in vectors:
+            lost = slice(first, min(first + step, V))
+            for sign in (-1, 1):
+                assert not says(total + sign * w[r][lost].sum(), spread + sign * (w[r][lost] * x[lost]).sum())
+                if top == 0:
+                    assert not says(total + sign * w[r][v], spread)
+        g, p = -0.5, w[r] / total
+        grad = -g * p
+        grad[y] += g
+        assert te.right_gradient((grad / te.T2).float(), w[r], y, g, te.T2, torch.float32)
+        assert not te.right_gradient((grad / te.T2 * (1 + 4 / V)).float(), w[r], y, g, te.T2, torch.float32)
+        wrong = grad.clone()
+        wrong[at[1] if at[1] != y else at[2]] = 0
+        assert not te.right_gradient((wrong / te.T2).float(), w[r], y, g, te.T2, torch.float32)
