@@ -324,3 +324,38 @@ def test_the_rest_of_a_list_counts_every_token_once(h, dtype, V, rows):
         d = torch.where(w[i % n] > 0, (p - 1 / count) / (count - 1), 0.0)
         d[V // 2] = -(p - 1 / count)
         assert tu.close(grad[i], d / te.T2, d.abs() / te.T2 * 2.0 ** -21, dtype), i
+
+
+# ---------------------------------------------------------------------------
+# the reverse divergence where a side has no mass
+
+def test_reverse_divergence_at_its_edges(h):
+    """Everything listed, a draft with nothing outside its list, a target sure of one token: the target's rest has its floor of
+    2^-20, and the divergence and each element of its gradient are finite and the formula's."""
+    V = 24
+    for dtype in (FP, BF):
+        z = tu.logits(6, V, dtype, 12, device="cuda")
+        lp = torch.log_softmax(z.float() + 0.3 * torch.sin(torch.arange(V, device="cuda").float()), 1)
+        ids = torch.full((6, V), -1, dtype=torch.int32, device="cuda")
+        t = torch.zeros(6, V, device="cuda")
+        ids[0] = torch.arange(V)                        # everything is listed
+        t[0] = lp[0]
+        z[1, 5:] = -math.inf                            # the draft has nothing outside the list, the target has
+        ids[1, :5], t[1, :5] = torch.arange(5, device="cuda", dtype=torch.int32), lp[1, :5]
+        ids[2, 3] = 7                                   # the target is sure of one token
+        z[3, 1:] = -math.inf                            # the draft is, of a listed one
+        ids[3, :2], t[3, :2] = torch.tensor([0, 3], device="cuda", dtype=torch.int32), torch.tensor([-1.0, -1.5], device="cuda")
+        z[4, 1:] = -math.inf                            # of one that is not listed
+        ids[4, :2], t[4, :2] = torch.tensor([2, 3], device="cuda", dtype=torch.int32), torch.tensor([-1.0, -1.5], device="cuda")
+        z[5, 5:] = -math.inf                            # neither has anything outside
+        ids[5, :5], t[5, :5] = torch.arange(5, device="cuda", dtype=torch.int32), torch.log_softmax(lp[5, :5], 0)
+        for T in (1.0, 0.5):
+            loss = h.distill_loss(z, ids, t, T, "rkl")
+            grad, same = h.distill_grad(z, ids, t, None, T, "rkl")
+            clean(h)
+            for i in range(6):
+                d = tu.Divergence(z[i], ids[i], t[i], T, "rkl")
+                assert math.isfinite(float(d.loss)) and torch.isfinite(d.grad).all()
+                assert tu.close(loss[i], d.loss, d.loss_err), (i, float(loss[i]), float(d.loss))
+                assert tu.close(same[i], d.loss, d.loss_err)
+                assert tu.close(grad[i], d.grad, d.grad_err, dtype), (i, grad[i].tolist(), d.grad.tolist())
