@@ -359,3 +359,52 @@ def test_reverse_divergence_at_its_edges(h):
                 assert tu.close(loss[i], d.loss, d.loss_err), (i, float(loss[i]), float(d.loss))
                 assert tu.close(same[i], d.loss, d.loss_err)
                 assert tu.close(grad[i], d.grad, d.grad_err, dtype), (i, grad[i].tolist(), d.grad.tolist())
+
+
+# ---------------------------------------------------------------------------
+# waits that run out, form by form
+
+FORMS = {"sums": lambda h, z, y, ids, t, one: h.token_logprobs(z, y, entropy=False, lse=False)[:1],
+         "entropy": lambda h, z, y, ids, t, one: h.token_logprobs(z, y)[:3],
+         "rank": lambda h, z, y, ids, t, one: h.token_logprobs(z, y, rank=True)[:4],
+         "top": lambda h, z, y, ids, t, one: [x for x in h.token_logprobs(z, y, k=9) if x is not None],
+         "both": lambda h, z, y, ids, t, one: h.token_logprobs(z, y, k=9, rank=True),
+         "grad": lambda h, z, y, ids, t, one: h.token_logprobs_grad(z, y, one, one),
+         "loss": lambda h, z, y, ids, t, one: [h.distill_loss(z, ids, t)],
+         "loss_grad": lambda h, z, y, ids, t, one: h.distill_grad(z, ids, t, divergence="jsd")}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows,V", [(3, 140001), (700, 50001)], ids=["clusters", "rows"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_each_form_gives_up_and_recovers(svm, form, rows, V, dtype):
+    """With a limit of a nanosecond each form of the kernel gives up at a first wait that lasts two microseconds (its logits come
+    from memory that something else keeps busy), says so, and the next call, with the default limit, is right."""
+    h = svm.SpecVerify(1, 1, 1000)
+    z = tu.logits(min(rows, 20), V, dtype, 31, device="cuda")
+    z = torch.as_strided(z, (z.shape[0], z.stride(0)), (z.stride(0), 1)).repeat(-(-rows // 20), 1)[:rows, :V]
+    ids, t = tu.lists(z[:20], 12, 31)
+    ids, t = ids.repeat(-(-rows // 20), 1)[:rows].contiguous(), t.repeat(-(-rows // 20), 1)[:rows].contiguous()
+    y = torch.arange(rows, dtype=torch.int32, device="cuda")
+    one = torch.ones(rows, device="cuda")
+    run = lambda: FORMS[form](h, z, y, ids, t, one)  # noqa: E731
+    want = [x.clone() for x in run()]
+    clean(h)
+    cold, side = torch.zeros(1 << 27, device="cuda"), torch.cuda.Stream()  # more than L2 holds
+    for _ in range(40):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                cold.add_(1)
+        h.set_wait_limit(1)
+        run()
+        status = h.device_status()
+        assert status in (0, svm.STATUS_BITS["timeout"])
+        h.set_wait_limit(0)
+        got = run()
+        clean(h)
+        assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(want, got))
+        if status:
+            break
+    assert status, "no call gave up"
+    h.close()
