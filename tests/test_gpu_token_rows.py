@@ -267,6 +267,33 @@ def test_gradients_of_sure_tokens(h, dtype, V, many, T, ent):
         assert tu.close(grad[i, at], own / s.T, lim / s.T, dtype), (i, float(grad[i, at]), own / s.T, lim / s.T)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("rows,V", [(6, 152061), (600, 2001)])
+def test_a_given_token_of_a_bad_logit_is_a_bad_row(svm, h, dtype, rows, V):
+    """The given token's own logit is NaN or infinite, or the only one that is not masked, or masked."""
+    z = tu.logits(rows, V, dtype, 3, device="cuda")
+    y = (torch.arange(rows, device="cuda") * 977 % V).to(torch.int32)
+    bad = []
+    for r in range(0, rows, 6):
+        for at, x in ((0, math.nan), (1, math.inf), (2, -math.inf)):
+            z[r + at, y[r + at].long()] = x
+        z[r + 3] = -math.inf
+        z[r + 3, y[r + 3].long()] = -7.0
+        z[r + 4] = -math.inf
+        bad += [r, r + 1, r + 4]
+    g, e = torch.ones(rows, device="cuda"), torch.full((rows,), 0.5, device="cuda")
+    for h_ in (None, e):
+        grad, lp, H = h.token_logprobs_grad(z, y, g, h_)
+        assert h.device_status() == svm.STATUS_BITS["bad_logit"]
+        assert lp.isnan().nonzero()[:, 0].tolist() == H.isnan().nonzero()[:, 0].tolist() == bad
+        assert grad[bad].isnan().all()
+        for r in (2, 3, 5, rows - 4, rows - 3, rows - 1):
+            s = tu.Soft(z[r], 1.0)
+            want, err = s.grad(int(y[r]), 1.0, 0.0 if h_ is None else 0.5)
+            assert tu.close(grad[r], want, err, dtype), r
+            assert tu.close(lp[r], s.lp[y[r]], s.lp_err(s.lp[y[r]])) and tu.close(H[r], s.entropy, s.entropy_err())
+
+
 # ---------------------------------------------------------------------------
 # sums that are known exactly: every token counts once
 
