@@ -1016,6 +1016,8 @@ Plan make_plan(const TokenParams &P, const int (&room)[5]) {
     p.cluster = 1 << log;
     p.slice_vecs = (int32_t)(((vecs + p.cluster - 1 >> log) + 31) / 32 * 32);
     const int words = log ? (2 * kConsumers * Kd::kWords * 8) << log : 0;
+    static_assert(!Kd::Top || sizeof(Shared) + 15 + sizeof(SharedTop) + 15 + 2 * kConsumers * Kd::kWords * 8 * kMaxCluster +
+                                      4 * Kd::kChunkBytes <= kHalfSmem, "kGroupRows");
     p.slots = std::min(kMaxSlots, (kHalfSmem - fixed - words) / Kd::kChunkBytes);
     // (the sums of a cluster's rows have no way to keep one another apart: it has one row)
     p.dynamic = (Kd::Grad || log == 0) && P.entries <= INT32_MAX >> log;

@@ -21,7 +21,11 @@ constexpr int kTopDepth = 2;                      // the same where top tokens a
 // row is taken the worse the rows are balanced).
 constexpr int kLead = 2;
 constexpr int kMaxCluster = 16;
-constexpr int kGroupRows = 20;                    // groups of a thread's vectors in a slice whose maxima are kept
+// Groups of a thread's vectors in a slice whose maxima are kept: as many as shared memory has room for (two rows of 24 x 256
+// halves) beside four slots of the ring and the words of the largest cluster. A group is 2^n chunks, the least that a slice fits
+// in: one up to 196608 bf16 or 98304 fp32 logits. (Larger groups have more vectors read again: of 2000 rows of 152064 with 64 top
+// tokens, 132 us for groups of two chunks, 124.9 for one.)
+constexpr int kGroupRows = 24;
 constexpr int kMine = 256, kKept = 512;           // groups that may hold top tokens, a warp's and all
 constexpr unsigned kLost = 1u << 24;
 constexpr int kKeys = 512;                        // tokens among them
