@@ -238,7 +238,7 @@ int specverify_row_features(specverify_t h, const void *rows, int32_t dtype, int
  * calls use the handle's device and its sticky status word and no workspace:
  * unlike the others, they may run beside one another and inside captured graphs
  * that do. Sums are fp32, results the same from run to run; logarithms are off by
- * 2^-20 of themselves or of one at most, whichever is larger. A bad row (a NaN or
+ * about 2^-20 of themselves or of one, whichever is larger. A bad row (a NaN or
  * +inf logit, every logit -inf, a bad token, list or row number) gets NaN for
  * each of its floats and -1 for its whole numbers, and sets its status bit.
  */
